@@ -264,7 +264,7 @@ def _prepare_fork(case, seed):
              "children": _int32(lay["children"]), "new": _int32(lay["new"])}
     if own:
         state["api"] = _api()
-        state["caches"] = [state["api"].KVCache(p[0], p[1]) for p in pools]
+        state["caches"] = state["api"].KVCacheStack([state["api"].KVCache(p[0], p[1]) for p in pools])
     return state
 
 
@@ -296,7 +296,7 @@ def _prepare_compact(case, seed):
     state["num_live"] = torch.empty(1, dtype=torch.int32, device="cuda")
     if own:                                        # the workspace that a serving program keeps
         api = state["api"] = _api()
-        state["caches"] = [api.KVCache(p[0], p[1]) for p in pools]
+        state["caches"] = api.KVCacheStack([api.KVCache(p[0], p[1]) for p in pools])
         state["workspace"] = torch.empty(api.cb_compact_workspace_size(case["blocks"]), dtype=torch.uint8, device="cuda")
     return state
 
