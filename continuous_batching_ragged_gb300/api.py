@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
-from typing import Optional
+from typing import Optional, Sequence
 
 import numpy as np
 import torch
@@ -74,6 +74,20 @@ class KVCache:
                                   self.num_heads, self.head_dim, _DTYPES[self.k.dtype])
 
 
+class KVCacheStack:
+    """The caches of a model's layers, all of one shape: the `layers` argument of the
+    page operations.  Holds the caches and the C array that describes them."""
+
+    def __init__(self, caches: Sequence[KVCache]):
+        self.caches = list(caches)
+        if not self.caches:
+            raise ValueError("at least one layer")
+        self.c_array = (native.cb_kv_cache * len(self.caches))(*(c.c_struct() for c in self.caches))
+
+    def __len__(self) -> int:
+        return len(self.caches)
+
+
 def cb_append_kv(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
                  cache: KVCache, stream=None) -> None:
     if slot_mapping.dtype != torch.int64:
@@ -81,6 +95,103 @@ def cb_append_kv(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.T
     c = cache.c_struct()
     check(native.lib().cb_append_kv(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), k_new.shape[0],
                                     ctypes.byref(c), _stream_handle(stream)), "cb_append_kv")
+
+
+def _token_rows(t: torch.Tensor, name: str, num_tokens: int, num_heads: int, like: torch.Tensor) -> int:
+    """Pointer of [T, heads, A] rows whose tokens may be strided (parts of one projection)."""
+    if not t.is_cuda or t.dtype != like.dtype:
+        raise ValueError(f"{name} must be a CUDA tensor of the cache's dtype")
+    if t.dim() != 3 or t.shape[0] != num_tokens or t.shape[1] != num_heads or t.shape[2] != like.shape[3]:
+        raise ValueError(f"{name} must be [num_tokens, {num_heads}, head_dim]")
+    if t.stride(2) != 1 or (num_heads > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.data_ptr()
+
+
+def cb_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
+                        cache: KVCache, *, q_out: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                        cos_sin: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                        k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                        dims: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """cb_norm_rope_append: per-head RMS norm of q and k (where a weight is given),
+    the position rotation (where cos_sin, [max_positions, rot_dim] fp32, is given)
+    and the append of k and v.  q, k, v: [T, heads, A], tokens may be strided.  With
+    `dims`, T is the capacity and dims[1] the step's token count."""
+    T = q.shape[0]
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be int64 [num_tokens]")
+    if positions is not None and (positions.dtype != torch.int32 or positions.numel() != T):
+        raise ValueError("positions must be int32 [num_tokens]")
+    if dims is not None and dims.dtype != torch.int32:
+        raise ValueError("dims must be int32")
+    if cos_sin is not None and (cos_sin.dtype != torch.float32 or cos_sin.dim() != 2):
+        raise ValueError("cos_sin must be fp32 [max_positions, rot_dim]")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and (w.dtype != cache.k.dtype or w.numel() != cache.head_dim):
+            raise ValueError(f"{name} must be [head_dim] of the cache's dtype")
+    if q_out.shape != q.shape or q_out.dtype != q.dtype:
+        raise ValueError("q_out must have q's shape and dtype")
+    heads, kv = q.shape[1], cache.num_heads
+    a = native.cb_norm_rope(_token_rows(q, "q", T, heads, cache.k), _token_rows(k, "k", T, kv, cache.k),
+                            _token_rows(v, "v", T, kv, cache.k), *(
+                                t.stride(0) if T > 1 else t.shape[1] * t.shape[2] for t in (q, k, v)),
+                            _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin),
+                            cos_sin.shape[0] if cos_sin is not None else 0,
+                            cos_sin.shape[1] if cos_sin is not None else 0, int(interleaved), eps)
+    c = cache.c_struct()
+    check(native.lib().cb_norm_rope_append(ctypes.byref(a), heads, _ptr(positions), _ptr(slot_mapping), _ptr(dims), T,
+                                           ctypes.byref(c), _ptr(q_out), _stream_handle(stream)),
+          "cb_norm_rope_append")
+    return q_out
+
+
+def _stack(layers) -> KVCacheStack:
+    return layers if isinstance(layers, KVCacheStack) else KVCacheStack(layers)
+
+
+def cb_fork_sequences(layers, block_tables: torch.Tensor, context_lens: torch.Tensor, parents: torch.Tensor,
+                      children: torch.Tensor, new_blocks: torch.Tensor, stream=None) -> None:
+    """cb_fork_sequences: rows `children` of block_tables and context_lens continue
+    rows `parents` (full pages shared, a last partial page copied to new_blocks).
+    layers: a KVCacheStack, or the layers' caches."""
+    for name, t in (("block_tables", block_tables), ("context_lens", context_lens), ("parents", parents),
+                    ("children", children), ("new_blocks", new_blocks)):
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+    if block_tables.dim() != 2 or context_lens.numel() != block_tables.shape[0]:
+        raise ValueError("block_tables must be [rows, max_blocks_per_seq] and context_lens [rows]")
+    n = parents.numel()
+    if children.numel() != n or new_blocks.numel() != n:
+        raise ValueError("parents, children and new_blocks must have one entry per fork")
+    ls = _stack(layers)
+    check(native.lib().cb_fork_sequences(ls.c_array, len(ls), _ptr(block_tables), _ptr(context_lens),
+                                         block_tables.shape[0], block_tables.shape[1], _ptr(parents), _ptr(children),
+                                         _ptr(new_blocks), n, _stream_handle(stream)), "cb_fork_sequences")
+
+
+def cb_compact_workspace_size(num_blocks: int) -> int:
+    return int(native.lib().cb_compact_workspace_size(num_blocks))
+
+
+def cb_compact_blocks(layers, block_tables: torch.Tensor, context_lens: torch.Tensor, *,
+                      new_block_tables: torch.Tensor, remap: torch.Tensor, num_live: torch.Tensor,
+                      workspace: torch.Tensor, stream=None) -> None:
+    """cb_compact_blocks: move the live pages to the lowest ids; new_block_tables (may
+    be block_tables), remap [num_blocks] and num_live [1] are written.  layers: a
+    KVCacheStack, or the layers' caches."""
+    for name, t in (("block_tables", block_tables), ("context_lens", context_lens),
+                    ("new_block_tables", new_block_tables), ("remap", remap), ("num_live", num_live)):
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+    if block_tables.dim() != 2 or context_lens.numel() != block_tables.shape[0]:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and context_lens [num_seqs]")
+    ls = _stack(layers)
+    if new_block_tables.shape != block_tables.shape or remap.numel() != ls.caches[0].num_blocks or num_live.numel() < 1:
+        raise ValueError("new_block_tables must be as block_tables, remap [num_blocks], num_live [1]")
+    check(native.lib().cb_compact_blocks(
+        ls.c_array, len(ls), _ptr(block_tables), _ptr(context_lens), block_tables.shape[0], block_tables.shape[1],
+        _ptr(new_block_tables), _ptr(remap), _ptr(num_live), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream)), "cb_compact_blocks")
 
 
 def cb_attention_workspace_size(cache: KVCache, num_seqs: int, num_tokens: int,

@@ -23,6 +23,7 @@ EXPORTS = ("cb_append_kv", "cb_attention_workspace_size", "cb_ragged_attention",
            "cb_ragged_attention_gqa", "cb_attention_workspace_size_gqa",
            "cb_plan_step_gqa", "cb_ragged_attention_planned_gqa",
            "cb_decode_attention_noalloc", "cb_padded_attention",
+           "cb_norm_rope_append", "cb_fork_sequences", "cb_compact_workspace_size", "cb_compact_blocks",
            "cb_scheduler_create", "cb_scheduler_destroy", "cb_add_request", "cb_build_batch",
            "cb_complete_step", "cb_scheduler_stats", "cb_check_device_errors", "cb_last_error",
            "cb_synth_tokens", "cb_synth_fill_cache", "cb_selftest_bounded_wait")
@@ -37,6 +38,14 @@ class cb_kv_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_blocks", ctypes.c_int32),
                 ("block_size", ctypes.c_int32), ("num_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
+class cb_norm_rope(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p),
+                ("max_positions", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class cb_sched_config(ctypes.Structure):
@@ -97,6 +106,10 @@ def lib() -> ctypes.CDLL:
         "cb_ragged_attention_planned_gqa": (st, [vp, i32, pcache, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32,
                                                  vp, vp, sz, vp]),
         "cb_decode_attention_noalloc": (st, [vp, pcache, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp]),
+        "cb_norm_rope_append": (st, [ctypes.POINTER(cb_norm_rope), i32, vp, vp, vp, i32, pcache, vp, vp]),
+        "cb_fork_sequences": (st, [pcache, i32, vp, vp, i32, i32, vp, vp, vp, i32, vp]),
+        "cb_compact_workspace_size": (sz, [i32]),
+        "cb_compact_blocks": (st, [pcache, i32, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp]),
         "cb_scheduler_create": (st, [ctypes.POINTER(cb_sched_config), ctypes.POINTER(vp)]),
         "cb_scheduler_destroy": (None, [vp]),
         "cb_add_request": (st, [vp, i64, i64, i32, i32]),

@@ -86,6 +86,114 @@ cb_status cb_append_kv(const void* k_new, const void* v_new, const int64_t* slot
                        int32_t num_tokens, const cb_kv_cache* cache, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * cb_norm_rope_append -- cb_append_kv with the work that comes before it: RMS
+ * norm of each query and key head and the position rotation, in the pass that
+ * writes the keys and values into the cache.
+ * The pages have no counterpart: they take projected queries and keys as given.
+ *
+ * Per token t and head, x the head's row in fp32:
+ *     y = x * rsqrt(mean(x^2) + eps) * weight     (skipped where the weight is NULL)
+ *     (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)  for each pair (a, b) of
+ * the first rot_dim dimensions: (i, i + rot_dim / 2), or (2i, 2i + 1) when
+ * `interleaved` is not 0.  Queries are written to q_out, keys and the unchanged
+ * values to cache slot slot_mapping[t].  fp32 from load to store, rounded once.
+ *
+ *   q, k, v       device rows of cache->dtype: token t's num_q_heads (k, v: the
+ *                 cache's) heads of head_dim elements are contiguous from
+ *                 q + t * q_stride (strides in elements, multiples of 16 bytes), so
+ *                 the three may be parts of one projection's output.
+ *   q_weight, k_weight  device [head_dim] of cache->dtype, or NULL: no norm.
+ *   cos_sin       device fp32 [max_positions][rot_dim]: the cosines of a position's
+ *                 rot_dim / 2 angles, then their sines.  May be NULL if rot_dim = 0.
+ *   positions     device int32 [num_tokens]; NULL allowed if rot_dim = 0.  A position
+ *                 outside [0, max_positions) sets CB_ERR_BOUNDS on the device word and
+ *                 its token is left out whole.
+ *   slot_mapping  as in cb_append_kv: a negative slot caches nothing (its query is
+ *                 still written), one past the pool sets CB_ERR_BOUNDS.  No slot may
+ *                 be given twice.
+ *   dims          NULL, or the device sizes of a planned step: the token count is
+ *                 dims[1] and num_tokens its capacity, as in cb_append_kv_dims.
+ *   q_out         device [num_tokens][num_q_heads][head_dim].  It may be q itself if
+ *                 q's rows are that dense; otherwise it overlaps no input.
+ * All buffers 16-byte aligned.  head_dim 64, 128 or (bf16) 256; rot_dim a multiple
+ * of 16 (bf16) or 8 (f32) up to head_dim; any block size.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos_sin;
+  int32_t max_positions;
+  int32_t rot_dim;
+  int32_t interleaved;
+  float eps;
+} cb_norm_rope;
+
+cb_status cb_norm_rope_append(const cb_norm_rope* in, int32_t num_q_heads, const int32_t* positions,
+                              const int64_t* slot_mapping, const int32_t* dims, int32_t num_tokens,
+                              const cb_kv_cache* cache, void* q_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * cb_fork_sequences -- child sequences that continue a parent's cached tokens.
+ * The pages have no counterpart; several samples of one prompt share its pages.
+ *
+ * Fork f: the child row children[f] of block_tables gets the parent's n =
+ * context_lens[parents[f]] cached tokens.  The parent's floor(n / block_size) full
+ * pages are shared (their ids are copied).  The tokens of a last, partial page
+ * are copied to page new_blocks[f], in every layer, so that parent and child
+ * can both append; the rest of that page is left as it was.  Table entries
+ * behind are set to -1 and context_lens[children[f]] to n.
+ *
+ *   layers        host array of num_layers caches of one shape and dtype.
+ *   block_tables  device int32 [table_rows][max_blocks_per_seq], in and out.
+ *   context_lens  device int32 [table_rows], in and out.
+ *   parents, children, new_blocks  device int32 [num_forks].  new_blocks[f] is not
+ *                 read if the parent ends on a page border.  A new page must be in no
+ *                 table (the caller allocates).
+ * On the device, a fork is left out whole and the error word set if a row or length
+ * is out of range (CB_ERR_INVALID), a page id is (CB_ERR_BOUNDS), its child is also a
+ * parent or another fork's child, or its new page is another fork's or a page that
+ * one copies from (CB_ERR_INVALID).
+ * ------------------------------------------------------------------------- */
+cb_status cb_fork_sequences(const cb_kv_cache* layers, int32_t num_layers, int32_t* block_tables,
+                            int32_t* context_lens, int32_t table_rows, int32_t max_blocks_per_seq,
+                            const int32_t* parents, const int32_t* children, const int32_t* new_blocks,
+                            int32_t num_forks, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * cb_compact_blocks -- the pages in use moved to the lowest ids of the pool, so that
+ * all pages from *num_live on are free.
+ * The pages have no counterpart beyond releasing a finished request's blocks.
+ *
+ * A page is live if some sequence's first ceil(context_lens[s] / block_size) table
+ * entries name it; pages may be in several tables.  With n live pages, those below
+ * id n stay, and the k-th live page at or above n moves to the k-th free id below
+ * n, in every layer.  The old copies are left as they were.
+ *
+ *   layers            host array of num_layers caches of one shape and dtype.
+ *   block_tables      device int32 [num_seqs][max_blocks_per_seq].
+ *   new_block_tables  device, same shape: the tables with the new ids, -1 behind each
+ *                     sequence's pages.  May be block_tables itself.
+ *   remap             device int32 [num_blocks]: a page's new id, -1 if not live.
+ *   num_live          device int32: n.
+ *   workspace         at least cb_compact_workspace_size(num_blocks) bytes, 256-byte
+ *                     aligned; not preserved, not shared by concurrent calls.
+ * A length outside the table (CB_ERR_INVALID) or a page id outside the pool
+ * (CB_ERR_BOUNDS) sets the error word, *num_live to -1, and nothing else is
+ * written.  Pools of up to 2^20 blocks (CB_ERR_UNSUPPORTED otherwise).
+ * ------------------------------------------------------------------------- */
+size_t cb_compact_workspace_size(int32_t num_blocks);
+cb_status cb_compact_blocks(const cb_kv_cache* layers, int32_t num_layers, const int32_t* block_tables,
+                            const int32_t* context_lens, int32_t num_seqs, int32_t max_blocks_per_seq,
+                            int32_t* new_block_tables, int32_t* remap, int32_t* num_live, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * cb_ragged_attention -- attention of one packed, padding-free step.
  * Hugging Face blog "Continuous batching from first principles", sections
  * "Attention" (masked row-wise softmax of Q K^T times V), "Chunked prefill"

@@ -1,0 +1,98 @@
+"""Arguments that the norm-and-rotation append and the page operations refuse on
+the host, before any CUDA call: no GPU needed."""
+import ctypes
+
+import pytest
+
+from continuous_batching_ragged_gb300 import native
+
+P = 0x10000                          # an aligned address that no refused call reads
+
+
+def cache(**kw):
+    f = dict(k=P, v=P, num_blocks=16, block_size=16, num_heads=8, head_dim=128, dtype=native.CB_DTYPE_BF16)
+    f.update(kw)
+    return native.cb_kv_cache(*(f[n] for n, _ in native.cb_kv_cache._fields_))
+
+
+def rope(lib, c=None, heads=32, pos=P, slots=P, tokens=4, q_out=P, **kw):
+    f = dict(q=P, k=P, v=P, q_stride=32 * 128, k_stride=8 * 128, v_stride=8 * 128, q_weight=P, k_weight=P, cos_sin=P,
+             max_positions=100, rot_dim=128, interleaved=0, eps=1e-6)
+    f.update(kw)
+    a = native.cb_norm_rope(*(f[n] for n, _ in native.cb_norm_rope._fields_))
+    return lib.cb_norm_rope_append(ctypes.byref(a), heads, pos, slots, None, tokens, ctypes.byref(c or cache()), q_out, None)
+
+
+@pytest.mark.parametrize("kw", [dict(q=None), dict(k=None), dict(v=None), dict(slots=None), dict(q_out=None), dict(pos=None),
+                                dict(cos_sin=None), dict(tokens=-1), dict(heads=0), dict(q=P + 2), dict(q_out=P + 8),
+                                dict(q_weight=P + 4), dict(cos_sin=P + 4), dict(q_stride=32 * 128 - 8), dict(k_stride=1024 - 8),
+                                dict(v_stride=8 * 128 + 4), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")),
+                                dict(max_positions=0)])
+def test_norm_rope_invalid(native_lib, kw):
+    assert rope(native_lib, **kw) == native.CB_ERR_INVALID
+    assert b"cb_norm_rope_append" in native_lib.cb_last_error()
+
+
+@pytest.mark.parametrize("kw,c", [(dict(rot_dim=8), {}), (dict(rot_dim=144), {}), (dict(rot_dim=-16), {}),
+                                  (dict(), dict(head_dim=96)), (dict(), dict(head_dim=256, dtype=native.CB_DTYPE_F32)),
+                                  (dict(), dict(dtype=7)), (dict(heads=1 << 20), {})])
+def test_norm_rope_unsupported(native_lib, kw, c):
+    assert rope(native_lib, cache(**c), **kw) == native.CB_ERR_UNSUPPORTED
+
+
+def test_norm_rope_null_and_empty(native_lib):
+    assert native_lib.cb_norm_rope_append(None, 1, None, None, None, 1, ctypes.byref(cache()), P, None) == native.CB_ERR_INVALID
+    assert rope(native_lib, cache(num_blocks=0)) == native.CB_ERR_INVALID
+    assert rope(native_lib, tokens=0, q=None) == native.CB_OK
+
+
+def layers(*caches):
+    return (native.cb_kv_cache * len(caches))(*caches)
+
+
+def fork(lib, ls=None, n=None, tables=P, ctx=P, rows=4, width=4, parents=P, children=P, new=P, forks=2):
+    ls = layers(cache(), cache()) if ls is None else ls
+    return lib.cb_fork_sequences(ls, len(ls) if n is None else n, tables, ctx, rows, width, parents, children, new, forks, None)
+
+
+def compact(lib, ls=None, tables=P, ctx=P, seqs=4, width=4, new=P, remap=P, live=P, ws=P, ws_bytes=1 << 20):
+    ls = layers(cache(), cache()) if ls is None else ls
+    return lib.cb_compact_blocks(ls, len(ls), tables, ctx, seqs, width, new, remap, live, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("call", [fork, compact])
+@pytest.mark.parametrize("kw", [dict(block_size=32), dict(num_blocks=17), dict(num_heads=4), dict(head_dim=64),
+                                dict(dtype=native.CB_DTYPE_F32), dict(k=None), dict(v=None), dict(k=P + 8)])
+def test_layers_must_be_alike(native_lib, call, kw):
+    assert call(native_lib, layers(cache(), cache(**kw))) == native.CB_ERR_INVALID
+
+
+@pytest.mark.parametrize("call", [fork, compact])
+def test_layer_shapes_refused(native_lib, call):
+    assert call(native_lib, layers(cache(num_heads=0))) == native.CB_ERR_INVALID
+    assert call(native_lib, layers(cache(head_dim=12))) == native.CB_ERR_UNSUPPORTED
+    assert call(native_lib, layers(cache(dtype=9))) == native.CB_ERR_UNSUPPORTED
+    assert call(native_lib, layers(cache(num_heads=1 << 20, block_size=1 << 10))) == native.CB_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [dict(n=0), dict(tables=None), dict(ctx=None), dict(parents=None), dict(children=None),
+                                dict(new=None), dict(forks=-1), dict(rows=-1), dict(width=-1)])
+def test_fork_invalid(native_lib, kw):
+    assert fork(native_lib, **kw) == native.CB_ERR_INVALID
+
+
+def test_fork_nothing(native_lib):
+    assert fork(native_lib, forks=0, tables=None) == native.CB_OK
+
+
+@pytest.mark.parametrize("kw", [dict(tables=None), dict(ctx=None), dict(new=None), dict(remap=None), dict(live=None), dict(ws=None),
+                                dict(ws_bytes=64), dict(ws=P + 16), dict(seqs=-1), dict(width=-1)])
+def test_compact_invalid(native_lib, kw):
+    assert compact(native_lib, **kw) == native.CB_ERR_INVALID
+
+
+def test_compact_sizes(native_lib):
+    assert compact(native_lib, layers(cache(num_blocks=(1 << 20) + 1)), ws_bytes=1 << 30) == native.CB_ERR_UNSUPPORTED
+    assert native_lib.cb_compact_workspace_size(0) == 0
+    # header, bitmap and its running counts (one word per 32 pages), holes and movers (half the pool each)
+    assert native_lib.cb_compact_workspace_size(10240) == 256 + 2 * 1280 + 2 * 20736
