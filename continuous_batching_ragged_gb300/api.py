@@ -267,6 +267,38 @@ def cb_ragged_attention_gqa(q: torch.Tensor, cache: KVCache, cu_seqlens_q: torch
     return out
 
 
+def cb_shared_prefix_workspace_size(cache: KVCache, num_q_heads: int, num_seqs: int, num_tokens: int,
+                                    num_groups: int, max_context_len: int) -> int:
+    c = cache.c_struct()
+    return int(native.lib().cb_shared_prefix_workspace_size(ctypes.byref(c), num_q_heads, num_seqs, num_tokens,
+                                                            num_groups, max_context_len))
+
+
+def cb_shared_prefix_attention(q: torch.Tensor, cache: KVCache, cu_seqlens_q: torch.Tensor,
+                               context_lens: torch.Tensor, block_tables: torch.Tensor, cu_groups: torch.Tensor,
+                               prefix_lens: torch.Tensor, *, max_q_len: int, max_context_len: int, scale: float,
+                               out: torch.Tensor, workspace: Optional[torch.Tensor], stream=None) -> torch.Tensor:
+    """cb_shared_prefix_attention: cb_ragged_attention_gqa where the sequences
+    cu_groups[g] .. cu_groups[g+1]-1 have their first prefix_lens[g] keys in common."""
+    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("context_lens", context_lens), ("block_tables", block_tables),
+                    ("cu_groups", cu_groups), ("prefix_lens", prefix_lens)):
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+    S, G = context_lens.shape[0], prefix_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or cu_seqlens_q.shape[0] != S + 1:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and cu_seqlens_q [num_seqs + 1]")
+    if cu_groups.shape[0] != G + 1:
+        raise ValueError("cu_groups must be [num_groups + 1]")
+    c = cache.c_struct()
+    ws_ptr = _ptr(workspace) if workspace is not None and workspace.numel() else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    check(native.lib().cb_shared_prefix_attention(
+        _ptr(q), q.shape[1], ctypes.byref(c), _ptr(cu_seqlens_q), _ptr(context_lens), _ptr(block_tables),
+        _ptr(cu_groups), _ptr(prefix_lens), G, S, q.shape[0], block_tables.shape[1], max_q_len, max_context_len,
+        float(scale), _ptr(out), ws_ptr, ws_bytes, _stream_handle(stream)), "cb_shared_prefix_attention")
+    return out
+
+
 def cb_append_kv_dims(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor,
                       dims: torch.Tensor, cache: KVCache, stream=None) -> None:
     """cb_append_kv with the token count in dims[1] (device); k_new's rows bound it."""

@@ -21,6 +21,9 @@
 
 namespace {
 
+// Query heads per key/value head that fit the prefix kernel's row tile.
+constexpr int kMaxPrefixGroup = 128;
+
 bool is_pow2(int32_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
 cb_status check_cache(const cb_kv_cache* c, const char* who) {
@@ -345,4 +348,48 @@ extern "C" cb_status cb_ragged_attention_planned_gqa(const void* q, int32_t num_
   return attention_planned("cb_ragged_attention_planned_gqa", q, num_q_heads, cache, cu_seqlens_q, context_lens,
                            block_tables, dims, num_seqs, num_tokens, max_blocks_per_seq, max_q_len,
                            max_context_len, scale, out, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t cb_shared_prefix_workspace_size(const cb_kv_cache* cache, int32_t num_q_heads, int32_t num_seqs,
+                                                  int32_t num_tokens, int32_t num_groups, int32_t max_context_len) {
+  if (!cache || cache->num_heads < 1 || num_q_heads < 1 || num_q_heads % cache->num_heads != 0 ||
+      num_q_heads / cache->num_heads > kMaxPrefixGroup || num_seqs < 0 || num_tokens < 0 || num_groups < 0 ||
+      max_context_len < 0)
+    return 0;
+  const size_t own = cb::step_workspace_bytes(num_seqs, num_tokens, num_q_heads, cache->head_dim, max_context_len);
+  return (own + 255) / 256 * 256 +
+         cb::prefix_workspace_bytes(num_q_heads, cache->num_heads, num_seqs, num_tokens, num_groups);
+}
+
+extern "C" cb_status cb_shared_prefix_attention(const void* q, int32_t num_q_heads, const cb_kv_cache* cache,
+                                                const int32_t* cu_seqlens_q, const int32_t* context_lens,
+                                                const int32_t* block_tables, const int32_t* cu_groups,
+                                                const int32_t* prefix_lens, int32_t num_groups, int32_t num_seqs,
+                                                int32_t num_tokens, int32_t max_blocks_per_seq, int32_t max_q_len,
+                                                int32_t max_context_len, float scale, void* out, void* workspace,
+                                                size_t workspace_bytes, void* stream) {
+  const char* who = "cb_shared_prefix_attention";
+  if (num_q_heads < 1) return cb::fail(CB_ERR_INVALID, "%s: num_q_heads < 1", who);
+  cb_status st = check_cache(cache, who);
+  if (st != CB_OK) return st;
+  if (cache->dtype != CB_DTYPE_BF16 || cache->block_size % 16 != 0)
+    return cb::fail(CB_ERR_UNSUPPORTED, "%s: needs a bf16 cache and a block size multiple of 16", who);
+  if (num_q_heads / cache->num_heads > kMaxPrefixGroup)
+    return cb::fail(CB_ERR_UNSUPPORTED, "%s: more than %d query heads per key/value head", who, kMaxPrefixGroup);
+  if (num_groups < 0) return cb::fail(CB_ERR_INVALID, "%s: negative size", who);
+  if (num_seqs > 0) {
+    if (num_groups < 1) return cb::fail(CB_ERR_INVALID, "%s: sequences without a group", who);
+    if (!cu_groups || !prefix_lens) return cb::fail(CB_ERR_INVALID, "%s: null pointer", who);
+    const size_t need = cb_shared_prefix_workspace_size(cache, num_q_heads, num_seqs, num_tokens, num_groups, max_context_len);
+    if (need > 0 && (!workspace || workspace_bytes < need))   // 0: sizes that the checks below refuse
+      return cb::fail(CB_ERR_INVALID, "%s: workspace too small: %zu bytes given, %zu needed", who, workspace_bytes, need);
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+      return cb::fail(CB_ERR_INVALID, "%s: workspace must be 256-byte aligned", who);
+  }
+  cb::AttnArgs a;
+  st = prepare(who, q, cache, cu_seqlens_q, context_lens, block_tables, num_seqs, num_tokens, max_blocks_per_seq,
+               max_q_len, max_context_len, scale, out, nullptr, false, a, num_q_heads);
+  if (st != CB_OK || num_seqs == 0) return st;
+  return cb::run_shared_prefix(a, cu_groups, prefix_lens, num_groups, workspace,
+                               static_cast<cudaStream_t>(stream));
 }

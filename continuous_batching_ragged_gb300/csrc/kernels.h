@@ -9,6 +9,21 @@
 
 namespace cb {
 
+// A row's state over the shared prefix and one KV segment: acc[kPrefixDim], the
+// reference maximum, the sum, padding to 16 bytes.
+constexpr int kPrefixDim = 128;
+constexpr int kPrefixRec = kPrefixDim + 4;
+
+// What the kernels that run a step's own keys need to know of its shared
+// prefixes (cb_shared_prefix_attention); null pointers elsewhere.
+struct PrefixView {
+  const int32_t* seq_info = nullptr;   // [num_seqs][4]: blocks of the table that the prefix covers,
+                                       // records per row, record stride per row, unused
+  const float* recs = nullptr;         // [token][query head][stride][kPrefixRec]
+  int32_t wait = 0;                    // the kernel launched just before is the prefix kernel: wait
+                                       // for it before reading its records
+};
+
 struct AttnArgs {
   const void* q;
   void* out;
@@ -39,6 +54,9 @@ struct AttnArgs {
   // p_s + pad - 1) are masked out of every row and their rows are not
   // written.  0 <= pad < q_len (the plan leaves a row out otherwise).
   const int32_t* pad_lens = nullptr;
+  // Shared prefixes, or null pointers: context_lens are then the keys behind
+  // the prefix, whose blocks come first in each sequence's table.
+  PrefixView prefix = {};
 };
 
 // Keys per split of the register split-KV kernel, and the smallest split of
@@ -145,6 +163,16 @@ float decode_tc_rate_per_sm(int group_heads);
 int decode_tc_ctas();
 cb_status launch_decode_tc(const AttnArgs& a, const StepPlan& plan, bool after_previous, bool wait_previous,
                            cudaStream_t stream);
+
+// Steps with shared prefixes (bf16, head_dim 128, block size a multiple of 16,
+// at most 128 query heads per key/value head): query tokens per row tile of
+// the prefix kernel, the workspace beyond the step's own (rounded up to 256
+// bytes), and the whole step in a workspace of both.
+int prefix_tile_tokens(int group_heads);
+size_t prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
+                              int32_t num_groups);
+cb_status run_shared_prefix(AttnArgs a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
+                            void* workspace, cudaStream_t stream);
 
 // Prefill chunks (q_len > 1) on tcgen05 tensor cores, bf16, head_dim 128:
 // persistent CTAs over the plan's prefill items.

@@ -51,6 +51,7 @@
 
 #include "device_common.cuh"
 #include "kernels.h"
+#include "prefix_merge.cuh"
 #include "runtime.h"
 #include "sm100_ptx.cuh"
 
@@ -152,9 +153,12 @@ __device__ __forceinline__ int ld_acquire_gpu(const int32_t* p) {
 // segment `mine` comes from TMEM (o_taddr) and registers, the same fp32
 // values its partial slot would hold; the others from their slots, two slots
 // of 32 dims in flight at a time.  Warp-wide (tcgen05.ld); `store`: this
-// thread's row is a real query row.
+// thread's row is a real query row.  PREFIX: the merged row is joined with its
+// n_rec shared-prefix records.
+template <bool PREFIX>
 __device__ __forceinline__ void merge_segments(const float* rows, int nseg, int mine, float m_own, float l_own,
-                                               uint32_t o_taddr, __nv_bfloat16* dst, bool store) {
+                                               uint32_t o_taddr, __nv_bfloat16* dst, bool store,
+                                               const float* rec, int n_rec) {
   constexpr int kM = HD * kPrefillPairRows, kL = (HD + 1) * kPrefillPairRows;
   float mx = m_own;
   for (int sg = 0; sg < nseg; ++sg)
@@ -164,7 +168,9 @@ __device__ __forceinline__ void merge_segments(const float* rows, int nseg, int 
     const float* src = rows + size_t(sg) * kSlotFloats;
     sum += sg == mine ? ex2(m_own - mx) * l_own : ex2(__ldcg(src + kM) - mx) * __ldcg(src + kL);
   }
-  const float inv = 1.0f / sum;
+  float mxp = mx, inv_row = 1.0f;
+  if (PREFIX) prefix_row_scale(rec, n_rec, mx, sum, mxp, inv_row);
+  const float inv = PREFIX ? 1.0f : 1.0f / sum;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t own[32];
@@ -194,6 +200,7 @@ __device__ __forceinline__ void merge_segments(const float* rows, int nseg, int 
       }
     }
     if (store) {
+      if constexpr (PREFIX) join_prefix_row(rec, n_rec, 32 * c, mx, mxp, inv_row, acc);
       uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -209,8 +216,10 @@ __device__ __forceinline__ void merge_segments(const float* rows, int nseg, int 
 // warp or CTA.  Every other segment first stores its unnormalised rows (acc,
 // max, sum) in its partial slot, dimension-major so a warp's 32 rows are one
 // coalesced line.  `rows`: this thread's row in the pair's first slot.
+template <bool PREFIX>
 __device__ __forceinline__ void segment_epilogue(float* rows, int32_t* ticket, int nseg, int mine, float m, float l,
-                                              uint32_t o_taddr, int lane, __nv_bfloat16* dst, bool store) {
+                                              uint32_t o_taddr, int lane, __nv_bfloat16* dst, bool store,
+                                              const float* rec, int n_rec) {
   int merge = 0;
   if (lane == 0 && ld_acquire_gpu(ticket) == nseg - 1) {   // the others are in: no partial needed
     *ticket = 0;                                   // ready for the next call
@@ -238,7 +247,7 @@ __device__ __forceinline__ void segment_epilogue(float* rows, int32_t* ticket, i
     }
     merge = __shfl_sync(0xffffffffu, merge, 0);
   }
-  if (merge) merge_segments(rows, nseg, mine, m, l, o_taddr, dst, store);
+  if (merge) merge_segments<PREFIX>(rows, nseg, mine, m, l, o_taddr, dst, store, rec, n_rec);
 }
 
 __device__ __forceinline__ void tma_prefetch_l2_3d(const void* tmap, int32_t x, int32_t y, int32_t z) {
@@ -286,7 +295,8 @@ __device__ __forceinline__ void load_kv_tile_ring(uint32_t dst, const CUtensorMa
 // segments, whose results then go to partial slots slot0 + j0 / segment).
 struct WorkItem {
   int u;                                           // entry index; >= the entry count: no more work
-  int s, h, row0, c0, q_len, ctx, j0, j1, slot0, pad, spare;   // pad: left-padding rows of the chunk
+  int s, h, row0, c0, q_len, ctx, j0, j1, slot0, pad;   // pad: left-padding rows of the chunk
+  int skip;                                        // blocks of the table that belong to a shared prefix (PREFIX)
 };
 static_assert(sizeof(WorkItem) == 48, "work item slot");
 
@@ -332,7 +342,10 @@ struct PrefillWork {
 // PADDED: the instantiation for left-padded batches (cb_padded_attention),
 // which masks each chunk's pad keys and skips its pad rows' stores; the
 // ragged path's instantiation carries none of that code.
-template <bool PADDED>
+// PREFIX: the instantiation for steps with shared prefixes, which starts each
+// chunk's keys behind its prefix's blocks (all of them before the chunk, so
+// the causal mask over the rest is unchanged) and joins the prefix's records.
+template <bool PADDED, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const AttnArgs a, const PrefillWork w) {
@@ -443,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.q_len = __ldcg(a.cu_seqlens_q + it.s + 1) - it.c0;
             it.ctx = __ldcg(a.context_lens + it.s);
             it.pad = PADDED ? __ldcg(a.pad_lens + it.s) : 0;
+            if constexpr (PREFIX) it.skip = prefix_info(a, it.s).x;
             bad = it.c0 < 0 || it.q_len < 2 || it.c0 + it.q_len > a.num_tokens || it.row0 >= it.q_len ||
                   it.ctx < it.q_len || it.ctx > a.max_context_len || it.pad < 0 || it.pad >= it.q_len;
             if (!bad) {
@@ -465,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const WorkItem it = items[slot];
       if (it.u >= n_units) break;
       const UnitShape sh = unit_shape(it);
-      const int32_t* bt = a.block_tables + size_t(it.s) * a.max_blocks_per_seq;
+      const int32_t* bt = a.block_tables + size_t(it.s) * a.max_blocks_per_seq + (PREFIX ? it.skip : 0);
       // Q of this unit goes in once every S MMA of the previous unit has read
       // the old Q; the first K tiles are requested before that wait.
       auto load_q = [&]() -> bool {
@@ -537,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(BAR_IE + n % kItemSlots));
       if (it.u >= n_units) break;
       const UnitShape sh = unit_shape(it);
-      const int32_t* bt = a.block_tables + size_t(it.s) * a.max_blocks_per_seq;
+      const int32_t* bt = a.block_tables + size_t(it.s) * a.max_blocks_per_seq + (PREFIX ? it.skip : 0);
       for (int j = 0; j < min(kLookAhead, sh.n); ++j)
         stage_boxes(sh.j0 + j, j, B, it.ctx, bt, a, it.h / G, lane, ring, &tm_v);
       for (int j = 0; j < sh.n; ++j) {
@@ -808,8 +822,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int e_row = it.c0 + qi, e_h = it.h, e_slot0 = it.slot0, e_j0 = sh.j0, e_ntiles = sh.n_tiles;
       const bool e_real = qi < it.q_len && (!PADDED || qi >= it.pad);   // padding rows are not written
       __nv_bfloat16* const e_dst = static_cast<__nv_bfloat16*>(a.out) + (size_t(e_row) * H + e_h) * HD;
+      const float* rec = nullptr;                  // the shared prefix's records of this row
+      int n_rec = 0;
+      if constexpr (PREFIX) {
+        const int4 info = prefix_info(a, it.s);
+        n_rec = e_real ? info.y : 0;
+        rec = prefix_records(a, info, e_row, e_h);
+      }
       if (e_slot0 < 0) {
-        const float inv = 1.0f / l;
+        float mx = m, inv;
+        if (PREFIX) prefix_row_scale(rec, n_rec, m, l, mx, inv);
+        else inv = 1.0f / l;
         __nv_bfloat16* dst = e_dst;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -818,18 +841,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           if (e_real) {
             uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
+            if constexpr (PREFIX) {
+              float acc[32];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float* f = reinterpret_cast<const float*>(&o[8 * e]);
-              d4[e] = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
-                                 pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
+              for (int e = 0; e < 32; ++e) acc[e] = __uint_as_float(o[e]);
+              join_prefix_row(rec, n_rec, 32 * c, m, mx, inv, acc);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                d4[e] = make_uint4(pack_bf16x2(acc[8 * e], acc[8 * e + 1]), pack_bf16x2(acc[8 * e + 2], acc[8 * e + 3]),
+                                   pack_bf16x2(acc[8 * e + 4], acc[8 * e + 5]), pack_bf16x2(acc[8 * e + 6], acc[8 * e + 7]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float* f = reinterpret_cast<const float*>(&o[8 * e]);
+                d4[e] = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                                   pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
+              }
             }
           }
         }
       } else {
-        segment_epilogue(w.partials + size_t(e_slot0) * kSlotFloats + BM * t + i,
+        segment_epilogue<PREFIX>(w.partials + size_t(e_slot0) * kSlotFloats + BM * t + i,
                          w.tickets + (e_slot0 * kSegTicketsPerSlot + t * 4 + wq), (e_ntiles + seg - 1) / seg,
-                         e_j0 / seg, m, l, lane_base + 128, lane, e_dst, e_real);
+                         e_j0 / seg, m, l, lane_base + 128, lane, e_dst, e_real, rec, n_rec);
       }
       tc_fence_before();                           // O read before the next unit's first P V overwrites it
       cnt += sh.n;
@@ -847,7 +881,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 std::mutex g_attr_mutex;
-bool g_attr_set[2][64] = {};
+bool g_attr_set[3][64] = {};
+
+using PrefillKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const AttnArgs, const PrefillWork);
+// 0: ragged, 1: left-padded, 2: shared prefixes (never with left padding)
+int variant(const AttnArgs& a) { return a.prefix.seq_info ? 2 : (a.pad_lens ? 1 : 0); }
+PrefillKernel kernel_of(int v) {
+  return v == 2 ? prefill_tc_kernel<false, true> : (v == 1 ? prefill_tc_kernel<true, false> : prefill_tc_kernel<false, false>);
+}
 
 }  // namespace
 
@@ -890,10 +931,9 @@ cb_status launch_prefill_tc(const AttnArgs& a, const StepPlan& plan, bool after_
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64) {
     std::lock_guard<std::mutex> lock(g_attr_mutex);   // first calls may race from several host threads
-    const int v = a.pad_lens ? 1 : 0;
+    const int v = variant(a);
     if (!g_attr_set[v][dev]) {
-      cudaError_t e = cudaFuncSetAttribute(v ? prefill_tc_kernel<true> : prefill_tc_kernel<false>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes));
+      cudaError_t e = cudaFuncSetAttribute(kernel_of(v), cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes));
       if (e != cudaSuccess) return cuda_fail(e, "prefill chunks: shared memory attribute");
       g_attr_set[v][dev] = true;
     }
@@ -911,9 +951,8 @@ cb_status launch_prefill_tc(const AttnArgs& a, const StepPlan& plan, bool after_
   const int64_t max_units = int64_t(plan.pre_cap) * a.num_heads + kPrefillSegSlots;
   const int64_t grid = std::min<int64_t>(sm_count(), max_units);
   if (grid < 1) return CB_OK;
-  cudaError_t e = launch_kernel(a.pad_lens ? prefill_tc_kernel<true> : prefill_tc_kernel<false>,
-                                dim3(unsigned(grid)), dim3(kThreads), kSmemBytes, stream, after_plan, tq, tk, tv,
-                                a, w);
+  cudaError_t e = launch_kernel(kernel_of(variant(a)), dim3(unsigned(grid)), dim3(kThreads), kSmemBytes, stream,
+                                after_plan, tq, tk, tv, a, w);
   if (e != cudaSuccess) return cuda_fail(e, "prefill chunks: launch");
   return CB_OK;
 }

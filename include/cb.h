@@ -369,6 +369,44 @@ cb_status cb_padded_attention(const void* q, const cb_kv_cache* cache, const int
                               void* stream);
 
 /* ---------------------------------------------------------------------------
+ * cb_shared_prefix_attention -- cb_ragged_attention_gqa for a batch whose sequences
+ * share prefixes, each prefix's keys and values read once for all of them.
+ * The pages have no counterpart; samples of one prompt and requests behind one
+ * system prompt share its pages (cb_fork_sequences).
+ *
+ * Same arguments and result as cb_ragged_attention_gqa, plus
+ *   cu_groups    device int32 [num_groups + 1]: group g is the sequences
+ *                cu_groups[g] .. cu_groups[g+1]-1; cu[0] = 0, cu[num_groups] = num_seqs.
+ *                A group may be empty, or one sequence.
+ *   prefix_lens  device int32 [num_groups]: the first prefix_lens[g] keys and values
+ *                of every sequence of group g are the same ones.  At most
+ *                context_lens[s] - q_len_s for each of them (cached before this
+ *                step); any length from 0, whole pages of it are shared work.
+ * The whole pages of the prefix are read through the table of the group's first
+ * sequence; a partial page behind them through each sequence's own.  The result
+ * is cb_ragged_attention_gqa's within fp32 accumulation rounding and the bf16
+ * rounding of P, not bit for bit; it is the same from call to call.
+ * Needs a bf16 cache with head_dim 128, a block size that is a multiple of 16
+ * and at most 128 query heads per key/value head (CB_ERR_UNSUPPORTED otherwise).
+ * On the device, groups that do not cover the sequences in order leave out the
+ * whole step, a prefix longer than a sequence's cached keys that sequence, both
+ * reported as CB_ERR_INVALID; a page id outside the pool as CB_ERR_BOUNDS.
+ * The workspace must be cb_shared_prefix_workspace_size bytes (0: arguments that
+ * are not supported), 256-byte aligned; concurrent calls must not share it.
+ * The launches' shapes depend on the host arguments alone, so a call can be
+ * captured in a graph and replayed with new metadata of the same sizes.
+ * ------------------------------------------------------------------------- */
+size_t cb_shared_prefix_workspace_size(const cb_kv_cache* cache, int32_t num_q_heads, int32_t num_seqs,
+                                       int32_t num_tokens, int32_t num_groups, int32_t max_context_len);
+cb_status cb_shared_prefix_attention(const void* q, int32_t num_q_heads, const cb_kv_cache* cache,
+                                     const int32_t* cu_seqlens_q, const int32_t* context_lens,
+                                     const int32_t* block_tables, const int32_t* cu_groups,
+                                     const int32_t* prefix_lens, int32_t num_groups, int32_t num_seqs,
+                                     int32_t num_tokens, int32_t max_blocks_per_seq, int32_t max_q_len,
+                                     int32_t max_context_len, float scale, void* out, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * cb_decode_attention_noalloc -- decode attention that allocates nothing.
  * The sources have no counterpart: this is a deployment variant of the decode
  * rows of cb_ragged_attention for callers that cannot allocate device memory

@@ -96,3 +96,39 @@ def test_compact_sizes(native_lib):
     assert native_lib.cb_compact_workspace_size(0) == 0
     # header, bitmap and its running counts (one word per 32 pages), holes and movers (half the pool each)
     assert native_lib.cb_compact_workspace_size(10240) == 256 + 2 * 1280 + 2 * 20736
+
+
+def prefix(lib, c=None, q=P, heads=32, cu=P, ctx=P, tables=P, groups=P, lens=P, num_groups=2, seqs=8, tokens=8, width=64, max_q=1,
+           max_ctx=512, scale=0.1, out=P, ws=P, ws_bytes=1 << 40):
+    return lib.cb_shared_prefix_attention(q, heads, ctypes.byref(c or cache()), cu, ctx, tables, groups, lens, num_groups, seqs, tokens,
+                                          width, max_q, max_ctx, scale, out, ws, ws_bytes, None)
+
+
+# None of these gets as far as resolving the device's error word, which needs a GPU.
+@pytest.mark.parametrize("kw", [dict(q=None), dict(cu=None), dict(ctx=None), dict(tables=None), dict(out=None), dict(heads=0),
+                                dict(heads=12), dict(seqs=-1), dict(seqs=0), dict(tokens=0), dict(tokens=4), dict(max_q=0),
+                                dict(max_q=9), dict(max_ctx=0), dict(width=10), dict(scale=0.0), dict(scale=float("nan")),
+                                dict(q=P + 8), dict(out=P + 8)])
+def test_shared_prefix_invalid(native_lib, kw):
+    assert prefix(native_lib, **kw) == native.CB_ERR_INVALID
+    assert b"cb_shared_prefix_attention" in native_lib.cb_last_error()
+
+
+@pytest.mark.parametrize("c", [dict(head_dim=64), dict(dtype=native.CB_DTYPE_F32), dict(block_size=8), dict(block_size=48)])
+def test_shared_prefix_unsupported(native_lib, c):
+    assert prefix(native_lib, cache(**c)) == native.CB_ERR_UNSUPPORTED
+
+
+def test_shared_prefix_groups_and_workspace(native_lib):
+    assert prefix(native_lib, groups=None) == native.CB_ERR_INVALID
+    assert prefix(native_lib, lens=None) == native.CB_ERR_INVALID
+    assert prefix(native_lib, num_groups=0) == native.CB_ERR_INVALID
+    assert prefix(native_lib, num_groups=-1) == native.CB_ERR_INVALID
+    assert prefix(native_lib, cache(num_heads=1), heads=129) == native.CB_ERR_UNSUPPORTED
+    assert prefix(native_lib, seqs=0, tokens=0) == native.CB_OK
+    size = native_lib.cb_shared_prefix_workspace_size
+    assert size(ctypes.byref(cache(num_heads=1)), 129, 8, 8, 1, 512) == 0
+    assert size(ctypes.byref(cache()), 12, 8, 8, 1, 512) == 0 and size(None, 8, 8, 8, 1, 512) == 0
+    n = size(ctypes.byref(cache()), 32, 8, 8, 2, 512)
+    assert n > native_lib.cb_attention_workspace_size_gqa(ctypes.byref(cache()), 32, 8, 8, 512)
+    assert prefix(native_lib, ws=None) == prefix(native_lib, ws_bytes=n - 1) == prefix(native_lib, ws=P + 16) == native.CB_ERR_INVALID
