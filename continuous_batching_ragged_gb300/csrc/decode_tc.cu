@@ -45,7 +45,6 @@
 
 #include "device_common.cuh"
 #include "kernels.h"
-#include "prefix_merge.cuh"
 #include "runtime.h"
 #include "sm100_ptx.cuh"
 
@@ -115,8 +114,7 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 // One claimed unit.
 struct Item {
   int u;                                           // unit index; >= the unit count: no more work
-  int s, g, t, ctx, k0, k1, split, nsplit, j0, nt;
-  int skip;                                        // blocks of the table that belong to a shared prefix (PREFIX)
+  int s, g, t, ctx, k0, k1, split, nsplit, j0, nt, pad;
 };
 static_assert(sizeof(Item) == 48, "item slot");
 
@@ -165,9 +163,6 @@ __device__ __forceinline__ void load_kv_tile(uint32_t dst, const CUtensorMap* tm
   }
 }
 
-// PREFIX: the instantiation for steps with shared prefixes, which starts each
-// row behind its prefix's blocks and joins the prefix's records into it.
-template <bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const AttnArgs a, const DecodeTcWork w) {
@@ -190,14 +185,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split_keys = __ldcg(w.header + 5);
   if (seen_tag != w.tag || n_items < 0 || n_items > w.item_cap || split_keys < kSplitKeys || split_keys % BN != 0) {
     if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, kErrInvalid);
-    if (PREFIX && a.prefix.wait) grid_dependency_wait();
     return;
   }
   const int n_units = n_items * Hkv;
-  if (int(blockIdx.x) >= n_units) {
-    if (PREFIX && a.prefix.wait) grid_dependency_wait();   // this grid ends after the prefix kernel
-    return;
-  }
+  if (int(blockIdx.x) >= n_units) return;
 
   // rows G..127 of the query tile stay zero for the whole launch
   for (uint32_t o = threadIdx.x * 16; o < kTile; o += kThreads * 16)
@@ -277,7 +268,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.t = __ldcg(a.cu_seqlens_q + it.s);
             it.ctx = __ldcg(a.context_lens + it.s);
             it.nsplit = (it.ctx + split_keys - 1) / split_keys;
-            if constexpr (PREFIX) it.skip = prefix_info(a, it.s).x;
             bad = it.t < 0 || it.t >= a.num_tokens || it.ctx < 1 || it.ctx > a.max_context_len ||
                   it.split >= it.nsplit || it.nsplit > w.max_splits;
           }
@@ -297,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       const Item it = items[slot];
       if (it.u >= n_units) break;
-      const int32_t* bt = a.block_tables + size_t(it.s) * a.max_blocks_per_seq + (PREFIX ? it.skip : 0);
+      const int32_t* bt = a.block_tables + size_t(it.s) * a.max_blocks_per_seq;
       // the query rows go in once every S MMA of the previous unit has read the old ones
       auto load_q = [&]() -> bool {
         if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(BAR_QE), (n - 1) & 1))) return false;
@@ -363,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       if (it.u >= n_units) break;
-      const int32_t* bt = a.block_tables + size_t(it.s) * a.max_blocks_per_seq + (PREFIX ? it.skip : 0);
+      const int32_t* bt = a.block_tables + size_t(it.s) * a.max_blocks_per_seq;
       for (int j = 0; j < min(kLookAhead, it.nt); ++j)
         stage_boxes(it.j0 + j, j, B, it.ctx, bt, a, it.g, lane, ring, &tm_v);
       for (int j = 0; j < it.nt; ++j) {
@@ -603,19 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool real = lane < G;
       const int h = it.g * G + lane;
-      // the shared prefix's records of this lane's row
-      const float* rec = nullptr;
-      int n_rec = 0;
-      if constexpr (PREFIX) {
-        if (a.prefix.wait) grid_dependency_wait();
-        const int4 info = prefix_info(a, it.s);
-        n_rec = real ? info.y : 0;
-        rec = prefix_records(a, info, it.t, h);
-      }
       if (it.nsplit == 1) {
-        float mx = m, inv;
-        if (PREFIX) prefix_row_scale(rec, n_rec, m, l, mx, inv);
-        else inv = 1.0f / l;
+        const float inv = 1.0f / l;
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (size_t(it.t) * H + h) * HD;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -624,22 +603,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           if (real) {
             uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
-            if constexpr (PREFIX) {
-              float acc[32];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) acc[e] = __uint_as_float(o[e]);
-              join_prefix_row(rec, n_rec, 32 * c, m, mx, inv, acc);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                d4[e] = make_uint4(pack_bf16x2(acc[8 * e], acc[8 * e + 1]), pack_bf16x2(acc[8 * e + 2], acc[8 * e + 3]),
-                                   pack_bf16x2(acc[8 * e + 4], acc[8 * e + 5]), pack_bf16x2(acc[8 * e + 6], acc[8 * e + 7]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float* f = reinterpret_cast<const float*>(&o[8 * e]);
-                d4[e] = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
-                                   pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
-              }
+            for (int e = 0; e < 4; ++e) {
+              const float* f = reinterpret_cast<const float*>(&o[8 * e]);
+              d4[e] = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                                 pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
             }
           }
         }
@@ -683,15 +651,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float* pk = rows + size_t(k) * (HD + 2);
               sum = fmaf(__ldcg(pk + HD + 1), ex2(__ldcg(pk + HD) - mx), sum);
             }
-            float mxp = mx, inv = 1.0f / sum;
-            if (PREFIX) prefix_row_scale(rec, n_rec, mx, sum, mxp, inv);
+            const float inv = 1.0f / sum;
             __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (size_t(it.t) * H + h) * HD;
 #pragma unroll 1
             for (int c = 0; c < HD; c += 8) {
               float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
               for (int k = 0; k < it.nsplit; ++k) {
                 const float* pk = rows + size_t(k) * (HD + 2);
-                const float wk = ex2(__ldcg(pk + HD) - mx) * (PREFIX ? 1.0f : inv);
+                const float wk = ex2(__ldcg(pk + HD) - mx) * inv;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const float2 x = __ldcg(reinterpret_cast<const float2*>(pk + c + 2 * e));
@@ -699,7 +666,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                   acc[2 * e + 1] = fmaf(wk, x.y, acc[2 * e + 1]);
                 }
               }
-              if constexpr (PREFIX) join_prefix_row(rec, n_rec, c, mx, mxp, inv, acc);
               *reinterpret_cast<uint4*>(dst + c) =
                   make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
                              pack_bf16x2(acc[6], acc[7]));
@@ -763,10 +729,8 @@ int decode_tc_ctas() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(g_attr_mutex);
   if (!g_attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(decode_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          int(kSmemBytes));
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes));
     if (e != cudaSuccess) {
       cuda_fail(e, "grouped decode: shared memory attribute");
       return 0;
@@ -827,7 +791,7 @@ cb_status launch_decode_tc(const AttnArgs& a, const StepPlan& plan, bool after_p
   const int64_t max_units = int64_t(plan.dec_cap) * a.num_kv_heads;
   const int64_t grid = std::min<int64_t>(ctas, max_units);
   if (grid < 1) return CB_OK;
-  cudaError_t e = launch_kernel(a.prefix.seq_info ? decode_tc_kernel<true> : decode_tc_kernel<false>, dim3(unsigned(grid)), dim3(kThreads), kSmemBytes, stream,
+  cudaError_t e = launch_kernel(decode_tc_kernel, dim3(unsigned(grid)), dim3(kThreads), kSmemBytes, stream,
                                 after_previous, tq, tk, tv, a, w);
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "grouped decode: launch");
 }

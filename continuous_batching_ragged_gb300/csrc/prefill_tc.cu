@@ -51,7 +51,6 @@
 
 #include "device_common.cuh"
 #include "kernels.h"
-#include "prefix_merge.cuh"
 #include "runtime.h"
 #include "sm100_ptx.cuh"
 
@@ -147,18 +146,24 @@ __device__ __forceinline__ int ld_acquire_gpu(const int32_t* p) {
   return v;
 }
 
+// 32 dims of a row's record.
+__device__ __forceinline__ void store_acc(float* rec, const uint32_t (&o)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4)
+    *reinterpret_cast<uint4*>(rec + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+}
+
 // The last-arriving segment of a pair merges its warp's rows (this thread:
 // `rows`, the row in slot 0) over all nseg segments by log-sum-exp, in slot
 // order whoever arrives last, so the bits never depend on timing.  Its own
 // segment `mine` comes from TMEM (o_taddr) and registers, the same fp32
 // values its partial slot would hold; the others from their slots, two slots
 // of 32 dims in flight at a time.  Warp-wide (tcgen05.ld); `store`: this
-// thread's row is a real query row.  PREFIX: the merged row is joined with its
-// n_rec shared-prefix records.
+// thread's row is a real query row.  PREFIX: a row with a record `rec` stores its
+// unnormalised state there instead of its output.
 template <bool PREFIX>
 __device__ __forceinline__ void merge_segments(const float* rows, int nseg, int mine, float m_own, float l_own,
-                                               uint32_t o_taddr, __nv_bfloat16* dst, bool store,
-                                               const float* rec, int n_rec) {
+                                               uint32_t o_taddr, __nv_bfloat16* dst, bool store, float* rec) {
   constexpr int kM = HD * kPrefillPairRows, kL = (HD + 1) * kPrefillPairRows;
   float mx = m_own;
   for (int sg = 0; sg < nseg; ++sg)
@@ -168,9 +173,8 @@ __device__ __forceinline__ void merge_segments(const float* rows, int nseg, int 
     const float* src = rows + size_t(sg) * kSlotFloats;
     sum += sg == mine ? ex2(m_own - mx) * l_own : ex2(__ldcg(src + kM) - mx) * __ldcg(src + kL);
   }
-  float mxp = mx, inv_row = 1.0f;
-  if (PREFIX) prefix_row_scale(rec, n_rec, mx, sum, mxp, inv_row);
-  const float inv = PREFIX ? 1.0f : 1.0f / sum;
+  const float inv = PREFIX && rec ? 1.0f : 1.0f / sum;
+  if (PREFIX && rec && store) *reinterpret_cast<float2*>(rec + HD) = make_float2(mx, sum);
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t own[32];
@@ -199,8 +203,9 @@ __device__ __forceinline__ void merge_segments(const float* rows, int nseg, int 
         for (int e = 0; e < 32; ++e) acc[e] = fmaf(w1, v1[e], acc[e]);
       }
     }
-    if (store) {
-      if constexpr (PREFIX) join_prefix_row(rec, n_rec, 32 * c, mx, mxp, inv_row, acc);
+    if (PREFIX && rec) {
+      if (store) store_acc(rec + 32 * c, reinterpret_cast<const uint32_t(&)[32]>(acc));
+    } else if (store) {
       uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -219,7 +224,7 @@ __device__ __forceinline__ void merge_segments(const float* rows, int nseg, int 
 template <bool PREFIX>
 __device__ __forceinline__ void segment_epilogue(float* rows, int32_t* ticket, int nseg, int mine, float m, float l,
                                               uint32_t o_taddr, int lane, __nv_bfloat16* dst, bool store,
-                                              const float* rec, int n_rec) {
+                                              float* rec) {
   int merge = 0;
   if (lane == 0 && ld_acquire_gpu(ticket) == nseg - 1) {   // the others are in: no partial needed
     *ticket = 0;                                   // ready for the next call
@@ -247,7 +252,7 @@ __device__ __forceinline__ void segment_epilogue(float* rows, int32_t* ticket, i
     }
     merge = __shfl_sync(0xffffffffu, merge, 0);
   }
-  if (merge) merge_segments<PREFIX>(rows, nseg, mine, m, l, o_taddr, dst, store, rec, n_rec);
+  if (merge) merge_segments<PREFIX>(rows, nseg, mine, m, l, o_taddr, dst, store, rec);
 }
 
 __device__ __forceinline__ void tma_prefetch_l2_3d(const void* tmap, int32_t x, int32_t y, int32_t z) {
@@ -344,7 +349,8 @@ struct PrefillWork {
 // ragged path's instantiation carries none of that code.
 // PREFIX: the instantiation for steps with shared prefixes, which starts each
 // chunk's keys behind its prefix's blocks (all of them before the chunk, so
-// the causal mask over the rest is unchanged) and joins the prefix's records.
+// the causal mask over the rest is unchanged) and leaves records of the rows
+// that have some of a prefix.
 template <bool PADDED, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.q_len = __ldcg(a.cu_seqlens_q + it.s + 1) - it.c0;
             it.ctx = __ldcg(a.context_lens + it.s);
             it.pad = PADDED ? __ldcg(a.pad_lens + it.s) : 0;
-            if constexpr (PREFIX) it.skip = prefix_info(a, it.s).x;
+            if constexpr (PREFIX) it.skip = __ldcg(a.prefix.seq_info + 4 * it.s);
             bad = it.c0 < 0 || it.q_len < 2 || it.c0 + it.q_len > a.num_tokens || it.row0 >= it.q_len ||
                   it.ctx < it.q_len || it.ctx > a.max_context_len || it.pad < 0 || it.pad >= it.q_len;
             if (!bad) {
@@ -822,17 +828,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int e_row = it.c0 + qi, e_h = it.h, e_slot0 = it.slot0, e_j0 = sh.j0, e_ntiles = sh.n_tiles;
       const bool e_real = qi < it.q_len && (!PADDED || qi >= it.pad);   // padding rows are not written
       __nv_bfloat16* const e_dst = static_cast<__nv_bfloat16*>(a.out) + (size_t(e_row) * H + e_h) * HD;
-      const float* rec = nullptr;                  // the shared prefix's records of this row
-      int n_rec = 0;
+      float* rec = nullptr;                        // this row's own record, where it has some of a prefix
       if constexpr (PREFIX) {
-        const int4 info = prefix_info(a, it.s);
-        n_rec = e_real ? info.y : 0;
-        rec = prefix_records(a, info, e_row, e_h);
+        const int4 info = __ldcg(reinterpret_cast<const int4*>(a.prefix.seq_info) + it.s);
+        if (info.y > 0) rec = a.prefix.recs + (size_t(info.z) + size_t(qi) * H + e_h) * kPrefixRec;
       }
       if (e_slot0 < 0) {
-        float mx = m, inv;
-        if (PREFIX) prefix_row_scale(rec, n_rec, m, l, mx, inv);
-        else inv = 1.0f / l;
+        const float inv = 1.0f / l;
+        if (PREFIX && rec && e_real) *reinterpret_cast<float2*>(rec + HD) = make_float2(m, l);
         __nv_bfloat16* dst = e_dst;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -841,15 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           if (e_real) {
             uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
-            if constexpr (PREFIX) {
-              float acc[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) acc[e] = __uint_as_float(o[e]);
-              join_prefix_row(rec, n_rec, 32 * c, m, mx, inv, acc);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                d4[e] = make_uint4(pack_bf16x2(acc[8 * e], acc[8 * e + 1]), pack_bf16x2(acc[8 * e + 2], acc[8 * e + 3]),
-                                   pack_bf16x2(acc[8 * e + 4], acc[8 * e + 5]), pack_bf16x2(acc[8 * e + 6], acc[8 * e + 7]));
+            if (PREFIX && rec) {
+              store_acc(rec + 32 * c, o);
             } else {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -863,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         segment_epilogue<PREFIX>(w.partials + size_t(e_slot0) * kSlotFloats + BM * t + i,
                          w.tickets + (e_slot0 * kSegTicketsPerSlot + t * 4 + wq), (e_ntiles + seg - 1) / seg,
-                         e_j0 / seg, m, l, lane_base + 128, lane, e_dst, e_real, rec, n_rec);
+                         e_j0 / seg, m, l, lane_base + 128, lane, e_dst, e_real, rec);
       }
       tc_fence_before();                           // O read before the next unit's first P V overwrites it
       cnt += sh.n;

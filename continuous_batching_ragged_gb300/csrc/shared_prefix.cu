@@ -6,8 +6,9 @@
 // group of sequences with R query tokens and G query heads per key/value head,
 // the prefix phase is, per key/value head, a dense product of R * G query rows
 // with the prefix's keys, no mask: softmax(Q K^T) V over those keys, left
-// unnormalised as one record (acc, max, sum) per row and KV segment.  The
-// kernels that run each row's own keys join the records (prefix_merge.cuh).
+// unnormalised as one record (acc, max, sum) per row and KV segment.  The rows'
+// own keys leave records too (suffix_decode.cu, or prefill_tc.cu for chunks of
+// many query rows), and a last kernel joins each row's.
 //
 // What bounds it: the prefix's K and V once from HBM while R * G is below about
 // 256 rows (the ridge of 4 flops per row and byte pair), the tensor cores
@@ -21,8 +22,9 @@
 //     the prefill kernel does.
 // Pieces are (row tile pair, key/value head, KV segment).  The plan cuts the
 // prefix into the number of segments that minimises the estimated time of the
-// piece waves; the segments' records cost the rows' own kernels n more reads.
+// piece waves; every segment costs the join one more record per row.
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include <cuda.h>
@@ -30,6 +32,7 @@
 #include "device_common.cuh"
 #include "kernels.h"
 #include "runtime.h"
+#include "shared_prefix.h"
 #include "sm100_ptx.cuh"
 
 namespace cb {
@@ -81,47 +84,24 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 // ------------------------------------------------------------------ plan
 
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 512;
 constexpr int kMaxSegs = 64;             // KV segments of a prefix
+constexpr int kGroupCache = 512;         // groups kept in shared memory
 constexpr int kExtraPieces = 1024;       // pieces beyond one per (row tile pair, key/value head)
-constexpr int64_t kExtraRecs = 131072;   // records beyond one per row (69 MB)
+constexpr int64_t kExtraRecs = 131072;   // prefix records beyond two per row (69 MB)
 // Estimated cost of a piece beyond its KV tiles, in tiles: the Q load, the
 // pipeline's fill and the records.
 constexpr float kPieceTiles = 2.5f;
+constexpr int kSuffixTile = 16;          // keys per tile of the suffix kernel
+constexpr int kMinChunkTiles = 8;        // shortest chunk of own keys, in those tiles
+constexpr int kSuffixRows = 16;          // query rows per row tile of the suffix kernel
+constexpr int kUnitsPerWarp = 3;         // suffix units that each warp should get
+constexpr int kMaxSms = 160;             // SMs that the lists are sized for
+// Query rows per key/value head up to which a sequence's own keys go to the
+// suffix kernel, which streams them once per 16 rows; beyond, to prefill tiles.
+constexpr int kMaxWarpRows = 128;
 
-struct alignas(16) Piece {
-  int s0;                      // the group's first sequence: its table holds the prefix's blocks
-  int tok0, ntok;              // query tokens
-  int hk;                      // key/value head
-  int j0, nt;                  // KV tiles
-  int shared;                  // keys of the prefix
-  int rec;                     // this piece's (first) record of each row
-  int alt;                     // 1: one row tile, KV tiles alternate over the two slots
-  int pad[3];
-};
-static_assert(sizeof(Piece) == 48, "piece");
-
-struct PrefixWork {
-  const int32_t* cu_groups;    // [num_groups + 1]
-  const int32_t* prefix_lens;  // [num_groups]
-  const int32_t* context_lens; // [num_seqs], whole
-  int32_t num_groups;
-  int32_t num_sms;
-  int32_t tile_tokens;         // query tokens per row tile
-  int32_t piece_cap;
-  int64_t rec_cap;
-  uint32_t tag;
-  // in the workspace
-  int32_t* header;             // [0] pieces, [1] record stride, [2] call tag, [3] claims
-  int32_t* suffix_lens;        // [num_seqs] keys behind the prefix
-  int4* seq_info;              // [num_seqs]
-  int4* groups;                // [num_groups] (first sequence, first token, tokens, shared keys)
-  int32_t* first_piece;        // [num_groups + 1]
-  Piece* pieces;
-  float* recs;
-};
-
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // Exclusive block-wide scan; `total` receives the sum.  Contains __syncthreads.
 __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
@@ -135,6 +115,7 @@ __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
   int64_t before = 0, all = 0;
+#pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
     if (w < warp) before += warp_sums[w];
     all += warp_sums[w];
@@ -144,50 +125,63 @@ __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
   return before + x - v;
 }
 
-// One CTA.  Checks the groups, chooses the segments, lists the pieces and
-// leaves, per sequence, the keys behind its prefix and what to join.
+// Whether a sequence's rows go to the prefill kernel, and its row tiles otherwise.
+__device__ __forceinline__ bool is_chunk(const PrefixWork& w, int q_len, int G) {
+  return q_len > 1 && int64_t(q_len) * G > w.max_warp_rows;
+}
+
+// One CTA.  Checks the groups, chooses the segments of the prefixes and the
+// chunks of the own keys, lists the pieces and the items and gives every row
+// its records.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArgs a, const PrefixWork w) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // they wait for this grid on the device
   __shared__ int64_t warp_sums[kPlanThreads / 32];
   __shared__ float best_cost[kMaxSegs];
+  __shared__ int4 gcache[kGroupCache];
   __shared__ int s_n, s_alt;
   const int tid = threadIdx.x;
-  const int S = a.num_seqs, NG = w.num_groups, TT = w.tile_tokens, Hkv = a.num_kv_heads;
+  const int S = a.num_seqs, T = a.num_tokens, NG = w.num_groups, TT = w.tile_tokens;
+  const int H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv;
   const int32_t* cu = a.cu_seqlens_q;
-
-  // the groups have to cover the sequences in order
-  int bad = 0;
-  for (int g = tid; g < NG; g += kPlanThreads) {
-    const int s0 = w.cu_groups[g], s1 = w.cu_groups[g + 1];
-    if (s0 < 0 || s1 < s0 || s1 > S || (g == 0 && s0 != 0) || (g == NG - 1 && s1 != S)) bad = 1;
-  }
-  if (tid == 0) s_alt = 0;
-  bad = __syncthreads_or(bad);
-  if (bad) {                                       // no sequence can be told its prefix: nothing runs
+  auto group = [&](int g) -> int4 { return g < kGroupCache ? gcache[g] : w.groups[g]; };
+  auto set_header = [&](int pieces, int stride, int items) {
+    w.header[0] = pieces;
+    w.header[1] = stride;
+    w.header[2] = int32_t(w.tag);
+    w.header[3] = 0;
+    w.header[4] = items;
+    w.header[5] = 0;
+  };
+  // nothing runs and no row is written
+  auto give_up = [&]() {
     for (int s = tid; s < S; s += kPlanThreads) {
       w.suffix_lens[s] = 0;
       w.seq_info[s] = make_int4(0, 0, 0, 0);
     }
+    for (int t = tid; t < T; t += kPlanThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
     if (tid == 0) {
       raise_error(a.err, kErrInvalid);
-      w.header[0] = 0;
-      w.header[1] = 0;
-      w.header[2] = int32_t(w.tag);
-      w.header[3] = 0;
+      set_header(0, 0, 0);
     }
-    return;
-  }
+  };
 
   // Each group's shared keys: whole blocks of its prefix, for at least two
   // sequences.  Where the first sequence, whose table names the blocks, does
-  // not hold them, every sequence of the group reads its own.
+  // not hold them, every sequence of the group reads its own.  The groups have
+  // to cover the sequences in order.
+  if (tid == 0) s_alt = 0;
+  __syncthreads();
+  int bad = 0;
   int64_t pairs_sum = 0;
   for (int g = tid; g < NG; g += kPlanThreads) {
     const int s0 = w.cu_groups[g], s1 = w.cu_groups[g + 1], p = w.prefix_lens[g];
     int t0 = 0, tokens = 0, shared = 0;
-    if (s1 - s0 >= 2 && p >= a.block_size) {
+    if (s0 < 0 || s1 < s0 || s1 > S || (g == 0 && s0 != 0) || (g == NG - 1 && s1 != S)) {
+      bad = 1;
+    } else if (s1 - s0 >= 2 && p >= a.block_size) {
       t0 = cu[s0];
       const int t1 = cu[s1], q0 = cu[s0 + 1] - t0, ctx0 = w.context_lens[s0];
-      if (t0 >= 0 && t1 <= a.num_tokens && t1 > t0 && q0 >= 1 && ctx0 <= a.max_context_len && ctx0 - q0 >= p &&
+      if (t0 >= 0 && t1 <= T && t1 > t0 && q0 >= 1 && ctx0 <= a.max_context_len && ctx0 - q0 >= p &&
           int64_t(ctx0) <= int64_t(a.max_blocks_per_seq) * a.block_size) {
         tokens = t1 - t0;
         shared = p / a.block_size * a.block_size;
@@ -195,23 +189,33 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
         if (tokens <= TT) s_alt = 1;
       }
     }
-    w.groups[g] = make_int4(s0, t0, tokens, shared);
+    const int4 gr = make_int4(s0, t0, tokens, shared);
+    w.groups[g] = gr;
+    if (g < kGroupCache) gcache[g] = gr;
+  }
+  if (__syncthreads_or(bad)) {                     // no sequence can be told its prefix
+    give_up();
+    return;
   }
   int64_t all_pairs;
   block_scan(pairs_sum, warp_sums, all_pairs);
-  const bool fits = all_pairs * Hkv <= w.piece_cap;   // more only if token ranges overlap (malformed metadata)
+  if (all_pairs * Hkv > w.piece_cap) {             // only if token ranges overlap (malformed metadata)
+    give_up();
+    return;
+  }
   const int alt_recs = s_alt ? 2 : 1;
-  if (!fits && tid == 0) raise_error(a.err, kErrInvalid);
 
   // Segments: the n that minimises the estimated time, n by thread.
-  if (tid < kMaxSegs) {
+  if (all_pairs == 0) {
+    if (tid == 0) s_n = 1;
+  } else if (tid < kMaxSegs) {
     const int n = tid + 1;
     float cost = 3.0e38f;
     int64_t pieces = 0;
     float work = 0.f;
     int longest = 0;
-    for (int g = 0; fits && g < NG; ++g) {
-      const int4 gr = w.groups[g];
+    for (int g = 0; g < NG; ++g) {
+      const int4 gr = group(g);
       if (gr.w == 0) continue;
       const int units = ceil_div(gr.z, 2 * TT) * Hkv, tiles = ceil_div(gr.w, BN);
       const int len = ceil_div(tiles, n), segs = ceil_div(tiles, len);
@@ -219,17 +223,17 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
       work += float(units) * (float(tiles) + kPieceTiles * segs);
       longest = max(longest, len);
     }
-    if (pieces <= w.piece_cap && int64_t(a.num_tokens) * a.num_heads * n * alt_recs <= w.rec_cap) {
+    if (pieces <= w.piece_cap && int64_t(T) * H * n * alt_recs <= w.rec_cap) {
       const float one = float(longest) + kPieceTiles;
-      const int64_t waves = (pieces + w.num_sms - 1) / w.num_sms;
+      const float waves = float((unsigned(pieces) + unsigned(w.num_sms) - 1) / unsigned(w.num_sms));
       // pieces of one size run in whole waves; unequal ones fill the gaps
-      const float even = float(waves) * one, filled = __fdividef(work, float(w.num_sms)) + 0.5f * one;
+      const float even = waves * one, filled = __fdividef(work, float(w.num_sms)) + 0.5f * one;
       cost = (NG == 1 ? even : fminf(even, fmaxf(filled, one))) + 0.05f * float(n);
     }
     best_cost[tid] = cost;
   }
   __syncthreads();
-  if (tid == 0) {
+  if (tid == 0 && all_pairs > 0) {
     int n = 1;
     for (int k = 1; k < kMaxSegs; ++k)
       if (best_cost[k] < best_cost[n - 1]) n = k + 1;
@@ -238,56 +242,130 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   __syncthreads();
   const int n = s_n, stride = n * alt_recs;
 
-  // what each sequence joins
+  // Each sequence: what its prefix covers, and the tiles of its own keys.
+  int64_t unit_tiles = 0;
   for (int s = tid; s < S; s += kPlanThreads) {
     int lo = 0, hi = NG - 1;                       // the last group starting at or before s (empty groups start there too)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (w.cu_groups[mid] <= s) lo = mid; else hi = mid - 1;
+      if (group(mid).x <= s) lo = mid; else hi = mid - 1;
     }
-    const int4 gr = w.groups[lo];
-    const int p = w.prefix_lens[lo], ctx = w.context_lens[s], q_len = cu[s + 1] - cu[s];
-    const int shared = fits ? gr.w : 0;
-    if (p < 0 || q_len < 1 || ctx < q_len || p > ctx - q_len || ctx > a.max_context_len ||
-        int64_t(ctx) > int64_t(a.max_blocks_per_seq) * a.block_size) {
-      raise_error(a.err, kErrInvalid);             // left out: the step plan refuses a length of 0
+    const int4 gr = group(lo);
+    const int p = w.prefix_lens[lo], ctx = w.context_lens[s], c0 = cu[s], q_len = cu[s + 1] - c0;
+    if (p < 0 || q_len < 1 || c0 < 0 || c0 + q_len > T || q_len > a.max_q_len || ctx < q_len || p > ctx - q_len ||
+        ctx > a.max_context_len || int64_t(ctx) > int64_t(a.max_blocks_per_seq) * a.block_size) {
+      raise_error(a.err, kErrInvalid);             // left out
       w.suffix_lens[s] = 0;
       w.seq_info[s] = make_int4(0, 0, 0, 0);
       continue;
     }
-    const int tiles = ceil_div(shared, BN), len = shared > 0 ? ceil_div(tiles, n) : 1;
+    const int tiles = ceil_div(gr.w, BN), len = gr.w > 0 ? ceil_div(tiles, n) : 1;
     const int segs = ceil_div(tiles, len);
-    w.suffix_lens[s] = ctx - shared;
-    w.seq_info[s] = make_int4(shared / a.block_size, segs * (gr.z <= TT ? 2 : 1), stride, 0);
+    const bool chunk = is_chunk(w, q_len, G);
+    w.suffix_lens[s] = ctx - gr.w;
+    w.seq_info[s] = make_int4(gr.w / a.block_size, segs * (gr.z <= TT ? 2 : 1), 0, chunk ? 1 : 0);
+    if (!chunk) unit_tiles += int64_t(ceil_div(q_len * G, kSuffixRows)) * Hkv * ceil_div(ctx - gr.w, kSuffixTile);
+  }
+  int64_t all_tiles;
+  block_scan(unit_tiles, warp_sums, all_tiles);
+  // chunk length: the suffix kernel's units come out even over its warps
+  const int64_t per = (all_tiles + w.suffix_units - 1) / w.suffix_units;
+  const int L = int(per < kMinChunkTiles ? kMinChunkTiles : (per > (1 << 26) ? (1 << 26) : per));
+
+  // Items and records.  (Each thread reads back its own sequences' entries.)
+  int64_t base = 0;                                // items in the low, records in the high word
+  for (int s0 = 0; s0 < S; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    int64_t n_items = 0, n_recs = 0;
+    int4 info = make_int4(0, 0, 0, 0);
+    int own = 0, c0 = 0, q_len = 0, rt = 0, nch = 0;
+    if (s < S) {
+      own = w.suffix_lens[s];
+      if (own > 0) {
+        info = w.seq_info[s];
+        c0 = cu[s];
+        q_len = cu[s + 1] - c0;
+        nch = info.w ? 1 : ceil_div(ceil_div(own, kSuffixTile), L);
+        rt = info.w ? 0 : ceil_div(q_len * G, kSuffixRows);
+        n_items = int64_t(rt) * nch;
+        n_recs = info.y + nch > 1 ? int64_t(q_len) * H * nch : 0;
+      }
+    }
+    int64_t total;
+    const int64_t at = base + block_scan(n_items | (n_recs << 32), warp_sums, total);
+    base += total;
+    if ((base & 0xffffffff) > w.item_cap || (base >> 32) > w.own_cap) {   // only if token ranges overlap
+      __syncthreads();
+      give_up();
+      return;
+    }
+    if (own > 0) {
+      info.z = int(at >> 32);
+      w.seq_info[s] = info;
+      SuffixItem it;
+      it.s = s, it.tok0 = c0, it.q_len = q_len, it.ctx = own, it.skip = info.x, it.base = info.z, it.nch = nch;
+      it.direct = n_recs == 0;
+      SuffixItem* out = w.items + (at & 0xffffffff);
+      for (int r = 0; r < rt; ++r)
+        for (int c = 0; c < nch; ++c) {
+          it.row0 = r * kSuffixRows;
+          it.chunk = c;
+          it.k0 = c * L * kSuffixTile;
+          it.k1 = min(own, it.k0 + L * kSuffixTile);
+          *out++ = it;
+        }
+    }
+  }
+  __syncthreads();                                 // every sequence's info is written
+  for (int t = tid; t < T; t += kPlanThreads) {
+    int lo = t < S ? t : S - 1;
+    if (cu[lo] != t) {                             // not all sequences before have one token
+      lo = 0;
+      int hi = S - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+    }
+    int4 ti = make_int4(0, 0, 0, 0);
+    const int own = w.suffix_lens[lo];
+    if (own > 0 && cu[lo] <= t && t < cu[lo + 1]) {
+      const int4 info = w.seq_info[lo];
+      const int nch = info.w ? 1 : ceil_div(ceil_div(own, kSuffixTile), L);
+      ti = make_int4(info.y, info.z + (t - cu[lo]) * H * nch, nch, 0);
+    }
+    w.token_info[t] = ti;
   }
 
   // the pieces: by segment, key/value head and row tile pair, so that the
   // pairs of one (segment, head) run side by side and share its K/V in L2
-  int64_t base = 0;
-  for (int g0 = 0; g0 < NG; g0 += kPlanThreads) {
-    const int g = g0 + tid;
-    int64_t count = 0;
-    if (fits && g < NG) {
-      const int4 gr = w.groups[g];
-      if (gr.w > 0) {
-        const int tiles = ceil_div(gr.w, BN), len = ceil_div(tiles, n);
-        count = int64_t(ceil_div(gr.z, 2 * TT)) * Hkv * ceil_div(tiles, len);
+  int64_t pbase = 0;
+  if (all_pairs > 0) {
+    for (int g0 = 0; g0 < NG; g0 += kPlanThreads) {
+      const int g = g0 + tid;
+      int64_t count = 0;
+      if (g < NG) {
+        const int4 gr = group(g);
+        if (gr.w > 0) {
+          const int tiles = ceil_div(gr.w, BN), len = ceil_div(tiles, n);
+          count = int64_t(ceil_div(gr.z, 2 * TT)) * Hkv * ceil_div(tiles, len);
+        }
       }
+      int64_t total;
+      const int64_t at = pbase + block_scan(count, warp_sums, total);
+      if (g < NG) w.first_piece[g] = int(at);
+      pbase += total;
     }
-    int64_t total;
-    const int64_t at = base + block_scan(count, warp_sums, total);
-    if (g < NG) w.first_piece[g] = int(at);
-    base += total;
+    __syncthreads();
   }
-  __syncthreads();
-  const int n_pieces = int(base);
+  const int n_pieces = int(pbase);
   for (int i = tid; i < n_pieces; i += kPlanThreads) {
     int lo = 0, hi = NG - 1;                       // the last group whose pieces start at or before i
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (w.first_piece[mid] <= i) lo = mid; else hi = mid - 1;
     }
-    const int4 gr = w.groups[lo];
+    const int4 gr = group(lo);
     const int tiles = ceil_div(gr.w, BN), len = ceil_div(tiles, n), pairs = ceil_div(gr.z, 2 * TT);
     const int local = i - w.first_piece[lo];
     const int pair = local % pairs, hk = local / pairs % Hkv, seg = local / (pairs * Hkv);
@@ -306,12 +384,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     pc.alt = alt;
     w.pieces[i] = pc;
   }
-  if (tid == 0) {
-    w.header[0] = n_pieces;
-    w.header[1] = stride;
-    w.header[2] = int32_t(w.tag);
-    w.header[3] = 0;
-  }
+  if (tid == 0) set_header(n_pieces, stride, int(base & 0xffffffff));
 }
 
 // ------------------------------------------------------------------ prefix phase
@@ -407,8 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, kErrInvalid);
     n_pieces = 0;
   }
-  // the kernel behind this one may start on the SMs that this grid leaves; it
-  // waits for the records on the device
+  // the plan is complete: the kernel behind this one may start on the SMs that
+  // this grid leaves
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (int(blockIdx.x) >= n_pieces) return;
 
@@ -840,17 +913,23 @@ bool g_attr_set[64] = {};
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Capacities of a step's lists, and whether the step may hold prefill chunks.
 struct PrefixSizes {
-  size_t S, T, NG, pieces, recs;
+  size_t S, T, NG, pieces, items, recs, own, units;
+  bool chunks;
 };
 PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups) {
   PrefixSizes z;
   z.S = size_t(num_seqs), z.T = size_t(num_tokens), z.NG = size_t(num_groups);
-  const size_t pair_tokens = 2 * size_t(prefix_tile_tokens(num_q_heads / num_kv_heads));
+  const size_t G = size_t(num_q_heads / num_kv_heads), rows = z.T * size_t(num_q_heads);
   // a group that shares has two sequences or more
-  z.pieces = size_t(num_kv_heads) * (z.T / pair_tokens + std::min(z.NG, z.S / 2) + 1) + kExtraPieces;
-  const size_t rows = z.T * size_t(num_q_heads);
+  z.pieces = size_t(num_kv_heads) * (z.T / (2 * size_t(prefix_tile_tokens(int(G)))) + std::min(z.NG, z.S / 2) + 1) + kExtraPieces;
   z.recs = std::min(rows * 2 * kMaxSegs, rows * 2 + size_t(kExtraRecs));
+  z.units = size_t(kMaxSms) * kSuffixWarps * kUnitsPerWarp;
+  // ceil(x / L) <= x / L + 1 for every sequence, and all x / L together are at most `units`
+  z.items = z.T * G / kSuffixRows + z.S + z.units + 1;
+  z.own = rows + kSuffixRows * z.units;
+  z.chunks = z.T > z.S && (z.T - z.S + 1) * G > size_t(kMaxWarpRows);
   return z;
 }
 
@@ -859,42 +938,12 @@ PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_
 int prefix_tile_tokens(int group_heads) { return BM / group_heads; }
 
 size_t prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
-                              int32_t num_groups) {
+                              int32_t num_groups, int32_t head_dim, int32_t max_context_len) {
   const PrefixSizes z = prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups);
   return 256 + align256(z.S * 4) + align256(z.S * 16) + align256(z.NG * 16) + align256((z.NG + 1) * 4) +
-         align256(z.pieces * sizeof(Piece)) + z.recs * kPrefixRec * sizeof(float);
-}
-
-// The prefix part of a step: its plan now, its kernel with launch_prefix.  `a` has the
-// whole context lengths; on return it describes the keys behind the prefixes.
-static cb_status prefix_layout(AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
-                               void* workspace, uint32_t tag, PrefixWork* w) {
-  const PrefixSizes z = prefix_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups);
-  if (z.pieces > 0x7FFFFFFF) return fail(CB_ERR_UNSUPPORTED, "shared prefixes: too many tokens");
-  w->cu_groups = cu_groups;
-  w->prefix_lens = prefix_lens;
-  w->context_lens = a.context_lens;
-  w->num_groups = num_groups;
-  w->num_sms = sm_count();
-  w->tile_tokens = prefix_tile_tokens(a.num_heads / a.num_kv_heads);
-  w->piece_cap = int32_t(z.pieces);
-  w->rec_cap = int64_t(z.recs);
-  w->tag = tag;
-  char* p = static_cast<char*>(workspace);
-  w->header = reinterpret_cast<int32_t*>(p);
-  p += 256;
-  w->suffix_lens = reinterpret_cast<int32_t*>(p);
-  p += align256(z.S * 4);
-  w->seq_info = reinterpret_cast<int4*>(p);
-  p += align256(z.S * 16);
-  w->groups = reinterpret_cast<int4*>(p);
-  p += align256(z.NG * 16);
-  w->first_piece = reinterpret_cast<int32_t*>(p);
-  p += align256((z.NG + 1) * 4);
-  w->pieces = reinterpret_cast<Piece*>(p);
-  p += align256(z.pieces * sizeof(Piece));
-  w->recs = reinterpret_cast<float*>(p);
-  return CB_OK;
+         align256(z.pieces * sizeof(Piece)) + align256(z.items * sizeof(SuffixItem)) + align256(z.T * 16) +
+         align256(z.recs * kPrefixRec * sizeof(float)) + align256(z.own * kPrefixRec * sizeof(float)) +
+         (z.chunks ? step_workspace_bytes(num_seqs, num_tokens, num_q_heads, head_dim, max_context_len) : 0);
 }
 
 static cb_status launch_prefix_tc(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
@@ -941,43 +990,79 @@ static cb_status launch_prefix_tc(const AttnArgs& a, const PrefixWork& w, cudaSt
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: launch");
 }
 
-// A step with shared prefixes on one stream: the prefix plan, the step plan over the keys behind
-// the prefixes, the prefix kernel, then the kernels of the rows' own keys, which start on the SMs
-// that the prefix kernel leaves and wait for its records before they join them.
+// A step with shared prefixes on one stream: the plan, the prefix kernel, the
+// kernels of the rows' own keys and the join.  Each starts as a programmatic
+// dependent of the one before: the own keys' kernel runs beside the prefix
+// kernel on the SMs that one leaves, and ends only after it.
 cb_status run_shared_prefix(AttnArgs a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
                             void* workspace, cudaStream_t stream) {
-  const size_t own = step_workspace_bytes(a.num_seqs, a.num_tokens, a.num_heads, a.head_dim, a.max_context_len);
+  NvtxRange nvtx("cb.shared_prefix");
   if (int64_t(a.num_blocks) * a.num_kv_heads >= (int64_t(1) << 31))
     return fail(CB_ERR_UNSUPPORTED, "shared prefixes: num_blocks * num_kv_heads must fit in int32");
-  StepPlan plan;
-  cb_status st = step_plan_layout(workspace, own, a.num_seqs, a.num_tokens, a.num_heads, a.head_dim, a.max_context_len, &plan);
-  if (st != CB_OK) return st;
+  const int G = a.num_heads / a.num_kv_heads;
+  const PrefixSizes z = prefix_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups);
+  if (z.pieces > 0x7FFFFFFF || z.items > size_t(0x7FFFFFFF / a.num_kv_heads) || z.own > 0x7FFFFFFF)
+    return fail(CB_ERR_UNSUPPORTED, "shared prefixes: too many tokens");
   PrefixWork w;
-  st = prefix_layout(a, cu_groups, prefix_lens, num_groups, static_cast<char*>(workspace) + align256(own), plan.tag, &w);
-  if (st != CB_OK) return st;
+  w.cu_groups = cu_groups;
+  w.prefix_lens = prefix_lens;
+  w.context_lens = a.context_lens;
+  w.num_groups = num_groups;
+  w.num_sms = sm_count();
+  w.tile_tokens = prefix_tile_tokens(G);
+  // a sequence has at most num_tokens - num_seqs + 1 tokens, which z.chunks says
+  const bool chunks = z.chunks && a.max_q_len > 1 && int64_t(a.max_q_len) * G > kMaxWarpRows;
+  w.max_warp_rows = chunks ? kMaxWarpRows : INT32_MAX;
+  w.suffix_units = std::min(w.num_sms, kMaxSms) * kSuffixWarps * kUnitsPerWarp;
+  w.piece_cap = int32_t(z.pieces);
+  w.item_cap = int32_t(z.items);
+  w.rec_cap = int64_t(z.recs);
+  w.own_cap = int64_t(z.own);
+  char* p = static_cast<char*>(workspace);
+  auto take = [&p](size_t bytes) {
+    char* at = p;
+    p += align256(bytes);
+    return at;
+  };
+  w.header = reinterpret_cast<int32_t*>(take(256));
+  w.suffix_lens = reinterpret_cast<int32_t*>(take(z.S * 4));
+  w.seq_info = reinterpret_cast<int4*>(take(z.S * 16));
+  w.groups = reinterpret_cast<int4*>(take(z.NG * 16));
+  w.first_piece = reinterpret_cast<int32_t*>(take((z.NG + 1) * 4));
+  w.pieces = reinterpret_cast<Piece*>(take(z.pieces * sizeof(Piece)));
+  w.items = reinterpret_cast<SuffixItem*>(take(z.items * sizeof(SuffixItem)));
+  w.token_info = reinterpret_cast<int4*>(take(z.T * 16));
+  w.recs = reinterpret_cast<float*>(take(z.recs * kPrefixRec * sizeof(float)));
+  w.own_recs = reinterpret_cast<float*>(take(z.own * kPrefixRec * sizeof(float)));
+  static std::atomic<uint32_t> next_tag{1};
+  w.tag = next_tag.fetch_add(1);
+
   prefix_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, w);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: plan launch");
-
-  a.context_lens = w.suffix_lens;
-  a.prefix.seq_info = reinterpret_cast<const int32_t*>(w.seq_info);
-  a.prefix.recs = w.recs;
-  set_decode_plan(a, &plan);
-  plan.split_sms = 1;
-  st = launch_plan(a, plan, stream);
-  if (st != CB_OK) return st;
-  {
-    NvtxRange nvtx("cb.prefix");
-    st = launch_prefix_tc(a, w, stream);
+  AttnArgs own = a;                                // the prefill chunks' view of the step
+  StepPlan plan;
+  cb_status st;
+  if (chunks) {
+    const size_t bytes = step_workspace_bytes(a.num_seqs, a.num_tokens, a.num_heads, a.head_dim, a.max_context_len);
+    st = step_plan_layout(p, bytes, a.num_seqs, a.num_tokens, a.num_heads, a.head_dim, a.max_context_len, &plan);
+    if (st != CB_OK) return st;
+    own.context_lens = w.suffix_lens;
+    own.prefix.seq_info = reinterpret_cast<const int32_t*>(w.seq_info);
+    own.prefix.recs = w.own_recs;
+    set_decode_plan(own, &plan);
+    st = launch_plan(own, plan, stream);
     if (st != CB_OK) return st;
   }
-  if (a.max_q_len == 1) {
-    a.prefix.wait = 1;
-    return launch_decode_persistent(a, plan, true, false, stream);
-  }
-  st = launch_prefill_tc(a, plan, true, stream);
+  st = launch_prefix_tc(a, w, stream);
   if (st != CB_OK) return st;
-  return launch_decode_persistent(a, plan, true, false, stream);
+  if (chunks) {
+    st = launch_prefill_tc(own, plan, true, stream);
+    if (st != CB_OK) return st;
+  }
+  st = launch_suffix(a, w, stream);
+  if (st != CB_OK) return st;
+  return launch_join(a, w, stream);
 }
 
 }  // namespace cb

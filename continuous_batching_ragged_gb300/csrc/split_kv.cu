@@ -29,7 +29,6 @@
 
 #include "device_common.cuh"
 #include "kernels.h"
-#include "prefix_merge.cuh"
 #include "runtime.h"
 #include "sm100_ptx.cuh"
 
@@ -428,7 +427,6 @@ __global__ void __launch_bounds__(kWarps * 32) split_kv_kernel(const SplitArgs s
 struct Unit {
   int u;                      // claimed unit index; >= the unit count: no more work
   int s, t, grp, h0, hkv, split, nsplit, k0, k1;
-  int skip;                   // blocks of the table that belong to a shared prefix (PREFIX)
 };
 
 // Shared scratch of the epilogue of a unit of GU query heads.
@@ -439,29 +437,15 @@ struct GroupSmem {
   int last;
 };
 
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // Combine the warps' (m, l, acc) of each of the unit's GU heads, then either
 // write the output rows (one split) or publish the partials and, in the last
 // CTA of the (sequence, group) to finish, merge every split by log-sum-exp.
-// PREFIX: a row's result is first joined with its shared prefix's records.
-template <int GU, bool PREFIX>
+template <int GU>
 __device__ __forceinline__ void finish_group(const SplitArgs& sa, const Unit& U, const float (&m_run)[GU],
                                              const float (&l_run)[GU], float (&acc)[GU][8], GroupSmem<GU>& sm) {
   using T = __nv_bfloat16;
   constexpr int A = 128, EPV = 8, LPR = 16;
   const AttnArgs& a = sa.a;
-  // the row's value in dimension d from its own state (o, M, L)
-  auto finish = [&](int h, int d, float o, float M, float L) -> float {
-    if constexpr (PREFIX) {
-      if (a.prefix.wait) grid_dependency_wait();
-      const int4 info = prefix_info(a, U.s);
-      if (info.y > 0) return join_prefix_dim(prefix_records(a, info, U.t, h), info.y, d, o, M, L);
-    }
-    return o / L;
-  };
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
   const int g = lane / LPR, c = lane % LPR;
@@ -497,7 +481,7 @@ __device__ __forceinline__ void finish_group(const SplitArgs& sa, const Unit& U,
     }
     const int h = U.h0 + hh;
     if (U.nsplit == 1) {
-      store1(static_cast<T*>(a.out) + (size_t(U.t) * H + h) * A + d, finish(h, d, o, M, L));
+      store1(static_cast<T*>(a.out) + (size_t(U.t) * H + h) * A + d, o / L);
     } else {
       float* part = part0 + (size_t(h) * sa.max_splits + U.split) * (A + 2);
       part[d] = o;
@@ -531,8 +515,12 @@ __device__ __forceinline__ void finish_group(const SplitArgs& sa, const Unit& U,
       LL = fmaf(__ldcg(pk + A + 1), f, LL);
       oo = fmaf(__ldcg(pk + d), f, oo);
     }
-    store1(static_cast<T*>(a.out) + (size_t(U.t) * H + h) * A + d, finish(h, d, oo, MM, LL));
+    store1(static_cast<T*>(a.out) + (size_t(U.t) * H + h) * A + d, oo / LL);
   }
+}
+
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int GU>
@@ -550,9 +538,7 @@ constexpr uint32_t bulk_smem_bytes() {
 // current unit it goes on with the first tiles of the unit the CTA claimed
 // next, so the copies of the next unit are in flight while the current one
 // is merged and written.
-// PREFIX: the instantiation for steps with shared prefixes, which starts each
-// row behind its prefix's blocks and joins the prefix's records into it.
-template <int GU, bool PREFIX>
+template <int GU>
 __global__ void __launch_bounds__(kWarps * 32, 2) split_kv_persistent_kernel(const SplitArgs sa) {
   using T = __nv_bfloat16;
   constexpr int A = 128, EPV = 8, LPR = 16, RPL = 2, NR = 8;
@@ -582,14 +568,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) split_kv_persistent_kernel(con
   const int n_items = __ldcg(sa.header);
   if (seen_tag != sa.tag || n_items < 0 || n_items > sa.item_cap || __ldcg(sa.header + 5) < kSplitKeys) {
     if (threadIdx.x == 0) raise_error(a.err, kErrInvalid);
-    if (PREFIX && a.prefix.wait) grid_dependency_wait();
     return;
   }
   const int n_units = n_items * n_groups;
-  if (int(blockIdx.x) >= n_units) {         // no unit could be left for this CTA
-    if (PREFIX && a.prefix.wait) grid_dependency_wait();   // this grid ends after the prefix kernel
-    return;
-  }
+  if (int(blockIdx.x) >= n_units) return;   // no unit could be left for this CTA
   const int split_keys = __ldcg(sa.header + 5);            // keys per split, chosen by the plan
   const T* kp = static_cast<const T*>(a.k_pool);
   const T* vp = static_cast<const T*>(a.v_pool);
@@ -614,7 +596,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) split_kv_persistent_kernel(con
         ctx = __ldcg(a.context_lens + U.s);
         U.nsplit = (ctx + split_keys - 1) / split_keys;
         bad = U.t < 0 || U.t >= a.num_tokens || ctx < 1 || ctx > a.max_context_len || U.split >= U.nsplit;
-        if constexpr (PREFIX) U.skip = prefix_info(a, U.s).x;
       }
       if (bad) {                            // never happens with a plan from this call
         raise_error(a.err, kErrInvalid);
@@ -645,7 +626,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) split_kv_persistent_kernel(con
       const int j0 = U.k0 + (warp + kWarps * o) * kTile;
       const int st = issued % kStages;
       const uint32_t bar = sm100::smem_u32(&bars[st]);
-      const int blk = a.block_tables[size_t(U.s) * a.max_blocks_per_seq + (PREFIX ? U.skip : 0) + j0 / B];
+      const int blk = a.block_tables[size_t(U.s) * a.max_blocks_per_seq + j0 / B];
       if (blk >= 0 && blk < a.num_blocks) {
         valid[st] = 1;
         const size_t off = size_t(blk) * blk_stride + size_t(U.hkv) * B * A + size_t(j0 % B) * A;
@@ -743,7 +724,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) split_kv_persistent_kernel(con
 #pragma unroll
       for (int hh = 0; hh < GU; ++hh) l_run[hh] = warp_sum(l_run[hh]);
     }
-    finish_group<GU, PREFIX>(sa, U0, m_run, l_run, acc, sm);
+    finish_group<GU>(sa, U0, m_run, l_run, acc, sm);
     U0 = U1;
     n0 = n1;
     i0 = i1;
@@ -801,7 +782,7 @@ float decode_rate_per_sm(int group_heads) {
   }
 }
 
-template <int GU, bool PREFIX>
+template <int GU>
 static int persistent_ctas(int dev) {
   // One-time, per-device set-up; first calls may come from several host
   // threads at once, so it runs under a lock.
@@ -810,10 +791,10 @@ static int persistent_ctas(int dev) {
   static bool ready[64] = {};
   std::lock_guard<std::mutex> lock(mu);
   if (!ready[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(split_kv_persistent_kernel<GU, PREFIX>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(bulk_smem_bytes<GU>()));
+    cudaError_t e = cudaFuncSetAttribute(split_kv_persistent_kernel<GU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(bulk_smem_bytes<GU>()));
     if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas_per_sm[dev], split_kv_persistent_kernel<GU, PREFIX>,
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas_per_sm[dev], split_kv_persistent_kernel<GU>,
                                                         kWarps * 32, bulk_smem_bytes<GU>());
     if (e != cudaSuccess) {
       cuda_fail(e, "split-KV: kernel attributes");
@@ -843,23 +824,16 @@ int decode_persistent_ctas(const AttnArgs& a) {
     fail(CB_ERR_UNSUPPORTED, "decode: no usable current device");
     return 0;
   }
-  const bool prefix = a.prefix.seq_info != nullptr;
   switch (decode_group_heads(a)) {
-    case 4: return prefix ? persistent_ctas<4, true>(dev) : persistent_ctas<4, false>(dev);
-    case 3: return prefix ? persistent_ctas<3, true>(dev) : persistent_ctas<3, false>(dev);
-    case 2: return prefix ? persistent_ctas<2, true>(dev) : persistent_ctas<2, false>(dev);
-    default: return prefix ? persistent_ctas<1, true>(dev) : persistent_ctas<1, false>(dev);
+    case 4: return persistent_ctas<4>(dev);
+    case 3: return persistent_ctas<3>(dev);
+    case 2: return persistent_ctas<2>(dev);
+    default: return persistent_ctas<1>(dev);
   }
 }
 
 static bool persistent_ok(const AttnArgs& a) {
   return a.dtype == CB_DTYPE_BF16 && a.head_dim == 128 && a.block_size % kTile == 0;
-}
-
-template <int GU>
-static cudaError_t launch_persistent(const SplitArgs& sa, unsigned grid, bool after_plan, cudaStream_t stream) {
-  return launch_kernel(sa.a.prefix.seq_info ? split_kv_persistent_kernel<GU, true> : split_kv_persistent_kernel<GU, false>,
-                       dim3(grid), dim3(kWarps * 32), bulk_smem_bytes<GU>(), stream, after_plan, sa);
 }
 
 cb_status launch_decode_persistent(const AttnArgs& a, const StepPlan& plan, bool after_plan,
@@ -903,10 +877,21 @@ cb_status launch_decode_persistent(const AttnArgs& a, const StepPlan& plan, bool
   if (grid < 1) return CB_OK;
   cudaError_t e;
   switch (gu) {
-    case 4: e = launch_persistent<4>(sa, unsigned(grid), after_plan, stream); break;
-    case 3: e = launch_persistent<3>(sa, unsigned(grid), after_plan, stream); break;
-    case 2: e = launch_persistent<2>(sa, unsigned(grid), after_plan, stream); break;
-    default: e = launch_persistent<1>(sa, unsigned(grid), after_plan, stream);
+    case 4:
+      e = launch_kernel(split_kv_persistent_kernel<4>, dim3(unsigned(grid)), dim3(kWarps * 32), bulk_smem_bytes<4>(),
+                        stream, after_plan, sa);
+      break;
+    case 3:
+      e = launch_kernel(split_kv_persistent_kernel<3>, dim3(unsigned(grid)), dim3(kWarps * 32), bulk_smem_bytes<3>(),
+                        stream, after_plan, sa);
+      break;
+    case 2:
+      e = launch_kernel(split_kv_persistent_kernel<2>, dim3(unsigned(grid)), dim3(kWarps * 32), bulk_smem_bytes<2>(),
+                        stream, after_plan, sa);
+      break;
+    default:
+      e = launch_kernel(split_kv_persistent_kernel<1>, dim3(unsigned(grid)), dim3(kWarps * 32), bulk_smem_bytes<1>(),
+                        stream, after_plan, sa);
   }
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "split-KV: persistent launch");
 }

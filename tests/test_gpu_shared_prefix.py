@@ -165,17 +165,16 @@ def test_peaked_rows(native_lib):
     run_checked([(1500, [(3, 1), (200, 1)] * 5)], 8, 8, 16, seed=6, q_scale=8.0)
 
 
-def test_equals_ragged_without_sharing(native_lib):
-    """Groups of one sequence share nothing: the bits of cb_ragged_attention_gqa."""
-    from continuous_batching_ragged_gb300 import api
-    st = Step([(300, [(7, 1)]), (900, [(1, 1)]), (0, [(200, 150)]), (64, [(30, 5)])], 8, 2, 16, seed=7)
-    st.run()
-    n = api.cb_attention_workspace_size_gqa(st.cache, 8, 4, st.q.shape[0], st.max_ctx)
-    other = api.cb_ragged_attention_gqa(st.q, st.cache, st.cu, st.ctx, st.tables, max_q_len=st.max_q, max_context_len=st.max_ctx,
-                                        scale=st.scale, out=torch.empty_like(st.q),
-                                        workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
-    api.cb_check_device_errors()
-    assert torch.equal(st.out, other)
+def test_without_sharing(native_lib):
+    """Groups of one sequence share nothing: every sequence reads its own pages, single rows and chunks."""
+    run_checked([(300, [(7, 1)]), (900, [(1, 1)]), (0, [(200, 150)]), (64, [(30, 5)]), (5000, [(1, 1)]), (0, [(1, 1)])],
+                8, 2, 16, seed=7)
+
+
+@pytest.mark.parametrize("H,K", [(8, 8), (32, 8), (16, 1), (32, 1)])
+def test_long_own_keys(native_lib, H, K):
+    """Own keys cut into chunks (several records a row), with and without a prefix, one and several query tokens."""
+    run_checked([(40, [(9000, 1), (5, 1), (700, 3)]), (0, [(4000, 1), (2500, 40)]), (2000, [(6000, 2)])], H, K, 16, seed=30 + H + K)
 
 
 def test_infinite_and_nan_keys_of_others(native_lib):
