@@ -20,8 +20,11 @@ _DTYPES = {torch.bfloat16: native.CB_DTYPE_BF16, torch.float32: native.CB_DTYPE_
 
 
 def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    # torch.cuda.current_stream().cuda_stream without building a Stream object (0.2 against 2.9 us a call)
+    torch.cuda.init()
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -70,8 +73,9 @@ class KVCache:
         return self.k.shape[3]
 
     def c_struct(self) -> native.cb_kv_cache:
-        return native.cb_kv_cache(_ptr(self.k), _ptr(self.v), self.num_blocks, self.block_size,
-                                  self.num_heads, self.head_dim, _DTYPES[self.k.dtype])
+        num_blocks, num_heads, block_size, head_dim = self.k.shape
+        return native.cb_kv_cache(_ptr(self.k), _ptr(self.v), num_blocks, block_size, num_heads, head_dim,
+                                  _DTYPES[self.k.dtype])
 
 
 class KVCacheStack:
@@ -97,15 +101,17 @@ def cb_append_kv(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.T
                                     ctypes.byref(c), _stream_handle(stream)), "cb_append_kv")
 
 
-def _token_rows(t: torch.Tensor, name: str, num_tokens: int, num_heads: int, like: torch.Tensor) -> int:
-    """Pointer of [T, heads, A] rows whose tokens may be strided (parts of one projection)."""
-    if not t.is_cuda or t.dtype != like.dtype:
+def _token_rows(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype):
+    """Pointer and token stride of [T, heads, A] rows whose tokens may be strided
+    (parts of one projection)."""
+    if t.dtype != dtype or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor of the cache's dtype")
-    if t.dim() != 3 or t.shape[0] != num_tokens or t.shape[1] != num_heads or t.shape[2] != like.shape[3]:
-        raise ValueError(f"{name} must be [num_tokens, {num_heads}, head_dim]")
-    if t.stride(2) != 1 or (num_heads > 1 and t.stride(1) != t.shape[2]):
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    token, head, one = t.stride()
+    if (one != 1 and shape[2] > 1) or (head != shape[2] and shape[1] > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.data_ptr()
+    return t.data_ptr(), token if shape[0] > 1 else shape[1] * shape[2]
 
 
 def cb_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
@@ -117,31 +123,34 @@ def cb_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slot_
     the position rotation (where cos_sin, [max_positions, rot_dim] fp32, is given)
     and the append of k and v.  q, k, v: [T, heads, A], tokens may be strided.  With
     `dims`, T is the capacity and dims[1] the step's token count."""
-    T = q.shape[0]
+    if q.dim() != 3:
+        raise ValueError("q must be [num_tokens, heads, head_dim]")
+    T, heads, _ = q.shape
+    c = cache.c_struct()
+    dtype, A = cache.k.dtype, c.head_dim
     if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != T:
         raise ValueError("slot_mapping must be int64 [num_tokens]")
     if positions is not None and (positions.dtype != torch.int32 or positions.numel() != T):
         raise ValueError("positions must be int32 [num_tokens]")
     if dims is not None and dims.dtype != torch.int32:
         raise ValueError("dims must be int32")
-    if cos_sin is not None and (cos_sin.dtype != torch.float32 or cos_sin.dim() != 2):
-        raise ValueError("cos_sin must be fp32 [max_positions, rot_dim]")
+    max_positions = rot_dim = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be fp32 [max_positions, rot_dim]")
+        max_positions, rot_dim = cos_sin.shape
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and (w.dtype != cache.k.dtype or w.numel() != cache.head_dim):
+        if w is not None and (w.dtype != dtype or w.numel() != A):
             raise ValueError(f"{name} must be [head_dim] of the cache's dtype")
-    if q_out.shape != q.shape or q_out.dtype != q.dtype:
+    q_ptr, q_stride = _token_rows(q, "q", (T, heads, A), dtype)
+    k_ptr, k_stride = _token_rows(k, "k", (T, c.num_heads, A), dtype)
+    v_ptr, v_stride = _token_rows(v, "v", (T, c.num_heads, A), dtype)
+    if q_out.shape != q.shape or q_out.dtype != dtype:
         raise ValueError("q_out must have q's shape and dtype")
-    heads, kv = q.shape[1], cache.num_heads
-    a = native.cb_norm_rope(_token_rows(q, "q", T, heads, cache.k), _token_rows(k, "k", T, kv, cache.k),
-                            _token_rows(v, "v", T, kv, cache.k), *(
-                                t.stride(0) if T > 1 else t.shape[1] * t.shape[2] for t in (q, k, v)),
-                            _ptr(q_weight), _ptr(k_weight), _ptr(cos_sin),
-                            cos_sin.shape[0] if cos_sin is not None else 0,
-                            cos_sin.shape[1] if cos_sin is not None else 0, int(interleaved), eps)
-    c = cache.c_struct()
-    check(native.lib().cb_norm_rope_append(ctypes.byref(a), heads, _ptr(positions), _ptr(slot_mapping), _ptr(dims), T,
-                                           ctypes.byref(c), _ptr(q_out), _stream_handle(stream)),
-          "cb_norm_rope_append")
+    a = native.cb_norm_rope(q_ptr, k_ptr, v_ptr, q_stride, k_stride, v_stride, _ptr(q_weight), _ptr(k_weight),
+                            _ptr(cos_sin), max_positions, rot_dim, int(interleaved), eps)
+    check(native.lib().cb_norm_rope_append(a, heads, _ptr(positions), _ptr(slot_mapping), _ptr(dims), T, c, _ptr(q_out),
+                                           _stream_handle(stream)), "cb_norm_rope_append")
     return q_out
 
 
@@ -284,18 +293,20 @@ def cb_shared_prefix_attention(q: torch.Tensor, cache: KVCache, cu_seqlens_q: to
                     ("cu_groups", cu_groups), ("prefix_lens", prefix_lens)):
         if t.dtype != torch.int32:
             raise ValueError(f"{name} must be int32")
-    S, G = context_lens.shape[0], prefix_lens.shape[0]
+    (S,), (num_groups,), (T, heads, _) = context_lens.shape, prefix_lens.shape, q.shape
     if block_tables.dim() != 2 or block_tables.shape[0] != S or cu_seqlens_q.shape[0] != S + 1:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and cu_seqlens_q [num_seqs + 1]")
-    if cu_groups.shape[0] != G + 1:
+    if cu_groups.shape[0] != num_groups + 1:
         raise ValueError("cu_groups must be [num_groups + 1]")
-    c = cache.c_struct()
-    ws_ptr = _ptr(workspace) if workspace is not None and workspace.numel() else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    if out.shape != q.shape or out.dtype != q.dtype or q.dtype != cache.k.dtype:
+        raise ValueError("q and out must have one shape and the cache's dtype")
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None and workspace.numel():
+        ws_ptr, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
     check(native.lib().cb_shared_prefix_attention(
-        _ptr(q), q.shape[1], ctypes.byref(c), _ptr(cu_seqlens_q), _ptr(context_lens), _ptr(block_tables),
-        _ptr(cu_groups), _ptr(prefix_lens), G, S, q.shape[0], block_tables.shape[1], max_q_len, max_context_len,
-        float(scale), _ptr(out), ws_ptr, ws_bytes, _stream_handle(stream)), "cb_shared_prefix_attention")
+        _ptr(q), heads, cache.c_struct(), _ptr(cu_seqlens_q), _ptr(context_lens), _ptr(block_tables), _ptr(cu_groups),
+        _ptr(prefix_lens), num_groups, S, T, block_tables.shape[1], max_q_len, max_context_len, scale, _ptr(out), ws_ptr,
+        ws_bytes, _stream_handle(stream)), "cb_shared_prefix_attention")
     return out
 
 

@@ -9,21 +9,6 @@
 
 namespace cb {
 
-// A row's state over a part of its keys, as one record: acc[kPrefixDim] (the sum
-// of 2^(s - m) v over scores s in the exp2 domain), the reference maximum m, the
-// sum of 2^(s - m), padding to 16 bytes.
-constexpr int kPrefixDim = 128;
-constexpr int kPrefixRec = kPrefixDim + 4;
-
-// What the step plan and the prefill kernel need to know of a step with shared
-// prefixes (cb_shared_prefix_attention); null pointers elsewhere.
-struct PrefixView {
-  const int32_t* seq_info = nullptr;   // [num_seqs][4]: blocks of the table that the prefix covers, records
-                                       // per row that it left, the sequence's first own record, and 1 if
-                                       // the sequence's rows are a prefill chunk (else: not in this plan)
-  float* recs = nullptr;               // own records, [kPrefixRec] each: (row of the sequence, query head)
-};
-
 struct AttnArgs {
   const void* q;
   void* out;
@@ -54,10 +39,6 @@ struct AttnArgs {
   // p_s + pad - 1) are masked out of every row and their rows are not
   // written.  0 <= pad < q_len (the plan leaves a row out otherwise).
   const int32_t* pad_lens = nullptr;
-  // Shared prefixes, or null pointers: context_lens are then the keys behind
-  // the prefix, whose blocks come first in each sequence's table, and a row
-  // that has records of a prefix leaves one of its own instead of its output.
-  PrefixView prefix = {};
 };
 
 // Keys per split of the register split-KV kernel, and the smallest split of
@@ -166,12 +147,10 @@ cb_status launch_decode_tc(const AttnArgs& a, const StepPlan& plan, bool after_p
                            cudaStream_t stream);
 
 // Steps with shared prefixes (bf16, head_dim 128, block size a multiple of 16,
-// at most 128 query heads per key/value head): query tokens per row tile of
-// the prefix kernel, the workspace, and the whole step.
-int prefix_tile_tokens(int group_heads);
-size_t prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
-                              int32_t num_groups, int32_t head_dim, int32_t max_context_len);
-cb_status run_shared_prefix(AttnArgs a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
+// at most 128 query heads per key/value head): the workspace, and the step.
+size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
+                                     int32_t num_groups);
+cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
                             void* workspace, cudaStream_t stream);
 
 // Prefill chunks (q_len > 1) on tcgen05 tensor cores, bf16, head_dim 128:

@@ -132,7 +132,6 @@ __device__ __forceinline__ RowInfo row_info(const AttnArgs& a, const StepSizes& 
   r.ctx = a.context_lens[s];
   r.bad = r.q_len < 1 || r.ctx < r.q_len || r.ctx > z.max_context_len || r.q_len > z.max_q_len || c0 < 0 ||
           c1 > z.num_tokens || (int64_t(r.ctx) + a.block_size - 1) / a.block_size > a.max_blocks_per_seq;
-  if (a.prefix.seq_info && !r.bad && a.prefix.seq_info[4 * s + 3] == 0) r.q_len = 0;   // not this plan's row
   if (a.pad_lens && !r.bad) {
     const int pad = a.pad_lens[s];
     r.bad = pad < 0 || pad >= r.q_len;           // a chunk keeps at least one real row
@@ -179,7 +178,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const AttnArgs 
   launch_dependents();                      // they wait for this grid on the device
   __shared__ uint64_t warp_sums[32];
   __shared__ uint32_t bucket[kCostBuckets];
-  __shared__ int2 row_cache[kRowCache];     // (q_len, or 0 for a row left out; ctx)
+  __shared__ int2 row_cache[kRowCache];     // (q_len, or 0 for a bad row; ctx)
   const int tid = threadIdx.x;
   StepSizes z = {a.num_seqs, a.num_tokens, a.max_q_len, a.max_context_len};
   if (a.dims) {
@@ -208,7 +207,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const AttnArgs 
       raise_error(a.err, kErrInvalid);
     else if (r.q_len == 1)
       dec_keys += uint64_t(r.ctx);
-    else if (r.q_len > 1)
+    else
       any_prefill = 1;
   }
   const bool decode_only = __syncthreads_or(any_prefill) == 0;

@@ -146,24 +146,15 @@ __device__ __forceinline__ int ld_acquire_gpu(const int32_t* p) {
   return v;
 }
 
-// 32 dims of a row's record.
-__device__ __forceinline__ void store_acc(float* rec, const uint32_t (&o)[32]) {
-#pragma unroll
-  for (int e = 0; e < 32; e += 4)
-    *reinterpret_cast<uint4*>(rec + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-}
-
 // The last-arriving segment of a pair merges its warp's rows (this thread:
 // `rows`, the row in slot 0) over all nseg segments by log-sum-exp, in slot
 // order whoever arrives last, so the bits never depend on timing.  Its own
 // segment `mine` comes from TMEM (o_taddr) and registers, the same fp32
 // values its partial slot would hold; the others from their slots, two slots
 // of 32 dims in flight at a time.  Warp-wide (tcgen05.ld); `store`: this
-// thread's row is a real query row.  PREFIX: a row with a record `rec` stores its
-// unnormalised state there instead of its output.
-template <bool PREFIX>
+// thread's row is a real query row.
 __device__ __forceinline__ void merge_segments(const float* rows, int nseg, int mine, float m_own, float l_own,
-                                               uint32_t o_taddr, __nv_bfloat16* dst, bool store, float* rec) {
+                                               uint32_t o_taddr, __nv_bfloat16* dst, bool store) {
   constexpr int kM = HD * kPrefillPairRows, kL = (HD + 1) * kPrefillPairRows;
   float mx = m_own;
   for (int sg = 0; sg < nseg; ++sg)
@@ -173,8 +164,7 @@ __device__ __forceinline__ void merge_segments(const float* rows, int nseg, int 
     const float* src = rows + size_t(sg) * kSlotFloats;
     sum += sg == mine ? ex2(m_own - mx) * l_own : ex2(__ldcg(src + kM) - mx) * __ldcg(src + kL);
   }
-  const float inv = PREFIX && rec ? 1.0f : 1.0f / sum;
-  if (PREFIX && rec && store) *reinterpret_cast<float2*>(rec + HD) = make_float2(mx, sum);
+  const float inv = 1.0f / sum;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t own[32];
@@ -203,9 +193,7 @@ __device__ __forceinline__ void merge_segments(const float* rows, int nseg, int 
         for (int e = 0; e < 32; ++e) acc[e] = fmaf(w1, v1[e], acc[e]);
       }
     }
-    if (PREFIX && rec) {
-      if (store) store_acc(rec + 32 * c, reinterpret_cast<const uint32_t(&)[32]>(acc));
-    } else if (store) {
+    if (store) {
       uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -221,10 +209,8 @@ __device__ __forceinline__ void merge_segments(const float* rows, int nseg, int 
 // warp or CTA.  Every other segment first stores its unnormalised rows (acc,
 // max, sum) in its partial slot, dimension-major so a warp's 32 rows are one
 // coalesced line.  `rows`: this thread's row in the pair's first slot.
-template <bool PREFIX>
 __device__ __forceinline__ void segment_epilogue(float* rows, int32_t* ticket, int nseg, int mine, float m, float l,
-                                              uint32_t o_taddr, int lane, __nv_bfloat16* dst, bool store,
-                                              float* rec) {
+                                              uint32_t o_taddr, int lane, __nv_bfloat16* dst, bool store) {
   int merge = 0;
   if (lane == 0 && ld_acquire_gpu(ticket) == nseg - 1) {   // the others are in: no partial needed
     *ticket = 0;                                   // ready for the next call
@@ -252,7 +238,7 @@ __device__ __forceinline__ void segment_epilogue(float* rows, int32_t* ticket, i
     }
     merge = __shfl_sync(0xffffffffu, merge, 0);
   }
-  if (merge) merge_segments<PREFIX>(rows, nseg, mine, m, l, o_taddr, dst, store, rec);
+  if (merge) merge_segments(rows, nseg, mine, m, l, o_taddr, dst, store);
 }
 
 __device__ __forceinline__ void tma_prefetch_l2_3d(const void* tmap, int32_t x, int32_t y, int32_t z) {
@@ -300,8 +286,7 @@ __device__ __forceinline__ void load_kv_tile_ring(uint32_t dst, const CUtensorMa
 // segments, whose results then go to partial slots slot0 + j0 / segment).
 struct WorkItem {
   int u;                                           // entry index; >= the entry count: no more work
-  int s, h, row0, c0, q_len, ctx, j0, j1, slot0, pad;   // pad: left-padding rows of the chunk
-  int skip;                                        // blocks of the table that belong to a shared prefix (PREFIX)
+  int s, h, row0, c0, q_len, ctx, j0, j1, slot0, pad, spare;   // pad: left-padding rows of the chunk
 };
 static_assert(sizeof(WorkItem) == 48, "work item slot");
 
@@ -347,11 +332,7 @@ struct PrefillWork {
 // PADDED: the instantiation for left-padded batches (cb_padded_attention),
 // which masks each chunk's pad keys and skips its pad rows' stores; the
 // ragged path's instantiation carries none of that code.
-// PREFIX: the instantiation for steps with shared prefixes, which starts each
-// chunk's keys behind its prefix's blocks (all of them before the chunk, so
-// the causal mask over the rest is unchanged) and leaves records of the rows
-// that have some of a prefix.
-template <bool PADDED, bool PREFIX>
+template <bool PADDED>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const AttnArgs a, const PrefillWork w) {
@@ -462,7 +443,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.q_len = __ldcg(a.cu_seqlens_q + it.s + 1) - it.c0;
             it.ctx = __ldcg(a.context_lens + it.s);
             it.pad = PADDED ? __ldcg(a.pad_lens + it.s) : 0;
-            if constexpr (PREFIX) it.skip = __ldcg(a.prefix.seq_info + 4 * it.s);
             bad = it.c0 < 0 || it.q_len < 2 || it.c0 + it.q_len > a.num_tokens || it.row0 >= it.q_len ||
                   it.ctx < it.q_len || it.ctx > a.max_context_len || it.pad < 0 || it.pad >= it.q_len;
             if (!bad) {
@@ -485,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const WorkItem it = items[slot];
       if (it.u >= n_units) break;
       const UnitShape sh = unit_shape(it);
-      const int32_t* bt = a.block_tables + size_t(it.s) * a.max_blocks_per_seq + (PREFIX ? it.skip : 0);
+      const int32_t* bt = a.block_tables + size_t(it.s) * a.max_blocks_per_seq;
       // Q of this unit goes in once every S MMA of the previous unit has read
       // the old Q; the first K tiles are requested before that wait.
       auto load_q = [&]() -> bool {
@@ -557,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(BAR_IE + n % kItemSlots));
       if (it.u >= n_units) break;
       const UnitShape sh = unit_shape(it);
-      const int32_t* bt = a.block_tables + size_t(it.s) * a.max_blocks_per_seq + (PREFIX ? it.skip : 0);
+      const int32_t* bt = a.block_tables + size_t(it.s) * a.max_blocks_per_seq;
       for (int j = 0; j < min(kLookAhead, sh.n); ++j)
         stage_boxes(sh.j0 + j, j, B, it.ctx, bt, a, it.h / G, lane, ring, &tm_v);
       for (int j = 0; j < sh.n; ++j) {
@@ -828,14 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int e_row = it.c0 + qi, e_h = it.h, e_slot0 = it.slot0, e_j0 = sh.j0, e_ntiles = sh.n_tiles;
       const bool e_real = qi < it.q_len && (!PADDED || qi >= it.pad);   // padding rows are not written
       __nv_bfloat16* const e_dst = static_cast<__nv_bfloat16*>(a.out) + (size_t(e_row) * H + e_h) * HD;
-      float* rec = nullptr;                        // this row's own record, where it has some of a prefix
-      if constexpr (PREFIX) {
-        const int4 info = __ldcg(reinterpret_cast<const int4*>(a.prefix.seq_info) + it.s);
-        if (info.y > 0) rec = a.prefix.recs + (size_t(info.z) + size_t(qi) * H + e_h) * kPrefixRec;
-      }
       if (e_slot0 < 0) {
         const float inv = 1.0f / l;
-        if (PREFIX && rec && e_real) *reinterpret_cast<float2*>(rec + HD) = make_float2(m, l);
         __nv_bfloat16* dst = e_dst;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -844,22 +818,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           if (e_real) {
             uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
-            if (PREFIX && rec) {
-              store_acc(rec + 32 * c, o);
-            } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float* f = reinterpret_cast<const float*>(&o[8 * e]);
-                d4[e] = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
-                                   pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
-              }
+            for (int e = 0; e < 4; ++e) {
+              const float* f = reinterpret_cast<const float*>(&o[8 * e]);
+              d4[e] = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                                 pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
             }
           }
         }
       } else {
-        segment_epilogue<PREFIX>(w.partials + size_t(e_slot0) * kSlotFloats + BM * t + i,
+        segment_epilogue(w.partials + size_t(e_slot0) * kSlotFloats + BM * t + i,
                          w.tickets + (e_slot0 * kSegTicketsPerSlot + t * 4 + wq), (e_ntiles + seg - 1) / seg,
-                         e_j0 / seg, m, l, lane_base + 128, lane, e_dst, e_real, rec);
+                         e_j0 / seg, m, l, lane_base + 128, lane, e_dst, e_real);
       }
       tc_fence_before();                           // O read before the next unit's first P V overwrites it
       cnt += sh.n;
@@ -877,14 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 std::mutex g_attr_mutex;
-bool g_attr_set[3][64] = {};
-
-using PrefillKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const AttnArgs, const PrefillWork);
-// 0: ragged, 1: left-padded, 2: shared prefixes (never with left padding)
-int variant(const AttnArgs& a) { return a.prefix.seq_info ? 2 : (a.pad_lens ? 1 : 0); }
-PrefillKernel kernel_of(int v) {
-  return v == 2 ? prefill_tc_kernel<false, true> : (v == 1 ? prefill_tc_kernel<true, false> : prefill_tc_kernel<false, false>);
-}
+bool g_attr_set[2][64] = {};
 
 }  // namespace
 
@@ -927,9 +890,10 @@ cb_status launch_prefill_tc(const AttnArgs& a, const StepPlan& plan, bool after_
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64) {
     std::lock_guard<std::mutex> lock(g_attr_mutex);   // first calls may race from several host threads
-    const int v = variant(a);
+    const int v = a.pad_lens ? 1 : 0;
     if (!g_attr_set[v][dev]) {
-      cudaError_t e = cudaFuncSetAttribute(kernel_of(v), cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes));
+      cudaError_t e = cudaFuncSetAttribute(v ? prefill_tc_kernel<true> : prefill_tc_kernel<false>,
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes));
       if (e != cudaSuccess) return cuda_fail(e, "prefill chunks: shared memory attribute");
       g_attr_set[v][dev] = true;
     }
@@ -947,8 +911,9 @@ cb_status launch_prefill_tc(const AttnArgs& a, const StepPlan& plan, bool after_
   const int64_t max_units = int64_t(plan.pre_cap) * a.num_heads + kPrefillSegSlots;
   const int64_t grid = std::min<int64_t>(sm_count(), max_units);
   if (grid < 1) return CB_OK;
-  cudaError_t e = launch_kernel(kernel_of(variant(a)), dim3(unsigned(grid)), dim3(kThreads), kSmemBytes, stream,
-                                after_plan, tq, tk, tv, a, w);
+  cudaError_t e = launch_kernel(a.pad_lens ? prefill_tc_kernel<true> : prefill_tc_kernel<false>,
+                                dim3(unsigned(grid)), dim3(kThreads), kSmemBytes, stream, after_plan, tq, tk, tv,
+                                a, w);
   if (e != cudaSuccess) return cuda_fail(e, "prefill chunks: launch");
   return CB_OK;
 }

@@ -6,19 +6,33 @@
 
 namespace cb {
 
-// A piece of the prefix phase: the query rows of one row tile or two, of one
-// key/value head, over one KV segment of their group's prefix.
+// A row's state over a part of its keys, as one record: acc[kPrefixDim] (the sum
+// of 2^(s - m) v over scores s in the exp2 domain), the reference maximum m, the
+// sum of 2^(s - m), padding to 16 bytes.
+constexpr int kPrefixDim = 128;
+constexpr int kPrefixRec = kPrefixDim + 4;
+
+// A piece: the query rows of one row tile or two, of one key/value head, over one
+// KV segment, either of their group's prefix or of their sequence's own keys.
 struct alignas(16) Piece {
-  int s0;                      // the group's first sequence: its table holds the prefix's blocks
+  int s0;                      // the table that names the blocks (a group's first sequence's, or the own one)
+  int skip;                    // blocks of it before key 0
   int tok0, ntok;              // query tokens
   int hk;                      // key/value head
-  int j0, nt;                  // KV tiles
-  int shared;                  // keys of the prefix
-  int rec;                     // this piece's (first) record of each row
-  int alt;                     // 1: one row tile, KV tiles alternate over the two slots
-  int pad[3];
+  int j0, nt;                  // KV tiles (none: the rows' records are empty)
+  int keys;                    // keys of the prefix, or own keys of the sequence
+  int lim0;                    // keys that the first token sees; the next one sees one more, up to `keys`
+  unsigned rec0;               // record of (tok0, head 0)
+  int rec_step;                // records per (token, head)
+  int flags;
+  int pad[4];
 };
-static_assert(sizeof(Piece) == 48, "piece");
+static_assert(sizeof(Piece) == 64, "piece");
+enum : int {
+  kPieceAlt = 1,               // one row tile: KV tiles alternate over the two slots, which have a record each
+  kPieceDirect = 2,            // nothing to join: the rows are written to out
+  kPieceEnd = 4                // no more pieces
+};
 
 // One row tile of a sequence over one chunk of its own keys, for every key/value head.
 struct alignas(16) SuffixItem {
@@ -28,9 +42,10 @@ struct alignas(16) SuffixItem {
   int k0, k1;                  // own keys of the chunk (0 = the first key behind the prefix)
   int ctx;                     // own keys of the sequence
   int skip;                    // blocks of the table that the prefix covers
-  int base;                    // the sequence's first own record
-  int nch, chunk;              // chunks of the sequence, this one
+  unsigned rec0;               // the chunk's record of (the sequence's first token, head 0)
+  int rec_step;                // records per (token, head)
   int direct;                  // 1: nothing to join, the rows are written to out
+  int pad;
 };
 static_assert(sizeof(SuffixItem) == 48, "item");
 
@@ -40,31 +55,27 @@ struct PrefixWork {
   const int32_t* context_lens; // [num_seqs], whole
   int32_t num_groups;
   int32_t num_sms;
-  int32_t tile_tokens;         // query tokens per row tile of the prefix kernel
-  int32_t max_warp_rows;       // sequences with more query rows per key/value head are prefill chunks
-  int32_t suffix_units;        // warps' units that the chunk length aims for
+  int32_t tile_tokens;         // query tokens per row tile of a piece
+  int32_t stream_units;        // streamed units that the chunk length aims for
   int32_t piece_cap, item_cap;
-  int64_t rec_cap, own_cap;
+  int64_t prefix_rec_cap;      // records of the prefixes; the own ones follow
+  int64_t piece_rec_cap;       // own records of pieces
+  int64_t own_rec_cap;         // all own records
   uint32_t tag;
   // in the workspace
   int32_t* header;             // [0] pieces, [1] prefix records per row (stride), [2] call tag, [3] piece
-                               // claims, [4] suffix items, [5] suffix claims
-  int32_t* suffix_lens;        // [num_seqs] keys behind the prefix (0: left out)
-  int4* seq_info;              // [num_seqs] see PrefixView
-  int4* groups;                // [num_groups] (first sequence, first token, tokens, shared keys)
-  int32_t* first_piece;        // [num_groups + 1]
+                               // claims, [4] streamed items, [5] unit claims, [6] CTAs that work on
+                               // pieces first (the others go to the streamed units at once)
+  int4* groups;                // [num_groups] (first sequence, first token, tokens, shared keys), those
+                               // that the plan does not hold in shared memory
+  int32_t* first_piece;        // [num_groups + num_seqs]
+  unsigned* seq_rec;           // [num_seqs] the sequence's first own record
   Piece* pieces;
   SuffixItem* items;
   int4* token_info;            // [num_tokens] (prefix records, first own record of head 0, own records per head, -)
-  float* recs;                 // prefix records [token][query head][stride]
-  float* own_recs;
+  float* recs;                 // prefix records [token][query head][stride], then the sequences' own ones
 };
 
-constexpr int kSuffixWarps = 8;          // warps of a suffix CTA, each with units of its own
-
-// The rows' own keys (sequences that are not prefill chunks), then the join of
-// every row that has more than one record.
-cb_status launch_suffix(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream);
-cb_status launch_join(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream);
+constexpr int kStreamWarps = 8;          // warps of a CTA that stream own keys, each with units of its own
 
 }  // namespace cb
