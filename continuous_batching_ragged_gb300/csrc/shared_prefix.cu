@@ -80,7 +80,6 @@ enum : int {
 };
 constexpr uint32_t kOffTmemSlot = kOffBar + 16 * ((NUM_BARS + 1) / 2);
 constexpr uint32_t kOffItems = kOffTmemSlot + 16;
-constexpr int kLookAhead = 4;                    // tiles ahead of the loads that are prefetched into L2
 constexpr uint32_t kOffOwnBars = kOffItems + kItemSlots * uint32_t(sizeof(Piece));   // streams: barriers, items;
 constexpr uint32_t kOffOwnSlots = kOffOwnBars + stream::kBarBytes;                  // their rings lie over the tiles
 constexpr uint32_t kSmemBytes = kOffOwnSlots + stream::kSlotBytes + 1024;   // + slack to align the base
@@ -92,8 +91,10 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 constexpr int kPlanThreads = 512;
 constexpr int kMaxSegs = 64;             // KV segments of a prefix, or of a chunk's own keys
+constexpr int kSegChoices = 32;          // numbers of segments that are scored: 1 .. 24, then every fifth to 64
 constexpr int kGroupCache = 512;         // groups kept in shared memory
-constexpr int kSeqCache = 1024;          // sequences kept in shared memory
+constexpr int kSeqCache = 768;           // sequences kept in shared memory
+constexpr int kJobCache = 768;           // jobs whose first piece is kept in shared memory
 constexpr int kExtraPieces = 1024;       // pieces beyond one per (row tile pair, key/value head)
 constexpr int64_t kExtraRecs = 131072;   // records beyond two per row (69 MB)
 constexpr int kMinChunkTiles = 8;        // shortest chunk of streamed keys, in 16-key tiles
@@ -104,21 +105,55 @@ constexpr int kMaxSms = 160;             // SMs that the lists are sized for
 // once per 16 rows; beyond, they are pieces.
 constexpr int kMaxStreamRows = 64;
 // Cost model of the segments and of the SM split, in microseconds and bytes.
-constexpr float kTileUsTwo = 1.95f;      // a KV tile against two row tiles, one SM
-constexpr float kTileUsOne = 1.2f;       // a KV tile against one row tile
-constexpr float kPieceUs = 3.0f;         // a piece beyond its tiles: Q, the pipeline's fill, the records
-constexpr float kBytesPerUs = 6.4e6f;    // HBM
+constexpr float kTileUsTwo = 1.8f;       // a KV tile against two row tiles, one SM
+constexpr float kTileUsOne = 1.4f;       // a KV tile against one row tile, at an SM's share of HBM (0.85 alone)
+constexpr float kPieceUs = 5.0f;         // a piece beyond its tiles: Q, the pipeline's fill, the records
+constexpr float kBytesPerUs = 6.7e6f;    // HBM
 constexpr float kStreamBytesPerUsPerSm = 6.0e4f;
 constexpr float kJoinBytesPerUs = 4.0e6f;
-constexpr int kSmSteps = 19;             // SM splits that are scored: 1/19 .. 19/19 of the SMs
+constexpr float kShareUs = 6.0f;          // what a step's pieces and join take at least
+constexpr int kSmSteps = 16;             // SM splits that are scored: 1/16 .. 16/16 of the SMs
+static_assert(kSegChoices * kSmSteps == kPlanThreads, "a thread scores one choice");
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+// The plan is one CTA that runs every line once: what it costs is latency, of the
+// instruction fetches first of all (about 9 us with everything inlined).  So its
+// helpers are functions of their own, and its arrays are reached through one
+// generic pointer each, in shared memory where they fit and in the workspace else.
+
+// ceil(a / b) through one approximate quotient, corrected to be exact; a, b >= 1.
+__device__ __noinline__ int ceil_div_fast(int a, int b) {
+  if (a >= (1 << 22)) return (a - 1) / b + 1;
+  int q = int(__fdividef(float(a), float(b)));
+  const int r = a - q * b;                         // the quotient is off by one at most
+  if (r < 0) --q;
+  else if (r >= b) ++q;
+  return q * b < a ? q + 1 : q;
+}
+
+// The segments of a range of keys where none is longer than `longest` KV tiles:
+// their number and length.
+__device__ __noinline__ int2 segments(int keys, int longest) {
+  const int tiles = (keys + BN - 1) / BN;
+  const int len = ceil_div_fast(tiles, ceil_div_fast(tiles, longest));
+  return make_int2(ceil_div_fast(tiles, len), len);
+}
+
+// The last i < n with p[i * stride] <= v; 0 if there is none.
+__device__ __noinline__ int last_at_or_before(const int* p, int stride, int n, int v) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p[mid * stride] <= v) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
 // Exclusive block-wide scan; `total` receives the sum.  Contains __syncthreads.
-__device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
+__device__ __noinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x = v;
-#pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
@@ -126,47 +161,25 @@ __device__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
   int64_t before = 0, all = 0;
-#pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
     if (w < warp) before += warp_sums[w];
     all += warp_sums[w];
   }
-  total = all;
+  *total = all;
   __syncthreads();
   return before + x - v;
 }
 
-// Block-wide sums of three values, in every thread.  Contains __syncthreads;
-// `sums` holds 3 per warp.
-__device__ void block_sums(int64_t& x, int64_t& y, int64_t& z, int64_t* sums) {
-  constexpr int kW = kPlanThreads / 32;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    x += __shfl_xor_sync(0xffffffffu, x, o);
-    y += __shfl_xor_sync(0xffffffffu, y, o);
-    z += __shfl_xor_sync(0xffffffffu, z, o);
-  }
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) sums[warp] = x, sums[kW + warp] = y, sums[2 * kW + warp] = z;
-  __syncthreads();
-  x = y = z = 0;
-#pragma unroll
-  for (int w = 0; w < kW; ++w) x += sums[w], y += sums[kW + w], z += sums[2 * kW + w];
-  __syncthreads();
+// *sum += the warp's v (0 <= v < 2^60), 20 bits at a time through the warp's reduction; one atomic a warp.
+__device__ __noinline__ void add_warp_sum(unsigned long long* sum, int64_t v) {
+  const unsigned lo = __reduce_add_sync(0xffffffffu, unsigned(v & 0xfffff));
+  const unsigned mid = __reduce_add_sync(0xffffffffu, unsigned((v >> 20) & 0xfffff));
+  const unsigned hi = __reduce_add_sync(0xffffffffu, unsigned((v >> 40) & 0xfffff));
+  if ((threadIdx.x & 31) == 0 && (lo | mid | hi))
+    atomicAdd(sum, lo + ((unsigned long long)mid << 20) + ((unsigned long long)hi << 40));
 }
 
-// The segments of a range of keys where none is longer than `longest` KV tiles:
-// their number and length.
-__device__ __forceinline__ int2 segments(int keys, int longest) {
-  const int tiles = ceil_div(keys, BN);
-  const int len = ceil_div(tiles, ceil_div(tiles, longest));
-  return make_int2(ceil_div(tiles, len), len);
-}
-
-// A sequence as the plan sees it; own = 0: left out.
-struct SeqPlan {
-  int own, c0, q_len, group;
-};
+__device__ __forceinline__ int seg_choice(int i) { return i < 24 ? i + 1 : 24 + (i - 23) * 5; }
 
 // Rows that a set of pieces has in common: a group's over its prefix, or a
 // chunk's over its own keys.  keys = 0: none.
@@ -174,54 +187,69 @@ struct Job {
   int keys, tok0, tokens, s0, skip, lim0;
 };
 
+// What the plan knows of the groups and sequences.
+struct PlanView {
+  const int4* groups;          // (first sequence, first token, tokens, shared keys)
+  const int4* seqs;            // (own keys, 0: left out; first token; tokens; group)
+  int num_groups, block_shift, group_heads;
+};
+__device__ __forceinline__ bool is_chunk(const int4& q, int G) {
+  return q.x > 0 && q.z > 1 && int64_t(q.z) * G > kMaxStreamRows;
+}
+// Job j: group j's prefix, then sequence (j - num_groups)'s own keys.
+__device__ __noinline__ Job get_job(const PlanView v, int j) {
+  if (j < v.num_groups) {
+    const int4 gr = v.groups[j];
+    return Job{gr.w, gr.y, gr.z, gr.x, 0, gr.w};
+  }
+  const int4 q = v.seqs[j - v.num_groups];
+  if (!is_chunk(q, v.group_heads)) return Job{0, 0, 0, 0, 0, 0};
+  return Job{q.x, q.y, q.z, j - v.num_groups, v.groups[q.w].w >> v.block_shift, q.x - q.z + 1};
+}
+
 // One CTA.  Checks the groups, chooses the segments of the pieces and the
 // chunks of the streams, lists both and gives every row its records.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArgs a, const PrefixWork w) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // they wait for this grid on the device
-  __shared__ int64_t warp_sums[3 * (kPlanThreads / 32)];
-  __shared__ float n_work[kMaxSegs], n_piece[kMaxSegs];
-  __shared__ int n_pieces_of[kMaxSegs];
-  __shared__ int4 gcache[kGroupCache];
-  __shared__ SeqPlan scache[kSeqCache];
-  __shared__ unsigned long long s_best;
+  __shared__ int64_t warp_sums[kPlanThreads / 32];
+  __shared__ unsigned long long sums[4], s_best;
+  __shared__ float n_work[kSegChoices], n_piece[kSegChoices];
+  __shared__ int n_pieces_of[kSegChoices];
+  __shared__ int4 gcache[kGroupCache], scache[kSeqCache];
+  __shared__ int m_cu[kSeqCache + 1], m_ctx[kSeqCache], p_first[kJobCache];
   __shared__ int s_alt, s_tiles;
   const int tid = threadIdx.x;
   const int S = a.num_seqs, T = a.num_tokens, NG = w.num_groups, TT = w.tile_tokens;
-  const int H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv;
-  const int32_t* cu = a.cu_seqlens_q;
+  const int H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv, block_shift = __ffs(a.block_size) - 1;
   const bool chunks = int64_t(a.max_q_len) * G > kMaxStreamRows && a.max_q_len > 1;   // some sequence's own keys may be pieces
-  auto group = [&](int g) -> int4 { return g < kGroupCache ? gcache[g] : w.groups[g]; };
-  auto set_header = [&](int pieces, int stride, int items, int working) {
-    w.header[0] = pieces;
-    w.header[1] = stride;
-    w.header[2] = int32_t(w.tag);
-    w.header[3] = 0;
-    w.header[4] = items;
-    w.header[5] = 0;
-    w.header[6] = working;
-  };
-  // nothing runs and no row is written
-  auto give_up = [&]() {
-    __syncthreads();
-    for (int t = tid; t < T; t += kPlanThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
-    if (tid == 0) {
-      raise_error(a.err, kErrInvalid);
-      set_header(0, 0, 0, 0);
-    }
-  };
-
-  // Each group's shared keys: whole blocks of its prefix, for at least two
-  // sequences.  Where the first sequence, whose table names the blocks, does
-  // not hold them, every sequence of the group reads its own.  The groups have
-  // to cover the sequences in order.
+  const int jobs = NG + (chunks ? S : 0);
+  int4* groups = NG <= kGroupCache ? gcache : w.groups;
+  int4* seqs = S <= kSeqCache ? scache : w.seqs;
+  int* first_piece = jobs <= kJobCache ? p_first : w.first_piece;
+  const int* cu = S <= kSeqCache ? m_cu : a.cu_seqlens_q;
+  const int* ctx = S <= kSeqCache ? m_ctx : w.context_lens;
+  const PlanView view = {groups, seqs, NG, block_shift, G};
+  if (tid < 4) sums[tid] = 0;
   if (tid == 0) {
     s_alt = 0;
     s_tiles = 1;
     s_best = ~0ull;
   }
+  if (S <= kSeqCache) {
+    for (int i = tid; i <= S; i += kPlanThreads) {
+      m_cu[i] = a.cu_seqlens_q[i];
+      if (i < S) m_ctx[i] = w.context_lens[i];
+    }
+  }
+  for (int t = tid; t < T; t += kPlanThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
   __syncthreads();
-  int bad = 0, tiles_max = 1;
-  int64_t n_first = 0;                             // pieces if nothing is cut, per key/value head
+
+  // Each group's shared keys: whole blocks of its prefix, for at least two
+  // sequences.  Where the first sequence, whose table names the blocks, does
+  // not hold them, every sequence of the group reads its own.  The groups have
+  // to cover the sequences in order.
+  int bad = 0;
+  int64_t saved = 0;                               // keys that are not read again
   for (int g = tid; g < NG; g += kPlanThreads) {
     const int s0 = w.cu_groups[g], s1 = w.cu_groups[g + 1], p = w.prefix_lens[g];
     int t0 = 0, tokens = 0, shared = 0;
@@ -229,74 +257,63 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
       bad = 1;
     } else if (s1 - s0 >= 2 && p >= a.block_size) {
       t0 = cu[s0];
-      const int t1 = cu[s1], q0 = cu[s0 + 1] - t0, ctx0 = w.context_lens[s0];
+      const int t1 = cu[s1], q0 = cu[s0 + 1] - t0, ctx0 = ctx[s0];
       if (t0 >= 0 && t1 <= T && t1 > t0 && q0 >= 1 && ctx0 <= a.max_context_len && ctx0 - q0 >= p &&
           int64_t(ctx0) <= int64_t(a.max_blocks_per_seq) * a.block_size) {
         tokens = t1 - t0;
-        shared = p / a.block_size * a.block_size;
-        n_first += ceil_div(tokens, 2 * TT);
-        tiles_max = max(tiles_max, ceil_div(shared, BN));
-        if (tokens <= TT) s_alt = 1;
+        shared = (p >> block_shift) << block_shift;
+        saved += int64_t(shared) * (s1 - s0 - 1);
       }
     }
-    const int4 gr = make_int4(s0, t0, tokens, shared);
-    if (g < kGroupCache) gcache[g] = gr;
-    else w.groups[g] = gr;
+    groups[g] = make_int4(s0, t0, tokens, shared);
   }
-  if (__syncthreads_or(bad)) {                     // no sequence can be told its prefix
-    give_up();
-    return;
+  add_warp_sum(&sums[3], saved);
+  bad = __syncthreads_or(bad);
+  // Sharing takes the pieces and the join, one after the other: where the bytes
+  // that it saves take HBM less time than that, every sequence reads its own
+  // table (4 samples behind 512 keys of 8 heads: 18.9 us shared and 25.1 not).
+  const float key_bytes = 4.0f * HD * float(Hkv);  // K and V of a key
+  if (float(sums[3]) * key_bytes < kShareUs * kBytesPerUs) {
+    for (int g = tid; g < NG; g += kPlanThreads) groups[g].w = 0;
   }
+  __syncthreads();
 
   // Each sequence: its group and own keys.
-  auto seq_plan = [&](int s) -> SeqPlan {
-    int lo = 0, hi = NG - 1;                       // the last group starting at or before s (empty groups start there too)
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (group(mid).x <= s) lo = mid; else hi = mid - 1;
-    }
-    const int p = w.prefix_lens[lo], ctx = w.context_lens[s], c0 = cu[s], q_len = cu[s + 1] - c0;
-    const bool ok = p >= 0 && q_len >= 1 && c0 >= 0 && c0 + q_len <= T && q_len <= a.max_q_len && ctx >= q_len &&
-                    p <= ctx - q_len && ctx <= a.max_context_len &&
-                    int64_t(ctx) <= int64_t(a.max_blocks_per_seq) * a.block_size;
-    return SeqPlan{ok ? ctx - group(lo).w : 0, c0, q_len, lo};
-  };
-  auto seq = [&](int s) -> SeqPlan { return s < kSeqCache ? scache[s] : seq_plan(s); };
-  auto is_chunk = [&](const SeqPlan& q) { return q.own > 0 && q.q_len > 1 && int64_t(q.q_len) * G > kMaxStreamRows; };
-  // job j: group j's prefix, then sequence (j - NG)'s own keys
-  const int jobs = NG + (chunks ? S : 0);
-  auto job = [&](int j) -> Job {
-    if (j < NG) {
-      const int4 gr = group(j);
-      return Job{gr.w, gr.y, gr.z, gr.x, 0, gr.w};
-    }
-    const SeqPlan q = seq(j - NG);
-    if (!is_chunk(q)) return Job{0, 0, 0, 0, 0, 0};
-    return Job{q.own, q.c0, q.q_len, j - NG, group(q.group).w / a.block_size, q.own - q.q_len + 1};
-  };
-  int64_t unit_tiles = 0, own_keys = 0;            // streamed units' tiles and keys
-  for (int s = tid; s < S; s += kPlanThreads) {
-    const SeqPlan q = seq_plan(s);
-    if (s < kSeqCache) scache[s] = q;
-    if (q.own == 0) {
+  int tiles_max = 1;
+  int64_t n_first = 0, unit_tiles = 0, own_keys = 0;   // pieces if nothing is cut, per key/value head; streamed
+                                                       // units' tiles, and keys
+  for (int g = tid; g < NG && !bad; g += kPlanThreads) {
+    const int4 gr = groups[g];
+    if (gr.w == 0) continue;
+    n_first += ceil_div_fast(gr.z, 2 * TT);
+    tiles_max = max(tiles_max, (gr.w + BN - 1) / BN);
+    if (gr.z <= TT) s_alt = 1;
+  }
+  for (int s = tid; s < S && !bad; s += kPlanThreads) {
+    const int g = last_at_or_before(&groups[0].x, 4, NG, s);   // empty groups start there too, and come before
+    const int p = w.prefix_lens[g], n = ctx[s], c0 = cu[s], q_len = cu[s + 1] - c0;
+    const bool ok = p >= 0 && q_len >= 1 && c0 >= 0 && c0 + q_len <= T && q_len <= a.max_q_len && n >= q_len &&
+                    p <= n - q_len && n <= a.max_context_len && int64_t(n) <= int64_t(a.max_blocks_per_seq) * a.block_size;
+    const int4 q = make_int4(ok ? n - groups[g].w : 0, c0, q_len, g);
+    seqs[s] = q;
+    if (!ok) {
       raise_error(a.err, kErrInvalid);             // left out
-    } else if (!is_chunk(q)) {
-      unit_tiles += int64_t(ceil_div(q.q_len * G, kStreamRows)) * Hkv * ceil_div(q.own, stream::kTileKeys);
-      own_keys += q.own;
+    } else if (is_chunk(q, G)) {
+      n_first += ceil_div_fast(q_len, 2 * TT);
+      tiles_max = max(tiles_max, (q.x + BN - 1) / BN);
     } else {
-      n_first += ceil_div(q.q_len, 2 * TT);
-      tiles_max = max(tiles_max, ceil_div(q.own, BN));
+      unit_tiles += int64_t((q_len * G + kStreamRows - 1) / kStreamRows) * Hkv * ((q.x + stream::kTileKeys - 1) / stream::kTileKeys);
+      own_keys += q.x;
     }
   }
-  for (int t = tid; t < T; t += kPlanThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
   tiles_max = __reduce_max_sync(0xffffffffu, tiles_max);
   if ((tid & 31) == 0) atomicMax(&s_tiles, tiles_max);
-  int64_t all_first = n_first, all_tiles = unit_tiles, all_keys = own_keys;
-  block_sums(all_first, all_tiles, all_keys, warp_sums);
-  if (all_first * Hkv > w.piece_cap) {             // only if token ranges overlap (malformed metadata)
-    give_up();
-    return;
-  }
+  add_warp_sum(&sums[0], n_first);
+  add_warp_sum(&sums[1], unit_tiles);
+  add_warp_sum(&sums[2], own_keys);
+  __syncthreads();
+  const int64_t all_first = int64_t(sums[0]), all_tiles = int64_t(sums[1]);
+  bad |= all_first * Hkv > w.piece_cap;            // only if token ranges overlap (malformed metadata)
   const int alt_recs = s_alt ? 2 : 1;
   tiles_max = s_tiles;
 
@@ -305,145 +322,124 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   // idle as large groups' pieces do HBM.  First the pieces of every n, then
   // every (n, SMs) is scored.
   int longest = 1, working = w.num_sms, n_segs = 1;
-  if (all_first > 0) {
-    constexpr int kLanes = kPlanThreads / kMaxSegs;   // threads per n, each with a share of the jobs
-    {
-      const int n = tid / kLanes + 1, len = ceil_div(tiles_max, n);
-      int64_t pieces = 0, own_recs = 0;
-      float work = 0.f, piece = 0.f;
-      for (int j = tid % kLanes; j < jobs; j += kLanes) {
-        const Job jb = job(j);
-        if (jb.keys == 0) continue;
-        const int2 sg = segments(jb.keys, len);
-        const int64_t units = int64_t(ceil_div(jb.tokens, 2 * TT)) * Hkv * sg.x;
-        const bool alt = jb.tokens <= TT;
-        const float us = float(sg.y) * (alt ? kTileUsOne : kTileUsTwo) + kPieceUs;
-        pieces += units;
-        if (j >= NG) own_recs += int64_t(jb.tokens) * H * sg.x * (alt ? 2 : 1);
-        work += float(units) * us;
-        piece = fmaxf(piece, us);
-      }
-#pragma unroll
-      for (int x = kLanes / 2; x > 0; x >>= 1) {
-        pieces += __shfl_xor_sync(0xffffffffu, pieces, x);
-        own_recs += __shfl_xor_sync(0xffffffffu, own_recs, x);
-        work += __shfl_xor_sync(0xffffffffu, work, x);
-        piece = fmaxf(piece, __shfl_xor_sync(0xffffffffu, piece, x));
-      }
-      if (tid % kLanes == 0) {
-        const bool fits = pieces <= w.piece_cap && int64_t(T) * H * n * alt_recs <= w.prefix_rec_cap &&
-                          own_recs <= w.piece_rec_cap;
-        n_pieces_of[n - 1] = fits ? int(pieces) : 0;
-        n_work[n - 1] = work;
-        n_piece[n - 1] = piece;
-      }
+  if (all_first > 0 && !bad) {
+    constexpr int kLanes = kPlanThreads / kSegChoices;   // threads per n, each with a share of the jobs
+    const int c = tid / kLanes, n = seg_choice(c), len = ceil_div_fast(tiles_max, n);
+    int64_t pieces = 0, own_recs = 0;
+    float work = 0.f, piece = 0.f, bytes = 0.f;
+    for (int j = tid % kLanes; j < jobs; j += kLanes) {
+      const Job jb = get_job(view, j);
+      if (jb.keys == 0) continue;
+      const int2 sg = segments(jb.keys, len);
+      const int64_t units = int64_t(ceil_div_fast(jb.tokens, 2 * TT)) * Hkv * sg.x;
+      const bool alt = jb.tokens <= TT;
+      const float us = float(sg.y) * (alt ? kTileUsOne : kTileUsTwo) + kPieceUs;
+      pieces += units;
+      if (j >= NG) own_recs += int64_t(jb.tokens) * H * sg.x * (alt ? 2 : 1);
+      work += float(units) * us;
+      piece = fmaxf(piece, us);
+      bytes += float(jb.keys);
     }
-    float piece_bytes = 0.f;                       // K and V bytes of the pieces, once
-    for (int j = tid & 31; j < jobs; j += 32) piece_bytes += float(job(j).keys);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) piece_bytes += __shfl_xor_sync(0xffffffffu, piece_bytes, x);
-    const float key_bytes = 4.0f * HD * float(Hkv);
-    piece_bytes *= key_bytes;
-    const float own_bytes = float(all_keys) * key_bytes;
+#pragma unroll 1
+    for (int x = kLanes / 2; x > 0; x >>= 1) {
+      pieces += __shfl_xor_sync(0xffffffffu, pieces, x);
+      own_recs += __shfl_xor_sync(0xffffffffu, own_recs, x);
+      work += __shfl_xor_sync(0xffffffffu, work, x);
+      piece = fmaxf(piece, __shfl_xor_sync(0xffffffffu, piece, x));
+      bytes += __shfl_xor_sync(0xffffffffu, bytes, x);
+    }
+    if (tid % kLanes == 0) {
+      const bool fits = pieces <= w.piece_cap && int64_t(T) * H * n * alt_recs <= w.prefix_rec_cap &&
+                        own_recs <= w.piece_rec_cap;
+      n_pieces_of[c] = fits ? int(pieces) : 0;
+      n_work[c] = work;
+      n_piece[c] = piece;
+    }
+    static_assert(kLanes == kSmSteps, "the thread's n is the one that it scores");
+    const float piece_bytes = bytes * key_bytes, own_bytes = float(sums[2]) * key_bytes;
     __syncthreads();
-    unsigned long long best = ~0ull;
-    for (int i = tid; i < kMaxSegs * kSmSteps; i += kPlanThreads) {
-      const int n = i / kSmSteps, k = (i % kSmSteps + 1) * w.num_sms / kSmSteps;
-      const int pieces = n_pieces_of[n];
-      if (pieces == 0 || k < 1 || (own_bytes == 0.f && k < w.num_sms)) continue;
+    const int k = (tid % kSmSteps + 1) * w.num_sms / kSmSteps, of_n = n_pieces_of[c];
+    unsigned long long key = ~0ull;
+    if (of_n > 0 && k > 0 && (own_bytes > 0.f || k == w.num_sms)) {
       // pieces of one size run in whole waves; unequal ones fill the gaps
-      const float waves = ceilf(__fdividef(float(pieces), float(k))) * n_piece[n];
-      float us = fminf(waves, __fdividef(n_work[n], float(k)) + n_piece[n]);
+      const float waves = ceilf(__fdividef(float(of_n), float(k))) * n_piece[c];
+      float us = fminf(waves, __fdividef(n_work[c], float(k)) + n_piece[c]);
       us = fmaxf(us, piece_bytes * (1.0f / kBytesPerUs));
       const float beside = fminf(kBytesPerUs * us - piece_bytes, float(w.num_sms - k) * kStreamBytesPerUsPerSm * us);
       us += fmaxf(0.f, own_bytes - beside) * (1.0f / kBytesPerUs);
-      us += float(T) * float(H) * float((n + 1) * alt_recs) * (kPrefixRec * 4.0f / kJoinBytesPerUs);
-      const unsigned long long key = ((unsigned long long)(__float_as_uint(us)) << 32) | unsigned(i);
-      best = key < best ? key : best;
+      us += float(T) * float(H) * float(n * alt_recs) * (kPrefixRec * 4.0f / kJoinBytesPerUs);
+      key = ((unsigned long long)(__float_as_uint(us)) << 32) | unsigned(tid);
     }
-#pragma unroll
+#pragma unroll 1
     for (int x = 16; x > 0; x >>= 1) {
-      const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, x);
-      best = other < best ? other : best;
+      const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, x);
+      key = other < key ? other : key;
     }
-    if ((tid & 31) == 0) atomicMin(&s_best, best);
+    if ((tid & 31) == 0) atomicMin(&s_best, key);
     __syncthreads();
-    if (s_best == ~0ull) {                         // n = 1 fits unless token ranges overlap
-      give_up();
-      return;
-    }
+    bad |= s_best == ~0ull;                        // n = 1 fits unless token ranges overlap
     const int i = int(unsigned(s_best));
-    n_segs = i / kSmSteps + 1;
+    n_segs = seg_choice((i & (kPlanThreads - 1)) / kSmSteps);
     working = (i % kSmSteps + 1) * w.num_sms / kSmSteps;
-    longest = ceil_div(tiles_max, n_segs);
+    longest = ceil_div_fast(tiles_max, n_segs);
   }
   const int stride = n_segs * alt_recs;
   const unsigned own_rec0 = unsigned(w.prefix_rec_cap);
   // chunk length: the streamed units come out even over the warps
   const int64_t per = (all_tiles + w.stream_units - 1) / w.stream_units;
   const int L = int(per < kMinChunkTiles ? kMinChunkTiles : (per > (1 << 26) ? (1 << 26) : per));
-  // records per (token, head) of a group's prefix and of a sequence's own keys
-  auto prefix_recs = [&](int g) -> int {
-    const int4 gr = group(g);
-    return gr.w > 0 ? segments(gr.w, longest).x * (gr.z <= TT ? 2 : 1) : 0;
-  };
-  auto own_recs_of = [&](const SeqPlan& q) -> int {
-    return is_chunk(q) ? segments(q.own, longest).x * (q.q_len <= TT ? 2 : 1) : ceil_div(ceil_div(q.own, stream::kTileKeys), L);
-  };
 
-  // Streamed items, and every sequence's own records.
-  int64_t base = 0;                                // items in the low, records in the high word
-  for (int s0 = 0; s0 < S; s0 += kPlanThreads) {
+  // Streamed items, and every sequence's records: its rows have `pre` of the
+  // prefix and `nch` own ones each.
+  int64_t base = 0;                                // items in the low, own records in the high word
+  for (int s0 = 0; s0 < S && !bad; s0 += kPlanThreads) {
     const int s = s0 + tid;
-    int64_t n_items = 0, n_recs = 0;
-    SeqPlan q = {0, 0, 0, 0};
+    int4 q = make_int4(0, 0, 0, 0), gr = q;
     int pre = 0, rt = 0, nch = 0;
-    if (s < S) q = seq(s);
-    if (q.own > 0) {
-      pre = prefix_recs(q.group);
-      nch = own_recs_of(q);
-      rt = is_chunk(q) ? 0 : ceil_div(q.q_len * G, kStreamRows);
-      n_items = int64_t(rt) * nch;
-      n_recs = pre + nch > 1 ? int64_t(q.q_len) * H * nch : 0;
+    if (s < S) q = seqs[s];
+    if (q.x > 0) {
+      gr = groups[q.w];
+      if (gr.w > 0) pre = segments(gr.w, longest).x * (gr.z <= TT ? 2 : 1);
+      if (is_chunk(q, G)) {
+        nch = segments(q.x, longest).x * (q.z <= TT ? 2 : 1);
+      } else {
+        nch = ceil_div_fast((q.x + stream::kTileKeys - 1) / stream::kTileKeys, L);
+        rt = (q.z * G + kStreamRows - 1) / kStreamRows;
+      }
     }
+    const int64_t n_items = int64_t(rt) * nch, n_recs = pre + nch > 1 ? int64_t(q.z) * H * nch : 0;
     int64_t total;
-    const int64_t at = base + block_scan(n_items | (n_recs << 32), warp_sums, total);
+    const int64_t at = base + block_scan(n_items | (n_recs << 32), warp_sums, &total);
     base += total;
-    if ((base & 0xffffffff) > w.item_cap || (base >> 32) > w.own_rec_cap) {   // only if token ranges overlap
-      give_up();
-      return;
-    }
-    if (q.own > 0) {
+    bad |= (base & 0xffffffff) > w.item_cap || (base >> 32) > w.own_rec_cap;   // only if token ranges overlap
+    if (q.x > 0 && !bad) {
       const unsigned rec = own_rec0 + unsigned(at >> 32);
-      if (a.max_q_len > 1) w.seq_rec[s] = rec;
-      if (a.max_q_len == 1) w.token_info[q.c0] = make_int4(pre, int(rec), nch, 0);
+      if (a.max_q_len > 1) w.seq_recs[s] = make_int4(pre, int(rec), nch, 0);
+      else w.token_info[q.y] = make_int4(pre, int(rec), nch, 0);
       SuffixItem it = {};
-      it.s = s, it.tok0 = q.c0, it.q_len = q.q_len, it.ctx = q.own, it.skip = group(q.group).w / a.block_size;
+      it.s = s, it.tok0 = q.y, it.q_len = q.z, it.ctx = q.x, it.skip = gr.w >> block_shift;
       it.rec_step = nch;
       it.direct = n_recs == 0;
       SuffixItem* out = w.items + (at & 0xffffffff);
-      for (int r = 0; r < rt; ++r)
-        for (int c = 0; c < nch; ++c) {
-          it.row0 = r * kStreamRows;
-          it.rec0 = rec + c;
-          it.k0 = c * L * stream::kTileKeys;
-          it.k1 = min(q.own, it.k0 + L * stream::kTileKeys);
-          *out++ = it;
-        }
+#pragma unroll 1
+      for (int i = 0; i < int(n_items); ++i) {
+        it.rec0 = rec + it.pad;                    // `pad` counts the chunks
+        it.k0 = it.pad * L * stream::kTileKeys;
+        it.k1 = min(q.x, it.k0 + L * stream::kTileKeys);
+        *out++ = it;
+        if (++it.pad == nch) it.pad = 0, it.row0 += kStreamRows;
+      }
     }
   }
-  if (a.max_q_len > 1) {                           // every token's sequence by search
+  if (a.max_q_len > 1 && !bad) {                   // every token's sequence by search
     __syncthreads();
     for (int t = tid; t < T; t += kPlanThreads) {
-      int lo = 0, hi = S - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((mid < kSeqCache ? scache[mid].c0 : cu[mid]) <= t) lo = mid; else hi = mid - 1;
-      }
-      const SeqPlan q = seq(lo);
-      if (q.own > 0 && q.c0 <= t && t < q.c0 + q.q_len) {
-        const int nch = own_recs_of(q);
-        w.token_info[t] = make_int4(prefix_recs(q.group), int(w.seq_rec[lo] + unsigned((t - q.c0) * H * nch)), nch, 0);
+      const int s = last_at_or_before(cu, 1, S, t);
+      const int4 q = seqs[s];
+      if (q.x > 0 && q.y <= t && t < q.y + q.z) {
+        int4 info = w.seq_recs[s];
+        info.y += (t - q.y) * H * info.z;
+        w.token_info[t] = info;
       }
     }
   }
@@ -451,33 +447,29 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   // the pieces: by segment, key/value head and row tile pair, so that the
   // pairs of one (segment, head) run side by side and share its K/V in L2
   int64_t pbase = 0;
-  if (all_first > 0) {
+  if (all_first > 0 && !bad) {
     for (int j0 = 0; j0 < jobs; j0 += kPlanThreads) {
       const int j = j0 + tid;
       int64_t count = 0;
       if (j < jobs) {
-        const Job jb = job(j);
-        if (jb.keys > 0) count = int64_t(ceil_div(jb.tokens, 2 * TT)) * Hkv * segments(jb.keys, longest).x;
+        const Job jb = get_job(view, j);
+        if (jb.keys > 0) count = int64_t(ceil_div_fast(jb.tokens, 2 * TT)) * Hkv * segments(jb.keys, longest).x;
       }
       int64_t total;
-      const int64_t at = pbase + block_scan(count, warp_sums, total);
-      if (j < jobs) w.first_piece[j] = int(at);
+      const int64_t at = pbase + block_scan(count, warp_sums, &total);
+      if (j < jobs) first_piece[j] = int(at);
       pbase += total;
     }
     __syncthreads();
   }
   const int n_pieces = int(pbase);
   for (int i = tid; i < n_pieces; i += kPlanThreads) {
-    int lo = 0, hi = jobs - 1;                     // the last job whose pieces start at or before i
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (w.first_piece[mid] <= i) lo = mid; else hi = mid - 1;
-    }
-    const Job jb = job(lo);
+    const int j = last_at_or_before(first_piece, 1, jobs, i);   // jobs without pieces start there too, and come before
+    const Job jb = get_job(view, j);
     const int2 sg = segments(jb.keys, longest);
-    const int pairs = ceil_div(jb.tokens, 2 * TT);
-    const int local = i - w.first_piece[lo];
-    const int pair = local % pairs, hk = local / pairs % Hkv, seg = local / (pairs * Hkv);
+    const int pairs = ceil_div_fast(jb.tokens, 2 * TT);
+    const int local = i - first_piece[j];
+    const int rest = local / pairs, pair = local - rest * pairs, seg = rest / Hkv, hk = rest - seg * Hkv;
     // tokens evenly over the pairs
     const int each = jb.tokens / pairs, more = jb.tokens - each * pairs;
     const int off = pair * each + min(pair, more);
@@ -493,17 +485,30 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     // tiles of the segment that some row of the pair sees
     const int seen = min(jb.keys, pc.lim0 + pc.ntok - 1);
     pc.j0 = seg * sg.y;
-    pc.nt = max(0, min(sg.y, ceil_div(seen, BN) - pc.j0));
+    pc.nt = max(0, min(sg.y, (seen + BN - 1) / BN - pc.j0));
     const int recs = sg.x * (alt ? 2 : 1);
-    pc.rec_step = lo < NG ? stride : recs;
-    pc.rec0 = (lo < NG ? unsigned(pc.tok0) * unsigned(H) * unsigned(stride)
-                       : w.seq_rec[lo - NG] + unsigned(off * H * recs)) + (alt ? 2 * seg : seg);
+    pc.rec_step = j < NG ? stride : recs;
+    pc.rec0 = (j < NG ? unsigned(pc.tok0) * unsigned(H) * unsigned(stride)
+                      : unsigned(w.seq_recs[j - NG].y) + unsigned(off * H * recs)) + (alt ? 2 * seg : seg);
     // one record in all: only a chunk without a prefix, in one segment of two row tiles
-    const bool direct = lo >= NG && recs == 1 && jb.skip == 0;
+    const bool direct = j >= NG && recs == 1 && jb.skip == 0;
     pc.flags = (alt ? kPieceAlt : 0) | (direct ? kPieceDirect : 0);
     w.pieces[i] = pc;
   }
-  if (tid == 0) set_header(n_pieces, stride, int(base & 0xffffffff), working);
+  if (bad) {                                       // nothing runs and no row is written
+    __syncthreads();
+    for (int t = tid; t < T; t += kPlanThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
+  }
+  if (tid == 0) {
+    if (bad) raise_error(a.err, kErrInvalid);
+    w.header[0] = bad ? 0 : n_pieces;
+    w.header[1] = stride;
+    w.header[2] = int32_t(w.tag);
+    w.header[3] = 0;
+    w.header[4] = bad ? 0 : int(base & 0xffffffff);
+    w.header[5] = 0;
+    w.header[6] = working;
+  }
 }
 
 // ------------------------------------------------------------------ prefix phase
@@ -537,16 +542,14 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return r;
 }
 
-__device__ __forceinline__ void tma_prefetch_l2_3d(const void* tmap, int32_t x, int32_t y, int32_t z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                   reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z)
-               : "memory");
-}
-
-// The paged blocks of a piece's KV tiles, for one loader warp: the block table is
+// The paged blocks of a piece's KV tiles, for one loader warp.  The block table is
 // read 32 entries at a time, one window ahead of the tiles, so that no load waits
-// for it, and each tile's boxes are prefetched into L2 kLookAhead tiles before
-// their load.
+// for it.  A tile is up to 16 TMA boxes (8 blocks of 16 keys, two 64-dim halves),
+// and issuing them is what bounds a piece with one row tile: from one lane in
+// turn, with an L2 prefetch of each box before, a tile took 1.64 us at 16 keys a
+// block; without the prefetches 1.26; with a lane for each box 0.85, against 0.78
+// at 128 keys a block (152 such pieces at once: 1.70, 1.36, 1.35 us, the last
+// 7.4 TB/s).
 struct BlockWindow {
   const int32_t* bt;           // the piece's first block
   int blocks;                  // blocks of the piece that hold keys
@@ -568,36 +571,19 @@ struct BlockWindow {
     cur = box(a, it.hk, lane);
     next = box(a, it.hk, 32 + lane);
   }
-  // the window holds block i from now on (i grows by tiles)
-  __device__ __forceinline__ void move_to(const AttnArgs& a, int hk, int i, int lane) {
-    if (i - at >= 32) {
+  // tile j (of the piece, in order) into dst: a lane per box
+  __device__ __forceinline__ void load(uint32_t dst, const CUtensorMap* tm, uint32_t bar, const AttnArgs& a, int hk, int j,
+                                       int lane) {
+    const int B = a.block_size, bpt = BN / B;
+    if (j * bpt - at >= 32) {
       at += 32;
       cur = next;
       next = box(a, hk, at + 32 + lane);
     }
-  }
-  // tile j's boxes into L2: lane i those of its block i
-  __device__ __forceinline__ void prefetch(const CUtensorMap* tm, const AttnArgs& a, int j, int lane) const {
-    const int bpt = BN / a.block_size, i = j * bpt + lane - at;    // within the two windows
-    const int z0 = __shfl_sync(0xffffffffu, cur, i & 31), z1 = __shfl_sync(0xffffffffu, next, i & 31);
-    const int z = i < 32 ? z0 : z1;
-    if (lane < bpt && z < a.num_blocks * a.num_kv_heads) {
-      tma_prefetch_l2_3d(tm, 0, 0, z);
-      tma_prefetch_l2_3d(tm, 64, 0, z);
-    }
-  }
-  // warp-wide; lane 0 loads tile j
-  __device__ __forceinline__ void load(uint32_t dst, const CUtensorMap* tm, uint32_t bar, const AttnArgs& a, int j,
-                                       int lane) const {
-    const int B = a.block_size, bpt = BN / B;
     if (lane == 0) mbar_arrive_expect_tx(bar, kTile);
-    for (int bi = 0; bi < bpt; ++bi) {
-      const int z = __shfl_sync(0xffffffffu, cur, j * bpt + bi - at);
-      if (lane == 0) {
-        tma_load_3d(dst + bi * B * 128, tm, bar, 0, 0, z);
-        tma_load_3d(dst + kHalf + bi * B * 128, tm, bar, 64, 0, z);
-      }
-    }
+    const int bi = lane >> 1, half = lane & 1;
+    const int z = __shfl_sync(0xffffffffu, cur, (j * bpt + bi - at) & 31);
+    if (bi < bpt) tma_load_3d(dst + half * kHalf + bi * B * 128, tm, bar, 64 * half, 0, z);
     __syncwarp();
   }
 };
@@ -607,8 +593,8 @@ struct BlockWindow {
 // a timeout the device error word is set, the roles wind down and the result is
 // false.
 __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                           const AttnArgs& a, const PrefixWork& w, uint8_t* gsm, uint32_t base, int n_pieces,
-                                           int with_pieces) {
+                                           const AttnArgs& a, const PrefixWork& w, uint8_t* gsm, uint32_t base, uint32_t tmem,
+                                           int n_pieces, int with_pieces) {
   auto bar = [&](int i) -> uint32_t { return base + kOffBar + 8u * uint32_t(i); };
   Piece* items = reinterpret_cast<Piece*>(gsm + kOffItems);
   const int warp = threadIdx.x >> 5;
@@ -617,40 +603,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
   const int H = a.num_heads;
   const int G = H / a.num_kv_heads;                // query heads per key/value head
   const int TT = w.tile_tokens;
-  const int bpt = BN / B;                          // blocks per KV tile
   bool role_ok = true;
-
-  if (threadIdx.x == 0) {
-    mbar_init(bar(BAR_Q), 1);
-    mbar_init(bar(BAR_QE), 1);
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(BAR_S + t), 1);
-      mbar_init(bar(BAR_P + t), BM);
-      mbar_init(bar(BAR_O + t), 1);
-    }
-    for (int st = 0; st < kKStages; ++st) {
-      mbar_init(bar(BAR_KF + st), 1);
-      mbar_init(bar(BAR_KE + st), 1);
-    }
-    for (int st = 0; st < kVStages; ++st) {
-      mbar_init(bar(BAR_VF + st), 1);
-      mbar_init(bar(BAR_VE + st), 1);
-    }
-    for (int i = 0; i < kItemSlots; ++i) {
-      mbar_init(bar(BAR_IF + i), 1);
-      mbar_init(bar(BAR_IE + i), kItemReaders);
-    }
-    mbar_init(bar(BAR_VTAIL), 1);
-    mbar_init(bar(BAR_DONE), 1);
-    fence_mbar_init();
-  }
-  if (warp == kWarpMma) {
-    tmem_alloc(base + kOffTmemSlot, kTmemCols);
-    tmem_relinquish();
-  }
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gsm + kOffTmemSlot);
 
   // A reader's view of piece n; `arrive`: this thread is its role's one arrival.
   auto read_item = [&](int n, bool arrive, Piece& it) -> bool {
@@ -663,10 +616,6 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
 
   if (warp == kWarpK) {
     // ------------------------------------------------------------ K loader (claims the pieces)
-    if (lane == 0) {
-      tma_prefetch_desc(tm_q);
-      tma_prefetch_desc(tm_k);
-    }
     uint32_t kc = 0;                               // K tiles requested
     uint32_t qc = 0;                               // Q loads requested
     bool ok = true;
@@ -711,22 +660,19 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
           return true;
         };
         const int q_at = min(kKStages - 1, it.nt);   // K tiles requested before the Q load
-        for (int j = 1; j < min(kLookAhead, it.nt); ++j) win.prefetch(tm_k, a, j, lane);
         for (int j = 0; j < it.nt; ++j) {
           if (j == q_at && !load_q()) {
             ok = false;
             site = kSitePfQFree;
             break;
           }
-          win.move_to(a, it.hk, j * bpt, lane);
-          if (j + kLookAhead < it.nt) win.prefetch(tm_k, a, j + kLookAhead, lane);
           const int st = kc % kKStages;
           if (kc >= kKStages && !__all_sync(0xffffffffu, mbar_wait(bar(BAR_KE + st), ((kc / kKStages) - 1) & 1))) {
             ok = false;
             site = kSitePfKFree;
             break;
           }
-          win.load(base + kOffK + st * kTile, tm_k, bar(BAR_KF + st), a, j, lane);
+          win.load(base + kOffK + st * kTile, tm_k, bar(BAR_KF + st), a, it.hk, j, lane);
           ++kc;
         }
         if (ok && q_at == it.nt && !load_q()) {
@@ -746,7 +692,6 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
     }
   } else if (warp == kWarpV) {
     // ------------------------------------------------------------ V loader
-    if (lane == 0) tma_prefetch_desc(tm_v);
     uint32_t vc = 0, tails = 0;                    // V tiles requested, of which tails
     bool ok = true, tail_pending = false;
     unsigned site = 0;
@@ -763,10 +708,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
       if (it.nt == 0) continue;
       BlockWindow win;
       win.start(a, it, lane);
-      for (int j = 1; j < min(kLookAhead, it.nt); ++j) win.prefetch(tm_v, a, j, lane);
       for (int j = 0; j < it.nt; ++j) {
-        win.move_to(a, it.hk, j * bpt, lane);
-        if (j + kLookAhead < it.nt) win.prefetch(tm_v, a, j + kLookAhead, lane);
         const int st = vc % kVStages;
         if (vc >= kVStages && !__all_sync(0xffffffffu, mbar_wait(bar(BAR_VE + st), ((vc / kVStages) - 1) & 1))) {
           ok = false;
@@ -776,7 +718,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         // rows of the last block behind the last key may hold anything: P is 0 there, but 0 * NaN is not
         const int kb = (it.j0 + j) * BN, r0 = it.keys - kb, r1 = min(BN, ceil_div(it.keys, B) * B - kb);
         const bool tail = r0 < r1;
-        win.load(base + kOffV + st * kTile, tm_v, tail ? bar(BAR_VTAIL) : bar(BAR_VF + st), a, j, lane);
+        win.load(base + kOffV + st * kTile, tm_v, tail ? bar(BAR_VTAIL) : bar(BAR_VF + st), a, it.hk, j, lane);
         ++vc;
         if (tail) {
           if (!__all_sync(0xffffffffu, mbar_wait(bar(BAR_VTAIL), tails & 1))) {
@@ -1090,11 +1032,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
   }
   tc_fence_before();
   const bool failed = __syncthreads_or(role_ok ? 0 : 1);
-  if (warp == kWarpMma) {
-    __syncwarp();
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
-  }
+  tc_fence_after();
   return !failed;
 }
 
@@ -1103,7 +1041,8 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_k16,
-                     const __grid_constant__ CUtensorMap tm_v16, const AttnArgs a, const PrefixWork w) {
+                     const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ AttnArgs a,
+                     const __grid_constant__ PrefixWork w) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;    // 128B-swizzled tiles need 1 KB alignment
@@ -1111,30 +1050,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan kernels have finished
+  // Set up while the plan still runs: barriers, and tensor memory for pieces
+  auto bar = [&](int i) -> uint32_t { return base + kOffBar + 8u * uint32_t(i); };
+  if (threadIdx.x == 0) {
+    mbar_init(bar(BAR_Q), 1);
+    mbar_init(bar(BAR_QE), 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(BAR_S + t), 1);
+      mbar_init(bar(BAR_P + t), BM);
+      mbar_init(bar(BAR_O + t), 1);
+    }
+    for (int st = 0; st < kKStages; ++st) {
+      mbar_init(bar(BAR_KF + st), 1);
+      mbar_init(bar(BAR_KE + st), 1);
+    }
+    for (int st = 0; st < kVStages; ++st) {
+      mbar_init(bar(BAR_VF + st), 1);
+      mbar_init(bar(BAR_VE + st), 1);
+    }
+    for (int i = 0; i < kItemSlots; ++i) {
+      mbar_init(bar(BAR_IF + i), 1);
+      mbar_init(bar(BAR_IE + i), kItemReaders);
+    }
+    mbar_init(bar(BAR_VTAIL), 1);
+    mbar_init(bar(BAR_DONE), 1);
+    fence_mbar_init();
+  }
+  const uint32_t bars = base + kOffOwnBars + warp * stream::kStages * 8;   // a streaming warp's own
+  if (warp < kStreamWarps && lane == 0) {
+    for (int st = 0; st < stream::kStages; ++st) mbar_init(bars + 8 * st, 1);
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(base + kOffTmemSlot, kTmemCols);
+    tmem_relinquish();
+  } else if (warp == kWarpK && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_k16);
+    tma_prefetch_desc(&tm_v16);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan has finished
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int n_pieces = __ldcg(w.header), n_items = __ldcg(w.header + 4);
   const int working = __ldcg(w.header + 6);
   if (uint32_t(__ldcg(w.header + 2)) != w.tag || n_pieces < 0 || n_pieces > w.piece_cap || n_items < 0 ||
       n_items > w.item_cap) {                      // a plan of another call: no work
     if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, kErrInvalid);
-    return;
+    n_pieces = n_items = 0;
   }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gsm + kOffTmemSlot);
   const int with_pieces = min(n_pieces, min(int(gridDim.x), working));   // CTAs that take pieces first
   const bool pieces_first = int(blockIdx.x) < with_pieces;
-  if (pieces_first && !run_pieces(&tm_q, &tm_k, &tm_v, a, w, gsm, base, n_pieces, with_pieces)) return;
-
-  // own keys: each streaming warp's ring (over the tiles, which the pieces are
-  // done with), barriers and item slots
-  if (warp >= kStreamWarps) return;
-  const uint32_t bars = base + kOffOwnBars + warp * stream::kStages * 8;
-  if (lane == 0) {
-    for (int st = 0; st < stream::kStages; ++st) mbar_init(bars + 8 * st, 1);
-    fence_mbar_init();
-    tma_prefetch_desc(&tm_k16);
-    tma_prefetch_desc(&tm_v16);
+  const bool ok = !pieces_first || run_pieces(&tm_q, &tm_k, &tm_v, a, w, gsm, base, tmem, n_pieces, with_pieces);
+  if (warp == kWarpMma) {
+    __syncwarp();
+    tmem_dealloc(tmem, kTmemCols);
   }
-  __syncwarp();
+
+  // own keys: each streaming warp's ring lies over the tiles, which the pieces are done with
+  if (!ok || warp >= kStreamWarps) return;
   // The first units are given to the CTAs that start with them, neighbouring
   // units to different SMs; the rest is claimed.
   const int others = int(gridDim.x) - with_pieces, warps = others * kStreamWarps;
@@ -1143,64 +1121,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                    pieces_first ? -1 : warp * others + int(blockIdx.x) - with_pieces, warps, 2 * warps);
 }
 
-// One warp per kJoinRows query heads of a token: their records are loaded four
-// at a time for all of them, one pass with a running maximum.
+// A warp joins kJoinRows query heads of a token at a time and goes on to the next
+// ones a grid further.  The records come from L2: what counts is bytes in flight,
+// so 8 records are requested at once, two of each of four rows or four of each of
+// two, and the next rows' description before them.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 2;
-constexpr int kJoinRecs = 4;
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a, const PrefixWork w) {
-  const int lane = threadIdx.x & 31;
-  const unsigned unit = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  const unsigned per_token = unsigned(a.num_heads + kJoinRows - 1) / kJoinRows;
-  const int tok = int(unit / per_token);
-  const int h0 = int(unit - unsigned(tok) * per_token) * kJoinRows;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tok >= a.num_tokens) return;
-  const uint32_t tag = uint32_t(__ldcg(w.header + 2));
-  const int stride = __ldcg(w.header + 1);
-  const int4 ti = __ldcg(w.token_info + tok);
+constexpr int kJoinRows = 4;
+constexpr int kJoinCtasPerSm = 2;
+
+// Rows h0 .. h0 + R - 1 of token tok, K records at a time, one pass with a running maximum.
+template <int R, int K>
+__device__ __forceinline__ void join_rows(const AttnArgs& a, const PrefixWork& w, int tok, int h0, int4 ti, int stride,
+                                          int lane) {
   const int np = ti.x, n = np + ti.z;
-  if (tag != w.tag || n < 2) return;                     // left out, or already written
-  float4 acc[kJoinRows];
-  float mx[kJoinRows], den[kJoinRows];
-  const float *pre[kJoinRows], *own[kJoinRows];
+  float4 acc[R];
+  float mx[R], den[R];
 #pragma unroll
-  for (int r = 0; r < kJoinRows; ++r) {
-    const int h = min(h0 + r, a.num_heads - 1);
-    pre[r] = w.recs + (size_t(tok) * a.num_heads + h) * stride * kPrefixRec;
-    own[r] = w.recs + (size_t(unsigned(ti.y)) + size_t(h) * ti.z) * kPrefixRec;
+  for (int r = 0; r < R; ++r) {
     acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
     mx[r] = -INFINITY;
     den[r] = 0.f;
   }
-  for (int k0 = 0; k0 < n; k0 += kJoinRecs) {
-    float4 x[kJoinRows][kJoinRecs];
-    float2 ml[kJoinRows][kJoinRecs];
+  const float* pre = w.recs + (size_t(tok) * a.num_heads + h0) * stride * kPrefixRec;
+  const float* own = w.recs + (size_t(unsigned(ti.y)) + size_t(h0) * ti.z) * kPrefixRec;
+  const int rows = min(R, a.num_heads - h0);
+  for (int k0 = 0; k0 < n; k0 += K) {
+    float4 x[R][K];
+    float2 ml[R][K];
 #pragma unroll
-    for (int k = 0; k < kJoinRecs; ++k)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int r = 0; r < kJoinRows; ++r) {
+      for (int k = 0; k < K; ++k) {
         const int kk = k0 + k;
         x[r][k] = make_float4(0.f, 0.f, 0.f, 0.f);
         ml[r][k] = make_float2(-INFINITY, 0.f);
-        if (kk < n) {
-          const float* p = kk < np ? pre[r] + size_t(kk) * kPrefixRec : own[r] + size_t(kk - np) * kPrefixRec;
+        if (kk < n && r < rows) {
+          const float* p = kk < np ? pre + size_t(r * stride + kk) * kPrefixRec : own + size_t(r * ti.z + kk - np) * kPrefixRec;
           x[r][k] = __ldcg(reinterpret_cast<const float4*>(p) + lane);
           ml[r][k] = __ldcg(reinterpret_cast<const float2*>(p + HD));
         }
       }
 #pragma unroll
-    for (int r = 0; r < kJoinRows; ++r) {
+    for (int r = 0; r < R; ++r) {
       float top = mx[r];
 #pragma unroll
-      for (int k = 0; k < kJoinRecs; ++k) top = fmaxf(top, ml[r][k].x);
+      for (int k = 0; k < K; ++k) top = fmaxf(top, ml[r][k].x);
       const float ref = top == -INFINITY ? 0.f : top;    // no key seen so far
       const float old = ex2(mx[r] - ref);
       acc[r].x *= old, acc[r].y *= old, acc[r].z *= old, acc[r].w *= old;
       den[r] *= old;
       mx[r] = top;
 #pragma unroll
-      for (int k = 0; k < kJoinRecs; ++k) {
+      for (int k = 0; k < K; ++k) {
         const float f = ex2(ml[r][k].x - ref);
         den[r] = fmaf(f, ml[r][k].y, den[r]);
         acc[r].x = fmaf(f, x[r][k].x, acc[r].x);
@@ -1211,13 +1183,43 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnArgs a, co
     }
   }
 #pragma unroll
-  for (int r = 0; r < kJoinRows; ++r) {
-    if (h0 + r >= a.num_heads) break;
+  for (int r = 0; r < R; ++r) {
+    if (r >= rows) break;
     const float inv = 1.0f / den[r];
     uint2 v;
     v.x = pack_bf16x2(acc[r].x * inv, acc[r].y * inv);
     v.y = pack_bf16x2(acc[r].z * inv, acc[r].w * inv);
     *(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (size_t(tok) * a.num_heads + h0 + r) * HD) + lane) = v;
+  }
+}
+
+// ROWS: kJoinRows, or 1 where there are few rows, which then need the fewest steps in turn.
+template <int ROWS>
+__global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) join_kernel(const AttnArgs a, const PrefixWork w) {
+  const int lane = threadIdx.x & 31;
+  const unsigned per_token = unsigned(a.num_heads + ROWS - 1) / ROWS;
+  const unsigned units = unsigned(a.num_tokens) * per_token, step = gridDim.x * (kJoinThreads / 32);
+  unsigned u = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (u >= units) return;
+  int4 ti = __ldcg(w.token_info + u / per_token);
+  const int stride = __ldcg(w.header + 1);
+  if (uint32_t(__ldcg(w.header + 2)) != w.tag) return;
+  while (u < units) {
+    const unsigned next = u + step;
+    const int4 ti_next = next < units ? __ldcg(w.token_info + next / per_token) : make_int4(0, 0, 0, 0);
+    const int tok = int(u / per_token), h0 = int(u - unsigned(tok) * per_token) * ROWS;
+    const int n = ti.x + ti.z;                           // below 2: left out, or already written
+    if (ROWS == 1) {
+      if (n > 1) join_rows<1, 8>(a, w, tok, h0, ti, stride, lane);
+    } else if (n == 2) {
+      join_rows<4, 2>(a, w, tok, h0, ti, stride, lane);
+    } else if (n > 2) {
+      join_rows<2, 4>(a, w, tok, h0, ti, stride, lane);
+      if (h0 + 2 < a.num_heads) join_rows<2, 4>(a, w, tok, h0 + 2, ti, stride, lane);
+    }
+    ti = ti_next;
+    u = next;
   }
 }
 
@@ -1253,7 +1255,7 @@ PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_
 size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
                                      int32_t num_groups) {
   const PrefixSizes z = prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups);
-  return 256 + align256(z.NG * 16) + align256((z.NG + z.S) * 4) + align256(z.S * 4) + align256(z.pieces * sizeof(Piece)) +
+  return 256 + align256(z.NG * 16) + 2 * align256(z.S * 16) + align256((z.NG + z.S) * 4) + align256(z.pieces * sizeof(Piece)) +
          align256(z.items * sizeof(SuffixItem)) + align256(z.T * 16) +
          align256((z.prefix_recs + z.own_recs) * kPrefixRec * sizeof(float));
 }
@@ -1276,22 +1278,26 @@ static cb_status launch_prefix_tc(const AttnArgs& a, const PrefixWork& w, cudaSt
   }
   const cuuint64_t dims[3] = {cuuint64_t(HD), cuuint64_t(B), cuuint64_t(a.num_blocks) * a.num_kv_heads};
   const cuuint64_t strides[2] = {cuuint64_t(HD) * 2, cuuint64_t(B) * HD * 2};
-  auto encode_kv = [&](CUtensorMap* tm, const void* pool, int rows) -> CUresult {
-    const cuuint32_t box[3] = {64, cuuint32_t(rows), 1};
+  // the pieces load blocks in 64-dim halves, the streams both halves of 16 rows at a time
+  auto encode_kv = [&](CUtensorMap* tm, const void* pool) -> CUresult {
+    const cuuint32_t box[3] = {64, cuuint32_t(B), 1};
     return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, ones,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
-  // the pieces load whole blocks, the own keys 16 rows at a time
+  auto encode_kv16 = [&](CUtensorMap* tm, const void* pool) -> CUresult {
+    const cuuint64_t dims4[4] = {64, cuuint64_t(B), 2, dims[2]};
+    const cuuint64_t strides4[3] = {cuuint64_t(HD) * 2, 128, strides[1]};
+    const cuuint32_t box[4] = {64, cuuint32_t(stream::kTileKeys), 2, 1}, ones4[4] = {1, 1, 1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims4, strides4, box, ones4,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
   CUtensorMap tk16, tv16;
-  CUresult r = encode_kv(&tk, a.k_pool, B);
-  if (r == CUDA_SUCCESS) r = encode_kv(&tv, a.v_pool, B);
-  tk16 = tk;
-  tv16 = tv;
-  if (B != stream::kTileKeys) {
-    if (r == CUDA_SUCCESS) r = encode_kv(&tk16, a.k_pool, stream::kTileKeys);
-    if (r == CUDA_SUCCESS) r = encode_kv(&tv16, a.v_pool, stream::kTileKeys);
-  }
+  CUresult r = encode_kv(&tk, a.k_pool);
+  if (r == CUDA_SUCCESS) r = encode_kv(&tv, a.v_pool);
+  if (r == CUDA_SUCCESS) r = encode_kv16(&tk16, a.k_pool);
+  if (r == CUDA_SUCCESS) r = encode_kv16(&tv16, a.v_pool);
   if (r != CUDA_SUCCESS) return fail(CB_ERR_CUDA, "shared prefixes: encoding the KV tensor maps failed (%d)", int(r));
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
@@ -1310,9 +1316,12 @@ static cb_status launch_prefix_tc(const AttnArgs& a, const PrefixWork& w, cudaSt
 }
 
 static cb_status launch_join(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
-  const int64_t warps = int64_t(a.num_tokens) * ((a.num_heads + kJoinRows - 1) / kJoinRows);
-  const unsigned grid = unsigned((warps * 32 + kJoinThreads - 1) / kJoinThreads);
-  cudaError_t e = launch_kernel(join_kernel, dim3(grid), dim3(kJoinThreads), 0, stream, true, a, w);
+  const int64_t slots = int64_t(w.num_sms) * kJoinCtasPerSm, per_cta = kJoinThreads / 32;
+  const bool few = int64_t(a.num_tokens) * a.num_heads <= slots * per_cta;
+  const int64_t warps = int64_t(a.num_tokens) * (few ? a.num_heads : (a.num_heads + kJoinRows - 1) / kJoinRows);
+  const int64_t grid = std::min<int64_t>(slots, (warps + per_cta - 1) / per_cta);
+  cudaError_t e = launch_kernel(few ? join_kernel<1> : join_kernel<kJoinRows>, dim3(unsigned(grid)), dim3(kJoinThreads), 0,
+                                stream, true, a, w);
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: join launch");
 }
 
@@ -1348,8 +1357,9 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   };
   w.header = reinterpret_cast<int32_t*>(take(256));
   w.groups = reinterpret_cast<int4*>(take(z.NG * 16));
+  w.seqs = reinterpret_cast<int4*>(take(z.S * 16));
   w.first_piece = reinterpret_cast<int32_t*>(take((z.NG + z.S) * 4));
-  w.seq_rec = reinterpret_cast<unsigned*>(take(z.S * 4));
+  w.seq_recs = reinterpret_cast<int4*>(take(z.S * 16));
   w.pieces = reinterpret_cast<Piece*>(take(z.pieces * sizeof(Piece)));
   w.items = reinterpret_cast<SuffixItem*>(take(z.items * sizeof(SuffixItem)));
   w.token_info = reinterpret_cast<int4*>(take(z.T * 16));

@@ -45,7 +45,7 @@ struct alignas(16) SuffixItem {
   unsigned rec0;               // the chunk's record of (the sequence's first token, head 0)
   int rec_step;                // records per (token, head)
   int direct;                  // 1: nothing to join, the rows are written to out
-  int pad;
+  int pad;                     // the plan's counter
 };
 static_assert(sizeof(SuffixItem) == 48, "item");
 
@@ -66,10 +66,10 @@ struct PrefixWork {
   int32_t* header;             // [0] pieces, [1] prefix records per row (stride), [2] call tag, [3] piece
                                // claims, [4] streamed items, [5] unit claims, [6] CTAs that work on
                                // pieces first (the others go to the streamed units at once)
-  int4* groups;                // [num_groups] (first sequence, first token, tokens, shared keys), those
-                               // that the plan does not hold in shared memory
-  int32_t* first_piece;        // [num_groups + num_seqs]
-  unsigned* seq_rec;           // [num_seqs] the sequence's first own record
+  int4* groups;                // [num_groups], [num_seqs], [num_groups + num_seqs]: the plan's own, where
+  int4* seqs;                  // they do not fit its shared memory
+  int32_t* first_piece;
+  int4* seq_recs;              // [num_seqs] as token_info, of the sequence's first token
   Piece* pieces;
   SuffixItem* items;
   int4* token_info;            // [num_tokens] (prefix records, first own record of head 0, own records per head, -)

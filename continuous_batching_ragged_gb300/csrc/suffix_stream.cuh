@@ -33,12 +33,20 @@ using namespace sm100;
 constexpr int kDim = kPrefixDim;
 constexpr int kTileKeys = 16;
 constexpr int kStages = 3;
-constexpr uint32_t kBox = kTileKeys * 128;             // 16 keys x 64 dims, 128-byte rows: 2 KB
+constexpr uint32_t kBox = kTileKeys * 128;             // 16 keys x 64 dims, 128-byte rows: 2 KB; a TMA box is both halves
 constexpr uint32_t kStageBytes = 4 * kBox;             // K and V, two 64-dim halves each
 constexpr uint32_t kRingBytes = kStreamWarps * kStages * kStageBytes;
 constexpr uint32_t kBarBytes = kStreamWarps * kStages * 8;
 constexpr uint32_t kSlotBytes = kStreamWarps * 2 * sizeof(SuffixItem);
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int32_t x, int32_t y, int32_t z,
+                                            int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -75,7 +83,7 @@ struct Unit {
 // `slots` are the warp's own.  `first`: its first two units, `first` and
 // first + step, are given rather than claimed; -1: claimed like the later ones,
 // which start at `claimed_from`.
-__device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttnArgs& a,
+__device__ __noinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttnArgs& a,
                                          const PrefixWork& w, int n_items, uint32_t ring, uint32_t bars,
                                          SuffixItem* slots, int first, int step, int claimed_from) {
   const int lane = threadIdx.x & 31;
@@ -117,10 +125,8 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
       const uint32_t dst = ring + st * kStageBytes, bar = bars + 8 * st;
       const int y = (it.k0 + i * kTileKeys) & (B - 1);
       mbar_arrive_expect_tx(bar, kStageBytes);
-      tma_load_3d(dst, tm_k, bar, 0, y, z);
-      tma_load_3d(dst + kBox, tm_k, bar, 64, y, z);
-      tma_load_3d(dst + 2 * kBox, tm_v, bar, 0, y, z);
-      tma_load_3d(dst + 3 * kBox, tm_v, bar, 64, y, z);
+      tma_load_4d(dst, tm_k, bar, 0, y, 0, z);
+      tma_load_4d(dst + 2 * kBox, tm_v, bar, 0, y, 0, z);
     }
     ++issued;
   };

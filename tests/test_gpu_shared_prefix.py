@@ -21,8 +21,13 @@ A = 128
 class Step:
     """Groups of sequences over one pool: [(prefix, [(own keys, query tokens), ...]), ...]; own keys include the query tokens."""
 
-    def __init__(self, groups, H, K, B, seed=0, q_scale=1.0, k_slope=0.0, extra_blocks=3, num_blocks=None, width=None):
+    def __init__(self, groups, H, K, B, seed=0, q_scale=1.0, k_slope=0.0, extra_blocks=3, num_blocks=None, width=None,
+                 ballast=True):
         from continuous_batching_ragged_gb300 import api
+        # a step shares only where that saves some 40 MB: one more group that does, whatever the others are
+        self.real = sum(len(members) for _, members in groups)
+        if ballast:
+            groups = list(groups) + [(2048, [(1, 1)] * (2 + 48_000_000 // (2048 * 4 * A * K)))]
         g = torch.Generator(device="cuda").manual_seed(seed)
         pick = torch.Generator().manual_seed(seed)
         self.H, self.K, self.B, self.groups = H, K, B, groups
@@ -82,7 +87,7 @@ class Step:
 
     def check(self, sequences=None):
         G = self.H // self.K
-        for s in range(len(self.q_l)) if sequences is None else sequences:
+        for s in range(min(self.real + 2, len(self.q_l))) if sequences is None else sequences:
             k, v = (x.double() for x in self.keys[s])
             a, b = self.cu_l[s], self.cu_l[s + 1]
             q = self.q[a:b].double().view(b - a, self.K, G, A)
@@ -138,7 +143,8 @@ def test_several_query_tokens(native_lib, H, K, B, q):
 @pytest.mark.parametrize("H,K,tokens", [(32, 8, 4), (32, 1, 2), (8, 8, 3), (32, 32, 64), (32, 8, 256)])
 def test_long_prefix(native_lib, H, K, tokens):
     """Prefixes cut into many KV segments (few rows) and into few (many rows)."""
-    st = run_checked([(20_000 if tokens < 64 else 5000, [(1 + 3 * (i % 5), 1) for i in range(tokens)])], H, K, 16, seed=tokens)
+    st = run_checked([(20_000 if tokens < 64 else 5000, [(1 + 3 * (i % 5), 1) for i in range(tokens)])], H, K, 16, seed=tokens,
+                     ballast=tokens < 64)
     first = st.out.clone()
     st.ws.fill_(7)
     st.out.fill_(float("nan"))
@@ -168,7 +174,14 @@ def test_peaked_rows(native_lib):
 def test_without_sharing(native_lib):
     """Groups of one sequence share nothing: every sequence reads its own pages, single rows and chunks."""
     run_checked([(300, [(7, 1)]), (900, [(1, 1)]), (0, [(200, 150)]), (64, [(30, 5)]), (5000, [(1, 1)]), (0, [(1, 1)])],
-                8, 2, 16, seed=7)
+                8, 2, 16, seed=7, ballast=False)
+
+
+@pytest.mark.parametrize("H,K", [(8, 8), (32, 4)])
+@pytest.mark.parametrize("q", [1, 3, 70])
+def test_small_steps(native_lib, H, K, q):
+    """Groups too small for sharing to pay: the same rows, through each sequence's own table."""
+    run_checked([(300, [(q, q)] * 3), (40, [(q + 9, q), (1, 1)]), (513, [(2, 1)] * 2)], H, K, 16, seed=8 + q, ballast=False)
 
 
 @pytest.mark.parametrize("H,K", [(8, 8), (32, 8), (16, 1), (32, 1)])
@@ -191,7 +204,7 @@ def test_infinite_and_nan_keys_of_others(native_lib):
     want[:5, 4:] = True
     want[6, :4] = True
     assert torch.equal(bad, want)
-    st.check([5, 7, 8, 9])
+    st.check([5, 7, 8, 9, 10, 11])
 
 
 @pytest.mark.parametrize("fault", ["prefix too long", "negative prefix", "gap", "overlap", "not all", "start", "page", "first page",
@@ -200,17 +213,17 @@ def test_bad_metadata(native_lib, fault):
     """What is wrong is reported; sequences that do not depend on it keep their results."""
     from continuous_batching_ragged_gb300 import api, native
     st = Step([(300, [(5, 1)] * 4), (200, [(8, 1)] * 3), (50, [(40, 1)] * 2)], 8, 2, 16, seed=9)
-    good, error = range(9), "INVALID"
+    good, error, n = range(9), "INVALID", len(st.q_l)
     if fault == "prefix too long":
         st.ctx[5], good = 200, [0, 1, 2, 3, 4, 6, 7, 8]   # its cached keys end before the prefix does
     elif fault == "negative prefix":
         st.prefix[1], good = -3, [0, 1, 2, 3, 7, 8]
     elif fault == "gap":
-        st.cu_groups[1], good = 10, []
+        st.cu_groups[1], good = n + 1, []
     elif fault == "overlap":
         st.cu_groups[2], good = 3, []
     elif fault == "not all":
-        st.cu_groups[3], good = 8, []
+        st.cu_groups[4], good = n - 1, []
     elif fault == "start":
         st.cu_groups[0], good = 1, []
     elif fault == "page":
@@ -231,24 +244,26 @@ def test_rows_behind_the_step_stay(native_lib):
     """q and out with rows behind the last sequence: the metadata's token count rules, the rest is not written."""
     from continuous_batching_ragged_gb300 import api
     st = Step([(300, [(5, 1)] * 4)], 8, 2, 16, seed=10)
+    rows = len(st.q)
     more = torch.full((7, 8, A), float("nan"), dtype=torch.bfloat16, device="cuda")
     st.q, st.out = torch.cat([st.q, more]), torch.cat([st.out, more])
-    n = api.cb_shared_prefix_workspace_size(st.cache, 8, 4, 11, 1, st.max_ctx)
+    n = api.cb_shared_prefix_workspace_size(st.cache, 8, len(st.q_l), rows + 7, 2, st.max_ctx)
     st.ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
     st.run()
     api.cb_check_device_errors()
     st.check()
-    assert bool(st.out[4:].isnan().all())
+    assert bool(st.out[rows:].isnan().all())
 
 
 def test_captured_and_replayed(native_lib):
     """A captured call replays over new groups, lengths and pages of the same sizes; two graphs share a workspace."""
     from continuous_batching_ragged_gb300 import api
-    first = Step([(300, [(5, 1)] * 4), (500, [(60, 1)] * 6)], 8, 2, 16, seed=11, width=40, num_blocks=400)
-    other = Step([(0, [(9, 1)] * 1), (540, [(25, 1)] * 9)], 8, 2, 16, seed=12, width=40, num_blocks=400)
+    sizes = dict(width=200, num_blocks=2000)
+    first = Step([(300, [(5, 1)] * 4), (500, [(60, 1)] * 6)], 8, 2, 16, seed=11, **sizes)
+    other = Step([(0, [(9, 1)] * 1), (540, [(25, 1)] * 9)], 8, 2, 16, seed=12, **sizes)
     for st in (first, other):
-        st.max_ctx = 600
-    n = api.cb_shared_prefix_workspace_size(first.cache, 8, 10, 10, 2, 600)
+        st.max_ctx = 2500
+    n = api.cb_shared_prefix_workspace_size(first.cache, 8, len(first.q_l), len(first.q), 3, 2500)
     first.ws = other.ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
     first.run()
     graphs = []
