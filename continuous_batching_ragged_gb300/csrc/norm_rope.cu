@@ -26,6 +26,7 @@ namespace {
 using cb::Vec16;
 
 constexpr int kThreads = 256;
+constexpr int kSpreadCtasPerSm = 8;   // up to so many CTAs of one row per lane group, a token is spread over several
 
 struct NormRopeArgs {
   const void *q, *k, *v;
@@ -109,11 +110,20 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
       if (!skip && turned) {
         const float* tab = a.cos_sin + int64_t(pos) * a.rot_dim;
         const int d0 = INTERLEAVED ? c * (EPV / 2) : (low ? c * EPV : c * EPV - half);
+        // 16 bytes at a time, or 8 where an interleaved fp32 lane has only two pairs
+        constexpr int kTab = INTERLEAVED ? EPV / 2 : EPV;
+        if constexpr (kTab % 4 == 0) {
 #pragma unroll
-        for (int e = 0; e < (INTERLEAVED ? EPV / 2 : EPV); e += 2) {
-          const float2 x = __ldg(reinterpret_cast<const float2*>(tab + d0 + e));
-          const float2 y = __ldg(reinterpret_cast<const float2*>(tab + half + d0 + e));
-          cs[e] = x.x, cs[e + 1] = x.y, sn[e] = y.x, sn[e + 1] = y.y;
+          for (int e = 0; e < kTab; e += 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(tab + d0 + e));
+            const float4 y = __ldg(reinterpret_cast<const float4*>(tab + half + d0 + e));
+            cs[e] = x.x, cs[e + 1] = x.y, cs[e + 2] = x.z, cs[e + 3] = x.w;
+            sn[e] = y.x, sn[e + 1] = y.y, sn[e + 2] = y.z, sn[e + 3] = y.w;
+          }
+        } else {
+          const float2 x = __ldg(reinterpret_cast<const float2*>(tab + d0));
+          const float2 y = __ldg(reinterpret_cast<const float2*>(tab + half + d0));
+          cs[0] = x.x, cs[1] = x.y, sn[0] = y.x, sn[1] = y.y;
         }
       }
     }
@@ -175,13 +185,23 @@ void launch_rows(const NormRopeArgs& a, bool interleaved, dim3 grid, cudaStream_
     norm_rope_append_kernel<T, LPR, kRows, false><<<grid, kThreads, 0, stream>>>(a);
 }
 
+// Rows in flight per lane group.
 template <typename T, int LPR>
 void launch(const NormRopeArgs& a, bool interleaved, cudaStream_t stream) {
   constexpr int kGroups = kThreads / LPR;
   const int64_t rows = int64_t(a.num_q_heads) + 2 * int64_t(a.num_kv_heads);
-  constexpr int kRows = 1;
-  const unsigned y = unsigned((rows + kRows * kGroups - 1) / (kRows * kGroups));
-  launch_rows<T, LPR, kRows>(a, interleaved, dim3(unsigned(a.num_tokens), y), stream);
+  const int64_t per_group = (rows + kGroups - 1) / kGroups;   // rows of a token per lane group, if one CTA takes it whole
+  int k = 1;
+  if (int64_t(a.num_tokens) * per_group > int64_t(kSpreadCtasPerSm) * cb::sm_count())
+    k = per_group <= 1 ? 1 : per_group == 2 ? 2 : per_group == 3 ? 3 : per_group == 4 ? 4 : 6;
+  const dim3 grid(unsigned(a.num_tokens), unsigned((rows + int64_t(k) * kGroups - 1) / (int64_t(k) * kGroups)));
+  switch (k) {
+    case 6: return launch_rows<T, LPR, 6>(a, interleaved, grid, stream);
+    case 4: return launch_rows<T, LPR, 4>(a, interleaved, grid, stream);
+    case 3: return launch_rows<T, LPR, 3>(a, interleaved, grid, stream);
+    case 2: return launch_rows<T, LPR, 2>(a, interleaved, grid, stream);
+    default: return launch_rows<T, LPR, 1>(a, interleaved, grid, stream);
+  }
 }
 
 }  // namespace

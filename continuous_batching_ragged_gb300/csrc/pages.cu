@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kMaxLayers = 128;        // layers per launch; more take several launches
 constexpr int kThreads = 256;
+constexpr int kVec = 8;                // 16-byte loads in flight per thread
 
 // The K and V pools of up to kMaxLayers layers: p[2 * layer] and p[2 * layer + 1].
 struct Pools {
@@ -109,10 +110,20 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a, const 
   for (int j = blockIdx.y; j < a.num_pools; j += gridDim.y) {
     const uint4* src = pools.p[j] + me.src * page;
     uint4* dst = pools.p[j] + me.dst * page;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const int h = i / used;
-      const int at = h * head_chunks + (i - h * used);
-      dst[at] = src[at];
+    for (int i0 = threadIdx.x; i0 < n; i0 += kThreads * kVec) {
+      uint4 v[kVec];
+      int at[kVec];
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) {
+        const int i = i0 + k * kThreads, h = i / used;
+        at[k] = i < n ? h * head_chunks + (i - h * used) : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < kVec; ++k)
+        if (at[k] >= 0) v[k] = src[at[k]];
+#pragma unroll
+      for (int k = 0; k < kVec; ++k)
+        if (at[k] >= 0) dst[at[k]] = v[k];
     }
   }
 }
@@ -174,21 +185,30 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
   const int words = (a.num_blocks + 31) / 32;
   for (int i = tid; i < words; i += kPlanThreads) bits[i] = 0;
   __syncthreads();
-  const int B = a.block_size, W = a.max_blocks_per_seq;
+  // 32 threads to a sequence, kMark pages of it in flight per thread
+  constexpr int kMark = 4;
+  const int B = a.block_size, W = a.max_blocks_per_seq, lane = tid & 31;
   unsigned bad = 0;
-  for (int s = tid; s < a.num_seqs; s += kPlanThreads) {
+  for (int s = tid >> 5; s < a.num_seqs; s += kPlanThreads / 32) {
     const int ctx = a.context_lens[s];
-    if (ctx < 0 || ctx > int64_t(W) * B) bad = cb::kErrInvalid;
-  }
-  const int64_t entries = int64_t(a.num_seqs) * W;
-  for (int64_t i = tid; i < entries; i += kPlanThreads) {
-    const int s = int(i / W), b = int(i - int64_t(s) * W);
-    if (int64_t(b) * B < a.context_lens[s]) {
-      const int blk = a.block_tables[i];
-      if (blk < 0 || blk >= a.num_blocks)
-        bad |= cb::kErrBounds;
-      else
-        atomicOr(&bits[blk >> 5], 1u << (blk & 31));
+    if (ctx < 0 || ctx > int64_t(W) * B) {
+      bad |= cb::kErrInvalid;
+      continue;
+    }
+    const int used = int((int64_t(ctx) + B - 1) / B);
+    const int32_t* row = a.block_tables + int64_t(s) * W;
+    for (int b0 = lane; b0 < used; b0 += 32 * kMark) {
+      int blk[kMark];
+#pragma unroll
+      for (int k = 0; k < kMark; ++k) blk[k] = b0 + 32 * k < used ? row[b0 + 32 * k] : 0;
+#pragma unroll
+      for (int k = 0; k < kMark; ++k) {
+        if (b0 + 32 * k >= used) break;
+        if (blk[k] < 0 || blk[k] >= a.num_blocks)
+          bad |= cb::kErrBounds;
+        else
+          atomicOr(&bits[blk[k] >> 5], 1u << (blk[k] & 31));
+      }
     }
   }
   if (bad) cb::raise_error(a.err, bad);
@@ -255,7 +275,6 @@ __global__ void __launch_bounds__(kThreads) compact_move_kernel(const CompactArg
   }
   if (n < 0) return;
   // a unit is kThreads * kVec chunks of one page of one pool
-  constexpr int kVec = 8;
   const int64_t per_page = (a.page_chunks + kThreads * kVec - 1) / (kThreads * kVec);
   const int64_t units = int64_t(moves) * a.num_pools * per_page;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
