@@ -19,11 +19,17 @@ from .native import check
 _DTYPES = {torch.bfloat16: native.CB_DTYPE_BF16, torch.float32: native.CB_DTYPE_F32}
 
 
+_cuda_ready = False
+
+
 def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
     if stream is not None:
         return int(stream.cuda_stream)
     # torch.cuda.current_stream().cuda_stream without building a Stream object (0.2 against 2.9 us a call)
-    torch.cuda.init()
+    global _cuda_ready
+    if not _cuda_ready:
+        torch.cuda.init()
+        _cuda_ready = True
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 

@@ -10,11 +10,16 @@
 // the load and the one rounding at the store is fp32.
 //
 // Bound by HBM: every row is read once and written once, a few dozen fp32
-// operations per 16 bytes in between.  A group of LPR lanes holds one row, 16
-// bytes a lane, so that the mean is log2(LPR) shuffles, the half-split pair of
-// an element sits in one other lane, and a lane's cosines, sines and weights
-// are the same for every head of its token: they are loaded once and serve the
-// kRows rows that the group keeps in flight.
+// operations per 16 bytes in between, which is near what the SMs can issue in
+// that time.  So a group of LPR lanes holds one row, 16 bytes a lane: the mean is
+// log2(LPR) shuffles, a lane's cosines, sines and weights are the same for every
+// head of its token, and where the whole head turns a lane takes 8 bytes of each
+// half, so that both elements of a pair are its own.  A persistent grid keeps the
+// next token's rows (up to three per lane group) on their way while it works on
+// one; a warp of values only copies.
+// 2048 tokens of 32 + 2 * 32 heads, bf16: 18.9 us, 5.4 TB/s (one row per lane
+// group 42 us; several rows 30; pairs in one lane and the next token in flight 24;
+// values only copied 21.9; three CTAs an SM 18.9).
 #include <algorithm>
 #include <cmath>
 
@@ -26,7 +31,8 @@ namespace {
 using cb::Vec16;
 
 constexpr int kThreads = 256;
-constexpr int kSpreadCtasPerSm = 8;   // up to so many CTAs of one row per lane group, a token is spread over several
+constexpr int kSpreadCtasPerSm = 1;   // up to so many CTAs of one row per lane group, a token is spread over several
+constexpr int kCtasPerSm = 3;         // 80 registers a thread; 2 and 4 were slower (2048 tokens: 21.9, 21.4 against 18.9 us)
 
 struct NormRopeArgs {
   const void *q, *k, *v;
@@ -57,14 +63,23 @@ __device__ __forceinline__ uint4 pack16(const float (&f)[4]) {
   return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
+// How a lane's 16 bytes of a row lie, and where its pairs are.
+enum RopeMode {
+  kHalves,       // rot_dim = head_dim, pairs (i, i + A / 2): 8 bytes of each half, so a lane has whole pairs
+  kPartial,      // pairs (i, i + rot_dim / 2): 16 bytes in order, the other element is in another lane
+  kInterleaved   // pairs (2i, 2i + 1): 16 bytes in order
+};
+
 // blockIdx.y takes kRows rows per lane group of the token's num_q_heads query,
 // num_kv_heads key and num_kv_heads value rows, in that order; blockIdx.x
-// strides over tokens.
-template <typename T, int LPR, int kRows, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRopeArgs a) {
+// strides over tokens, the next token's rows already on their way while one is
+// worked on.
+template <typename T, int LPR, int kRows, int MODE>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_append_kernel(const NormRopeArgs a) {
   constexpr int EPV = Vec16<T>::N;              // elements per lane
   constexpr int A = LPR * EPV;                  // head_dim
   constexpr int kGroups = kThreads / LPR;       // rows side by side in the CTA
+  constexpr int kTab = MODE == kPartial ? EPV : EPV / 2;   // cosines (and sines) that a lane needs
   int32_t n_tok = a.num_tokens;
   if (a.dims) {                                 // the step's token count, at most num_tokens (the capacity)
     const int32_t t = a.dims[1];
@@ -75,59 +90,80 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
     n_tok = t;
   }
   const int lane = threadIdx.x & 31;
-  const int c = threadIdx.x % LPR;              // this lane's 16-byte chunk of the row
+  const int c = threadIdx.x % LPR;              // this lane's part of the row
   const int H = a.num_q_heads, K = a.num_kv_heads, n_rows = H + 2 * K;
   const int row0 = (blockIdx.y * kRows) * kGroups + threadIdx.x / LPR;
   const int half = a.rot_dim / 2;
-  const bool turned = c * EPV < a.rot_dim;      // rot_dim is a multiple of 2 * EPV: a lane turns all or nothing
-  // half-split pairs: element d of the first half pairs with d + rot_dim / 2
-  const bool low = c * EPV < half;
-  const int partner = INTERLEAVED || !turned ? lane : lane + (low ? 1 : -1) * (half / EPV);
+  const bool turned = MODE == kHalves || c * EPV < a.rot_dim;   // rot_dim is a multiple of 2 * EPV: a lane turns all or nothing
+  const bool low = c * EPV < half;              // kPartial: element d of the first half pairs with d + rot_dim / 2
+  const int partner = MODE == kPartial && turned ? lane + (low ? 1 : -1) * (half / EPV) : lane;
+  const int d0 = MODE == kPartial ? (low ? c * EPV : c * EPV - half) : c * (EPV / 2);   // its first table entry
 
-  float wq[EPV], wk[EPV];
-  if (a.q_weight) Vec16<T>::to_float(__ldg(static_cast<const uint4*>(a.q_weight) + c), wq);
-  if (a.k_weight) Vec16<T>::to_float(__ldg(static_cast<const uint4*>(a.k_weight) + c), wk);
-
-  for (int tok = blockIdx.x; tok < n_tok; tok += gridDim.x) {
-    uint4 raw[kRows];
+  auto load16 = [&](const uint4* row) -> uint4 {
+    if constexpr (MODE != kHalves) return row[c];
+    const uint2* r = reinterpret_cast<const uint2*>(row);
+    const uint2 x = r[c], y = r[LPR + c];
+    return make_uint4(x.x, x.y, y.x, y.y);
+  };
+  auto store16 = [&](uint4* row, const uint4& v) {
+    if constexpr (MODE != kHalves) {
+      row[c] = v;
+    } else {
+      uint2* r = reinterpret_cast<uint2*>(row);
+      r[c] = make_uint2(v.x, v.y);
+      r[LPR + c] = make_uint2(v.z, v.w);
+    }
+  };
+  auto load_rows = [&](int tok, uint4 (&raw)[kRows]) {
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
       const int r = row0 + u * kGroups;
       const uint4* src = r < H       ? static_cast<const uint4*>(a.q) + tok * a.q_stride + int64_t(r) * LPR
                          : r < H + K ? static_cast<const uint4*>(a.k) + tok * a.k_stride + int64_t(r - H) * LPR
                                      : static_cast<const uint4*>(a.v) + tok * a.v_stride + int64_t(r - H - K) * LPR;
-      raw[u] = r < n_rows ? *(src + c) : make_uint4(0, 0, 0, 0);
+      raw[u] = r < n_rows ? load16(src) : make_uint4(0, 0, 0, 0);
     }
-    const int64_t slot = a.slots[tok];
-    float cs[EPV], sn[EPV];                     // interleaved: the first EPV / 2 hold the lane's pairs
+  };
+
+  int tok = blockIdx.x;
+  if (tok >= n_tok) return;
+  uint4 next[kRows];
+  load_rows(tok, next);
+  int64_t next_slot = a.slots[tok];
+  int next_pos = a.rot_dim > 0 ? a.positions[tok] : 0;
+  const uint4 wq = a.q_weight ? load16(static_cast<const uint4*>(a.q_weight)) : make_uint4(0, 0, 0, 0);
+  const uint4 wk = a.k_weight ? load16(static_cast<const uint4*>(a.k_weight)) : make_uint4(0, 0, 0, 0);
+
+  for (; tok < n_tok; tok += gridDim.x) {
+    uint4 raw[kRows];
 #pragma unroll
-    for (int e = 0; e < EPV; ++e) cs[e] = 1.f, sn[e] = 0.f;
-    bool skip = false;
-    if (a.rot_dim > 0) {
-      const int pos = a.positions[tok];
-      skip = pos < 0 || pos >= a.max_positions;
-      if (skip && threadIdx.x == 0 && blockIdx.y == 0) cb::raise_error(a.err, cb::kErrBounds);
-      if (!skip && turned) {
-        const float* tab = a.cos_sin + int64_t(pos) * a.rot_dim;
-        const int d0 = INTERLEAVED ? c * (EPV / 2) : (low ? c * EPV : c * EPV - half);
-        // 16 bytes at a time, or 8 where an interleaved fp32 lane has only two pairs
-        constexpr int kTab = INTERLEAVED ? EPV / 2 : EPV;
-        if constexpr (kTab % 4 == 0) {
+    for (int u = 0; u < kRows; ++u) raw[u] = next[u];
+    const int64_t slot = next_slot;
+    const int pos = next_pos;
+    const bool skip = a.rot_dim > 0 && (pos < 0 || pos >= a.max_positions);
+    float cs[kTab], sn[kTab];
+    if (a.rot_dim > 0 && !skip && turned) {
+      const float* tab = a.cos_sin + int64_t(pos) * a.rot_dim + d0;
 #pragma unroll
-          for (int e = 0; e < kTab; e += 4) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(tab + d0 + e));
-            const float4 y = __ldg(reinterpret_cast<const float4*>(tab + half + d0 + e));
-            cs[e] = x.x, cs[e + 1] = x.y, cs[e + 2] = x.z, cs[e + 3] = x.w;
-            sn[e] = y.x, sn[e + 1] = y.y, sn[e + 2] = y.z, sn[e + 3] = y.w;
-          }
-        } else {
-          const float2 x = __ldg(reinterpret_cast<const float2*>(tab + d0));
-          const float2 y = __ldg(reinterpret_cast<const float2*>(tab + half + d0));
-          cs[0] = x.x, cs[1] = x.y, sn[0] = y.x, sn[1] = y.y;
-        }
+      for (int e = 0; e < kTab; e += 2) {       // 8 bytes each: merged to 16 where they are aligned
+        const float2 x = __ldg(reinterpret_cast<const float2*>(tab + e));
+        const float2 y = __ldg(reinterpret_cast<const float2*>(tab + half + e));
+        cs[e] = x.x, cs[e + 1] = x.y, sn[e] = y.x, sn[e + 1] = y.y;
       }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kTab; ++e) cs[e] = 1.f, sn[e] = 0.f;
     }
-    if (skip) continue;                         // the same for the whole CTA
+    if (tok + int(gridDim.x) < n_tok) {
+      const int t = tok + gridDim.x;
+      load_rows(t, next);
+      next_slot = a.slots[t];
+      next_pos = a.rot_dim > 0 ? a.positions[t] : 0;
+    }
+    if (skip) {                                 // the same for the whole CTA
+      if (threadIdx.x == 0 && blockIdx.y == 0) cb::raise_error(a.err, cb::kErrBounds);
+      continue;
+    }
     const bool bad_slot = slot >= a.num_slots;
     if (bad_slot && threadIdx.x == 0 && blockIdx.y == 0) cb::raise_error(a.err, cb::kErrBounds);
     const bool cached = slot >= 0 && !bad_slot;
@@ -136,6 +172,10 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
       const int r = row0 + u * kGroups;
+      if (!__any_sync(0xffffffffu, r < H + K)) {  // values only: nothing to compute
+        if (r < n_rows && cached) store16(a.v_pool + dst0 + (r - H - K) * head_step, raw[u]);
+        continue;
+      }
       float x[EPV];
       Vec16<T>::to_float(raw[u], x);
       const bool is_q = r < H, norm = is_q ? a.q_weight != nullptr : a.k_weight != nullptr;
@@ -146,61 +186,65 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
       for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       if (norm) {
         const float inv = rsqrtf(ss * (1.0f / A) + a.eps);
+        float wt[EPV];
+        Vec16<T>::to_float(is_q ? wq : wk, wt);
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) x[e] = x[e] * inv * (is_q ? wq[e] : wk[e]);
+        for (int e = 0; e < EPV; ++e) x[e] = x[e] * inv * wt[e];
       }
-      if (INTERLEAVED) {
-        if (turned) {
-#pragma unroll
-          for (int p = 0; p < EPV / 2; ++p) {
-            const float y = x[2 * p] * cs[p] - x[2 * p + 1] * sn[p];
-            x[2 * p + 1] = x[2 * p + 1] * cs[p] + x[2 * p] * sn[p];
-            x[2 * p] = y;
-          }
-        }
-      } else {
+      if constexpr (MODE == kPartial) {
 #pragma unroll
         for (int e = 0; e < EPV; ++e) {
           const float other = __shfl_sync(0xffffffffu, x[e], partner);
           if (turned) x[e] = x[e] * cs[e] + (low ? -other : other) * sn[e];
         }
+      } else if (turned) {
+#pragma unroll
+        for (int p = 0; p < EPV / 2; ++p) {
+          const int i = MODE == kHalves ? p : 2 * p, j = MODE == kHalves ? p + EPV / 2 : 2 * p + 1;
+          const float y = x[i] * cs[p] - x[j] * sn[p];
+          x[j] = x[j] * cs[p] + x[i] * sn[p];
+          x[i] = y;
+        }
       }
       if (r < H) {
-        a.q_out[(int64_t(tok) * H + r) * LPR + c] = pack16(x);
+        store16(a.q_out + (int64_t(tok) * H + r) * LPR, pack16(x));
       } else if (r < n_rows && cached) {
         if (r < H + K)
-          a.k_pool[dst0 + (r - H) * head_step + c] = pack16(x);
+          store16(a.k_pool + dst0 + (r - H) * head_step, pack16(x));
         else
-          a.v_pool[dst0 + (r - H - K) * head_step + c] = raw[u];
+          store16(a.v_pool + dst0 + (r - H - K) * head_step, raw[u]);
       }
     }
   }
 }
 
 template <typename T, int LPR, int kRows>
-void launch_rows(const NormRopeArgs& a, bool interleaved, dim3 grid, cudaStream_t stream) {
+void launch_rows(const NormRopeArgs& a, bool interleaved, unsigned chunks, cudaStream_t stream) {
+  const int64_t ctas = std::max<int64_t>(1, int64_t(kCtasPerSm) * cb::sm_count() / chunks);
+  const dim3 grid(unsigned(std::min<int64_t>(a.num_tokens, ctas)), chunks);
   if (interleaved)
-    norm_rope_append_kernel<T, LPR, kRows, true><<<grid, kThreads, 0, stream>>>(a);
+    norm_rope_append_kernel<T, LPR, kRows, kInterleaved><<<grid, kThreads, 0, stream>>>(a);
+  else if (a.rot_dim == LPR * Vec16<T>::N)
+    norm_rope_append_kernel<T, LPR, kRows, kHalves><<<grid, kThreads, 0, stream>>>(a);
   else
-    norm_rope_append_kernel<T, LPR, kRows, false><<<grid, kThreads, 0, stream>>>(a);
+    norm_rope_append_kernel<T, LPR, kRows, kPartial><<<grid, kThreads, 0, stream>>>(a);
 }
 
-// Rows in flight per lane group.
+// Rows in flight per lane group: as many as a token has for each, where there are
+// tokens enough to fill the GPU that way.
 template <typename T, int LPR>
 void launch(const NormRopeArgs& a, bool interleaved, cudaStream_t stream) {
   constexpr int kGroups = kThreads / LPR;
   const int64_t rows = int64_t(a.num_q_heads) + 2 * int64_t(a.num_kv_heads);
-  const int64_t per_group = (rows + kGroups - 1) / kGroups;   // rows of a token per lane group, if one CTA takes it whole
+  const int64_t per_group = (rows + kGroups - 1) / kGroups;
   int k = 1;
   if (int64_t(a.num_tokens) * per_group > int64_t(kSpreadCtasPerSm) * cb::sm_count())
-    k = per_group <= 1 ? 1 : per_group == 2 ? 2 : per_group == 3 ? 3 : per_group == 4 ? 4 : 6;
-  const dim3 grid(unsigned(a.num_tokens), unsigned((rows + int64_t(k) * kGroups - 1) / (int64_t(k) * kGroups)));
+    k = per_group <= 1 ? 1 : per_group % 3 != 0 && per_group % 2 == 0 ? 2 : 3;
+  const unsigned chunks = unsigned((rows + int64_t(k) * kGroups - 1) / (int64_t(k) * kGroups));
   switch (k) {
-    case 6: return launch_rows<T, LPR, 6>(a, interleaved, grid, stream);
-    case 4: return launch_rows<T, LPR, 4>(a, interleaved, grid, stream);
-    case 3: return launch_rows<T, LPR, 3>(a, interleaved, grid, stream);
-    case 2: return launch_rows<T, LPR, 2>(a, interleaved, grid, stream);
-    default: return launch_rows<T, LPR, 1>(a, interleaved, grid, stream);
+    case 3: return launch_rows<T, LPR, 3>(a, interleaved, chunks, stream);
+    case 2: return launch_rows<T, LPR, 2>(a, interleaved, chunks, stream);
+    default: return launch_rows<T, LPR, 1>(a, interleaved, chunks, stream);
   }
 }
 
