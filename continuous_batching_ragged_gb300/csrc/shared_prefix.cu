@@ -97,7 +97,7 @@ constexpr int kSeqCache = 768;           // sequences kept in shared memory
 constexpr int kJobCache = 768;           // jobs whose first piece is kept in shared memory
 constexpr int kExtraPieces = 1024;       // pieces beyond one per (row tile pair, key/value head)
 constexpr int64_t kExtraRecs = 131072;   // records beyond two per row (69 MB)
-constexpr int kMinChunkTiles = 8;        // shortest chunk of streamed keys, in 16-key tiles
+constexpr int kMinChunkTiles = 4;        // shortest chunk of streamed keys, in 16-key tiles
 constexpr int kStreamRows = 16;          // query rows per row tile of a stream
 constexpr int kUnitsPerWarp = 3;         // streamed units that each warp should get
 constexpr int kMaxSms = 160;             // SMs that the lists are sized for
@@ -109,11 +109,11 @@ constexpr float kTileUsTwo = 1.8f;       // a KV tile against two row tiles, one
 constexpr float kTileUsOne = 1.4f;       // a KV tile against one row tile, at an SM's share of HBM (0.85 alone)
 constexpr float kPieceUs = 5.0f;         // a piece beyond its tiles: Q, the pipeline's fill, the records
 constexpr float kBytesPerUs = 6.7e6f;    // HBM
-constexpr float kStreamBytesPerUsPerSm = 6.0e4f;
+constexpr float kStreamBytesPerUsPerSm = 4.2e4f;   // streams of one SM
 constexpr float kJoinBytesPerUs = 4.0e6f;
 constexpr float kShareUs = 6.0f;          // what a step's pieces and join take at least
-constexpr int kSmSteps = 16;             // SM splits that are scored: 1/16 .. 16/16 of the SMs
-static_assert(kSegChoices * kSmSteps == kPlanThreads, "a thread scores one choice");
+constexpr int kWaveSteps = 16;           // SM splits that are scored: those that the pieces fill in 1 .. 16 waves
+static_assert(kSegChoices * kWaveSteps == kPlanThreads, "a thread scores one choice");
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -179,6 +179,7 @@ __device__ __noinline__ void add_warp_sum(unsigned long long* sum, int64_t v) {
     atomicAdd(sum, lo + ((unsigned long long)mid << 20) + ((unsigned long long)hi << 40));
 }
 
+__device__ __forceinline__ int sms_of(int pieces, int waves, int num_sms) { return min(num_sms, (pieces + waves - 1) / waves); }
 __device__ __forceinline__ int seg_choice(int i) { return i < 24 ? i + 1 : 24 + (i - 23) * 5; }
 
 // Rows that a set of pieces has in common: a group's over its prefix, or a
@@ -355,18 +356,19 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
       n_work[c] = work;
       n_piece[c] = piece;
     }
-    static_assert(kLanes == kSmSteps, "the thread's n is the one that it scores");
+    static_assert(kLanes == kWaveSteps, "the thread's n is the one that it scores");
     const float piece_bytes = bytes * key_bytes, own_bytes = float(sums[2]) * key_bytes;
     __syncthreads();
-    const int k = (tid % kSmSteps + 1) * w.num_sms / kSmSteps, of_n = n_pieces_of[c];
+    // as many SMs as the pieces fill in 1 .. 16 waves
+    const int of_n = n_pieces_of[c], k = of_n > 0 ? sms_of(of_n, tid % kWaveSteps + 1, w.num_sms) : 0;
     unsigned long long key = ~0ull;
-    if (of_n > 0 && k > 0 && (own_bytes > 0.f || k == w.num_sms)) {
+    if (of_n > 0) {
       // pieces of one size run in whole waves; unequal ones fill the gaps
       const float waves = ceilf(__fdividef(float(of_n), float(k))) * n_piece[c];
       float us = fminf(waves, __fdividef(n_work[c], float(k)) + n_piece[c]);
       us = fmaxf(us, piece_bytes * (1.0f / kBytesPerUs));
       const float beside = fminf(kBytesPerUs * us - piece_bytes, float(w.num_sms - k) * kStreamBytesPerUsPerSm * us);
-      us += fmaxf(0.f, own_bytes - beside) * (1.0f / kBytesPerUs);
+      us += __fdividef(fmaxf(0.f, own_bytes - beside), fminf(kBytesPerUs, float(w.num_sms) * kStreamBytesPerUsPerSm));
       us += float(T) * float(H) * float(n * alt_recs) * (kPrefixRec * 4.0f / kJoinBytesPerUs);
       key = ((unsigned long long)(__float_as_uint(us)) << 32) | unsigned(tid);
     }
@@ -379,8 +381,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     __syncthreads();
     bad |= s_best == ~0ull;                        // n = 1 fits unless token ranges overlap
     const int i = int(unsigned(s_best));
-    n_segs = seg_choice((i & (kPlanThreads - 1)) / kSmSteps);
-    working = (i % kSmSteps + 1) * w.num_sms / kSmSteps;
+    const int best_c = (i & (kPlanThreads - 1)) / kWaveSteps;
+    n_segs = seg_choice(best_c);
+    working = sms_of(max(1, n_pieces_of[best_c]), (i & (kWaveSteps - 1)) + 1, w.num_sms);
     longest = ceil_div_fast(tiles_max, n_segs);
   }
   const int stride = n_segs * alt_recs;
