@@ -356,7 +356,8 @@ extern "C" size_t cb_shared_prefix_workspace_size(const cb_kv_cache* cache, int3
       num_q_heads / cache->num_heads > kMaxPrefixGroup || num_seqs < 0 || num_tokens < 0 || num_groups < 0 ||
       max_context_len < 0)
     return 0;
-  return cb::shared_prefix_workspace_bytes(num_q_heads, cache->num_heads, num_seqs, num_tokens, num_groups);
+  return cb::shared_prefix_workspace_bytes(num_q_heads, cache->num_heads, num_seqs, num_tokens, num_groups,
+                                           max_context_len);
 }
 
 extern "C" cb_status cb_shared_prefix_attention(const void* q, int32_t num_q_heads, const cb_kv_cache* cache,

@@ -149,7 +149,7 @@ cb_status launch_decode_tc(const AttnArgs& a, const StepPlan& plan, bool after_p
 // Steps with shared prefixes (bf16, head_dim 128, block size a multiple of 16,
 // at most 128 query heads per key/value head): the workspace, and the step.
 size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
-                                     int32_t num_groups);
+                                     int32_t num_groups, int32_t max_context_len);
 cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
                             void* workspace, cudaStream_t stream);
 

@@ -399,6 +399,9 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     const int s = s0 + tid;
     int4 q = make_int4(0, 0, 0, 0), gr = q;
     int pre = 0, rt = 0, nch = 0;
+    // units are claimed in the order of the sequences: the last quarter's are half as long, so that the
+    // warps end closer together
+    const int Ls = s < S - S / 4 ? L : max(kMinChunkTiles, (L + 1) / 2);
     if (s < S) q = seqs[s];
     if (q.x > 0) {
       gr = groups[q.w];
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
       if (is_chunk(q, G)) {
         nch = segments(q.x, longest).x * (q.z <= TT ? 2 : 1);
       } else {
-        nch = ceil_div_fast((q.x + stream::kTileKeys - 1) / stream::kTileKeys, L);
+        nch = ceil_div_fast((q.x + stream::kTileKeys - 1) / stream::kTileKeys, Ls);
         rt = (q.z * G + kStreamRows - 1) / kStreamRows;
       }
     }
@@ -427,8 +430,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
 #pragma unroll 1
       for (int i = 0; i < int(n_items); ++i) {
         it.rec0 = rec + it.pad;                    // `pad` counts the chunks
-        it.k0 = it.pad * L * stream::kTileKeys;
-        it.k1 = min(q.x, it.k0 + L * stream::kTileKeys);
+        it.k0 = it.pad * Ls * stream::kTileKeys;
+        it.k1 = min(q.x, it.k0 + Ls * stream::kTileKeys);
         *out++ = it;
         if (++it.pad == nch) it.pad = 0, it.row0 += kStreamRows;
       }
@@ -1236,7 +1239,8 @@ struct PrefixSizes {
   size_t S, T, NG, pieces, items, prefix_recs, piece_recs, own_recs;
 };
 int tile_tokens(int group_heads) { return BM / group_heads; }
-PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups) {
+PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
+                         int32_t max_context_len) {
   PrefixSizes z;
   z.S = size_t(num_seqs), z.T = size_t(num_tokens), z.NG = size_t(num_groups);
   const size_t G = size_t(num_q_heads / num_kv_heads), rows = z.T * size_t(num_q_heads);
@@ -1246,18 +1250,20 @@ PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_
   z.pieces = size_t(num_kv_heads) * (pairs + std::min(z.NG, z.S / 2) + 1 + (chunks ? pairs + z.S : 0)) + kExtraPieces;
   z.prefix_recs = std::min(rows * 2 * kMaxSegs, rows * 2 + size_t(kExtraRecs));
   z.piece_recs = chunks ? rows * 2 + size_t(kExtraRecs) : 0;
-  // ceil(x / L) <= x / L + 1 for every streamed sequence, and all x / L together are at most `units`
-  const size_t units = size_t(kMaxSms) * kStreamWarps * kUnitsPerWarp;
+  // ceil(x / L) <= x / L + 1 for every streamed sequence, and all x / L together are at most the units aimed for,
+  // twice that where L is halved
+  const size_t units = 2 * size_t(kMaxSms) * kStreamWarps * kUnitsPerWarp;
+  const size_t chunks_of_row = (size_t(max_context_len) + stream::kTileKeys * kMinChunkTiles - 1) / (stream::kTileKeys * kMinChunkTiles);
   z.items = z.T * G / kStreamRows + z.S + units + 1;
-  z.own_recs = z.piece_recs + rows + kStreamRows * units;
+  z.own_recs = z.piece_recs + std::min(rows * chunks_of_row, rows + kStreamRows * units);
   return z;
 }
 
 }  // namespace
 
 size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
-                                     int32_t num_groups) {
-  const PrefixSizes z = prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups);
+                                     int32_t num_groups, int32_t max_context_len) {
+  const PrefixSizes z = prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len);
   return 256 + align256(z.NG * 16) + 2 * align256(z.S * 16) + align256((z.NG + z.S) * 4) + align256(z.pieces * sizeof(Piece)) +
          align256(z.items * sizeof(SuffixItem)) + align256(z.T * 16) +
          align256((z.prefix_recs + z.own_recs) * kPrefixRec * sizeof(float));
@@ -1335,7 +1341,7 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   NvtxRange nvtx("cb.shared_prefix");
   if (int64_t(a.num_blocks) * a.num_kv_heads >= (int64_t(1) << 31))
     return fail(CB_ERR_UNSUPPORTED, "shared prefixes: num_blocks * num_kv_heads must fit in int32");
-  const PrefixSizes z = prefix_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups);
+  const PrefixSizes z = prefix_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups, a.max_context_len);
   if (z.pieces > 0x7FFFFFFF || z.items > size_t(0x7FFFFFFF / a.num_kv_heads) || z.prefix_recs > 0x7FFFFFFF ||
       z.own_recs > 0x7FFFFFFF)
     return fail(CB_ERR_UNSUPPORTED, "shared prefixes: too many tokens");
