@@ -86,10 +86,11 @@ class KVCache:
 
 class KVCacheStack:
     """The caches of a model's layers, all of one shape: the `layers` argument of the
-    page operations.  Holds the caches and the C array that describes them."""
+    page operations.  Holds the tensors that the caches have when it is made, and the C
+    array that describes them; a cache that gets other tensors needs a new stack."""
 
     def __init__(self, caches: Sequence[KVCache]):
-        self.caches = list(caches)
+        self.caches = tuple(KVCache(c.k, c.v) for c in caches)
         if not self.caches:
             raise ValueError("at least one layer")
         self.c_array = (native.cb_kv_cache * len(self.caches))(*(c.c_struct() for c in self.caches))

@@ -13,8 +13,7 @@
 //   * 1 to 16 rows would leave a 64- or 128-row tcgen05 tile nearly empty and
 //     its accumulator a round trip through tensor memory away.  Here the warp's
 //     16 x 16 score tile and 16 x 128 output tile stay in registers between
-//     mma.sync m16n8k16 steps: 32 of them per 8 KB of keys and values, an
-//     eighth of what that path could issue in the time HBM needs for the bytes;
+//     mma.sync m16n8k16 steps, 32 of them per 8 KB of keys and values;
 //   * a unit leaves its rows unnormalised, (acc, max, sum) in fp32, for the join;
 //     a row with a single record is written to out at once.
 #pragma once

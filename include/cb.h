@@ -156,9 +156,10 @@ cb_status cb_norm_rope_append(const cb_norm_rope* in, int32_t num_q_heads, const
  *                 read if the parent ends on a page border.  A new page must be in no
  *                 table (the caller allocates).
  * On the device, a fork is left out whole and the error word set if a row or length
- * is out of range (CB_ERR_INVALID), a page id is (CB_ERR_BOUNDS), its child is also a
- * parent or another fork's child, or its new page is another fork's or a page that
- * one copies from (CB_ERR_INVALID).
+ * is out of range (CB_ERR_INVALID), the page copied from or to is (CB_ERR_BOUNDS), its
+ * child is also a parent or another fork's child, or its new page is another fork's or
+ * a page that one copies from (CB_ERR_INVALID).  Ids of full pages are copied as they
+ * are.
  * ------------------------------------------------------------------------- */
 cb_status cb_fork_sequences(const cb_kv_cache* layers, int32_t num_layers, int32_t* block_tables,
                             int32_t* context_lens, int32_t table_rows, int32_t max_blocks_per_seq,
@@ -382,10 +383,11 @@ cb_status cb_padded_attention(const void* q, const cb_kv_cache* cache, const int
  *                of every sequence of group g are the same ones.  At most
  *                context_lens[s] - q_len_s for each of them (cached before this
  *                step); any length from 0, whole pages of it are shared work.
- * The whole pages of the prefix are read through the table of the group's first
- * sequence; a partial page behind them through each sequence's own.  The result
- * is cb_ragged_attention_gqa's within fp32 accumulation rounding and the bf16
- * rounding of P, not bit for bit; it is the same from call to call.
+ * Where a step saves enough reads for it, the whole pages of a prefix are read through
+ * the table of the group's first sequence, and all else through each sequence's own;
+ * so every sequence's table has to name its whole context.  The result is
+ * cb_ragged_attention_gqa's within fp32 accumulation rounding and the bf16 rounding
+ * of P, not bit for bit; it is the same from call to call.
  * Needs a bf16 cache with head_dim 128, a block size that is a multiple of 16
  * and at most 128 query heads per key/value head (CB_ERR_UNSUPPORTED otherwise).
  * On the device, groups that do not cover the sequences in order leave out the

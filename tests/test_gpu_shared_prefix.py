@@ -308,3 +308,32 @@ def test_on_another_stream_back_to_back(native_lib):
 def test_pages_past_32_bit_offsets(native_lib):
     nb = (1 << 32) // (8 * 16 * A) + 500
     run_checked([(500, [(3, 1), (40, 1), (90, 50)]), (100, [(1, 1)] * 2)], 8, 8, 16, seed=13, num_blocks=nb)
+
+
+@pytest.mark.parametrize("q", [1, 90])
+def test_more_sequences_than_the_plan_caches(native_lib, q):
+    """More groups and sequences than the plan keeps in shared memory; with chunks, more jobs too."""
+    g = torch.Generator().manual_seed(q)
+    r = lambda a, b: int(torch.randint(a, b + 1, (1,), generator=g))  # noqa: E731
+    groups = [(r(0, 200), [(q + r(0, 9), q) if i % 40 == 0 else (r(1, 40), 1)] * r(0, 3)) for i in range(700)]
+    run_checked(groups, 4, 2, 16, seed=90 + q)
+
+
+@pytest.mark.parametrize("H,K", [(128, 1), (100, 1), (66, 1), (240, 2)])
+def test_many_query_heads_of_one_key_head(native_lib, H, K):
+    """One token, or few, fill a row tile: 128 rows, and tiles with rows of no token."""
+    run_checked([(300, [(5, 1)] * 3), (700, [(40, 1), (9, 3)]), (50, [(200, 30)])], H, K, 32, seed=H)
+
+
+def test_two_calls_at_once(native_lib):
+    """Two streams, a workspace each."""
+    from continuous_batching_ragged_gb300 import api
+    steps = [Step([(400, [(90 + i, 1)] * 20), (100, [(300, 70)])], 8, 2, 16, seed=40 + i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, stream in zip(steps, streams):
+            st.run(stream=stream)
+    for st, stream in zip(steps, streams):
+        api.cb_check_device_errors(stream)
+        st.check()
