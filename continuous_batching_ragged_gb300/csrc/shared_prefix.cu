@@ -214,8 +214,6 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // they wait for this grid on the device
   __shared__ int64_t warp_sums[kPlanThreads / 32];
   __shared__ unsigned long long sums[4], s_best;
-  __shared__ float n_work[kSegChoices], n_piece[kSegChoices];
-  __shared__ int n_pieces_of[kSegChoices];
   __shared__ int4 gcache[kGroupCache], scache[kSeqCache];
   __shared__ int m_cu[kSeqCache + 1], m_ctx[kSeqCache], p_first[kJobCache];
   __shared__ int s_alt, s_tiles;
@@ -320,14 +318,14 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
 
   // Segments: no longer than the longest range / n, and the SMs that take pieces
   // first; the rest streams own keys beside them, which leaves the tensor cores
-  // idle as large groups' pieces do HBM.  First the pieces of every n, then
-  // every (n, SMs) is scored.
+  // idle as large groups' pieces do HBM.  A thread scores one (n, SMs).
   int longest = 1, working = w.num_sms, n_segs = 1;
   if (all_first > 0 && !bad) {
     constexpr int kLanes = kPlanThreads / kSegChoices;   // threads per n, each with a share of the jobs
     const int c = tid / kLanes, n = seg_choice(c), len = ceil_div_fast(tiles_max, n);
+    float bytes = 0.f, work = 0.f, piece = 0.f;
     int64_t pieces = 0, own_recs = 0;
-    float work = 0.f, piece = 0.f, bytes = 0.f;
+#pragma unroll 1
     for (int j = tid % kLanes; j < jobs; j += kLanes) {
       const Job jb = get_job(view, j);
       if (jb.keys == 0) continue;
@@ -349,28 +347,20 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
       piece = fmaxf(piece, __shfl_xor_sync(0xffffffffu, piece, x));
       bytes += __shfl_xor_sync(0xffffffffu, bytes, x);
     }
-    if (tid % kLanes == 0) {
-      const bool fits = pieces <= w.piece_cap && int64_t(T) * H * n * alt_recs <= w.prefix_rec_cap &&
-                        own_recs <= w.piece_rec_cap;
-      n_pieces_of[c] = fits ? int(pieces) : 0;
-      n_work[c] = work;
-      n_piece[c] = piece;
-    }
+    const int64_t recs = int64_t(T) * H * n * alt_recs;
     static_assert(kLanes == kWaveSteps, "the thread's n is the one that it scores");
     const float piece_bytes = bytes * key_bytes, own_bytes = float(sums[2]) * key_bytes;
-    __syncthreads();
-    // as many SMs as the pieces fill in 1 .. 16 waves
-    const int of_n = n_pieces_of[c], k = of_n > 0 ? sms_of(of_n, tid % kWaveSteps + 1, w.num_sms) : 0;
     unsigned long long key = ~0ull;
-    if (of_n > 0) {
-      // pieces of one size run in whole waves; unequal ones fill the gaps
-      const float waves = ceilf(__fdividef(float(of_n), float(k))) * n_piece[c];
-      float us = fminf(waves, __fdividef(n_work[c], float(k)) + n_piece[c]);
+    if (pieces > 0 && pieces <= w.piece_cap && recs <= w.prefix_rec_cap && own_recs <= w.piece_rec_cap) {
+      // as many SMs as the pieces fill in 1 .. 16 waves; those of one size run in whole waves, unequal ones fill the gaps
+      const int k = sms_of(int(pieces), tid % kWaveSteps + 1, w.num_sms);
+      const float per_sm = __fdividef(1.0f, float(k));
+      float us = fminf(ceilf(float(pieces) * per_sm) * piece, work * per_sm + piece);
       us = fmaxf(us, piece_bytes * (1.0f / kBytesPerUs));
       const float beside = fminf(kBytesPerUs * us - piece_bytes, float(w.num_sms - k) * kStreamBytesPerUsPerSm * us);
       us += __fdividef(fmaxf(0.f, own_bytes - beside), fminf(kBytesPerUs, float(w.num_sms) * kStreamBytesPerUsPerSm));
-      us += float(T) * float(H) * float(n * alt_recs) * (kPrefixRec * 4.0f / kJoinBytesPerUs);
-      key = ((unsigned long long)(__float_as_uint(us)) << 32) | unsigned(tid);
+      us += float(recs) * (kPrefixRecBytes / kJoinBytesPerUs);
+      key = ((unsigned long long)(__float_as_uint(us)) << 32) | unsigned(k << 16 | n);
     }
 #pragma unroll 1
     for (int x = 16; x > 0; x >>= 1) {
@@ -380,10 +370,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     if ((tid & 31) == 0) atomicMin(&s_best, key);
     __syncthreads();
     bad |= s_best == ~0ull;                        // n = 1 fits unless token ranges overlap
-    const int i = int(unsigned(s_best));
-    const int best_c = (i & (kPlanThreads - 1)) / kWaveSteps;
-    n_segs = seg_choice(best_c);
-    working = sms_of(max(1, n_pieces_of[best_c]), (i & (kWaveSteps - 1)) + 1, w.num_sms);
+    n_segs = bad ? 1 : int(s_best & 0xffff);
+    working = bad ? w.num_sms : int(unsigned(s_best) >> 16);
     longest = ceil_div_fast(tiles_max, n_segs);
   }
   const int stride = n_segs * alt_recs;
@@ -542,6 +530,12 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t x, uint64_t y) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
   return r;
 }
+// 32 bytes in one store (aligned)
+__device__ __forceinline__ void store32(float* p, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -600,7 +594,7 @@ struct BlockWindow {
 // false.
 __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                            const AttnArgs& a, const PrefixWork& w, uint8_t* gsm, uint32_t base, uint32_t tmem,
-                                           int n_pieces, int with_pieces) {
+                                           int n_pieces, int with_pieces, int4 first_part) {
   auto bar = [&](int i) -> uint32_t { return base + kOffBar + 8u * uint32_t(i); };
   Piece* items = reinterpret_cast<Piece*>(gsm + kOffItems);
   const int warp = threadIdx.x >> 5;
@@ -636,8 +630,8 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         break;
       }
       if (lane < int(sizeof(Piece) / 16)) {
-        int4 part = make_int4(0, 0, 0, 0);
-        if (u < n_pieces) part = __ldcg(reinterpret_cast<const int4*>(w.pieces + u) + lane);
+        int4 part = first_part;
+        if (n > 0 && u < n_pieces) part = __ldcg(reinterpret_cast<const int4*>(w.pieces + u) + lane);
         reinterpret_cast<int4*>(items + slot)[lane] = part;
       }
       __syncwarp();
@@ -981,14 +975,23 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
       cnt += steps;
       // The rows' records of this segment (in the alternating mode, of its even
       // or odd tiles).  A lane holds one row; stored as it is, each store of the
-      // warp would touch 32 lines.  So every 8 lanes first transpose their 8
-      // rows of 32 dims in units of 16 bytes: a store is then 4 whole lines.
+      // warp would touch 32 lines.  So every 4 lanes first transpose their 4
+      // rows of 32 dims in units of 32 bytes: a store is then 8 whole lines (2.4 to
+      // 3.5 us a piece; in units of 16 bytes over 8 lanes, 3.5 to 4.8).
       const bool direct = it.flags & kPieceDirect;
       const int row_tok = toff + i / G, head = it.hk * G + i % G;
       const unsigned rec = direct ? unsigned(it.tok0 + row_tok) * unsigned(H) + unsigned(head)
                                   : it.rec0 + unsigned((row_tok * H + head) * it.rec_step + (alt ? t : 0));
       const float inv = direct ? 1.0f / l : 1.0f;
       if (work) {
+        unsigned at[4];                            // of the rows of this lane's 4
+        float f[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          at[r] = __shfl_sync(0xffffffffu, rec, (lane & ~3) + r);
+          f[r] = __shfl_sync(0xffffffffu, inv, (lane & ~3) + r);
+        }
+        const int row4 = wq * 32 + (lane & ~3);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
@@ -1000,36 +1003,33 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
 #pragma unroll
-          for (int d = 4; d > 0; d >>= 1) {
+          for (int d = 2; d > 0; d >>= 1) {
             const bool hi = lane & d;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < 4; ++u) {
               if (u & d) continue;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? o[4 * u + e] : o[4 * (u | d) + e], d);
-                if (hi) o[4 * u + e] = got;
-                else o[4 * (u | d) + e] = got;
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? o[8 * u + e] : o[8 * (u | d) + e], d);
+                if (hi) o[8 * u + e] = got;
+                else o[8 * (u | d) + e] = got;
               }
             }
           }
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {            // unit r now belongs to row r of these 8 lanes
-            const int from = (lane & ~7) + r;
-            const unsigned at = __shfl_sync(0xffffffffu, rec, from);
-            const float f = __shfl_sync(0xffffffffu, inv, from);
-            if (wq * 32 + from >= rows) continue;
+          for (int r = 0; r < 4; ++r) {            // unit r now belongs to row r of these 4 lanes
+            if (row4 + r >= rows) continue;
+            const uint32_t* x = &o[8 * r];
             if (direct) {
-              const float* x = reinterpret_cast<const float*>(&o[4 * r]);
-              *(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + size_t(at) * HD + 32 * c) + (lane & 7)) =
-                  make_uint2(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f));
+              auto two = [&](int e) { return pack_bf16x2(__uint_as_float(x[e]) * f[r], __uint_as_float(x[e + 1]) * f[r]); };
+              *(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + size_t(at[r]) * HD + 32 * c) + (lane & 3)) =
+                  make_uint4(two(0), two(2), two(4), two(6));
             } else {
-              __stcg(reinterpret_cast<uint4*>(w.recs + size_t(at) * kPrefixRec + 32 * c) + (lane & 7),
-                     make_uint4(o[4 * r], o[4 * r + 1], o[4 * r + 2], o[4 * r + 3]));
+              store32(w.recs + size_t(at[r]) * HD + 32 * c + 8 * (lane & 3), x);
             }
           }
         }
-        if (i < rows && !direct) __stcg(reinterpret_cast<float2*>(w.recs + size_t(rec) * kPrefixRec + HD), make_float2(m, l));
+        if (i < rows && !direct) __stcg(w.rec_ml + rec, make_float2(m, l));
       }
       tc_fence_before();                           // O read before the next piece's first P V overwrites it
     }
@@ -1099,6 +1099,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan has finished
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int4 first_part = make_int4(0, 0, 0, 0);         // the first piece, requested along with the header
+  if (warp == kWarpK && lane < int(sizeof(Piece) / 16) && int(blockIdx.x) < w.piece_cap)
+    first_part = __ldcg(reinterpret_cast<const int4*>(w.pieces + blockIdx.x) + lane);
   int n_pieces = __ldcg(w.header), n_items = __ldcg(w.header + 4);
   const int working = __ldcg(w.header + 6);
   if (uint32_t(__ldcg(w.header + 2)) != w.tag || n_pieces < 0 || n_pieces > w.piece_cap || n_items < 0 ||
@@ -1111,7 +1114,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gsm + kOffTmemSlot);
   const int with_pieces = min(n_pieces, min(int(gridDim.x), working));   // CTAs that take pieces first
   const bool pieces_first = int(blockIdx.x) < with_pieces;
-  const bool ok = !pieces_first || run_pieces(&tm_q, &tm_k, &tm_v, a, w, gsm, base, tmem, n_pieces, with_pieces);
+  const bool ok = !pieces_first || run_pieces(&tm_q, &tm_k, &tm_v, a, w, gsm, base, tmem, n_pieces, with_pieces,
+                                             first_part);
   if (warp == kWarpMma) {
     __syncwarp();
     tmem_dealloc(tmem, kTmemCols);
@@ -1148,8 +1152,7 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const PrefixWork& w
     mx[r] = -INFINITY;
     den[r] = 0.f;
   }
-  const float* pre = w.recs + (size_t(tok) * a.num_heads + h0) * stride * kPrefixRec;
-  const float* own = w.recs + (size_t(unsigned(ti.y)) + size_t(h0) * ti.z) * kPrefixRec;
+  const size_t pre = (size_t(tok) * a.num_heads + h0) * stride, own = size_t(unsigned(ti.y)) + size_t(h0) * ti.z;
   const int rows = min(R, a.num_heads - h0);
   for (int k0 = 0; k0 < n; k0 += K) {
     float4 x[R][K];
@@ -1162,9 +1165,9 @@ __device__ __forceinline__ void join_rows(const AttnArgs& a, const PrefixWork& w
         x[r][k] = make_float4(0.f, 0.f, 0.f, 0.f);
         ml[r][k] = make_float2(-INFINITY, 0.f);
         if (kk < n && r < rows) {
-          const float* p = kk < np ? pre + size_t(r * stride + kk) * kPrefixRec : own + size_t(r * ti.z + kk - np) * kPrefixRec;
-          x[r][k] = __ldcg(reinterpret_cast<const float4*>(p) + lane);
-          ml[r][k] = __ldcg(reinterpret_cast<const float2*>(p + HD));
+          const size_t at = kk < np ? pre + size_t(r * stride + kk) : own + size_t(r * ti.z + kk - np);
+          x[r][k] = __ldcg(reinterpret_cast<const float4*>(w.recs + at * HD) + lane);
+          ml[r][k] = __ldcg(w.rec_ml + at);
         }
       }
 #pragma unroll
@@ -1266,7 +1269,7 @@ size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, 
   const PrefixSizes z = prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len);
   return 256 + align256(z.NG * 16) + 2 * align256(z.S * 16) + align256((z.NG + z.S) * 4) + align256(z.pieces * sizeof(Piece)) +
          align256(z.items * sizeof(SuffixItem)) + align256(z.T * 16) +
-         align256((z.prefix_recs + z.own_recs) * kPrefixRec * sizeof(float));
+         align256((z.prefix_recs + z.own_recs) * kPrefixRecBytes);
 }
 
 static cb_status launch_prefix_tc(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
@@ -1372,7 +1375,8 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   w.pieces = reinterpret_cast<Piece*>(take(z.pieces * sizeof(Piece)));
   w.items = reinterpret_cast<SuffixItem*>(take(z.items * sizeof(SuffixItem)));
   w.token_info = reinterpret_cast<int4*>(take(z.T * 16));
-  w.recs = reinterpret_cast<float*>(take((z.prefix_recs + z.own_recs) * kPrefixRec * sizeof(float)));
+  w.recs = reinterpret_cast<float*>(p);
+  w.rec_ml = reinterpret_cast<float2*>(w.recs + (z.prefix_recs + z.own_recs) * HD);
   static std::atomic<uint32_t> next_tag{1};
   w.tag = next_tag.fetch_add(1);
 

@@ -6,11 +6,11 @@
 
 namespace cb {
 
-// A row's state over a part of its keys, as one record: acc[kPrefixDim] (the sum
-// of 2^(s - m) v over scores s in the exp2 domain), the reference maximum m, the
-// sum of 2^(s - m), padding to 16 bytes.
+// A row's state over a part of its keys is a record: acc[kPrefixDim], the sum of
+// 2^(s - m) v over scores s in the exp2 domain, and apart from it (so that acc
+// fills whole lines) the reference maximum m and the sum of 2^(s - m).
 constexpr int kPrefixDim = 128;
-constexpr int kPrefixRec = kPrefixDim + 4;
+constexpr int kPrefixRecBytes = (kPrefixDim + 2) * 4;
 
 // A piece: the query rows of one row tile or two, of one key/value head, over one
 // KV segment, either of their group's prefix or of their sequence's own keys.
@@ -73,7 +73,8 @@ struct PrefixWork {
   Piece* pieces;
   SuffixItem* items;
   int4* token_info;            // [num_tokens] (prefix records, first own record of head 0, own records per head, -)
-  float* recs;                 // prefix records [token][query head][stride], then the sequences' own ones
+  float* recs;                 // acc of the prefix records [token][query head][stride], then the sequences' own ones
+  float2* rec_ml;              // (m, sum) of the same
 };
 
 constexpr int kStreamWarps = 8;          // warps of a CTA that stream own keys, each with units of its own

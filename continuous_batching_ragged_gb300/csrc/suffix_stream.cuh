@@ -277,11 +277,12 @@ __device__ __noinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap
 #pragma unroll
           for (int j = 0; j < 16; ++j) dst[4 * j] = pack2(o[j][2 * half] * inv, o[j][2 * half + 1] * inv);
         } else {
-          float* rec = w.recs + (size_t(it.rec0) + (size_t(tok) * H + h) * it.rec_step) * kPrefixRec;
+          const size_t at = size_t(it.rec0) + (size_t(tok) * H + h) * it.rec_step;
+          float* rec = w.recs + at * kDim;
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             __stcg(reinterpret_cast<float2*>(rec + 8 * j + 2 * t), make_float2(o[j][2 * half], o[j][2 * half + 1]));
-          if (t == 0) __stcg(reinterpret_cast<float2*>(rec + kDim), make_float2(m, l));
+          if (t == 0) __stcg(w.rec_ml + at, make_float2(m, l));
         }
       }
     }
