@@ -1126,9 +1126,101 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The first units are given to the CTAs that start with them, neighbouring
   // units to different SMs; the rest is claimed.
   const int others = int(gridDim.x) - with_pieces, warps = others * kStreamWarps;
-  stream::run_warp(&tm_k16, &tm_v16, a, w, n_items, base + warp * stream::kStages * stream::kStageBytes, bars,
+  stream::run_warp<false>(&tm_k16, &tm_v16, a, w, n_items, base + warp * stream::kStages * stream::kStageBytes, bars,
                    reinterpret_cast<SuffixItem*>(gsm + kOffOwnSlots) + 2 * warp,
-                   pieces_first ? -1 : warp * others + int(blockIdx.x) - with_pieces, warps, 2 * warps);
+                          pieces_first ? -1 : warp * others + int(blockIdx.x) - with_pieces, warps, 2 * warps,
+                          stream::SmallSeq{});
+}
+
+// Small steps: at most a warp's lanes of sequences, and too few keys for sharing to
+// pay.  The plan of such a step costs a warp less than waiting for another
+// kernel's, so every warp makes its own (4 samples behind 512 keys: 17.4 us with
+// the plan kernel), with the same checks, chunks and records.
+constexpr int kSmallSeqs = 32;
+constexpr int kSmallTokens = 4096;
+constexpr int kSmallThreads = 32 * kStreamWarps;
+constexpr uint32_t kSmallOffBars = stream::kRingBytes, kSmallOffSlots = kSmallOffBars + stream::kBarBytes;
+constexpr uint32_t kSmallSmem = kSmallOffSlots + stream::kSlotBytes + 1024;
+static_assert(kSmallOffSlots % 16 == 0 && kSmallSmem <= 232448, "shared memory");
+
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ int warp_scan(int v, int lane) {   // exclusive
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x - v;
+}
+
+__global__ void __launch_bounds__(kSmallThreads, 1)
+    small_step_kernel(const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
+                      const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* gsm = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool writer = blockIdx.x == 0 && warp == 0;   // of what the join reads, and of the errors
+  const uint32_t bars = base + kSmallOffBars + warp * stream::kStages * 8;
+  const int S = a.num_seqs, T = a.num_tokens, NG = w.num_groups, H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv;
+
+  int s0 = 0x7fffffff, s1 = 0, p = 0, c0 = 0, q_len = 0, n = 0;
+  if (lane < NG) s0 = w.cu_groups[lane], s1 = w.cu_groups[lane + 1], p = w.prefix_lens[lane];
+  if (lane < S) c0 = a.cu_seqlens_q[lane], q_len = a.cu_seqlens_q[lane + 1] - c0, n = w.context_lens[lane];
+  if (lane == 0) {
+    for (int st = 0; st < stream::kStages; ++st) mbar_init(bars + 8 * st, 1);
+    fence_mbar_init();
+    if (warp == 0) {
+      tma_prefetch_desc(&tm_k16);
+      tma_prefetch_desc(&tm_v16);
+    }
+  }
+  if (writer)
+    for (int t = lane; t < T; t += 32) w.token_info[t] = make_int4(0, 0, 0, 0);
+  bool bad = lane < NG && (s0 < 0 || s1 < s0 || s1 > S || (lane == 0 && s0 != 0) || (lane == NG - 1 && s1 != S));
+  bad = __any_sync(0xffffffffu, bad);
+  int g = 0;                                       // the sequence's group: the last that starts at or before it
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (__shfl_sync(0xffffffffu, s0, g + o) <= lane) g += o;
+  p = __shfl_sync(0xffffffffu, p, g);
+  const bool ok = lane < S && p >= 0 && q_len >= 1 && c0 >= 0 && c0 + q_len <= T && q_len <= a.max_q_len && n >= q_len &&
+                  p <= n - q_len && n <= a.max_context_len && int64_t(n) <= int64_t(a.max_blocks_per_seq) * a.block_size;
+  bool wrong = lane < S && !ok;
+  const int tiles = ok ? (n - 1) / stream::kTileKeys + 1 : 0, rt = ok ? (q_len * G + kStreamRows - 1) / kStreamRows : 0;
+  const int64_t per = (warp_sum(int64_t(tiles) * rt * Hkv) + w.stream_units - 1) / w.stream_units;
+  const int L = int(per < kMinChunkTiles ? kMinChunkTiles : (per > (1 << 26) ? (1 << 26) : per));
+  stream::SmallSeq seq;
+  seq.len = L;
+  seq.nch = ok ? (tiles - 1) / L + 1 : 0;
+  seq.tok0 = c0, seq.q_len = q_len, seq.keys = n;
+  const int64_t n_recs = seq.nch > 1 ? int64_t(q_len) * H * seq.nch : 0;
+  bad |= warp_sum(n_recs) > w.own_rec_cap || warp_sum(int64_t(rt) * seq.nch) > w.item_cap;   // only if token ranges overlap
+  const int items = bad ? 0 : rt * seq.nch;
+  seq.item0 = warp_scan(items, lane);
+  seq.rec0 = unsigned(w.prefix_rec_cap) + unsigned(warp_scan(bad ? 0 : int(n_recs), lane));
+  const int n_items = __shfl_sync(0xffffffffu, seq.item0 + items, 31);
+  if (writer) {
+    if (bad || wrong) raise_error(a.err, kErrInvalid);
+    __syncwarp();
+    if (ok && !bad)
+      for (int t = 0; t < q_len; ++t) w.token_info[c0 + t] = make_int4(0, int(seq.rec0 + unsigned(t * H * seq.nch)), seq.nch, 0);
+    if (lane == 0) {
+      w.header[1] = 0;
+      w.header[2] = int32_t(w.tag);
+    }
+  }
+  __syncwarp();
+  const int warps = int(gridDim.x) * kStreamWarps;
+  stream::run_warp<true>(&tm_k16, &tm_v16, a, w, n_items, base + warp * stream::kStages * stream::kStageBytes, bars,
+                         reinterpret_cast<SuffixItem*>(gsm + kSmallOffSlots) + 2 * warp, warp * int(gridDim.x) + int(blockIdx.x),
+                         warps, 0, seq);
 }
 
 // A warp joins kJoinRows query heads of a token at a time and goes on to the next
@@ -1272,58 +1364,74 @@ size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, 
          align256((z.prefix_recs + z.own_recs) * kPrefixRecBytes);
 }
 
-static cb_status launch_prefix_tc(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
-  EncodeTiledFn enc = encode_tiled_fn();
-  if (!enc) return CB_ERR_CUDA;
-  const int G = a.num_heads / a.num_kv_heads, B = a.block_size;
-  CUtensorMap tq, tk, tv;
-  const cuuint32_t ones[3] = {1, 1, 1};
-  {
-    // q as [tokens][heads][128]: a box is one key/value head's query heads of tile_tokens tokens, one 64-dim half
-    const cuuint64_t dims[3] = {cuuint64_t(HD), cuuint64_t(a.num_heads), cuuint64_t(a.num_tokens)};
-    const cuuint64_t strides[2] = {cuuint64_t(HD) * 2, cuuint64_t(a.num_heads) * HD * 2};
-    const cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(w.tile_tokens)};
-    CUresult r = enc(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, ones,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(CB_ERR_CUDA, "shared prefixes: encoding the Q tensor map failed (%d)", int(r));
+// The tensor maps of the K and V pools, boxes of one block and head.
+static cb_status encode_pools(const AttnArgs& a, EncodeTiledFn enc, bool tiles16, CUtensorMap* tk, CUtensorMap* tv) {
+  const cuuint64_t B = cuuint64_t(a.block_size), boxes = cuuint64_t(a.num_blocks) * a.num_kv_heads;
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  CUresult r = CUDA_SUCCESS;
+  for (int v = 0; v < 2 && r == CUDA_SUCCESS; ++v) {
+    void* pool = const_cast<void*>(v ? a.v_pool : a.k_pool);
+    CUtensorMap* tm = v ? tv : tk;
+    if (tiles16) {                                 // both 64-dim halves of 16 rows at a time, for the streams
+      const cuuint64_t dims[4] = {64, B, 2, boxes}, strides[3] = {HD * 2, 128, B * HD * 2};
+      const cuuint32_t box[4] = {64, cuuint32_t(stream::kTileKeys), 2, 1};
+      r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    } else {                                       // a block's 64-dim half, for the pieces
+      const cuuint64_t dims[3] = {cuuint64_t(HD), B, boxes}, strides[2] = {HD * 2, B * HD * 2};
+      const cuuint32_t box[3] = {64, cuuint32_t(B), 1};
+      r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
   }
-  const cuuint64_t dims[3] = {cuuint64_t(HD), cuuint64_t(B), cuuint64_t(a.num_blocks) * a.num_kv_heads};
-  const cuuint64_t strides[2] = {cuuint64_t(HD) * 2, cuuint64_t(B) * HD * 2};
-  // the pieces load blocks in 64-dim halves, the streams both halves of 16 rows at a time
-  auto encode_kv = [&](CUtensorMap* tm, const void* pool) -> CUresult {
-    const cuuint32_t box[3] = {64, cuuint32_t(B), 1};
-    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, ones,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  };
-  auto encode_kv16 = [&](CUtensorMap* tm, const void* pool) -> CUresult {
-    const cuuint64_t dims4[4] = {64, cuuint64_t(B), 2, dims[2]};
-    const cuuint64_t strides4[3] = {cuuint64_t(HD) * 2, 128, strides[1]};
-    const cuuint32_t box[4] = {64, cuuint32_t(stream::kTileKeys), 2, 1}, ones4[4] = {1, 1, 1, 1};
-    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool), dims4, strides4, box, ones4,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  };
-  CUtensorMap tk16, tv16;
-  CUresult r = encode_kv(&tk, a.k_pool);
-  if (r == CUDA_SUCCESS) r = encode_kv(&tv, a.v_pool);
-  if (r == CUDA_SUCCESS) r = encode_kv16(&tk16, a.k_pool);
-  if (r == CUDA_SUCCESS) r = encode_kv16(&tv16, a.v_pool);
-  if (r != CUDA_SUCCESS) return fail(CB_ERR_CUDA, "shared prefixes: encoding the KV tensor maps failed (%d)", int(r));
+  return r == CUDA_SUCCESS ? CB_OK : fail(CB_ERR_CUDA, "shared prefixes: encoding the KV tensor maps failed (%d)", int(r));
+}
+
+// Lets the kernels take their dynamic shared memory on the current device.
+static cb_status allow_shared_memory() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
     return fail(CB_ERR_UNSUPPORTED, "shared prefixes: no usable current device");
-  {
-    std::lock_guard<std::mutex> lock(g_attr_mutex);
-    if (!g_attr_set[dev]) {
-      cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes));
-      if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: shared memory attribute");
-      g_attr_set[dev] = true;
-    }
-  }
+  std::lock_guard<std::mutex> lock(g_attr_mutex);
+  if (g_attr_set[dev]) return CB_OK;
+  cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(small_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallSmem));
+  if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: shared memory attribute");
+  g_attr_set[dev] = true;
+  return CB_OK;
+}
+
+static cb_status launch_prefix_tc(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return CB_ERR_CUDA;
+  const int G = a.num_heads / a.num_kv_heads;
+  CUtensorMap tq, tk, tv, tk16, tv16;
+  // q as [tokens][heads][128]: a box is one key/value head's query heads of tile_tokens tokens, one 64-dim half
+  const cuuint64_t dims[3] = {cuuint64_t(HD), cuuint64_t(a.num_heads), cuuint64_t(a.num_tokens)};
+  const cuuint64_t strides[2] = {cuuint64_t(HD) * 2, cuuint64_t(a.num_heads) * HD * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(w.tile_tokens)}, ones[3] = {1, 1, 1};
+  CUresult r = enc(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, ones,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(CB_ERR_CUDA, "shared prefixes: encoding the Q tensor map failed (%d)", int(r));
+  cb_status st = encode_pools(a, enc, false, &tk, &tv);
+  if (st == CB_OK) st = encode_pools(a, enc, true, &tk16, &tv16);
+  if (st == CB_OK) st = allow_shared_memory();
+  if (st != CB_OK) return st;
   cudaError_t e = launch_kernel(prefix_tc_kernel, dim3(unsigned(w.num_sms)), dim3(kThreads), kSmemBytes, stream, true, tq, tk,
                                 tv, tk16, tv16, a, w);
+  return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: launch");
+}
+
+static cb_status launch_small_step(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return CB_ERR_CUDA;
+  CUtensorMap tk16, tv16;
+  cb_status st = encode_pools(a, enc, true, &tk16, &tv16);
+  if (st == CB_OK) st = allow_shared_memory();
+  if (st != CB_OK) return st;
+  cudaError_t e = launch_kernel(small_step_kernel, dim3(unsigned(w.num_sms)), dim3(kSmallThreads), kSmallSmem, stream, false,
+                                tk16, tv16, a, w);
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: launch");
 }
 
@@ -1337,8 +1445,8 @@ static cb_status launch_join(const AttnArgs& a, const PrefixWork& w, cudaStream_
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: join launch");
 }
 
-// A step with shared prefixes on one stream: the plan, the pieces and streams, and
-// the join, each a programmatic dependent of the one before.
+// A step with shared prefixes on one stream: the plan, the pieces and streams (a small
+// step's streams alone), and the join, each a programmatic dependent of the one before.
 cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
                             void* workspace, cudaStream_t stream) {
   NvtxRange nvtx("cb.shared_prefix");
@@ -1380,10 +1488,20 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   static std::atomic<uint32_t> next_tag{1};
   w.tag = next_tag.fetch_add(1);
 
-  prefix_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, w);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: plan launch");
-  cb_status st = launch_prefix_tc(a, w, stream);
+  // the keys that sharing could save at most do not pay for it, and no sequence's own keys are pieces
+  const double saved = double(a.num_seqs - 1) * a.max_context_len * a.num_kv_heads * (4.0 * HD);
+  const bool small = a.num_seqs <= kSmallSeqs && num_groups <= kSmallSeqs && a.num_tokens <= kSmallTokens &&
+                     (a.max_q_len == 1 || int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= kMaxStreamRows) &&
+                     saved < double(kShareUs) * kBytesPerUs;
+  cb_status st;
+  if (small) {
+    st = launch_small_step(a, w, stream);
+  } else {
+    prefix_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, w);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: plan launch");
+    st = launch_prefix_tc(a, w, stream);
+  }
   if (st != CB_OK) return st;
   return launch_join(a, w, stream);
 }

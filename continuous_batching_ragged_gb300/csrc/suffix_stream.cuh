@@ -78,13 +78,24 @@ struct Unit {
   int zt, z;                    // lane i: TMA box index of tile zt + i
 };
 
+// A sequence of a small step, one per lane: every warp works the whole plan of such
+// a step out for itself.
+struct SmallSeq {
+  int item0, nch;               // its first item, chunks
+  int tok0, q_len, keys;
+  int len;                      // tiles of a chunk
+  unsigned rec0;
+};
+
 // One warp (0 .. kStreamWarps - 1 of its CTA).  `ring`, `bars` (initialised) and
 // `slots` are the warp's own.  `first`: its first two units, `first` and
 // first + step, are given rather than claimed; -1: claimed like the later ones,
-// which start at `claimed_from`.
+// which start at `claimed_from`.  kSmall: the items are those of `seq`, and all
+// units are given, `step` apart.
+template <bool kSmall>
 __device__ __noinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttnArgs& a,
                                          const PrefixWork& w, int n_items, uint32_t ring, uint32_t bars,
-                                         SuffixItem* slots, int first, int step, int claimed_from) {
+                                         SuffixItem* slots, int first, int step, int claimed_from, const SmallSeq seq) {
   const int lane = threadIdx.x & 31;
   const int H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv, B = a.block_size;
   const int n_units = n_items * Hkv;
@@ -105,8 +116,24 @@ __device__ __noinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap
     u.n = u.hk = u.issued = u.zt = u.z = 0;
     if (idx >= n_units) return;
     __syncwarp();                                        // every lane is done with the slot's last item
-    if (lane < int(sizeof(SuffixItem) / 16))
+    if (kSmall) {
+      const int item = idx / Hkv;
+      int s = 0;                                         // the last sequence that starts at or before it
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (__shfl_sync(0xffffffffu, seq.item0, s + o) <= item) s += o;
+      if (lane == s) {
+        const int local = item - seq.item0, row = local / seq.nch, chunk = local - row * seq.nch;
+        SuffixItem x = {};
+        x.s = s, x.tok0 = seq.tok0, x.q_len = seq.q_len, x.row0 = 16 * row, x.ctx = seq.keys;
+        x.k0 = chunk * seq.len * kTileKeys;
+        x.k1 = x.k0 + min(seq.keys - x.k0, seq.len * kTileKeys);
+        x.rec0 = seq.rec0 + chunk, x.rec_step = seq.nch, x.direct = seq.nch == 1;
+        it = x;
+      }
+    } else if (lane < int(sizeof(SuffixItem) / 16)) {
       reinterpret_cast<int4*>(&it)[lane] = __ldcg(reinterpret_cast<const int4*>(w.items + idx / Hkv) + lane);
+    }
     __syncwarp();
     u.hk = idx % Hkv;
     u.n = (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys;
@@ -132,6 +159,7 @@ __device__ __noinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap
 
   Unit cur, nxt;
   int slot = 0;                                          // of the current unit; the next one's is the other
+  int given = first + step;                              // kSmall: the last unit taken
   {
     int c0 = first, c1 = first + step;
     if (first < 0) {
@@ -157,7 +185,9 @@ __device__ __noinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap
       }
     };
     top_up();
-    const int ahead = nxt.n > 0 ? claim() : n_units;     // for the unit after the next; read at this one's end
+    int ahead = n_units;
+    if (kSmall) ahead = given = min(given, n_units) + step;
+    else if (nxt.n > 0) ahead = claim();                 // for the unit after the next; read at this one's end
     // the unit's query rows, as A fragments; rows past the sequence's are zero
     const int rows = min(16, it.q_len * G - it.row0);
     uint32_t qf[8][4];

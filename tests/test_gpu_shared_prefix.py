@@ -337,3 +337,73 @@ def test_two_calls_at_once(native_lib):
     for st, stream in zip(steps, streams):
         api.cb_check_device_errors(stream)
         st.check()
+
+
+@pytest.mark.parametrize("fault", ["prefix too long", "negative prefix", "gap", "overlap", "not all", "start", "page", "context",
+                                   "no query", "tokens"])
+def test_bad_metadata_of_a_small_step(native_lib, fault):
+    """The same of steps that every warp plans for itself."""
+    from continuous_batching_ragged_gb300 import api, native
+    st = Step([(300, [(5, 1)] * 4), (200, [(8, 1)] * 3), (50, [(40, 1)] * 2)], 8, 2, 16, seed=9, ballast=False)
+    good, error, n = [0, 1, 2, 3, 4, 6, 7, 8], "INVALID", 9
+    if fault == "prefix too long":
+        st.ctx[5] = 200
+    elif fault == "negative prefix":
+        st.prefix[1], good = -3, [0, 1, 2, 3, 7, 8]
+    elif fault == "gap":
+        st.cu_groups[1], good = n + 1, []
+    elif fault == "overlap":
+        st.cu_groups[2], good = 3, []
+    elif fault == "not all":
+        st.cu_groups[3], good = n - 1, []
+    elif fault == "start":
+        st.cu_groups[0], good = 1, []
+    elif fault == "page":
+        st.tables[5, 4], error = st.cache.num_blocks, "BOUNDS"
+    elif fault == "context":
+        st.ctx[5] = st.max_ctx + 1
+    elif fault == "no query":
+        st.cu[6], good = 5, [0, 1, 2, 3, 4, 7, 8]      # sequence 5 has no row, sequence 6 two: more than max_q_len
+    elif fault == "tokens":
+        st.cu[9], good = 10, range(8)
+    st.run()
+    with pytest.raises(native.CBError, match=error):
+        api.cb_check_device_errors()
+    st.check(good)
+    if not good:
+        assert bool(st.out.isnan().all())
+    elif error == "INVALID" and fault not in ("no query", "tokens"):
+        for s in set(range(9)) - set(good):
+            assert bool(st.out[s].isnan().all())
+
+
+@pytest.mark.parametrize("S", [1, 31, 32, 33])
+@pytest.mark.parametrize("H,K,q", [(8, 2, 1), (8, 8, 3), (128, 1, 1), (100, 1, 1)])
+def test_few_sequences(native_lib, S, H, K, q):
+    """Steps on both sides of what a warp's lanes hold, in groups of three, with rows behind the last sequence."""
+    from continuous_batching_ragged_gb300 import api
+    groups = [(40 * i % 300, [(q + 37 * j % 200, q if j % 2 else 1) for j in range(i, min(i + 3, S))]) for i in range(0, S, 3)]
+    st = Step(groups, H, K, 16, seed=S, ballast=False)
+    rows = len(st.q)
+    more = torch.full((7, H, A), float("nan"), dtype=torch.bfloat16, device="cuda")
+    st.q, st.out = torch.cat([st.q, more]), torch.cat([st.out, more])
+    n = api.cb_shared_prefix_workspace_size(st.cache, H, S, rows + 7, len(groups), st.max_ctx)
+    st.ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    st.run()
+    api.cb_check_device_errors()
+    st.check()
+    assert bool(st.out[rows:].isnan().all())
+    first = st.out[:rows].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st.run()
+    for _ in range(2):
+        st.out.fill_(float("nan"))
+        graph.replay()
+    api.cb_check_device_errors()
+    assert torch.equal(first, st.out[:rows])
+
+
+def test_one_long_sequence(native_lib):
+    """More units than warps, for one row."""
+    run_checked([(100, [(70_000, 1)])], 16, 16, 16, seed=14, ballast=False)
