@@ -112,6 +112,7 @@ constexpr float kBytesPerUs = 6.7e6f;    // HBM
 constexpr float kStreamBytesPerUsPerSm = 4.2e4f;   // streams of one SM
 constexpr float kJoinBytesPerUs = 4.0e6f;
 constexpr float kShareUs = 6.0f;          // what a step's pieces and join take at least
+constexpr float kSmallUs = 16.0f;         // the same with the plan, for steps that can do without
 constexpr int kWaveSteps = 16;           // SM splits that are scored: those that the pieces fill in 1 .. 16 waves
 static_assert(kSegChoices * kWaveSteps == kPlanThreads, "a thread scores one choice");
 
@@ -1129,33 +1130,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   stream::run_warp<false>(&tm_k16, &tm_v16, a, w, n_items, base + warp * stream::kStages * stream::kStageBytes, bars,
                    reinterpret_cast<SuffixItem*>(gsm + kOffOwnSlots) + 2 * warp,
                           pieces_first ? -1 : warp * others + int(blockIdx.x) - with_pieces, warps, 2 * warps,
-                          stream::SmallSeq{});
+                          stream::SmallStep{});
 }
 
-// Small steps: at most a warp's lanes of sequences, and too few keys for sharing to
-// pay.  The plan of such a step costs a warp less than waiting for another
-// kernel's, so every warp makes its own (4 samples behind 512 keys: 17.4 us with
-// the plan kernel), with the same checks, chunks and records.
-constexpr int kSmallSeqs = 32;
-constexpr int kSmallTokens = 4096;
+// Small steps: too few keys for sharing to pay, and a thread of a CTA for each
+// sequence.  The plan of such a step costs a CTA less than waiting for another
+// kernel's, so every CTA makes its own, with the same checks, chunks and records
+// (4 samples behind 512 keys 10.1 us, with the plan kernel 17.4).  That also holds
+// where sharing would save some bytes: 32 sequences behind 512 keys, 70 MB in all,
+// 16.2 us and 24.6 with sharing; 6 behind 4096, 101 MB, 26.3 and 27.5.
 constexpr int kSmallThreads = 32 * kStreamWarps;
+constexpr int kSmallSeqs = kSmallThreads;
+constexpr int kSmallTokens = 4096;
 constexpr uint32_t kSmallOffBars = stream::kRingBytes, kSmallOffSlots = kSmallOffBars + stream::kBarBytes;
 constexpr uint32_t kSmallSmem = kSmallOffSlots + stream::kSlotBytes + 1024;
-static_assert(kSmallOffSlots % 16 == 0 && kSmallSmem <= 232448, "shared memory");
+static_assert(kSmallOffSlots % 16 == 0 && kSmallSmem <= 220 * 1024, "shared memory");
 
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
-}
-__device__ __forceinline__ int warp_scan(int v, int lane) {   // exclusive
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  return x - v;
 }
 
 __global__ void __launch_bounds__(kSmallThreads, 1)
@@ -1163,16 +1157,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
                       const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
+  __shared__ stream::SmallSeq seqs[kSmallSeqs];
+  __shared__ int group_s0[kSmallSeqs], group_p[kSmallSeqs];
+  __shared__ int64_t sums[3][kStreamWarps];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* gsm = smem_raw + (base - raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool writer = blockIdx.x == 0 && warp == 0;   // of what the join reads, and of the errors
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool writer = blockIdx.x == 0;             // of what the join reads, and of the errors
   const uint32_t bars = base + kSmallOffBars + warp * stream::kStages * 8;
   const int S = a.num_seqs, T = a.num_tokens, NG = w.num_groups, H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv;
 
-  int s0 = 0x7fffffff, s1 = 0, p = 0, c0 = 0, q_len = 0, n = 0;
-  if (lane < NG) s0 = w.cu_groups[lane], s1 = w.cu_groups[lane + 1], p = w.prefix_lens[lane];
-  if (lane < S) c0 = a.cu_seqlens_q[lane], q_len = a.cu_seqlens_q[lane + 1] - c0, n = w.context_lens[lane];
+  int s0 = 0, s1 = 0, p = 0, c0 = 0, q_len = 0, n = 0;
+  if (tid < NG) s0 = w.cu_groups[tid], s1 = w.cu_groups[tid + 1], p = w.prefix_lens[tid];
+  if (tid < S) c0 = a.cu_seqlens_q[tid], q_len = a.cu_seqlens_q[tid + 1] - c0, n = w.context_lens[tid];
   if (lane == 0) {
     for (int st = 0; st < stream::kStages; ++st) mbar_init(bars + 8 * st, 1);
     fence_mbar_init();
@@ -1182,45 +1179,62 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     }
   }
   if (writer)
-    for (int t = lane; t < T; t += 32) w.token_info[t] = make_int4(0, 0, 0, 0);
-  bool bad = lane < NG && (s0 < 0 || s1 < s0 || s1 > S || (lane == 0 && s0 != 0) || (lane == NG - 1 && s1 != S));
-  bad = __any_sync(0xffffffffu, bad);
+    for (int t = tid; t < T; t += kSmallThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
+  group_s0[tid] = s0;
+  group_p[tid] = p;
+  int bad = tid < NG && (s0 < 0 || s1 < s0 || s1 > S || (tid == 0 && s0 != 0) || (tid == NG - 1 && s1 != S));
+  bad = __syncthreads_or(bad);
   int g = 0;                                       // the sequence's group: the last that starts at or before it
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    if (__shfl_sync(0xffffffffu, s0, g + o) <= lane) g += o;
-  p = __shfl_sync(0xffffffffu, p, g);
-  const bool ok = lane < S && p >= 0 && q_len >= 1 && c0 >= 0 && c0 + q_len <= T && q_len <= a.max_q_len && n >= q_len &&
+  for (int hi = NG - 1; g < hi;) {
+    const int mid = (g + hi + 1) >> 1;
+    if (group_s0[mid] <= tid) g = mid; else hi = mid - 1;
+  }
+  p = group_p[g];
+  const bool ok = tid < S && p >= 0 && q_len >= 1 && c0 >= 0 && c0 + q_len <= T && q_len <= a.max_q_len && n >= q_len &&
                   p <= n - q_len && n <= a.max_context_len && int64_t(n) <= int64_t(a.max_blocks_per_seq) * a.block_size;
-  bool wrong = lane < S && !ok;
   const int tiles = ok ? (n - 1) / stream::kTileKeys + 1 : 0, rt = ok ? (q_len * G + kStreamRows - 1) / kStreamRows : 0;
-  const int64_t per = (warp_sum(int64_t(tiles) * rt * Hkv) + w.stream_units - 1) / w.stream_units;
+  const int64_t mine = warp_sum(int64_t(tiles) * rt * Hkv);
+  if (lane == 0) sums[0][warp] = mine;
+  __syncthreads();
+  int64_t per = w.stream_units - 1;
+#pragma unroll
+  for (int i = 0; i < kStreamWarps; ++i) per += sums[0][i];
+  per /= w.stream_units;
   const int L = int(per < kMinChunkTiles ? kMinChunkTiles : (per > (1 << 26) ? (1 << 26) : per));
-  stream::SmallSeq seq;
-  seq.len = L;
-  seq.nch = ok ? (tiles - 1) / L + 1 : 0;
-  seq.tok0 = c0, seq.q_len = q_len, seq.keys = n;
-  const int64_t n_recs = seq.nch > 1 ? int64_t(q_len) * H * seq.nch : 0;
-  bad |= warp_sum(n_recs) > w.own_rec_cap || warp_sum(int64_t(rt) * seq.nch) > w.item_cap;   // only if token ranges overlap
-  const int items = bad ? 0 : rt * seq.nch;
-  seq.item0 = warp_scan(items, lane);
-  seq.rec0 = unsigned(w.prefix_rec_cap) + unsigned(warp_scan(bad ? 0 : int(n_recs), lane));
-  const int n_items = __shfl_sync(0xffffffffu, seq.item0 + items, 31);
+  const int nch = ok ? (tiles - 1) / L + 1 : 0;
+  const int64_t items = int64_t(rt) * nch, recs = nch > 1 ? int64_t(q_len) * H * nch : 0;
+  int64_t item0 = items, rec0 = recs;              // exclusive scans over the CTA
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, item0, o), y = __shfl_up_sync(0xffffffffu, rec0, o);
+    if (lane >= o) item0 += x, rec0 += y;
+  }
+  if (lane == 31) sums[1][warp] = item0, sums[2][warp] = rec0;
+  __syncthreads();
+  item0 -= items, rec0 -= recs;
+  int64_t all_items = 0, all_recs = 0;
+#pragma unroll
+  for (int i = 0; i < kStreamWarps; ++i) {
+    if (i < warp) item0 += sums[1][i], rec0 += sums[2][i];
+    all_items += sums[1][i], all_recs += sums[2][i];
+  }
+  bad |= all_items > w.item_cap || all_recs > w.own_rec_cap;   // only if token ranges overlap
+  seqs[tid] = stream::SmallSeq{int(item0), nch, c0, q_len, n, unsigned(w.prefix_rec_cap + rec0)};
   if (writer) {
-    if (bad || wrong) raise_error(a.err, kErrInvalid);
-    __syncwarp();
+    if (bad || (tid < S && !ok)) raise_error(a.err, kErrInvalid);
     if (ok && !bad)
-      for (int t = 0; t < q_len; ++t) w.token_info[c0 + t] = make_int4(0, int(seq.rec0 + unsigned(t * H * seq.nch)), seq.nch, 0);
-    if (lane == 0) {
+      for (int t = 0; t < q_len; ++t)
+        w.token_info[c0 + t] = make_int4(0, int(unsigned(w.prefix_rec_cap + rec0 + int64_t(t) * H * nch)), nch, 0);
+    if (tid == 0) {
       w.header[1] = 0;
       w.header[2] = int32_t(w.tag);
     }
   }
-  __syncwarp();
+  __syncthreads();
   const int warps = int(gridDim.x) * kStreamWarps;
-  stream::run_warp<true>(&tm_k16, &tm_v16, a, w, n_items, base + warp * stream::kStages * stream::kStageBytes, bars,
-                         reinterpret_cast<SuffixItem*>(gsm + kSmallOffSlots) + 2 * warp, warp * int(gridDim.x) + int(blockIdx.x),
-                         warps, 0, seq);
+  stream::run_warp<true>(&tm_k16, &tm_v16, a, w, bad ? 0 : int(all_items), base + warp * stream::kStages * stream::kStageBytes,
+                         bars, reinterpret_cast<SuffixItem*>(gsm + kSmallOffSlots) + 2 * warp,
+                         warp * int(gridDim.x) + int(blockIdx.x), warps, 0, stream::SmallStep{seqs, S, L});
 }
 
 // A warp joins kJoinRows query heads of a token at a time and goes on to the next
@@ -1488,11 +1502,11 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   static std::atomic<uint32_t> next_tag{1};
   w.tag = next_tag.fetch_add(1);
 
-  // the keys that sharing could save at most do not pay for it, and no sequence's own keys are pieces
+  // what sharing could save at most does not pay for it, and no sequence's own keys are pieces
   const double saved = double(a.num_seqs - 1) * a.max_context_len * a.num_kv_heads * (4.0 * HD);
   const bool small = a.num_seqs <= kSmallSeqs && num_groups <= kSmallSeqs && a.num_tokens <= kSmallTokens &&
                      (a.max_q_len == 1 || int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= kMaxStreamRows) &&
-                     saved < double(kShareUs) * kBytesPerUs;
+                     saved < double(kSmallUs) * kBytesPerUs;
   cb_status st;
   if (small) {
     st = launch_small_step(a, w, stream);

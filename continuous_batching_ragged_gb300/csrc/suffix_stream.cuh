@@ -78,24 +78,28 @@ struct Unit {
   int zt, z;                    // lane i: TMA box index of tile zt + i
 };
 
-// A sequence of a small step, one per lane: every warp works the whole plan of such
-// a step out for itself.
+// A sequence of a small step, in shared memory: every CTA works the whole plan of
+// such a step out for itself.
 struct SmallSeq {
   int item0, nch;               // its first item, chunks
   int tok0, q_len, keys;
-  int len;                      // tiles of a chunk
   unsigned rec0;
+};
+struct SmallStep {
+  const SmallSeq* seqs;
+  int num_seqs;
+  int len;                      // tiles of a chunk
 };
 
 // One warp (0 .. kStreamWarps - 1 of its CTA).  `ring`, `bars` (initialised) and
 // `slots` are the warp's own.  `first`: its first two units, `first` and
 // first + step, are given rather than claimed; -1: claimed like the later ones,
-// which start at `claimed_from`.  kSmall: the items are those of `seq`, and all
+// which start at `claimed_from`.  kSmall: the items are those of `small`, and all
 // units are given, `step` apart.
 template <bool kSmall>
 __device__ __noinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttnArgs& a,
                                          const PrefixWork& w, int n_items, uint32_t ring, uint32_t bars,
-                                         SuffixItem* slots, int first, int step, int claimed_from, const SmallSeq seq) {
+                                         SuffixItem* slots, int first, int step, int claimed_from, const SmallStep small) {
   const int lane = threadIdx.x & 31;
   const int H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv, B = a.block_size;
   const int n_units = n_items * Hkv;
@@ -119,16 +123,18 @@ __device__ __noinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap
     if (kSmall) {
       const int item = idx / Hkv;
       int s = 0;                                         // the last sequence that starts at or before it
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        if (__shfl_sync(0xffffffffu, seq.item0, s + o) <= item) s += o;
-      if (lane == s) {
-        const int local = item - seq.item0, row = local / seq.nch, chunk = local - row * seq.nch;
+      for (int hi = small.num_seqs - 1; s < hi;) {
+        const int mid = (s + hi + 1) >> 1;
+        if (small.seqs[mid].item0 <= item) s = mid; else hi = mid - 1;
+      }
+      if (lane == 0) {
+        const SmallSeq q = small.seqs[s];
+        const int local = item - q.item0, row = local / q.nch, chunk = local - row * q.nch;
         SuffixItem x = {};
-        x.s = s, x.tok0 = seq.tok0, x.q_len = seq.q_len, x.row0 = 16 * row, x.ctx = seq.keys;
-        x.k0 = chunk * seq.len * kTileKeys;
-        x.k1 = x.k0 + min(seq.keys - x.k0, seq.len * kTileKeys);
-        x.rec0 = seq.rec0 + chunk, x.rec_step = seq.nch, x.direct = seq.nch == 1;
+        x.s = s, x.tok0 = q.tok0, x.q_len = q.q_len, x.row0 = 16 * row, x.ctx = q.keys;
+        x.k0 = chunk * small.len * kTileKeys;
+        x.k1 = x.k0 + min(q.keys - x.k0, small.len * kTileKeys);
+        x.rec0 = q.rec0 + chunk, x.rec_step = q.nch, x.direct = q.nch == 1;
         it = x;
       }
     } else if (lane < int(sizeof(SuffixItem) / 16)) {

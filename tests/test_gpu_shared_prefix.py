@@ -24,10 +24,10 @@ class Step:
     def __init__(self, groups, H, K, B, seed=0, q_scale=1.0, k_slope=0.0, extra_blocks=3, num_blocks=None, width=None,
                  ballast=True):
         from continuous_batching_ragged_gb300 import api
-        # a step shares only where that saves some 40 MB: one more group that does, whatever the others are
+        # a step shares only where that saves some 100 MB: one more group that does, whatever the others are
         self.real = sum(len(members) for _, members in groups)
         if ballast:
-            groups = list(groups) + [(2048, [(1, 1)] * (2 + 48_000_000 // (2048 * 4 * A * K)))]
+            groups = list(groups) + [(2048, [(1, 1)] * (2 + 115_000_000 // (2048 * 4 * A * K)))]
         g = torch.Generator(device="cuda").manual_seed(seed)
         pick = torch.Generator().manual_seed(seed)
         self.H, self.K, self.B, self.groups = H, K, B, groups
@@ -342,7 +342,7 @@ def test_two_calls_at_once(native_lib):
 @pytest.mark.parametrize("fault", ["prefix too long", "negative prefix", "gap", "overlap", "not all", "start", "page", "context",
                                    "no query", "tokens"])
 def test_bad_metadata_of_a_small_step(native_lib, fault):
-    """The same of steps that every warp plans for itself."""
+    """The same of steps that every CTA plans for itself."""
     from continuous_batching_ragged_gb300 import api, native
     st = Step([(300, [(5, 1)] * 4), (200, [(8, 1)] * 3), (50, [(40, 1)] * 2)], 8, 2, 16, seed=9, ballast=False)
     good, error, n = [0, 1, 2, 3, 4, 6, 7, 8], "INVALID", 9
@@ -377,10 +377,10 @@ def test_bad_metadata_of_a_small_step(native_lib, fault):
             assert bool(st.out[s].isnan().all())
 
 
-@pytest.mark.parametrize("S", [1, 31, 32, 33])
+@pytest.mark.parametrize("S", [1, 32, 33, 255, 256, 257])
 @pytest.mark.parametrize("H,K,q", [(8, 2, 1), (8, 8, 3), (128, 1, 1), (100, 1, 1)])
 def test_few_sequences(native_lib, S, H, K, q):
-    """Steps on both sides of what a warp's lanes hold, in groups of three, with rows behind the last sequence."""
+    """Steps on both sides of what a CTA's threads plan, in groups of three, with rows behind the last sequence."""
     from continuous_batching_ragged_gb300 import api
     groups = [(40 * i % 300, [(q + 37 * j % 200, q if j % 2 else 1) for j in range(i, min(i + 3, S))]) for i in range(0, S, 3)]
     st = Step(groups, H, K, 16, seed=S, ballast=False)

@@ -121,9 +121,10 @@ class Loop:
         return int(live)
 
 
-def test_samples_of_two_prompts(native_lib):
-    long, short, samples = 1500, 37, 12                # 11 * 1488 keys of 8 heads saved: 67 MB, enough to share
-    loop = Loop(num_blocks=700, max_rows=32, width=110, seed=1)
+@pytest.mark.parametrize("long", [300, 2600])          # of 8 heads: shared reads would save 15 MB, and do save 117 MB
+def test_samples_of_two_prompts(native_lib, long):
+    short, samples = 37, 12
+    loop = Loop(num_blocks=700, max_rows=32, width=180, seed=1)
     loop.step([0, 20], [long, short], None, None)                       # both prompts
     loop.fork(0, list(range(1, samples)))
     loop.fork(20, [21, 22])
