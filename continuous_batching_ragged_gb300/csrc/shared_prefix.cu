@@ -151,33 +151,45 @@ __device__ __noinline__ int last_at_or_before(const int* p, int stride, int n, i
   return lo;
 }
 
-// Exclusive block-wide scan; `total` receives the sum.  Contains __syncthreads.
-__device__ __noinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The plan's last lists, the streamed items and the pieces, are made side by side,
+// by half of the threads each.
+constexpr int kHalfThreads = kPlanThreads / 2;
+__device__ __forceinline__ void half_sync(int half) { asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(kHalfThreads) : "memory"); }
+
+// Exclusive scan over a half's threads; `total` receives the sum.  Contains half_sync.
+__device__ __noinline__ int64_t half_scan(int64_t v, int64_t* warp_sums, int half, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = half * (kHalfThreads / 32);
   int64_t x = v;
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
+  half_sync(half);
   int64_t before = 0, all = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
+  for (int w = first; w < first + kHalfThreads / 32; ++w) {
     if (w < warp) before += warp_sums[w];
     all += warp_sums[w];
   }
   *total = all;
-  __syncthreads();
+  half_sync(half);
   return before + x - v;
 }
 
-// *sum += the warp's v (0 <= v < 2^60), 20 bits at a time through the warp's reduction; one atomic a warp.
-__device__ __noinline__ void add_warp_sum(unsigned long long* sum, int64_t v) {
+// Sums over the CTA without shared atomics, which are slow in 64 bits: every
+// warp's part (0 <= v < 2^60), 20 bits at a time through the warp's reduction, ...
+__device__ __noinline__ void put_warp_sum(int64_t* parts, int64_t v) {
   const unsigned lo = __reduce_add_sync(0xffffffffu, unsigned(v & 0xfffff));
   const unsigned mid = __reduce_add_sync(0xffffffffu, unsigned((v >> 20) & 0xfffff));
   const unsigned hi = __reduce_add_sync(0xffffffffu, unsigned((v >> 40) & 0xfffff));
-  if ((threadIdx.x & 31) == 0 && (lo | mid | hi))
-    atomicAdd(sum, lo + ((unsigned long long)mid << 20) + ((unsigned long long)hi << 40));
+  if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = int64_t(lo) + (int64_t(mid) << 20) + (int64_t(hi) << 40);
+}
+// ... and, after a __syncthreads, their sum.
+__device__ __noinline__ int64_t sum_parts(const int64_t* parts) {
+  int64_t x = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) x += parts[w];
+  return x;
 }
 
 __device__ __forceinline__ int sms_of(int pieces, int waves, int num_sms) { return min(num_sms, (pieces + waves - 1) / waves); }
@@ -214,7 +226,8 @@ __device__ __noinline__ Job get_job(const PlanView v, int j) {
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArgs a, const PrefixWork w) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // they wait for this grid on the device
   __shared__ int64_t warp_sums[kPlanThreads / 32];
-  __shared__ unsigned long long sums[4], s_best;
+  __shared__ int64_t sums[4][kPlanThreads / 32];
+  __shared__ unsigned long long best[kPlanThreads / 32];
   __shared__ int4 gcache[kGroupCache], scache[kSeqCache];
   __shared__ int m_cu[kSeqCache + 1], m_ctx[kSeqCache], p_first[kJobCache];
   __shared__ int s_alt, s_tiles;
@@ -229,12 +242,12 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   const int* cu = S <= kSeqCache ? m_cu : a.cu_seqlens_q;
   const int* ctx = S <= kSeqCache ? m_ctx : w.context_lens;
   const PlanView view = {groups, seqs, NG, block_shift, G};
-  if (tid < 4) sums[tid] = 0;
   if (tid == 0) {
     s_alt = 0;
     s_tiles = 1;
-    s_best = ~0ull;
   }
+  int g_s0 = 0, g_s1 = 0, g_p = 0;                 // group tid, requested along with the sequences
+  if (tid < NG) g_s0 = w.cu_groups[tid], g_s1 = w.cu_groups[tid + 1], g_p = w.prefix_lens[tid];
   if (S <= kSeqCache) {
     for (int i = tid; i <= S; i += kPlanThreads) {
       m_cu[i] = a.cu_seqlens_q[i];
@@ -251,7 +264,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   int bad = 0;
   int64_t saved = 0;                               // keys that are not read again
   for (int g = tid; g < NG; g += kPlanThreads) {
-    const int s0 = w.cu_groups[g], s1 = w.cu_groups[g + 1], p = w.prefix_lens[g];
+    if (g != tid) g_s0 = w.cu_groups[g], g_s1 = w.cu_groups[g + 1], g_p = w.prefix_lens[g];
+    const int s0 = g_s0, s1 = g_s1, p = g_p;
     int t0 = 0, tokens = 0, shared = 0;
     if (s0 < 0 || s1 < s0 || s1 > S || (g == 0 && s0 != 0) || (g == NG - 1 && s1 != S)) {
       bad = 1;
@@ -267,13 +281,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     }
     groups[g] = make_int4(s0, t0, tokens, shared);
   }
-  add_warp_sum(&sums[3], saved);
+  put_warp_sum(sums[3], saved);
   bad = __syncthreads_or(bad);
   // Sharing takes the pieces and the join, one after the other: where the bytes
   // that it saves take HBM less time than that, every sequence reads its own
   // table (4 samples behind 512 keys of 8 heads: 25.1 us shared, 17.4 not).
   const float key_bytes = 4.0f * HD * float(Hkv);  // K and V of a key
-  if (float(sums[3]) * key_bytes < kShareUs * kBytesPerUs) {
+  if (float(sum_parts(sums[3])) * key_bytes < kShareUs * kBytesPerUs) {
     for (int g = tid; g < NG; g += kPlanThreads) groups[g].w = 0;
   }
   __syncthreads();
@@ -308,11 +322,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   }
   tiles_max = __reduce_max_sync(0xffffffffu, tiles_max);
   if ((tid & 31) == 0) atomicMax(&s_tiles, tiles_max);
-  add_warp_sum(&sums[0], n_first);
-  add_warp_sum(&sums[1], unit_tiles);
-  add_warp_sum(&sums[2], own_keys);
+  put_warp_sum(sums[0], n_first);
+  put_warp_sum(sums[1], unit_tiles);
+  put_warp_sum(sums[2], own_keys);
   __syncthreads();
-  const int64_t all_first = int64_t(sums[0]), all_tiles = int64_t(sums[1]);
+  const int64_t all_first = sum_parts(sums[0]), all_tiles = sum_parts(sums[1]);
   bad |= all_first * Hkv > w.piece_cap;            // only if token ranges overlap (malformed metadata)
   const int alt_recs = s_alt ? 2 : 1;
   tiles_max = s_tiles;
@@ -350,7 +364,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     }
     const int64_t recs = int64_t(T) * H * n * alt_recs;
     static_assert(kLanes == kWaveSteps, "the thread's n is the one that it scores");
-    const float piece_bytes = bytes * key_bytes, own_bytes = float(sums[2]) * key_bytes;
+    const float piece_bytes = bytes * key_bytes, own_bytes = float(sum_parts(sums[2])) * key_bytes;
     unsigned long long key = ~0ull;
     if (pieces > 0 && pieces <= w.piece_cap && recs <= w.prefix_rec_cap && own_recs <= w.piece_rec_cap) {
       // as many SMs as the pieces fill in 1 .. 16 waves; those of one size run in whole waves, unequal ones fill the gaps
@@ -368,11 +382,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
       const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, x);
       key = other < key ? other : key;
     }
-    if ((tid & 31) == 0) atomicMin(&s_best, key);
+    if ((tid & 31) == 0) best[tid >> 5] = key;
     __syncthreads();
-    bad |= s_best == ~0ull;                        // n = 1 fits unless token ranges overlap
-    n_segs = bad ? 1 : int(s_best & 0xffff);
-    working = bad ? w.num_sms : int(unsigned(s_best) >> 16);
+#pragma unroll
+    for (int x = 0; x < kPlanThreads / 32; ++x) key = best[x] < key ? best[x] : key;
+    bad |= key == ~0ull;                           // n = 1 fits unless token ranges overlap
+    n_segs = bad ? 1 : int(key & 0xffff);
+    working = bad ? w.num_sms : int(unsigned(key) >> 16);
     longest = ceil_div_fast(tiles_max, n_segs);
   }
   const int stride = n_segs * alt_recs;
@@ -383,9 +399,10 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
 
   // Streamed items, and every sequence's records: its rows have `pre` of the
   // prefix and `nch` own ones each.
+  const int half = tid / kHalfThreads, htid = tid - half * kHalfThreads;
   int64_t base = 0;                                // items in the low, own records in the high word
-  for (int s0 = 0; s0 < S && !bad; s0 += kPlanThreads) {
-    const int s = s0 + tid;
+  for (int s0 = 0; half == 0 && s0 < S && !bad; s0 += kHalfThreads) {
+    const int s = s0 + htid;
     int4 q = make_int4(0, 0, 0, 0), gr = q;
     int pre = 0, rt = 0, nch = 0;
     // units are claimed in the order of the sequences: the last quarter's are half as long, so that the
@@ -404,7 +421,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     }
     const int64_t n_items = int64_t(rt) * nch, n_recs = pre + nch > 1 ? int64_t(q.z) * H * nch : 0;
     int64_t total;
-    const int64_t at = base + block_scan(n_items | (n_recs << 32), warp_sums, &total);
+    const int64_t at = base + half_scan(n_items | (n_recs << 32), warp_sums, half, &total);
     base += total;
     bad |= (base & 0xffffffff) > w.item_cap || (base >> 32) > w.own_rec_cap;   // only if token ranges overlap
     if (q.x > 0 && !bad) {
@@ -426,9 +443,27 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
       }
     }
   }
-  if (a.max_q_len > 1 && !bad) {                   // every token's sequence by search
-    __syncthreads();
-    for (int t = tid; t < T; t += kPlanThreads) {
+  // the pieces: by segment, key/value head and row tile pair, so that the
+  // pairs of one (segment, head) run side by side and share its K/V in L2
+  int64_t pbase = 0;
+  if (half == 1 && all_first > 0 && !bad) {
+    for (int j0 = 0; j0 < jobs; j0 += kHalfThreads) {
+      const int j = j0 + htid;
+      int64_t count = 0;
+      if (j < jobs) {
+        const Job jb = get_job(view, j);
+        if (jb.keys > 0) count = int64_t(ceil_div_fast(jb.tokens, 2 * TT)) * Hkv * segments(jb.keys, longest).x;
+      }
+      int64_t total;
+      const int64_t at = pbase + half_scan(count, warp_sums, half, &total);
+      if (j < jobs) first_piece[j] = int(at);
+      pbase += total;
+    }
+    half_sync(half);
+  }
+  if (a.max_q_len > 1) __syncthreads();            // the sequences' records are known
+  if (half == 0 && a.max_q_len > 1 && !bad) {      // every token's sequence by search
+    for (int t = htid; t < T; t += kHalfThreads) {
       const int s = last_at_or_before(cu, 1, S, t);
       const int4 q = seqs[s];
       if (q.x > 0 && q.y <= t && t < q.y + q.z) {
@@ -438,27 +473,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
       }
     }
   }
-
-  // the pieces: by segment, key/value head and row tile pair, so that the
-  // pairs of one (segment, head) run side by side and share its K/V in L2
-  int64_t pbase = 0;
-  if (all_first > 0 && !bad) {
-    for (int j0 = 0; j0 < jobs; j0 += kPlanThreads) {
-      const int j = j0 + tid;
-      int64_t count = 0;
-      if (j < jobs) {
-        const Job jb = get_job(view, j);
-        if (jb.keys > 0) count = int64_t(ceil_div_fast(jb.tokens, 2 * TT)) * Hkv * segments(jb.keys, longest).x;
-      }
-      int64_t total;
-      const int64_t at = pbase + block_scan(count, warp_sums, &total);
-      if (j < jobs) first_piece[j] = int(at);
-      pbase += total;
-    }
-    __syncthreads();
-  }
   const int n_pieces = int(pbase);
-  for (int i = tid; i < n_pieces; i += kPlanThreads) {
+  for (int i = htid; i < n_pieces; i += kHalfThreads) {   // none in the other half
     const int j = last_at_or_before(first_piece, 1, jobs, i);   // jobs without pieces start there too, and come before
     const Job jb = get_job(view, j);
     const int2 sg = segments(jb.keys, longest);
@@ -490,13 +506,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     pc.flags = (alt ? kPieceAlt : 0) | (direct ? kPieceDirect : 0);
     w.pieces[i] = pc;
   }
-  if (bad) {                                       // nothing runs and no row is written
-    __syncthreads();
+  bad = __syncthreads_or(bad);
+  if (bad)                                         // nothing runs and no row is written
     for (int t = tid; t < T; t += kPlanThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
-  }
   if (tid == 0) {
     if (bad) raise_error(a.err, kErrInvalid);
-    w.header[0] = bad ? 0 : n_pieces;
     w.header[1] = stride;
     w.header[2] = int32_t(w.tag);
     w.header[3] = 0;
@@ -504,6 +518,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     w.header[5] = 0;
     w.header[6] = working;
   }
+  if (tid == kHalfThreads) w.header[0] = bad ? 0 : n_pieces;
 }
 
 // ------------------------------------------------------------------ prefix phase
