@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = H / Hkv;
 
   if (w.wait_previous) grid_dependency_wait();    // the plan kernel has finished
+  const EndAfterPrevious end{!w.wait_previous && blockIdx.x == 0};
   const uint32_t seen_tag = uint32_t(__ldcg(w.header + 4));
   const int n_items = __ldcg(w.header);
   const int split_keys = __ldcg(w.header + 5);

@@ -40,6 +40,16 @@ __device__ __forceinline__ void raise_error(unsigned* word, unsigned bits) {
   atomicOr(word, bits);
 }
 
+// A grid that does not wait for the one launched before it ends no sooner all the
+// same: its first CTA waits at its end, whichever way it leaves.  So whoever waits
+// for this grid (a programmatic dependent launch behind it) has waited for both.
+struct EndAfterPrevious {
+  bool wait;
+  __device__ __forceinline__ ~EndAfterPrevious() {
+    if (wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
+};
+
 // A persistent grid's claim counter returns to zero for the next launch over
 // the same plan (the layers of a planned step): each CTA that claimed counts
 // itself in `done` once it will claim no more, and the last of the

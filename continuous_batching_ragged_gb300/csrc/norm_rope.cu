@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_append_kernel(
   constexpr int A = LPR * EPV;                  // head_dim
   constexpr int kGroups = kThreads / LPR;       // rows side by side in the CTA
   constexpr int kTab = MODE == kPartial ? EPV : EPV / 2;   // cosines (and sines) that a lane needs
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // it may start while the stream's last kernel ends
   int32_t n_tok = a.num_tokens;
   if (a.dims) {                                 // the step's token count, at most num_tokens (the capacity)
     const int32_t t = a.dims[1];
@@ -219,21 +220,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) norm_rope_append_kernel(
 }
 
 template <typename T, int LPR, int kRows>
-void launch_rows(const NormRopeArgs& a, bool interleaved, unsigned chunks, cudaStream_t stream) {
+cudaError_t launch_rows(const NormRopeArgs& a, bool interleaved, unsigned chunks, cudaStream_t stream) {
   const int64_t ctas = std::max<int64_t>(1, int64_t(kCtasPerSm) * cb::sm_count() / chunks);
   const dim3 grid(unsigned(std::min<int64_t>(a.num_tokens, ctas)), chunks);
-  if (interleaved)
-    norm_rope_append_kernel<T, LPR, kRows, kInterleaved><<<grid, kThreads, 0, stream>>>(a);
-  else if (a.rot_dim == LPR * Vec16<T>::N)
-    norm_rope_append_kernel<T, LPR, kRows, kHalves><<<grid, kThreads, 0, stream>>>(a);
-  else
-    norm_rope_append_kernel<T, LPR, kRows, kPartial><<<grid, kThreads, 0, stream>>>(a);
+  auto kernel = interleaved                         ? norm_rope_append_kernel<T, LPR, kRows, kInterleaved>
+                : a.rot_dim == LPR * Vec16<T>::N ? norm_rope_append_kernel<T, LPR, kRows, kHalves>
+                                                 : norm_rope_append_kernel<T, LPR, kRows, kPartial>;
+  return cb::launch_kernel(kernel, grid, dim3(kThreads), 0, stream, true, a);
 }
 
 // Rows in flight per lane group: as many as a token has for each, where there are
 // tokens enough to fill the GPU that way.
 template <typename T, int LPR>
-void launch(const NormRopeArgs& a, bool interleaved, cudaStream_t stream) {
+cudaError_t launch(const NormRopeArgs& a, bool interleaved, cudaStream_t stream) {
   constexpr int kGroups = kThreads / LPR;
   const int64_t rows = int64_t(a.num_q_heads) + 2 * int64_t(a.num_kv_heads);
   const int64_t per_group = (rows + kGroups - 1) / kGroups;
@@ -311,12 +310,11 @@ extern "C" cb_status cb_norm_rope_append(const cb_norm_rope* in, int32_t num_q_h
   a.err = err;
   const bool il = in->interleaved != 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (bf16 && A == 64) launch<__nv_bfloat16, 8>(a, il, st);
-  else if (bf16 && A == 128) launch<__nv_bfloat16, 16>(a, il, st);
-  else if (bf16) launch<__nv_bfloat16, 32>(a, il, st);
-  else if (A == 64) launch<float, 16>(a, il, st);
-  else launch<float, 32>(a, il, st);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = bf16 && A == 64    ? launch<__nv_bfloat16, 8>(a, il, st)
+                        : bf16 && A == 128 ? launch<__nv_bfloat16, 16>(a, il, st)
+                        : bf16             ? launch<__nv_bfloat16, 32>(a, il, st)
+                        : A == 64          ? launch<float, 16>(a, il, st)
+                                           : launch<float, 32>(a, il, st);
   if (e != cudaSuccess) return cb::cuda_fail(e, "norm and rotation: launch");
   return CB_OK;
 }

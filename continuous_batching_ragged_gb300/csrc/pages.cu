@@ -79,6 +79,7 @@ __device__ __forceinline__ Fork read_fork(const ForkArgs& a, int f) {
 // no fork that passes it.
 __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a, const Pools pools) {
   const int f = blockIdx.x;
+  grid_dependency_wait();              // it may start while the stream's last kernel ends
   const Fork me = read_fork(a, f);
   unsigned bad = me.bad;
   if (!bad) {
@@ -180,6 +181,7 @@ __device__ __forceinline__ int block_sum_scan(int v, int* warp_sums, int& total)
 // the moves need no order.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactArgs a) {
   launch_dependents();                 // they wait for this grid on the device
+  grid_dependency_wait();              // it may start while the stream's last kernel ends
   extern __shared__ uint32_t bits[];
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x;
@@ -372,8 +374,8 @@ extern "C" cb_status cb_fork_sequences(const cb_kv_cache* layers, int32_t num_la
     // 16 CTAs an SM in all: 256 forks over 16 layers take 47.7 us, at 4, 8 and 32 CTAs 55.9, 51.3 and 49.5
     const int64_t want = (int64_t(cb::sm_count()) * 16 + num_forks - 1) / num_forks;
     const unsigned y = unsigned(std::max<int64_t>(1, std::min<int64_t>(a.num_pools, want)));
-    fork_kernel<<<dim3(unsigned(num_forks), y), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a, pools);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = cb::launch_kernel(fork_kernel, dim3(unsigned(num_forks), y), dim3(kThreads), 0,
+                                      static_cast<cudaStream_t>(stream), true, a, pools);
     if (e != cudaSuccess) return cb::cuda_fail(e, "fork: launch");
   }
   return CB_OK;
@@ -446,8 +448,7 @@ extern "C" cb_status cb_compact_blocks(const cb_kv_cache* layers, int32_t num_la
     }
   }
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  compact_plan_kernel<<<1, kPlanThreads, smem, cs>>>(a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = cb::launch_kernel(compact_plan_kernel, dim3(1), dim3(kPlanThreads), smem, cs, true, a);
   if (e != cudaSuccess) return cb::cuda_fail(e, "compact: plan launch");
   for (int32_t first = 0; first < num_layers; first += kMaxLayers) {
     Pools pools;

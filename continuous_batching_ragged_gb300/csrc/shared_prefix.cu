@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     s_alt = 0;
     s_tiles = 1;
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // it may start while the stream's last kernel ends
   int g_s0 = 0, g_s1 = 0, g_p = 0;                 // group tid, requested along with the sequences
   if (tid < NG) g_s0 = w.cu_groups[tid], g_s1 = w.cu_groups[tid + 1], g_p = w.prefix_lens[tid];
   if (S <= kSeqCache) {
@@ -1182,9 +1183,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   const uint32_t bars = base + kSmallOffBars + warp * stream::kStages * 8;
   const int S = a.num_seqs, T = a.num_tokens, NG = w.num_groups, H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv;
 
-  int s0 = 0, s1 = 0, p = 0, c0 = 0, q_len = 0, n = 0;
-  if (tid < NG) s0 = w.cu_groups[tid], s1 = w.cu_groups[tid + 1], p = w.prefix_lens[tid];
-  if (tid < S) c0 = a.cu_seqlens_q[tid], q_len = a.cu_seqlens_q[tid + 1] - c0, n = w.context_lens[tid];
   if (lane == 0) {
     for (int st = 0; st < stream::kStages; ++st) mbar_init(bars + 8 * st, 1);
     fence_mbar_init();
@@ -1193,6 +1191,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       tma_prefetch_desc(&tm_v16);
     }
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // it may start while the stream's last kernel ends
+  int s0 = 0, s1 = 0, p = 0, c0 = 0, q_len = 0, n = 0;
+  if (tid < NG) s0 = w.cu_groups[tid], s1 = w.cu_groups[tid + 1], p = w.prefix_lens[tid];
+  if (tid < S) c0 = a.cu_seqlens_q[tid], q_len = a.cu_seqlens_q[tid + 1] - c0, n = w.context_lens[tid];
   if (writer)
     for (int t = tid; t < T; t += kSmallThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
   group_s0[tid] = s0;
@@ -1459,7 +1461,7 @@ static cb_status launch_small_step(const AttnArgs& a, const PrefixWork& w, cudaS
   cb_status st = encode_pools(a, enc, true, &tk16, &tv16);
   if (st == CB_OK) st = allow_shared_memory();
   if (st != CB_OK) return st;
-  cudaError_t e = launch_kernel(small_step_kernel, dim3(unsigned(w.num_sms)), dim3(kSmallThreads), kSmallSmem, stream, false,
+  cudaError_t e = launch_kernel(small_step_kernel, dim3(unsigned(w.num_sms)), dim3(kSmallThreads), kSmallSmem, stream, true,
                                 tk16, tv16, a, w);
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: launch");
 }
@@ -1526,8 +1528,7 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   if (small) {
     st = launch_small_step(a, w, stream);
   } else {
-    prefix_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a, w);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_kernel(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, a, w);
     if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: plan launch");
     st = launch_prefix_tc(a, w, stream);
   }

@@ -561,6 +561,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) split_kv_persistent_kernel(con
   }
   if (threadIdx.x == 0) abort_flag = 0;
   if (sa.wait_previous) grid_dependency_wait();   // the plan kernel has finished
+  const EndAfterPrevious end{!sa.wait_previous && blockIdx.x == 0};
   const int H = a.num_heads;                // query heads
   const int G = H / a.num_kv_heads;         // query heads per KV head
   const int n_groups = sa.n_groups;         // = H / GU
