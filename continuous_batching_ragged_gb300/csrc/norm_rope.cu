@@ -17,9 +17,11 @@
 // half, so that both elements of a pair are its own.  A persistent grid keeps the
 // next token's rows (up to three per lane group) on their way while it works on
 // one; a warp of values only copies.
-// 2048 tokens of 32 + 2 * 32 heads, bf16: 18.9 us, 5.4 TB/s (one row per lane
+// 2048 tokens of 32 + 2 * 32 heads, bf16: 18.2 us, 5.6 TB/s (one row per lane
 // group 42 us; several rows 30; pairs in one lane and the next token in flight 24;
-// values only copied 21.9; three CTAs an SM 18.9).
+// values only copied 21.9; three CTAs an SM 18.9).  Back to back it was 20.8 before
+// it could be launched while the kernel in front ends; released to its own
+// successor early, 20.4: that one's CTAs then wait where its own would run.
 #include <algorithm>
 #include <cmath>
 

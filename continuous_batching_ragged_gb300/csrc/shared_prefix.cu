@@ -26,7 +26,13 @@
 //   * both run in one launch: some CTAs take pieces first, the others stream own
 //     keys at once, and whoever runs out of pieces goes on to the streams;
 //   * the plan, one CTA, cuts the pieces' KV ranges and splits the SMs by
-//     estimated time.  Every segment costs the join one more record per row.
+//     estimated time.  Every segment costs the join one more record per row;
+//   * a step whose keys are too few for sharing to pay is streams alone, and every
+//     CTA plans it for itself.
+// Measured (graph replays; behind the bar, with every sequence reading its whole
+// context): 64 sequences behind 2048 keys of 32 heads 75 us | 286; 256 behind 8192
+// keys of 8 heads 129 | 1590; 24 prompts of up to 7 samples 69 | 101; 12 chunks of
+// 200 tokens behind 4096 keys 164 | 220; 4 behind 512 keys 10 | 27.
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -119,7 +125,7 @@ static_assert(kSegChoices * kWaveSteps == kPlanThreads, "a thread scores one cho
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // The plan is one CTA that runs every line once: what it costs is latency, of the
-// instruction fetches first of all (about 9 us with everything inlined).  So its
+// instruction fetches first of all (some 10 us for 200 sequences).  So its
 // helpers are functions of their own, and its arrays are reached through one
 // generic pointer each, in shared memory where they fit and in the workspace else.
 
@@ -1152,7 +1158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Small steps: too few keys for sharing to pay, and a thread of a CTA for each
 // sequence.  The plan of such a step costs a CTA less than waiting for another
 // kernel's, so every CTA makes its own, with the same checks, chunks and records
-// (4 samples behind 512 keys 10.1 us, with the plan kernel 17.4).  That also holds
+// (4 samples behind 512 keys 9.9 us, with the plan kernel 17.4).  That also holds
 // where sharing would save some bytes: 32 sequences behind 512 keys, 70 MB in all,
 // 16.2 us and 24.6 with sharing; 6 behind 4096, 101 MB, 26.3 and 27.5.
 constexpr int kSmallThreads = 32 * kStreamWarps;
@@ -1257,7 +1263,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 // A warp joins kJoinRows query heads of a token at a time and goes on to the next
 // ones a grid further.  The records come from L2: what counts is bytes in flight,
 // so 8 records are requested at once, two of each of four rows or four of each of
-// two, and the next rows' description before them.
+// two, and the next rows' description before them.  76,800 rows of 3 records: 23 us,
+// 5.2 TB/s.  More CTAs an SM leave too few registers for that: the step of 12 prompt
+// chunks takes 166 us with two, 167 with three, 183 with four.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 4;
 constexpr int kJoinCtasPerSm = 2;

@@ -16,6 +16,8 @@
 //     mma.sync m16n8k16 steps, 32 of them per 8 KB of keys and values;
 //   * a unit leaves its rows unnormalised, (acc, max, sum) in fp32, for the join;
 //     a row with a single record is written to out at once.
+// Large steps stream at 6.4 to 6.8 TB/s.  One of 114 us took 163 with 4 warps of 6
+// stages, 112 with both 64-dim halves in one box; its loads alone take 104.
 #pragma once
 
 #include <cuda.h>

@@ -20,6 +20,11 @@
  *     workspace (cb_attention_workspace_size).
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *     Device work is enqueued on it and the call returns after the launch.
+ *   - cb_norm_rope_append, cb_fork_sequences, cb_compact_blocks and
+ *     cb_shared_prefix_attention are programmatic dependent launches that wait, on
+ *     the device, for the kernel in front of them.  A kernel of the caller's own
+ *     that is launched with programmatic stream serialization in front of them has
+ *     to execute griddepcontrol.wait too.
  *   - Errors that can be seen on the host (null pointers, sizes, unsupported
  *     dtype/shape combinations, bounds given by the caller) are returned before
  *     anything is launched.  Errors that only the device can see (a slot or
