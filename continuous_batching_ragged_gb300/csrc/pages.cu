@@ -182,8 +182,8 @@ __device__ __forceinline__ int block_sum_scan(int v, int* warp_sums, int& total)
 // are as many of the one as of the other, and no page is on both sides, so
 // the moves need no order.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactArgs a) {
-  launch_dependents();                 // they wait for this grid on the device
   grid_dependency_wait();              // it may start while the stream's last kernel ends
+  launch_dependents();                 // they wait for this grid on the device
   extern __shared__ uint32_t bits[];
   __shared__ int warp_sums[32];
   const int tid = threadIdx.x;

@@ -230,7 +230,6 @@ __device__ __noinline__ Job get_job(const PlanView v, int j) {
 // One CTA.  Checks the groups, chooses the segments of the pieces and the
 // chunks of the streams, lists both and gives every row its records.
 __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArgs a, const PrefixWork w) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // they wait for this grid on the device
   __shared__ int64_t warp_sums[kPlanThreads / 32];
   __shared__ int64_t sums[4][kPlanThreads / 32];
   __shared__ unsigned long long best[kPlanThreads / 32];
@@ -253,6 +252,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     s_tiles = 1;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // it may start while the stream's last kernel ends
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // they wait for this grid on the device
   int g_s0 = 0, g_s1 = 0, g_p = 0;                 // group tid, requested along with the sequences
   if (tid < NG) g_s0 = w.cu_groups[tid], g_s1 = w.cu_groups[tid + 1], g_p = w.prefix_lens[tid];
   if (S <= kSeqCache) {
@@ -1177,7 +1177,6 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 __global__ void __launch_bounds__(kSmallThreads, 1)
     small_step_kernel(const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
                       const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
   __shared__ stream::SmallSeq seqs[kSmallSeqs];
   __shared__ int group_s0[kSmallSeqs], group_p[kSmallSeqs];
@@ -1198,6 +1197,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // it may start while the stream's last kernel ends
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int s0 = 0, s1 = 0, p = 0, c0 = 0, q_len = 0, n = 0;
   if (tid < NG) s0 = w.cu_groups[tid], s1 = w.cu_groups[tid + 1], p = w.prefix_lens[tid];
   if (tid < S) c0 = a.cu_seqlens_q[tid], q_len = a.cu_seqlens_q[tid + 1] - c0, n = w.context_lens[tid];

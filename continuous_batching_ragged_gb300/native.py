@@ -23,7 +23,8 @@ EXPORTS = ("cb_append_kv", "cb_attention_workspace_size", "cb_ragged_attention",
            "cb_ragged_attention_gqa", "cb_attention_workspace_size_gqa",
            "cb_plan_step_gqa", "cb_ragged_attention_planned_gqa",
            "cb_decode_attention_noalloc", "cb_padded_attention",
-           "cb_shared_prefix_workspace_size", "cb_shared_prefix_attention", "cb_norm_rope_append", "cb_fork_sequences", "cb_compact_workspace_size", "cb_compact_blocks",
+           "cb_shared_prefix_workspace_size", "cb_shared_prefix_attention", "cb_norm_rope_append",
+           "cb_fork_sequences", "cb_compact_workspace_size", "cb_compact_blocks",
            "cb_scheduler_create", "cb_scheduler_destroy", "cb_add_request", "cb_build_batch",
            "cb_complete_step", "cb_scheduler_stats", "cb_check_device_errors", "cb_last_error",
            "cb_synth_tokens", "cb_synth_fill_cache", "cb_selftest_bounded_wait")
