@@ -1164,6 +1164,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kSmallThreads = 32 * kStreamWarps;
 constexpr int kSmallSeqs = kSmallThreads;
 constexpr int kSmallTokens = 4096;
+// Contexts up to which a small step's rows are one chunk each, written at once, where the
+// join and its launch cost more than the longer chunks: few units wait for every
+// tile of theirs, some 0.6 us each, many fill the GPU all the same.  4 sequences of 8
+// heads, 128 keys: 9.1 us and 8.7 with a join (called one after the other, from the host,
+// 10.8 and 13.7); 192 keys 11.5 and 9.1.  214 of 4 heads, 190 keys: 13.4 and 21.0; 120 of
+// 240 keys 13.8 and 15.2.
+constexpr int kOneChunkKeysFew = 128, kOneChunkKeysMany = 384;
+constexpr int kManyUnitsPerSm = 2;
 constexpr uint32_t kSmallOffBars = stream::kRingBytes, kSmallOffSlots = kSmallOffBars + stream::kBarBytes;
 constexpr uint32_t kSmallSmem = kSmallOffSlots + stream::kSlotBytes + 1024;
 static_assert(kSmallOffSlots % 16 == 0 && kSmallSmem <= 220 * 1024, "shared memory");
@@ -1223,7 +1231,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 #pragma unroll
   for (int i = 0; i < kStreamWarps; ++i) per += sums[0][i];
   per /= w.stream_units;
-  const int L = int(per < kMinChunkTiles ? kMinChunkTiles : (per > (1 << 26) ? (1 << 26) : per));
+  const int L = int(per < w.min_chunk_tiles ? w.min_chunk_tiles : (per > (1 << 26) ? (1 << 26) : per));
   const int nch = ok ? (tiles - 1) / L + 1 : 0;
   const int64_t items = int64_t(rt) * nch, recs = nch > 1 ? int64_t(q_len) * H * nch : 0;
   int64_t item0 = items, rec0 = recs;              // exclusive scans over the CTA
@@ -1532,6 +1540,9 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   const bool small = a.num_seqs <= kSmallSeqs && num_groups <= kSmallSeqs && a.num_tokens <= kSmallTokens &&
                      (a.max_q_len == 1 || int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= kMaxStreamRows) &&
                      saved < double(kSmallUs) * kBytesPerUs;
+  const bool many = int64_t(a.num_seqs) * a.num_kv_heads >= int64_t(kManyUnitsPerSm) * w.num_sms;
+  const bool one_chunk = small && a.max_context_len <= (many ? kOneChunkKeysMany : kOneChunkKeysFew);
+  w.min_chunk_tiles = one_chunk ? kOneChunkKeysMany / stream::kTileKeys : kMinChunkTiles;
   cb_status st;
   if (small) {
     st = launch_small_step(a, w, stream);
@@ -1540,7 +1551,7 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
     if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: plan launch");
     st = launch_prefix_tc(a, w, stream);
   }
-  if (st != CB_OK) return st;
+  if (st != CB_OK || one_chunk) return st;
   return launch_join(a, w, stream);
 }
 

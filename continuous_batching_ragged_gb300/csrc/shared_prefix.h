@@ -57,6 +57,7 @@ struct PrefixWork {
   int32_t num_sms;
   int32_t tile_tokens;         // query tokens per row tile of a piece
   int32_t stream_units;        // streamed units that the chunk length aims for
+  int32_t min_chunk_tiles;     // shortest chunk of a small step's streams, in 16-key tiles
   int32_t piece_cap, item_cap;
   int64_t prefix_rec_cap;      // records of the prefixes; the own ones follow
   int64_t piece_rec_cap;       // own records of pieces

@@ -407,3 +407,20 @@ def test_few_sequences(native_lib, S, H, K, q):
 def test_one_long_sequence(native_lib):
     """More units than warps, for one row."""
     run_checked([(100, [(70_000, 1)])], 16, 16, 16, seed=14, ballast=False)
+
+
+@pytest.mark.parametrize("S,H,K,q,longest", [(3, 8, 8, 1, 128), (3, 8, 8, 1, 129), (90, 8, 4, 1, 384), (90, 8, 4, 1, 385), (50, 16, 8, 9, 300)])
+def test_short_contexts(native_lib, S, H, K, q, longest):
+    """Rows of one chunk, which no join follows, on both sides of their lengths."""
+    from continuous_batching_ragged_gb300 import api
+    own = [max(q, 1 + 53 * i % (longest - 33)) for i in range(S - 1)] + [longest - 33]
+    st = run_checked([(33, [(n, q if i % 2 else 1) for i, n in enumerate(own)])], H, K, 16, seed=S, ballast=False)
+    assert st.max_ctx == longest
+    st.ctx[1] = longest + 1                            # left out, and its rows as they were
+    st.out.fill_(float("nan"))
+    st.run()
+    from continuous_batching_ragged_gb300 import native
+    with pytest.raises(native.CBError, match="INVALID"):
+        api.cb_check_device_errors()
+    assert bool(st.out[st.cu_l[1]:st.cu_l[2]].isnan().all())
+    st.check([s for s in range(S) if s != 1])
