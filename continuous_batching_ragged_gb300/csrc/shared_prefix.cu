@@ -118,7 +118,7 @@ constexpr float kBytesPerUs = 6.7e6f;    // HBM
 constexpr float kStreamBytesPerUsPerSm = 4.2e4f;   // streams of one SM
 constexpr float kJoinBytesPerUs = 4.0e6f;
 constexpr float kShareUs = 6.0f;          // what a step's pieces and join take at least
-constexpr float kSmallUs = 16.0f;         // the same with the plan, for steps that can do without
+constexpr float kSmallUs = 28.0f;         // the same with the plan, for steps that can do without
 constexpr int kWaveSteps = 16;           // SM splits that are scored: those that the pieces fill in 1 .. 16 waves
 static_assert(kSegChoices * kWaveSteps == kPlanThreads, "a thread scores one choice");
 
@@ -1158,9 +1158,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Small steps: too few keys for sharing to pay, and a thread of a CTA for each
 // sequence.  The plan of such a step costs a CTA less than waiting for another
 // kernel's, so every CTA makes its own, with the same checks, chunks and records
-// (4 samples behind 512 keys 9.9 us, with the plan kernel 17.4).  That also holds
-// where sharing would save some bytes: 32 sequences behind 512 keys, 70 MB in all,
-// 16.2 us and 24.6 with sharing; 6 behind 4096, 101 MB, 26.3 and 27.5.
+// (4 samples behind 512 keys 8.7 us, with the plan kernel 17.4).  That also holds
+// where sharing would save some bytes, which are in L2 after the first reader: 32
+// sequences behind 1024 keys, 137 MB in all, 20.0 us and 25.1 with sharing; 24 behind
+// 2048, 203 MB, 25.2 and 25.5; 100 behind 1024, 271 MB, 35.8 and 28.2.
 constexpr int kSmallThreads = 32 * kStreamWarps;
 constexpr int kSmallSeqs = kSmallThreads;
 constexpr int kSmallTokens = 4096;
@@ -1170,6 +1171,7 @@ constexpr int kSmallTokens = 4096;
 // heads, 128 keys: 9.1 us and 8.7 with a join (called one after the other, from the host,
 // 10.8 and 13.7); 192 keys 11.5 and 9.1.  214 of 4 heads, 190 keys: 13.4 and 21.0; 120 of
 // 240 keys 13.8 and 15.2.
+constexpr int kSmallChunkTiles = stream::kStages;   // shortest chunk, all of it in flight at once (2 rows of 320 keys: 8.7 us, 9.1 with one more)
 constexpr int kOneChunkKeysFew = 128, kOneChunkKeysMany = 384;
 constexpr int kManyUnitsPerSm = 2;
 constexpr uint32_t kSmallOffBars = stream::kRingBytes, kSmallOffSlots = kSmallOffBars + stream::kBarBytes;
@@ -1188,7 +1190,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ stream::SmallSeq seqs[kSmallSeqs];
   __shared__ int group_s0[kSmallSeqs], group_p[kSmallSeqs];
-  __shared__ int64_t sums[3][kStreamWarps];
+  __shared__ int64_t sums[4][kStreamWarps];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* gsm = smem_raw + (base - raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1224,13 +1226,16 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   const bool ok = tid < S && p >= 0 && q_len >= 1 && c0 >= 0 && c0 + q_len <= T && q_len <= a.max_q_len && n >= q_len &&
                   p <= n - q_len && n <= a.max_context_len && int64_t(n) <= int64_t(a.max_blocks_per_seq) * a.block_size;
   const int tiles = ok ? (n - 1) / stream::kTileKeys + 1 : 0, rt = ok ? (q_len * G + kStreamRows - 1) / kStreamRows : 0;
-  const int64_t mine = warp_sum(int64_t(tiles) * rt * Hkv);
-  if (lane == 0) sums[0][warp] = mine;
+  const int64_t my_tiles = warp_sum(int64_t(tiles) * rt * Hkv), my_rows = warp_sum(int64_t(rt) * Hkv);
+  if (lane == 0) sums[0][warp] = my_tiles, sums[3][warp] = my_rows;
   __syncthreads();
-  int64_t per = w.stream_units - 1;
+  const int warps = int(gridDim.x) * kStreamWarps;
+  int64_t all_tiles = 0, spare = warps;            // ceil(x / L) is less than x / L + 1 for each row tile and head
 #pragma unroll
-  for (int i = 0; i < kStreamWarps; ++i) per += sums[0][i];
-  per /= w.stream_units;
+  for (int i = 0; i < kStreamWarps; ++i) all_tiles += sums[0][i], spare -= sums[3][i];
+  // One unit a warp, where there are warps enough: a unit's beginning and end cost as much as some tiles (6 sequences
+  // behind 4900 keys 13.2 us, with kUnitsPerWarp units a warp 18.5; one of 130,000 keys 89 and 99)
+  const int64_t units = spare > 0 ? spare : w.stream_units, per = (all_tiles + units - 1) / units;
   const int L = int(per < w.min_chunk_tiles ? w.min_chunk_tiles : (per > (1 << 26) ? (1 << 26) : per));
   const int nch = ok ? (tiles - 1) / L + 1 : 0;
   const int64_t items = int64_t(rt) * nch, recs = nch > 1 ? int64_t(q_len) * H * nch : 0;
@@ -1262,7 +1267,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     }
   }
   __syncthreads();
-  const int warps = int(gridDim.x) * kStreamWarps;
   stream::run_warp<true>(&tm_k16, &tm_v16, a, w, bad ? 0 : int(all_items), base + warp * stream::kStages * stream::kStageBytes,
                          bars, reinterpret_cast<SuffixItem*>(gsm + kSmallOffSlots) + 2 * warp,
                          warp * int(gridDim.x) + int(blockIdx.x), warps, 0, stream::SmallStep{seqs, S, L});
@@ -1371,6 +1375,79 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinCtasPerSm) join_kernel(cons
   }
 }
 
+// Very few rows, which may have very many records: a CTA to a row.  Each warp joins its
+// share of the records, the first warp the eight results.
+constexpr int kWideCtasPerSm = 4;
+constexpr int kWideWarps = kJoinThreads / 32;
+__global__ void __launch_bounds__(kJoinThreads, kWideCtasPerSm) join_wide_kernel(const AttnArgs a, const PrefixWork w) {
+  constexpr int K = 4;                             // records in flight per warp
+  __shared__ float4 part_acc[kWideWarps][32];
+  __shared__ float2 part_ml[kWideWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tok = int(blockIdx.x) / a.num_heads, h = int(blockIdx.x) - tok * a.num_heads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 ti = __ldcg(w.token_info + tok);
+  const int stride = __ldcg(w.header + 1);
+  if (uint32_t(__ldcg(w.header + 2)) != w.tag) return;
+  const int np = ti.x, n = np + ti.z;
+  if (n < 2) return;                               // left out, or already written
+  const size_t pre = (size_t(tok) * a.num_heads + h) * stride, own = size_t(unsigned(ti.y)) + size_t(h) * ti.z;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float mx = -INFINITY, den = 0.f;
+  auto add = [&](float top, const float4& x, float2 ml) {   // top: a maximum of at least ml.x
+    const float f = ex2(ml.x - (top == -INFINITY ? 0.f : top));
+    den = fmaf(f, ml.y, den);
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
+  };
+  auto raise = [&](float top) {
+    const float old = ex2(mx - (top == -INFINITY ? 0.f : top));
+    acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+    den *= old;
+    mx = top;
+  };
+  for (int k0 = warp; k0 < n; k0 += kWideWarps * K) {
+    float4 x[K];
+    float2 ml[K];
+    float top = mx;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int kk = k0 + k * kWideWarps;
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (kk < n) {
+        const size_t at = kk < np ? pre + kk : own + kk - np;
+        x[k] = __ldcg(reinterpret_cast<const float4*>(w.recs + at * HD) + lane);
+        ml[k] = __ldcg(w.rec_ml + at);
+      }
+      top = fmaxf(top, ml[k].x);
+    }
+    raise(top);
+#pragma unroll
+    for (int k = 0; k < K; ++k) add(top, x[k], ml[k]);
+  }
+  part_acc[warp][lane] = acc;
+  if (lane == 0) part_ml[warp] = make_float2(mx, den);
+  __syncthreads();
+  if (warp > 0) return;
+  float top = mx;
+#pragma unroll
+  for (int k = 1; k < kWideWarps; ++k) top = fmaxf(top, part_ml[k].x);
+  raise(top);
+#pragma unroll
+  for (int k = 1; k < kWideWarps; ++k) add(top, part_acc[k][lane], part_ml[k]);
+  const float inv = 1.0f / den;
+  uint2 v;
+  v.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+  v.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+  *(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + size_t(blockIdx.x) * HD) + lane) = v;
+}
+bool wide_join(const AttnArgs& a, const PrefixWork& w) {
+  return int64_t(a.num_tokens) * a.num_heads <= int64_t(w.num_sms) * kWideCtasPerSm;
+}
+
 std::mutex g_attr_mutex;
 bool g_attr_set[64] = {};
 
@@ -1395,7 +1472,8 @@ PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_
   // ceil(x / L) <= x / L + 1 for every streamed sequence, and all x / L together are at most the units aimed for,
   // twice that where L is halved
   const size_t units = 2 * size_t(kMaxSms) * kStreamWarps * kUnitsPerWarp;
-  const size_t chunks_of_row = (size_t(max_context_len) + stream::kTileKeys * kMinChunkTiles - 1) / (stream::kTileKeys * kMinChunkTiles);
+  const size_t shortest = size_t(stream::kTileKeys) * std::min(kMinChunkTiles, kSmallChunkTiles);
+  const size_t chunks_of_row = (size_t(max_context_len) + shortest - 1) / shortest;
   z.items = z.T * G / kStreamRows + z.S + units + 1;
   z.own_recs = z.piece_recs + std::min(rows * chunks_of_row, rows + kStreamRows * units);
   return z;
@@ -1483,6 +1561,11 @@ static cb_status launch_small_step(const AttnArgs& a, const PrefixWork& w, cudaS
 }
 
 static cb_status launch_join(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
+  if (wide_join(a, w)) {
+    cudaError_t e = launch_kernel(join_wide_kernel, dim3(unsigned(a.num_tokens) * unsigned(a.num_heads)), dim3(kJoinThreads), 0,
+                                  stream, true, a, w);
+    return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: join launch");
+  }
   const int64_t slots = int64_t(w.num_sms) * kJoinCtasPerSm, per_cta = kJoinThreads / 32;
   const bool few = int64_t(a.num_tokens) * a.num_heads <= slots * per_cta;
   const int64_t warps = int64_t(a.num_tokens) * (few ? a.num_heads : (a.num_heads + kJoinRows - 1) / kJoinRows);
@@ -1536,13 +1619,14 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   w.tag = next_tag.fetch_add(1);
 
   // what sharing could save at most does not pay for it, and no sequence's own keys are pieces
-  const double saved = double(a.num_seqs - 1) * a.max_context_len * a.num_kv_heads * (4.0 * HD);
+  const int64_t row_tiles = (int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) + kStreamRows - 1) / kStreamRows;
+  const double saved = double(std::max(0, a.num_seqs - num_groups)) * a.max_context_len * a.num_kv_heads * (4.0 * HD) * row_tiles;
   const bool small = a.num_seqs <= kSmallSeqs && num_groups <= kSmallSeqs && a.num_tokens <= kSmallTokens &&
                      (a.max_q_len == 1 || int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= kMaxStreamRows) &&
                      saved < double(kSmallUs) * kBytesPerUs;
   const bool many = int64_t(a.num_seqs) * a.num_kv_heads >= int64_t(kManyUnitsPerSm) * w.num_sms;
   const bool one_chunk = small && a.max_context_len <= (many ? kOneChunkKeysMany : kOneChunkKeysFew);
-  w.min_chunk_tiles = one_chunk ? kOneChunkKeysMany / stream::kTileKeys : kMinChunkTiles;
+  w.min_chunk_tiles = one_chunk ? kOneChunkKeysMany / stream::kTileKeys : kSmallChunkTiles;
   cb_status st;
   if (small) {
     st = launch_small_step(a, w, stream);

@@ -24,10 +24,10 @@ class Step:
     def __init__(self, groups, H, K, B, seed=0, q_scale=1.0, k_slope=0.0, extra_blocks=3, num_blocks=None, width=None,
                  ballast=True):
         from continuous_batching_ragged_gb300 import api
-        # a step shares only where that saves some 100 MB: one more group that does, whatever the others are
+        # a step shares only where that saves some 190 MB: one more group that does, whatever the others are
         self.real = sum(len(members) for _, members in groups)
         if ballast:
-            groups = list(groups) + [(2048, [(1, 1)] * (2 + 115_000_000 // (2048 * 4 * A * K)))]
+            groups = list(groups) + [(2048, [(1, 1)] * (2 + 200_000_000 // (2048 * 4 * A * K)))]
         g = torch.Generator(device="cuda").manual_seed(seed)
         pick = torch.Generator().manual_seed(seed)
         self.H, self.K, self.B, self.groups = H, K, B, groups

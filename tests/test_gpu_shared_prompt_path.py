@@ -29,7 +29,7 @@ class Loop:
         self.tables = torch.full((max_rows, width), -1, dtype=torch.int32, device="cuda")
         self.ctx = torch.zeros(max_rows, dtype=torch.int32, device="cuda")
         self.free = list(range(num_blocks))
-        ang = torch.arange(4096, dtype=torch.float64, device="cuda")[:, None] * 1e4 ** (
+        ang = torch.arange(8192, dtype=torch.float64, device="cuda")[:, None] * 1e4 ** (
             -torch.arange(0, A, 2, dtype=torch.float64, device="cuda") / A)
         self.cos_sin = torch.cat([ang.cos(), ang.sin()], 1).float().contiguous()
         self.w = [(1 + 0.2 * torch.randn(A, generator=self.g, device="cuda")).bfloat16() for _ in range(2)]
@@ -121,10 +121,10 @@ class Loop:
         return int(live)
 
 
-@pytest.mark.parametrize("long", [300, 2600])          # of 8 heads: shared reads would save 15 MB, and do save 117 MB
+@pytest.mark.parametrize("long", [300, 5000])          # of 8 heads: shared reads would save 13 MB, and do save 205 MB
 def test_samples_of_two_prompts(native_lib, long):
     short, samples = 37, 12
-    loop = Loop(num_blocks=700, max_rows=32, width=180, seed=1)
+    loop = Loop(num_blocks=700, max_rows=32, width=330, seed=1)
     loop.step([0, 20], [long, short], None, None)                       # both prompts
     loop.fork(0, list(range(1, samples)))
     loop.fork(20, [21, 22])
