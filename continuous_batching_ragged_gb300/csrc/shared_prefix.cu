@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   // sequences.  Where the first sequence, whose table names the blocks, does
   // not hold them, every sequence of the group reads its own.  The groups have
   // to cover the sequences in order.
+  const float key_bytes = 4.0f * HD * float(Hkv);  // K and V of a key
   int bad = 0;
   int64_t saved = 0;                               // keys that are not read again
   for (int g = tid; g < NG; g += kPlanThreads) {
@@ -283,7 +284,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
           int64_t(ctx0) <= int64_t(a.max_blocks_per_seq) * a.block_size) {
         tokens = t1 - t0;
         shared = (p >> block_shift) << block_shift;
-        saved += int64_t(shared) * (s1 - s0 - 1);
+        const float keys = float(shared) * float(s1 - s0 - 1);
+        const float cost = float(ceil_div_fast(tokens, 2 * TT) * Hkv) *
+                           (float((shared + BN - 1) / BN) * (tokens <= TT ? kTileUsOne : kTileUsTwo) + kPieceUs);
+        // many small groups' pieces take longer than the reads that they save
+        // (150 pairs behind 96 keys of 8 heads: 92 us shared, 51 not); chunks are pieces either way
+        if (!chunks && keys * key_bytes * float(w.num_sms) < cost * kBytesPerUs) shared = 0;
+        else saved += int64_t(keys);
       }
     }
     groups[g] = make_int4(s0, t0, tokens, shared);
@@ -293,7 +300,6 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   // Sharing takes the pieces and the join, one after the other: where the bytes
   // that it saves take HBM less time than that, every sequence reads its own
   // table (4 samples behind 512 keys of 8 heads: 25.1 us shared, 17.4 not).
-  const float key_bytes = 4.0f * HD * float(Hkv);  // K and V of a key
   if (float(sum_parts(sums[3])) * key_bytes < kShareUs * kBytesPerUs) {
     for (int g = tid; g < NG; g += kPlanThreads) groups[g].w = 0;
   }

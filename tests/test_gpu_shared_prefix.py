@@ -22,12 +22,13 @@ class Step:
     """Groups of sequences over one pool: [(prefix, [(own keys, query tokens), ...]), ...]; own keys include the query tokens."""
 
     def __init__(self, groups, H, K, B, seed=0, q_scale=1.0, k_slope=0.0, extra_blocks=3, num_blocks=None, width=None,
-                 ballast=True):
+                 ballast=True, force=False):
         from continuous_batching_ragged_gb300 import api
         # a step shares only where that saves some 190 MB: one more group that does, whatever the others are
         self.real = sum(len(members) for _, members in groups)
         if ballast:
-            groups = list(groups) + [(2048, [(1, 1)] * (2 + 200_000_000 // (2048 * 4 * A * K)))]
+            n = 2 + 200_000_000 // (2048 * 4 * A * K)
+            groups = list(groups) + [(2048, [(1, 1)] * max(n, force * (64 // (H // K) + 1)))]
         g = torch.Generator(device="cuda").manual_seed(seed)
         pick = torch.Generator().manual_seed(seed)
         self.H, self.K, self.B, self.groups = H, K, B, groups
@@ -74,6 +75,8 @@ class Step:
         self.cu, self.ctx, self.tables = i32(self.cu_l), i32(self.ctx_l), i32(self.tables_l)
         self.cu_groups, self.prefix = i32(self.cu_groups_l), i32([p for p, _ in groups])
         self.max_q, self.max_ctx, self.scale = max(self.q_l), max(self.ctx_l), 1 / math.sqrt(A)
+        if force:                                  # where there may be chunks, even small groups share
+            self.max_q = max(self.max_q, 64 // (H // K) + 1)
         self.out = torch.full_like(self.q, float("nan"))
         n = api.cb_shared_prefix_workspace_size(self.cache, H, len(seqs), self.cu_l[-1], len(groups), self.max_ctx)
         self.ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")   # contents need no initialisation
@@ -116,20 +119,22 @@ HEADS = [(8, 8, 16), (8, 2, 16), (4, 1, 64), (12, 4, 32), (16, 1, 16), (5, 1, 12
 
 
 @pytest.mark.parametrize("H,K,B", HEADS)
-def test_prefix_lengths(native_lib, H, K, B):
+@pytest.mark.parametrize("force", [False, True])
+def test_prefix_lengths(native_lib, H, K, B, force):
     """Prefixes around blocks and KV tiles, from none to several tiles; suffixes of one key and more."""
     own = [(1, 1), (5, 1), (130, 1)]
-    run_checked([(p, own) for p in (0, 1, B - 1, B, B + 1, 127, 128, 129, 256, 257, 640, 1000)], H, K, B, seed=H + K)
+    run_checked([(p, own) for p in (0, 1, B - 1, B, B + 1, 127, 128, 129, 256, 257, 640, 1000)], H, K, B, seed=H + K, force=force)
 
 
 @pytest.mark.parametrize("H,K,B", HEADS)
-def test_group_sizes(native_lib, H, K, B):
+@pytest.mark.parametrize("force", [False, True])
+def test_group_sizes(native_lib, H, K, B, force):
     """Groups of one sequence to more rows than two tiles hold: the one-tile mode with its
     last rows, exactly one tile, one row more, two tiles, and a third."""
     tt = 128 // (H // K)
     sizes = sorted({1, 2, 3, tt - 1, tt, tt + 1, 2 * tt, 2 * tt + 1} - {0})
     sizes = [n for n in sizes if n <= 257]
-    run_checked([(300, [(1 + i % 7, 1) for i in range(n)]) for n in sizes], H, K, B, seed=50 + H)
+    run_checked([(300, [(1 + i % 7, 1) for i in range(n)]) for n in sizes], H, K, B, seed=50 + H, force=force)
 
 
 @pytest.mark.parametrize("H,K,B", [(8, 8, 16), (8, 2, 32), (16, 2, 16), (12, 4, 64)])
@@ -153,22 +158,25 @@ def test_long_prefix(native_lib, H, K, tokens):
     assert torch.equal(first, st.out)                # the same bits from call to call
 
 
-def test_many_groups(native_lib):
+@pytest.mark.parametrize("force", [False, True])
+def test_many_groups(native_lib, force):
     """More groups than the plan has threads, sizes and prefixes mixed, some empty or without a prefix."""
     g = torch.Generator().manual_seed(3)
     r = lambda a, b: int(torch.randint(a, b + 1, (1,), generator=g))  # noqa: E731
     groups = [(r(0, 400) if i % 5 else 0, [(r(1, 60), 1) for _ in range(r(0, 4))]) for i in range(300)]
-    run_checked(groups, 8, 2, 16, seed=4)
+    run_checked(groups, 8, 2, 16, seed=4, force=force)
 
 
-def test_growing_scores(native_lib):
+@pytest.mark.parametrize("force", [False, True])
+def test_growing_scores(native_lib, force):
     """The running maximum is overtaken again and again, in the prefix and behind it."""
-    run_checked([(900, [(40, 1), (300, 1), (70, 30)]), (600, [(2, 1)] * 20)], 8, 2, 16, seed=5, q_scale=0.5, k_slope=0.2)
+    run_checked([(900, [(40, 1), (300, 1), (70, 30)]), (600, [(2, 1)] * 20)], 8, 2, 16, seed=5, q_scale=0.5, k_slope=0.2, force=force)
 
 
-def test_peaked_rows(native_lib):
+@pytest.mark.parametrize("force", [False, True])
+def test_peaked_rows(native_lib, force):
     """Scores of tens: nearly all weight on single keys."""
-    run_checked([(1500, [(3, 1), (200, 1)] * 5)], 8, 8, 16, seed=6, q_scale=8.0)
+    run_checked([(1500, [(3, 1), (200, 1)] * 5)], 8, 8, 16, seed=6, q_scale=8.0, force=force)
 
 
 def test_without_sharing(native_lib):
@@ -194,7 +202,7 @@ def test_infinite_and_nan_keys_of_others(native_lib):
     """NaN and infinities in one group's prefix or one sequence's own keys reach no other."""
     from continuous_batching_ragged_gb300 import api
     groups = [(400, [(9, 1)] * 5), (400, [(9, 1)] * 5)]
-    st = Step(groups, 8, 2, 16, seed=8)
+    st = Step(groups, 8, 2, 16, seed=8, force=True)
     st.cache.k[st.tables_l[0][3], 1] = float("nan")          # group 0, key/value head 1
     st.cache.v[st.tables_l[6][25], 0, 0] = float("inf")      # sequence 6, head 0, a key of its own
     st.run()
@@ -212,7 +220,7 @@ def test_infinite_and_nan_keys_of_others(native_lib):
 def test_bad_metadata(native_lib, fault):
     """What is wrong is reported; sequences that do not depend on it keep their results."""
     from continuous_batching_ragged_gb300 import api, native
-    st = Step([(300, [(5, 1)] * 4), (200, [(8, 1)] * 3), (50, [(40, 1)] * 2)], 8, 2, 16, seed=9)
+    st = Step([(300, [(5, 1)] * 4), (200, [(8, 1)] * 3), (50, [(40, 1)] * 2)], 8, 2, 16, seed=9, force=True)
     good, error, n = range(9), "INVALID", len(st.q_l)
     if fault == "prefix too long":
         st.ctx[5], good = 200, [0, 1, 2, 3, 4, 6, 7, 8]   # its cached keys end before the prefix does
@@ -243,7 +251,7 @@ def test_bad_metadata(native_lib, fault):
 def test_rows_behind_the_step_stay(native_lib):
     """q and out with rows behind the last sequence: the metadata's token count rules, the rest is not written."""
     from continuous_batching_ragged_gb300 import api
-    st = Step([(300, [(5, 1)] * 4)], 8, 2, 16, seed=10)
+    st = Step([(300, [(5, 1)] * 4)], 8, 2, 16, seed=10, force=True)
     rows = len(st.q)
     more = torch.full((7, 8, A), float("nan"), dtype=torch.bfloat16, device="cuda")
     st.q, st.out = torch.cat([st.q, more]), torch.cat([st.out, more])
@@ -259,8 +267,8 @@ def test_captured_and_replayed(native_lib):
     """A captured call replays over new groups, lengths and pages of the same sizes; two graphs share a workspace."""
     from continuous_batching_ragged_gb300 import api
     sizes = dict(width=200, num_blocks=2000)
-    first = Step([(300, [(5, 1)] * 4), (500, [(60, 1)] * 6)], 8, 2, 16, seed=11, **sizes)
-    other = Step([(0, [(9, 1)] * 1), (540, [(25, 1)] * 9)], 8, 2, 16, seed=12, **sizes)
+    first = Step([(300, [(5, 1)] * 4), (500, [(60, 1)] * 6)], 8, 2, 16, seed=11, force=True, **sizes)
+    other = Step([(0, [(9, 1)] * 1), (540, [(25, 1)] * 9)], 8, 2, 16, seed=12, force=True, **sizes)
     for st in (first, other):
         st.max_ctx = 2500
     n = api.cb_shared_prefix_workspace_size(first.cache, 8, len(first.q_l), len(first.q), 3, 2500)
@@ -320,9 +328,10 @@ def test_more_sequences_than_the_plan_caches(native_lib, q):
 
 
 @pytest.mark.parametrize("H,K", [(128, 1), (100, 1), (66, 1), (240, 2)])
-def test_many_query_heads_of_one_key_head(native_lib, H, K):
+@pytest.mark.parametrize("force", [False, True])
+def test_many_query_heads_of_one_key_head(native_lib, H, K, force):
     """One token, or few, fill a row tile: 128 rows, and tiles with rows of no token."""
-    run_checked([(300, [(5, 1)] * 3), (700, [(40, 1), (9, 3)]), (50, [(200, 30)])], H, K, 32, seed=H)
+    run_checked([(300, [(5, 1)] * 3), (700, [(40, 1), (9, 3)]), (50, [(200, 30)] if force else [(200, 1)])], H, K, 32, seed=H, force=force)
 
 
 def test_two_calls_at_once(native_lib):
