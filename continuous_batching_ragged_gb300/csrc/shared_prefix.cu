@@ -1156,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // units to different SMs; the rest is claimed.
   const int others = int(gridDim.x) - with_pieces, warps = others * kStreamWarps;
   stream::run_warp<false>(&tm_k16, &tm_v16, a, w, n_items, base + warp * stream::kStages * stream::kStageBytes, bars,
-                   reinterpret_cast<SuffixItem*>(gsm + kOffOwnSlots) + 2 * warp,
+                          reinterpret_cast<SuffixItem*>(gsm + kOffOwnSlots) + 2 * warp,
                           pieces_first ? -1 : warp * others + int(blockIdx.x) - with_pieces, warps, 2 * warps,
                           stream::SmallStep{});
 }
@@ -1177,9 +1177,10 @@ constexpr int kSmallTokens = 4096;
 // heads, 128 keys: 9.1 us and 8.7 with a join (called one after the other, from the host,
 // 10.8 and 13.7); 192 keys 11.5 and 9.1.  214 of 4 heads, 190 keys: 13.4 and 21.0; 120 of
 // 240 keys 13.8 and 15.2.
-constexpr int kSmallChunkTiles = stream::kStages;   // shortest chunk, all of it in flight at once (2 rows of 320 keys: 8.7 us, 9.1 with one more)
 constexpr int kOneChunkKeysFew = 128, kOneChunkKeysMany = 384;
 constexpr int kManyUnitsPerSm = 2;
+// Shortest chunk: all of it in flight at once (2 rows of 320 keys: 8.7 us, 9.1 with one more tile).
+constexpr int kSmallChunkTiles = stream::kStages;
 constexpr uint32_t kSmallOffBars = stream::kRingBytes, kSmallOffSlots = kSmallOffBars + stream::kBarBytes;
 constexpr uint32_t kSmallSmem = kSmallOffSlots + stream::kSlotBytes + 1024;
 static_assert(kSmallOffSlots % 16 == 0 && kSmallSmem <= 220 * 1024, "shared memory");

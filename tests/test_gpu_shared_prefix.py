@@ -418,7 +418,8 @@ def test_one_long_sequence(native_lib):
     run_checked([(100, [(70_000, 1)])], 16, 16, 16, seed=14, ballast=False)
 
 
-@pytest.mark.parametrize("S,H,K,q,longest", [(3, 8, 8, 1, 128), (3, 8, 8, 1, 129), (90, 8, 4, 1, 384), (90, 8, 4, 1, 385), (50, 16, 8, 9, 300)])
+@pytest.mark.parametrize("S,H,K,q,longest", [(3, 8, 8, 1, 128), (3, 8, 8, 1, 129), (90, 8, 4, 1, 384), (90, 8, 4, 1, 385),
+                                             (50, 16, 8, 9, 300)])
 def test_short_contexts(native_lib, S, H, K, q, longest):
     """Rows of one chunk, which no join follows, on both sides of their lengths."""
     from continuous_batching_ragged_gb300 import api
