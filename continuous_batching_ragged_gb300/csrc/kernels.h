@@ -123,7 +123,8 @@ float decode_rate_for(const AttnArgs& a);
 // behind the kernel launched just before on the same stream; `wait_previous`:
 // the kernel waits for that one to finish before reading the plan (false
 // when it is the prefill kernel, which releases its dependents only after
-// the plan it follows is complete).
+// the plan it follows is complete; the grid
+// then still ends no sooner than that kernel).
 cb_status launch_decode_persistent(const AttnArgs& a, const StepPlan& plan, bool after_previous,
                                    bool wait_previous, cudaStream_t stream);
 
