@@ -300,6 +300,8 @@ def cb_shared_prefix_attention(q: torch.Tensor, cache: KVCache, cu_seqlens_q: to
                     ("cu_groups", cu_groups), ("prefix_lens", prefix_lens)):
         if t.dtype != torch.int32:
             raise ValueError(f"{name} must be int32")
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError("q must be [num_tokens, heads, head_dim] of the cache's head_dim")
     (S,), (num_groups,), (T, heads, _) = context_lens.shape, prefix_lens.shape, q.shape
     if block_tables.dim() != 2 or block_tables.shape[0] != S or cu_seqlens_q.shape[0] != S + 1:
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and cu_seqlens_q [num_seqs + 1]")

@@ -3,8 +3,9 @@ the host, before any CUDA call: no GPU needed."""
 import ctypes
 
 import pytest
+import torch
 
-from continuous_batching_ragged_gb300 import native
+from continuous_batching_ragged_gb300 import api, native
 
 P = 0x10000                          # an aligned address that no refused call reads
 
@@ -132,3 +133,21 @@ def test_shared_prefix_groups_and_workspace(native_lib):
     n = size(ctypes.byref(cache()), 32, 8, 8, 2, 512)
     assert n > native_lib.cb_attention_workspace_size_gqa(ctypes.byref(cache()), 32, 8, 8, 512)
     assert prefix(native_lib, ws=None) == prefix(native_lib, ws_bytes=n - 1) == prefix(native_lib, ws=P + 16) == native.CB_ERR_INVALID
+
+
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+# The binding's own checks come before it asks for CUDA tensors, so host tensors show them.
+@pytest.mark.parametrize("shape", [(2, 8, 64), (2, 8, 256), (2, 8, 127), (2, 1024), (2, 8, 128, 1)])
+def test_shared_prefix_query_shape(shape):
+    """The kernels take rows of the cache's head_dim: q and out of shorter ones would be read and written past their ends."""
+    q, cache = bf16(*shape), api.KVCache(bf16(4, 8, 16, 128), bf16(4, 8, 16, 128))
+    with pytest.raises(ValueError, match="head_dim"):
+        api.cb_shared_prefix_attention(q, cache, i32(0, 1, 2), i32(1, 1), i32(0, 1).view(2, 1), i32(0, 2), i32(0), max_q_len=1,
+                                       max_context_len=16, scale=0.1, out=torch.empty_like(q), workspace=None)
