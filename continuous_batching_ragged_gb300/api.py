@@ -132,6 +132,8 @@ def cb_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slot_
     `dims`, T is the capacity and dims[1] the step's token count."""
     if q.dim() != 3:
         raise ValueError("q must be [num_tokens, heads, head_dim]")
+    if dims is not None and (dims.dtype != torch.int32 or dims.numel() < 2):
+        raise ValueError("dims must be int32 [num_seqs, num_tokens, ...]")
     T, heads, _ = q.shape
     c = cache.c_struct()
     dtype, A = cache.k.dtype, c.head_dim
@@ -139,8 +141,6 @@ def cb_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slot_
         raise ValueError("slot_mapping must be int64 [num_tokens]")
     if positions is not None and (positions.dtype != torch.int32 or positions.numel() != T):
         raise ValueError("positions must be int32 [num_tokens]")
-    if dims is not None and dims.dtype != torch.int32:
-        raise ValueError("dims must be int32")
     max_positions = rot_dim = 0
     if cos_sin is not None:
         if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:

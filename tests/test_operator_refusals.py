@@ -151,3 +151,11 @@ def test_shared_prefix_query_shape(shape):
     with pytest.raises(ValueError, match="head_dim"):
         api.cb_shared_prefix_attention(q, cache, i32(0, 1, 2), i32(1, 1), i32(0, 1).view(2, 1), i32(0, 2), i32(0), max_q_len=1,
                                        max_context_len=16, scale=0.1, out=torch.empty_like(q), workspace=None)
+
+
+@pytest.mark.parametrize("dims", [i32(3), i32(), torch.zeros(4, dtype=torch.int64)])
+def test_norm_rope_dims(dims):
+    """The kernel reads dims[1]: a shorter tensor is refused, as another type is."""
+    q, cache = bf16(2, 8, 128), api.KVCache(bf16(4, 8, 16, 128), bf16(4, 8, 16, 128))
+    with pytest.raises(ValueError, match="dims"):
+        api.cb_norm_rope_append(q, q, q, torch.zeros(2, dtype=torch.int64), cache, q_out=q, dims=dims)
