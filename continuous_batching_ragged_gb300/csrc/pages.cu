@@ -17,6 +17,7 @@ namespace {
 constexpr int kMaxLayers = 128;        // layers per launch; more take several launches
 constexpr int kThreads = 256;
 constexpr int kVec = 8;                // 16-byte loads in flight per thread
+constexpr int kMaxForks = 1 << 16;     // every fork's CTA checks it against all others: so many take 21 ms
 
 // The K and V pools of up to kMaxLayers layers: p[2 * layer] and p[2 * layer + 1].
 struct Pools {
@@ -351,6 +352,7 @@ extern "C" cb_status cb_fork_sequences(const cb_kv_cache* layers, int32_t num_la
   cb_status st = check_layers(who, layers, num_layers, &row_chunks);
   if (st != CB_OK) return st;
   if (num_forks < 0 || table_rows < 0 || max_blocks_per_seq < 0) return cb::fail(CB_ERR_INVALID, "%s: negative size", who);
+  if (num_forks > kMaxForks) return cb::fail(CB_ERR_UNSUPPORTED, "%s: more than %d forks", who, kMaxForks);
   if (num_forks == 0) return CB_OK;
   if (!block_tables || !context_lens || !parents || !children || !new_blocks)
     return cb::fail(CB_ERR_INVALID, "%s: null pointer", who);

@@ -82,6 +82,13 @@ def test_fork_invalid(native_lib, kw):
     assert fork(native_lib, **kw) == native.CB_ERR_INVALID
 
 
+def test_fork_count(native_lib):
+    """Every fork is checked against all others: their number is bounded."""
+    assert fork(native_lib, rows=1 << 18, forks=(1 << 16) + 1) == native.CB_ERR_UNSUPPORTED
+    assert fork(native_lib, rows=1 << 18, forks=(1 << 31) - 1) == native.CB_ERR_UNSUPPORTED
+    assert b"forks" in native_lib.cb_last_error()
+
+
 def test_fork_nothing(native_lib):
     assert fork(native_lib, forks=0, tables=None) == native.CB_OK
 
