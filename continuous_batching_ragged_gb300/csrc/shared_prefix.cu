@@ -212,9 +212,10 @@ struct PlanView {
   const int4* groups;          // (first sequence, first token, tokens, shared keys)
   const int4* seqs;            // (own keys, 0: left out; first token; tokens; group)
   int num_groups, block_shift, group_heads;
+  int stream_rows;             // query rows per key/value head up to which own keys are streamed
 };
-__device__ __forceinline__ bool is_chunk(const int4& q, int G) {
-  return q.x > 0 && q.z > 1 && int64_t(q.z) * G > kMaxStreamRows;
+__device__ __forceinline__ bool is_chunk(const int4& q, const PlanView& v) {
+  return q.x > 0 && q.z > 1 && int64_t(q.z) * v.group_heads > v.stream_rows;
 }
 // Job j: group j's prefix, then sequence (j - num_groups)'s own keys.
 __device__ __noinline__ Job get_job(const PlanView v, int j) {
@@ -223,7 +224,7 @@ __device__ __noinline__ Job get_job(const PlanView v, int j) {
     return Job{gr.w, gr.y, gr.z, gr.x, 0, gr.w};
   }
   const int4 q = v.seqs[j - v.num_groups];
-  if (!is_chunk(q, v.group_heads)) return Job{0, 0, 0, 0, 0, 0};
+  if (!is_chunk(q, v)) return Job{0, 0, 0, 0, 0, 0};
   return Job{q.x, q.y, q.z, j - v.num_groups, v.groups[q.w].w >> v.block_shift, q.x - q.z + 1};
 }
 
@@ -239,14 +240,16 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   const int tid = threadIdx.x;
   const int S = a.num_seqs, T = a.num_tokens, NG = w.num_groups, TT = w.tile_tokens;
   const int H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv, block_shift = __ffs(a.block_size) - 1;
-  const bool chunks = int64_t(a.max_q_len) * G > kMaxStreamRows && a.max_q_len > 1;   // some sequence's own keys may be pieces
+  // no room for chunks' records: a step that has one all the same (others have no token) streams it
+  const int stream_rows = w.piece_rec_cap > 0 ? kMaxStreamRows : 0x7fffffff;
+  const bool chunks = int64_t(a.max_q_len) * G > stream_rows && a.max_q_len > 1;   // some sequence's own keys may be pieces
   const int jobs = NG + (chunks ? S : 0);
   int4* groups = NG <= kGroupCache ? gcache : w.groups;
   int4* seqs = S <= kSeqCache ? scache : w.seqs;
   int* first_piece = jobs <= kJobCache ? p_first : w.first_piece;
   const int* cu = S <= kSeqCache ? m_cu : a.cu_seqlens_q;
   const int* ctx = S <= kSeqCache ? m_ctx : w.context_lens;
-  const PlanView view = {groups, seqs, NG, block_shift, G};
+  const PlanView view = {groups, seqs, NG, block_shift, G, stream_rows};
   if (tid == 0) {
     s_alt = 0;
     s_tiles = 1;
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     seqs[s] = q;
     if (!ok) {
       raise_error(a.err, kErrInvalid);             // left out
-    } else if (is_chunk(q, G)) {
+    } else if (is_chunk(q, view)) {
       n_first += ceil_div_fast(q_len, 2 * TT);
       tiles_max = max(tiles_max, (q.x + BN - 1) / BN);
     } else {
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     if (q.x > 0) {
       gr = groups[q.w];
       if (gr.w > 0) pre = segments(gr.w, longest).x * (gr.z <= TT ? 2 : 1);
-      if (is_chunk(q, G)) {
+      if (is_chunk(q, view)) {
         nch = segments(q.x, longest).x * (q.z <= TT ? 2 : 1);
       } else {
         nch = ceil_div_fast((q.x + stream::kTileKeys - 1) / stream::kTileKeys, Ls);
@@ -1471,7 +1474,7 @@ PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_
   PrefixSizes z;
   z.S = size_t(num_seqs), z.T = size_t(num_tokens), z.NG = size_t(num_groups);
   const size_t G = size_t(num_q_heads / num_kv_heads), rows = z.T * size_t(num_q_heads);
-  const bool chunks = z.T > z.S && (z.T - z.S + 1) * G > size_t(kMaxStreamRows);
+  const bool chunks = z.T > z.S && (z.T - z.S + 1) * G > size_t(kMaxStreamRows);   // where every sequence has a token
   // uncut: groups that share have two sequences or more; chunks are all of their tokens
   const size_t pairs = z.T / (2 * size_t(tile_tokens(int(G))));
   z.pieces = size_t(num_kv_heads) * (pairs + std::min(z.NG, z.S / 2) + 1 + (chunks ? pairs + z.S : 0)) + kExtraPieces;

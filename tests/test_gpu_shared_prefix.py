@@ -434,3 +434,25 @@ def test_short_contexts(native_lib, S, H, K, q, longest):
         api.cb_check_device_errors()
     assert bool(st.out[st.cu_l[1]:st.cu_l[2]].isnan().all())
     st.check([s for s in range(S) if s != 1])
+
+
+def pieces(st):
+    """Pieces that the last call's plan listed; -1 where its CTAs planned the step themselves, without sharing."""
+    return int(st.ws[:4].view(torch.int32))
+
+
+@pytest.mark.parametrize("H,K", [(8, 1), (16, 2)])
+@pytest.mark.parametrize("prefix", [0, 400])
+@pytest.mark.parametrize("ballast", [False, True])
+@pytest.mark.parametrize("singles,empty", [(7, 8), (3, 6)])
+def test_sequences_without_tokens_beside_a_chunk(native_lib, H, K, prefix, ballast, singles, empty):
+    """Sequences that have no row leave room for a chunk among no more tokens than sequences, or hardly more: they are
+    left out and reported, and the others run."""
+    from continuous_batching_ragged_gb300 import api, native
+    chunk = 64 // (H // K) + 1
+    st = Step([(prefix, [(20, chunk)] + [(5 + i, 1) for i in range(singles)] + [(9, 0)] * empty)], H, K, 16, seed=15, ballast=ballast)
+    assert (len(st.q) - len(st.q_l) + 1) * (H // K) <= 64
+    st.run()
+    with pytest.raises(native.CBError, match="INVALID"):
+        api.cb_check_device_errors()
+    st.check([s for s, n in enumerate(st.q_l) if n > 0])
