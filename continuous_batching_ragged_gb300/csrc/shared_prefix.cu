@@ -291,8 +291,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
         const float cost = float(ceil_div_fast(tokens, 2 * TT) * Hkv) *
                            (float((shared + BN - 1) / BN) * (tokens <= TT ? kTileUsOne : kTileUsTwo) + kPieceUs);
         // many small groups' pieces take longer than the reads that they save
-        // (150 pairs behind 96 keys of 8 heads: 92 us shared, 51 not); chunks are pieces either way
-        if (!chunks && keys * key_bytes * float(w.num_sms) < cost * kBytesPerUs) shared = 0;
+        // (150 pairs behind 96 keys of 8 heads: 97 us shared, 50 not); the rows of a
+        // group that can hold a chunk, more query tokens than one a sequence, are pieces either way
+        const int most = tokens - (s1 - s0 - 1);
+        const bool chunk = most > 1 && int64_t(most) * G > stream_rows;
+        if (!chunk && keys * key_bytes * float(w.num_sms) < cost * kBytesPerUs) shared = 0;
         else saved += int64_t(keys);
       }
     }

@@ -456,3 +456,49 @@ def test_sequences_without_tokens_beside_a_chunk(native_lib, H, K, prefix, balla
     with pytest.raises(native.CBError, match="INVALID"):
         api.cb_check_device_errors()
     st.check([s for s, n in enumerate(st.q_l) if n > 0])
+
+
+@pytest.mark.parametrize("chunk", [False, True])
+def test_small_groups_beside_a_chunk_read_their_own(native_lib, chunk):
+    """Pairs whose pieces take longer than the reads they save do not share, whatever the bound on query tokens allows
+    for and whatever chunk runs beside them."""
+    pairs = [(96, [(1 + i % 9, 1), (20, 1)]) for i in range(150)]
+    st = run_checked(pairs + [(0, [(100, 100)] if chunk else [(7, 2)] * 16)], 32, 8, 16, seed=16, force=True)
+    assert 0 < pieces(st) < len(pairs) * 8           # the other group's, and the chunk's
+
+
+@pytest.mark.parametrize("H,K,B", HEADS)
+def test_prefix_lengths_of_groups_with_a_chunk(native_lib, H, K, B):
+    """Prefixes around blocks and KV tiles, whatever sharing them saves: a chunk's rows are pieces either way."""
+    c = 64 // (H // K) + 1
+    prefixes = (0, 1, B - 1, B, B + 1, 127, 128, 129, 256, 257, 640, 1000)
+    st = run_checked([(p, [(1, 1), (c + 3, c), (130, 1)]) for p in prefixes], H, K, B, seed=17 + H + K)
+    assert pieces(st) >= K * (len(prefixes) + sum(p >= B for p in prefixes) + 1)
+
+
+@pytest.mark.parametrize("H,K,B", HEADS)
+def test_sizes_of_groups_with_a_chunk(native_lib, H, K, B):
+    """From the chunk's rows alone behind the prefix to more rows than two tiles hold."""
+    c, tt = 64 // (H // K) + 1, 128 // (H // K)
+    sizes = sorted({c + 1, c + 2, tt - 1, tt, tt + 1, 2 * tt, 2 * tt + 1} - set(range(c + 1)))
+    st = run_checked([(300, [(c, c)] + [(1 + i % 7, 1) for i in range(n - c)]) for n in sizes], H, K, B, seed=18 + H)
+    assert pieces(st) >= K * (2 * len(sizes) + 1)
+
+
+@pytest.mark.parametrize("fault", ["first page", "own page", "length"])
+def test_bad_pages_of_groups_with_a_chunk(native_lib, fault):
+    """A bad page that the whole group reads costs the group, any other its own sequence."""
+    from continuous_batching_ragged_gb300 import api, native
+    st = Step([(300, [(5, 1)] * 2 + [(40, 33)]), (200, [(8, 1)] * 2 + [(50, 17)])], 8, 2, 16, seed=19)
+    good, error = [0, 1, 2], "BOUNDS"
+    if fault == "first page":
+        st.tables[3, 2] = -1
+    elif fault == "own page":
+        st.tables[5, 14], good = st.cache.num_blocks, [0, 1, 2, 3, 4]
+    else:
+        st.ctx[4], good, error = 150, [0, 1, 2, 3, 5], "INVALID"
+    st.run()
+    with pytest.raises(native.CBError, match=error):
+        api.cb_check_device_errors()
+    st.check(good)
+    assert pieces(st) >= 2 * 5
