@@ -35,6 +35,7 @@
 // 200 tokens behind 4096 keys 164 | 220; 4 behind 512 keys 9 | 27.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include <cuda.h>
@@ -256,6 +257,13 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // it may start while the stream's last kernel ends
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // they wait for this grid on the device
+  if (w.max_sharers >= 0 && __ldcg(w.header + 7) != 0) {             // the small step's kernel ran it: nothing to do
+    if (tid == 0) {
+      w.header[0] = w.header[1] = w.header[4] = w.header[6] = 0;
+      w.header[2] = int32_t(w.tag);
+    }
+    return;
+  }
   int g_s0 = 0, g_s1 = 0, g_p = 0;                 // group tid, requested along with the sequences
   if (tid < NG) g_s0 = w.cu_groups[tid], g_s1 = w.cu_groups[tid + 1], g_p = w.prefix_lens[tid];
   if (S <= kSeqCache) {
@@ -1174,6 +1182,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // where sharing would save some bytes, which are in L2 after the first reader: 32
 // sequences behind 1024 keys, 137 MB in all, 20.0 us and 25.1 with sharing; 24 behind
 // 2048, 203 MB, 25.2 and 25.5; 100 behind 1024, 271 MB, 35.8 and 28.2.
+// How many sequences could share depends on the groups that are empty.  Where that
+// decides, this kernel counts them and runs the step or leaves it to the kernels behind
+// it, which have no work in the one case (64 sequences of 1000 keys, a group each, 58 us;
+// 51 without them, 69 by the plan) and are late in the other (200 behind 4096 keys among
+// empty groups 55 us; 51 by the plan alone, 269 here).
 constexpr int kSmallThreads = 32 * kStreamWarps;
 constexpr int kSmallSeqs = kSmallThreads;
 constexpr int kSmallTokens = 4096;
@@ -1230,6 +1243,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   group_p[tid] = p;
   int bad = tid < NG && (s0 < 0 || s1 < s0 || s1 > S || (tid == 0 && s0 != 0) || (tid == NG - 1 && s1 != S));
   bad = __syncthreads_or(bad);
+  if (w.max_sharers >= 0) {
+    const bool leave = S - __syncthreads_count(tid < NG && s1 > s0) > w.max_sharers;   // all but one of each group
+    if (writer && tid == 0) w.header[7] = leave ? 0 : 1;
+    if (leave) return;
+  }
   int g = 0;                                       // the sequence's group: the last that starts at or before it
   for (int hi = NG - 1; g < hi;) {
     const int mid = (g + hi + 1) >> 1;
@@ -1632,24 +1650,30 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   static std::atomic<uint32_t> next_tag{1};
   w.tag = next_tag.fetch_add(1);
 
-  // what sharing could save at most does not pay for it, and no sequence's own keys are pieces
+  // Small: what sharing could save does not pay for it, and no sequence's own keys are pieces.  All sequences but
+  // one of each group could share, at most their whole contexts, and any group but one may be empty.  With at
+  // least two sequences a group, counting all groups misses half of the sharers at most (84 behind 1024 keys
+  // among 41 empty groups 53 us, 28 without those); with fewer, the device counts.
   const int64_t row_tiles = (int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) + kStreamRows - 1) / kStreamRows;
-  const double saved = double(std::max(0, a.num_seqs - num_groups)) * a.max_context_len * a.num_kv_heads * (4.0 * HD) * row_tiles;
-  const bool small = a.num_seqs <= kSmallSeqs && num_groups <= kSmallSeqs && a.num_tokens <= kSmallTokens &&
-                     (a.max_q_len == 1 || int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= kMaxStreamRows) &&
-                     saved < double(kSmallUs) * kBytesPerUs;
+  const double each = double(a.max_context_len) * a.num_kv_heads * (4.0 * HD) * row_tiles;
+  const int sharers = int(std::min(double(kSmallSeqs), std::ceil(double(kSmallUs) * kBytesPerUs / each) - 1.0));
+  const bool fits = a.num_seqs <= kSmallSeqs && num_groups <= kSmallSeqs && a.num_tokens <= kSmallTokens &&
+                    (a.max_q_len == 1 || int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= kMaxStreamRows);
+  const bool maybe = fits && a.num_seqs - num_groups <= sharers;
+  const bool small = maybe && (a.num_seqs - 1 <= sharers || num_groups <= a.num_seqs / 2);
+  const bool both = maybe && !small;
+  w.max_sharers = both ? sharers : -1;
   const bool many = int64_t(a.num_seqs) * a.num_kv_heads >= int64_t(kManyUnitsPerSm) * w.num_sms;
-  const bool one_chunk = small && a.max_context_len <= (many ? kOneChunkKeysMany : kOneChunkKeysFew);
+  const bool one_chunk = maybe && a.max_context_len <= (many ? kOneChunkKeysMany : kOneChunkKeysFew);
   w.min_chunk_tiles = one_chunk ? kOneChunkKeysMany / stream::kTileKeys : kSmallChunkTiles;
-  cb_status st;
-  if (small) {
-    st = launch_small_step(a, w, stream);
-  } else {
+  cb_status st = CB_OK;
+  if (maybe) st = launch_small_step(a, w, stream);
+  if (st == CB_OK && !small) {
     cudaError_t e = launch_kernel(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, a, w);
     if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: plan launch");
     st = launch_prefix_tc(a, w, stream);
   }
-  if (st != CB_OK || one_chunk) return st;
+  if (st != CB_OK || (small && one_chunk)) return st;
   return launch_join(a, w, stream);
 }
 

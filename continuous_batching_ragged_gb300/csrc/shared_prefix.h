@@ -58,6 +58,8 @@ struct PrefixWork {
   int32_t tile_tokens;         // query tokens per row tile of a piece
   int32_t stream_units;        // streamed units that the chunk length aims for
   int32_t min_chunk_tiles;     // shortest chunk of a small step's streams, in 16-key tiles
+  int32_t max_sharers;         // sequences that could share, up to which the small step's kernel runs the step and
+                               // beyond which it leaves it to the plan's behind it; -1: one of them is launched
   int32_t piece_cap, item_cap;
   int64_t prefix_rec_cap;      // records of the prefixes; the own ones follow
   int64_t piece_rec_cap;       // own records of pieces
@@ -66,7 +68,8 @@ struct PrefixWork {
   // in the workspace
   int32_t* header;             // [0] pieces, [1] prefix records per row (stride), [2] call tag, [3] piece
                                // claims, [4] streamed items, [5] unit claims, [6] CTAs that work on
-                               // pieces first (the others go to the streamed units at once)
+                               // pieces first (the others go to the streamed units at once), [7] where both
+                               // are launched: 1 if the small step's kernel runs the step, else 0
   int4* groups;                // [num_groups], [num_seqs], [num_groups + num_seqs]: the plan's own, where
   int4* seqs;                  // they do not fit its shared memory
   int32_t* first_piece;

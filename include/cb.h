@@ -391,6 +391,9 @@ cb_status cb_padded_attention(const void* q, const cb_kv_cache* cache, const int
  *                of every sequence of group g are the same ones.  At most
  *                context_lens[s] - q_len_s for each of them (cached before this
  *                step); any length from 0, whole pages of it are shared work.
+ * Empty groups cost next to nothing, but where at least two sequences come to a group,
+ * all groups count as used in the choice whether to share at all: many empty ones can
+ * then keep a step of up to 400 MB of keys and values from it, at twice the time.
  * Where a step saves enough reads for it, the whole pages of a prefix are read through
  * the table of the group's first sequence, and all else through each sequence's own;
  * so every sequence's table has to name its whole context.  The result is

@@ -502,3 +502,78 @@ def test_bad_pages_of_groups_with_a_chunk(native_lib, fault):
         api.cb_check_device_errors()
     st.check(good)
     assert pieces(st) >= 2 * 5
+
+
+@pytest.mark.parametrize("empty", [25, 200])
+def test_empty_groups_do_not_stop_sharing(native_lib, empty):
+    """Reads that one group saves are saved whatever the number of empty groups around it, captured too."""
+    from continuous_batching_ragged_gb300 import api
+    group = [(2048, [(1 + i % 7, 1) for i in range(26)])]
+    st = run_checked([(0, [])] * (empty // 2) + group + [(0, [])] * (empty - empty // 2), 32, 8, 16, seed=20, ballast=False)
+    assert pieces(st) > 0
+    alone = Step(group, 32, 8, 16, seed=20, ballast=False)
+    assert torch.equal(alone.run(), st.out) and pieces(alone) == pieces(st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st.run()
+    st.out.fill_(float("nan"))
+    graph.replay()
+    api.cb_check_device_errors()
+    assert torch.equal(alone.out, st.out)
+
+
+def test_captured_among_small_and_shared_steps(native_lib):
+    """One captured call over groups that leave the step small, then over one group, then back; rows behind stay."""
+    from continuous_batching_ragged_gb300 import api
+    sizes = dict(width=200, num_blocks=4200, ballast=False)
+    apart = Step([(2000 - 30 * i, [(9 + i, 1)]) for i in range(28)], 32, 8, 16, seed=21, **sizes)
+    shared = Step([(0, [])] * 20 + [(1984, [(30 - i, 1) for i in range(28)])] + [(7, [])] * 7, 32, 8, 16, seed=22, **sizes)
+    assert len(apart.groups) == len(shared.groups) == len(apart.q_l)
+    calls = [{n: getattr(st, n).clone() for n in ("q", "cu", "ctx", "tables", "cu_groups", "prefix")} for st in (apart, shared)]
+    pools = [(st.cache.k.clone(), st.cache.v.clone()) for st in (apart, shared)]
+    run = apart
+    run.max_ctx = 2048
+    run.out = torch.full((31, 32, A), float("nan"), dtype=torch.bfloat16, device="cuda")
+    run.q = torch.cat([run.q, torch.zeros_like(run.q[:3])])
+    n = api.cb_shared_prefix_workspace_size(run.cache, 32, 28, 31, 28, 2048)
+    run.ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    run.run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run.run()
+    for i in (0, 1, 0, 1):
+        for name, t in calls[i].items():
+            getattr(run, name)[:len(t)].copy_(t)
+        run.cache.k.copy_(pools[i][0])
+        run.cache.v.copy_(pools[i][1])
+        run.out.fill_(float("nan"))
+        graph.replay()
+        api.cb_check_device_errors()
+        st = (apart, shared)[i]
+        st.out = run.out
+        st.check()
+        assert bool(run.out[28:].isnan().all()) and (pieces(run) > 0) == (i == 1)
+
+
+@pytest.mark.parametrize("fault", ["prefix too long", "gap", "page", "no query"])
+@pytest.mark.parametrize("shared", [False, True])
+def test_bad_metadata_where_the_groups_decide(native_lib, fault, shared):
+    from continuous_batching_ragged_gb300 import api, native
+    members = [(9 + i, 1) for i in range(30)]
+    groups = [(0, [])] * 29 + [(2000, members)] if shared else [(2000, [m]) for m in members]
+    st = Step(groups, 8, 8, 16, seed=23, ballast=False)
+    good, error = [s for s in range(30) if s != 5], "INVALID"
+    if fault == "prefix too long":
+        st.ctx[5] = 1200
+    elif fault == "gap":
+        st.cu_groups[29], good = 31, []
+    elif fault == "page":
+        st.tables[5, 125], error = st.cache.num_blocks, "BOUNDS"
+    elif fault == "no query":
+        st.cu[6], good = 5, [s for s in range(30) if s not in (5, 6)]
+    st.run()
+    with pytest.raises(native.CBError, match=error):
+        api.cb_check_device_errors()
+    st.check(good)
+    if not good:
+        assert bool(st.out.isnan().all())
