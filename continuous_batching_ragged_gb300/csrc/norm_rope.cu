@@ -9,19 +9,20 @@
 // to the token's cache slot, values to theirs unchanged.  Everything between
 // the load and the one rounding at the store is fp32.
 //
-// Bound by HBM: every row is read once and written once, a few dozen fp32
-// operations per 16 bytes in between, which is near what the SMs can issue in
-// that time.  So a group of LPR lanes holds one row, 16 bytes a lane: the mean is
-// log2(LPR) shuffles, a lane's cosines, sines and weights are the same for every
-// head of its token, and where the whole head turns a lane takes 8 bytes of each
-// half, so that both elements of a pair are its own.  A persistent grid keeps the
-// next token's rows (up to three per lane group) on their way while it works on
-// one; a warp of values only copies.
-// 2048 tokens of 32 + 2 * 32 heads, bf16: 18.2 us, 5.6 TB/s (one row per lane
-// group 42 us; several rows 30; pairs in one lane and the next token in flight 24;
-// values only copied 21.9; three CTAs an SM 18.9).  Back to back it was 20.8 before
-// it could be launched while the kernel in front ends; released to its own
-// successor early, 20.4: that one's CTAs then wait where its own would run.
+// Every row is read once and written once, but with a few dozen fp32 operations per
+// 16 bytes in between it is issue slots (half of them taken) and loads in flight that
+// bound a step of thousands of tokens, before HBM does.  So a group of LPR lanes
+// holds one row, 16 bytes a lane: the mean is log2(LPR) shuffles, a lane's cosines,
+// sines and weights are the same for every head of its token, and where the whole
+// head turns a lane takes 8 bytes of each half, so that both elements of a pair are
+// its own.  A persistent grid keeps the next token's rows (up to three per lane
+// group) on their way while it works on one; a warp of values only copies.
+// 2048 tokens of 32 + 2 * 32 heads, bf16: 21.0 us over several sets of inputs in turn,
+// 4.8 TB/s; 18.5 us on one set, whose writes stay in L2 (57 of its 102 MB pass DRAM).
+// On one set: one row per lane group 42 us; several rows 30; pairs in one lane and the
+// next token in flight 24; values only copied 21.9; three CTAs an SM 18.9.  Back to
+// back it was 20.8 before it could be launched while the kernel in front ends; released
+// to its own successor early, 20.4: that one's CTAs then wait where its own would run.
 #include <algorithm>
 #include <cmath>
 

@@ -78,8 +78,8 @@ __device__ __forceinline__ Fork read_fork(const ForkArgs& a, int f) {
 // checks its fork against all others first: a child row that is also a parent
 // or another fork's child, or a new page that another fork writes or copies
 // from, would make the result depend on who runs first, so such a fork is
-// left out.  What the check reads (parents' rows and lengths) is written by
-// no fork that passes it.
+// left out.  That is quadratic in the forks (kMaxForks).  What the check reads
+// (parents' rows and lengths) is written by no fork that passes it.
 __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs a, const Pools pools) {
   const int f = blockIdx.x;
   grid_dependency_wait();              // it may start while the stream's last kernel ends
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const Compac
   }
 }
 
-constexpr int kMoveCtasPerSm = 3;    // 200 pages of 2 layers: 8.3 us, at 8 CTAs 13.2; large pools alike
+constexpr int kMoveCtasPerSm = 3;    // 200 pages of 2 layers: 8.9 us with the plan, at 8 CTAs 13.0; 10,240 pages 317 and 315
 
 // Moves the pages and rewrites the tables, from the plan's lists.
 __global__ void __launch_bounds__(kThreads) compact_move_kernel(const CompactArgs a, const Pools pools, int first) {

@@ -31,8 +31,8 @@
 //     CTA plans it for itself.
 // Measured (graph replays; behind the bar, with every sequence reading its whole
 // context): 64 sequences behind 2048 keys of 32 heads 75 us | 286; 256 behind 8192
-// keys of 8 heads 129 | 1590; 24 prompts of up to 7 samples 69 | 101; 12 chunks of
-// 200 tokens behind 4096 keys 164 | 220; 4 behind 512 keys 9 | 27.
+// keys of 8 heads 129 to 133 | 1590; 24 prompts of up to 7 samples 69 | 101; 12 chunks
+// of up to 200 tokens behind 4096 keys 164 | 220; 4 behind 512 keys 9 | 27.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -971,8 +971,10 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         const float m_sub = m_use == -INFINITY ? 0.f : m_use;   // scores all -inf so far
         const uint64_t scale2 = f2_pack(sl2, sl2), neg_m2 = f2_pack(-m_sub, -m_sub);
         uint64_t sum2[4] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+        // P over the scores, rounded to bf16 since the tensor core takes it no wider: half a step, 2^-8, of each
+        // weight.  Outputs are off by 0.0023 of 64 bits where their own rounding is 0.0017; the sums stay in fp32.
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {             // P, rounded to bf16 for the tensor core, over the scores
+        for (int c = 0; c < 64; ++c) {
           float x0, x1;
           f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), scale2, neg_m2), x0, x1);
           const float p0 = ex2(x0), p1 = ex2(x1);
@@ -1306,8 +1308,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 // A warp joins kJoinRows query heads of a token at a time and goes on to the next
 // ones a grid further.  The records come from L2: what counts is bytes in flight,
 // so 8 records are requested at once, two of each of four rows or four of each of
-// two, and the next rows' description before them.  76,800 rows of 3 records: 23 us,
-// 5.2 TB/s.  More CTAs an SM leave too few registers for that: the step of 12 prompt
+// two, and the next rows' description before them.  55,040 rows of 3 records: 23 us,
+// 3.7 TB/s of them.  More CTAs an SM leave too few registers for that: the step of 12 prompt
 // chunks takes 166 us with two, 167 with three, 183 with four.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 4;

@@ -275,7 +275,7 @@ __device__ __noinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap
         for (int j = 0; j < 16; ++j) o[j][0] *= f0, o[j][1] *= f0, o[j][2] *= f1, o[j][3] *= f1;
       }
       const float z0 = m0 == -INFINITY ? 0.f : -m0, z1 = m1 == -INFINITY ? 0.f : -m1;   // a row that sees no key yet
-      uint32_t pf[4];                                    // P, rounded to bf16 for the tensor core
+      uint32_t pf[4];                                    // P, rounded to bf16 as in the pieces: half a step of a weight
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const float p0 = ex2(fmaf(s[x][0], sl2, z0)), p1 = ex2(fmaf(s[x][1], sl2, z0));

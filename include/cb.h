@@ -398,7 +398,9 @@ cb_status cb_padded_attention(const void* q, const cb_kv_cache* cache, const int
  * the table of the group's first sequence, and all else through each sequence's own;
  * so every sequence's table has to name its whole context.  The result is
  * cb_ragged_attention_gqa's within fp32 accumulation rounding and the bf16 rounding
- * of P, not bit for bit; it is the same from call to call.
+ * of P, not bit for bit; it is the same from call to call.  As there, a NaN or an
+ * infinity among the values of a chunk's token reaches the chunk's earlier rows, which
+ * weigh it with 0; one among its keys does not.
  * Needs a bf16 cache with head_dim 128, a block size that is a multiple of 16
  * and at most 128 query heads per key/value head (CB_ERR_UNSUPPORTED otherwise).
  * On the device, groups that do not cover the sequences in order leave out the
