@@ -84,6 +84,52 @@ class KVCache:
                                   _DTYPES[self.k.dtype])
 
 
+@dataclasses.dataclass
+class QuantKVCache:
+    """One layer's paged cache in 8 bits: k, v are [num_blocks, H, block_size, A]
+    tensors of float8_e4m3fn, k_scale and v_scale fp32 [num_blocks, H]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    def __post_init__(self):
+        if self.k.shape != self.v.shape or self.k.dim() != 4 or not self.k.dtype == self.v.dtype == torch.float8_e4m3fn:
+            raise ValueError("k and v must be equal-shaped [num_blocks, H, B, A] tensors of float8_e4m3fn")
+        if not self.k_scale.shape == self.v_scale.shape == self.k.shape[:2]:
+            raise ValueError("k_scale and v_scale must be [num_blocks, H]")
+        if not self.k_scale.dtype == self.v_scale.dtype == torch.float32:
+            raise ValueError("k_scale and v_scale must be fp32")
+
+    @classmethod
+    def empty(cls, num_blocks: int, num_heads: int, block_size: int, head_dim: int, device="cuda") -> "QuantKVCache":
+        k, v = (torch.empty((num_blocks, num_heads, block_size, head_dim), dtype=torch.float8_e4m3fn, device=device)
+                for _ in range(2))
+        ks, vs = (torch.empty((num_blocks, num_heads), dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+    @property
+    def num_blocks(self) -> int:
+        return self.k.shape[0]
+
+    @property
+    def num_heads(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def block_size(self) -> int:
+        return self.k.shape[2]
+
+    @property
+    def head_dim(self) -> int:
+        return self.k.shape[3]
+
+    def c_struct(self) -> native.cb_kv_cache_q8:
+        num_blocks, num_heads, block_size, head_dim = self.k.shape
+        return native.cb_kv_cache_q8(_ptr(self.k), _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale), num_blocks,
+                                     block_size, num_heads, head_dim)
+
+
 class KVCacheStack:
     """The caches of a model's layers, all of one shape: the `layers` argument of the
     page operations.  Holds the tensors that the caches have when it is made, and the C
@@ -108,11 +154,11 @@ def cb_append_kv(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.T
                                     ctypes.byref(c), _stream_handle(stream)), "cb_append_kv")
 
 
-def _token_rows(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype):
+def _token_rows(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, of: str = "the cache's dtype"):
     """Pointer and token stride of [T, heads, A] rows whose tokens may be strided
     (parts of one projection)."""
     if t.dtype != dtype or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor of the cache's dtype")
+        raise ValueError(f"{name} must be a CUDA tensor of {of}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}")
     token, head, one = t.stride()
@@ -159,6 +205,50 @@ def cb_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slot_
     check(native.lib().cb_norm_rope_append(a, heads, _ptr(positions), _ptr(slot_mapping), _ptr(dims), T, c, _ptr(q_out),
                                            _stream_handle(stream)), "cb_norm_rope_append")
     return q_out
+
+
+def cb_append_kv_q8(k_new: torch.Tensor, v_new: torch.Tensor, slot_mapping: torch.Tensor, cache: QuantKVCache, *,
+                    dims: Optional[torch.Tensor] = None, stream=None) -> None:
+    """cb_append_kv_q8: cb_append_kv into a cache in 8 bits.  k_new, v_new: [T, H, A]
+    bf16 or fp32, tokens may be strided.  With `dims`, T is the capacity and dims[1]
+    the step's token count."""
+    if dims is not None and (dims.dtype != torch.int32 or dims.numel() < 2):
+        raise ValueError("dims must be int32 [num_seqs, num_tokens, ...]")
+    T = slot_mapping.numel()
+    if slot_mapping.dtype != torch.int64:
+        raise ValueError("slot_mapping must be int64 [num_tokens]")
+    if k_new.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {k_new.dtype}")
+    c = cache.c_struct()
+    shape = (T, c.num_heads, c.head_dim)
+    k_ptr, k_stride = _token_rows(k_new, "k_new", shape, k_new.dtype, "bf16 or fp32")
+    v_ptr, v_stride = _token_rows(v_new, "v_new", shape, k_new.dtype, "k_new's dtype")
+    check(native.lib().cb_append_kv_q8(k_ptr, v_ptr, _DTYPES[k_new.dtype], k_stride, v_stride, _ptr(slot_mapping),
+                                       _ptr(dims), T, c, _stream_handle(stream)), "cb_append_kv_q8")
+
+
+def cb_gather_kv_q8(cache: QuantKVCache, block_tables: torch.Tensor, cu_keys: torch.Tensor, *,
+                    k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor], starts: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """cb_gather_kv_q8: sequence s's cached tokens from starts[s] (0 where not given) on
+    to rows cu_keys[s] .. cu_keys[s+1]-1 of k_out and v_out, [rows, H, A] bf16 or fp32
+    (either may be None)."""
+    for name, t in (("block_tables", block_tables), ("cu_keys", cu_keys), ("starts", starts)):
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+    S = cu_keys.numel() - 1
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or (starts is not None and starts.numel() != S):
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq], cu_keys [num_seqs + 1], starts [num_seqs]")
+    c = cache.c_struct()
+    outs = [t for t in (k_out, v_out) if t is not None]
+    if not outs:
+        return
+    for t in outs:
+        if t.dtype not in _DTYPES or t.dtype != outs[0].dtype or t.shape != (outs[0].shape[0], c.num_heads, c.head_dim):
+            raise ValueError("k_out and v_out must be [rows, H, A] of one dtype, bf16 or fp32")
+    check(native.lib().cb_gather_kv_q8(c, _ptr(block_tables), _ptr(cu_keys), _ptr(starts), S, block_tables.shape[1],
+                                       outs[0].shape[0], _DTYPES[outs[0].dtype], _ptr(k_out), _ptr(v_out),
+                                       _stream_handle(stream)), "cb_gather_kv_q8")
 
 
 def _stack(layers) -> KVCacheStack:
@@ -316,6 +406,47 @@ def cb_shared_prefix_attention(q: torch.Tensor, cache: KVCache, cu_seqlens_q: to
         _ptr(q), heads, cache.c_struct(), _ptr(cu_seqlens_q), _ptr(context_lens), _ptr(block_tables), _ptr(cu_groups),
         _ptr(prefix_lens), num_groups, S, T, block_tables.shape[1], max_q_len, max_context_len, scale, _ptr(out), ws_ptr,
         ws_bytes, _stream_handle(stream)), "cb_shared_prefix_attention")
+    return out
+
+
+def cb_ragged_attention_q8_workspace_size(cache: QuantKVCache, num_q_heads: int, num_seqs: int, num_tokens: int,
+                                          max_context_len: int, num_groups: int = 0) -> int:
+    c = cache.c_struct()
+    return int(native.lib().cb_ragged_attention_q8_workspace_size(ctypes.byref(c), num_q_heads, num_seqs, num_tokens,
+                                                                  num_groups, max_context_len))
+
+
+def cb_ragged_attention_q8(q: torch.Tensor, cache: QuantKVCache, cu_seqlens_q: torch.Tensor,
+                           context_lens: torch.Tensor, block_tables: torch.Tensor, *, max_q_len: int,
+                           max_context_len: int, scale: float, out: torch.Tensor, workspace: Optional[torch.Tensor],
+                           cu_groups: Optional[torch.Tensor] = None, prefix_lens: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """cb_ragged_attention_q8: attention over a cache in 8 bits; q, out [T, heads, A]
+    bf16.  With cu_groups and prefix_lens, as in cb_shared_prefix_attention."""
+    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("context_lens", context_lens), ("block_tables", block_tables),
+                    ("cu_groups", cu_groups), ("prefix_lens", prefix_lens)):
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+    c = cache.c_struct()
+    if q.dim() != 3 or q.shape[2] != c.head_dim:
+        raise ValueError("q must be [num_tokens, heads, head_dim] of the cache's head_dim")
+    (S,), (T, heads, _) = context_lens.shape, q.shape
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or cu_seqlens_q.shape[0] != S + 1:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and cu_seqlens_q [num_seqs + 1]")
+    num_groups = 0
+    if cu_groups is not None or prefix_lens is not None:
+        if cu_groups is None or prefix_lens is None or cu_groups.numel() != prefix_lens.numel() + 1:
+            raise ValueError("cu_groups must be [num_groups + 1], and prefix_lens [num_groups] given with it")
+        num_groups = prefix_lens.numel()
+    if out.shape != q.shape or not out.dtype == q.dtype == torch.bfloat16:
+        raise ValueError("q and out must have one shape and be bf16")
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None and workspace.numel():
+        ws_ptr, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    check(native.lib().cb_ragged_attention_q8(
+        _ptr(q), heads, c, _ptr(cu_seqlens_q), _ptr(context_lens), _ptr(block_tables), _ptr(cu_groups), _ptr(prefix_lens),
+        num_groups, S, T, block_tables.shape[1], max_q_len, max_context_len, scale, _ptr(out), ws_ptr, ws_bytes,
+        _stream_handle(stream)), "cb_ragged_attention_q8")
     return out
 
 

@@ -357,7 +357,7 @@ extern "C" size_t cb_shared_prefix_workspace_size(const cb_kv_cache* cache, int3
       max_context_len < 0)
     return 0;
   return cb::shared_prefix_workspace_bytes(num_q_heads, cache->num_heads, num_seqs, num_tokens, num_groups,
-                                           max_context_len);
+                                           max_context_len, false);
 }
 
 extern "C" cb_status cb_shared_prefix_attention(const void* q, int32_t num_q_heads, const cb_kv_cache* cache,
@@ -391,4 +391,59 @@ extern "C" cb_status cb_shared_prefix_attention(const void* q, int32_t num_q_hea
   if (st != CB_OK || num_seqs == 0) return st;
   return cb::run_shared_prefix(a, cu_groups, prefix_lens, num_groups, workspace,
                                static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+// A cache in 8 bits as the attention's checks and arguments see it.
+cb_kv_cache as_bf16_shape(const cb_kv_cache_q8& c) {
+  return cb_kv_cache{c.k, c.v, c.num_blocks, c.block_size, c.num_heads, c.head_dim, CB_DTYPE_BF16};
+}
+
+}  // namespace
+
+extern "C" size_t cb_ragged_attention_q8_workspace_size(const cb_kv_cache_q8* cache, int32_t num_q_heads, int32_t num_seqs,
+                                                        int32_t num_tokens, int32_t num_groups, int32_t max_context_len) {
+  if (!cache || cache->num_heads < 1 || num_q_heads < 1 || num_q_heads % cache->num_heads != 0 ||
+      num_q_heads / cache->num_heads > kMaxPrefixGroup || num_seqs < 0 || num_tokens < 0 || num_groups < 0 ||
+      max_context_len < 0)
+    return 0;
+  return cb::shared_prefix_workspace_bytes(num_q_heads, cache->num_heads, num_seqs, num_tokens, num_groups, max_context_len,
+                                           true);
+}
+
+extern "C" cb_status cb_ragged_attention_q8(const void* q, int32_t num_q_heads, const cb_kv_cache_q8* cache,
+                                            const int32_t* cu_seqlens_q, const int32_t* context_lens,
+                                            const int32_t* block_tables, const int32_t* cu_groups, const int32_t* prefix_lens,
+                                            int32_t num_groups, int32_t num_seqs, int32_t num_tokens,
+                                            int32_t max_blocks_per_seq, int32_t max_q_len, int32_t max_context_len,
+                                            float scale, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "cb_ragged_attention_q8";
+  if (num_q_heads < 1) return cb::fail(CB_ERR_INVALID, "%s: num_q_heads < 1", who);
+  if (!cache) return cb::fail(CB_ERR_INVALID, "%s: null cache", who);
+  const cb_kv_cache shape = as_bf16_shape(*cache);
+  cb_status st = check_cache(&shape, who);
+  if (st != CB_OK) return st;
+  if (cache->block_size % 16 != 0) return cb::fail(CB_ERR_UNSUPPORTED, "%s: needs a block size multiple of 16", who);
+  if (num_q_heads / cache->num_heads > kMaxPrefixGroup)
+    return cb::fail(CB_ERR_UNSUPPORTED, "%s: more than %d query heads per key/value head", who, kMaxPrefixGroup);
+  if (num_groups < 0) return cb::fail(CB_ERR_INVALID, "%s: negative size", who);
+  if (num_seqs > 0) {
+    if ((num_groups > 0) != (cu_groups != nullptr) || (num_groups > 0) != (prefix_lens != nullptr))
+      return cb::fail(CB_ERR_INVALID, "%s: cu_groups, prefix_lens and num_groups come together", who);
+    if (!cache->k_scale || !cache->v_scale) return cb::fail(CB_ERR_INVALID, "%s: null pointer", who);
+    const size_t need = cb_ragged_attention_q8_workspace_size(cache, num_q_heads, num_seqs, num_tokens, num_groups,
+                                                              max_context_len);
+    if (need > 0 && (!workspace || workspace_bytes < need))   // 0: sizes that the checks below refuse
+      return cb::fail(CB_ERR_INVALID, "%s: workspace too small: %zu bytes given, %zu needed", who, workspace_bytes, need);
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+      return cb::fail(CB_ERR_INVALID, "%s: workspace must be 256-byte aligned", who);
+  }
+  cb::AttnArgs a;
+  st = prepare(who, q, &shape, cu_seqlens_q, context_lens, block_tables, num_seqs, num_tokens, max_blocks_per_seq,
+               max_q_len, max_context_len, scale, out, nullptr, false, a, num_q_heads);
+  if (st != CB_OK || num_seqs == 0) return st;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  return cb::run_shared_prefix(a, cu_groups, prefix_lens, num_groups, workspace, static_cast<cudaStream_t>(stream));
 }

@@ -34,6 +34,9 @@ struct AttnArgs {
   // null.  When set, the four host sizes above are capacities: buffer extents
   // that bound the device values, which only the step plan reads.
   const int32_t* dims = nullptr;
+  // Scales of a cache in 8 bits, [num_blocks][num_kv_heads]; null: the pools are of `dtype`.
+  const float* k_scale = nullptr;
+  const float* v_scale = nullptr;
   // Left padding (cb_padded_attention), or null: the first pad_lens[s] rows
   // of sequence s's chunk are padding, their keys (positions p_s ..
   // p_s + pad - 1) are masked out of every row and their rows are not
@@ -149,8 +152,9 @@ cb_status launch_decode_tc(const AttnArgs& a, const StepPlan& plan, bool after_p
 
 // Steps with shared prefixes (bf16, head_dim 128, block size a multiple of 16,
 // at most 128 query heads per key/value head): the workspace, and the step.
+// num_groups 0 (and cu_groups, prefix_lens null): no sequence shares.  `q8`, a.k_scale: a cache in 8 bits.
 size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
-                                     int32_t num_groups, int32_t max_context_len);
+                                     int32_t num_groups, int32_t max_context_len, bool q8);
 cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
                             void* workspace, cudaStream_t stream);
 

@@ -45,6 +45,7 @@
 #include "runtime.h"
 #include "shared_prefix.h"
 #include "sm100_ptx.cuh"
+#include "quant_stream.cuh"
 #include "suffix_stream.cuh"
 
 namespace cb {
@@ -265,7 +266,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     return;
   }
   int g_s0 = 0, g_s1 = 0, g_p = 0;                 // group tid, requested along with the sequences
-  if (tid < NG) g_s0 = w.cu_groups[tid], g_s1 = w.cu_groups[tid + 1], g_p = w.prefix_lens[tid];
+  auto group = [&](int g) {
+    if (w.cu_groups) g_s0 = w.cu_groups[g], g_s1 = w.cu_groups[g + 1], g_p = w.prefix_lens[g];
+    else g_s1 = S;
+  };
+  if (tid < NG) group(tid);
   if (S <= kSeqCache) {
     for (int i = tid; i <= S; i += kPlanThreads) {
       m_cu[i] = a.cu_seqlens_q[i];
@@ -279,11 +284,11 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   // sequences.  Where the first sequence, whose table names the blocks, does
   // not hold them, every sequence of the group reads its own.  The groups have
   // to cover the sequences in order.
-  const float key_bytes = 4.0f * HD * float(Hkv);  // K and V of a key
+  const float key_bytes = w.key_bytes;
   int bad = 0;
   int64_t saved = 0;                               // keys that are not read again
   for (int g = tid; g < NG; g += kPlanThreads) {
-    if (g != tid) g_s0 = w.cu_groups[g], g_s1 = w.cu_groups[g + 1], g_p = w.prefix_lens[g];
+    if (g != tid) group(g);
     const int s0 = g_s0, s1 = g_s1, p = g_p;
     int t0 = 0, tokens = 0, shared = 0;
     if (s0 < 0 || s1 < s0 || s1 > S || (g == 0 && s0 != 0) || (g == NG - 1 && s1 != S)) {
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   }
   for (int s = tid; s < S && !bad; s += kPlanThreads) {
     const int g = last_at_or_before(&groups[0].x, 4, NG, s);   // empty groups start there too, and come before
-    const int p = w.prefix_lens[g], n = ctx[s], c0 = cu[s], q_len = cu[s + 1] - c0;
+    const int p = w.cu_groups ? w.prefix_lens[g] : 0, n = ctx[s], c0 = cu[s], q_len = cu[s + 1] - c0;
     const bool ok = p >= 0 && q_len >= 1 && c0 >= 0 && c0 + q_len <= T && q_len <= a.max_q_len && n >= q_len &&
                     p <= n - q_len && n <= a.max_context_len && int64_t(n) <= int64_t(a.max_blocks_per_seq) * a.block_size;
     const int4 q = make_int4(ok ? n - groups[g].w : 0, c0, q_len, g);
@@ -1202,7 +1207,8 @@ constexpr int kOneChunkKeysFew = 128, kOneChunkKeysMany = 384;
 constexpr int kManyUnitsPerSm = 2;
 // Shortest chunk: all of it in flight at once (2 rows of 320 keys: 8.7 us, 9.1 with one more tile).
 constexpr int kSmallChunkTiles = stream::kStages;
-constexpr uint32_t kSmallOffBars = stream::kRingBytes, kSmallOffSlots = kSmallOffBars + stream::kBarBytes;
+constexpr uint32_t kSmallOffBars = stream::kRingBytes, kSmallOffSlots = kSmallOffBars + qstream::kBarBytes;
+static_assert(qstream::kRingBytes <= stream::kRingBytes && stream::kBarBytes <= qstream::kBarBytes, "one layout for both");
 constexpr uint32_t kSmallSmem = kSmallOffSlots + stream::kSlotBytes + 1024;
 static_assert(kSmallOffSlots % 16 == 0 && kSmallSmem <= 220 * 1024, "shared memory");
 
@@ -1212,6 +1218,7 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
   return v;
 }
 
+template <bool kQ8>
 __global__ void __launch_bounds__(kSmallThreads, 1)
     small_step_kernel(const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
                       const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
@@ -1223,11 +1230,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   uint8_t* gsm = smem_raw + (base - raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool writer = blockIdx.x == 0;             // of what the join reads, and of the errors
-  const uint32_t bars = base + kSmallOffBars + warp * stream::kStages * 8;
+  constexpr int kStages = kQ8 ? qstream::kStages : stream::kStages;
+  const uint32_t bars = base + kSmallOffBars + warp * kStages * (kQ8 ? 16 : 8);
   const int S = a.num_seqs, T = a.num_tokens, NG = w.num_groups, H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv;
 
   if (lane == 0) {
-    for (int st = 0; st < stream::kStages; ++st) mbar_init(bars + 8 * st, 1);
+    for (int st = 0; st < kStages; ++st) mbar_init(bars + 8 * st, kQ8 ? qstream::kBarArrivals : 1);
     fence_mbar_init();
     if (warp == 0) {
       tma_prefetch_desc(&tm_k16);
@@ -1237,7 +1245,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");   // it may start while the stream's last kernel ends
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int s0 = 0, s1 = 0, p = 0, c0 = 0, q_len = 0, n = 0;
-  if (tid < NG) s0 = w.cu_groups[tid], s1 = w.cu_groups[tid + 1], p = w.prefix_lens[tid];
+  if (tid < NG) {
+    if (w.cu_groups) s0 = w.cu_groups[tid], s1 = w.cu_groups[tid + 1], p = w.prefix_lens[tid];
+    else s1 = S;
+  }
   if (tid < S) c0 = a.cu_seqlens_q[tid], q_len = a.cu_seqlens_q[tid + 1] - c0, n = w.context_lens[tid];
   if (writer)
     for (int t = tid; t < T; t += kSmallThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
@@ -1300,9 +1311,44 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     }
   }
   __syncthreads();
-  stream::run_warp<true>(&tm_k16, &tm_v16, a, w, bad ? 0 : int(all_items), base + warp * stream::kStages * stream::kStageBytes,
-                         bars, reinterpret_cast<SuffixItem*>(gsm + kSmallOffSlots) + 2 * warp,
-                         warp * int(gridDim.x) + int(blockIdx.x), warps, 0, stream::SmallStep{seqs, S, L});
+  SuffixItem* slots = reinterpret_cast<SuffixItem*>(gsm + kSmallOffSlots) + 2 * warp;
+  const int n_items = bad ? 0 : int(all_items), first = warp * int(gridDim.x) + int(blockIdx.x);
+  if constexpr (kQ8)
+    qstream::run_warp<true>(&tm_k16, &tm_v16, a, w, n_items, base + warp * qstream::kStages * qstream::kStageBytes, bars,
+                            reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * kStages), slots, first, warps, 0,
+                            stream::SmallStep{seqs, S, L});
+  else
+    stream::run_warp<true>(&tm_k16, &tm_v16, a, w, n_items, base + warp * stream::kStages * stream::kStageBytes, bars, slots,
+                           first, warps, 0, stream::SmallStep{seqs, S, L});
+}
+
+// The streams of a step over a cache in 8 bits, as the plan lists them.
+__global__ void __launch_bounds__(kSmallThreads, 1)
+    q8_streams_kernel(const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
+                      const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* gsm = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kStages = qstream::kStages;
+  const uint32_t bars = base + kSmallOffBars + warp * kStages * 16;
+  if (lane == 0) {
+    for (int st = 0; st < kStages; ++st) mbar_init(bars + 8 * st, qstream::kBarArrivals);
+    fence_mbar_init();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan has finished
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int n_items = __ldcg(w.header + 4);
+  if (uint32_t(__ldcg(w.header + 2)) != w.tag || n_items < 0 || n_items > w.item_cap) {   // a plan of another call: no work
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, kErrInvalid);
+    n_items = 0;
+  }
+  __syncwarp();
+  const int warps = int(gridDim.x) * kStreamWarps;
+  qstream::run_warp<false>(&tm_k16, &tm_v16, a, w, n_items, base + warp * kStages * qstream::kStageBytes, bars,
+                           reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * kStages),
+                           reinterpret_cast<SuffixItem*>(gsm + kSmallOffSlots) + 2 * warp,
+                           warp * int(gridDim.x) + int(blockIdx.x), warps, 2 * warps, stream::SmallStep{});
 }
 
 // A warp joins kJoinRows query heads of a token at a time and goes on to the next
@@ -1493,11 +1539,11 @@ struct PrefixSizes {
 };
 int tile_tokens(int group_heads) { return BM / group_heads; }
 PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
-                         int32_t max_context_len) {
+                         int32_t max_context_len, bool q8) {
   PrefixSizes z;
-  z.S = size_t(num_seqs), z.T = size_t(num_tokens), z.NG = size_t(num_groups);
+  z.S = size_t(num_seqs), z.T = size_t(num_tokens), z.NG = size_t(std::max(num_groups, 1));
   const size_t G = size_t(num_q_heads / num_kv_heads), rows = z.T * size_t(num_q_heads);
-  const bool chunks = z.T > z.S && (z.T - z.S + 1) * G > size_t(kMaxStreamRows);   // where every sequence has a token
+  const bool chunks = !q8 && z.T > z.S && (z.T - z.S + 1) * G > size_t(kMaxStreamRows);   // where every sequence has a token
   // uncut: groups that share have two sequences or more; chunks are all of their tokens
   const size_t pairs = z.T / (2 * size_t(tile_tokens(int(G))));
   z.pieces = size_t(num_kv_heads) * (pairs + std::min(z.NG, z.S / 2) + 1 + (chunks ? pairs + z.S : 0)) + kExtraPieces;
@@ -1516,8 +1562,8 @@ PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_
 }  // namespace
 
 size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
-                                     int32_t num_groups, int32_t max_context_len) {
-  const PrefixSizes z = prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len);
+                                     int32_t num_groups, int32_t max_context_len, bool q8) {
+  const PrefixSizes z = prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len, q8);
   return 256 + align256(z.NG * 16) + 2 * align256(z.S * 16) + align256((z.NG + z.S) * 4) + align256(z.pieces * sizeof(Piece)) +
          align256(z.items * sizeof(SuffixItem)) + align256(z.T * 16) +
          align256((z.prefix_recs + z.own_recs) * kPrefixRecBytes);
@@ -1531,7 +1577,12 @@ static cb_status encode_pools(const AttnArgs& a, EncodeTiledFn enc, bool tiles16
   for (int v = 0; v < 2 && r == CUDA_SUCCESS; ++v) {
     void* pool = const_cast<void*>(v ? a.v_pool : a.k_pool);
     CUtensorMap* tm = v ? tv : tk;
-    if (tiles16) {                                 // both 64-dim halves of 16 rows at a time, for the streams
+    if (a.k_scale) {                               // 16 rows of a block in 8 bits
+      const cuuint64_t dims[3] = {HD, B, boxes}, strides[2] = {HD, B * HD};
+      const cuuint32_t box[3] = {HD, cuuint32_t(stream::kTileKeys), 1};
+      r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    } else if (tiles16) {                                 // both 64-dim halves of 16 rows at a time, for the streams
       const cuuint64_t dims[4] = {64, B, 2, boxes}, strides[3] = {HD * 2, 128, B * HD * 2};
       const cuuint32_t box[4] = {64, cuuint32_t(stream::kTileKeys), 2, 1};
       r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1554,7 +1605,8 @@ static cb_status allow_shared_memory() {
   std::lock_guard<std::mutex> lock(g_attr_mutex);
   if (g_attr_set[dev]) return CB_OK;
   cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(small_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallSmem));
+  for (auto kernel : {small_step_kernel<false>, small_step_kernel<true>, q8_streams_kernel})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallSmem));
   if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: shared memory attribute");
   g_attr_set[dev] = true;
   return CB_OK;
@@ -1589,7 +1641,19 @@ static cb_status launch_small_step(const AttnArgs& a, const PrefixWork& w, cudaS
   cb_status st = encode_pools(a, enc, true, &tk16, &tv16);
   if (st == CB_OK) st = allow_shared_memory();
   if (st != CB_OK) return st;
-  cudaError_t e = launch_kernel(small_step_kernel, dim3(unsigned(w.num_sms)), dim3(kSmallThreads), kSmallSmem, stream, true,
+  cudaError_t e = launch_kernel(a.k_scale ? small_step_kernel<true> : small_step_kernel<false>, dim3(unsigned(w.num_sms)), dim3(kSmallThreads), kSmallSmem, stream, true,
+                                tk16, tv16, a, w);
+  return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: launch");
+}
+
+static cb_status launch_q8_streams(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return CB_ERR_CUDA;
+  CUtensorMap tk16, tv16;
+  cb_status st = encode_pools(a, enc, true, &tk16, &tv16);
+  if (st == CB_OK) st = allow_shared_memory();
+  if (st != CB_OK) return st;
+  cudaError_t e = launch_kernel(q8_streams_kernel, dim3(unsigned(w.num_sms)), dim3(kSmallThreads), kSmallSmem, stream, true,
                                 tk16, tv16, a, w);
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: launch");
 }
@@ -1616,7 +1680,9 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   NvtxRange nvtx("cb.shared_prefix");
   if (int64_t(a.num_blocks) * a.num_kv_heads >= (int64_t(1) << 31))
     return fail(CB_ERR_UNSUPPORTED, "shared prefixes: num_blocks * num_kv_heads must fit in int32");
-  const PrefixSizes z = prefix_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups, a.max_context_len);
+  const bool q8 = a.k_scale != nullptr;
+  if (q8) cu_groups = prefix_lens = nullptr, num_groups = 0;
+  const PrefixSizes z = prefix_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups, a.max_context_len, q8);
   if (z.pieces > 0x7FFFFFFF || z.items > size_t(0x7FFFFFFF / a.num_kv_heads) || z.prefix_recs > 0x7FFFFFFF ||
       z.own_recs > 0x7FFFFFFF)
     return fail(CB_ERR_UNSUPPORTED, "shared prefixes: too many tokens");
@@ -1624,7 +1690,8 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   w.cu_groups = cu_groups;
   w.prefix_lens = prefix_lens;
   w.context_lens = a.context_lens;
-  w.num_groups = num_groups;
+  w.num_groups = std::max(num_groups, 1);
+  w.key_bytes = 2.0f * HD * float(a.num_kv_heads) * (q8 ? 1.0f : 2.0f);
   w.num_sms = sm_count();
   w.tile_tokens = tile_tokens(a.num_heads / a.num_kv_heads);
   w.stream_units = std::min(w.num_sms, kMaxSms) * kStreamWarps * kUnitsPerWarp;
@@ -1657,12 +1724,12 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   // least two sequences a group, counting all groups misses half of the sharers at most (84 behind 1024 keys
   // among 41 empty groups 53 us, 28 without those); with fewer, the device counts.
   const int64_t row_tiles = (int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) + kStreamRows - 1) / kStreamRows;
-  const double each = double(a.max_context_len) * a.num_kv_heads * (4.0 * HD) * row_tiles;
+  const double each = double(a.max_context_len) * w.key_bytes * row_tiles;
   const int sharers = int(std::min(double(kSmallSeqs), std::ceil(double(kSmallUs) * kBytesPerUs / each) - 1.0));
   const bool fits = a.num_seqs <= kSmallSeqs && num_groups <= kSmallSeqs && a.num_tokens <= kSmallTokens &&
                     (a.max_q_len == 1 || int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= kMaxStreamRows);
-  const bool maybe = fits && a.num_seqs - num_groups <= sharers;
-  const bool small = maybe && (a.num_seqs - 1 <= sharers || num_groups <= a.num_seqs / 2);
+  const bool maybe = fits && (num_groups == 0 || a.num_seqs - num_groups <= sharers);
+  const bool small = maybe && (num_groups == 0 || a.num_seqs - 1 <= sharers || num_groups <= a.num_seqs / 2);
   const bool both = maybe && !small;
   w.max_sharers = both ? sharers : -1;
   const bool many = int64_t(a.num_seqs) * a.num_kv_heads >= int64_t(kManyUnitsPerSm) * w.num_sms;
@@ -1673,7 +1740,7 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   if (st == CB_OK && !small) {
     cudaError_t e = launch_kernel(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, a, w);
     if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: plan launch");
-    st = launch_prefix_tc(a, w, stream);
+    st = q8 ? launch_q8_streams(a, w, stream) : launch_prefix_tc(a, w, stream);
   }
   if (st != CB_OK || (small && one_chunk)) return st;
   return launch_join(a, w, stream);

@@ -50,11 +50,12 @@ struct alignas(16) SuffixItem {
 static_assert(sizeof(SuffixItem) == 48, "item");
 
 struct PrefixWork {
-  const int32_t* cu_groups;    // [num_groups + 1]
+  const int32_t* cu_groups;    // [num_groups + 1]; null: one group of all sequences, with no prefix
   const int32_t* prefix_lens;  // [num_groups]
   const int32_t* context_lens; // [num_seqs], whole
   int32_t num_groups;
   int32_t num_sms;
+  float key_bytes;             // K and V of a key, all key/value heads
   int32_t tile_tokens;         // query tokens per row tile of a piece
   int32_t stream_units;        // streamed units that the chunk length aims for
   int32_t min_chunk_tiles;     // shortest chunk of a small step's streams, in 16-key tiles

@@ -25,6 +25,8 @@ EXPORTS = ("cb_append_kv", "cb_attention_workspace_size", "cb_ragged_attention",
            "cb_decode_attention_noalloc", "cb_padded_attention",
            "cb_shared_prefix_workspace_size", "cb_shared_prefix_attention", "cb_norm_rope_append",
            "cb_fork_sequences", "cb_compact_workspace_size", "cb_compact_blocks",
+           "cb_append_kv_q8", "cb_gather_kv_q8", "cb_ragged_attention_q8",
+           "cb_ragged_attention_q8_workspace_size",
            "cb_scheduler_create", "cb_scheduler_destroy", "cb_add_request", "cb_build_batch",
            "cb_complete_step", "cb_scheduler_stats", "cb_check_device_errors", "cb_last_error",
            "cb_synth_tokens", "cb_synth_fill_cache", "cb_selftest_bounded_wait")
@@ -39,6 +41,12 @@ class cb_kv_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_blocks", ctypes.c_int32),
                 ("block_size", ctypes.c_int32), ("num_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
+class cb_kv_cache_q8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 class cb_norm_rope(ctypes.Structure):
@@ -91,6 +99,7 @@ def lib() -> ctypes.CDLL:
                                   ctypes.c_float, ctypes.c_size_t)
     st = ctypes.c_int
     pcache = ctypes.POINTER(cb_kv_cache)
+    pcache8 = ctypes.POINTER(cb_kv_cache_q8)
     sigs = {
         "cb_append_kv": (st, [vp, vp, vp, i32, pcache, vp]),
         "cb_attention_workspace_size": (sz, [pcache, i32, i32, i32]),
@@ -114,6 +123,11 @@ def lib() -> ctypes.CDLL:
         "cb_fork_sequences": (st, [pcache, i32, vp, vp, i32, i32, vp, vp, vp, i32, vp]),
         "cb_compact_workspace_size": (sz, [i32]),
         "cb_compact_blocks": (st, [pcache, i32, vp, vp, i32, i32, vp, vp, vp, vp, sz, vp]),
+        "cb_append_kv_q8": (st, [vp, vp, ctypes.c_int, i64, i64, vp, vp, i32, pcache8, vp]),
+        "cb_gather_kv_q8": (st, [pcache8, vp, vp, vp, i32, i32, i32, ctypes.c_int, vp, vp, vp]),
+        "cb_ragged_attention_q8_workspace_size": (sz, [pcache8, i32, i32, i32, i32, i32]),
+        "cb_ragged_attention_q8": (st, [vp, i32, pcache8, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, vp, sz,
+                                        vp]),
         "cb_scheduler_create": (st, [ctypes.POINTER(cb_sched_config), ctypes.POINTER(vp)]),
         "cb_scheduler_destroy": (None, [vp]),
         "cb_add_request": (st, [vp, i64, i64, i32, i32]),

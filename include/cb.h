@@ -20,9 +20,10 @@
  *     workspace (cb_attention_workspace_size).
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *     Device work is enqueued on it and the call returns after the launch.
- *   - cb_norm_rope_append, cb_fork_sequences, cb_compact_blocks and
- *     cb_shared_prefix_attention are programmatic dependent launches that wait, on
- *     the device, for the kernel in front of them.  A kernel of the caller's own
+ *   - cb_norm_rope_append, cb_fork_sequences, cb_compact_blocks,
+ *     cb_shared_prefix_attention and the calls on caches in 8 bits (_q8) are
+ *     programmatic dependent launches that wait, on the device, for the kernel in
+ *     front of them.  A kernel of the caller's own
  *     that is launched with programmatic stream serialization in front of them has
  *     to execute griddepcontrol.wait too.
  *   - Errors that can be seen on the host (null pointers, sizes, unsupported
@@ -201,6 +202,79 @@ cb_status cb_compact_blocks(const cb_kv_cache* layers, int32_t num_layers, const
                             const int32_t* context_lens, int32_t num_seqs, int32_t max_blocks_per_seq,
                             int32_t* new_block_tables, int32_t* remap, int32_t* num_live, void* workspace,
                             size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged cache in 8 bits: half the memory, and half the bytes that a decode
+ * step reads.  The pages have no counterpart.
+ *
+ * k and v are pools as in cb_kv_cache, of e4m3 numbers (1 byte each; four
+ * significant bits, 2^-9 to 448).  k_scale and v_scale are device fp32
+ * [num_blocks][num_heads]: the numbers of a block and head stand for
+ * number * scale.  Caller-owned; pools 16-byte aligned.  Blocks need no
+ * initialisation: a block's scale counts once its first slot has been written.
+ * block_size is a power of two up to 1024, head_dim 64, 128 or 256; attention
+ * needs block_size 16 to 128 and head_dim 128.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t num_blocks;
+  int32_t block_size;
+  int32_t num_heads;
+  int32_t head_dim;
+} cb_kv_cache_q8;
+
+/* ---------------------------------------------------------------------------
+ * cb_append_kv_q8 -- cb_append_kv into a cache in 8 bits.
+ *
+ * For each block that gets tokens, each head, and keys and values apart: need is
+ * the least power of two (at least 2^-100) with which the new tokens' largest
+ * magnitude is at most 448 * need.  If the first of the new tokens is the block's
+ * slot 0, its scale becomes need; otherwise the larger of need and what it was,
+ * and where that grew, the tokens in the slots before the first new one are rounded
+ * anew to it.  A number x becomes the e4m3 number nearest to x / scale, ties to
+ * even: off by at most 2^-4 |x| or 2^-10 scale.  An infinity or a NaN becomes NaN
+ * and does not count for the scale.  Other slots keep their bits.
+ *
+ *   k_new, v_new  device rows of `dtype` (bf16 or f32): token t's num_heads heads of
+ *                 head_dim elements are contiguous from k_new + t * k_stride (strides
+ *                 in elements, multiples of 16 bytes).  16-byte aligned.
+ *   slot_mapping  device int64 [num_tokens], as in cb_append_kv: a negative slot skips
+ *                 the token, one past the pool sets CB_ERR_BOUNDS and skips it.
+ *                 The tokens of one block follow one another, at rising slots; skipped
+ *                 ones may lie between.  (A block whose slots do not rise is left out
+ *                 and sets CB_ERR_INVALID; a block that comes again after tokens of
+ *                 another one gets wrong numbers.)
+ *   dims          NULL, or the device sizes of a planned step: the token count is
+ *                 dims[1] and num_tokens its capacity, as in cb_append_kv_dims.
+ * At most 65,536 tokens a call; head_dim 256 needs bf16 (CB_ERR_UNSUPPORTED otherwise).
+ * ------------------------------------------------------------------------- */
+cb_status cb_append_kv_q8(const void* k_new, const void* v_new, cb_dtype dtype, int64_t k_stride,
+                          int64_t v_stride, const int64_t* slot_mapping, const int32_t* dims, int32_t num_tokens,
+                          const cb_kv_cache_q8* cache, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * cb_gather_kv_q8 -- keys and values read back from a cache in 8 bits, as dense rows.
+ *
+ * Sequence s's tokens starts[s] .. starts[s] + n - 1, n = cu_keys[s + 1] - cu_keys[s],
+ * go to rows cu_keys[s] .. cu_keys[s + 1] - 1 of k_out and v_out: number * scale,
+ * rounded once.
+ *
+ *   block_tables  device int32 [num_seqs][max_blocks_per_seq].
+ *   cu_keys       device int32 [num_seqs + 1], cu_keys[0] = 0, not falling.
+ *   starts        device int32 [num_seqs], or NULL: 0 for every sequence.
+ *   num_rows      rows of the outputs: rows from cu_keys[num_seqs] on are left as they
+ *                 were, and nothing is written past num_rows.
+ *   k_out, v_out  device [num_rows][num_heads][head_dim] of `dtype` (bf16 or f32),
+ *                 16-byte aligned; either may be NULL: not wanted.
+ * A row whose position lies outside its table, or whose start is negative, sets
+ * CB_ERR_INVALID, one whose block is outside the pool CB_ERR_BOUNDS; it is left as it was.
+ * ------------------------------------------------------------------------- */
+cb_status cb_gather_kv_q8(const cb_kv_cache_q8* cache, const int32_t* block_tables, const int32_t* cu_keys,
+                          const int32_t* starts, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_rows,
+                          cb_dtype dtype, void* k_out, void* v_out, void* stream);
 
 /* ---------------------------------------------------------------------------
  * cb_ragged_attention -- attention of one packed, padding-free step.
@@ -420,6 +494,38 @@ cb_status cb_shared_prefix_attention(const void* q, int32_t num_q_heads, const c
                                      int32_t num_tokens, int32_t max_blocks_per_seq, int32_t max_q_len,
                                      int32_t max_context_len, float scale, void* out, void* workspace,
                                      size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * cb_ragged_attention_q8 -- attention of one packed step over a cache in 8 bits:
+ * decode rows, prompt chunks, grouped heads, and shared prefixes.
+ * The pages have no counterpart.
+ *
+ * Same arguments and result as cb_ragged_attention_gqa, with keys and values
+ * number * scale; q and out are bf16.  K and V go to the tensor cores as they are,
+ * exact; the scales multiply scores and weights in fp32.
+ *   cu_groups, prefix_lens, num_groups  as in cb_shared_prefix_attention, or NULL, NULL
+ *                 and 0: nothing is shared.  The whole blocks of a prefix have to hold
+ *                 the same numbers for every sequence of its group, scales among them;
+ *                 its last, partial block is read through each sequence's own table.
+ * The result is the same from call to call.  As in cb_ragged_attention, a NaN among
+ * the values of a chunk's token reaches the chunk's earlier rows; one among its
+ * keys does not.
+ * Needs head_dim 128, a block size of 16, 32, 64 or 128 and at most 128 query
+ * heads per key/value head (CB_ERR_UNSUPPORTED otherwise).  Errors on the device
+ * are cb_shared_prefix_attention's.
+ * The workspace must be cb_ragged_attention_q8_workspace_size bytes (0: arguments that
+ * are not supported), 256-byte aligned; concurrent calls must not share it.
+ * The launches' shapes depend on the host arguments alone, so a call can be
+ * captured in a graph and replayed with new metadata of the same sizes.
+ * ------------------------------------------------------------------------- */
+size_t cb_ragged_attention_q8_workspace_size(const cb_kv_cache_q8* cache, int32_t num_q_heads, int32_t num_seqs,
+                                             int32_t num_tokens, int32_t num_groups, int32_t max_context_len);
+cb_status cb_ragged_attention_q8(const void* q, int32_t num_q_heads, const cb_kv_cache_q8* cache,
+                                 const int32_t* cu_seqlens_q, const int32_t* context_lens,
+                                 const int32_t* block_tables, const int32_t* cu_groups, const int32_t* prefix_lens,
+                                 int32_t num_groups, int32_t num_seqs, int32_t num_tokens,
+                                 int32_t max_blocks_per_seq, int32_t max_q_len, int32_t max_context_len,
+                                 float scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * cb_decode_attention_noalloc -- decode attention that allocates nothing.

@@ -1,0 +1,346 @@
+"""cb_append_kv_q8 and cb_gather_kv_q8 against their rules restated in 64 bits.
+
+Scales are powers of two, so dividing by one is exact and each number is rounded
+once, to the nearest e4m3 number: the comparisons of e4m3 numbers and scales are
+exact.  What is read back is number * scale, exact in fp32 (four significant bits)
+and in bf16, wherever the scale is a power of two; with other scales, rounded once."""
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def grid(x):
+    """The nearest e4m3 numbers to 64-bit numbers of magnitude up to 448, ties to even; NaN for what is not finite."""
+    m, e = torch.frexp(x.abs().clamp(min=2.0 ** -6))
+    step = torch.ldexp(torch.ones_like(m), e - 4)
+    y = torch.round(x / step) * step
+    return torch.where(torch.isfinite(x), y, float("nan"))
+
+
+def need(amax):
+    """The least power of two, 2^-100 or more, with amax <= 448 of it."""
+    e = -100
+    while amax > 448 * 2.0 ** e:
+        e += 1
+    return 2.0 ** e
+
+
+def append_plain(new, slots, q, scale):
+    """One token run after the other; q, scale: 64-bit copies, written in place."""
+    B = q.shape[2]
+    runs = []
+    for t, s in enumerate(slots):
+        if s < 0 or s >= q.shape[0] * B:
+            continue
+        if runs and runs[-1][0] == s // B:
+            runs[-1][1].append((t, s % B))
+        else:
+            runs.append((s // B, [(t, s % B)]))
+    for page, toks in runs:
+        first = toks[0][1]
+        for h in range(q.shape[1]):
+            x = new[[t for t, _ in toks], h]
+            fine = x[torch.isfinite(x)].abs()
+            s = need(float(fine.max()) if fine.numel() else 0.0)
+            if first > 0:
+                s = max(s, float(scale[page, h]))
+                if s > float(scale[page, h]):
+                    q[page, h, :first] = grid(q[page, h, :first] * float(scale[page, h]) / s)
+            scale[page, h] = s
+            for (t, o), row in zip(toks, x):
+                q[page, h, o] = grid(row / s)
+
+
+def same(a, b):
+    """Equal numbers, NaN where NaN."""
+    a, b = a.double().cpu(), b.double().cpu()
+    return bool(((a == b) | (a.isnan() & b.isnan())).all())
+
+
+class Pool:
+    def __init__(self, blocks, K, B, A, seed=0):
+        from continuous_batching_ragged_gb300 import api
+        g = torch.Generator().manual_seed(seed)
+        self.k, self.v = (torch.randn((blocks, K, B, A), generator=g).mul(60).clamp(-448, 448).to(E4M3).cuda() for _ in range(2))
+        self.ks, self.vs = (torch.exp2(torch.randint(-9, -5, (blocks, K), generator=g).float()).cuda() for _ in range(2))
+        self.cache = api.QuantKVCache(self.k, self.v, self.ks, self.vs)
+        self.want = [x.double().cpu() for x in (self.k, self.v, self.ks, self.vs)]
+
+    def append(self, k, v, slots, **kw):
+        from continuous_batching_ragged_gb300 import api
+        api.cb_append_kv_q8(k, v, torch.tensor(slots, dtype=torch.int64, device="cuda"), self.cache, **kw)
+
+    def plain(self, k, v, slots):
+        wk, wv, ws, wt = self.want
+        append_plain(k.double().cpu(), slots, wk, ws)
+        append_plain(v.double().cpu(), slots, wv, wt)
+
+    def check(self):
+        for name, got, want in zip(("k", "v", "k_scale", "v_scale"), (self.k, self.v, self.ks, self.vs), self.want):
+            assert same(got, want), name
+
+
+def rows(T, K, A, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((T, K, A), generator=g) * scale
+    return (x * torch.exp2(4 * torch.rand((T, K, 1), generator=g) - 2)).to(DT[dtype]).cuda()
+
+
+def chunk_slots(page_ids, B, start, n):
+    return [page_ids[j // B] * B + j % B for j in range(start, start + n)]
+
+
+SHAPES = [(1, 16, 128, "bf16"), (8, 16, 128, "bf16"), (3, 32, 64, "bf16"), (5, 8, 256, "bf16"), (4, 64, 64, "f32"), (2, 128, 128, "f32"),
+          (32, 16, 128, "bf16"), (3, 1, 128, "bf16"), (2, 256, 64, "bf16")]
+
+
+@pytest.mark.parametrize("K,B,A,dtype", SHAPES)
+def test_append(native_lib, K, B, A, dtype):
+    """Decode rows at every kind of place in a page, and chunks that begin and end inside pages, begin one, fill one,
+    and span several; skipped tokens between; numbers of widely different size."""
+    from continuous_batching_ragged_gb300 import api
+    n = 3 * B + 3
+    p = Pool(40, K, B, A)
+    ids = torch.randperm(40, generator=torch.Generator().manual_seed(1)).tolist()
+    slots = [ids[0] * B, ids[1] * B + B - 1, ids[2] * B + B // 2]                      # decode rows
+    slots += chunk_slots(ids[20:30], B, B // 3, n)
+    slots += [-1, -1]
+    slots += chunk_slots(ids[8:12], B, 0, B)
+    slots += chunk_slots(ids[12:14], B, B - 1, 1)
+    tail = chunk_slots(ids[14:20], B, 0, 2 * B + 1)
+    tail[len(tail) // 2] = -1                                                          # a token that is not cached, inside a page
+    slots += tail + [-5]
+    k, v = (rows(len(slots), K, A, dtype, s) for s in (2, 3))
+    p.append(k, v, slots)
+    api.cb_check_device_errors()
+    p.plain(k, v, slots)
+    p.check()
+
+
+@pytest.mark.parametrize("growth", [0.25, 1.0, 3.0, 100.0])
+def test_token_by_token(native_lib, growth):
+    """A page filled one token a call, the tokens shrinking, alike and growing: scales that stay and that grow at every token."""
+    from continuous_batching_ragged_gb300 import api
+    K, B, A = 4, 16, 128
+    p = Pool(5, K, B, A, seed=4)
+    slots = chunk_slots([3, 0, 4], B, 0, 35)
+    for i, s in enumerate(slots):
+        k, v = (rows(1, K, A, "bf16", 10 + 2 * i + j, growth ** (i % 16)) for j in range(2))
+        p.append(k, v, [s])
+        p.plain(k, v, [s])
+    api.cb_check_device_errors()
+    p.check()
+
+
+def test_scale_borders(native_lib):
+    """Largest numbers just below, at and above 448 of a power of two, zeros, the smallest and the largest numbers of bf16."""
+    from continuous_batching_ragged_gb300 import api
+    K, B, A = 1, 16, 64
+    tops = [0.0, 3.5, 3.515625, 3.484375, 448.0, 450.0, 1.75, 2.0, 2.0 ** -126, 2.0 ** -133, 3e38, 1.1 * 2.0 ** -92, 1.75 * 2.0 ** -92, 1e-20]
+    p = Pool(len(tops), K, B, A)
+    x = rows(len(tops), K, A, "bf16", 5).clamp(-1, 1)
+    x *= torch.tensor(tops, device="cuda")[:, None, None].bfloat16()
+    x[:, :, 7] = torch.tensor(tops, device="cuda")[:, None].bfloat16()
+    slots = [i * B for i in range(len(tops))]
+    p.append(x, -x, slots)
+    api.cb_check_device_errors()
+    p.plain(x, -x, slots)
+    p.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_not_finite(native_lib, dtype):
+    """Infinities and NaN become NaN, spare the scale, and stay NaN when the page is scaled anew; a row of nothing else too."""
+    from continuous_batching_ragged_gb300 import api
+    K, B, A = 2, 16, 64
+    p = Pool(4, K, B, A)
+    k, v = (rows(6, K, A, dtype, s) for s in (6, 7))
+    k[0, 0, 5], k[0, 1, 6], k[1, 0, 7], v[2, 0] = math.inf, -math.inf, math.nan, math.inf
+    slots = [0, 1, 2, 16, 17, 40]
+    for a, b in ((0, 4), (4, 6)):
+        p.append(k[a:b], v[a:b], slots[a:b])
+        p.plain(k[a:b], v[a:b], slots[a:b])
+    big = rows(1, K, A, dtype, 8, 1e4)
+    p.append(big, big, [3])
+    p.plain(big, big, [3])
+    api.cb_check_device_errors()
+    p.check()
+    assert bool(p.k[0, 0, 0, 5].float().isnan()) and bool(p.v[0, 0, 2].float().isnan().all())
+
+
+@pytest.mark.parametrize("T,dtype", [(300, "bf16"), (2500, "f32")])
+def test_strided_tokens_and_many(native_lib, T, dtype):
+    """Parts of one projection's output; more tokens than a CTA has threads, decode rows behind a long gap of skipped tokens."""
+    from continuous_batching_ragged_gb300 import api
+    K, B, A = 3, 16, 64
+    p = Pool(T // B + 70, K, B, A, seed=9)
+    ids = torch.randperm(T // B + 70, generator=torch.Generator().manual_seed(2)).tolist()
+    qkv = rows(T, 5 * K, A, dtype, 11)
+    k, v = qkv[:, 3 * K:4 * K], qkv[:, 4 * K:]
+    gap = T // 2
+    slots = chunk_slots(ids[:T // B + 2], B, 5, T - gap - 40) + [-1] * gap + [i * B + 3 for i in ids[-40:]]
+    p.append(k, v, slots)
+    api.cb_check_device_errors()
+    p.plain(k, v, slots)
+    p.check()
+
+
+def test_bad_slots(native_lib):
+    """Slots past the pool are skipped, slots that fall or repeat leave their page as it was; the others are written."""
+    from continuous_batching_ragged_gb300 import api, native
+    K, B, A = 2, 16, 128
+    p = Pool(6, K, B, A)
+    slots = [5, 6, 6 * 16, 7, 16 + 4, 16 + 4, 2 * 16 + 9, 2 * 16 + 8, 1 << 40, 3 * 16]
+    k, v = (rows(len(slots), K, A, "bf16", s) for s in (12, 13))
+    p.append(k, v, slots)
+    with pytest.raises(native.CBError) as e:
+        api.cb_check_device_errors()
+    assert e.value.status == native.CB_ERR_BOUNDS
+    good = [s if i in (0, 1, 3, 9) else -1 for i, s in enumerate(slots)]
+    p.plain(k, v, good)
+    p.check()
+    p.append(k[4:6], v[4:6], slots[4:6])
+    with pytest.raises(native.CBError) as e:
+        api.cb_check_device_errors()
+    assert e.value.status == native.CB_ERR_INVALID
+    p.check()
+
+
+def test_dims(native_lib):
+    """The token count on the device: fewer, none, and more than the capacity."""
+    from continuous_batching_ragged_gb300 import api, native
+    K, B, A = 2, 16, 128
+    p = Pool(6, K, B, A)
+    k, v = (rows(20, K, A, "bf16", s) for s in (14, 15))
+    slots = chunk_slots([4, 2], B, 3, 20)
+    for n in (7, 0, 20):
+        p.append(k, v, slots, dims=torch.tensor([1, n, 1, 1], dtype=torch.int32, device="cuda"))
+        p.plain(k[:n], v[:n], slots[:n])
+        api.cb_check_device_errors()
+        p.check()
+    p.append(k, v, slots, dims=torch.tensor([1, 21, 1, 1], dtype=torch.int32, device="cuda"))
+    with pytest.raises(native.CBError):
+        api.cb_check_device_errors()
+    p.check()
+
+
+def gather_plain(p, tables, cu, starts, total):
+    q = [(p.k.double() * p.ks.double()[..., None, None]).cpu(), (p.v.double() * p.vs.double()[..., None, None]).cpu()]
+    B = p.k.shape[2]
+    out = [torch.full((total, p.k.shape[1], p.k.shape[3]), float("nan"), dtype=torch.float64) for _ in range(2)]
+    for s in range(len(tables)):
+        for r in range(cu[s], cu[s + 1]):
+            pos = starts[s] + r - cu[s]
+            for o, x in zip(out, q):
+                o[r] = x[tables[s][pos // B], :, pos % B]
+    return out
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("K,B,A,dtype", [(1, 16, 128, "bf16"), (8, 16, 128, "f32"), (3, 32, 64, "bf16"), (32, 1, 256, "bf16"), (2, 256, 64, "f32")])
+@pytest.mark.parametrize("with_starts", [False, True])
+def test_gather(native_lib, K, B, A, dtype, with_starts):
+    """Sequences of no, one and many keys, from inside pages on; rows behind the last sequence stay."""
+    from continuous_batching_ragged_gb300 import api
+    p = Pool(60, K, B, A, seed=20)
+    n = [0, 1, B, B + 1, 2 * B - 1, 0, 5]
+    starts = [0, 1, B // 2, 0, B - 1, 3, B] if with_starts else [0] * 7
+    perm = torch.randperm(60, generator=torch.Generator().manual_seed(3)).tolist()
+    tables = [perm[6 * s:6 * s + 6] + [-1] for s in range(7)]
+    cu = [0]
+    for x in n:
+        cu.append(cu[-1] + x)
+    k, v = (torch.full((cu[-1] + 3, K, A), float("nan"), dtype=DT[dtype], device="cuda") for _ in range(2))
+    api.cb_gather_kv_q8(p.cache, ints(tables), ints(cu), k_out=k, v_out=v, starts=ints(starts) if with_starts else None)
+    api.cb_check_device_errors()
+    for got, want in zip((k, v), gather_plain(p, tables, cu, starts, cu[-1] + 3)):
+        assert same(got, want)
+    again = torch.full_like(v, float("nan"))
+    api.cb_gather_kv_q8(p.cache, ints(tables), ints(cu), k_out=None, v_out=again, starts=ints(starts) if with_starts else None)
+    assert same(again, v)
+
+
+def test_gather_other_scales(native_lib):
+    """Scales that are no powers of two: the product is rounded once."""
+    from continuous_batching_ragged_gb300 import api
+    p = Pool(4, 2, 16, 128, seed=21)
+    p.ks.copy_(torch.rand(4, 2) + 0.1)
+    k = torch.empty((40, 2, 128), dtype=torch.bfloat16, device="cuda")
+    api.cb_gather_kv_q8(p.cache, ints([[2, 0, 3]]), ints([0, 40]), k_out=k, v_out=None)
+    want = gather_plain(p, [[2, 0, 3]], [0, 40], [0], 40)[0]
+    assert same(k, want.to(torch.bfloat16))          # the product of 4 and 24 bits is exact in 64
+
+
+def test_gather_bad_metadata(native_lib):
+    """Rows outside their table or with a negative start, and pages outside the pool, are left as they were and reported;
+    rows past the outputs are not written."""
+    from continuous_batching_ragged_gb300 import api, native
+    p = Pool(8, 2, 16, 64, seed=22)
+
+    def run(tables, cu, starts, rows_, status):
+        k = torch.full((rows_, 2, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+        api.cb_gather_kv_q8(p.cache, ints(tables), ints(cu), k_out=k, v_out=None, starts=ints(starts))
+        if status is None:
+            api.cb_check_device_errors()
+        else:
+            with pytest.raises(native.CBError) as e:
+                api.cb_check_device_errors()
+            assert e.value.status == status
+        return k
+
+    a = run([[1, 9], [3, 4]], [0, 20, 40], [0, 0], 40, native.CB_ERR_BOUNDS)
+    want = gather_plain(p, [[1, 1], [3, 4]], [0, 20, 40], [0, 0], 40)[0]
+    want[16:20] = float("nan")
+    assert same(a, want)
+    a = run([[1, 2], [3, 4]], [0, 20, 40], [-1, 30], 40, native.CB_ERR_INVALID)
+    want = torch.full_like(want, float("nan"))
+    want[20:22] = gather_plain(p, [[1, 2], [3, 4]], [0, 20, 22], [0, 30], 40)[0][20:22]
+    assert same(a, want)
+    a = run([[1, 2], [3, 4]], [0, 20, 40], [0, 0], 25, None)
+    assert same(a, gather_plain(p, [[1, 2], [3, 4]], [0, 20, 25], [0, 0], 25)[0])
+
+
+def test_append_then_gather_on_streams(native_lib):
+    """Calls on a stream of the caller's, one behind the other without a wait between; and captured, replayed over new values."""
+    from continuous_batching_ragged_gb300 import api
+    K, B, A = 4, 16, 128
+    p = Pool(10, K, B, A, seed=23)
+    slots = chunk_slots([7, 2, 5], B, 0, 41)
+    k, v = (rows(41, K, A, "bf16", s) for s in (24, 25))
+    ko, vo = (torch.empty_like(k) for _ in range(2))
+    sl, tables, cu = torch.tensor(slots, device="cuda"), ints([[7, 2, 5]]), ints([0, 41])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def step(stream):
+        api.cb_append_kv_q8(k, v, sl, p.cache, stream=stream)
+        api.cb_gather_kv_q8(p.cache, tables, cu, k_out=ko, v_out=vo, stream=stream)
+
+    step(side)
+    side.synchronize()
+    p.plain(k, v, slots)
+    p.check()
+    want = gather_plain(p, [[7, 2, 5]], [0, 41], [0], 41)
+    assert same(ko, want[0]) and same(vo, want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(side)
+    for seed in (30, 31):
+        k.copy_(rows(41, K, A, "bf16", seed, 4.0))
+        v.copy_(rows(41, K, A, "bf16", seed + 5, 0.1))
+        graph.replay()
+        torch.cuda.synchronize()
+        p.plain(k, v, slots)
+        p.check()
+        want = gather_plain(p, [[7, 2, 5]], [0, 41], [0], 41)
+        assert same(ko, want[0]) and same(vo, want[1])
+    api.cb_check_device_errors()
