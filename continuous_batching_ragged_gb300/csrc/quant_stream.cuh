@@ -3,6 +3,12 @@
 //
 // A tile is 16 keys of one block: 2 KB of keys and 2 KB of values by TMA, and the
 // block's two scales by a 4-byte asynchronous copy each, all on the tile's barrier.
+//   * Half the bytes a key leave half the time for its arithmetic: it is latency and
+//     instructions that bound a stream, before HBM does.  So keys and dims are the 16
+//     rows of the matrix steps (m16n8k16), S^T = K Q^T and O^T = V^T P^T, and the query
+//     rows their 8 columns, in NT sets: a key's bytes are converted once for all rows,
+//     and up to 8 rows (a decoding sequence's query heads of one key/value head) take
+//     half the steps, registers and exponentials that 16 would.
 //   * e4m3 numbers are exact in f16, so the matrix steps are f16's.  A query row is
 //     scaled by a power of two that brings its largest number to 2^13 .. 2^14: its
 //     bf16 numbers are then exact in f16 down to 2^-27 of that, and off by at most
@@ -10,8 +16,8 @@
 //   * ldmatrix moves pairs of bytes as its 16-bit numbers.  For the scores a lane
 //     gets four neighbouring dims of its key, and both operands take the dims of a
 //     step in that order; for the output it gets two dims of two keys, one byte
-//     permutation makes them two pairs of keys, and even and odd dims are columns of
-//     different tiles.
+//     permutation makes them two pairs of keys, and even and odd dims are the upper
+//     and lower rows of a step.
 //   * A block's key scale multiplies its scores.  Its value scale vs multiplies the
 //     weights, of which the tensor core takes 11 bits and 2^-24 .. 2^16 in f16: so a
 //     row keeps, beside its running maximum m of the scores (exp2 domain), the running
@@ -35,16 +41,25 @@ using stream::pack2;
 using stream::SmallStep;
 using stream::Unit;
 
-constexpr int kStages = 6;
 constexpr uint32_t kBox = kTileKeys * kDim;            // 2 KB, rows of 128 bytes, 128-byte swizzled
 constexpr uint32_t kStageBytes = 2 * kBox;
-constexpr uint32_t kRingBytes = kStreamWarps * kStages * kStageBytes;
-constexpr uint32_t kBarBytes = kStreamWarps * kStages * 16;   // per warp: barriers, then (key, value) scales of each stage
 constexpr int kBarArrivals = 3;                        // of a stage: the copies' bytes, and either scale
 
-__device__ __forceinline__ void tma_load_3d_tile(uint32_t dst, const void* tmap, uint32_t bar, int32_t y, int32_t z) {
-  tma_load_3d(dst, tmap, bar, 0, y, z);
-}
+// Warps of a CTA and tiles in flight of each: as many warps as the registers allow, 192 KB in flight.
+template <int NT>
+struct Shape {
+  static constexpr int kWarps = NT == 1 ? 16 : 8;
+  static constexpr int kStages = NT == 1 ? 3 : 6;
+  static constexpr int kRows = 8 * NT;                 // query rows of a unit, at most
+  static constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
+  static constexpr uint32_t kWarpBarBytes = kStages * 16;   // barriers, then (key, value) scales of each stage
+  static constexpr uint32_t kSlotBytes = kWarps * 2 * sizeof(SuffixItem);
+  static constexpr uint32_t kOffBars = kRingBytes;
+  static constexpr uint32_t kOffSlots = kOffBars + kWarps * kWarpBarBytes;
+  static constexpr uint32_t kSmem = kOffSlots + kSlotBytes + 1024;   // + slack to align the ring
+  static_assert(kOffSlots % 16 == 0 && kSmem <= 220 * 1024, "shared memory");
+};
+
 __device__ __forceinline__ void copy4_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -53,10 +68,16 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
 }
 // D(16 x 8, fp32) += A(16 x 16) B(16 x 8), f16
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Lane (g, t) gives row g, columns 2t and 2t + 1 of an 8 x 8 matrix and gets those of its transpose.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -73,11 +94,12 @@ __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x 
 
 // As stream::run_warp.  `bars`: kStages barriers (initialised for kBarArrivals),
 // then kStages pairs of scales, which `scales` points to.
-template <bool kSmall>
+template <int NT, bool kSmall>
 __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttnArgs& a,
                                          const PrefixWork& w, int n_items, uint32_t ring, uint32_t bars,
                                          const volatile float2* scales, SuffixItem* slots, int first, int step,
                                          int claimed_from, const SmallStep small) {
+  constexpr int kStages = Shape<NT>::kStages, kRows = Shape<NT>::kRows;
   const int lane = threadIdx.x & 31;
   const int H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv, B = a.block_size;
   const int n_units = n_items * Hkv;
@@ -85,16 +107,14 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
   const int g = lane >> 2, t = lane & 3;                 // fragment row and column pair
   const uint32_t scale_at = bars + 8 * kStages;
 
-  // pages of tiles zt .. zt + 31 of the unit in slot `sl`, one per lane
-  auto load_pages = [&](Unit& u, const SuffixItem& it, int zt) {
-    u.zt = zt;
-    u.z = boxes;                                         // out of range: TMA fills zeros
+  // pages of tiles zt .. zt + 31 of a unit, one per lane
+  auto load_pages = [&](const SuffixItem& it, int hk, int n, int zt) -> int {
     const int i = zt + lane;
-    if (i < u.n) {
-      const int blk = a.block_tables[size_t(it.s) * a.max_blocks_per_seq + it.skip + (it.k0 + i * kTileKeys) / B];
-      if (blk >= 0 && blk < a.num_blocks) u.z = blk * Hkv + u.hk;
-      else raise_error(a.err, kErrBounds);
-    }
+    if (i >= n) return boxes;                            // out of range: TMA fills zeros
+    const int blk = a.block_tables[size_t(it.s) * a.max_blocks_per_seq + it.skip + (it.k0 + i * kTileKeys) / B];
+    if (blk >= 0 && blk < a.num_blocks) return blk * Hkv + hk;
+    raise_error(a.err, kErrBounds);
+    return boxes;
   };
   auto load_unit = [&](int idx, Unit& u, SuffixItem& it) {
     u.n = u.hk = u.issued = u.zt = u.z = 0;
@@ -111,7 +131,7 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
         const stream::SmallSeq q = small.seqs[s];
         const int local = item - q.item0, row = local / q.nch, chunk = local - row * q.nch;
         SuffixItem x = {};
-        x.s = s, x.tok0 = q.tok0, x.q_len = q.q_len, x.row0 = 16 * row, x.ctx = q.keys;
+        x.s = s, x.tok0 = q.tok0, x.q_len = q.q_len, x.row0 = kRows * row, x.ctx = q.keys;
         x.k0 = chunk * small.len * kTileKeys;
         x.k1 = x.k0 + min(q.keys - x.k0, small.len * kTileKeys);
         x.rec0 = q.rec0 + chunk, x.rec_step = q.nch, x.direct = q.nch == 1;
@@ -123,31 +143,13 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
     __syncwarp();
     u.hk = idx % Hkv;
     u.n = (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys;
-    load_pages(u, it, 0);
+    u.z = load_pages(it, u.hk, u.n, 0);
   };
   auto claim = [&]() -> int { return lane == 0 ? claimed_from + atomicAdd(w.header + 5, 1) : 0; };
 
   uint32_t issued = 0, consumed = 0;                     // ring positions
-  auto issue = [&](Unit& u, const SuffixItem& it) {
-    const int i = u.issued++;
-    if (i - u.zt >= 32) load_pages(u, it, i);
-    const int z = __shfl_sync(0xffffffffu, u.z, i - u.zt);
-    const int st = issued % kStages;
-    const uint32_t bar = bars + 8 * st;
-    if (lane < 2) {
-      const float* scale = lane == 0 ? a.k_scale : a.v_scale;
-      copy4_async(scale_at + 8 * st + 4 * lane, scale + (z < boxes ? z : 0));
-      copies_arrive(bar);
-    }
-    if (lane == 0) {
-      const uint32_t dst = ring + st * kStageBytes;
-      const int y = (it.k0 + i * kTileKeys) & (B - 1);
-      mbar_arrive_expect_tx(bar, kStageBytes);
-      tma_load_3d_tile(dst, tm_k, bar, y, z);
-      tma_load_3d_tile(dst + kBox, tm_v, bar, y, z);
-    }
-    ++issued;
-  };
+  int st_in = 0, st_out = 0;                             // their stages
+  uint32_t phase = 0;                                    // of st_out
 
   Unit cur, nxt;
   int slot = 0;                                          // of the current unit; the next one's is the other
@@ -162,75 +164,103 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
     load_unit(c0, cur, slots[0]);
     load_unit(c1, nxt, slots[1]);
   }
+  // Requests tiles of the current unit, then of the next, while stages are free.
+  auto top_up = [&]() {
+    while (issued - consumed < uint32_t(kStages)) {
+      const bool ahead = cur.issued >= cur.n;
+      if (ahead && nxt.issued >= nxt.n) break;
+      const SuffixItem& it = slots[slot ^ int(ahead)];
+      const int i = ahead ? nxt.issued : cur.issued;
+      int zt = ahead ? nxt.zt : cur.zt, zs = ahead ? nxt.z : cur.z;
+      if (i - zt >= 32) {
+        zt = i;
+        zs = load_pages(it, ahead ? nxt.hk : cur.hk, ahead ? nxt.n : cur.n, i);
+        if (ahead) nxt.zt = zt, nxt.z = zs;
+        else cur.zt = zt, cur.z = zs;
+      }
+      if (ahead) ++nxt.issued;
+      else ++cur.issued;
+      const int z = __shfl_sync(0xffffffffu, zs, i - zt);
+      const uint32_t bar = bars + 8 * st_in;
+      if (lane < 2) {
+        copy4_async(scale_at + 8 * st_in + 4 * lane, (lane == 0 ? a.k_scale : a.v_scale) + (z < boxes ? z : 0));
+        copies_arrive(bar);
+      }
+      if (lane == 0) {
+        const uint32_t dst = ring + st_in * kStageBytes;
+        const int y = (it.k0 + i * kTileKeys) & (B - 1);
+        mbar_arrive_expect_tx(bar, kStageBytes);
+        tma_load_3d(dst, tm_k, bar, 0, y, z);
+        tma_load_3d(dst + kBox, tm_v, bar, 0, y, z);
+      }
+      ++issued;
+      st_in = st_in + 1 == kStages ? 0 : st_in + 1;
+    }
+  };
   bool ok = true;
-  // this lane's part of an ldmatrix address: matrix mi, its row mr
+  // This lane's row in a tile's ldmatrix: four 8 x 16-byte matrices, of the keys' halves and two chunks of 16 dims; the j-th
+  // pair of chunks is at `part ^ 32 * j`.
   const int mi = lane >> 3, mr = lane & 7;
+  const uint32_t part = ((mi & 1) * 8 + mr) * 128 + (((mi >> 1) ^ mr) << 4);
   while (cur.n > 0) {
     const SuffixItem& it = slots[slot];
-    auto top_up = [&]() {
-      while (issued - consumed < uint32_t(kStages)) {
-        if (cur.issued < cur.n) issue(cur, it);
-        else if (nxt.issued < nxt.n) issue(nxt, slots[slot ^ 1]);
-        else break;
-      }
-    };
     top_up();
     int ahead = n_units;
     if (kSmall) ahead = given = min(given, n_units) + step;
     else if (nxt.n > 0) ahead = claim();                 // for the unit after the next; read at this one's end
-    // The unit's query rows, as A fragments in f16; rows past the sequence's are zero.
-    const int rows = min(16, it.q_len * G - it.row0);
-    uint32_t qf[8][4];
-    float e0, e1;                                        // a score's factor, without its block's scale
-    {
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-      const int r0 = it.row0 + g, r1 = r0 + 8;
-      const __nv_bfloat16* p0 = q + (size_t(it.tok0 + r0 / G) * H + cur.hk * G + r0 % G) * kDim + 4 * t;
-      const __nv_bfloat16* p1 = q + (size_t(it.tok0 + r1 / G) * H + cur.hk * G + r1 % G) * kDim + 4 * t;
-      const bool in0 = g < rows, in1 = g + 8 < rows;
-      uint32_t top0 = 0, top1 = 0;                       // bits of the largest magnitude
+    // The unit's query rows as B fragments in f16 (columns past the sequence's are zero), and of this lane's two
+    // columns per set the factor of a score without its block's scale, and the keys that the row sees: all before
+    // its own token's, and its own.
+    const int rows = min(kRows, it.q_len * G - it.row0);
+    const int k0 = it.k0, k1 = it.k1, ctx = it.ctx, before = ctx - it.q_len;
+    const int lim_all = min(k1, before + it.row0 / G + 1);   // keys that every row sees
+    uint32_t qf[NT][8][2];
+    float ef[NT][2];
+    int lim[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = it.row0 + 8 * n + g;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (size_t(it.tok0 + r / G) * H + cur.hk * G + r % G) * kDim + 4 * t;
+      const bool in = 8 * n + g < rows;
+      uint32_t top = 0;                                  // bits of the largest magnitude
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        const uint2 x = in0 ? *reinterpret_cast<const uint2*>(p0 + 16 * ks) : make_uint2(0, 0);
-        const uint2 y = in1 ? *reinterpret_cast<const uint2*>(p1 + 16 * ks) : make_uint2(0, 0);
-        qf[ks][0] = x.x, qf[ks][1] = y.x, qf[ks][2] = x.y, qf[ks][3] = y.y;
-        top0 = max(max(top0, (x.x << 16) & 0x7fff0000u), max(x.x & 0x7fff0000u, max((x.y << 16) & 0x7fff0000u, x.y & 0x7fff0000u)));
-        top1 = max(max(top1, (y.x << 16) & 0x7fff0000u), max(y.x & 0x7fff0000u, max((y.y << 16) & 0x7fff0000u, y.y & 0x7fff0000u)));
+        const uint2 x = in ? *reinterpret_cast<const uint2*>(src + 16 * ks) : make_uint2(0, 0);
+        qf[n][ks][0] = x.x, qf[n][ks][1] = x.y;
+        top = max(max(top, (x.x << 16) & 0x7fff0000u), max(x.x & 0x7fff0000u, max((x.y << 16) & 0x7fff0000u, x.y & 0x7fff0000u)));
       }
 #pragma unroll
-      for (int x = 1; x <= 2; x <<= 1) {
-        top0 = max(top0, __shfl_xor_sync(0xffffffffu, top0, x));
-        top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, x));
-      }
-      const uint32_t x0 = min(254u, 267u - (top0 >> 23)), x1 = min(254u, 267u - (top1 >> 23));   // 2^13 / largest, as exponents
-      const float f0 = __uint_as_float(x0 << 23), f1 = __uint_as_float(x1 << 23);
-      e0 = a.scale_log2 * __uint_as_float((254u - x0) << 23);
-      e1 = a.scale_log2 * __uint_as_float((254u - x1) << 23);
+      for (int x = 1; x <= 2; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const uint32_t ex = min(254u, 267u - (top >> 23));     // 2^13 / largest, as an exponent
+      const float f = __uint_as_float(ex << 23), back = a.scale_log2 * __uint_as_float((254u - ex) << 23);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        qf[ks][0] = pack_f16(bf16_lo(qf[ks][0]) * f0, bf16_hi(qf[ks][0]) * f0);
-        qf[ks][1] = pack_f16(bf16_lo(qf[ks][1]) * f1, bf16_hi(qf[ks][1]) * f1);
-        qf[ks][2] = pack_f16(bf16_lo(qf[ks][2]) * f0, bf16_hi(qf[ks][2]) * f0);
-        qf[ks][3] = pack_f16(bf16_lo(qf[ks][3]) * f1, bf16_hi(qf[ks][3]) * f1);
+        qf[n][ks][0] = pack_f16(bf16_lo(qf[n][ks][0]) * f, bf16_hi(qf[n][ks][0]) * f);
+        qf[n][ks][1] = pack_f16(bf16_lo(qf[n][ks][1]) * f, bf16_hi(qf[n][ks][1]) * f);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        ef[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e));
+        lim[n][e] = min(k1, before + (it.row0 + 8 * n + 2 * t + e) / G + 1);
       }
     }
-    // keys that a row sees: all before its own token's, and its own
-    const int k0 = it.k0, k1 = it.k1, ctx = it.ctx, before = ctx - it.q_len;
-    const int lim0 = min(k1, before + (it.row0 + g) / G + 1), lim1 = min(k1, before + (it.row0 + g + 8) / G + 1);
-    const int lim_all = min(k1, before + it.row0 / G + 1);   // keys that every row sees
-    float o[16][4];                                      // [2 * chunk of 16 dims + odd dims]
+    float o[NT][8][4];                                   // [chunk of 16 dims]: dim 2g of rows 2t, 2t + 1, dim 2g + 1 of them
+    // of rows 2t and 2t + 1 of each set: m, l, M and 2^(m - M)
+    float m[NT][2], l[NT][2], mw[NT][2], fw[NT][2];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    float w0 = -INFINITY, w1 = -INFINITY, f0 = 1.f, f1 = 1.f;   // M of either row, and 2^(m - M)
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[n][e] = mw[n][e] = -INFINITY, l[n][e] = 0.f, fw[n][e] = 1.f;
+    }
     for (int i = 0; i < cur.n; ++i) {
-      const int st = consumed % kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * st, (consumed / kStages) & 1))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * st_out, phase))) {
         ok = false;
         break;
       }
-      const float ks = scales[st].x, vs = scales[st].y;
-      const uint32_t kt = ring + st * kStageBytes, vt = kt + kBox;
+      const float ks = scales[st_out].x, vs = scales[st_out].y;
+      const uint32_t kt = ring + st_out * kStageBytes, vt = kt + kBox;
       const int kb = k0 + i * kTileKeys;
       if (kb + kTileKeys > ctx) {                        // rows behind the sequence's last key: P is 0, but 0 * NaN is not
         const int from = ctx - kb;
@@ -239,115 +269,118 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
         fence_proxy_async_smem();                        // before the slot's next TMA write
         __syncwarp();
       }
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float s[NT][4];                                    // keys g: rows 2t, 2t + 1; keys 8 + g
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t kf[4];
-          ldmatrix4(kt + (8 * x + mr) * 128 + (((4 * c + mi) ^ mr) << 4), kf);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t kf[4];
+        ldmatrix4(kt + (part ^ (32 * j)), kf);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mma_f16(s[x], qf[4 * c + j], e4m3x2_to_f16x2(kf[j]), e4m3x2_hi_to_f16x2(kf[j]));
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t a0 = e4m3x2_to_f16x2(kf[2 * x]), a1 = e4m3x2_to_f16x2(kf[2 * x + 1]);
+          const uint32_t a2 = e4m3x2_hi_to_f16x2(kf[2 * x]), a3 = e4m3x2_hi_to_f16x2(kf[2 * x + 1]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(s[n], a0, a1, a2, a3, qf[n][2 * j + x][0], qf[n][2 * j + x][1]);
         }
+      }
       if (kb + kTileKeys > lim_all) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int key = kb + 8 * x + 2 * t + e;
-            if (key >= lim0) s[x][e] = -INFINITY;
-            if (key >= lim1) s[x][2 + e] = -INFINITY;
+            if (kb + g >= lim[n][e]) s[n][e] = -INFINITY;
+            if (kb + 8 + g >= lim[n][e]) s[n][2 + e] = -INFINITY;
           }
       }
-      const float a0 = fmaxf(e0 * ks, 1.2e-38f), a1 = fmaxf(e1 * ks, 1.2e-38f);   // not 0: -inf stays
       const float lv = fmaxf(lg2(vs), -126.f);
-      float t0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])) * a0;
-      float t1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3])) * a1;
-      // keep stale maxima while 2^x stays <= 2^8
-      if (__any_sync(0xffffffffu, t0 > m0 + 8.0f || t1 > m1 + 8.0f || t0 + lv > w0 + 8.0f || t1 + lv > w1 + 8.0f)) {
+      float af[NT][2], top[NT][2];
+      bool grown = false;
 #pragma unroll
-        for (int x = 1; x <= 2; x <<= 1) {
-          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
-          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
-        }
-        const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1), v0 = fmaxf(w0, t0 + lv), v1 = fmaxf(w1, t1 + lv);
-        if (n0 != -INFINITY) {
-          l0 *= ex2(m0 - n0);
-          const float x = ex2(w0 - v0);
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j][0] *= x, o[j][1] *= x;
-          f0 = ex2(fminf(n0 - v0, 126.f));
+        for (int e = 0; e < 2; ++e) {
+          af[n][e] = fmaxf(ef[n][e] * ks, 1.2e-38f);     // not 0: -inf stays
+          top[n][e] = fmaxf(s[n][e], s[n][2 + e]) * af[n][e];
+          grown = grown || top[n][e] > m[n][e] + 8.0f || top[n][e] + lv > mw[n][e] + 8.0f;
         }
-        if (n1 != -INFINITY) {
-          l1 *= ex2(m1 - n1);
-          const float x = ex2(w1 - v1);
+      if (__any_sync(0xffffffffu, grown)) {              // stale maxima are kept while 2^x stays <= 2^8
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j][2] *= x, o[j][3] *= x;
-          f1 = ex2(fminf(n1 - v1, 126.f));
-        }
-        m0 = n0, m1 = n1, w0 = v0, w1 = v1;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = top[n][e];
+#pragma unroll
+            for (int d = 4; d <= 16; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            const float to = fmaxf(m[n][e], x), tw = fmaxf(mw[n][e], x + lv);
+            if (to != -INFINITY) {                       // the row has seen a key
+              l[n][e] *= ex2(m[n][e] - to);
+              const float f = ex2(mw[n][e] - tw);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[n][j][e] *= f, o[n][j][2 + e] *= f;
+              fw[n][e] = ex2(fminf(to - tw, 126.f));
+            }
+            m[n][e] = to, mw[n][e] = tw;
+          }
       }
-      const float z0 = m0 == -INFINITY ? 0.f : -m0, z1 = m1 == -INFINITY ? 0.f : -m1;   // a row that sees no key yet
-      const float c0 = fminf(vs * f0, 3e38f), c1 = fminf(vs * f1, 3e38f);
-      uint32_t pf[4];                                    // weights in f16: within 2^-12 of each, 2^-25 of 2^(M - m)
+      uint32_t pf[NT][2];                                // weights in f16: within 2^-11 of each, 2^-25 of 2^(M - m)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float p0 = ex2(fmaf(s[x][0], a0, z0)), p1 = ex2(fmaf(s[x][1], a0, z0));
-        const float p2 = ex2(fmaf(s[x][2], a1, z1)), p3 = ex2(fmaf(s[x][3], a1, z1));
-        l0 += p0 + p1;
-        l1 += p2 + p3;
-        pf[2 * x] = pack_f16(p0 * c0, p1 * c0);
-        pf[2 * x + 1] = pack_f16(p2 * c1, p3 * c1);
+      for (int n = 0; n < NT; ++n) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float z = m[n][e] == -INFINITY ? 0.f : -m[n][e], c = fminf(vs * fw[n][e], 3e38f);
+          const float x = ex2(fmaf(s[n][e], af[n][e], z)), y = ex2(fmaf(s[n][2 + e], af[n][e], z));
+          l[n][e] += x + y;
+          p[e] = x * c, p[2 + e] = y * c;
+        }
+        pf[n][0] = transpose8(pack_f16(p[0], p[1]));
+        pf[n][1] = transpose8(pack_f16(p[2], p[3]));
       }
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
+      for (int j = 0; j < 4; ++j) {
         uint32_t vf[4];
-        ldmatrix4_trans(vt + ((mi & 1) * 8 + mr) * 128 + (((2 * jj + (mi >> 1)) ^ mr) << 4), vf);
+        ldmatrix4_trans(vt + (part ^ (32 * j)), vf);
 #pragma unroll
         for (int x = 0; x < 4; ++x) vf[x] = __byte_perm(vf[x], 0, 0x3120);   // (key, key + 1) of the even dim, of the odd dim
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          mma_f16(o[4 * jj + 2 * x], pf, e4m3x2_to_f16x2(vf[2 * x]), e4m3x2_to_f16x2(vf[2 * x + 1]));
-          mma_f16(o[4 * jj + 2 * x + 1], pf, e4m3x2_hi_to_f16x2(vf[2 * x]), e4m3x2_hi_to_f16x2(vf[2 * x + 1]));
+          const uint32_t a0 = e4m3x2_to_f16x2(vf[2 * x]), a1 = e4m3x2_hi_to_f16x2(vf[2 * x]);
+          const uint32_t a2 = e4m3x2_to_f16x2(vf[2 * x + 1]), a3 = e4m3x2_hi_to_f16x2(vf[2 * x + 1]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * j + x], a0, a1, a2, a3, pf[n][0], pf[n][1]);
         }
       }
       __syncwarp();                                      // every lane has read the slot
       ++consumed;
+      if (++st_out == kStages) st_out = 0, phase ^= 1;
       top_up();
     }
     if (!ok) break;
-#pragma unroll
-    for (int x = 1; x <= 2; x <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, x);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, x);
-    }
     // the rows' records, or, with nothing to join, the rows; o is in units of 2^M, a record's in 2^m
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (g + 8 * half < rows) {
-        const int r = it.row0 + g + 8 * half, tok = r / G, h = cur.hk * G + r % G;
-        const float m = half ? m1 : m0, l = half ? l1 : l0, top = half ? w1 : w0;
-        const float to_m = m == -INFINITY ? 0.f : ex2(top - m);
-        if (it.direct) {
-          const float f = to_m / l;
-          uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (size_t(it.tok0 + tok) * H + h) * kDim) + t;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float *even = &o[2 * j][2 * half], *odd = &o[2 * j + 1][2 * half];
-            dst[4 * j] = make_uint2(pack2(even[0] * f, odd[0] * f), pack2(even[1] * f, odd[1] * f));
-          }
+      for (int e = 0; e < 2; ++e) {
+        float sum = l[n][e];
+#pragma unroll
+        for (int d = 4; d <= 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (8 * n + 2 * t + e >= rows) continue;
+        const int r = it.row0 + 8 * n + 2 * t + e, tok = r / G, h = cur.hk * G + r % G;
+        const float to_m = m[n][e] == -INFINITY ? 0.f : ex2(mw[n][e] - m[n][e]);
+        if (it.direct) {
+          const float f = to_m / sum;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + (size_t(it.tok0 + tok) * H + h) * kDim) + g;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dst[8 * j] = pack2(o[n][j][e] * f, o[n][j][2 + e] * f);
         } else {
           const size_t at = size_t(it.rec0) + (size_t(tok) * H + h) * it.rec_step;
-          float4* rec = reinterpret_cast<float4*>(w.recs + at * kDim) + t;
+          float2* rec = reinterpret_cast<float2*>(w.recs + at * kDim) + g;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float *even = &o[2 * j][2 * half], *odd = &o[2 * j + 1][2 * half];
-            __stcg(rec + 4 * j, make_float4(even[0] * to_m, odd[0] * to_m, even[1] * to_m, odd[1] * to_m));
-          }
-          if (t == 0) __stcg(w.rec_ml + at, make_float2(m, l));
+          for (int j = 0; j < 8; ++j) __stcg(rec + 8 * j, make_float2(o[n][j][e] * to_m, o[n][j][2 + e] * to_m));
+          if (g == 0) __stcg(w.rec_ml + at, make_float2(m[n][e], sum));
         }
       }
-    }
     cur = nxt;
     load_unit(__shfl_sync(0xffffffffu, ahead, 0), nxt, slots[slot]);
     slot ^= 1;
@@ -355,8 +388,9 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
   if (!ok && lane == 0) raise_error(a.err, kErrTimeout | kSiteDecodeRing);
   // after a timeout some copies may still be in flight: wait for them (bounded) before exiting
   while (consumed < issued) {
-    mbar_wait(bars + 8 * (consumed % kStages), (consumed / kStages) & 1);
+    mbar_wait(bars + 8 * st_out, phase);
     ++consumed;
+    if (++st_out == kStages) st_out = 0, phase ^= 1;
   }
 }
 

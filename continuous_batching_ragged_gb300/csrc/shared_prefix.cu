@@ -1194,8 +1194,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 // it, which have no work in the one case (64 sequences of 1000 keys, a group each, 58 us;
 // 51 without them, 69 by the plan) and are late in the other (200 behind 4096 keys among
 // empty groups 55 us; 51 by the plan alone, 269 here).
-constexpr int kSmallThreads = 32 * kStreamWarps;
-constexpr int kSmallSeqs = kSmallThreads;
+// The streams of a kernel, by NT: 0 over a bf16 cache, else sets of 8 query rows over one in 8 bits.
+template <int NT>
+struct StreamShape : qstream::Shape<NT> {};
+template <>
+struct StreamShape<0> {
+  static constexpr int kWarps = kStreamWarps, kStages = stream::kStages;
+  static constexpr uint32_t kWarpBarBytes = kStages * 8, kOffBars = stream::kRingBytes;
+  static constexpr uint32_t kOffSlots = kOffBars + stream::kBarBytes, kSmem = kOffSlots + stream::kSlotBytes + 1024;
+  static_assert(kOffSlots % 16 == 0 && kSmem <= 220 * 1024, "shared memory");
+};
+template <int NT>
+__device__ __forceinline__ void init_stage_bars(uint32_t bars) {
+  for (int st = 0; st < StreamShape<NT>::kStages; ++st) mbar_init(bars + 8 * st, NT == 0 ? 1 : qstream::kBarArrivals);
+  fence_mbar_init();
+}
+template <int NT, bool kSmall>
+__device__ __forceinline__ void run_stream(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttnArgs& a,
+                                           const PrefixWork& w, int n_items, uint8_t* gsm, uint32_t base, int warp, int first,
+                                           int step, int claimed_from, const stream::SmallStep& small) {
+  using S = StreamShape<NT>;
+  const uint32_t bars = base + S::kOffBars + warp * S::kWarpBarBytes;
+  SuffixItem* slots = reinterpret_cast<SuffixItem*>(gsm + S::kOffSlots) + 2 * warp;
+  if constexpr (NT == 0)
+    stream::run_warp<kSmall>(tm_k, tm_v, a, w, n_items, base + warp * S::kStages * stream::kStageBytes, bars, slots, first, step,
+                             claimed_from, small);
+  else
+    qstream::run_warp<NT, kSmall>(tm_k, tm_v, a, w, n_items, base + warp * S::kStages * qstream::kStageBytes, bars,
+                                  reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * S::kStages), slots, first, step,
+                                  claimed_from, small);
+}
 constexpr int kSmallTokens = 4096;
 // Contexts up to which a small step's rows are one chunk each, written at once, where the
 // join and its launch cost more than the longer chunks: few units wait for every
@@ -1207,10 +1235,6 @@ constexpr int kOneChunkKeysFew = 128, kOneChunkKeysMany = 384;
 constexpr int kManyUnitsPerSm = 2;
 // Shortest chunk: all of it in flight at once (2 rows of 320 keys: 8.7 us, 9.1 with one more tile).
 constexpr int kSmallChunkTiles = stream::kStages;
-constexpr uint32_t kSmallOffBars = stream::kRingBytes, kSmallOffSlots = kSmallOffBars + qstream::kBarBytes;
-static_assert(qstream::kRingBytes <= stream::kRingBytes && stream::kBarBytes <= qstream::kBarBytes, "one layout for both");
-constexpr uint32_t kSmallSmem = kSmallOffSlots + stream::kSlotBytes + 1024;
-static_assert(kSmallOffSlots % 16 == 0 && kSmallSmem <= 220 * 1024, "shared memory");
 
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
@@ -1218,25 +1242,23 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
   return v;
 }
 
-template <bool kQ8>
-__global__ void __launch_bounds__(kSmallThreads, 1)
+template <int NT>
+__global__ void __launch_bounds__(32 * StreamShape<NT>::kWarps, 1)
     small_step_kernel(const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
                       const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
+  constexpr int kWarps = StreamShape<NT>::kWarps, kThreads = 32 * kWarps, kSeqs = kThreads;   // a thread for each sequence
   extern __shared__ uint8_t smem_raw[];
-  __shared__ stream::SmallSeq seqs[kSmallSeqs];
-  __shared__ int group_s0[kSmallSeqs], group_p[kSmallSeqs];
-  __shared__ int64_t sums[4][kStreamWarps];
+  __shared__ stream::SmallSeq seqs[kSeqs];
+  __shared__ int group_s0[kSeqs], group_p[kSeqs];
+  __shared__ int64_t sums[4][kWarps];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* gsm = smem_raw + (base - raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool writer = blockIdx.x == 0;             // of what the join reads, and of the errors
-  constexpr int kStages = kQ8 ? qstream::kStages : stream::kStages;
-  const uint32_t bars = base + kSmallOffBars + warp * kStages * (kQ8 ? 16 : 8);
   const int S = a.num_seqs, T = a.num_tokens, NG = w.num_groups, H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv;
 
   if (lane == 0) {
-    for (int st = 0; st < kStages; ++st) mbar_init(bars + 8 * st, kQ8 ? qstream::kBarArrivals : 1);
-    fence_mbar_init();
+    init_stage_bars<NT>(base + StreamShape<NT>::kOffBars + warp * StreamShape<NT>::kWarpBarBytes);
     if (warp == 0) {
       tma_prefetch_desc(&tm_k16);
       tma_prefetch_desc(&tm_v16);
@@ -1251,7 +1273,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   }
   if (tid < S) c0 = a.cu_seqlens_q[tid], q_len = a.cu_seqlens_q[tid + 1] - c0, n = w.context_lens[tid];
   if (writer)
-    for (int t = tid; t < T; t += kSmallThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
+    for (int t = tid; t < T; t += kThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
   group_s0[tid] = s0;
   group_p[tid] = p;
   int bad = tid < NG && (s0 < 0 || s1 < s0 || s1 > S || (tid == 0 && s0 != 0) || (tid == NG - 1 && s1 != S));
@@ -1273,10 +1295,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   const int64_t my_tiles = warp_sum(int64_t(tiles) * rt * Hkv), my_rows = warp_sum(int64_t(rt) * Hkv);
   if (lane == 0) sums[0][warp] = my_tiles, sums[3][warp] = my_rows;
   __syncthreads();
-  const int warps = int(gridDim.x) * kStreamWarps;
+  const int warps = int(gridDim.x) * kWarps;
   int64_t all_tiles = 0, spare = warps;            // ceil(x / L) is less than x / L + 1 for each row tile and head
 #pragma unroll
-  for (int i = 0; i < kStreamWarps; ++i) all_tiles += sums[0][i], spare -= sums[3][i];
+  for (int i = 0; i < kWarps; ++i) all_tiles += sums[0][i], spare -= sums[3][i];
   // One unit a warp, where there are warps enough: a unit's beginning and end cost as much as some tiles (6 sequences
   // behind 4900 keys 13.2 us, with kUnitsPerWarp units a warp 18.5; one of 130,000 keys 89 and 99)
   const int64_t units = spare > 0 ? spare : w.stream_units, per = (all_tiles + units - 1) / units;
@@ -1294,7 +1316,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   item0 -= items, rec0 -= recs;
   int64_t all_items = 0, all_recs = 0;
 #pragma unroll
-  for (int i = 0; i < kStreamWarps; ++i) {
+  for (int i = 0; i < kWarps; ++i) {
     if (i < warp) item0 += sums[1][i], rec0 += sums[2][i];
     all_items += sums[1][i], all_recs += sums[2][i];
   }
@@ -1311,31 +1333,20 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     }
   }
   __syncthreads();
-  SuffixItem* slots = reinterpret_cast<SuffixItem*>(gsm + kSmallOffSlots) + 2 * warp;
-  const int n_items = bad ? 0 : int(all_items), first = warp * int(gridDim.x) + int(blockIdx.x);
-  if constexpr (kQ8)
-    qstream::run_warp<true>(&tm_k16, &tm_v16, a, w, n_items, base + warp * qstream::kStages * qstream::kStageBytes, bars,
-                            reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * kStages), slots, first, warps, 0,
-                            stream::SmallStep{seqs, S, L});
-  else
-    stream::run_warp<true>(&tm_k16, &tm_v16, a, w, n_items, base + warp * stream::kStages * stream::kStageBytes, bars, slots,
-                           first, warps, 0, stream::SmallStep{seqs, S, L});
+  run_stream<NT, true>(&tm_k16, &tm_v16, a, w, bad ? 0 : int(all_items), gsm, base, warp,
+                       warp * int(gridDim.x) + int(blockIdx.x), warps, 0, stream::SmallStep{seqs, S, L});
 }
 
 // The streams of a step over a cache in 8 bits, as the plan lists them.
-__global__ void __launch_bounds__(kSmallThreads, 1)
+template <int NT>
+__global__ void __launch_bounds__(32 * StreamShape<NT>::kWarps, 1)
     q8_streams_kernel(const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
                       const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
+  using Sh = StreamShape<NT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-  uint8_t* gsm = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kStages = qstream::kStages;
-  const uint32_t bars = base + kSmallOffBars + warp * kStages * 16;
-  if (lane == 0) {
-    for (int st = 0; st < kStages; ++st) mbar_init(bars + 8 * st, qstream::kBarArrivals);
-    fence_mbar_init();
-  }
+  if (lane == 0) init_stage_bars<NT>(base + Sh::kOffBars + warp * Sh::kWarpBarBytes);
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan has finished
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int n_items = __ldcg(w.header + 4);
@@ -1344,11 +1355,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     n_items = 0;
   }
   __syncwarp();
-  const int warps = int(gridDim.x) * kStreamWarps;
-  qstream::run_warp<false>(&tm_k16, &tm_v16, a, w, n_items, base + warp * kStages * qstream::kStageBytes, bars,
-                           reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * kStages),
-                           reinterpret_cast<SuffixItem*>(gsm + kSmallOffSlots) + 2 * warp,
-                           warp * int(gridDim.x) + int(blockIdx.x), warps, 2 * warps, stream::SmallStep{});
+  const int warps = int(gridDim.x) * Sh::kWarps;
+  run_stream<NT, false>(&tm_k16, &tm_v16, a, w, n_items, smem_raw + (base - raw), base, warp,
+                        warp * int(gridDim.x) + int(blockIdx.x), warps, 2 * warps, stream::SmallStep{});
 }
 
 // A warp joins kJoinRows query heads of a token at a time and goes on to the next
@@ -1551,7 +1560,7 @@ PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_
   z.piece_recs = chunks ? rows * 2 + size_t(kExtraRecs) : 0;
   // ceil(x / L) <= x / L + 1 for every streamed sequence, and all x / L together are at most the units aimed for,
   // twice that where L is halved
-  const size_t units = 2 * size_t(kMaxSms) * kStreamWarps * kUnitsPerWarp;
+  const size_t units = 2 * size_t(kMaxSms) * (q8 ? StreamShape<1>::kWarps : kStreamWarps) * kUnitsPerWarp;
   const size_t shortest = size_t(stream::kTileKeys) * std::min(kMinChunkTiles, kSmallChunkTiles);
   const size_t chunks_of_row = (size_t(max_context_len) + shortest - 1) / shortest;
   z.items = z.T * G / kStreamRows + z.S + units + 1;
@@ -1605,8 +1614,14 @@ static cb_status allow_shared_memory() {
   std::lock_guard<std::mutex> lock(g_attr_mutex);
   if (g_attr_set[dev]) return CB_OK;
   cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes));
-  for (auto kernel : {small_step_kernel<false>, small_step_kernel<true>, q8_streams_kernel})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallSmem));
+  const auto allow = [&e](const void* kernel, uint32_t bytes) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  };
+  allow(reinterpret_cast<const void*>(small_step_kernel<0>), StreamShape<0>::kSmem);
+  allow(reinterpret_cast<const void*>(small_step_kernel<1>), StreamShape<1>::kSmem);
+  allow(reinterpret_cast<const void*>(small_step_kernel<2>), StreamShape<2>::kSmem);
+  allow(reinterpret_cast<const void*>(q8_streams_kernel<1>), StreamShape<1>::kSmem);
+  allow(reinterpret_cast<const void*>(q8_streams_kernel<2>), StreamShape<2>::kSmem);
   if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: shared memory attribute");
   g_attr_set[dev] = true;
   return CB_OK;
@@ -1634,6 +1649,13 @@ static cb_status launch_prefix_tc(const AttnArgs& a, const PrefixWork& w, cudaSt
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: launch");
 }
 
+// Sets of 8 query rows of a stream's units; 0: a bf16 cache.
+int stream_sets(const AttnArgs& a) {
+  return !a.k_scale ? 0 : int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= 8 ? 1 : 2;
+}
+int stream_warps(int sets) { return sets == 0 ? StreamShape<0>::kWarps : sets == 1 ? StreamShape<1>::kWarps : StreamShape<2>::kWarps; }
+int stream_smem(int sets) { return sets == 0 ? StreamShape<0>::kSmem : sets == 1 ? StreamShape<1>::kSmem : StreamShape<2>::kSmem; }
+
 static cb_status launch_small_step(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return CB_ERR_CUDA;
@@ -1641,7 +1663,9 @@ static cb_status launch_small_step(const AttnArgs& a, const PrefixWork& w, cudaS
   cb_status st = encode_pools(a, enc, true, &tk16, &tv16);
   if (st == CB_OK) st = allow_shared_memory();
   if (st != CB_OK) return st;
-  cudaError_t e = launch_kernel(a.k_scale ? small_step_kernel<true> : small_step_kernel<false>, dim3(unsigned(w.num_sms)), dim3(kSmallThreads), kSmallSmem, stream, true,
+  const int sets = stream_sets(a);
+  auto kernel = sets == 0 ? small_step_kernel<0> : sets == 1 ? small_step_kernel<1> : small_step_kernel<2>;
+  cudaError_t e = launch_kernel(kernel, dim3(unsigned(w.num_sms)), dim3(32 * stream_warps(sets)), stream_smem(sets), stream, true,
                                 tk16, tv16, a, w);
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: launch");
 }
@@ -1653,8 +1677,9 @@ static cb_status launch_q8_streams(const AttnArgs& a, const PrefixWork& w, cudaS
   cb_status st = encode_pools(a, enc, true, &tk16, &tv16);
   if (st == CB_OK) st = allow_shared_memory();
   if (st != CB_OK) return st;
-  cudaError_t e = launch_kernel(q8_streams_kernel, dim3(unsigned(w.num_sms)), dim3(kSmallThreads), kSmallSmem, stream, true,
-                                tk16, tv16, a, w);
+  const int sets = stream_sets(a);
+  cudaError_t e = launch_kernel(sets == 1 ? q8_streams_kernel<1> : q8_streams_kernel<2>, dim3(unsigned(w.num_sms)),
+                                dim3(32 * stream_warps(sets)), stream_smem(sets), stream, true, tk16, tv16, a, w);
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: launch");
 }
 
@@ -1694,7 +1719,8 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   w.key_bytes = 2.0f * HD * float(a.num_kv_heads) * (q8 ? 1.0f : 2.0f);
   w.num_sms = sm_count();
   w.tile_tokens = tile_tokens(a.num_heads / a.num_kv_heads);
-  w.stream_units = std::min(w.num_sms, kMaxSms) * kStreamWarps * kUnitsPerWarp;
+  const int warps = stream_warps(stream_sets(a)), small_seqs = 32 * warps;
+  w.stream_units = std::min(w.num_sms, kMaxSms) * warps * kUnitsPerWarp;
   w.piece_cap = int32_t(z.pieces);
   w.item_cap = int32_t(z.items);
   w.prefix_rec_cap = int64_t(z.prefix_recs);
@@ -1725,8 +1751,8 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   // among 41 empty groups 53 us, 28 without those); with fewer, the device counts.
   const int64_t row_tiles = (int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) + kStreamRows - 1) / kStreamRows;
   const double each = double(a.max_context_len) * w.key_bytes * row_tiles;
-  const int sharers = int(std::min(double(kSmallSeqs), std::ceil(double(kSmallUs) * kBytesPerUs / each) - 1.0));
-  const bool fits = a.num_seqs <= kSmallSeqs && num_groups <= kSmallSeqs && a.num_tokens <= kSmallTokens &&
+  const int sharers = int(std::min(double(small_seqs), std::ceil(double(kSmallUs) * kBytesPerUs / each) - 1.0));
+  const bool fits = a.num_seqs <= small_seqs && num_groups <= small_seqs && a.num_tokens <= kSmallTokens &&
                     (a.max_q_len == 1 || int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= kMaxStreamRows);
   const bool maybe = fits && (num_groups == 0 || a.num_seqs - num_groups <= sharers);
   const bool small = maybe && (num_groups == 0 || a.num_seqs - 1 <= sharers || num_groups <= a.num_seqs / 2);
