@@ -25,7 +25,7 @@ VALUES_LIB = os.path.join(PKG, "libcb_values.so")
 
 CUDA_SOURCES = ["runtime.cu", "append_kv.cu", "plan.cu", "split_kv.cu", "prefill_tc.cu", "attention.cu",
                 "synth.cu", "decode_noalloc.cu", "selftest.cu", "decode_tc.cu", "norm_rope.cu", "pages.cu", "shared_prefix.cu",
-                "quant_kv.cu"]
+                "quant_kv.cu", "quant_attention.cu"]
 CXX_SOURCES = ["scheduler.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O3",

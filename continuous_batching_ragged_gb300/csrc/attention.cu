@@ -357,7 +357,7 @@ extern "C" size_t cb_shared_prefix_workspace_size(const cb_kv_cache* cache, int3
       max_context_len < 0)
     return 0;
   return cb::shared_prefix_workspace_bytes(num_q_heads, cache->num_heads, num_seqs, num_tokens, num_groups,
-                                           max_context_len, false);
+                                           max_context_len);
 }
 
 extern "C" cb_status cb_shared_prefix_attention(const void* q, int32_t num_q_heads, const cb_kv_cache* cache,
@@ -408,8 +408,7 @@ extern "C" size_t cb_ragged_attention_q8_workspace_size(const cb_kv_cache_q8* ca
       num_q_heads / cache->num_heads > kMaxPrefixGroup || num_seqs < 0 || num_tokens < 0 || num_groups < 0 ||
       max_context_len < 0)
     return 0;
-  return cb::shared_prefix_workspace_bytes(num_q_heads, cache->num_heads, num_seqs, num_tokens, num_groups, max_context_len,
-                                           true);
+  return cb::quant_attention_workspace_bytes(num_q_heads, cache->num_heads, num_seqs, num_tokens, num_groups, max_context_len);
 }
 
 extern "C" cb_status cb_ragged_attention_q8(const void* q, int32_t num_q_heads, const cb_kv_cache_q8* cache,
@@ -445,5 +444,5 @@ extern "C" cb_status cb_ragged_attention_q8(const void* q, int32_t num_q_heads, 
   if (st != CB_OK || num_seqs == 0) return st;
   a.k_scale = cache->k_scale;
   a.v_scale = cache->v_scale;
-  return cb::run_shared_prefix(a, cu_groups, prefix_lens, num_groups, workspace, static_cast<cudaStream_t>(stream));
+  return cb::run_quant_attention(a, cu_groups, prefix_lens, num_groups, workspace, static_cast<cudaStream_t>(stream));
 }

@@ -152,11 +152,16 @@ cb_status launch_decode_tc(const AttnArgs& a, const StepPlan& plan, bool after_p
 
 // Steps with shared prefixes (bf16, head_dim 128, block size a multiple of 16,
 // at most 128 query heads per key/value head): the workspace, and the step.
-// num_groups 0 (and cu_groups, prefix_lens null): no sequence shares.  `q8`, a.k_scale: a cache in 8 bits.
 size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
-                                     int32_t num_groups, int32_t max_context_len, bool q8);
+                                     int32_t num_groups, int32_t max_context_len);
 cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
                             void* workspace, cudaStream_t stream);
+
+// The same over a cache in 8 bits (a.k_scale, a.v_scale).  num_groups 0 (cu_groups and prefix_lens null): nothing is shared.
+size_t quant_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
+                                       int32_t num_groups, int32_t max_context_len);
+cb_status run_quant_attention(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
+                              void* workspace, cudaStream_t stream);
 
 // Prefill chunks (q_len > 1) on tcgen05 tensor cores, bf16, head_dim 128:
 // persistent CTAs over the plan's prefill items.

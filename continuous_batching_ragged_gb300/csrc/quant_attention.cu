@@ -1,0 +1,377 @@
+// cb_ragged_attention_q8: attention of a packed step over a cache in 8 bits (e4m3
+// pages, a fp32 scale for each page and key/value head; head_dim 128).
+//
+//     out = sum_j p_j vs_j v_j / sum_j p_j,  p_j = exp(scale * ks_j q . k_j),
+// ks_j, vs_j the scales of key j's page, k_j and v_j its e4m3 numbers.
+//
+// Rows are streams of single warps (quant_stream.cuh).  A step without chunks and
+// without a plan kernel: every CTA lays the step's streams end to end for itself and
+// every warp of the grid takes an equal share of all tiles, whatever the lengths of
+// the contexts.  A share begins and ends inside a stream at most, so a warp leaves at
+// most two records a row, and the join reads what it needs: 2 records for each warp
+// of the grid, however many sequences there are.  Steps of more sequences than a CTA
+// has threads are planned by the kernel that plans steps with shared prefixes.
+#include <algorithm>
+#include <mutex>
+
+#include <cuda.h>
+
+#include "device_common.cuh"
+#include "kernels.h"
+#include "quant_stream.cuh"
+#include "runtime.h"
+#include "shared_prefix.h"
+#include "sm100_ptx.cuh"
+
+namespace cb {
+namespace {
+
+using namespace sm100;
+using qstream::RangeSeq;
+using qstream::RangeUnits;
+using qstream::Shape;
+
+constexpr int HD = kPrefixDim;
+constexpr int kMaxSms = 160;             // SMs that the records are sized for
+constexpr int kMaxRows = 64;             // query rows per key/value head that are streamed, 8 or 16 at a time
+constexpr int kStepTokens = 4096;        // of a step without a plan kernel
+constexpr int kMinShareTiles = 3;        // shortest share of a warp
+
+// What the CTAs of a step without a plan kernel make of it, for the join.
+struct StepWork {
+  const int32_t* cu_groups;              // null: none
+  const int32_t* prefix_lens;
+  int32_t num_groups;
+  int32_t share_tiles;                   // least tiles of a share; 0: whole streams only, there is no join
+  int32_t* header;                       // [0] tiles of a share
+  int4* token_info;                      // [num_tokens] (first tile of its sequence's streams, tiles of each, token of the
+                                         // sequence, 1: there is something to join)
+  float* recs;                           // [2 * warps][row tile][HD]
+  float2* rec_ml;
+};
+
+template <int NT>
+__device__ __forceinline__ void init_bars(uint32_t bars) {
+  for (int st = 0; st < Shape<NT>::kStages; ++st) mbar_init(bars + 8 * st, qstream::kBarArrivals);
+  fence_mbar_init();
+}
+
+template <int NT>
+__global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
+    q8_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ AttnArgs a, const __grid_constant__ StepWork w) {
+  using Sh = Shape<NT>;
+  constexpr int kWarps = Sh::kWarps, kThreads = 32 * kWarps, kSeqs = kThreads;   // a thread for each sequence
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ RangeSeq seqs[kSeqs];
+  __shared__ int group_s0[kSeqs], group_p[kSeqs];
+  __shared__ int2 sums[kWarps];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* gsm = smem_raw + (base - raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool writer = blockIdx.x == 0;             // of what the join reads, and of the errors
+  const uint32_t bars = base + Sh::kOffBars + warp * Sh::kWarpBarBytes;
+  const int S = a.num_seqs, T = a.num_tokens, NG = w.num_groups, H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv;
+
+  if (lane == 0) {
+    init_bars<NT>(bars);
+    if (warp == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // it may start while the stream's last kernel ends
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int s0 = 0, s1 = 0, p = 0, c0 = 0, q_len = 0, n = 0;
+  if (tid < NG) s0 = w.cu_groups[tid], s1 = w.cu_groups[tid + 1], p = w.prefix_lens[tid];
+  if (tid < S) c0 = a.cu_seqlens_q[tid], q_len = a.cu_seqlens_q[tid + 1] - c0, n = a.context_lens[tid];
+  if (writer)
+    for (int t = tid; t < T; t += kThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
+  bool bad = false;
+  if (NG > 0) {                                    // nothing is shared here, but what does not hold is reported
+    group_s0[tid] = s0;
+    group_p[tid] = p;
+    bad = tid < NG && (s0 < 0 || s1 < s0 || s1 > S || (tid == 0 && s0 != 0) || (tid == NG - 1 && s1 != S));
+    bad = __syncthreads_or(bad);
+    int g = 0;                                     // the sequence's group: the last that starts at or before it
+    for (int hi = NG - 1; g < hi;) {
+      const int mid = (g + hi + 1) >> 1;
+      if (group_s0[mid] <= tid) g = mid; else hi = mid - 1;
+    }
+    p = group_p[g];
+  }
+  const bool ok = tid < S && p >= 0 && q_len >= 1 && c0 >= 0 && c0 + q_len <= T && q_len <= a.max_q_len && n >= q_len &&
+                  p <= n - q_len && n <= a.max_context_len && int64_t(n) <= int64_t(a.max_blocks_per_seq) * a.block_size;
+  const int tiles = ok && !bad ? (n - 1) / qstream::kTileKeys + 1 : 0;
+  const int streams = tiles > 0 ? (q_len * G + Sh::kRows - 1) / Sh::kRows * Hkv : 0;
+  int off = tiles * streams, st0 = streams;        // exclusive scans over the CTA (the host has checked their range)
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, off, o), y = __shfl_up_sync(0xffffffffu, st0, o);
+    if (lane >= o) off += x, st0 += y;
+  }
+  if (lane == 31) sums[warp] = make_int2(off, st0);
+  __syncthreads();
+  off -= tiles * streams, st0 -= streams;
+  int all_tiles = 0, all_streams = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) off += sums[i].x, st0 += sums[i].y;
+    all_tiles += sums[i].x, all_streams += sums[i].y;
+  }
+  const int warps = int(gridDim.x) * kWarps, id = warp * int(gridDim.x) + int(blockIdx.x);
+  const bool whole = w.share_tiles == 0;
+  const int per = whole ? 0 : max(w.share_tiles, (all_tiles - 1) / warps + 1);
+  seqs[tid] = RangeSeq{off, tiles, st0, c0, q_len, n};
+  if (writer) {
+    if ((bad && tid == 0) || (tid < S && !ok)) raise_error(a.err, kErrInvalid);
+    if (tiles > 0 && !whole)
+      for (int t = 0; t < q_len; ++t) w.token_info[c0 + t] = make_int4(off, tiles, t, 1);
+    if (tid == 0) w.header[0] = per;
+  }
+  __syncthreads();
+  RangeUnits units{seqs, S, Hkv, Sh::kRows, whole ? id : int(min(int64_t(all_tiles), int64_t(id) * per)),
+                   whole ? all_streams : int(min(int64_t(all_tiles), int64_t(id + 1) * per)), whole ? warps : 0,
+                   unsigned(2 * id * Sh::kRows)};
+  qstream::run_warp<NT>(&tm_k, &tm_v, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
+                        reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * Sh::kStages),
+                        reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
+}
+
+// The streams of a step as the plan lists them.
+template <int NT>
+__global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
+    q8_streams_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
+  using Sh = Shape<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* gsm = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bars = base + Sh::kOffBars + warp * Sh::kWarpBarBytes;
+  if (lane == 0) init_bars<NT>(bars);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan has finished
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int n_items = __ldcg(w.header + 4);
+  if (uint32_t(__ldcg(w.header + 2)) != w.tag || n_items < 0 || n_items > w.item_cap) {   // a plan of another call: no work
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, kErrInvalid);
+    n_items = 0;
+  }
+  __syncwarp();
+  const int warps = int(gridDim.x) * Sh::kWarps;
+  qstream::ListedUnits units{w, a.num_kv_heads, n_items * a.num_kv_heads, warp * int(gridDim.x) + int(blockIdx.x), warps, 2 * warps};
+  qstream::run_warp<NT>(&tm_k, &tm_v, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
+                        reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * Sh::kStages),
+                        reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
+}
+
+// One row's records, `step` apart from the first on: their weighted sum, by the lanes of a warp, 4 dims each.
+struct Joined {
+  float4 acc;
+  float mx, den;
+  __device__ __forceinline__ void raise(float top) {
+    const float old = ex2(mx - (top == -INFINITY ? 0.f : top));
+    acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+    den *= old;
+    mx = top;
+  }
+  __device__ __forceinline__ void add(const float4& x, float2 ml) {   // mx is at least ml.x
+    const float f = ex2(ml.x - (mx == -INFINITY ? 0.f : mx));
+    den = fmaf(f, ml.y, den);
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
+  }
+};
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinFlight = 4;           // records of a row requested at once
+
+// Joins the rows that lie in several shares.  WIDE: a CTA to a row, each warp with its part of the records, where rows are
+// few and may have very many; else a warp to a row.
+template <bool WIDE>
+__global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(const AttnArgs a, const StepWork w, int row_tile) {
+  __shared__ float4 part_acc[WIDE ? kJoinWarps : 1][32];
+  __shared__ float2 part_ml[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv;
+  const int rows = a.num_tokens * H, step = WIDE ? int(gridDim.x) : int(gridDim.x) * kJoinWarps;
+  int row = WIDE ? int(blockIdx.x) : int(blockIdx.x) * kJoinWarps + warp;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int per = __ldcg(w.header);
+  for (; row < rows; row += step) {
+    const int tok = row / H, h = row - tok * H;
+    const int4 ti = __ldcg(w.token_info + tok);
+    if (ti.w == 0) continue;                       // left out
+    const int hk = h / G, r = ti.z * G + h - hk * G, rt = r / row_tile;
+    const int begin = ti.x + (rt * Hkv + hk) * ti.y;   // of the row's stream, in tiles
+    const int f = begin / per, n = (begin + ti.y - 1) / per - f + 1;   // its first share, and shares
+    if (n == 1) continue;                          // written already
+    const int in_tile = r - rt * row_tile;
+    const int first = (2 * f + (begin > f * per ? 1 : 0)) * row_tile + in_tile;   // the last part of share f, or its first
+    Joined j{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+    for (int k0 = WIDE ? warp * kJoinFlight : 0; k0 < n; k0 += WIDE ? kJoinThreads / 32 * kJoinFlight : kJoinFlight) {
+      float4 x[kJoinFlight];
+      float2 ml[kJoinFlight];
+      float top = j.mx;
+#pragma unroll
+      for (int i = 0; i < kJoinFlight; ++i) {
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        ml[i] = make_float2(-INFINITY, 0.f);
+        if (k0 + i < n) {
+          const size_t at = k0 + i == 0 ? first : size_t(2 * (f + k0 + i)) * row_tile + in_tile;
+          x[i] = __ldcg(reinterpret_cast<const float4*>(w.recs + at * HD) + lane);
+          ml[i] = __ldcg(w.rec_ml + at);
+        }
+        top = fmaxf(top, ml[i].x);
+      }
+      j.raise(top);
+#pragma unroll
+      for (int i = 0; i < kJoinFlight; ++i) j.add(x[i], ml[i]);
+    }
+    if (WIDE) {
+      part_acc[warp][lane] = j.acc;
+      if (lane == 0) part_ml[warp] = make_float2(j.mx, j.den);
+      __syncthreads();
+      if (warp == 0) {
+        float top = j.mx;
+#pragma unroll
+        for (int k = 1; k < kJoinWarps; ++k) top = fmaxf(top, part_ml[k].x);
+        j.raise(top);
+#pragma unroll
+        for (int k = 1; k < kJoinWarps; ++k) j.add(part_acc[k][lane], part_ml[k]);
+      }
+    }
+    if (!WIDE || warp == 0) {
+      const float inv = 1.0f / j.den;
+      *(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + size_t(row) * HD) + lane) =
+          make_uint2(stream::pack2(j.acc.x * inv, j.acc.y * inv), stream::pack2(j.acc.z * inv, j.acc.w * inv));
+    }
+    if (WIDE) __syncthreads();                     // the parts are read before the next row's
+  }
+}
+
+std::mutex g_attr_mutex;
+bool g_attr_set[64] = {};
+
+// Lets the kernels take their dynamic shared memory on the current device.
+cb_status allow_shared_memory() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+    return fail(CB_ERR_UNSUPPORTED, "8-bit attention: no usable current device");
+  std::lock_guard<std::mutex> lock(g_attr_mutex);
+  if (g_attr_set[dev]) return CB_OK;
+  cudaError_t e = cudaSuccess;
+  const auto allow = [&e](const void* kernel, uint32_t bytes) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  };
+  allow(reinterpret_cast<const void*>(q8_step_kernel<1>), Shape<1>::kSmem);
+  allow(reinterpret_cast<const void*>(q8_step_kernel<2>), Shape<2>::kSmem);
+  allow(reinterpret_cast<const void*>(q8_streams_kernel<1>), Shape<1>::kSmem);
+  allow(reinterpret_cast<const void*>(q8_streams_kernel<2>), Shape<2>::kSmem);
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: shared memory attribute");
+  g_attr_set[dev] = true;
+  return CB_OK;
+}
+
+// The tensor maps of the K and V pools: boxes of `rows` rows of one block and head.
+cb_status encode_pools(const AttnArgs& a, int rows, CUtensorMap* tk, CUtensorMap* tv) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return CB_ERR_CUDA;
+  const cuuint64_t B = cuuint64_t(a.block_size), boxes = cuuint64_t(a.num_blocks) * a.num_kv_heads;
+  const cuuint64_t dims[3] = {HD, B, boxes}, strides[2] = {HD, B * HD};
+  const cuuint32_t box[3] = {HD, cuuint32_t(rows), 1}, ones[3] = {1, 1, 1};
+  for (int v = 0; v < 2; ++v) {
+    const CUresult r = enc(v ? tv : tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(v ? a.v_pool : a.k_pool), dims, strides,
+                           box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(CB_ERR_CUDA, "8-bit attention: encoding the KV tensor maps failed (%d)", int(r));
+  }
+  return CB_OK;
+}
+
+// Sets of 8 query rows of a stream's units.
+int stream_sets(const AttnArgs& a) { return int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= 8 ? 1 : 2; }
+int stream_warps(int sets) { return sets == 1 ? Shape<1>::kWarps : Shape<2>::kWarps; }
+int stream_smem(int sets) { return sets == 1 ? Shape<1>::kSmem : Shape<2>::kSmem; }
+constexpr int kMaxWarps = Shape<1>::kWarps;
+static_assert(Shape<2>::kWarps * Shape<2>::kRows <= 2 * kMaxWarps * Shape<1>::kRows && Shape<2>::kWarps <= kMaxWarps, "sizes");
+
+// Records of a step without a plan kernel: two of a row tile for each warp that may have a share.
+size_t step_records(int num_sms) { return size_t(num_sms) * std::max(2 * Shape<1>::kWarps * Shape<1>::kRows, 2 * Shape<2>::kWarps * Shape<2>::kRows); }
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+size_t step_workspace_bytes(int32_t num_tokens) {
+  return 256 + align256(size_t(num_tokens) * 16) + align256(step_records(kMaxSms) * kPrefixRecBytes);
+}
+PrefixSizes listed_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t max_context_len) {
+  return prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, 0, max_context_len, kMaxWarps, false);
+}
+
+cb_status run_step(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups, void* workspace,
+                   cudaStream_t stream) {
+  const int sets = stream_sets(a), sms = std::min(sm_count(), kMaxSms);
+  StepWork w;
+  w.cu_groups = cu_groups;
+  w.prefix_lens = prefix_lens;
+  w.num_groups = num_groups;
+  w.share_tiles = kMinShareTiles;
+  char* p = static_cast<char*>(workspace);
+  w.header = reinterpret_cast<int32_t*>(p);
+  w.token_info = reinterpret_cast<int4*>(p + 256);
+  w.recs = reinterpret_cast<float*>(p + 256 + align256(size_t(a.num_tokens) * 16));
+  w.rec_ml = reinterpret_cast<float2*>(w.recs + step_records(kMaxSms) * HD);
+  CUtensorMap tk, tv;
+  cb_status st = encode_pools(a, qstream::kTileKeys, &tk, &tv);
+  if (st == CB_OK) st = allow_shared_memory();
+  if (st != CB_OK) return st;
+  cudaError_t e = launch_kernel(sets == 1 ? q8_step_kernel<1> : q8_step_kernel<2>, dim3(unsigned(sms)),
+                                dim3(32 * stream_warps(sets)), stream_smem(sets), stream, true, tk, tv, a, w);
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: launch");
+  if (w.share_tiles == 0) return CB_OK;
+  const int64_t rows = int64_t(a.num_tokens) * a.num_heads;
+  const int row_tile = 8 * sets;
+  if (rows <= int64_t(sms) * 4)
+    e = launch_kernel(q8_join_kernel<true>, dim3(unsigned(rows)), dim3(kJoinThreads), 0, stream, true, a, w, row_tile);
+  else
+    e = launch_kernel(q8_join_kernel<false>, dim3(unsigned(std::min<int64_t>((rows + kJoinWarps - 1) / kJoinWarps, int64_t(sms) * 8))),
+                      dim3(kJoinThreads), 0, stream, true, a, w, row_tile);
+  return e == cudaSuccess ? CB_OK : cuda_fail(e, "8-bit attention: join launch");
+}
+
+}  // namespace
+
+size_t quant_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
+                                       int32_t, int32_t max_context_len) {
+  return std::max(step_workspace_bytes(num_tokens),
+                  prefix_workspace_bytes(listed_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, max_context_len)));
+}
+
+cb_status run_quant_attention(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
+                              void* workspace, cudaStream_t stream) {
+  NvtxRange nvtx("cb.ragged_attention_q8");
+  if (int64_t(a.num_blocks) * a.num_kv_heads >= (int64_t(1) << 31))
+    return fail(CB_ERR_UNSUPPORTED, "8-bit attention: num_blocks * num_kv_heads must fit in int32");
+  const int sets = stream_sets(a), threads = 32 * stream_warps(sets);
+  const int64_t rows = int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads), row_tiles = (rows + 8 * sets - 1) / (8 * sets);
+  const int64_t tiles = (int64_t(a.max_context_len) + qstream::kTileKeys - 1) / qstream::kTileKeys;
+  const bool fits = a.num_seqs <= threads && num_groups <= threads && a.num_tokens <= kStepTokens &&
+                    (a.max_q_len == 1 || rows <= kMaxRows) &&
+                    double(tiles) * double(row_tiles) * a.num_kv_heads * a.num_seqs < double(1 << 30);
+  if (fits) return run_step(a, cu_groups, prefix_lens, num_groups, workspace, stream);
+  const PrefixSizes z = listed_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, a.max_context_len);
+  PrefixWork w;
+  cb_status st = prefix_work(a, nullptr, nullptr, 0, z, stream_warps(sets), 2.0f * HD * float(a.num_kv_heads), workspace, &w);
+  if (st == CB_OK) st = launch_prefix_plan(a, w, stream);
+  CUtensorMap tk, tv;
+  if (st == CB_OK) st = encode_pools(a, qstream::kTileKeys, &tk, &tv);
+  if (st == CB_OK) st = allow_shared_memory();
+  if (st != CB_OK) return st;
+  cudaError_t e = launch_kernel(sets == 1 ? q8_streams_kernel<1> : q8_streams_kernel<2>, dim3(unsigned(w.num_sms)),
+                                dim3(32 * stream_warps(sets)), stream_smem(sets), stream, true, tk, tv, a, w);
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: launch");
+  return launch_prefix_join(a, w, stream);
+}
+
+}  // namespace cb

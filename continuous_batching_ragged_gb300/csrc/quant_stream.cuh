@@ -38,7 +38,6 @@ using stream::kTileKeys;
 using stream::ldmatrix4;
 using stream::ldmatrix4_trans;
 using stream::pack2;
-using stream::SmallStep;
 using stream::Unit;
 
 constexpr uint32_t kBox = kTileKeys * kDim;            // 2 KB, rows of 128 bytes, 128-byte swizzled
@@ -48,8 +47,14 @@ constexpr int kBarArrivals = 3;                        // of a stage: the copies
 // Warps of a CTA and tiles in flight of each: as many warps as the registers allow, 192 KB in flight.
 template <int NT>
 struct Shape {
-  static constexpr int kWarps = NT == 1 ? 16 : 8;
-  static constexpr int kStages = NT == 1 ? 3 : 6;
+#ifndef QW1
+#define QW1 16
+#endif
+#ifndef QW2
+#define QW2 8
+#endif
+  static constexpr int kWarps = NT == 1 ? QW1 : QW2;
+  static constexpr int kStages = 48 / kWarps;
   static constexpr int kRows = 8 * NT;                 // query rows of a unit, at most
   static constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr uint32_t kWarpBarBytes = kStages * 16;   // barriers, then (key, value) scales of each stage
@@ -92,17 +97,93 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
-// As stream::run_warp.  `bars`: kStages barriers (initialised for kBarArrivals),
-// then kStages pairs of scales, which `scales` points to.
-template <int NT, bool kSmall>
-__device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttnArgs& a,
-                                         const PrefixWork& w, int n_items, uint32_t ring, uint32_t bars,
-                                         const volatile float2* scales, SuffixItem* slots, int first, int step,
-                                         int claimed_from, const SmallStep small) {
+// Where a warp's units come from: take() describes the next one in `it` (the warp is in step before and after) and
+// returns its key/value head and tiles, no tiles if there is none; ahead() is called at a unit's beginning.
+struct Taken {
+  int hk, n;
+};
+__device__ __forceinline__ int tiles_of(const SuffixItem& it) { return (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys; }
+
+// Units (item, key/value head) that a plan kernel listed: the first two are given, the later ones claimed.
+struct ListedUnits {
+  const PrefixWork& w;
+  int kv_heads, n_units;
+  int first, step, claimed_from;        // first < 0: the first two are claimed as well
+  int given = 0, claimed = 0;
+
+  __device__ __forceinline__ void ahead(int lane, bool more) {
+    claimed = n_units;
+    if (more && lane == 0) claimed = claimed_from + atomicAdd(w.header + 5, 1);
+  }
+  __device__ __forceinline__ Taken take(SuffixItem& it, int lane) {
+    if (first < 0) {
+      int c = 0;
+      if (lane == 0) c = claimed_from + atomicAdd(w.header + 5, 2);
+      first = __shfl_sync(0xffffffffu, c, 0);
+      step = 1;
+    }
+    const int idx = given < 2 ? first + given++ * step : __shfl_sync(0xffffffffu, claimed, 0);
+    if (idx >= n_units) return {0, 0};
+    if (lane < int(sizeof(SuffixItem) / 16))
+      reinterpret_cast<int4*>(&it)[lane] = __ldcg(reinterpret_cast<const int4*>(w.items + idx / kv_heads) + lane);
+    __syncwarp();
+    return {idx % kv_heads, tiles_of(it)};
+  }
+};
+
+// A sequence of a step that every CTA plans for itself.  Its streams, one per (row tile, key/value head), are `tiles`
+// tiles each, laid end to end from `off`; those of the sequences follow one another.
+struct RangeSeq {
+  int off, tiles;
+  int stream0;                          // streams of the sequences before
+  int tok0, q_len, keys;
+};
+// The warp's share of all tiles, [pos, end), or (step > 0) every `step`-th whole stream from `pos` on to `end`.
+// A stream that lies in several shares leaves a record of each row in each of them: a share begins and ends with at most
+// one such part, so its records are rec0 .. rec0 + row_tile - 1 and the row_tile behind.
+struct RangeUnits {
+  const RangeSeq* seqs;
+  int num_seqs, kv_heads, row_tile;
+  int pos, end, step;
+  unsigned rec0;
+  bool begun = false;
+
+  __device__ __forceinline__ void ahead(int, bool) {}
+  __device__ __forceinline__ Taken take(SuffixItem& it, int lane) {
+    if (pos >= end) return {0, 0};
+    int s = 0;                          // the last sequence that starts at or before it; ones without tiles come before
+    for (int hi = num_seqs - 1; s < hi;) {
+      const int mid = (s + hi + 1) >> 1;
+      if ((step ? seqs[mid].stream0 : seqs[mid].off) <= pos) s = mid; else hi = mid - 1;
+    }
+    const RangeSeq q = seqs[s];
+    const int local = pos - (step ? q.stream0 : q.off);
+    const int x = step ? local : local / q.tiles, t0 = step ? 0 : local - x * q.tiles;
+    const int n = step ? q.tiles : min(q.tiles - t0, end - pos);
+    if (lane == 0) {
+      SuffixItem u = {};
+      u.s = s, u.tok0 = q.tok0, u.q_len = q.q_len, u.row0 = x / kv_heads * row_tile, u.ctx = q.keys;
+      u.k0 = t0 * kTileKeys, u.k1 = min(q.keys, (t0 + n) * kTileKeys);
+      u.direct = n == q.tiles;
+      u.rec0 = rec0 + (begun ? row_tile : 0);
+      it = u;
+    }
+    begun = true;
+    pos += step ? step : n;
+    __syncwarp();
+    return {x % kv_heads, n};
+  }
+};
+
+// One warp.  `ring` and `slots` are its own, so are `bars`: kStages barriers (initialised for kBarArrivals), then kStages
+// pairs of scales, which `scales` points to.
+template <int NT, class Units>
+__device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttnArgs& a, float* recs,
+                                         float2* rec_ml, uint32_t ring, uint32_t bars, const volatile float2* scales,
+                                         SuffixItem* slots, Units& units) {
   constexpr int kStages = Shape<NT>::kStages, kRows = Shape<NT>::kRows;
   const int lane = threadIdx.x & 31;
   const int H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv, B = a.block_size;
-  const int n_units = n_items * Hkv;
   const int boxes = a.num_blocks * Hkv;
   const int g = lane >> 2, t = lane & 3;                 // fragment row and column pair
   const uint32_t scale_at = bars + 8 * kStages;
@@ -116,36 +197,13 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
     raise_error(a.err, kErrBounds);
     return boxes;
   };
-  auto load_unit = [&](int idx, Unit& u, SuffixItem& it) {
-    u.n = u.hk = u.issued = u.zt = u.z = 0;
-    if (idx >= n_units) return;
+  auto load_unit = [&](Unit& u, SuffixItem& it) {
     __syncwarp();                                        // every lane is done with the slot's last item
-    if (kSmall) {
-      const int item = idx / Hkv;
-      int s = 0;                                         // the last sequence that starts at or before it
-      for (int hi = small.num_seqs - 1; s < hi;) {
-        const int mid = (s + hi + 1) >> 1;
-        if (small.seqs[mid].item0 <= item) s = mid; else hi = mid - 1;
-      }
-      if (lane == 0) {
-        const stream::SmallSeq q = small.seqs[s];
-        const int local = item - q.item0, row = local / q.nch, chunk = local - row * q.nch;
-        SuffixItem x = {};
-        x.s = s, x.tok0 = q.tok0, x.q_len = q.q_len, x.row0 = kRows * row, x.ctx = q.keys;
-        x.k0 = chunk * small.len * kTileKeys;
-        x.k1 = x.k0 + min(q.keys - x.k0, small.len * kTileKeys);
-        x.rec0 = q.rec0 + chunk, x.rec_step = q.nch, x.direct = q.nch == 1;
-        it = x;
-      }
-    } else if (lane < int(sizeof(SuffixItem) / 16)) {
-      reinterpret_cast<int4*>(&it)[lane] = __ldcg(reinterpret_cast<const int4*>(w.items + idx / Hkv) + lane);
-    }
-    __syncwarp();
-    u.hk = idx % Hkv;
-    u.n = (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys;
-    u.z = load_pages(it, u.hk, u.n, 0);
+    const Taken next = units.take(it, lane);
+    u.n = next.n, u.hk = next.hk;
+    u.issued = u.zt = u.z = 0;
+    if (u.n > 0) u.z = load_pages(it, u.hk, u.n, 0);
   };
-  auto claim = [&]() -> int { return lane == 0 ? claimed_from + atomicAdd(w.header + 5, 1) : 0; };
 
   uint32_t issued = 0, consumed = 0;                     // ring positions
   int st_in = 0, st_out = 0;                             // their stages
@@ -153,17 +211,8 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
 
   Unit cur, nxt;
   int slot = 0;                                          // of the current unit; the next one's is the other
-  int given = first + step;                              // kSmall: the last unit taken
-  {
-    int c0 = first, c1 = first + step;
-    if (first < 0) {
-      if (lane == 0) c0 = claimed_from + atomicAdd(w.header + 5, 2);
-      c0 = __shfl_sync(0xffffffffu, c0, 0);
-      c1 = c0 + 1;
-    }
-    load_unit(c0, cur, slots[0]);
-    load_unit(c1, nxt, slots[1]);
-  }
+  load_unit(cur, slots[0]);
+  load_unit(nxt, slots[1]);
   // Requests tiles of the current unit, then of the next, while stages are free.
   auto top_up = [&]() {
     while (issued - consumed < uint32_t(kStages)) {
@@ -205,9 +254,7 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
   while (cur.n > 0) {
     const SuffixItem& it = slots[slot];
     top_up();
-    int ahead = n_units;
-    if (kSmall) ahead = given = min(given, n_units) + step;
-    else if (nxt.n > 0) ahead = claim();                 // for the unit after the next; read at this one's end
+    units.ahead(lane, nxt.n > 0);                        // for the unit after the next, taken at this one's end
     // The unit's query rows as B fragments in f16 (columns past the sequence's are zero), and of this lane's two
     // columns per set the factor of a score without its block's scale, and the keys that the row sees: all before
     // its own token's, and its own.
@@ -374,15 +421,16 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
 #pragma unroll
           for (int j = 0; j < 8; ++j) dst[8 * j] = pack2(o[n][j][e] * f, o[n][j][2 + e] * f);
         } else {
-          const size_t at = size_t(it.rec0) + (size_t(tok) * H + h) * it.rec_step;
-          float2* rec = reinterpret_cast<float2*>(w.recs + at * kDim) + g;
+          // records of a listed item's rows are `rec_step` apart in the order of tokens and heads, of a share's in the tile's
+          const size_t at = size_t(it.rec0) + (it.rec_step ? (size_t(tok) * H + h) * it.rec_step : size_t(8 * n + 2 * t + e));
+          float2* rec = reinterpret_cast<float2*>(recs + at * kDim) + g;
 #pragma unroll
           for (int j = 0; j < 8; ++j) __stcg(rec + 8 * j, make_float2(o[n][j][e] * to_m, o[n][j][2 + e] * to_m));
-          if (g == 0) __stcg(w.rec_ml + at, make_float2(m[n][e], sum));
+          if (g == 0) __stcg(rec_ml + at, make_float2(m[n][e], sum));
         }
       }
     cur = nxt;
-    load_unit(__shfl_sync(0xffffffffu, ahead, 0), nxt, slots[slot]);
+    load_unit(nxt, slots[slot]);
     slot ^= 1;
   }
   if (!ok && lane == 0) raise_error(a.err, kErrTimeout | kSiteDecodeRing);

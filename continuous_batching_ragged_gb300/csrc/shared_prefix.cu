@@ -45,7 +45,6 @@
 #include "runtime.h"
 #include "shared_prefix.h"
 #include "sm100_ptx.cuh"
-#include "quant_stream.cuh"
 #include "suffix_stream.cuh"
 
 namespace cb {
@@ -106,8 +105,6 @@ constexpr int kJobCache = 768;           // jobs whose first piece is kept in sh
 constexpr int kExtraPieces = 1024;       // pieces beyond one per (row tile pair, key/value head)
 constexpr int64_t kExtraRecs = 131072;   // records beyond two per row (69 MB)
 constexpr int kMinChunkTiles = 4;        // shortest chunk of streamed keys, in 16-key tiles
-constexpr int kStreamRows = 16;          // query rows per row tile of a stream
-constexpr int kUnitsPerWarp = 3;         // streamed units that each warp should get
 constexpr int kMaxSms = 160;             // SMs that the lists are sized for
 // Query rows per key/value head up to which a sequence's own keys are streamed,
 // once per 16 rows; beyond, they are pieces.
@@ -1194,36 +1191,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // it, which have no work in the one case (64 sequences of 1000 keys, a group each, 58 us;
 // 51 without them, 69 by the plan) and are late in the other (200 behind 4096 keys among
 // empty groups 55 us; 51 by the plan alone, 269 here).
-// The streams of a kernel, by NT: 0 over a bf16 cache, else sets of 8 query rows over one in 8 bits.
-template <int NT>
-struct StreamShape : qstream::Shape<NT> {};
-template <>
-struct StreamShape<0> {
-  static constexpr int kWarps = kStreamWarps, kStages = stream::kStages;
-  static constexpr uint32_t kWarpBarBytes = kStages * 8, kOffBars = stream::kRingBytes;
-  static constexpr uint32_t kOffSlots = kOffBars + stream::kBarBytes, kSmem = kOffSlots + stream::kSlotBytes + 1024;
-  static_assert(kOffSlots % 16 == 0 && kSmem <= 220 * 1024, "shared memory");
-};
-template <int NT>
-__device__ __forceinline__ void init_stage_bars(uint32_t bars) {
-  for (int st = 0; st < StreamShape<NT>::kStages; ++st) mbar_init(bars + 8 * st, NT == 0 ? 1 : qstream::kBarArrivals);
-  fence_mbar_init();
-}
-template <int NT, bool kSmall>
-__device__ __forceinline__ void run_stream(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttnArgs& a,
-                                           const PrefixWork& w, int n_items, uint8_t* gsm, uint32_t base, int warp, int first,
-                                           int step, int claimed_from, const stream::SmallStep& small) {
-  using S = StreamShape<NT>;
-  const uint32_t bars = base + S::kOffBars + warp * S::kWarpBarBytes;
-  SuffixItem* slots = reinterpret_cast<SuffixItem*>(gsm + S::kOffSlots) + 2 * warp;
-  if constexpr (NT == 0)
-    stream::run_warp<kSmall>(tm_k, tm_v, a, w, n_items, base + warp * S::kStages * stream::kStageBytes, bars, slots, first, step,
-                             claimed_from, small);
-  else
-    qstream::run_warp<NT, kSmall>(tm_k, tm_v, a, w, n_items, base + warp * S::kStages * qstream::kStageBytes, bars,
-                                  reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * S::kStages), slots, first, step,
-                                  claimed_from, small);
-}
+constexpr int kSmallThreads = 32 * kStreamWarps;
+constexpr int kSmallSeqs = kSmallThreads;
 constexpr int kSmallTokens = 4096;
 // Contexts up to which a small step's rows are one chunk each, written at once, where the
 // join and its launch cost more than the longer chunks: few units wait for every
@@ -1235,6 +1204,9 @@ constexpr int kOneChunkKeysFew = 128, kOneChunkKeysMany = 384;
 constexpr int kManyUnitsPerSm = 2;
 // Shortest chunk: all of it in flight at once (2 rows of 320 keys: 8.7 us, 9.1 with one more tile).
 constexpr int kSmallChunkTiles = stream::kStages;
+constexpr uint32_t kSmallOffBars = stream::kRingBytes, kSmallOffSlots = kSmallOffBars + stream::kBarBytes;
+constexpr uint32_t kSmallSmem = kSmallOffSlots + stream::kSlotBytes + 1024;
+static_assert(kSmallOffSlots % 16 == 0 && kSmallSmem <= 220 * 1024, "shared memory");
 
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
@@ -1242,23 +1214,23 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
   return v;
 }
 
-template <int NT>
-__global__ void __launch_bounds__(32 * StreamShape<NT>::kWarps, 1)
+__global__ void __launch_bounds__(kSmallThreads, 1)
     small_step_kernel(const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
                       const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
-  constexpr int kWarps = StreamShape<NT>::kWarps, kThreads = 32 * kWarps, kSeqs = kThreads;   // a thread for each sequence
   extern __shared__ uint8_t smem_raw[];
-  __shared__ stream::SmallSeq seqs[kSeqs];
-  __shared__ int group_s0[kSeqs], group_p[kSeqs];
-  __shared__ int64_t sums[4][kWarps];
+  __shared__ stream::SmallSeq seqs[kSmallSeqs];
+  __shared__ int group_s0[kSmallSeqs], group_p[kSmallSeqs];
+  __shared__ int64_t sums[4][kStreamWarps];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* gsm = smem_raw + (base - raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool writer = blockIdx.x == 0;             // of what the join reads, and of the errors
+  const uint32_t bars = base + kSmallOffBars + warp * stream::kStages * 8;
   const int S = a.num_seqs, T = a.num_tokens, NG = w.num_groups, H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv;
 
   if (lane == 0) {
-    init_stage_bars<NT>(base + StreamShape<NT>::kOffBars + warp * StreamShape<NT>::kWarpBarBytes);
+    for (int st = 0; st < stream::kStages; ++st) mbar_init(bars + 8 * st, 1);
+    fence_mbar_init();
     if (warp == 0) {
       tma_prefetch_desc(&tm_k16);
       tma_prefetch_desc(&tm_v16);
@@ -1267,13 +1239,10 @@ __global__ void __launch_bounds__(32 * StreamShape<NT>::kWarps, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");   // it may start while the stream's last kernel ends
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int s0 = 0, s1 = 0, p = 0, c0 = 0, q_len = 0, n = 0;
-  if (tid < NG) {
-    if (w.cu_groups) s0 = w.cu_groups[tid], s1 = w.cu_groups[tid + 1], p = w.prefix_lens[tid];
-    else s1 = S;
-  }
+  if (tid < NG) s0 = w.cu_groups[tid], s1 = w.cu_groups[tid + 1], p = w.prefix_lens[tid];
   if (tid < S) c0 = a.cu_seqlens_q[tid], q_len = a.cu_seqlens_q[tid + 1] - c0, n = w.context_lens[tid];
   if (writer)
-    for (int t = tid; t < T; t += kThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
+    for (int t = tid; t < T; t += kSmallThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
   group_s0[tid] = s0;
   group_p[tid] = p;
   int bad = tid < NG && (s0 < 0 || s1 < s0 || s1 > S || (tid == 0 && s0 != 0) || (tid == NG - 1 && s1 != S));
@@ -1295,10 +1264,10 @@ __global__ void __launch_bounds__(32 * StreamShape<NT>::kWarps, 1)
   const int64_t my_tiles = warp_sum(int64_t(tiles) * rt * Hkv), my_rows = warp_sum(int64_t(rt) * Hkv);
   if (lane == 0) sums[0][warp] = my_tiles, sums[3][warp] = my_rows;
   __syncthreads();
-  const int warps = int(gridDim.x) * kWarps;
+  const int warps = int(gridDim.x) * kStreamWarps;
   int64_t all_tiles = 0, spare = warps;            // ceil(x / L) is less than x / L + 1 for each row tile and head
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) all_tiles += sums[0][i], spare -= sums[3][i];
+  for (int i = 0; i < kStreamWarps; ++i) all_tiles += sums[0][i], spare -= sums[3][i];
   // One unit a warp, where there are warps enough: a unit's beginning and end cost as much as some tiles (6 sequences
   // behind 4900 keys 13.2 us, with kUnitsPerWarp units a warp 18.5; one of 130,000 keys 89 and 99)
   const int64_t units = spare > 0 ? spare : w.stream_units, per = (all_tiles + units - 1) / units;
@@ -1316,7 +1285,7 @@ __global__ void __launch_bounds__(32 * StreamShape<NT>::kWarps, 1)
   item0 -= items, rec0 -= recs;
   int64_t all_items = 0, all_recs = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
+  for (int i = 0; i < kStreamWarps; ++i) {
     if (i < warp) item0 += sums[1][i], rec0 += sums[2][i];
     all_items += sums[1][i], all_recs += sums[2][i];
   }
@@ -1333,31 +1302,9 @@ __global__ void __launch_bounds__(32 * StreamShape<NT>::kWarps, 1)
     }
   }
   __syncthreads();
-  run_stream<NT, true>(&tm_k16, &tm_v16, a, w, bad ? 0 : int(all_items), gsm, base, warp,
-                       warp * int(gridDim.x) + int(blockIdx.x), warps, 0, stream::SmallStep{seqs, S, L});
-}
-
-// The streams of a step over a cache in 8 bits, as the plan lists them.
-template <int NT>
-__global__ void __launch_bounds__(32 * StreamShape<NT>::kWarps, 1)
-    q8_streams_kernel(const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
-                      const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
-  using Sh = StreamShape<NT>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane == 0) init_stage_bars<NT>(base + Sh::kOffBars + warp * Sh::kWarpBarBytes);
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan has finished
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int n_items = __ldcg(w.header + 4);
-  if (uint32_t(__ldcg(w.header + 2)) != w.tag || n_items < 0 || n_items > w.item_cap) {   // a plan of another call: no work
-    if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, kErrInvalid);
-    n_items = 0;
-  }
-  __syncwarp();
-  const int warps = int(gridDim.x) * Sh::kWarps;
-  run_stream<NT, false>(&tm_k16, &tm_v16, a, w, n_items, smem_raw + (base - raw), base, warp,
-                        warp * int(gridDim.x) + int(blockIdx.x), warps, 2 * warps, stream::SmallStep{});
+  stream::run_warp<true>(&tm_k16, &tm_v16, a, w, bad ? 0 : int(all_items), base + warp * stream::kStages * stream::kStageBytes,
+                         bars, reinterpret_cast<SuffixItem*>(gsm + kSmallOffSlots) + 2 * warp,
+                         warp * int(gridDim.x) + int(blockIdx.x), warps, 0, stream::SmallStep{seqs, S, L});
 }
 
 // A warp joins kJoinRows query heads of a token at a time and goes on to the next
@@ -1542,17 +1489,16 @@ bool g_attr_set[64] = {};
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Capacities of a step's lists.
-struct PrefixSizes {
-  size_t S, T, NG, pieces, items, prefix_recs, piece_recs, own_recs;
-};
 int tile_tokens(int group_heads) { return BM / group_heads; }
+
+}  // namespace
+
 PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
-                         int32_t max_context_len, bool q8) {
+                         int32_t max_context_len, int stream_warps, bool pieces) {
   PrefixSizes z;
   z.S = size_t(num_seqs), z.T = size_t(num_tokens), z.NG = size_t(std::max(num_groups, 1));
   const size_t G = size_t(num_q_heads / num_kv_heads), rows = z.T * size_t(num_q_heads);
-  const bool chunks = !q8 && z.T > z.S && (z.T - z.S + 1) * G > size_t(kMaxStreamRows);   // where every sequence has a token
+  const bool chunks = pieces && z.T > z.S && (z.T - z.S + 1) * G > size_t(kMaxStreamRows);   // where every sequence has a token
   // uncut: groups that share have two sequences or more; chunks are all of their tokens
   const size_t pairs = z.T / (2 * size_t(tile_tokens(int(G))));
   z.pieces = size_t(num_kv_heads) * (pairs + std::min(z.NG, z.S / 2) + 1 + (chunks ? pairs + z.S : 0)) + kExtraPieces;
@@ -1560,7 +1506,7 @@ PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_
   z.piece_recs = chunks ? rows * 2 + size_t(kExtraRecs) : 0;
   // ceil(x / L) <= x / L + 1 for every streamed sequence, and all x / L together are at most the units aimed for,
   // twice that where L is halved
-  const size_t units = 2 * size_t(kMaxSms) * (q8 ? StreamShape<1>::kWarps : kStreamWarps) * kUnitsPerWarp;
+  const size_t units = 2 * size_t(kMaxSms) * size_t(stream_warps) * kUnitsPerWarp;
   const size_t shortest = size_t(stream::kTileKeys) * std::min(kMinChunkTiles, kSmallChunkTiles);
   const size_t chunks_of_row = (size_t(max_context_len) + shortest - 1) / shortest;
   z.items = z.T * G / kStreamRows + z.S + units + 1;
@@ -1568,14 +1514,16 @@ PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_
   return z;
 }
 
-}  // namespace
-
-size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
-                                     int32_t num_groups, int32_t max_context_len, bool q8) {
-  const PrefixSizes z = prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len, q8);
+size_t prefix_workspace_bytes(const PrefixSizes& z) {
   return 256 + align256(z.NG * 16) + 2 * align256(z.S * 16) + align256((z.NG + z.S) * 4) + align256(z.pieces * sizeof(Piece)) +
          align256(z.items * sizeof(SuffixItem)) + align256(z.T * 16) +
          align256((z.prefix_recs + z.own_recs) * kPrefixRecBytes);
+}
+
+size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
+                                     int32_t num_groups, int32_t max_context_len) {
+  return prefix_workspace_bytes(prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len,
+                                             kStreamWarps, true));
 }
 
 // The tensor maps of the K and V pools, boxes of one block and head.
@@ -1586,12 +1534,7 @@ static cb_status encode_pools(const AttnArgs& a, EncodeTiledFn enc, bool tiles16
   for (int v = 0; v < 2 && r == CUDA_SUCCESS; ++v) {
     void* pool = const_cast<void*>(v ? a.v_pool : a.k_pool);
     CUtensorMap* tm = v ? tv : tk;
-    if (a.k_scale) {                               // 16 rows of a block in 8 bits
-      const cuuint64_t dims[3] = {HD, B, boxes}, strides[2] = {HD, B * HD};
-      const cuuint32_t box[3] = {HD, cuuint32_t(stream::kTileKeys), 1};
-      r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    } else if (tiles16) {                                 // both 64-dim halves of 16 rows at a time, for the streams
+    if (tiles16) {                                 // both 64-dim halves of 16 rows at a time, for the streams
       const cuuint64_t dims[4] = {64, B, 2, boxes}, strides[3] = {HD * 2, 128, B * HD * 2};
       const cuuint32_t box[4] = {64, cuuint32_t(stream::kTileKeys), 2, 1};
       r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1614,14 +1557,7 @@ static cb_status allow_shared_memory() {
   std::lock_guard<std::mutex> lock(g_attr_mutex);
   if (g_attr_set[dev]) return CB_OK;
   cudaError_t e = cudaFuncSetAttribute(prefix_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes));
-  const auto allow = [&e](const void* kernel, uint32_t bytes) {
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-  };
-  allow(reinterpret_cast<const void*>(small_step_kernel<0>), StreamShape<0>::kSmem);
-  allow(reinterpret_cast<const void*>(small_step_kernel<1>), StreamShape<1>::kSmem);
-  allow(reinterpret_cast<const void*>(small_step_kernel<2>), StreamShape<2>::kSmem);
-  allow(reinterpret_cast<const void*>(q8_streams_kernel<1>), StreamShape<1>::kSmem);
-  allow(reinterpret_cast<const void*>(q8_streams_kernel<2>), StreamShape<2>::kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(small_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmallSmem));
   if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: shared memory attribute");
   g_attr_set[dev] = true;
   return CB_OK;
@@ -1649,13 +1585,6 @@ static cb_status launch_prefix_tc(const AttnArgs& a, const PrefixWork& w, cudaSt
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: launch");
 }
 
-// Sets of 8 query rows of a stream's units; 0: a bf16 cache.
-int stream_sets(const AttnArgs& a) {
-  return !a.k_scale ? 0 : int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= 8 ? 1 : 2;
-}
-int stream_warps(int sets) { return sets == 0 ? StreamShape<0>::kWarps : sets == 1 ? StreamShape<1>::kWarps : StreamShape<2>::kWarps; }
-int stream_smem(int sets) { return sets == 0 ? StreamShape<0>::kSmem : sets == 1 ? StreamShape<1>::kSmem : StreamShape<2>::kSmem; }
-
 static cb_status launch_small_step(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (!enc) return CB_ERR_CUDA;
@@ -1663,27 +1592,17 @@ static cb_status launch_small_step(const AttnArgs& a, const PrefixWork& w, cudaS
   cb_status st = encode_pools(a, enc, true, &tk16, &tv16);
   if (st == CB_OK) st = allow_shared_memory();
   if (st != CB_OK) return st;
-  const int sets = stream_sets(a);
-  auto kernel = sets == 0 ? small_step_kernel<0> : sets == 1 ? small_step_kernel<1> : small_step_kernel<2>;
-  cudaError_t e = launch_kernel(kernel, dim3(unsigned(w.num_sms)), dim3(32 * stream_warps(sets)), stream_smem(sets), stream, true,
+  cudaError_t e = launch_kernel(small_step_kernel, dim3(unsigned(w.num_sms)), dim3(kSmallThreads), kSmallSmem, stream, true,
                                 tk16, tv16, a, w);
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: launch");
 }
 
-static cb_status launch_q8_streams(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
-  EncodeTiledFn enc = encode_tiled_fn();
-  if (!enc) return CB_ERR_CUDA;
-  CUtensorMap tk16, tv16;
-  cb_status st = encode_pools(a, enc, true, &tk16, &tv16);
-  if (st == CB_OK) st = allow_shared_memory();
-  if (st != CB_OK) return st;
-  const int sets = stream_sets(a);
-  cudaError_t e = launch_kernel(sets == 1 ? q8_streams_kernel<1> : q8_streams_kernel<2>, dim3(unsigned(w.num_sms)),
-                                dim3(32 * stream_warps(sets)), stream_smem(sets), stream, true, tk16, tv16, a, w);
-  return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: launch");
+cb_status launch_prefix_plan(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
+  cudaError_t e = launch_kernel(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, a, w);
+  return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: plan launch");
 }
 
-static cb_status launch_join(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
+cb_status launch_prefix_join(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream) {
   if (wide_join(a, w)) {
     cudaError_t e = launch_kernel(join_wide_kernel, dim3(unsigned(a.num_tokens) * unsigned(a.num_heads)), dim3(kJoinThreads), 0,
                                   stream, true, a, w);
@@ -1698,29 +1617,24 @@ static cb_status launch_join(const AttnArgs& a, const PrefixWork& w, cudaStream_
   return e == cudaSuccess ? CB_OK : cuda_fail(e, "shared prefixes: join launch");
 }
 
-// A step with shared prefixes on one stream: the plan, the pieces and streams (a small
-// step's streams alone), and the join, each a programmatic dependent of the one before.
-cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
-                            void* workspace, cudaStream_t stream) {
-  NvtxRange nvtx("cb.shared_prefix");
+cb_status prefix_work(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
+                      const PrefixSizes& z, int stream_warps, float key_bytes, void* workspace, PrefixWork* work) {
   if (int64_t(a.num_blocks) * a.num_kv_heads >= (int64_t(1) << 31))
     return fail(CB_ERR_UNSUPPORTED, "shared prefixes: num_blocks * num_kv_heads must fit in int32");
-  const bool q8 = a.k_scale != nullptr;
-  if (q8) cu_groups = prefix_lens = nullptr, num_groups = 0;
-  const PrefixSizes z = prefix_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups, a.max_context_len, q8);
   if (z.pieces > 0x7FFFFFFF || z.items > size_t(0x7FFFFFFF / a.num_kv_heads) || z.prefix_recs > 0x7FFFFFFF ||
       z.own_recs > 0x7FFFFFFF)
     return fail(CB_ERR_UNSUPPORTED, "shared prefixes: too many tokens");
-  PrefixWork w;
+  PrefixWork& w = *work;
   w.cu_groups = cu_groups;
   w.prefix_lens = prefix_lens;
   w.context_lens = a.context_lens;
   w.num_groups = std::max(num_groups, 1);
-  w.key_bytes = 2.0f * HD * float(a.num_kv_heads) * (q8 ? 1.0f : 2.0f);
   w.num_sms = sm_count();
+  w.key_bytes = key_bytes;
   w.tile_tokens = tile_tokens(a.num_heads / a.num_kv_heads);
-  const int warps = stream_warps(stream_sets(a)), small_seqs = 32 * warps;
-  w.stream_units = std::min(w.num_sms, kMaxSms) * warps * kUnitsPerWarp;
+  w.stream_units = std::min(w.num_sms, kMaxSms) * stream_warps * kUnitsPerWarp;
+  w.min_chunk_tiles = kMinChunkTiles;
+  w.max_sharers = -1;
   w.piece_cap = int32_t(z.pieces);
   w.item_cap = int32_t(z.items);
   w.prefix_rec_cap = int64_t(z.prefix_recs);
@@ -1744,32 +1658,43 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   w.rec_ml = reinterpret_cast<float2*>(w.recs + (z.prefix_recs + z.own_recs) * HD);
   static std::atomic<uint32_t> next_tag{1};
   w.tag = next_tag.fetch_add(1);
+  return CB_OK;
+}
+
+// A step with shared prefixes on one stream: the plan, the pieces and streams (a small
+// step's streams alone), and the join, each a programmatic dependent of the one before.
+cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
+                            void* workspace, cudaStream_t stream) {
+  NvtxRange nvtx("cb.shared_prefix");
+  const PrefixSizes z = prefix_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups, a.max_context_len,
+                                     kStreamWarps, true);
+  PrefixWork w;
+  cb_status st = prefix_work(a, cu_groups, prefix_lens, num_groups, z, kStreamWarps, 4.0f * HD * float(a.num_kv_heads), workspace, &w);
+  if (st != CB_OK) return st;
 
   // Small: what sharing could save does not pay for it, and no sequence's own keys are pieces.  All sequences but
   // one of each group could share, at most their whole contexts, and any group but one may be empty.  With at
   // least two sequences a group, counting all groups misses half of the sharers at most (84 behind 1024 keys
   // among 41 empty groups 53 us, 28 without those); with fewer, the device counts.
   const int64_t row_tiles = (int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) + kStreamRows - 1) / kStreamRows;
-  const double each = double(a.max_context_len) * w.key_bytes * row_tiles;
-  const int sharers = int(std::min(double(small_seqs), std::ceil(double(kSmallUs) * kBytesPerUs / each) - 1.0));
-  const bool fits = a.num_seqs <= small_seqs && num_groups <= small_seqs && a.num_tokens <= kSmallTokens &&
+  const double each = double(a.max_context_len) * a.num_kv_heads * (4.0 * HD) * row_tiles;
+  const int sharers = int(std::min(double(kSmallSeqs), std::ceil(double(kSmallUs) * kBytesPerUs / each) - 1.0));
+  const bool fits = a.num_seqs <= kSmallSeqs && num_groups <= kSmallSeqs && a.num_tokens <= kSmallTokens &&
                     (a.max_q_len == 1 || int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= kMaxStreamRows);
-  const bool maybe = fits && (num_groups == 0 || a.num_seqs - num_groups <= sharers);
-  const bool small = maybe && (num_groups == 0 || a.num_seqs - 1 <= sharers || num_groups <= a.num_seqs / 2);
+  const bool maybe = fits && a.num_seqs - num_groups <= sharers;
+  const bool small = maybe && (a.num_seqs - 1 <= sharers || num_groups <= a.num_seqs / 2);
   const bool both = maybe && !small;
   w.max_sharers = both ? sharers : -1;
   const bool many = int64_t(a.num_seqs) * a.num_kv_heads >= int64_t(kManyUnitsPerSm) * w.num_sms;
   const bool one_chunk = maybe && a.max_context_len <= (many ? kOneChunkKeysMany : kOneChunkKeysFew);
   w.min_chunk_tiles = one_chunk ? kOneChunkKeysMany / stream::kTileKeys : kSmallChunkTiles;
-  cb_status st = CB_OK;
   if (maybe) st = launch_small_step(a, w, stream);
   if (st == CB_OK && !small) {
-    cudaError_t e = launch_kernel(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, true, a, w);
-    if (e != cudaSuccess) return cuda_fail(e, "shared prefixes: plan launch");
-    st = q8 ? launch_q8_streams(a, w, stream) : launch_prefix_tc(a, w, stream);
+    st = launch_prefix_plan(a, w, stream);
+    if (st == CB_OK) st = launch_prefix_tc(a, w, stream);
   }
   if (st != CB_OK || (small && one_chunk)) return st;
-  return launch_join(a, w, stream);
+  return launch_prefix_join(a, w, stream);
 }
 
 }  // namespace cb

@@ -83,5 +83,23 @@ struct PrefixWork {
 };
 
 constexpr int kStreamWarps = 8;          // warps of a CTA that stream own keys, each with units of its own
+constexpr int kStreamRows = 16;          // query rows per row tile of a listed stream
+constexpr int kUnitsPerWarp = 3;         // streamed units that each warp should get
+
+// Capacities of a step's lists.  stream_warps: warps that stream, per SM; pieces: whether the kernels behind the plan take
+// pieces at all.
+struct PrefixSizes {
+  size_t S, T, NG, pieces, items, prefix_recs, piece_recs, own_recs;
+};
+PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
+                         int32_t max_context_len, int stream_warps, bool pieces);
+size_t prefix_workspace_bytes(const PrefixSizes& z);
+// Fills `w` for a step and carves its workspace, whose lists sizes have to be `z`.  num_groups 0 (cu_groups and prefix_lens
+// null): no sequence shares.  key_bytes: K and V of a key, all key/value heads.
+cb_status prefix_work(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
+                      const PrefixSizes& z, int stream_warps, float key_bytes, void* workspace, PrefixWork* w);
+// The plan, and the join of the records of the rows that it listed: programmatic dependents of what is before them.
+cb_status launch_prefix_plan(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream);
+cb_status launch_prefix_join(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream);
 
 }  // namespace cb
