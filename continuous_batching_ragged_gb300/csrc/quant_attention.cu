@@ -18,6 +18,7 @@
 
 #include "device_common.cuh"
 #include "kernels.h"
+#include "quant_pieces.cuh"
 #include "quant_stream.cuh"
 #include "runtime.h"
 #include "shared_prefix.h"
@@ -36,6 +37,9 @@ constexpr int kMaxSms = 160;             // SMs that the records are sized for
 constexpr int kMaxRows = 64;             // query rows per key/value head that are streamed, 8 or 16 at a time
 constexpr int kStepTokens = 4096;        // of a step without a plan kernel
 constexpr int kMinShareTiles = 3;        // shortest share of a warp
+constexpr double kSharingBytes = 1.9e8;  // reads that sharing has to be able to save, for the plan to be worth its time
+// What the plan's estimates go by, in microseconds and bytes.
+constexpr float kTileUsTwo = 2.2f, kTileUsOne = 1.6f, kStreamBytesPerUsPerSm = 3.0e4f;
 
 // What the CTAs of a step without a plan kernel make of it, for the join.
 struct StepWork {
@@ -138,31 +142,67 @@ __global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
                         reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
 }
 
-// The streams of a step as the plan lists them.
-template <int NT>
-__global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
-    q8_streams_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
-  using Sh = Shape<NT>;
+// A step as the plan lists it, one CTA per SM.  The first header[6] CTAs take pieces, then stream like the rest, each of
+// their first eight warps on its own.
+__global__ void __launch_bounds__(qpieces::kThreads, 1)
+    q8_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k64,
+                 const __grid_constant__ CUtensorMap tm_v64, const __grid_constant__ CUtensorMap tm_k16,
+                 const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
+  using Sh = Shape<2>;
+  static_assert(Sh::kWarps == 8 && Sh::kOffBars >= qpieces::kOffStaged && Sh::kSmem - 1024 <= qpieces::kOffBar, "streams over pieces");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* gsm = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t bars = base + Sh::kOffBars + warp * Sh::kWarpBarBytes;
-  if (lane == 0) init_bars<NT>(bars);
+  // Set up while the plan still runs: barriers, and tensor memory for pieces
+  if (threadIdx.x == 0) qpieces::init_bars(base);
+  if (warp == qpieces::kWarpMma) {
+    tmem_alloc(base + qpieces::kOffTmemSlot, qpieces::kTmemCols);
+    tmem_relinquish();
+  } else if (warp == qpieces::kWarpK && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k64);
+    tma_prefetch_desc(&tm_v64);
+    tma_prefetch_desc(&tm_k16);
+    tma_prefetch_desc(&tm_v16);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan has finished
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int n_items = __ldcg(w.header + 4);
-  if (uint32_t(__ldcg(w.header + 2)) != w.tag || n_items < 0 || n_items > w.item_cap) {   // a plan of another call: no work
+  int n_pieces = __ldcg(w.header), n_items = __ldcg(w.header + 4);
+  const int working = __ldcg(w.header + 6);
+  if (uint32_t(__ldcg(w.header + 2)) != w.tag || n_pieces < 0 || n_pieces > w.piece_cap || n_items < 0 ||
+      n_items > w.item_cap) {                      // a plan of another call: no work
     if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, kErrInvalid);
-    n_items = 0;
+    n_pieces = n_items = 0;
   }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gsm + qpieces::kOffTmemSlot);
+  const int with_pieces = min(n_pieces, min(int(gridDim.x), working));   // CTAs that take pieces first
+  const bool pieces_first = int(blockIdx.x) < with_pieces;
+  bool ok = true;
+  if (pieces_first) ok = qpieces::run_pieces(&tm_q, &tm_k64, &tm_v64, a, w, gsm, base, tmem, n_pieces, with_pieces);
+  if (warp == qpieces::kWarpMma) {
+    __syncwarp();
+    tmem_dealloc(tmem, qpieces::kTmemCols);
+  }
+  if (warp >= Sh::kWarps) {
+    qpieces::regs_down<24>();
+    return;
+  }
+  qpieces::regs_up<232>();
+  if (!ok) return;
+  // Streams: the rings lie over the tiles, their barriers and items over the staging buffers.  The first units are given to
+  // the CTAs that start with them, neighbouring units to different SMs; the rest is claimed.
+  const uint32_t bars = base + Sh::kOffBars + warp * Sh::kWarpBarBytes;
+  if (lane == 0) init_bars<2>(bars);
   __syncwarp();
-  const int warps = int(gridDim.x) * Sh::kWarps;
-  qstream::ListedUnits units{w, a.num_kv_heads, n_items * a.num_kv_heads, warp * int(gridDim.x) + int(blockIdx.x), warps, 2 * warps};
-  qstream::run_warp<NT>(&tm_k, &tm_v, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
-                        reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * Sh::kStages),
-                        reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
+  const int others = int(gridDim.x) - with_pieces, warps = others * Sh::kWarps;
+  qstream::ListedUnits units{w, a.num_kv_heads, n_items * a.num_kv_heads,
+                             pieces_first ? -1 : warp * others + int(blockIdx.x) - with_pieces, warps, 2 * warps};
+  qstream::run_warp<2>(&tm_k16, &tm_v16, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
+                       reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * Sh::kStages),
+                       reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
 }
 
 // One row's records, `step` apart from the first on: their weighted sum, by the lanes of a warp, 4 dims each.
@@ -268,8 +308,7 @@ cb_status allow_shared_memory() {
   };
   allow(reinterpret_cast<const void*>(q8_step_kernel<1>), Shape<1>::kSmem);
   allow(reinterpret_cast<const void*>(q8_step_kernel<2>), Shape<2>::kSmem);
-  allow(reinterpret_cast<const void*>(q8_streams_kernel<1>), Shape<1>::kSmem);
-  allow(reinterpret_cast<const void*>(q8_streams_kernel<2>), Shape<2>::kSmem);
+  allow(reinterpret_cast<const void*>(q8_tc_kernel), qpieces::kSmemBytes);
   if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: shared memory attribute");
   g_attr_set[dev] = true;
   return CB_OK;
@@ -295,8 +334,6 @@ cb_status encode_pools(const AttnArgs& a, int rows, CUtensorMap* tk, CUtensorMap
 int stream_sets(const AttnArgs& a) { return int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= 8 ? 1 : 2; }
 int stream_warps(int sets) { return sets == 1 ? Shape<1>::kWarps : Shape<2>::kWarps; }
 int stream_smem(int sets) { return sets == 1 ? Shape<1>::kSmem : Shape<2>::kSmem; }
-constexpr int kMaxWarps = Shape<1>::kWarps;
-static_assert(Shape<2>::kWarps * Shape<2>::kRows <= 2 * kMaxWarps * Shape<1>::kRows && Shape<2>::kWarps <= kMaxWarps, "sizes");
 
 // Records of a step without a plan kernel: two of a row tile for each warp that may have a share.
 size_t step_records(int num_sms) { return size_t(num_sms) * std::max(2 * Shape<1>::kWarps * Shape<1>::kRows, 2 * Shape<2>::kWarps * Shape<2>::kRows); }
@@ -305,8 +342,9 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 size_t step_workspace_bytes(int32_t num_tokens) {
   return 256 + align256(size_t(num_tokens) * 16) + align256(step_records(kMaxSms) * kPrefixRecBytes);
 }
-PrefixSizes listed_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t max_context_len) {
-  return prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, 0, max_context_len, kMaxWarps, false);
+PrefixSizes listed_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
+                         int32_t max_context_len) {
+  return prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len, Shape<2>::kWarps, true);
 }
 
 cb_status run_step(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups, void* workspace,
@@ -343,9 +381,9 @@ cb_status run_step(const AttnArgs& a, const int32_t* cu_groups, const int32_t* p
 }  // namespace
 
 size_t quant_attention_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
-                                       int32_t, int32_t max_context_len) {
-  return std::max(step_workspace_bytes(num_tokens),
-                  prefix_workspace_bytes(listed_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, max_context_len)));
+                                       int32_t num_groups, int32_t max_context_len) {
+  return std::max(step_workspace_bytes(num_tokens), prefix_workspace_bytes(listed_sizes(num_q_heads, num_kv_heads, num_seqs,
+                                                                                        num_tokens, num_groups, max_context_len)));
 }
 
 cb_status run_quant_attention(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
@@ -353,23 +391,43 @@ cb_status run_quant_attention(const AttnArgs& a, const int32_t* cu_groups, const
   NvtxRange nvtx("cb.ragged_attention_q8");
   if (int64_t(a.num_blocks) * a.num_kv_heads >= (int64_t(1) << 31))
     return fail(CB_ERR_UNSUPPORTED, "8-bit attention: num_blocks * num_kv_heads must fit in int32");
-  const int sets = stream_sets(a), threads = 32 * stream_warps(sets);
-  const int64_t rows = int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads), row_tiles = (rows + 8 * sets - 1) / (8 * sets);
+  const int G = a.num_heads / a.num_kv_heads, sets = stream_sets(a), threads = 32 * stream_warps(sets);
+  const int64_t rows = int64_t(a.max_q_len) * G, row_tiles = (rows + 8 * sets - 1) / (8 * sets);
   const int64_t tiles = (int64_t(a.max_context_len) + qstream::kTileKeys - 1) / qstream::kTileKeys;
+  const float key_bytes = 2.0f * HD * float(a.num_kv_heads);
+  // sequences that may share (all but one of each group), and what sharing may save
+  const double saved = num_groups == 0 ? 0.0 : double(a.num_seqs - num_groups) * double(a.max_context_len) * key_bytes;
   const bool fits = a.num_seqs <= threads && num_groups <= threads && a.num_tokens <= kStepTokens &&
-                    (a.max_q_len == 1 || rows <= kMaxRows) &&
+                    (a.max_q_len == 1 || rows <= kMaxRows) && saved <= kSharingBytes &&
                     double(tiles) * double(row_tiles) * a.num_kv_heads * a.num_seqs < double(1 << 30);
   if (fits) return run_step(a, cu_groups, prefix_lens, num_groups, workspace, stream);
-  const PrefixSizes z = listed_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, a.max_context_len);
+
+  const PrefixSizes z = listed_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups, a.max_context_len);
   PrefixWork w;
-  cb_status st = prefix_work(a, nullptr, nullptr, 0, z, stream_warps(sets), 2.0f * HD * float(a.num_kv_heads), workspace, &w);
-  if (st == CB_OK) st = launch_prefix_plan(a, w, stream);
-  CUtensorMap tk, tv;
-  if (st == CB_OK) st = encode_pools(a, qstream::kTileKeys, &tk, &tv);
-  if (st == CB_OK) st = allow_shared_memory();
+  cb_status st = prefix_work(a, cu_groups, prefix_lens, num_groups, z, Shape<2>::kWarps, workspace, &w);
   if (st != CB_OK) return st;
-  cudaError_t e = launch_kernel(sets == 1 ? q8_streams_kernel<1> : q8_streams_kernel<2>, dim3(unsigned(w.num_sms)),
-                                dim3(32 * stream_warps(sets)), stream_smem(sets), stream, true, tk, tv, a, w);
+  w.key_bytes = key_bytes;
+  w.tile_us_two = kTileUsTwo;
+  w.tile_us_one = kTileUsOne;
+  w.stream_rate = kStreamBytesPerUsPerSm;
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return CB_ERR_CUDA;
+  CUtensorMap tq, tk64, tv64, tk16, tv16;
+  // q as [tokens][heads][128]: a box is one key/value head's query heads of tile_tokens tokens, one 64-dim half
+  const cuuint64_t dims[3] = {cuuint64_t(HD), cuuint64_t(a.num_heads), cuuint64_t(a.num_tokens)};
+  const cuuint64_t strides[2] = {cuuint64_t(HD) * 2, cuuint64_t(a.num_heads) * HD * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(w.tile_tokens)}, ones[3] = {1, 1, 1};
+  const CUresult r = enc(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, ones,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(CB_ERR_CUDA, "8-bit attention: encoding the Q tensor map failed (%d)", int(r));
+  st = encode_pools(a, std::min(a.block_size, qpieces::HN), &tk64, &tv64);
+  if (st == CB_OK) st = encode_pools(a, qstream::kTileKeys, &tk16, &tv16);
+  if (st == CB_OK) st = allow_shared_memory();
+  if (st == CB_OK) st = launch_prefix_plan(a, w, stream);
+  if (st != CB_OK) return st;
+  cudaError_t e = launch_kernel(q8_tc_kernel, dim3(unsigned(w.num_sms)), dim3(qpieces::kThreads), qpieces::kSmemBytes, stream, true,
+                                tq, tk64, tv64, tk16, tv16, a, w);
   if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: launch");
   return launch_prefix_join(a, w, stream);
 }

@@ -47,13 +47,7 @@ constexpr int kBarArrivals = 3;                        // of a stage: the copies
 // Warps of a CTA and tiles in flight of each: as many warps as the registers allow, 192 KB in flight.
 template <int NT>
 struct Shape {
-#ifndef QW1
-#define QW1 16
-#endif
-#ifndef QW2
-#define QW2 8
-#endif
-  static constexpr int kWarps = NT == 1 ? QW1 : QW2;
+  static constexpr int kWarps = NT == 1 ? 16 : 8;
   static constexpr int kStages = 48 / kWarps;
   static constexpr int kRows = 8 * NT;                 // query rows of a unit, at most
   static constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;

@@ -110,11 +110,11 @@ constexpr int kMaxSms = 160;             // SMs that the lists are sized for
 // once per 16 rows; beyond, they are pieces.
 constexpr int kMaxStreamRows = 64;
 // Cost model of the segments and of the SM split, in microseconds and bytes.
-constexpr float kTileUsTwo = 1.8f;       // a KV tile against two row tiles, one SM
+constexpr float kTileUsTwo = 1.8f;       // a KV tile against two row tiles
 constexpr float kTileUsOne = 1.4f;       // a KV tile against one row tile, at an SM's share of HBM (0.85 alone)
+constexpr float kStreamBytesPerUsPerSm = 4.2e4f;   // streams of one SM
 constexpr float kPieceUs = 5.0f;         // a piece beyond its tiles: Q, the pipeline's fill, the records
 constexpr float kBytesPerUs = 6.7e6f;    // HBM
-constexpr float kStreamBytesPerUsPerSm = 4.2e4f;   // streams of one SM
 constexpr float kJoinBytesPerUs = 4.0e6f;
 constexpr float kShareUs = 6.0f;          // what a step's pieces and join take at least
 constexpr float kSmallUs = 28.0f;         // the same with the plan, for steps that can do without
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
         shared = (p >> block_shift) << block_shift;
         const float keys = float(shared) * float(s1 - s0 - 1);
         const float cost = float(ceil_div_fast(tokens, 2 * TT) * Hkv) *
-                           (float((shared + BN - 1) / BN) * (tokens <= TT ? kTileUsOne : kTileUsTwo) + kPieceUs);
+                           (float((shared + BN - 1) / BN) * (tokens <= TT ? w.tile_us_one : w.tile_us_two) + kPieceUs);
         // many small groups' pieces take longer than the reads that they save
         // (150 pairs behind 96 keys of 8 heads: 97 us shared, 50 not); the rows of a
         // group that can hold a chunk, more query tokens than one a sequence, are pieces either way
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
       const int2 sg = segments(jb.keys, len);
       const int64_t units = int64_t(ceil_div_fast(jb.tokens, 2 * TT)) * Hkv * sg.x;
       const bool alt = jb.tokens <= TT;
-      const float us = float(sg.y) * (alt ? kTileUsOne : kTileUsTwo) + kPieceUs;
+      const float us = float(sg.y) * (alt ? w.tile_us_one : w.tile_us_two) + kPieceUs;
       pieces += units;
       if (j >= NG) own_recs += int64_t(jb.tokens) * H * sg.x * (alt ? 2 : 1);
       work += float(units) * us;
@@ -401,8 +401,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
       const float per_sm = __fdividef(1.0f, float(k));
       float us = fminf(ceilf(float(pieces) * per_sm) * piece, work * per_sm + piece);
       us = fmaxf(us, piece_bytes * (1.0f / kBytesPerUs));
-      const float beside = fminf(kBytesPerUs * us - piece_bytes, float(w.num_sms - k) * kStreamBytesPerUsPerSm * us);
-      us += __fdividef(fmaxf(0.f, own_bytes - beside), fminf(kBytesPerUs, float(w.num_sms) * kStreamBytesPerUsPerSm));
+      const float beside = fminf(kBytesPerUs * us - piece_bytes, float(w.num_sms - k) * w.stream_rate * us);
+      us += __fdividef(fmaxf(0.f, own_bytes - beside), fminf(kBytesPerUs, float(w.num_sms) * w.stream_rate));
       us += float(recs) * (kPrefixRecBytes / kJoinBytesPerUs);
       key = ((unsigned long long)(__float_as_uint(us)) << 32) | unsigned(k << 16 | n);
     }
@@ -1618,7 +1618,7 @@ cb_status launch_prefix_join(const AttnArgs& a, const PrefixWork& w, cudaStream_
 }
 
 cb_status prefix_work(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
-                      const PrefixSizes& z, int stream_warps, float key_bytes, void* workspace, PrefixWork* work) {
+                      const PrefixSizes& z, int stream_warps, void* workspace, PrefixWork* work) {
   if (int64_t(a.num_blocks) * a.num_kv_heads >= (int64_t(1) << 31))
     return fail(CB_ERR_UNSUPPORTED, "shared prefixes: num_blocks * num_kv_heads must fit in int32");
   if (z.pieces > 0x7FFFFFFF || z.items > size_t(0x7FFFFFFF / a.num_kv_heads) || z.prefix_recs > 0x7FFFFFFF ||
@@ -1630,7 +1630,6 @@ cb_status prefix_work(const AttnArgs& a, const int32_t* cu_groups, const int32_t
   w.context_lens = a.context_lens;
   w.num_groups = std::max(num_groups, 1);
   w.num_sms = sm_count();
-  w.key_bytes = key_bytes;
   w.tile_tokens = tile_tokens(a.num_heads / a.num_kv_heads);
   w.stream_units = std::min(w.num_sms, kMaxSms) * stream_warps * kUnitsPerWarp;
   w.min_chunk_tiles = kMinChunkTiles;
@@ -1669,8 +1668,12 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
   const PrefixSizes z = prefix_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups, a.max_context_len,
                                      kStreamWarps, true);
   PrefixWork w;
-  cb_status st = prefix_work(a, cu_groups, prefix_lens, num_groups, z, kStreamWarps, 4.0f * HD * float(a.num_kv_heads), workspace, &w);
+  cb_status st = prefix_work(a, cu_groups, prefix_lens, num_groups, z, kStreamWarps, workspace, &w);
   if (st != CB_OK) return st;
+  w.key_bytes = 4.0f * HD * float(a.num_kv_heads);
+  w.tile_us_two = kTileUsTwo;
+  w.tile_us_one = kTileUsOne;
+  w.stream_rate = kStreamBytesPerUsPerSm;
 
   // Small: what sharing could save does not pay for it, and no sequence's own keys are pieces.  All sequences but
   // one of each group could share, at most their whole contexts, and any group but one may be empty.  With at

@@ -55,7 +55,11 @@ struct PrefixWork {
   const int32_t* context_lens; // [num_seqs], whole
   int32_t num_groups;
   int32_t num_sms;
+  // what the plan's estimates go by
   float key_bytes;             // K and V of a key, all key/value heads
+  float tile_us_two;           // a KV tile against two row tiles, one SM
+  float tile_us_one;           // against one row tile, at an SM's share of HBM
+  float stream_rate;           // bytes that the streams of one SM read per microsecond
   int32_t tile_tokens;         // query tokens per row tile of a piece
   int32_t stream_units;        // streamed units that the chunk length aims for
   int32_t min_chunk_tiles;     // shortest chunk of a small step's streams, in 16-key tiles
@@ -95,9 +99,9 @@ PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_
                          int32_t max_context_len, int stream_warps, bool pieces);
 size_t prefix_workspace_bytes(const PrefixSizes& z);
 // Fills `w` for a step and carves its workspace, whose lists sizes have to be `z`.  num_groups 0 (cu_groups and prefix_lens
-// null): no sequence shares.  key_bytes: K and V of a key, all key/value heads.
+// null): no sequence shares.  The estimates are left to the caller.
 cb_status prefix_work(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
-                      const PrefixSizes& z, int stream_warps, float key_bytes, void* workspace, PrefixWork* w);
+                      const PrefixSizes& z, int stream_warps, void* workspace, PrefixWork* w);
 // The plan, and the join of the records of the rows that it listed: programmatic dependents of what is before them.
 cb_status launch_prefix_plan(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream);
 cb_status launch_prefix_join(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream);
