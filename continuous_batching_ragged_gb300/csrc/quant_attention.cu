@@ -142,67 +142,70 @@ __global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
                         reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
 }
 
-// A step as the plan lists it, one CTA per SM.  The first header[6] CTAs take pieces, then stream like the rest, each of
-// their first eight warps on its own.
+// The pieces of a step as the plan lists them, one CTA per SM; those beyond the header[6] that take pieces leave their SMs to
+// the streams behind.
 __global__ void __launch_bounds__(qpieces::kThreads, 1)
-    q8_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k64,
-                 const __grid_constant__ CUtensorMap tm_v64, const __grid_constant__ CUtensorMap tm_k16,
-                 const __grid_constant__ CUtensorMap tm_v16, const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
-  using Sh = Shape<2>;
-  static_assert(Sh::kWarps == 8 && Sh::kOffBars >= qpieces::kOffStaged && Sh::kSmem - 1024 <= qpieces::kOffBar, "streams over pieces");
+    q8_pieces_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* gsm = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // Set up while the plan still runs: barriers, and tensor memory for pieces
+  // Set up while the plan still runs: barriers, and tensor memory
   if (threadIdx.x == 0) qpieces::init_bars(base);
   if (warp == qpieces::kWarpMma) {
     tmem_alloc(base + qpieces::kOffTmemSlot, qpieces::kTmemCols);
     tmem_relinquish();
   } else if (warp == qpieces::kWarpK && lane == 0) {
     tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k64);
-    tma_prefetch_desc(&tm_v64);
-    tma_prefetch_desc(&tm_k16);
-    tma_prefetch_desc(&tm_v16);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan has finished
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int n_pieces = __ldcg(w.header), n_items = __ldcg(w.header + 4);
+  int n_pieces = __ldcg(w.header);
   const int working = __ldcg(w.header + 6);
-  if (uint32_t(__ldcg(w.header + 2)) != w.tag || n_pieces < 0 || n_pieces > w.piece_cap || n_items < 0 ||
-      n_items > w.item_cap) {                      // a plan of another call: no work
+  if (uint32_t(__ldcg(w.header + 2)) != w.tag || n_pieces < 0 || n_pieces > w.piece_cap) {   // a plan of another call: no work
     if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, kErrInvalid);
-    n_pieces = n_items = 0;
+    n_pieces = 0;
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gsm + qpieces::kOffTmemSlot);
-  const int with_pieces = min(n_pieces, min(int(gridDim.x), working));   // CTAs that take pieces first
-  const bool pieces_first = int(blockIdx.x) < with_pieces;
-  bool ok = true;
-  if (pieces_first) ok = qpieces::run_pieces(&tm_q, &tm_k64, &tm_v64, a, w, gsm, base, tmem, n_pieces, with_pieces);
+  const int with_pieces = min(n_pieces, min(int(gridDim.x), working));
+  if (int(blockIdx.x) < with_pieces) qpieces::run_pieces(&tm_q, &tm_k, &tm_v, a, w, gsm, base, tmem, n_pieces, with_pieces);
   if (warp == qpieces::kWarpMma) {
     __syncwarp();
     tmem_dealloc(tmem, qpieces::kTmemCols);
   }
-  if (warp >= Sh::kWarps) {
-    qpieces::regs_down<24>();
-    return;
-  }
-  qpieces::regs_up<232>();
-  if (!ok) return;
-  // Streams: the rings lie over the tiles, their barriers and items over the staging buffers.  The first units are given to
-  // the CTAs that start with them, neighbouring units to different SMs; the rest is claimed.
+}
+
+// The streams of a step as the plan lists them.  wait_previous 0: behind the pieces' kernel, which lets this one start once
+// the plan has finished, on the SMs without pieces and, as those end, on theirs.  The grid ends no sooner than that one.
+template <int NT>
+__global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
+    q8_streams_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w, int wait_previous) {
+  using Sh = Shape<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* gsm = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bars = base + Sh::kOffBars + warp * Sh::kWarpBarBytes;
-  if (lane == 0) init_bars<2>(bars);
+  if (lane == 0) init_bars<NT>(bars);
+  if (wait_previous) asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan has finished
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const EndAfterPrevious end{!wait_previous && blockIdx.x == 0};
+  int n_items = __ldcg(w.header + 4);
+  if (uint32_t(__ldcg(w.header + 2)) != w.tag || n_items < 0 || n_items > w.item_cap) {   // a plan of another call: no work
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(a.err, kErrInvalid);
+    n_items = 0;
+  }
   __syncwarp();
-  const int others = int(gridDim.x) - with_pieces, warps = others * Sh::kWarps;
-  qstream::ListedUnits units{w, a.num_kv_heads, n_items * a.num_kv_heads,
-                             pieces_first ? -1 : warp * others + int(blockIdx.x) - with_pieces, warps, 2 * warps};
-  qstream::run_warp<2>(&tm_k16, &tm_v16, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
-                       reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * Sh::kStages),
-                       reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
+  qstream::ListedUnits units{w, a.num_kv_heads, n_items * a.num_kv_heads, -1, 0, 0};   // all claimed: which CTAs start first is open
+  qstream::run_warp<NT>(&tm_k, &tm_v, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
+                        reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * Sh::kStages),
+                        reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
 }
 
 // One row's records, `step` apart from the first on: their weighted sum, by the lanes of a warp, 4 dims each.
@@ -308,7 +311,9 @@ cb_status allow_shared_memory() {
   };
   allow(reinterpret_cast<const void*>(q8_step_kernel<1>), Shape<1>::kSmem);
   allow(reinterpret_cast<const void*>(q8_step_kernel<2>), Shape<2>::kSmem);
-  allow(reinterpret_cast<const void*>(q8_tc_kernel), qpieces::kSmemBytes);
+  allow(reinterpret_cast<const void*>(q8_streams_kernel<1>), Shape<1>::kSmem);
+  allow(reinterpret_cast<const void*>(q8_streams_kernel<2>), Shape<2>::kSmem);
+  allow(reinterpret_cast<const void*>(q8_pieces_kernel), qpieces::kSmemBytes);
   if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: shared memory attribute");
   g_attr_set[dev] = true;
   return CB_OK;
@@ -332,6 +337,9 @@ cb_status encode_pools(const AttnArgs& a, int rows, CUtensorMap* tk, CUtensorMap
 
 // Sets of 8 query rows of a stream's units.
 int stream_sets(const AttnArgs& a) { return int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= 8 ? 1 : 2; }
+// Of a listed step's, whose sequences may have more rows than one unit: small units, of up to 8 rows, where one token's rows
+// fit them.
+int listed_sets(int group_heads) { return group_heads <= 8 ? 1 : 2; }
 int stream_warps(int sets) { return sets == 1 ? Shape<1>::kWarps : Shape<2>::kWarps; }
 int stream_smem(int sets) { return sets == 1 ? Shape<1>::kSmem : Shape<2>::kSmem; }
 
@@ -344,7 +352,8 @@ size_t step_workspace_bytes(int32_t num_tokens) {
 }
 PrefixSizes listed_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
                          int32_t max_context_len) {
-  return prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len, Shape<2>::kWarps, true);
+  const int sets = listed_sets(num_q_heads / num_kv_heads);
+  return prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len, stream_warps(sets), 8 * sets, true);
 }
 
 cb_status run_step(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups, void* workspace,
@@ -404,7 +413,8 @@ cb_status run_quant_attention(const AttnArgs& a, const int32_t* cu_groups, const
 
   const PrefixSizes z = listed_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups, a.max_context_len);
   PrefixWork w;
-  cb_status st = prefix_work(a, cu_groups, prefix_lens, num_groups, z, Shape<2>::kWarps, workspace, &w);
+  const int lsets = listed_sets(G);
+  cb_status st = prefix_work(a, cu_groups, prefix_lens, num_groups, z, stream_warps(lsets), 8 * lsets, workspace, &w);
   if (st != CB_OK) return st;
   w.key_bytes = key_bytes;
   w.tile_us_two = kTileUsTwo;
@@ -426,8 +436,14 @@ cb_status run_quant_attention(const AttnArgs& a, const int32_t* cu_groups, const
   if (st == CB_OK) st = allow_shared_memory();
   if (st == CB_OK) st = launch_prefix_plan(a, w, stream);
   if (st != CB_OK) return st;
-  cudaError_t e = launch_kernel(q8_tc_kernel, dim3(unsigned(w.num_sms)), dim3(qpieces::kThreads), qpieces::kSmemBytes, stream, true,
-                                tq, tk64, tv64, tk16, tv16, a, w);
+  const bool pieces = num_groups > 0 || (a.max_q_len > 1 && rows > kMaxRows);
+  cudaError_t e = cudaSuccess;
+  if (pieces)
+    e = launch_kernel(q8_pieces_kernel, dim3(unsigned(w.num_sms)), dim3(qpieces::kThreads), qpieces::kSmemBytes, stream, true, tq, tk64,
+                      tv64, a, w);
+  if (e == cudaSuccess)
+    e = launch_kernel(lsets == 1 ? q8_streams_kernel<1> : q8_streams_kernel<2>, dim3(unsigned(w.num_sms)),
+                      dim3(32 * stream_warps(lsets)), stream_smem(lsets), stream, true, tk16, tv16, a, w, pieces ? 0 : 1);
   if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: launch");
   return launch_prefix_join(a, w, stream);
 }

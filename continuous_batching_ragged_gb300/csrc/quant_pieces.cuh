@@ -1,24 +1,26 @@
 // Pieces of a step (shared_prefix.h) over a cache in 8 bits, on tcgen05: the query
 // rows of one or two 128-row tiles against a KV segment, left as records.
 //
-// The tensor core multiplies bf16 by bf16: queries are bf16, and weights need its
-// range once the values' scales are in them.  So the e4m3 tiles, exact in bf16, are
-// widened on their way: TMA brings half tiles (64 keys, 8 KB) into two staging
+// e4m3 tiles are exact in f16, so the tensor core multiplies f16 by f16 and the tiles
+// are widened on their way: TMA brings half tiles (64 keys, 8 KB) into two staging
 // buffers each for K and V, two warps each widen them into the swizzled tiles that the
-// MMAs read (a quarter of the issue slots; the L2 and DRAM traffic stays that of 8
-// bits), and everything behind is as over a bf16 cache (prefix_tc_kernel).  The scales
-// of a tile's blocks go around the tensor core: the K loader puts 8 of K and 8 of V,
-// one for each 16 keys, into a ring in shared memory, the softmax multiplies the
-// scores by the ones and the weights by the others.
+// MMAs read, and L2 and DRAM see 8 bits.  (Widened to bf16, which takes four times the
+// conversions, 4.1 us a tile.)  As in the streams (quant_stream.cuh), a query row is
+// scaled by a power of two, on its way too, and the weights, of which f16 holds 2^-24 to
+// 2^16, keep a running maximum M of score + log2(vs) of their own.  The scales of a
+// tile's blocks go around the tensor core: the K loader puts 8 of K and 8 of V, one
+// for each 16 keys, and the logarithms of V's, into a ring in shared memory; the softmax
+// multiplies the scores by the ones and the weights by the others.
 //
-// Roles, in warpgroups whose registers are split by need: 0 and 1 softmax of row
-// tiles 0 and 1, 2 K loader, MMA and V loader, 3 widening (two warps K, two V).
+// Warps 0 to 7 are the softmax of row tiles 0 and 1, 8 the K loader, 9 the MMA thread's,
+// 10 the V loader, 12 and 13 widen K, 14 and 15 V; all with 128 registers.
 #pragma once
 
 #include <cuda.h>
 
 #include "device_common.cuh"
 #include "e4m3.cuh"
+#include "quant_stream.cuh"
 #include "shared_prefix.h"
 #include "sm100_ptx.cuh"
 
@@ -34,13 +36,12 @@ constexpr int HD = kPrefixDim;
 constexpr int kStages = 2;                       // K tiles, and V tiles
 constexpr int kThreads = 512;
 constexpr int kWarpK = 8, kWarpMma = 9, kWarpV = 10, kWarpWiden = 12;
-constexpr int kSoftmaxRegs = 184, kLoaderRegs = 56, kWidenRegs = 88;
-static_assert(2 * kSoftmaxRegs + kLoaderRegs + kWidenRegs <= 512, "128 registers a thread in all");
 constexpr uint32_t kHalf = BM * 64 * 2;          // one 64-dim swizzled half of a bf16 tile: 16 KB
 constexpr uint32_t kTile = 2 * kHalf;
 constexpr uint32_t kStaged = HN * HD;            // 64 keys in 8 bits
 constexpr uint32_t kTmemCols = 512;              // per slot t: S (then P) at 256t, O at 256t + 128
-constexpr int kScaleSlots = 8;                   // tiles whose scales are kept; the loader is at most 5 ahead of the softmax
+constexpr int kScaleSlots = 6;                   // tiles whose scales are kept: the softmax may be 4 behind the loader
+constexpr int kTileScales = 24;                  // of K, of V, their logarithms
 
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + 2 * kTile;
@@ -51,8 +52,9 @@ constexpr int kItemSlots = 2;
 constexpr int kItemReaders = 1 + 1 + 8 + 4;      // V loader, MMA, softmax and widening warps
 enum : int {
   BAR_Q = 0,                   // Q tiles landed
-  BAR_QE = 1,                  // every S MMA of the piece has read Q
-  BAR_S = 2,                   // + slot: S ready
+  BAR_QE = 1,                  // every S MMA of the piece has read Q, every softmax warp its rows' factors
+  BAR_QF = 2,                  // Q tiles in f16, their rows' factors written
+  BAR_S = 3,                   // + slot: S ready
   BAR_P = BAR_S + 2,           // + slot: P written (128 arrivals)
   BAR_O = BAR_P + 2,           // + slot: the piece's last P V in the slot done
   BAR_F = BAR_O + 2,           // + 2 * (0: K, 1: V) + stage: widened
@@ -67,21 +69,22 @@ enum : int {
 constexpr uint32_t kOffTmemSlot = kOffBar + 16 * ((NUM_BARS + 1) / 2);
 constexpr uint32_t kOffItems = kOffTmemSlot + 16;
 constexpr uint32_t kOffScales = kOffItems + kItemSlots * uint32_t(sizeof(Piece));
-constexpr uint32_t kSmemBytes = kOffScales + kScaleSlots * 64 + 1024;   // + slack to align the base
+constexpr uint32_t kOffFactors = kOffScales + kScaleSlots * kTileScales * 4;   // of the query rows' scores
+constexpr uint32_t kSmemBytes = kOffFactors + 2 * BM * 4 + 1024;   // + slack to align the base
 static_assert(kOffItems % 16 == 0 && kOffScales % 16 == 0 && kSmemBytes <= 232448, "shared memory");
-
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+// idesc_bf16_f32 with f16 A and B
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return idesc_bf16_f32(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 // Packed fp32 pairs: two lanes of work per instruction.
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
@@ -121,6 +124,18 @@ __device__ __forceinline__ void store32(float* p, const uint32_t* x) {
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ float lds4(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -178,7 +193,8 @@ struct BlockWindow {
 __device__ __forceinline__ void init_bars(uint32_t base) {
   auto bar = [&](int i) -> uint32_t { return base + kOffBar + 8u * uint32_t(i); };
   mbar_init(bar(BAR_Q), 1);
-  mbar_init(bar(BAR_QE), 1);
+  mbar_init(bar(BAR_QE), 1 + 8);
+  mbar_init(bar(BAR_QF), 4);
   for (int t = 0; t < 2; ++t) {
     mbar_init(bar(BAR_S + t), 1);
     mbar_init(bar(BAR_P + t), BM);
@@ -206,6 +222,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
   auto bar = [&](int i) -> uint32_t { return base + kOffBar + 8u * uint32_t(i); };
   Piece* items = reinterpret_cast<Piece*>(gsm + kOffItems);
   float* scales = reinterpret_cast<float*>(gsm + kOffScales);
+  const uint32_t scales_at = base + kOffScales;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int B = a.block_size;
@@ -215,117 +232,148 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
   bool ok = true;
   unsigned site = 0;
 
-  // A reader's view of piece n; `arrive`: this thread is its role's one arrival.
-  auto read_item = [&](int n, bool arrive, Piece& it) -> bool {
-    const int slot = n % kItemSlots;
-    if (!mbar_wait(bar(BAR_IF + slot), (n / kItemSlots) & 1)) return false;
-    it = items[slot];
-    if (arrive) mbar_arrive(bar(BAR_IE + slot));
-    return true;
-  };
-  // the same for a whole warp
-  auto read_item_warp = [&](int n, Piece& it) -> bool {
-    if (!__all_sync(0xffffffffu, read_item(n, false, it))) return false;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(BAR_IE + n % kItemSlots));
-    return true;
-  };
   auto warp_wait = [&](int b, uint32_t parity, unsigned where) -> bool {
     if (__all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1u))) return true;
     ok = false;
     site = where;
     return false;
   };
+  // a reading warp's view of piece n
+  auto item_landed = [&](int n) -> bool { return warp_wait(BAR_IF + n % kItemSlots, n / kItemSlots, kSitePfItem); };
+  auto item_read = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(BAR_IE + n % kItemSlots));
+  };
 
   if (warp < kWarpK) {
     // ------------------------------------------------------------ softmax of slot t
-    regs_up<kSoftmaxRegs>();
     const int t = warp >> 2;
     const int wq = warp & 3;                       // TMEM lane quarter
     const int i = threadIdx.x - BM * t;            // tile row = TMEM lane
     const uint32_t lane_base = tmem + (uint32_t(wq * 32) << 16) + 256 * t;
-    const float sl2 = a.scale_log2;
     uint32_t cnt = 0, ocnt = 0;                    // S/P phases and O phases of this slot consumed
     uint32_t tiles = 0;                            // of the pieces before
     for (int n = 0; ok; ++n) {
-      Piece it;
-      if (!read_item_warp(n, it)) {
-        ok = false;
-        site = kSitePfItem;
+      if (!item_landed(n)) break;
+      // what the piece's end needs of it is read there: the slot is given back after that
+      const volatile Piece* it = items + n % kItemSlots;
+      if (it->flags & kPieceEnd) {
+        item_read(n);
         break;
       }
-      if (it.flags & kPieceEnd) break;
       // this slot's rows and KV tiles j = first, first + step, ...
-      const bool alt = it.flags & kPieceAlt;
+      const bool alt = it->flags & kPieceAlt;
+      const int nt = it->nt;
       const int toff = alt ? 0 : t * TT;           // the slot's first token, within the piece
-      const int ntok = alt ? it.ntok : min(TT, it.ntok - toff);
-      const int step = alt ? 2 : 1, first = alt ? t : 0;
-      const uint32_t tile0 = tiles;
-      tiles += it.nt;
-      if (ntok <= 0) continue;                     // no rows in the second tile
-      const int rows = ntok * G;
-      const int steps = (it.nt - first + step - 1) / step;
-      // keys that this thread's row sees, and that every row of its warp does
-      const int lim = min(it.keys, it.lim0 + toff + i / G), lim_warp = min(it.keys, it.lim0 + toff + wq * 32 / G);
+      const int rows = (alt ? it->ntok : min(TT, it->ntok - toff)) * G;
+      const int step = alt ? 2 : 1;
+      const int steps = alt ? (nt - t + 1) / 2 : nt;
       const bool work = wq * 32 < rows;            // some row of this warp is real
-      float m = -INFINITY, l = 0.f;
+      if (nt > 0 && (steps == 0 || !work) && lane == 0) mbar_arrive(bar(BAR_QE));   // no factor to read
+      if (rows <= 0) {                             // no rows in the second tile
+        tiles += nt;
+        item_read(n);
+        continue;
+      }
+      // keys of the current tile that this thread's row sees, and that every row of its warp does
+      int lim, lim_warp;
+      {
+        const int k0 = (it->j0 + (alt ? t : 0)) * BN;
+        lim = min(it->keys, it->lim0 + toff + i / G) - k0;
+        lim_warp = min(it->keys, it->lim0 + toff + wq * 32 / G) - k0;
+      }
+      uint32_t tile = (tiles + (alt ? t : 0)) % kScaleSlots;
+      tiles += nt;
+      float m = -INFINITY, l = 0.f, mw = -INFINITY, fw = 1.f, sl2 = 0.f;   // mw: M; fw: 2^(m - M)
+#pragma unroll 1
       for (int x = 0; x < steps; ++x) {
         if (!warp_wait(BAR_S + t, cnt + x, kSitePfS)) break;
         if (!work) {                               // rows of no token: their P may be anything
           mbar_arrive(bar(BAR_P + t));
           continue;
         }
+        if (x == 0) {
+          sl2 = a.scale_log2 * lds4(base + kOffFactors + ((alt ? 0 : BM * t) + i) * 4);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(BAR_QE));
+        }
         tc_fence_after();
-        uint32_t sr[128];
+        // The scores are read twice, 32 at a time and one read ahead: first for their maxima, then for the weights, which go
+        // over scores that have been read.  (All 128 held at once need some 200 registers a thread.)
+        const bool masked = BN > lim_warp;         // keys behind the last one, or the causal mask
+        const uint32_t sc = base + kOffScales + tile * (kTileScales * 4);
+        uint32_t buf[2][32];
+        auto mask = [&](int c, uint32_t (&s)[32]) {
+          if (masked) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(lane_base + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
-        tmem_wait_ld();
-        const int kb = (it.j0 + first + x * step) * BN;
-        if (kb + BN > lim_warp) {                  // keys behind the last one, or the causal mask
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e >= lim) s[e] = __float_as_uint(-INFINITY);
+          }
+        };
+        auto factor = [&](int g) { return fmaxf(sl2 * lds4(sc + 4 * g), 1.2e-38f); };   // of 16 keys' scores; not 0: -inf stays
+        float mt = -INFINITY, wt = -INFINITY;
+        tmem_ld32(lane_base, buf[0]);
 #pragma unroll
-          for (int c = 0; c < BN; ++c)
-            if (kb + c >= lim) sr[c] = __float_as_uint(-INFINITY);
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld();
+          tmem_ld32(lane_base + 32 * ((c + 1) & 3), buf[(c + 1) & 1]);   // at the end, the first again
+          uint32_t(&sr)[32] = buf[c & 1];
+          mask(c, sr);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {            // 16 keys of one block
+            auto s = [&](int e) { return __uint_as_float(sr[16 * g + e]); };
+            const float u = max3(max3(s(0), s(1), s(2)), max3(s(3), s(4), s(5)), max3(s(6), s(7), s(8)));
+            const float v = max3(max3(s(9), s(10), s(11)), max3(s(12), s(13), s(14)), s(15));
+            const float top = fmaxf(u, v) * factor(2 * c + g);
+            mt = fmaxf(mt, top);
+            wt = fmaxf(wt, top + lds4(sc + 64 + 4 * (2 * c + g)));
+          }
         }
-        const float* sc = scales + ((tile0 + first + x * step) % kScaleSlots) * 16;
-        float mt = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {              // 16 keys of one block
-          auto s = [&](int e) { return __uint_as_float(sr[16 * c + e]); };
-          const float u = max3(max3(s(0), s(1), s(2)), max3(s(3), s(4), s(5)), max3(s(6), s(7), s(8)));
-          const float v = max3(max3(s(9), s(10), s(11)), max3(s(12), s(13), s(14)), s(15));
-          mt = fmaxf(mt, fmaxf(u, v) * fmaxf(sl2 * sc[c], 1.2e-38f));   // not 0: -inf stays
+        const bool resc = mt > m + 8.0f || wt > mw + 8.0f;   // keep stale maxima while 2^x stays <= 2^8
+        float alpha = 1.0f;                        // of O
+        if (resc) {
+          const float m_new = fmaxf(m, mt), w_new = fmaxf(mw, wt);
+          l *= ex2(m - m_new);
+          alpha = ex2(mw - w_new);
+          m = m_new;
+          mw = w_new;
+          fw = ex2(fminf(m - mw, 126.f));
         }
-        const float m_new = fmaxf(m, mt);
-        const bool resc = m_new > m + 8.0f;        // keep a stale max while exp2 stays <= 2^8
-        const float m_use = resc ? m_new : m;
-        const float alpha = resc ? ex2(m - m_new) : 1.0f;
-        const float m_sub = m_use == -INFINITY ? 0.f : m_use;   // scores all -inf so far
+        const float m_sub = m == -INFINITY ? 0.f : m;   // scores all -inf so far
         const uint64_t neg_m2 = f2_pack(-m_sub, -m_sub);
         uint64_t sum2[4] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-        // weights times the values' scale over the scores, rounded to bf16 since the tensor core takes them no wider: half a
-        // step, 2^-8, of each.  The sums are of the weights in fp32.
+        // weights times the values' scale over the scores, in f16: within 2^-11 of each, 2^-25 of 2^(M - m); the sums are of
+        // the weights in fp32
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float f = fmaxf(sl2 * sc[c], 1.2e-38f), vs = sc[8 + c];
-          const uint64_t f2 = f2_pack(f, f), vs2 = f2_pack(vs, vs);
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld();
+          if (c < 3) tmem_ld32(lane_base + 32 * (c + 1), buf[(c + 1) & 1]);
+          uint32_t(&sr)[32] = buf[c & 1];
+          mask(c, sr);
+          uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int k = 8 * c + e;
-            float x0, x1, p0, p1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), f2, neg_m2), x0, x1);
-            const uint64_t p2 = f2_pack(ex2(x0), ex2(x1));
-            sum2[e & 3] = f2_add(sum2[e & 3], p2);
-            f2_unpack(f2_mul(p2, vs2), p0, p1);
-            sr[k] = pack_bf16x2(p0, p1);
+          for (int g = 0; g < 2; ++g) {
+            const float f = factor(2 * c + g), vs = fminf(lds4(sc + 32 + 4 * (2 * c + g)) * fw, 3e38f);
+            const uint64_t f2 = f2_pack(f, f), vs2 = f2_pack(vs, vs);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int k = 16 * g + 2 * e;
+              float x0, x1, p0, p1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), f2, neg_m2), x0, x1);
+              const uint64_t p2 = f2_pack(ex2(x0), ex2(x1));
+              sum2[e & 3] = f2_add(sum2[e & 3], p2);
+              f2_unpack(f2_mul(p2, vs2), p0, p1);
+              p[8 * g + e] = pack_f16x2(p0, p1);
+            }
           }
+          tmem_st16(lane_base + 16 * c, p);        // over scores of this chunk and those before
         }
         float r0, r1, r2, r3, r4, r5, r6, r7;
         f2_unpack(sum2[0], r0, r1);
         f2_unpack(sum2[1], r2, r3);
         f2_unpack(sum2[2], r4, r5);
         f2_unpack(sum2[3], r6, r7);
-        l = l * alpha + (((r0 + r1) + (r2 + r3)) + ((r4 + r5) + (r6 + r7)));
-        m = m_use;
+        l += ((r0 + r1) + (r2 + r3)) + ((r4 + r5) + (r6 + r7));
         // S done implies the slot's earlier P V done (one thread issues both, in order,
         // and the commit behind S covers them): O is stable for the rescale
         if (x > 0 && __any_sync(0xffffffffu, resc)) {
@@ -339,11 +387,12 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             tmem_st32(lane_base + 128 + 32 * c, o);
           }
         }
-        tmem_st32(lane_base, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-        tmem_st32(lane_base + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(BAR_P + t));
+        lim -= step * BN;
+        lim_warp -= step * BN;
+        tile = (tile + step) % kScaleSlots;
       }
       if (!ok) break;
       if (steps > 0) {
@@ -354,19 +403,17 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
       cnt += steps;
       // The rows' records of this segment (in the alternating mode, of its even or odd tiles).  A lane holds one row; so that
       // a store is 8 whole lines, every 4 lanes first transpose their 4 rows of 32 dims in units of 32 bytes.
-      const bool direct = it.flags & kPieceDirect;
-      const int row_tok = toff + i / G, head = it.hk * G + i % G;
-      const unsigned rec = direct ? unsigned(it.tok0 + row_tok) * unsigned(H) + unsigned(head)
-                                  : it.rec0 + unsigned((row_tok * H + head) * it.rec_step + (alt ? t : 0));
-      const float inv = direct ? 1.0f / l : 1.0f;
+      const bool direct = it->flags & kPieceDirect;
+      unsigned rec;
+      {
+        const int row_tok = toff + i / G, head = it->hk * G + i % G;
+        rec = direct ? unsigned(it->tok0 + row_tok) * unsigned(H) + unsigned(head)
+                     : it->rec0 + unsigned((row_tok * H + head) * it->rec_step + (alt ? t : 0));
+      }
+      item_read(n);
+      const float to_m = m == -INFINITY ? 0.f : ex2(mw - m);   // O is in units of 2^M, a record's in 2^m
+      const float inv = direct ? to_m / l : to_m;
       if (work) {
-        unsigned at[4];                            // of the rows of this lane's 4
-        float f[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          at[r] = __shfl_sync(0xffffffffu, rec, (lane & ~3) + r);
-          f[r] = __shfl_sync(0xffffffffu, inv, (lane & ~3) + r);
-        }
         const int row4 = wq * 32 + (lane & ~3);
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -394,14 +441,18 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
           }
 #pragma unroll
           for (int r = 0; r < 4; ++r) {            // unit r now belongs to row r of these 4 lanes
+            const unsigned at = __shfl_sync(0xffffffffu, rec, (lane & ~3) + r);
+            const float f = __shfl_sync(0xffffffffu, inv, (lane & ~3) + r);
             if (row4 + r >= rows) continue;
-            const uint32_t* x = &o[8 * r];
+            uint32_t* x = &o[8 * r];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
             if (direct) {
-              auto two = [&](int e) { return pack_bf16x2(__uint_as_float(x[e]) * f[r], __uint_as_float(x[e + 1]) * f[r]); };
-              *(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + size_t(at[r]) * HD + 32 * c) + (lane & 3)) =
+              auto two = [&](int e) { return pack_bf16x2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])); };
+              *(reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + size_t(at) * HD + 32 * c) + (lane & 3)) =
                   make_uint4(two(0), two(2), two(4), two(6));
             } else {
-              store32(w.recs + size_t(at[r]) * HD + 32 * c + 8 * (lane & 3), x);
+              store32(w.recs + size_t(at) * HD + 32 * c + 8 * (lane & 3), x);
             }
           }
         }
@@ -411,7 +462,6 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
     }
     if (!ok && lane == 0) raise_error(a.err, kErrTimeout | site);
   } else if (warp < kWarpWiden) {
-    regs_down<kLoaderRegs>();
     if (warp == kWarpK) {
       // ---------------------------------------------------------- K loader (claims the pieces, brings the scales)
       uint32_t tc = 0, hc = 0, qc = 0;             // tiles, halves and Q loads requested
@@ -462,7 +512,9 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
               const int buf = hc & 1;
               if (hc >= 2 && !warp_wait(BAR_SE + buf, (hc >> 1) - 1, kSitePfKFree)) break;
               if (hh == 0) {                       // ahead of the half, which carries them to the softmax
-                if (lane < 16) scales[(tc % kScaleSlots) * 16 + lane] = scale;
+                float* to = scales + (tc % kScaleSlots) * kTileScales + lane;
+                if (lane < 16) to[0] = scale;
+                if (lane >= 8 && lane < 16) to[8] = fmaxf(qstream::lg2(scale), -126.f);
                 __syncwarp();
               }
               win.load(base + kOffStaged + buf * kStaged, tm_k, bar(BAR_SF + buf), a, j, hh, lane);
@@ -485,12 +537,9 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
       // ---------------------------------------------------------- V loader
       uint32_t hc = 0;
       for (int n = 0; ok; ++n) {
-        Piece it;
-        if (!read_item_warp(n, it)) {
-          ok = false;
-          site = kSitePfItem;
-          break;
-        }
+        if (!item_landed(n)) break;
+        const Piece it = items[n % kItemSlots];
+        item_read(n);
         if (it.flags & kPieceEnd) break;
         if (it.nt == 0) continue;
         BlockWindow win;
@@ -510,8 +559,8 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         for (uint32_t x = hc > 2u ? hc - 2 : 0; x < hc; ++x) mbar_wait(bar(BAR_SF + 2 + (x & 1)), (x >> 1) & 1);
     } else if (warp == kWarpMma && lane == 0) {
       // ---------------------------------------------------------- MMA
-      constexpr uint32_t idS = idesc_bf16_f32(BM, BN, false);   // Q (K-major) x K (K-major)
-      constexpr uint32_t idO = idesc_bf16_f32(BM, HD, true);    // P (TMEM) x V (N-contiguous)
+      constexpr uint32_t idS = idesc_f16_f32(BM, BN, false);   // Q (K-major) x K (K-major)
+      constexpr uint32_t idO = idesc_f16_f32(BM, HD, true);    // P (TMEM) x V (N-contiguous)
       const uint64_t dq0 = smem_desc(base + kOffQ, 16, 1024);
       const uint64_t dk0 = smem_desc(base + kOffK, 16, 1024);
       const uint64_t dv0 = smem_desc(base + kOffV, kHalf, 1024);
@@ -547,15 +596,12 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
       auto k_landed = [&](uint32_t gk) { return wait(BAR_F + gk % kStages, gk / kStages, kSitePfK); };
       auto v_landed = [&](uint32_t gv) { return wait(BAR_F + 2 + gv % kStages, gv / kStages, kSitePfV); };
       for (int n = 0; ok; ++n) {
-        Piece it;
-        if (!read_item(n, true, it)) {
-          ok = false;
-          site = kSitePfItem;
-          break;
-        }
+        if (!wait(BAR_IF + n % kItemSlots, n / kItemSlots, kSitePfItem)) break;
+        struct { int nt, ntok, flags; } it = {items[n % kItemSlots].nt, items[n % kItemSlots].ntok, items[n % kItemSlots].flags};
+        mbar_arrive(bar(BAR_IE + n % kItemSlots));
         if (it.flags & kPieceEnd) break;
         if (it.nt == 0) continue;
-        if (!wait(BAR_Q, qc++, kSitePfQ)) break;
+        if (!wait(BAR_QF, qc++, kSitePfQ)) break;
         if (it.flags & kPieceAlt) {
           for (int j = 0; ok && j < min(2, it.nt); ++j) {
             const uint32_t gk = kc + j;
@@ -622,21 +668,49 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
     }
   } else {
     // ------------------------------------------------------------ widening: two warps K, two V
-    regs_down<kWidenRegs>();
     const int type = (warp - kWarpWiden) >> 1, sub = warp & 1;
     const uint32_t ring = base + (type ? kOffV : kOffK), staged = base + kOffStaged + type * 2 * kStaged;
     // this lane: 16 dims (chunk c) of rows r0, r0 + 4, ... of its warp's 32; 8 lanes read a row's 128 bytes.  The lanes of the
     // upper 64 dims store their second 16 bytes first, so that 8 lanes' stores touch every bank once.
     const int c = lane & 7, r0 = sub * 32 + (lane >> 3), half = c >> 2, lo = 2 * (c & 3);
-    uint32_t tc = 0, hc = 0;
+    uint32_t tc = 0, hc = 0, qc = 0;
     for (int n = 0; ok; ++n) {
-      Piece it;
-      if (!read_item_warp(n, it)) {
-        ok = false;
-        site = kSitePfItem;
-        break;
-      }
+      if (!item_landed(n)) break;
+      const Piece it = items[n % kItemSlots];
+      item_read(n);
       if (it.flags & kPieceEnd) break;
+      if (it.nt == 0) continue;
+      // the piece's Q tiles to f16, in place, a row a thread
+      auto widen_q = [&]() -> bool {
+        if (!warp_wait(BAR_Q, qc, kSitePfQ)) return false;
+        ++qc;
+        const int nq = !(it.flags & kPieceAlt) && it.ntok > TT ? 2 : 1, row = threadIdx.x - kWarpWiden * 32;
+        for (int t = 0; t < nq; ++t) {
+          const uint32_t at = base + kOffQ + t * kTile + row * 128;
+          uint32_t top = 0;                        // bits of the largest magnitude
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint4 v = lds16(at + (k >> 3) * kHalf + (((k & 7) ^ (row & 7)) << 4));
+            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max((in[e] << 16) & 0x7fff0000u, in[e] & 0x7fff0000u));
+          }
+          const uint32_t ex = min(254u, 267u - (top >> 23));   // 2^13 / largest, as an exponent
+          const float f = __uint_as_float(ex << 23);
+          reinterpret_cast<float*>(gsm + kOffFactors)[t * BM + row] = __uint_as_float((254u - ex) << 23);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const uint32_t p = at + (k >> 3) * kHalf + (((k & 7) ^ (row & 7)) << 4);
+            const uint4 v = lds16(p);
+            auto two = [&](uint32_t x) { return pack_f16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f); };
+            sts16(p, two(v.x), two(v.y), two(v.z), two(v.w));
+          }
+        }
+        fence_proxy_async_smem();                  // for the tensor core
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_QF));
+        return true;
+      };
       for (int j = 0; ok && j < it.nt; ++j, ++tc) {
         const int st = tc % kStages;
         if (tc >= kStages && !warp_wait(BAR_E + 2 * type + st, (tc / kStages) - 1, type ? kSitePfVFree : kSitePfKFree)) break;
@@ -660,12 +734,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
             uint32_t y[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float f[4];
-              e4m3x4_to_float(in[e], f);
-              y[2 * e] = pack_bf16x2(f[0], f[1]);
-              y[2 * e + 1] = pack_bf16x2(f[2], f[3]);
-            }
+            for (int e = 0; e < 4; ++e) y[2 * e] = e4m3x2_to_f16x2(in[e]), y[2 * e + 1] = e4m3x2_hi_to_f16x2(in[e]);
             const uint32_t row = ring + st * kTile + half * kHalf + r * 128, at0 = row + ((lo ^ (r & 7)) << 4),
                            at1 = row + (((lo + 1) ^ (r & 7)) << 4);
             if (half) {
@@ -680,6 +749,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(BAR_F + 2 * type + st));
         }
+        if (ok && j == 0) widen_q();               // requested behind the piece's first K tile
       }
     }
     if (!ok && lane == 0) raise_error(a.err, kErrTimeout | site);

@@ -105,6 +105,7 @@ constexpr int kJobCache = 768;           // jobs whose first piece is kept in sh
 constexpr int kExtraPieces = 1024;       // pieces beyond one per (row tile pair, key/value head)
 constexpr int64_t kExtraRecs = 131072;   // records beyond two per row (69 MB)
 constexpr int kMinChunkTiles = 4;        // shortest chunk of streamed keys, in 16-key tiles
+constexpr int kStreamRows = 16;          // query rows per row tile of a stream over a bf16 cache
 constexpr int kMaxSms = 160;             // SMs that the lists are sized for
 // Query rows per key/value head up to which a sequence's own keys are streamed,
 // once per 16 rows; beyond, they are pieces.
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
       n_first += ceil_div_fast(q_len, 2 * TT);
       tiles_max = max(tiles_max, (q.x + BN - 1) / BN);
     } else {
-      unit_tiles += int64_t((q_len * G + kStreamRows - 1) / kStreamRows) * Hkv * ((q.x + stream::kTileKeys - 1) / stream::kTileKeys);
+      unit_tiles += int64_t((q_len * G + w.stream_rows - 1) / w.stream_rows) * Hkv * ((q.x + stream::kTileKeys - 1) / stream::kTileKeys);
       own_keys += q.x;
     }
   }
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
         nch = segments(q.x, longest).x * (q.z <= TT ? 2 : 1);
       } else {
         nch = ceil_div_fast((q.x + stream::kTileKeys - 1) / stream::kTileKeys, Ls);
-        rt = (q.z * G + kStreamRows - 1) / kStreamRows;
+        rt = (q.z * G + w.stream_rows - 1) / w.stream_rows;
       }
     }
     const int64_t n_items = int64_t(rt) * nch, n_recs = pre + nch > 1 ? int64_t(q.z) * H * nch : 0;
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
         it.k0 = it.pad * Ls * stream::kTileKeys;
         it.k1 = it.k0 + min(q.x - it.k0, Ls * stream::kTileKeys);
         *out++ = it;
-        if (++it.pad == nch) it.pad = 0, it.row0 += kStreamRows;
+        if (++it.pad == nch) it.pad = 0, it.row0 += w.stream_rows;
       }
     }
   }
@@ -1494,7 +1495,7 @@ int tile_tokens(int group_heads) { return BM / group_heads; }
 }  // namespace
 
 PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
-                         int32_t max_context_len, int stream_warps, bool pieces) {
+                         int32_t max_context_len, int stream_warps, int stream_rows, bool pieces) {
   PrefixSizes z;
   z.S = size_t(num_seqs), z.T = size_t(num_tokens), z.NG = size_t(std::max(num_groups, 1));
   const size_t G = size_t(num_q_heads / num_kv_heads), rows = z.T * size_t(num_q_heads);
@@ -1509,8 +1510,8 @@ PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_
   const size_t units = 2 * size_t(kMaxSms) * size_t(stream_warps) * kUnitsPerWarp;
   const size_t shortest = size_t(stream::kTileKeys) * std::min(kMinChunkTiles, kSmallChunkTiles);
   const size_t chunks_of_row = (size_t(max_context_len) + shortest - 1) / shortest;
-  z.items = z.T * G / kStreamRows + z.S + units + 1;
-  z.own_recs = z.piece_recs + std::min(rows * chunks_of_row, rows + kStreamRows * units);
+  z.items = z.T * G / size_t(stream_rows) + z.S + units + 1;
+  z.own_recs = z.piece_recs + std::min(rows * chunks_of_row, rows + size_t(stream_rows) * units);
   return z;
 }
 
@@ -1523,7 +1524,7 @@ size_t prefix_workspace_bytes(const PrefixSizes& z) {
 size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
                                      int32_t num_groups, int32_t max_context_len) {
   return prefix_workspace_bytes(prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len,
-                                             kStreamWarps, true));
+                                             kStreamWarps, kStreamRows, true));
 }
 
 // The tensor maps of the K and V pools, boxes of one block and head.
@@ -1618,7 +1619,7 @@ cb_status launch_prefix_join(const AttnArgs& a, const PrefixWork& w, cudaStream_
 }
 
 cb_status prefix_work(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
-                      const PrefixSizes& z, int stream_warps, void* workspace, PrefixWork* work) {
+                      const PrefixSizes& z, int stream_warps, int stream_rows, void* workspace, PrefixWork* work) {
   if (int64_t(a.num_blocks) * a.num_kv_heads >= (int64_t(1) << 31))
     return fail(CB_ERR_UNSUPPORTED, "shared prefixes: num_blocks * num_kv_heads must fit in int32");
   if (z.pieces > 0x7FFFFFFF || z.items > size_t(0x7FFFFFFF / a.num_kv_heads) || z.prefix_recs > 0x7FFFFFFF ||
@@ -1631,6 +1632,7 @@ cb_status prefix_work(const AttnArgs& a, const int32_t* cu_groups, const int32_t
   w.num_groups = std::max(num_groups, 1);
   w.num_sms = sm_count();
   w.tile_tokens = tile_tokens(a.num_heads / a.num_kv_heads);
+  w.stream_rows = stream_rows;
   w.stream_units = std::min(w.num_sms, kMaxSms) * stream_warps * kUnitsPerWarp;
   w.min_chunk_tiles = kMinChunkTiles;
   w.max_sharers = -1;
@@ -1666,9 +1668,9 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
                             void* workspace, cudaStream_t stream) {
   NvtxRange nvtx("cb.shared_prefix");
   const PrefixSizes z = prefix_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups, a.max_context_len,
-                                     kStreamWarps, true);
+                                     kStreamWarps, kStreamRows, true);
   PrefixWork w;
-  cb_status st = prefix_work(a, cu_groups, prefix_lens, num_groups, z, kStreamWarps, workspace, &w);
+  cb_status st = prefix_work(a, cu_groups, prefix_lens, num_groups, z, kStreamWarps, kStreamRows, workspace, &w);
   if (st != CB_OK) return st;
   w.key_bytes = 4.0f * HD * float(a.num_kv_heads);
   w.tile_us_two = kTileUsTwo;

@@ -61,6 +61,7 @@ struct PrefixWork {
   float tile_us_one;           // against one row tile, at an SM's share of HBM
   float stream_rate;           // bytes that the streams of one SM read per microsecond
   int32_t tile_tokens;         // query tokens per row tile of a piece
+  int32_t stream_rows;         // query rows per row tile of a streamed unit
   int32_t stream_units;        // streamed units that the chunk length aims for
   int32_t min_chunk_tiles;     // shortest chunk of a small step's streams, in 16-key tiles
   int32_t max_sharers;         // sequences that could share, up to which the small step's kernel runs the step and
@@ -87,21 +88,20 @@ struct PrefixWork {
 };
 
 constexpr int kStreamWarps = 8;          // warps of a CTA that stream own keys, each with units of its own
-constexpr int kStreamRows = 16;          // query rows per row tile of a listed stream
 constexpr int kUnitsPerWarp = 3;         // streamed units that each warp should get
 
-// Capacities of a step's lists.  stream_warps: warps that stream, per SM; pieces: whether the kernels behind the plan take
+// Capacities of a step's lists.  stream_warps: warps that stream, per SM; stream_rows: query rows of a unit; pieces: whether the kernels behind the plan take
 // pieces at all.
 struct PrefixSizes {
   size_t S, T, NG, pieces, items, prefix_recs, piece_recs, own_recs;
 };
 PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
-                         int32_t max_context_len, int stream_warps, bool pieces);
+                         int32_t max_context_len, int stream_warps, int stream_rows, bool pieces);
 size_t prefix_workspace_bytes(const PrefixSizes& z);
 // Fills `w` for a step and carves its workspace, whose lists sizes have to be `z`.  num_groups 0 (cu_groups and prefix_lens
 // null): no sequence shares.  The estimates are left to the caller.
 cb_status prefix_work(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups,
-                      const PrefixSizes& z, int stream_warps, void* workspace, PrefixWork* w);
+                      const PrefixSizes& z, int stream_warps, int stream_rows, void* workspace, PrefixWork* w);
 // The plan, and the join of the records of the rows that it listed: programmatic dependents of what is before them.
 cb_status launch_prefix_plan(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream);
 cb_status launch_prefix_join(const AttnArgs& a, const PrefixWork& w, cudaStream_t stream);
