@@ -39,7 +39,7 @@ constexpr int kStepTokens = 4096;        // of a step without a plan kernel
 constexpr int kMinShareTiles = 3;        // shortest share of a warp
 constexpr double kSharingBytes = 1.9e8;  // reads that sharing has to be able to save, for the plan to be worth its time
 // What the plan's estimates go by, in microseconds and bytes.
-constexpr float kTileUsTwo = 2.2f, kTileUsOne = 1.6f, kStreamBytesPerUsPerSm = 3.0e4f;
+constexpr float kTileUsTwo = 2.2f, kTileUsOne = 2.2f, kStreamBytesPerUsPerSm = 3.0e4f;
 
 // What the CTAs of a step without a plan kernel make of it, for the join.
 struct StepWork {

@@ -49,37 +49,102 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float(uint32_t(max(e, kLeastExp) + 127) << 23);
 }
 
-// NaN for anything that is not finite.
-__device__ __forceinline__ float nan_unless_finite(float x) { return x + (x - x); }
+// The largest magnitude of a lane's numbers: NaN does not count, an infinity shows and is left out by a second pass.
+template <typename T>
+struct Largest;
+template <>
+struct Largest<__nv_bfloat16> {
+  uint32_t m = 0;                                      // two numbers of any sign
+  __device__ __forceinline__ void add(const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+  }
+  __device__ __forceinline__ void add_finite(const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t y = w[i];
+      if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u;
+      if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
+      asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(y));
+    }
+  }
+  __device__ __forceinline__ float get() const {
+    return fmaxf(__uint_as_float((m << 16) & 0x7fff0000u), __uint_as_float(m & 0x7fff0000u));
+  }
+};
+template <>
+struct Largest<float> {
+  float m = 0.f;
+  __device__ __forceinline__ void add(const uint4& x) {
+    m = fmaxf(fmaxf(m, fabsf(__uint_as_float(x.x))), fabsf(__uint_as_float(x.y)));
+    m = fmaxf(fmaxf(m, fabsf(__uint_as_float(x.z))), fabsf(__uint_as_float(x.w)));
+  }
+  __device__ __forceinline__ void add_finite(const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if ((w[i] & 0x7f800000u) != 0x7f800000u) m = fmaxf(m, fabsf(__uint_as_float(w[i])));
+  }
+  __device__ __forceinline__ float get() const { return m; }
+};
 
+// x / s as e4m3, `inv` = 1 / s.  FINITE: no infinity among the numbers; else one becomes NaN, as x - x is where x is not finite.
+template <bool FINITE>
+__device__ __forceinline__ float scaled(float x, float inv) {
+  const float y = x * inv;
+  return FINITE ? y : y + (y - y);
+}
+template <bool FINITE>
 __device__ __forceinline__ uint2 to_e4m3(const float (&x)[8], float inv) {
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = nan_unless_finite(x[i] * inv);
+  for (int i = 0; i < 8; ++i) y[i] = scaled<FINITE>(x[i], inv);
   return make_uint2(cb::float_to_e4m3x4(y[0], y[1], y[2], y[3]), cb::float_to_e4m3x4(y[4], y[5], y[6], y[7]));
 }
+template <bool FINITE>
 __device__ __forceinline__ uint32_t to_e4m3(const float (&x)[4], float inv) {
   float y[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) y[i] = nan_unless_finite(x[i] * inv);
+  for (int i = 0; i < 4; ++i) y[i] = scaled<FINITE>(x[i], inv);
   return cb::float_to_e4m3x4(y[0], y[1], y[2], y[3]);
 }
 __device__ __forceinline__ void store_lane(uint8_t* row, int c, const uint2& v) { reinterpret_cast<uint2*>(row)[c] = v; }
 __device__ __forceinline__ void store_lane(uint8_t* row, int c, uint32_t v) { reinterpret_cast<uint32_t*>(row)[c] = v; }
 
-// The tokens of one page follow one another in a step: a run.  A warp takes a
-// run's rows of one head, keys or values, LPR lanes to a row, and holds up to 32 (16)
-// rows in registers between the maximum and the rounding; longer runs (pages of
-// 64 and more) are read again.  Which tokens begin a run, every CTA finds out for
-// itself from the slots, so that the warps of the whole grid share the runs
-// evenly whatever mix of decode rows and chunks they come from.
-template <typename T, int LPR>
+// The first n 16-byte chunks of a head's page, times `ratio`: by `lanes` lanes, of which this is `lane`.
+__device__ __forceinline__ void rescale_rows(uint8_t* rows, int n, int lane, int lanes, float ratio) {
+  for (int i = lane; i < n; i += lanes) {
+    uint4 old = reinterpret_cast<uint4*>(rows)[i];
+    uint32_t* w = &old.x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float f[4];
+      cb::e4m3x4_to_float(w[e], f);
+      w[e] = cb::float_to_e4m3x4(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+    }
+    reinterpret_cast<uint4*>(rows)[i] = old;
+  }
+}
+
+// The tokens of one page follow one another in a step: a run.  A warp takes a run's
+// rows of one head at a time, keys or values, LPR lanes to a row, and holds 32 rows in
+// registers between the maximum and the rounding (longer runs are read again), or with
+// pages of up to 16 tokens 16 rows of two heads.  A run of one token, as decode rows
+// are, has four heads for each row that the warp holds side by side.  It goes on to as
+// many heads of its run as there are for each warp of the grid, so that finding the
+// run, its slots and offsets is paid for once.  Which tokens begin a run, every CTA finds out for
+// itself from the slots, so that the warps of the whole grid share the runs evenly
+// whatever mix of decode rows and chunks they come from.
+template <typename T, int LPR, bool LONG>
 __global__ void __launch_bounds__(kThreads, kAppendCtasPerSm) append_q8_kernel(const AppendArgs a) {
   constexpr int EPV = Vec16<T>::N;               // elements per lane
   constexpr int A = LPR * EPV;                   // head_dim
   constexpr int RPW = 32 / LPR;                  // rows side by side in the warp
-  constexpr int kSpan = LPR < 32 ? 32 : 16;      // positions that the warp holds at a time
+  constexpr int kSpan = LONG && LPR < 32 ? 32 : 16;   // positions that the warp holds at a time
   constexpr int kHeld = kSpan / RPW;             // rows of them a lane
+  constexpr int kHeads = !LONG && LPR < 32 ? 2 : 1;   // heads (keys or values) at a time
   constexpr int kWords = kMaxTokens / 32;
   __shared__ uint32_t kept[kWords], lead[kWords], before[kWords + 1];   // tokens that are cached; that begin a run; runs before the word
   __shared__ uint32_t warp_sum[kWarps];
@@ -95,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtasPerSm) append_q8_kernel(c
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int words = (n_tok + 31) / 32;
+#pragma unroll 4
   for (int w = warp; w < words; w += kWarps) {
     const int t = 32 * w + lane;
     const int64_t slot = t < n_tok ? a.slots[t] : -1;
@@ -104,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtasPerSm) append_q8_kernel(c
   }
   __syncthreads();
   // a kept token begins a run if the last kept one before it is of another page
+#pragma unroll 4
   for (int w = warp; w < words; w += kWarps) {
     const int t = 32 * w + lane;
     const uint32_t mine = kept[w];
@@ -146,11 +213,13 @@ __global__ void __launch_bounds__(kThreads, kAppendCtasPerSm) append_q8_kernel(c
 
   const int K = a.num_heads, B = 1 << a.block_shift;
   const int c = lane % LPR, r0 = lane / LPR;
-  const unsigned units = runs * unsigned(2 * K);
-  for (unsigned u = blockIdx.x * kWarps + warp; u < units; u += gridDim.x * kWarps) {
-    const unsigned run = u / unsigned(2 * K);
-    const int part = int(u - run * unsigned(2 * K)), h = part % K;
-    const bool is_v = part >= K;
+  const unsigned warps = gridDim.x * kWarps, parts = unsigned(2 * K);
+  // as few heads to a warp as leave no warp with a second run, where there are warps enough
+  const unsigned most = runs == 0 ? parts : max(1u, min(parts, warps / runs));
+  const unsigned per_warp = (parts + most - 1) / most, groups = (parts + per_warp - 1) / per_warp;
+  for (unsigned u = blockIdx.x * kWarps + warp; u < runs * groups; u += warps) {
+    const unsigned run = u / groups;
+    const int part0 = int((u - run * groups) * per_warp), part1 = min(int(parts), part0 + int(per_warp));
     // the run's first token, and the next run's
     int lo = 0;
     for (int hi = words - 1; lo < hi;) {
@@ -163,100 +232,177 @@ __global__ void __launch_bounds__(kThreads, kAppendCtasPerSm) append_q8_kernel(c
     m &= m - 1;
     int w1 = lo;
     while (m == 0 && ++w1 < words) m = lead[w1];
-    const int t1 = m ? 32 * w1 + __ffs(m) - 1 : n_tok;
-
-    const uint4* src = static_cast<const uint4*>(is_v ? a.v_new : a.k_new) + int64_t(h) * LPR + c;
-    const int64_t stride = is_v ? a.v_stride : a.k_stride;
+    int t1 = m ? 32 * w1 + __ffs(m) - 1 : n_tok;
+    {                                              // behind the run's last kept token, whatever is skipped behind it
+      int w = (t1 - 1) >> 5;
+      uint32_t k = kept[w] & (0xffffffffu >> (31 - ((t1 - 1) & 31)));
+      while (k == 0) k = kept[--w];                // it has t0 at least
+      t1 = 32 * w + 32 - __clz(k);
+    }
     const int64_t slot0 = a.slots[t0];
     const int64_t page = slot0 >> a.block_shift;
     const int first = int(slot0) & (B - 1);
-    float* scale = (is_v ? a.v_scale : a.k_scale) + page * K + h;
-    const float held = first > 0 ? *scale : 0.f;     // tokens before the first new one, with this scale
-    uint8_t* rows = (is_v ? a.v : a.k) + (page * K + h) * int64_t(B) * A;
 
-    // rows of positions p .. p + kSpan - 1 of the run; `offs`: lane i's offset in the page, -1 if its token is not cached
-    uint4 raw[kHeld];
-    auto load = [&](int p, int offs) {
+    if (t1 - t0 == 1) {                            // one token: a head for each row of the warp, four times
+      for (int q = part0; q < part1; q += 4 * RPW) {
+        uint4 raw[4];
+        float *scale[4], held[4];
+        uint8_t* rows[4];
+        bool mine[4];
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        if (t0 + p + i * RPW >= t1) break;
-        const int j = i * RPW + r0;
-        const int o = __shfl_sync(0xffffffffu, offs, j);
-        raw[i] = o >= 0 ? src[int64_t(t0 + p + j) * stride] : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+          const int part = q + i * RPW + r0, h = part % K;
+          const bool is_v = part >= K;
+          mine[i] = part < part1;
+          scale[i] = (is_v ? a.v_scale : a.k_scale) + page * K + h;
+          rows[i] = (is_v ? a.v : a.k) + (page * K + h) * int64_t(B) * A;
+          const uint4* src = static_cast<const uint4*>(is_v ? a.v_new : a.k_new) + int64_t(h) * LPR + c;
+          raw[i] = mine[i] ? src[int64_t(t0) * (is_v ? a.v_stride : a.k_stride)] : make_uint4(0, 0, 0, 0);
+          held[i] = mine[i] && first > 0 ? *scale[i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float f[EPV];
+          Vec16<T>::to_float(raw[i], f);
+          Largest<T> top;
+          top.add_finite(raw[i]);
+          float amax = top.get();
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const float s = fmaxf(scale_for(amax), held[i]), inv = 1.0f / s;
+          if (!mine[i]) continue;
+          if (first > 0 && s > held[i]) rescale_rows(rows[i], first * (A / 16), c, LPR, held[i] * inv);
+          if (c == 0) *scale[i] = s;
+          store_lane(rows[i] + first * A, c, to_e4m3<false>(f, inv));
+        }
       }
-    };
+      continue;
+    }
+
+    // lane i's offset in the page, of position p + i of the run; -1 if its token is not cached
     auto offsets = [&](int p) -> int {
       const int t = t0 + p + lane;
       if (t >= t1 || lane >= kSpan) return -1;
       const int64_t s = a.slots[t];
       return s >= 0 && s < a.num_slots ? int(s) & (B - 1) : -1;
     };
-    float amax = 0.f;
-    int offs = -1, top = -1;
-    bool rising = true;
-    for (int p = 0; t0 + p < t1; p += kSpan) {
-      offs = offsets(p);
-      load(p, offs);
-      // each kept token's offset has to be above all before it
-      int upto = offs;
+    int offs = -1;
+    {
+      bool rising = true;
+      int top = -1;
+      for (int p = 0; t0 + p < t1; p += kSpan) {   // each kept token's offset has to be above all before it
+        const int o = offsets(p);
+        if (p == 0) offs = o;
+        int upto = o;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto = max(upto, y);
-      }
-      int prev = __shfl_up_sync(0xffffffffu, upto, 1);
-      prev = lane == 0 ? top : max(prev, top);
-      rising = rising && __all_sync(0xffffffffu, offs < 0 || offs > prev);
-      top = max(top, __shfl_sync(0xffffffffu, upto, 31));
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        if (t0 + p + i * RPW >= t1) break;
-        float f[EPV];
-        Vec16<T>::to_float(raw[i], f);
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-          const float y = fabsf(f[e]);
-          if (y <= 3.402823466e38f) amax = fmaxf(amax, y);   // what is not finite does not count
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto = max(upto, y);
         }
+        int prev = __shfl_up_sync(0xffffffffu, upto, 1);
+        prev = lane == 0 ? top : max(prev, top);
+        rising = rising && __all_sync(0xffffffffu, o < 0 || o > prev);
+        top = max(top, __shfl_sync(0xffffffffu, upto, 31));
+      }
+      if (!rising) {                               // left out
+        if (lane == 0 && part0 == 0) cb::raise_error(a.err, cb::kErrInvalid);
+        continue;
       }
     }
-    if (!rising) {                                   // left out
-      if (lane == 0 && part == 0) cb::raise_error(a.err, cb::kErrInvalid);
-      continue;
-    }
+    const bool held_all = t1 - t0 <= kSpan;
+
+    for (int q = part0; q < part1; q += kHeads) {
+      const int n = min(kHeads, part1 - q);
+      const uint4* src[kHeads];
+      int64_t stride[kHeads];
+      float *scale[kHeads], held[kHeads], amax[kHeads];
+      Largest<T> top[kHeads];
+      uint8_t* rows[kHeads];
+      uint4 raw[kHeads][kHeld];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float need = scale_for(amax);
-    const float s = fmaxf(need, held), inv = 1.0f / s;
-    if (first > 0 && s > held) {                     // the tokens before: 16 bytes a lane
-      const float ratio = held * inv;
-      for (int i = lane; i < first * (A / 16); i += 32) {
-        uint4 v = reinterpret_cast<uint4*>(rows)[i];
-        uint32_t* w = &v.x;
+      for (int v = 0; v < kHeads; ++v) {
+        const int part = v < n ? q + v : q, h = part % K;
+        const bool is_v = part >= K;
+        src[v] = static_cast<const uint4*>(is_v ? a.v_new : a.k_new) + int64_t(h) * LPR + c;
+        stride[v] = is_v ? a.v_stride : a.k_stride;
+        scale[v] = (is_v ? a.v_scale : a.k_scale) + page * K + h;
+        held[v] = first > 0 ? *scale[v] : 0.f;     // tokens before the first new one, with this scale
+        rows[v] = (is_v ? a.v : a.k) + (page * K + h) * int64_t(B) * A;
+      }
+      // rows of positions p .. p + kSpan - 1 of the run
+      auto load = [&](int p, int o16) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float f[4];
-          cb::e4m3x4_to_float(w[e], f);
-          w[e] = cb::float_to_e4m3x4(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+        for (int i = 0; i < kHeld; ++i) {
+          if (t0 + p + i * RPW >= t1) break;
+          const int j = i * RPW + r0;
+          const int o = __shfl_sync(0xffffffffu, o16, j);
+#pragma unroll
+          for (int v = 0; v < kHeads; ++v) raw[v][i] = o >= 0 && v < n ? src[v][int64_t(t0 + p + j) * stride[v]] : make_uint4(0, 0, 0, 0);
         }
-        reinterpret_cast<uint4*>(rows)[i] = v;
-      }
-    }
-    for (int p = 0; t0 + p < t1; p += kSpan) {
-      if (t1 - t0 > kSpan) {                            // longer than the lanes hold
-        offs = offsets(p);
+      };
+      for (int p = 0; t0 + p < t1; p += kSpan) {
+        if (p > 0) offs = offsets(p);
         load(p, offs);
-      }
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        if (t0 + p + i * RPW >= t1) break;
-        const int o = __shfl_sync(0xffffffffu, offs, i * RPW + r0);
-        float f[EPV];
-        Vec16<T>::to_float(raw[i], f);
-        if (o >= 0) store_lane(rows + o * A, c, to_e4m3(f, inv));
+        for (int i = 0; i < kHeld; ++i) {
+          if (t0 + p + i * RPW >= t1) break;
+#pragma unroll
+          for (int v = 0; v < kHeads; ++v) top[v].add(raw[v][i]);
+        }
       }
+      bool finite = true;
+#pragma unroll
+      for (int v = 0; v < kHeads; ++v) {
+        amax[v] = top[v].get();
+        finite = finite && amax[v] <= 3.402823466e38f;
+      }
+      finite = __all_sync(0xffffffffu, finite);
+      if (!finite) {                               // rare: once more, without what is not finite
+#pragma unroll
+        for (int v = 0; v < kHeads; ++v) top[v] = Largest<T>();
+        for (int p = 0; t0 + p < t1; p += kSpan) {
+          offs = offsets(p);
+          load(p, offs);
+#pragma unroll
+          for (int i = 0; i < kHeld; ++i) {
+            if (t0 + p + i * RPW >= t1) break;
+#pragma unroll
+            for (int v = 0; v < kHeads; ++v) top[v].add_finite(raw[v][i]);
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < kHeads; ++v) amax[v] = top[v].get();
+      }
+      float inv[kHeads];
+#pragma unroll
+      for (int v = 0; v < kHeads; ++v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax[v] = fmaxf(amax[v], __shfl_xor_sync(0xffffffffu, amax[v], o));
+        const float s = fmaxf(scale_for(amax[v]), held[v]);
+        inv[v] = 1.0f / s;
+        if (v >= n) continue;
+        if (first > 0 && s > held[v]) rescale_rows(rows[v], first * (A / 16), lane, 32, held[v] * inv[v]);
+        if (lane == 0) *scale[v] = s;
+      }
+      for (int p = 0; t0 + p < t1; p += kSpan) {
+        if (!held_all) {
+          offs = offsets(p);
+          load(p, offs);
+        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+          if (t0 + p + i * RPW >= t1) break;
+          const int o = __shfl_sync(0xffffffffu, offs, i * RPW + r0);
+#pragma unroll
+          for (int v = 0; v < kHeads; ++v) {
+            float f[EPV];
+            Vec16<T>::to_float(raw[v][i], f);
+            if (o >= 0 && v < n) store_lane(rows[v] + o * A, c, finite ? to_e4m3<true>(f, inv[v]) : to_e4m3<false>(f, inv[v]));
+          }
+        }
+      }
+      if (!held_all) offs = offsets(0);
     }
-    if (lane == 0) *scale = s;
   }
 }
 
@@ -356,7 +502,8 @@ template <typename T, int LPR>
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   const int64_t units = int64_t(a.num_tokens) * 2 * a.num_heads;      // at most: a run for each token
   const int64_t grid = std::min<int64_t>((units + kWarps - 1) / kWarps, int64_t(kAppendCtasPerSm) * cb::sm_count());
-  return cb::launch_kernel(append_q8_kernel<T, LPR>, dim3(unsigned(grid)), dim3(kThreads), 0, stream, true, a);
+  return cb::launch_kernel(a.block_shift > 4 ? append_q8_kernel<T, LPR, true> : append_q8_kernel<T, LPR, false>, dim3(unsigned(grid)),
+                           dim3(kThreads), 0, stream, true, a);
 }
 
 }  // namespace

@@ -298,8 +298,8 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
           if (lane == 0) mbar_arrive(bar(BAR_QE));
         }
         tc_fence_after();
-        // The scores are read twice, 32 at a time and one read ahead: first for their maxima, then for the weights, which go
-        // over scores that have been read.  (All 128 held at once need some 200 registers a thread.)
+        // Half of the scores is held between the maxima and the weights, the other half read twice: all 128 held need some 200
+        // registers a thread, all read twice cost 0.3 us a tile more.  The weights go over scores that are not read again.
         const bool masked = BN > lim_warp;         // keys behind the last one, or the causal mask
         const uint32_t sc = base + kOffScales + tile * (kTileScales * 4);
         uint32_t buf[2][32];
@@ -312,12 +312,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         };
         auto factor = [&](int g) { return fmaxf(sl2 * lds4(sc + 4 * g), 1.2e-38f); };   // of 16 keys' scores; not 0: -inf stays
         float mt = -INFINITY, wt = -INFINITY;
-        tmem_ld32(lane_base, buf[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait_ld();
-          tmem_ld32(lane_base + 32 * ((c + 1) & 3), buf[(c + 1) & 1]);   // at the end, the first again
-          uint32_t(&sr)[32] = buf[c & 1];
+        auto maxima = [&](int c, uint32_t (&sr)[32]) {
           mask(c, sr);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {            // 16 keys of one block
@@ -328,7 +323,18 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             mt = fmaxf(mt, top);
             wt = fmaxf(wt, top + lds4(sc + 64 + 4 * (2 * c + g)));
           }
-        }
+        };
+        tmem_ld32(lane_base + 64, buf[0]);
+        tmem_ld32(lane_base + 96, buf[1]);
+        tmem_wait_ld();
+        maxima(2, buf[0]);
+        tmem_ld32(lane_base, buf[0]);
+        maxima(3, buf[1]);
+        tmem_wait_ld();
+        tmem_ld32(lane_base + 32, buf[1]);
+        maxima(0, buf[0]);
+        tmem_wait_ld();
+        maxima(1, buf[1]);
         const bool resc = mt > m + 8.0f || wt > mw + 8.0f;   // keep stale maxima while 2^x stays <= 2^8
         float alpha = 1.0f;                        // of O
         if (resc) {
@@ -344,13 +350,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         uint64_t sum2[4] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
         // weights times the values' scale over the scores, in f16: within 2^-11 of each, 2^-25 of 2^(M - m); the sums are of
         // the weights in fp32
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait_ld();
-          if (c < 3) tmem_ld32(lane_base + 32 * (c + 1), buf[(c + 1) & 1]);
-          uint32_t(&sr)[32] = buf[c & 1];
-          mask(c, sr);
-          uint32_t p[16];
+        auto weigh = [&](int c, uint32_t (&sr)[32], uint32_t (&p)[16]) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const float f = factor(2 * c + g), vs = fminf(lds4(sc + 32 + 4 * (2 * c + g)) * fw, 3e38f);
@@ -366,8 +366,22 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
               p[8 * g + e] = pack_f16x2(p0, p1);
             }
           }
-          tmem_st16(lane_base + 16 * c, p);        // over scores of this chunk and those before
-        }
+        };
+        uint32_t p[2][16];
+        weigh(0, buf[0], p[0]);
+        tmem_ld32(lane_base + 64, buf[0]);         // those of the other half that are read again lie behind the weights
+        weigh(1, buf[1], p[1]);
+        tmem_st16(lane_base, p[0]);
+        tmem_st16(lane_base + 16, p[1]);
+        tmem_wait_ld();
+        tmem_ld32(lane_base + 96, buf[1]);
+        mask(2, buf[0]);
+        weigh(2, buf[0], p[0]);
+        tmem_st16(lane_base + 32, p[0]);
+        tmem_wait_ld();
+        mask(3, buf[1]);
+        weigh(3, buf[1], p[1]);
+        tmem_st16(lane_base + 48, p[1]);
         float r0, r1, r2, r3, r4, r5, r6, r7;
         f2_unpack(sum2[0], r0, r1);
         f2_unpack(sum2[1], r2, r3);
@@ -484,14 +498,6 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         const Piece it = items[slot];
         if (it.nt > 0) {
           const int nq = !(it.flags & kPieceAlt) && it.ntok > TT ? 2 : 1;
-          BlockWindow win;
-          win.start(a, it, lane);
-          // lanes 0 .. 7: a tile's K scales, 16 keys each; 8 .. 15: its V scales
-          auto scale_of = [&](int j) -> float {
-            const int z = win.of(B, j, (lane & 7) * 16);
-            return lane < 16 && z < a.num_blocks * a.num_kv_heads ? (lane < 8 ? a.k_scale : a.v_scale)[z] : 1.0f;
-          };
-          float scale = scale_of(0);
           auto load_q = [&]() -> bool {
             if (qc > 0 && !warp_wait(BAR_QE, qc - 1, kSitePfQFree)) return false;
             if (lane == 0) {
@@ -505,8 +511,18 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             __syncwarp();
             return true;
           };
+          BlockWindow win;
+          bool q_loaded = false;                   // the first piece's at once, later ones' behind a K tile: the last piece may still read Q
+          if (n == 0) q_loaded = load_q();
+          win.start(a, it, lane);
+          // lanes 0 .. 7: a tile's K scales, 16 keys each; 8 .. 15: its V scales
+          auto scale_of = [&](int j) -> float {
+            const int z = win.of(B, j, (lane & 7) * 16);
+            return lane < 16 && z < a.num_blocks * a.num_kv_heads ? (lane < 8 ? a.k_scale : a.v_scale)[z] : 1.0f;
+          };
+          float scale = scale_of(0);
           for (int j = 0; ok && j < it.nt; ++j) {
-            if (j == 1 && !load_q()) break;
+            if (j == 1 && !q_loaded && !load_q()) break;
             win.advance(a, it.hk, j, lane);
             for (int hh = 0; hh < 2; ++hh) {
               const int buf = hc & 1;
@@ -523,7 +539,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             ++tc;
             scale = scale_of(j + 1);
           }
-          if (ok && it.nt == 1) load_q();
+          if (ok && it.nt == 1 && !q_loaded) load_q();
         }
         u = __shfl_sync(0xffffffffu, ahead, 0);
       }
@@ -711,6 +727,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         if (lane == 0) mbar_arrive(bar(BAR_QF));
         return true;
       };
+      if (n == 0 && !widen_q()) break;
       for (int j = 0; ok && j < it.nt; ++j, ++tc) {
         const int st = tc % kStages;
         if (tc >= kStages && !warp_wait(BAR_E + 2 * type + st, (tc / kStages) - 1, type ? kSitePfVFree : kSitePfKFree)) break;
@@ -749,7 +766,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(BAR_F + 2 * type + st));
         }
-        if (ok && j == 0) widen_q();               // requested behind the piece's first K tile
+        if (ok && j == 0 && n > 0) widen_q();      // requested behind the piece's first K tile, or, in the first piece, before
       }
     }
     if (!ok && lane == 0) raise_error(a.err, kErrTimeout | site);
