@@ -9,8 +9,11 @@
 // every warp of the grid takes an equal share of all tiles, whatever the lengths of
 // the contexts.  A share begins and ends inside a stream at most, so a warp leaves at
 // most two records a row, and the join reads what it needs: 2 records for each warp
-// of the grid, however many sequences there are.  Steps of more sequences than a CTA
-// has threads are planned by the kernel that plans steps with shared prefixes.
+// of the grid, however many sequences there are.  Where the streams are no more than
+// the SMs and short, each is a CTA's, in equal parts to its warps, and the CTA joins
+// them: one launch.  Steps of more sequences than a CTA has threads, with chunks, or
+// whose prefixes are worth sharing, are listed by a plan kernel (shared_prefix.h) as
+// pieces (quant_pieces.cuh) and streams.
 #include <algorithm>
 #include <mutex>
 
@@ -37,6 +40,11 @@ constexpr int kMaxSms = 160;             // SMs that the records are sized for
 constexpr int kMaxRows = 64;             // query rows per key/value head that are streamed, 8 or 16 at a time
 constexpr int kStepTokens = 4096;        // of a step without a plan kernel
 constexpr int kMinShareTiles = 3;        // shortest share of a warp
+// Tiles a warp, at most, of a step whose streams are a CTA's each, which needs no join kernel.  Steps of 1 to 4 tokens, us,
+// so and in shares: 32/8 heads, 16 warps, contexts of 64 5.2 .. 5.6 and 10.1 .. 10.9, of 512 8.8 .. 9.2 and 10.7 .. 11.5, of
+// 1024 10.9 .. 11.4 and 11.1 .. 11.5, of 2048 15.4 .. 15.9 and 11.8 .. 12.5; one key/value head, 8 warps, contexts of 512
+// 11.2 and 13.2, of 1024 14.8 and 13.5.
+constexpr int kApartTiles = 4;
 constexpr double kSharingBytes = 1.9e8;  // reads that sharing has to be able to save, for the plan to be worth its time
 // What the plan's estimates go by, in microseconds and bytes.
 constexpr float kTileUsTwo = 2.2f, kTileUsOne = 2.2f, kStreamBytesPerUsPerSm = 3.0e4f;
@@ -46,13 +54,61 @@ struct StepWork {
   const int32_t* cu_groups;              // null: none
   const int32_t* prefix_lens;
   int32_t num_groups;
-  int32_t share_tiles;                   // least tiles of a share; 0: whole streams only, there is no join
+  int32_t share_tiles;                   // least tiles of a share; 0: a CTA to a stream, which joins its warps' parts itself
   int32_t* header;                       // [0] tiles of a share
   int4* token_info;                      // [num_tokens] (first tile of its sequence's streams, tiles of each, token of the
                                          // sequence, 1: there is something to join)
   float* recs;                           // [2 * warps][row tile][HD]
   float2* rec_ml;
 };
+
+// The weighted sum of a row's records, by the lanes of a warp, 4 dims each.
+struct Joined {
+  float4 acc;
+  float mx, den;
+  __device__ __forceinline__ void raise(float top) {
+    const float old = ex2(mx - (top == -INFINITY ? 0.f : top));
+    acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+    den *= old;
+    mx = top;
+  }
+  __device__ __forceinline__ void add(const float4& x, float2 ml) {   // mx is at least ml.x
+    const float f = ex2(ml.x - (mx == -INFINITY ? 0.f : mx));
+    den = fmaf(f, ml.y, den);
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, x.z, acc.z);
+    acc.w = fmaf(f, x.w, acc.w);
+  }
+};
+constexpr int kJoinFlight = 4;           // records of a row requested at once
+
+// Adds the records from part k0 of n on, kJoinFlight of them, to j; at(k) is where part k's is.
+template <class At>
+__device__ __forceinline__ void join_parts(Joined& j, const StepWork& w, int k0, int n, int lane, const At& at) {
+  float4 x[kJoinFlight];
+  float2 ml[kJoinFlight];
+  float top = j.mx;
+#pragma unroll
+  for (int i = 0; i < kJoinFlight; ++i) {
+    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    ml[i] = make_float2(-INFINITY, 0.f);
+    if (k0 + i < n) {
+      const size_t rec = at(k0 + i);
+      x[i] = __ldcg(reinterpret_cast<const float4*>(w.recs + rec * HD) + lane);
+      ml[i] = __ldcg(w.rec_ml + rec);
+    }
+    top = fmaxf(top, ml[i].x);
+  }
+  j.raise(top);
+#pragma unroll
+  for (int i = 0; i < kJoinFlight; ++i) j.add(x[i], ml[i]);
+}
+__device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, const Joined& j, int lane) {
+  const float inv = 1.0f / j.den;
+  *(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * HD) + lane) =
+      make_uint2(stream::pack2(j.acc.x * inv, j.acc.y * inv), stream::pack2(j.acc.z * inv, j.acc.w * inv));
+}
 
 template <int NT>
 __device__ __forceinline__ void init_bars(uint32_t bars) {
@@ -123,23 +179,46 @@ __global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
     if (i < warp) off += sums[i].x, st0 += sums[i].y;
     all_tiles += sums[i].x, all_streams += sums[i].y;
   }
-  const int warps = int(gridDim.x) * kWarps, id = warp * int(gridDim.x) + int(blockIdx.x);
-  const bool whole = w.share_tiles == 0;
-  const int per = whole ? 0 : max(w.share_tiles, (all_tiles - 1) / warps + 1);
+  const int id = warp * int(gridDim.x) + int(blockIdx.x);
   seqs[tid] = RangeSeq{off, tiles, st0, c0, q_len, n};
-  if (writer) {
-    if ((bad && tid == 0) || (tid < S && !ok)) raise_error(a.err, kErrInvalid);
-    if (tiles > 0 && !whole)
-      for (int t = 0; t < q_len; ++t) w.token_info[c0 + t] = make_int4(off, tiles, t, 1);
-    if (tid == 0) w.header[0] = per;
+  if (writer && ((bad && tid == 0) || (tid < S && !ok))) raise_error(a.err, kErrInvalid);
+  int per, begin = 0, limit = all_tiles, k = id;   // tiles of a share; the tiles that are shared; the warp's share of them
+  RangeSeq own = {};                               // the sequence of the CTA's one stream
+  if (w.share_tiles > 0) {
+    per = max(w.share_tiles, (all_tiles - 1) / (int(gridDim.x) * kWarps) + 1);
+    if (writer) {
+      if (tiles > 0)
+        for (int t = 0; t < q_len; ++t) w.token_info[c0 + t] = make_int4(off, tiles, t, 1);
+      if (tid == 0) w.header[0] = per;
+    }
+    __syncthreads();
+  } else {
+    __syncthreads();
+    if (int(blockIdx.x) >= all_streams) return;
+    int s = 0;                                     // the last sequence whose streams begin at or before it
+    for (int hi = S - 1; s < hi;) {
+      const int mid = (s + hi + 1) >> 1;
+      if (seqs[mid].stream0 <= int(blockIdx.x)) s = mid; else hi = mid - 1;
+    }
+    own = seqs[s];
+    per = (own.tiles - 1) / kWarps + 1;
+    begin = own.off + (int(blockIdx.x) - own.stream0) * own.tiles, limit = begin + own.tiles, k = warp;
   }
-  __syncthreads();
-  RangeUnits units{seqs, S, Hkv, Sh::kRows, whole ? id : int(min(int64_t(all_tiles), int64_t(id) * per)),
-                   whole ? all_streams : int(min(int64_t(all_tiles), int64_t(id + 1) * per)), whole ? warps : 0,
-                   unsigned(2 * id * Sh::kRows)};
+  RangeUnits units{seqs, S, Hkv, Sh::kRows, int(min(int64_t(limit), begin + int64_t(k) * per)),
+                   int(min(int64_t(limit), begin + int64_t(k + 1) * per)), unsigned(2 * id * Sh::kRows)};
   qstream::run_warp<NT>(&tm_k, &tm_v, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
                         reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * Sh::kStages),
                         reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
+  if (w.share_tiles > 0 || own.tiles <= 1) return;
+  __syncthreads();                                 // the warps' records are written
+  const int x = int(blockIdx.x) - own.stream0, hk = x % Hkv, row0 = x / Hkv * Sh::kRows, parts = (own.tiles - 1) / per + 1;
+  for (int r = warp; r < min(Sh::kRows, own.q_len * G - row0); r += kWarps) {
+    Joined j{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+    for (int k0 = 0; k0 < parts; k0 += kJoinFlight)
+      join_parts(j, w, k0, parts, lane,
+                 [&](int part) { return size_t(2 * (part * int(gridDim.x) + int(blockIdx.x))) * Sh::kRows + r; });
+    write_row(a, size_t(own.tok0 + (row0 + r) / G) * H + hk * G + (row0 + r) % G, j, lane);
+  }
 }
 
 // The pieces of a step as the plan lists them, one CTA per SM; those beyond the header[6] that take pieces leave their SMs to
@@ -208,28 +287,8 @@ __global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
                         reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
 }
 
-// One row's records, `step` apart from the first on: their weighted sum, by the lanes of a warp, 4 dims each.
-struct Joined {
-  float4 acc;
-  float mx, den;
-  __device__ __forceinline__ void raise(float top) {
-    const float old = ex2(mx - (top == -INFINITY ? 0.f : top));
-    acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
-    den *= old;
-    mx = top;
-  }
-  __device__ __forceinline__ void add(const float4& x, float2 ml) {   // mx is at least ml.x
-    const float f = ex2(ml.x - (mx == -INFINITY ? 0.f : mx));
-    den = fmaf(f, ml.y, den);
-    acc.x = fmaf(f, x.x, acc.x);
-    acc.y = fmaf(f, x.y, acc.y);
-    acc.z = fmaf(f, x.z, acc.z);
-    acc.w = fmaf(f, x.w, acc.w);
-  }
-};
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kJoinFlight = 4;           // records of a row requested at once
 
 // Joins the rows that lie in several shares.  WIDE: a CTA to a row, each warp with its part of the records, where rows are
 // few and may have very many; else a warp to a row.
@@ -255,23 +314,7 @@ __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(const AttnArgs a,
     const int first = (2 * f + (begin > f * per ? 1 : 0)) * row_tile + in_tile;   // the last part of share f, or its first
     Joined j{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
     for (int k0 = WIDE ? warp * kJoinFlight : 0; k0 < n; k0 += WIDE ? kJoinThreads / 32 * kJoinFlight : kJoinFlight) {
-      float4 x[kJoinFlight];
-      float2 ml[kJoinFlight];
-      float top = j.mx;
-#pragma unroll
-      for (int i = 0; i < kJoinFlight; ++i) {
-        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        ml[i] = make_float2(-INFINITY, 0.f);
-        if (k0 + i < n) {
-          const size_t at = k0 + i == 0 ? first : size_t(2 * (f + k0 + i)) * row_tile + in_tile;
-          x[i] = __ldcg(reinterpret_cast<const float4*>(w.recs + at * HD) + lane);
-          ml[i] = __ldcg(w.rec_ml + at);
-        }
-        top = fmaxf(top, ml[i].x);
-      }
-      j.raise(top);
-#pragma unroll
-      for (int i = 0; i < kJoinFlight; ++i) j.add(x[i], ml[i]);
+      join_parts(j, w, k0, n, lane, [&](int k) { return k == 0 ? size_t(first) : size_t(2 * (f + k)) * row_tile + in_tile; });
     }
     if (WIDE) {
       part_acc[warp][lane] = j.acc;
@@ -286,11 +329,7 @@ __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(const AttnArgs a,
         for (int k = 1; k < kJoinWarps; ++k) j.add(part_acc[k][lane], part_ml[k]);
       }
     }
-    if (!WIDE || warp == 0) {
-      const float inv = 1.0f / j.den;
-      *(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + size_t(row) * HD) + lane) =
-          make_uint2(stream::pack2(j.acc.x * inv, j.acc.y * inv), stream::pack2(j.acc.z * inv, j.acc.w * inv));
-    }
+    if (!WIDE || warp == 0) write_row(a, size_t(row), j, lane);
     if (WIDE) __syncthreads();                     // the parts are read before the next row's
   }
 }
@@ -363,7 +402,10 @@ cb_status run_step(const AttnArgs& a, const int32_t* cu_groups, const int32_t* p
   w.cu_groups = cu_groups;
   w.prefix_lens = prefix_lens;
   w.num_groups = num_groups;
-  w.share_tiles = kMinShareTiles;
+  const int64_t streams = int64_t(a.num_seqs) * a.num_kv_heads *
+                          ((int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) + 8 * sets - 1) / (8 * sets));
+  const bool apart = streams <= sms && a.max_context_len <= kApartTiles * qstream::kTileKeys * stream_warps(sets);
+  w.share_tiles = apart ? 0 : kMinShareTiles;
   char* p = static_cast<char*>(workspace);
   w.header = reinterpret_cast<int32_t*>(p);
   w.token_info = reinterpret_cast<int4*>(p + 256);
@@ -373,10 +415,10 @@ cb_status run_step(const AttnArgs& a, const int32_t* cu_groups, const int32_t* p
   cb_status st = encode_pools(a, qstream::kTileKeys, &tk, &tv);
   if (st == CB_OK) st = allow_shared_memory();
   if (st != CB_OK) return st;
-  cudaError_t e = launch_kernel(sets == 1 ? q8_step_kernel<1> : q8_step_kernel<2>, dim3(unsigned(sms)),
+  cudaError_t e = launch_kernel(sets == 1 ? q8_step_kernel<1> : q8_step_kernel<2>, dim3(unsigned(apart ? streams : sms)),
                                 dim3(32 * stream_warps(sets)), stream_smem(sets), stream, true, tk, tv, a, w);
   if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: launch");
-  if (w.share_tiles == 0) return CB_OK;
+  if (apart) return CB_OK;
   const int64_t rows = int64_t(a.num_tokens) * a.num_heads;
   const int row_tile = 8 * sets;
   if (rows <= int64_t(sms) * 4)

@@ -5,7 +5,7 @@
 // are widened on their way: TMA brings half tiles (64 keys, 8 KB) into two staging
 // buffers each for K and V, two warps each widen them into the swizzled tiles that the
 // MMAs read, and L2 and DRAM see 8 bits.  (Widened to bf16, which takes four times the
-// conversions, 4.1 us a tile.)  As in the streams (quant_stream.cuh), a query row is
+// conversions, a tile's pair of row tiles took 4.1 us, and so 2.8.)  As in the streams (quant_stream.cuh), a query row is
 // scaled by a power of two, on its way too, and the weights, of which f16 holds 2^-24 to
 // 2^16, keep a running maximum M of score + log2(vs) of their own.  The scales of a
 // tile's blocks go around the tensor core: the K loader puts 8 of K and 8 of V, one
@@ -222,7 +222,6 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
   auto bar = [&](int i) -> uint32_t { return base + kOffBar + 8u * uint32_t(i); };
   Piece* items = reinterpret_cast<Piece*>(gsm + kOffItems);
   float* scales = reinterpret_cast<float*>(gsm + kOffScales);
-  const uint32_t scales_at = base + kOffScales;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int B = a.block_size;
@@ -299,7 +298,8 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         }
         tc_fence_after();
         // Half of the scores is held between the maxima and the weights, the other half read twice: all 128 held need some 200
-        // registers a thread, all read twice cost 0.3 us a tile more.  The weights go over scores that are not read again.
+        // registers a thread, which leave too few warps to widen (a 2048-token chunk behind 30,720 keys, 32 heads: 1513 us), all read twice
+        // took 1471 us, and so 1343.  The weights go over scores that are not read again.
         const bool masked = BN > lim_warp;         // keys behind the last one, or the causal mask
         const uint32_t sc = base + kOffScales + tile * (kTileScales * 4);
         uint32_t buf[2][32];

@@ -132,13 +132,13 @@ struct RangeSeq {
   int stream0;                          // streams of the sequences before
   int tok0, q_len, keys;
 };
-// The warp's share of all tiles, [pos, end), or (step > 0) every `step`-th whole stream from `pos` on to `end`.
-// A stream that lies in several shares leaves a record of each row in each of them: a share begins and ends with at most
-// one such part, so its records are rec0 .. rec0 + row_tile - 1 and the row_tile behind.
+// The warp's share of all tiles, [pos, end).  A stream that lies in several shares leaves a record of each row in each of
+// them: a share begins and ends with at most one such part, so its records are rec0 .. rec0 + row_tile - 1 and the row_tile
+// behind.
 struct RangeUnits {
   const RangeSeq* seqs;
   int num_seqs, kv_heads, row_tile;
-  int pos, end, step;
+  int pos, end;
   unsigned rec0;
   bool begun = false;
 
@@ -148,12 +148,10 @@ struct RangeUnits {
     int s = 0;                          // the last sequence that starts at or before it; ones without tiles come before
     for (int hi = num_seqs - 1; s < hi;) {
       const int mid = (s + hi + 1) >> 1;
-      if ((step ? seqs[mid].stream0 : seqs[mid].off) <= pos) s = mid; else hi = mid - 1;
+      if (seqs[mid].off <= pos) s = mid; else hi = mid - 1;
     }
     const RangeSeq q = seqs[s];
-    const int local = pos - (step ? q.stream0 : q.off);
-    const int x = step ? local : local / q.tiles, t0 = step ? 0 : local - x * q.tiles;
-    const int n = step ? q.tiles : min(q.tiles - t0, end - pos);
+    const int local = pos - q.off, x = local / q.tiles, t0 = local - x * q.tiles, n = min(q.tiles - t0, end - pos);
     if (lane == 0) {
       SuffixItem u = {};
       u.s = s, u.tok0 = q.tok0, u.q_len = q.q_len, u.row0 = x / kv_heads * row_tile, u.ctx = q.keys;
@@ -163,7 +161,7 @@ struct RangeUnits {
       it = u;
     }
     begun = true;
-    pos += step ? step : n;
+    pos += n;
     __syncwarp();
     return {x % kv_heads, n};
   }

@@ -344,3 +344,87 @@ def test_append_then_gather_on_streams(native_lib):
         want = gather_plain(p, [[7, 2, 5]], [0, 41], [0], 41)
         assert same(ko, want[0]) and same(vo, want[1])
     api.cb_check_device_errors()
+
+
+def test_wide_offsets(native_lib):
+    """Pages whose numbers begin behind 2^31 and 2^32 bytes of their pools, and gathered rows behind 2^31 bytes of the output."""
+    from continuous_batching_ragged_gb300 import api
+    K, B, A = 8, 128, 128
+    p = Pool(5, K, B, A, seed=26)
+    far_ids = [0, 2 ** 31 // (K * B * A) - 1, 2 ** 31 // (K * B * A), 2 ** 32 // (K * B * A) - 1, 2 ** 32 // (K * B * A) + 3]
+    at = torch.tensor(far_ids, device="cuda")
+    far = [torch.zeros((far_ids[-1] + 1, K, B, A), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    far_scales = [torch.ones((far_ids[-1] + 1, K), device="cuda") for _ in range(2)]
+    for x, y in zip(far, (p.k, p.v)):
+        x[at] = y.view(torch.uint8)
+    for x, y in zip(far_scales, (p.ks, p.vs)):
+        x[at] = y
+    cache = api.QuantKVCache(*(x.view(E4M3) for x in far), *far_scales)
+    for n, order in ((300, [1, 4, 3]), (1, [2]), (1, [4])):
+        slots = chunk_slots(order, B, 70, n)
+        k, v = (rows(n, K, A, "bf16", s) for s in (27, 28))
+        api.cb_append_kv_q8(k, v, torch.tensor([far_ids[s // B] * B + s % B for s in slots], device="cuda"), cache)
+        api.cb_check_device_errors()
+        p.plain(k, v, slots)
+    for x, y in zip(far, (p.k, p.v)):
+        y.copy_(x[at].view(E4M3))
+        x[at] = 0
+        assert not bool(x.any())                     # nothing elsewhere
+        x[at] = y.view(torch.uint8)
+    for x, y in zip(far_scales, (p.ks, p.vs)):
+        y.copy_(x[at])
+    p.check()
+    T = 2 ** 31 // (K * A * 4) + 40
+    ko = torch.full((T, K, A), float("nan"), device="cuda")
+    vo = torch.full((T, K, A), float("nan"), device="cuda")
+    long = [4, 2, 3, 1, 0] * (T // B // 5 + 1)
+    tables = torch.tensor([[far_ids[i] for i in long], [far_ids[i] for i in (0, 1, 4)] + [-1] * (len(long) - 3)])
+    cu = [0, T - 300, T - 5]
+    api.cb_gather_kv_q8(cache, tables.int().cuda(), ints(cu), k_out=ko, v_out=vo)
+    api.cb_check_device_errors()
+    first = (T - 300) // (5 * B) * 5 * B              # of the long sequence's last rows
+    want = gather_plain(p, [long, [0, 1, 4]], [0, T - 300 - first, T - 5 - first], [0, 0], T - first)
+    for got, w in zip((ko, vo), want):
+        assert same(got[first:], w)
+        assert same(got[:5 * B], got[first - 5 * B:first])
+        assert same(got[:5 * B], gather_plain(p, [long], [0, 5 * B], [0], 5 * B)[0 if got is ko else 1])
+
+
+@pytest.mark.parametrize("B", [16, 128])
+@pytest.mark.parametrize("tail", [2900, 64_800])
+def test_few_tokens_of_many(native_lib, B, tail):
+    """A padded batch: most slots are skipped, before, between and behind the tokens."""
+    from continuous_batching_ragged_gb300 import api
+    K, A = 3, 64
+    p = Pool(30, K, B, A, seed=29)
+    ids = torch.randperm(30, generator=torch.Generator().manual_seed(30)).tolist()
+    slots = [-1] * 70 + [ids[i] * B + 5 for i in range(9)] + [-1] * (tail // 2) + chunk_slots(ids[10:16], B, 3, 4 * B)
+    slots += [-1] * 33 + [ids[20] * B] + [-1] * (tail - tail // 2)
+    k, v = (rows(len(slots), K, A, "bf16", s) for s in (31, 32))
+    p.append(k, v, slots)
+    api.cb_check_device_errors()
+    p.plain(k, v, slots)
+    p.check()
+
+
+def test_captured_append_with_a_count(native_lib):
+    """A captured append replayed with other counts and slots on the device."""
+    from continuous_batching_ragged_gb300 import api
+    K, B, A = 4, 16, 128
+    p = Pool(12, K, B, A, seed=33)
+    k, v = (rows(60, K, A, "bf16", s) for s in (34, 35))
+    slots = torch.full((60,), -1, dtype=torch.int64, device="cuda")
+    dims = torch.tensor([1, 0, 1, 1], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        api.cb_append_kv_q8(k, v, slots, p.cache, dims=dims, stream=side)
+    for n, ids, start in ((0, [0, 1, 2, 3, 4], 0), (60, [9, 3, 1, 7, 0], 2), (17, [5, 2], 0), (1, [5], 1), (2, [2, 5], 15)):
+        mine = chunk_slots(ids, B, start, n)
+        slots.copy_(torch.tensor(mine + [ids[0] * B] * (60 - n)))   # those behind the count are not read
+        dims[1] = n
+        graph.replay()
+        api.cb_check_device_errors()
+        p.plain(k[:n], v[:n], mine)
+        p.check()
