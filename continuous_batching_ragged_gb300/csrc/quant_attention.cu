@@ -83,26 +83,26 @@ struct Joined {
 };
 constexpr int kJoinFlight = 4;           // records of a row requested at once
 
-// Adds the records from part k0 of n on, kJoinFlight of them, to j; at(k) is where part k's is.
-template <class At>
-__device__ __forceinline__ void join_parts(Joined& j, const StepWork& w, int k0, int n, int lane, const At& at) {
-  float4 x[kJoinFlight];
-  float2 ml[kJoinFlight];
+// Adds the records of parts k0 .. k0 + K - 1 of n to j; at(k) is where part k's is.
+template <int K, class At>
+__device__ __forceinline__ void join_parts(Joined& j, const float* recs, const float2* rec_ml, int k0, int n, int lane, const At& at) {
+  float4 x[K];
+  float2 ml[K];
   float top = j.mx;
 #pragma unroll
-  for (int i = 0; i < kJoinFlight; ++i) {
+  for (int i = 0; i < K; ++i) {
     x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     ml[i] = make_float2(-INFINITY, 0.f);
     if (k0 + i < n) {
       const size_t rec = at(k0 + i);
-      x[i] = __ldcg(reinterpret_cast<const float4*>(w.recs + rec * HD) + lane);
-      ml[i] = __ldcg(w.rec_ml + rec);
+      x[i] = __ldcg(reinterpret_cast<const float4*>(recs + rec * HD) + lane);
+      ml[i] = __ldcg(rec_ml + rec);
     }
     top = fmaxf(top, ml[i].x);
   }
   j.raise(top);
 #pragma unroll
-  for (int i = 0; i < kJoinFlight; ++i) j.add(x[i], ml[i]);
+  for (int i = 0; i < K; ++i) j.add(x[i], ml[i]);
 }
 __device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, const Joined& j, int lane) {
   const float inv = 1.0f / j.den;
@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
   for (int r = warp; r < min(Sh::kRows, own.q_len * G - row0); r += kWarps) {
     Joined j{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
     for (int k0 = 0; k0 < parts; k0 += kJoinFlight)
-      join_parts(j, w, k0, parts, lane,
-                 [&](int part) { return size_t(2 * (part * int(gridDim.x) + int(blockIdx.x))) * Sh::kRows + r; });
+      join_parts<kJoinFlight>(j, w.recs, w.rec_ml, k0, parts, lane,
+                              [&](int part) { return size_t(2 * (part * int(gridDim.x) + int(blockIdx.x))) * Sh::kRows + r; });
     write_row(a, size_t(own.tok0 + (row0 + r) / G) * H + hk * G + (row0 + r) % G, j, lane);
   }
 }
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(const AttnArgs a,
     const int first = (2 * f + (begin > f * per ? 1 : 0)) * row_tile + in_tile;   // the last part of share f, or its first
     Joined j{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
     for (int k0 = WIDE ? warp * kJoinFlight : 0; k0 < n; k0 += WIDE ? kJoinThreads / 32 * kJoinFlight : kJoinFlight) {
-      join_parts(j, w, k0, n, lane, [&](int k) { return k == 0 ? size_t(first) : size_t(2 * (f + k)) * row_tile + in_tile; });
+      join_parts<kJoinFlight>(j, w.recs, w.rec_ml, k0, n, lane, [&](int k) { return k == 0 ? size_t(first) : size_t(2 * (f + k)) * row_tile + in_tile; });
     }
     if (WIDE) {
       part_acc[warp][lane] = j.acc;
@@ -331,6 +331,70 @@ __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(const AttnArgs a,
     }
     if (!WIDE || warp == 0) write_row(a, size_t(row), j, lane);
     if (WIDE) __syncthreads();                     // the parts are read before the next row's
+  }
+}
+
+// Joins the rows of a listed step, a warp to every W-th row.  Its lanes look 32 rows ahead for those with records to join:
+// in a step of prompts and decode rows most have none, and the others have many, so that what bounds it is the steps that
+// one row's records take in turn.  3 chunks of 662 tokens and 64 decode rows of up to 26 records, 32/8 heads: the step 172 us,
+// 190 with units of 4 neighbouring rows a warp, which few warps then hold; 4 CTAs an SM, of 64 registers, 175.
+constexpr int kListedFlight = 8, kListedCtasPerSm = 2;
+__global__ void __launch_bounds__(kJoinThreads, kListedCtasPerSm) q8_listed_join_kernel(const AttnArgs a, const PrefixWork w) {
+  const int lane = threadIdx.x & 31, H = a.num_heads;
+  const int64_t rows = int64_t(a.num_tokens) * H;
+  const int warps = int(gridDim.x) * kJoinWarps, first = int(threadIdx.x >> 5) * int(gridDim.x) + int(blockIdx.x);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int stride = __ldcg(w.header + 1);
+  if (uint32_t(__ldcg(w.header + 2)) != w.tag) return;   // a plan of another call
+  for (int64_t r0 = first; r0 < rows; r0 += int64_t(warps) * 32) {
+    const int64_t mine = r0 + int64_t(lane) * warps;
+    const int4 ti = mine < rows ? __ldcg(w.token_info + mine / H) : make_int4(0, 0, 0, 0);
+    unsigned two = __ballot_sync(0xffffffffu, ti.x + ti.z == 2);    // below 2: left out, or already written
+    unsigned more = __ballot_sync(0xffffffffu, ti.x + ti.z > 2);
+    // where record k of the row in lane `from` is
+    int np, own, n;
+    size_t row, own0;
+    auto look = [&](int from) {
+      np = __shfl_sync(0xffffffffu, ti.x, from), own = __shfl_sync(0xffffffffu, ti.y, from);
+      n = __shfl_sync(0xffffffffu, ti.z, from);
+      row = size_t(r0 + int64_t(from) * warps);
+      own0 = size_t(unsigned(own)) + row % unsigned(H) * size_t(n);
+      n += np;
+    };
+    auto at = [&](int k) { return k < np ? row * size_t(stride) + k : own0 + (k - np); };
+    while (two) {                                        // 4 at once
+      float4 x[4][2];
+      float2 ml[4][2];
+      const unsigned these = two;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!two) break;
+        look(__ffs(two) - 1);
+        two &= two - 1;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          x[i][k] = __ldcg(reinterpret_cast<const float4*>(w.recs + at(k) * HD) + lane);
+          ml[i][k] = __ldcg(w.rec_ml + at(k));
+        }
+      }
+      unsigned left = these;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (left == two) break;
+        Joined j{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+        j.raise(fmaxf(ml[i][0].x, ml[i][1].x));
+        j.add(x[i][0], ml[i][0]);
+        j.add(x[i][1], ml[i][1]);
+        write_row(a, size_t(r0 + int64_t(__ffs(left) - 1) * warps), j, lane);
+        left &= left - 1;
+      }
+    }
+    for (; more; more &= more - 1) {
+      look(__ffs(more) - 1);
+      Joined j{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+      for (int k0 = 0; k0 < n; k0 += kListedFlight) join_parts<kListedFlight>(j, w.recs, w.rec_ml, k0, n, lane, at);
+      write_row(a, row, j, lane);
+    }
   }
 }
 
@@ -487,7 +551,12 @@ cb_status run_quant_attention(const AttnArgs& a, const int32_t* cu_groups, const
     e = launch_kernel(lsets == 1 ? q8_streams_kernel<1> : q8_streams_kernel<2>, dim3(unsigned(w.num_sms)),
                       dim3(32 * stream_warps(lsets)), stream_smem(lsets), stream, true, tk16, tv16, a, w, pieces ? 0 : 1);
   if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: launch");
-  return launch_prefix_join(a, w, stream);
+  const int64_t rows_all = int64_t(a.num_tokens) * a.num_heads;
+  if (rows_all <= int64_t(w.num_sms) * 4) return launch_prefix_join(a, w, stream);
+  e = launch_kernel(q8_listed_join_kernel,
+                    dim3(unsigned(std::min<int64_t>((rows_all + kJoinWarps - 1) / kJoinWarps, int64_t(w.num_sms) * kListedCtasPerSm))),
+                    dim3(kJoinThreads), 0, stream, true, a, w);
+  return e == cudaSuccess ? CB_OK : cuda_fail(e, "8-bit attention: join launch");
 }
 
 }  // namespace cb
