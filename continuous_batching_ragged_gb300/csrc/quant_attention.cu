@@ -33,7 +33,9 @@ namespace {
 using namespace sm100;
 using qstream::RangeSeq;
 using qstream::RangeUnits;
-using qstream::Shape;
+using qstream::FewShape;
+using qstream::SharesShape;
+using qstream::WideShape;
 
 constexpr int HD = kPrefixDim;
 constexpr int kMaxSms = 160;             // SMs that the records are sized for
@@ -41,9 +43,9 @@ constexpr int kMaxRows = 64;             // query rows per key/value head that a
 constexpr int kStepTokens = 4096;        // of a step without a plan kernel
 constexpr int kMinShareTiles = 3;        // shortest share of a warp
 // Tiles a warp, at most, of a step whose streams are a CTA's each, which needs no join kernel.  Steps of 1 to 4 tokens, us,
-// so and in shares: 32/8 heads, 16 warps, contexts of 64 5.2 .. 5.6 and 10.1 .. 10.9, of 512 8.8 .. 9.2 and 10.7 .. 11.5, of
-// 1024 10.9 .. 11.4 and 11.1 .. 11.5, of 2048 15.4 .. 15.9 and 11.8 .. 12.5; one key/value head, 8 warps, contexts of 512
-// 11.2 and 13.2, of 1024 14.8 and 13.5.
+// so and in shares: 32/8 heads, 12 warps, contexts of 64 5.1 .. 5.6 and 10.1 .. 10.9, of 512 7.9 .. 8.5 and 10.7 .. 11.5,
+// of 1024 (16 warps) 10.9 .. 11.4 and 11.1 .. 11.5; one key/value head, 8 warps, contexts of 512 11.4 and 13.2, of 1024 14.8
+// and 13.5.
 constexpr int kApartTiles = 4;
 constexpr double kSharingBytes = 1.9e8;  // reads that sharing has to be able to save, for the plan to be worth its time
 // What the plan's estimates go by, in microseconds and bytes.
@@ -110,18 +112,17 @@ __device__ __forceinline__ void write_row(const AttnArgs& a, size_t row, const J
       make_uint2(stream::pack2(j.acc.x * inv, j.acc.y * inv), stream::pack2(j.acc.z * inv, j.acc.w * inv));
 }
 
-template <int NT>
+template <class Sh>
 __device__ __forceinline__ void init_bars(uint32_t bars) {
-  for (int st = 0; st < Shape<NT>::kStages; ++st) mbar_init(bars + 8 * st, qstream::kBarArrivals);
+  for (int st = 0; st < Sh::kStages; ++st) mbar_init(bars + 8 * st, qstream::kBarArrivals);
   fence_mbar_init();
 }
 
-template <int NT>
-__global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
+template <class Sh>
+__global__ void __launch_bounds__(Sh::kThreads, 1)
     q8_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ AttnArgs a, const __grid_constant__ StepWork w) {
-  using Sh = Shape<NT>;
-  constexpr int kWarps = Sh::kWarps, kThreads = 32 * kWarps, kSeqs = kThreads;   // a thread for each sequence
+  constexpr int kWarps = Sh::kWarps, kThreads = Sh::kThreads, kSeqs = kThreads;   // a thread for each sequence
   extern __shared__ uint8_t smem_raw[];
   __shared__ RangeSeq seqs[kSeqs];
   __shared__ int group_s0[kSeqs], group_p[kSeqs];
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
   const int S = a.num_seqs, T = a.num_tokens, NG = w.num_groups, H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv;
 
   if (lane == 0) {
-    init_bars<NT>(bars);
+    init_bars<Sh>(bars);
     if (warp == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
   }
   RangeUnits units{seqs, S, Hkv, Sh::kRows, int(min(int64_t(limit), begin + int64_t(k) * per)),
                    int(min(int64_t(limit), begin + int64_t(k + 1) * per)), unsigned(2 * id * Sh::kRows)};
-  qstream::run_warp<NT>(&tm_k, &tm_v, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
+  qstream::run_warp<Sh>(&tm_k, &tm_v, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
                         reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * Sh::kStages),
                         reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
   if (w.share_tiles > 0 || own.tiles <= 1) return;
@@ -261,17 +262,16 @@ __global__ void __launch_bounds__(qpieces::kThreads, 1)
 
 // The streams of a step as the plan lists them.  wait_previous 0: behind the pieces' kernel, which lets this one start once
 // the plan has finished, on the SMs without pieces and, as those end, on theirs.  The grid ends no sooner than that one.
-template <int NT>
-__global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
+template <class Sh>
+__global__ void __launch_bounds__(Sh::kThreads, 1)
     q8_streams_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ AttnArgs a, const __grid_constant__ PrefixWork w, int wait_previous) {
-  using Sh = Shape<NT>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* gsm = smem_raw + (base - raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bars = base + Sh::kOffBars + warp * Sh::kWarpBarBytes;
-  if (lane == 0) init_bars<NT>(bars);
+  if (lane == 0) init_bars<Sh>(bars);
   if (wait_previous) asm volatile("griddepcontrol.wait;" ::: "memory");   // the plan has finished
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const EndAfterPrevious end{!wait_previous && blockIdx.x == 0};
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(32 * Shape<NT>::kWarps, 1)
   }
   __syncwarp();
   qstream::ListedUnits units{w, a.num_kv_heads, n_items * a.num_kv_heads, -1, 0, 0};   // all claimed: which CTAs start first is open
-  qstream::run_warp<NT>(&tm_k, &tm_v, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
+  qstream::run_warp<Sh>(&tm_k, &tm_v, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
                         reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * Sh::kStages),
                         reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
 }
@@ -412,10 +412,11 @@ cb_status allow_shared_memory() {
   const auto allow = [&e](const void* kernel, uint32_t bytes) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
   };
-  allow(reinterpret_cast<const void*>(q8_step_kernel<1>), Shape<1>::kSmem);
-  allow(reinterpret_cast<const void*>(q8_step_kernel<2>), Shape<2>::kSmem);
-  allow(reinterpret_cast<const void*>(q8_streams_kernel<1>), Shape<1>::kSmem);
-  allow(reinterpret_cast<const void*>(q8_streams_kernel<2>), Shape<2>::kSmem);
+  allow(reinterpret_cast<const void*>(q8_step_kernel<SharesShape>), SharesShape::kSmem);
+  allow(reinterpret_cast<const void*>(q8_step_kernel<FewShape>), FewShape::kSmem);
+  allow(reinterpret_cast<const void*>(q8_step_kernel<WideShape>), WideShape::kSmem);
+  allow(reinterpret_cast<const void*>(q8_streams_kernel<FewShape>), FewShape::kSmem);
+  allow(reinterpret_cast<const void*>(q8_streams_kernel<WideShape>), WideShape::kSmem);
   allow(reinterpret_cast<const void*>(q8_pieces_kernel), qpieces::kSmemBytes);
   if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: shared memory attribute");
   g_attr_set[dev] = true;
@@ -443,11 +444,13 @@ int stream_sets(const AttnArgs& a) { return int64_t(a.max_q_len) * (a.num_heads 
 // Of a listed step's, whose sequences may have more rows than one unit: small units, of up to 8 rows, where one token's rows
 // fit them.
 int listed_sets(int group_heads) { return group_heads <= 8 ? 1 : 2; }
-int stream_warps(int sets) { return sets == 1 ? Shape<1>::kWarps : Shape<2>::kWarps; }
-int stream_smem(int sets) { return sets == 1 ? Shape<1>::kSmem : Shape<2>::kSmem; }
+int listed_warps(int sets) { return sets == 1 ? FewShape::kWarps : WideShape::kWarps; }
 
 // Records of a step without a plan kernel: two of a row tile for each warp that may have a share.
-size_t step_records(int num_sms) { return size_t(num_sms) * std::max(2 * Shape<1>::kWarps * Shape<1>::kRows, 2 * Shape<2>::kWarps * Shape<2>::kRows); }
+size_t step_records(int num_sms) {
+  return size_t(num_sms) * std::max({2 * SharesShape::kWarps * SharesShape::kRows, 2 * FewShape::kWarps * FewShape::kRows,
+                                     2 * WideShape::kWarps * WideShape::kRows});
+}
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 size_t step_workspace_bytes(int32_t num_tokens) {
@@ -456,7 +459,7 @@ size_t step_workspace_bytes(int32_t num_tokens) {
 PrefixSizes listed_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
                          int32_t max_context_len) {
   const int sets = listed_sets(num_q_heads / num_kv_heads);
-  return prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len, stream_warps(sets), 8 * sets, true);
+  return prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len, listed_warps(sets), 8 * sets, true);
 }
 
 cb_status run_step(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups, void* workspace,
@@ -468,7 +471,8 @@ cb_status run_step(const AttnArgs& a, const int32_t* cu_groups, const int32_t* p
   w.num_groups = num_groups;
   const int64_t streams = int64_t(a.num_seqs) * a.num_kv_heads *
                           ((int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) + 8 * sets - 1) / (8 * sets));
-  const bool apart = streams <= sms && a.max_context_len <= kApartTiles * qstream::kTileKeys * stream_warps(sets);
+  const bool apart = streams <= sms && num_groups <= (sets == 1 ? FewShape::kThreads : WideShape::kThreads) &&
+                     a.max_context_len <= kApartTiles * qstream::kTileKeys * listed_warps(sets);
   w.share_tiles = apart ? 0 : kMinShareTiles;
   char* p = static_cast<char*>(workspace);
   w.header = reinterpret_cast<int32_t*>(p);
@@ -479,8 +483,16 @@ cb_status run_step(const AttnArgs& a, const int32_t* cu_groups, const int32_t* p
   cb_status st = encode_pools(a, qstream::kTileKeys, &tk, &tv);
   if (st == CB_OK) st = allow_shared_memory();
   if (st != CB_OK) return st;
-  cudaError_t e = launch_kernel(sets == 1 ? q8_step_kernel<1> : q8_step_kernel<2>, dim3(unsigned(apart ? streams : sms)),
-                                dim3(32 * stream_warps(sets)), stream_smem(sets), stream, true, tk, tv, a, w);
+  cudaError_t e;
+  if (sets == 1 && !apart)
+    e = launch_kernel(q8_step_kernel<SharesShape>, dim3(unsigned(sms)), dim3(SharesShape::kThreads), SharesShape::kSmem, stream, true,
+                      tk, tv, a, w);
+  else if (sets == 1)
+    e = launch_kernel(q8_step_kernel<FewShape>, dim3(unsigned(streams)), dim3(FewShape::kThreads), FewShape::kSmem, stream, true, tk,
+                      tv, a, w);
+  else
+    e = launch_kernel(q8_step_kernel<WideShape>, dim3(unsigned(apart ? streams : sms)), dim3(WideShape::kThreads), WideShape::kSmem,
+                      stream, true, tk, tv, a, w);
   if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: launch");
   if (apart) return CB_OK;
   const int64_t rows = int64_t(a.num_tokens) * a.num_heads;
@@ -506,7 +518,7 @@ cb_status run_quant_attention(const AttnArgs& a, const int32_t* cu_groups, const
   NvtxRange nvtx("cb.ragged_attention_q8");
   if (int64_t(a.num_blocks) * a.num_kv_heads >= (int64_t(1) << 31))
     return fail(CB_ERR_UNSUPPORTED, "8-bit attention: num_blocks * num_kv_heads must fit in int32");
-  const int G = a.num_heads / a.num_kv_heads, sets = stream_sets(a), threads = 32 * stream_warps(sets);
+  const int G = a.num_heads / a.num_kv_heads, sets = stream_sets(a), threads = sets == 1 ? SharesShape::kThreads : WideShape::kThreads;
   const int64_t rows = int64_t(a.max_q_len) * G, row_tiles = (rows + 8 * sets - 1) / (8 * sets);
   const int64_t tiles = (int64_t(a.max_context_len) + qstream::kTileKeys - 1) / qstream::kTileKeys;
   const float key_bytes = 2.0f * HD * float(a.num_kv_heads);
@@ -520,7 +532,7 @@ cb_status run_quant_attention(const AttnArgs& a, const int32_t* cu_groups, const
   const PrefixSizes z = listed_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups, a.max_context_len);
   PrefixWork w;
   const int lsets = listed_sets(G);
-  cb_status st = prefix_work(a, cu_groups, prefix_lens, num_groups, z, stream_warps(lsets), 8 * lsets, workspace, &w);
+  cb_status st = prefix_work(a, cu_groups, prefix_lens, num_groups, z, listed_warps(lsets), 8 * lsets, workspace, &w);
   if (st != CB_OK) return st;
   w.key_bytes = key_bytes;
   w.tile_us_two = kTileUsTwo;
@@ -548,8 +560,10 @@ cb_status run_quant_attention(const AttnArgs& a, const int32_t* cu_groups, const
     e = launch_kernel(q8_pieces_kernel, dim3(unsigned(w.num_sms)), dim3(qpieces::kThreads), qpieces::kSmemBytes, stream, true, tq, tk64,
                       tv64, a, w);
   if (e == cudaSuccess)
-    e = launch_kernel(lsets == 1 ? q8_streams_kernel<1> : q8_streams_kernel<2>, dim3(unsigned(w.num_sms)),
-                      dim3(32 * stream_warps(lsets)), stream_smem(lsets), stream, true, tk16, tv16, a, w, pieces ? 0 : 1);
+    e = lsets == 1 ? launch_kernel(q8_streams_kernel<FewShape>, dim3(unsigned(w.num_sms)), dim3(FewShape::kThreads), FewShape::kSmem,
+                                   stream, true, tk16, tv16, a, w, pieces ? 0 : 1)
+                   : launch_kernel(q8_streams_kernel<WideShape>, dim3(unsigned(w.num_sms)), dim3(WideShape::kThreads), WideShape::kSmem,
+                                   stream, true, tk16, tv16, a, w, pieces ? 0 : 1);
   if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: launch");
   const int64_t rows_all = int64_t(a.num_tokens) * a.num_heads;
   if (rows_all <= int64_t(w.num_sms) * 4) return launch_prefix_join(a, w, stream);

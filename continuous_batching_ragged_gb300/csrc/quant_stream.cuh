@@ -44,20 +44,30 @@ constexpr uint32_t kBox = kTileKeys * kDim;            // 2 KB, rows of 128 byte
 constexpr uint32_t kStageBytes = 2 * kBox;
 constexpr int kBarArrivals = 3;                        // of a stage: the copies' bytes, and either scale
 
-// Warps of a CTA and tiles in flight of each: as many warps as the registers allow, 192 KB in flight.
-template <int NT>
+// Warps of a CTA, and 192 KB of tiles in flight.  Two tiles an iteration: more independent work between one matrix step and
+// the next, and half the barriers' and maxima's part of it (256 rows of 32 heads at 4096 keys: 777 us one at a time, 727 so).
+// 16 warps take 128 registers each, which hides most latency where streams are long and HBM bounds them (727 us; 12 warps 768);
+// 12 warps start and end sooner (4 rows at 512 keys 8.7 us and 9.5, 64 rows behind a shared prompt 37.3 and 39.3).  With 16 rows
+// a unit 8 warps of 231 registers (140 rows of 32 heads on one: 44.9 us; 12 warps, which spill: 53.4).
+template <int NT, int WARPS>
 struct Shape {
-  static constexpr int kWarps = NT == 1 ? 16 : 8;
+  static constexpr int kSets = NT;
+  static constexpr int kWarps = WARPS;
   static constexpr int kStages = 48 / kWarps;
+  static constexpr int kAtOnce = 2;                    // tiles of an iteration
   static constexpr int kRows = 8 * NT;                 // query rows of a unit, at most
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr uint32_t kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr uint32_t kWarpBarBytes = kStages * 16;   // barriers, then (key, value) scales of each stage
   static constexpr uint32_t kSlotBytes = kWarps * 2 * sizeof(SuffixItem);
   static constexpr uint32_t kOffBars = kRingBytes;
   static constexpr uint32_t kOffSlots = kOffBars + kWarps * kWarpBarBytes;
   static constexpr uint32_t kSmem = kOffSlots + kSlotBytes + 1024;   // + slack to align the ring
-  static_assert(kOffSlots % 16 == 0 && kSmem <= 220 * 1024, "shared memory");
+  static_assert(48 % kWarps == 0 && kStages >= kAtOnce && kOffSlots % 16 == 0 && kSmem <= 220 * 1024, "shared memory");
 };
+using SharesShape = Shape<1, 16>;                      // up to 8 rows, all tiles of a step dealt out
+using FewShape = Shape<1, 12>;                         // up to 8 rows, a CTA to a stream, or listed units
+using WideShape = Shape<2, 8>;                         // up to 16 rows
 
 __device__ __forceinline__ void copy4_async(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -169,11 +179,11 @@ struct RangeUnits {
 
 // One warp.  `ring` and `slots` are its own, so are `bars`: kStages barriers (initialised for kBarArrivals), then kStages
 // pairs of scales, which `scales` points to.
-template <int NT, class Units>
+template <class Sh, class Units>
 __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensorMap* tm_v, const AttnArgs& a, float* recs,
                                          float2* rec_ml, uint32_t ring, uint32_t bars, const volatile float2* scales,
                                          SuffixItem* slots, Units& units) {
-  constexpr int kStages = Shape<NT>::kStages, kRows = Shape<NT>::kRows;
+  constexpr int NT = Sh::kSets, kStages = Sh::kStages, kRows = Sh::kRows, kAtOnce = Sh::kAtOnce;
   const int lane = threadIdx.x & 31;
   const int H = a.num_heads, Hkv = a.num_kv_heads, G = H / Hkv, B = a.block_size;
   const int boxes = a.num_blocks * Hkv;
@@ -293,65 +303,89 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
 #pragma unroll
       for (int e = 0; e < 2; ++e) m[n][e] = mw[n][e] = -INFINITY, l[n][e] = 0.f, fw[n][e] = 1.f;
     }
-    for (int i = 0; i < cur.n; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * st_out, phase))) {
-        ok = false;
-        break;
+    // Tiles i .. i + U - 1 of the unit; false after a timeout.
+    auto tiles = [&](auto U_, int i) -> bool {
+      constexpr int U = decltype(U_)::value;
+      uint32_t kt[U];
+      float ks[U], vs[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * st_out, phase))) {
+          consumed += u;                                 // for the waits at the end
+          return false;
+        }
+        ks[u] = scales[st_out].x, vs[u] = scales[st_out].y;
+        kt[u] = ring + st_out * kStageBytes;
+        if (++st_out == kStages) st_out = 0, phase ^= 1;
       }
-      const float ks = scales[st_out].x, vs = scales[st_out].y;
-      const uint32_t kt = ring + st_out * kStageBytes, vt = kt + kBox;
       const int kb = k0 + i * kTileKeys;
-      if (kb + kTileKeys > ctx) {                        // rows behind the sequence's last key: P is 0, but 0 * NaN is not
-        const int from = ctx - kb;
+      if (kb + U * kTileKeys > ctx) {                    // rows behind the sequence's last key: P is 0, but 0 * NaN is not
+        const int from = ctx - kb - (U - 1) * kTileKeys;   // of the last tile, which has a key
         for (int c = lane; c < (kTileKeys - from) * 8; c += 32)
-          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vt + (from + c / 8) * 128 + (c % 8) * 16), "r"(0) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(kt[U - 1] + kBox + (from + c / 8) * 128 + (c % 8) * 16), "r"(0)
+                       : "memory");
         fence_proxy_async_smem();                        // before the slot's next TMA write
         __syncwarp();
       }
-      float s[NT][4];                                    // keys g: rows 2t, 2t + 1; keys 8 + g
+      float s[U][NT][4];                                 // keys g: rows 2t, 2t + 1; keys 8 + g
 #pragma unroll
-      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t kf[4];
-        ldmatrix4(kt + (part ^ (32 * j)), kf);
+        for (int n = 0; n < NT; ++n) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.f;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t a0 = e4m3x2_to_f16x2(kf[2 * x]), a1 = e4m3x2_to_f16x2(kf[2 * x + 1]);
-          const uint32_t a2 = e4m3x2_hi_to_f16x2(kf[2 * x]), a3 = e4m3x2_hi_to_f16x2(kf[2 * x + 1]);
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(s[n], a0, a1, a2, a3, qf[n][2 * j + x][0], qf[n][2 * j + x][1]);
-        }
-      }
-      if (kb + kTileKeys > lim_all) {
+        for (int u = 0; u < U; ++u) {
+          uint32_t kf[4];
+          ldmatrix4(kt[u] + (part ^ (32 * j)), kf);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t a0 = e4m3x2_to_f16x2(kf[2 * x]), a1 = e4m3x2_to_f16x2(kf[2 * x + 1]);
+            const uint32_t a2 = e4m3x2_hi_to_f16x2(kf[2 * x]), a3 = e4m3x2_hi_to_f16x2(kf[2 * x + 1]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (kb + g >= lim[n][e]) s[n][e] = -INFINITY;
-            if (kb + 8 + g >= lim[n][e]) s[n][2 + e] = -INFINITY;
+            for (int n = 0; n < NT; ++n) mma_f16(s[u][n], a0, a1, a2, a3, qf[n][2 * j + x][0], qf[n][2 * j + x][1]);
           }
+        }
+      if (kb + U * kTileKeys > lim_all) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (kb + u * kTileKeys + g >= lim[n][e]) s[u][n][e] = -INFINITY;
+              if (kb + u * kTileKeys + 8 + g >= lim[n][e]) s[u][n][2 + e] = -INFINITY;
+            }
       }
-      const float lv = fmaxf(lg2(vs), -126.f);
-      float af[NT][2], top[NT][2];
+      float lv[U], af[U][NT][2], top[NT][2], topw[NT][2];
       bool grown = false;
+#pragma unroll
+      for (int u = 0; u < U; ++u) lv[u] = fmaxf(lg2(vs[u]), -126.f);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          af[n][e] = fmaxf(ef[n][e] * ks, 1.2e-38f);     // not 0: -inf stays
-          top[n][e] = fmaxf(s[n][e], s[n][2 + e]) * af[n][e];
-          grown = grown || top[n][e] > m[n][e] + 8.0f || top[n][e] + lv > mw[n][e] + 8.0f;
+          top[n][e] = topw[n][e] = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            af[u][n][e] = fmaxf(ef[n][e] * ks[u], 1.2e-38f);   // not 0: -inf stays
+            const float x = fmaxf(s[u][n][e], s[u][n][2 + e]) * af[u][n][e];
+            top[n][e] = fmaxf(top[n][e], x), topw[n][e] = fmaxf(topw[n][e], x + lv[u]);
+          }
+          grown = grown || top[n][e] > m[n][e] + 8.0f || topw[n][e] > mw[n][e] + 8.0f;
         }
       if (__any_sync(0xffffffffu, grown)) {              // stale maxima are kept while 2^x stays <= 2^8
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = top[n][e];
+            float x = top[n][e], y = topw[n][e];
 #pragma unroll
-            for (int d = 4; d <= 16; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-            const float to = fmaxf(m[n][e], x), tw = fmaxf(mw[n][e], x + lv);
+            for (int d = 4; d <= 16; d <<= 1) {
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+            }
+            const float to = fmaxf(m[n][e], x), tw = fmaxf(mw[n][e], y);
             if (to != -INFINITY) {                       // the row has seen a key
               l[n][e] *= ex2(m[n][e] - to);
               const float f = ex2(mw[n][e] - tw);
@@ -362,39 +396,46 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
             m[n][e] = to, mw[n][e] = tw;
           }
       }
-      uint32_t pf[NT][2];                                // weights in f16: within 2^-11 of each, 2^-25 of 2^(M - m)
+      uint32_t pf[U][NT][2];                             // weights in f16: within 2^-11 of each, 2^-25 of 2^(M - m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float p[4];
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float z = m[n][e] == -INFINITY ? 0.f : -m[n][e], c = fminf(vs * fw[n][e], 3e38f);
-          const float x = ex2(fmaf(s[n][e], af[n][e], z)), y = ex2(fmaf(s[n][2 + e], af[n][e], z));
-          l[n][e] += x + y;
-          p[e] = x * c, p[2 + e] = y * c;
+        for (int n = 0; n < NT; ++n) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float z = m[n][e] == -INFINITY ? 0.f : -m[n][e], c = fminf(vs[u] * fw[n][e], 3e38f);
+            const float x = ex2(fmaf(s[u][n][e], af[u][n][e], z)), y = ex2(fmaf(s[u][n][2 + e], af[u][n][e], z));
+            l[n][e] += x + y;
+            p[e] = x * c, p[2 + e] = y * c;
+          }
+          pf[u][n][0] = transpose8(pack_f16(p[0], p[1]));
+          pf[u][n][1] = transpose8(pack_f16(p[2], p[3]));
         }
-        pf[n][0] = transpose8(pack_f16(p[0], p[1]));
-        pf[n][1] = transpose8(pack_f16(p[2], p[3]));
-      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t vf[4];
-        ldmatrix4_trans(vt + (part ^ (32 * j)), vf);
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) vf[x] = __byte_perm(vf[x], 0, 0x3120);   // (key, key + 1) of the even dim, of the odd dim
+        for (int u = 0; u < U; ++u) {
+          uint32_t vf[4];
+          ldmatrix4_trans(kt[u] + kBox + (part ^ (32 * j)), vf);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t a0 = e4m3x2_to_f16x2(vf[2 * x]), a1 = e4m3x2_hi_to_f16x2(vf[2 * x]);
-          const uint32_t a2 = e4m3x2_to_f16x2(vf[2 * x + 1]), a3 = e4m3x2_hi_to_f16x2(vf[2 * x + 1]);
+          for (int x = 0; x < 4; ++x) vf[x] = __byte_perm(vf[x], 0, 0x3120);   // (key, key + 1) of the even dim, of the odd dim
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * j + x], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t a0 = e4m3x2_to_f16x2(vf[2 * x]), a1 = e4m3x2_hi_to_f16x2(vf[2 * x]);
+            const uint32_t a2 = e4m3x2_to_f16x2(vf[2 * x + 1]), a3 = e4m3x2_hi_to_f16x2(vf[2 * x + 1]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * j + x], a0, a1, a2, a3, pf[u][n][0], pf[u][n][1]);
+          }
         }
-      }
-      __syncwarp();                                      // every lane has read the slot
-      ++consumed;
-      if (++st_out == kStages) st_out = 0, phase ^= 1;
+      __syncwarp();                                      // every lane has read the slots
+      consumed += U;
       top_up();
-    }
+      return true;
+    };
+    int i = 0;
+    for (; ok && i + kAtOnce <= cur.n; i += kAtOnce) ok = tiles(std::integral_constant<int, kAtOnce>(), i);
+    if (ok && i < cur.n) ok = tiles(std::integral_constant<int, 1>(), i);
     if (!ok) break;
     // the rows' records, or, with nothing to join, the rows; o is in units of 2^M, a record's in 2^m
 #pragma unroll
