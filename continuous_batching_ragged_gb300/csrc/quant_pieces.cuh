@@ -41,7 +41,8 @@ constexpr uint32_t kTile = 2 * kHalf;
 constexpr uint32_t kStaged = HN * HD;            // 64 keys in 8 bits
 constexpr uint32_t kTmemCols = 512;              // per slot t: S (then P) at 256t, O at 256t + 128
 constexpr int kScaleSlots = 6;                   // tiles whose scales are kept: the softmax may be 4 behind the loader
-constexpr int kTileScales = 24;                  // of K, of V, their logarithms
+constexpr int kTileScales = 16;                  // of K, and the logarithms of V's
+constexpr float kNoScore = -3e38f;               // maxima before the first key
 
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + 2 * kTile;
@@ -131,6 +132,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ float lds4(uint32_t addr) {
@@ -283,7 +292,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
       }
       uint32_t tile = (tiles + (alt ? t : 0)) % kScaleSlots;
       tiles += nt;
-      float m = -INFINITY, l = 0.f, mw = -INFINITY, fw = 1.f, sl2 = 0.f;   // mw: M; fw: 2^(m - M)
+      float m = kNoScore, l = 0.f, mw = kNoScore, sl2 = 0.f;   // mw: M
 #pragma unroll 1
       for (int x = 0; x < steps; ++x) {
         if (!warp_wait(BAR_S + t, cnt + x, kSitePfS)) break;
@@ -297,23 +306,40 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
           if (lane == 0) mbar_arrive(bar(BAR_QE));
         }
         tc_fence_after();
-        // Half of the scores is held between the maxima and the weights, the other half read twice: all 128 held need some 200
-        // registers a thread, which leave too few warps to widen (a 2048-token chunk behind 30,720 keys, 32 heads: 1513 us), all read twice
-        // took 1471 us, and so 1343.  The weights go over scores that are not read again.
+        // One pass, 32 keys at a time: weights by the maxima that the row has, which hold for nearly all keys behind the first;
+        // where their sum shows a weight beyond f16, the maxima are raised, what they scaled so far is rescaled (M is whole, so that
+        // is exact but for numbers below f16's normal ones), and the 32 keys are weighed again.
         const bool masked = BN > lim_warp;         // keys behind the last one, or the causal mask
         const uint32_t sc = base + kOffScales + tile * (kTileScales * 4);
-        uint32_t buf[2][32];
-        auto mask = [&](int c, uint32_t (&s)[32]) {
-          if (masked) {
+        auto factor = [&](int g) { return fmaxf(sl2 * lds4(sc + 4 * g), 1.2e-38f); };   // of 16 keys' scores; not 0: -inf stays
+        // weights times the values' scale, in units of 2^M, in f16: within 2^-11 of each, 2^-25 of 2^M; `sum` is theirs, `add`
+        // that of the weights alone, in units of 2^m.  A scale too small for any of its weights to count is raised to one
+        // whose weights' sum is still in fp32's range.
+        auto weigh = [&](int c, const uint32_t (&sr)[32], uint32_t (&p)[16], float& sum, float& add) {
+          const float d = mw - m;
+          sum = add = 0.f;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e >= lim) s[e] = __float_as_uint(-INFINITY);
+          for (int g = 0; g < 2; ++g) {
+            const float f = factor(2 * c + g), lv = fmaxf(lds4(sc + 32 + 4 * (2 * c + g)), d - 60.f), z = lv - mw;
+            const uint64_t f2 = f2_pack(f, f), z2 = f2_pack(z, z);
+            uint64_t s2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int k = 16 * g + 2 * e;
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), f2, z2), x0, x1);
+              x0 = ex2(x0), x1 = ex2(x1);
+              s2[e & 1] = f2_add(s2[e & 1], f2_pack(x0, x1));
+              p[8 * g + e] = pack_f16x2(x0, x1);
+            }
+            float r0, r1;
+            f2_unpack(f2_add(s2[0], s2[1]), r0, r1);
+            sum += r0 + r1;
+            add = fmaf(r0 + r1, ex2(d - lv), add);
           }
         };
-        auto factor = [&](int g) { return fmaxf(sl2 * lds4(sc + 4 * g), 1.2e-38f); };   // of 16 keys' scores; not 0: -inf stays
-        float mt = -INFINITY, wt = -INFINITY;
-        auto maxima = [&](int c, uint32_t (&sr)[32]) {
-          mask(c, sr);
+        auto raise = [&](int c, const uint32_t (&sr)[32]) {
+          float mt = kNoScore, wt = kNoScore;
 #pragma unroll
           for (int g = 0; g < 2; ++g) {            // 16 keys of one block
             auto s = [&](int e) { return __uint_as_float(sr[16 * g + e]); };
@@ -321,85 +347,64 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             const float v = max3(max3(s(9), s(10), s(11)), max3(s(12), s(13), s(14)), s(15));
             const float top = fmaxf(u, v) * factor(2 * c + g);
             mt = fmaxf(mt, top);
-            wt = fmaxf(wt, top + lds4(sc + 64 + 4 * (2 * c + g)));
+            wt = fmaxf(wt, top + fmaxf(lds4(sc + 32 + 4 * (2 * c + g)), -126.f));
           }
-        };
-        tmem_ld32(lane_base + 64, buf[0]);
-        tmem_ld32(lane_base + 96, buf[1]);
-        tmem_wait_ld();
-        maxima(2, buf[0]);
-        tmem_ld32(lane_base, buf[0]);
-        maxima(3, buf[1]);
-        tmem_wait_ld();
-        tmem_ld32(lane_base + 32, buf[1]);
-        maxima(0, buf[0]);
-        tmem_wait_ld();
-        maxima(1, buf[1]);
-        const bool resc = mt > m + 8.0f || wt > mw + 8.0f;   // keep stale maxima while 2^x stays <= 2^8
-        float alpha = 1.0f;                        // of O
-        if (resc) {
-          const float m_new = fmaxf(m, mt), w_new = fmaxf(mw, wt);
+          const float m_new = fmaxf(m, mt), w_new = fmaxf(mw, ceilf(wt) - 1.f), alpha = ex2(mw - w_new);
           l *= ex2(m - m_new);
-          alpha = ex2(mw - w_new);
-          m = m_new;
-          mw = w_new;
-          fw = ex2(fminf(m - mw, 126.f));
-        }
-        const float m_sub = m == -INFINITY ? 0.f : m;   // scores all -inf so far
-        const uint64_t neg_m2 = f2_pack(-m_sub, -m_sub);
-        uint64_t sum2[4] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-        // weights times the values' scale over the scores, in f16: within 2^-11 of each, 2^-25 of 2^(M - m); the sums are of
-        // the weights in fp32
-        auto weigh = [&](int c, uint32_t (&sr)[32], uint32_t (&p)[16]) {
+          m = m_new, mw = w_new;
+          tmem_wait_st();                          // of this tile's weights so far
+#pragma unroll 1
+          for (int k = 0; k < c; ++k) {
+            uint32_t p[16];
+            tmem_ld16(lane_base + 16 * k, p);
+            tmem_wait_ld();
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float f = factor(2 * c + g), vs = fminf(lds4(sc + 32 + 4 * (2 * c + g)) * fw, 3e38f);
-            const uint64_t f2 = f2_pack(f, f), vs2 = f2_pack(vs, vs);
+            for (int e = 0; e < 16; ++e) {
+              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&p[e]));
+              p[e] = pack_f16x2(v.x * alpha, v.y * alpha);
+            }
+            tmem_st16(lane_base + 16 * k, p);
+          }
+          // S done implies the slot's earlier P V done (one thread issues both, in order, and the commit behind S covers them):
+          // O is stable
+          if (x > 0) {
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+              uint32_t o[16];
+              tmem_ld16(lane_base + 128 + 16 * k, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int k = 16 * g + 2 * e;
-              float x0, x1, p0, p1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), f2, neg_m2), x0, x1);
-              const uint64_t p2 = f2_pack(ex2(x0), ex2(x1));
-              sum2[e & 3] = f2_add(sum2[e & 3], p2);
-              f2_unpack(f2_mul(p2, vs2), p0, p1);
-              p[8 * g + e] = pack_f16x2(p0, p1);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(lane_base + 128 + 16 * k, o);
             }
           }
         };
-        uint32_t p[2][16];
-        weigh(0, buf[0], p[0]);
-        tmem_ld32(lane_base + 64, buf[0]);         // those of the other half that are read again lie behind the weights
-        weigh(1, buf[1], p[1]);
-        tmem_st16(lane_base, p[0]);
-        tmem_st16(lane_base + 16, p[1]);
-        tmem_wait_ld();
-        tmem_ld32(lane_base + 96, buf[1]);
-        mask(2, buf[0]);
-        weigh(2, buf[0], p[0]);
-        tmem_st16(lane_base + 32, p[0]);
-        tmem_wait_ld();
-        mask(3, buf[1]);
-        weigh(3, buf[1], p[1]);
-        tmem_st16(lane_base + 48, p[1]);
-        float r0, r1, r2, r3, r4, r5, r6, r7;
-        f2_unpack(sum2[0], r0, r1);
-        f2_unpack(sum2[1], r2, r3);
-        f2_unpack(sum2[2], r4, r5);
-        f2_unpack(sum2[3], r6, r7);
-        l += ((r0 + r1) + (r2 + r3)) + ((r4 + r5) + (r6 + r7));
-        // S done implies the slot's earlier P V done (one thread issues both, in order,
-        // and the commit behind S covers them): O is stable for the rescale
-        if (x > 0 && __any_sync(0xffffffffu, resc)) {
+        auto chunk = [&](int c, uint32_t (&sr)[32]) {
+          if (masked) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(lane_base + 128 + 32 * c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(lane_base + 128 + 32 * c, o);
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e >= lim) sr[e] = __float_as_uint(-INFINITY);
           }
+          uint32_t p[16];
+          float sum, add;
+          weigh(c, sr, p, sum, add);
+          if (__any_sync(0xffffffffu, sum > 32768.f || add > 1e12f)) {
+            raise(c, sr);
+            weigh(c, sr, p, sum, add);
+          }
+          l += add;
+          tmem_st16(lane_base + 16 * c, p);        // over scores that are in registers
+        };
+        uint32_t buf[2][32];
+        tmem_ld32(lane_base, buf[0]);
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          tmem_wait_ld();
+          tmem_ld32(lane_base + 32 * c + 32, buf[1]);
+          chunk(c, buf[0]);
+          tmem_wait_ld();
+          if (c == 0) tmem_ld32(lane_base + 64, buf[0]);
+          chunk(c + 1, buf[1]);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -425,7 +430,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
                      : it->rec0 + unsigned((row_tok * H + head) * it->rec_step + (alt ? t : 0));
       }
       item_read(n);
-      const float to_m = m == -INFINITY ? 0.f : ex2(mw - m);   // O is in units of 2^M, a record's in 2^m
+      const float to_m = ex2(mw - m);   // O is in units of 2^M, a record's in 2^m
       const float inv = direct ? to_m / l : to_m;
       if (work) {
         const int row4 = wq * 32 + (lane & ~3);
@@ -470,7 +475,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             }
           }
         }
-        if (i < rows && !direct) __stcg(w.rec_ml + rec, make_float2(m, l));
+        if (i < rows && !direct) __stcg(w.rec_ml + rec, make_float2(m == kNoScore ? -INFINITY : m, l));
       }
       tc_fence_before();                           // O read before the next piece's first P V overwrites it
     }
@@ -529,8 +534,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
               if (hc >= 2 && !warp_wait(BAR_SE + buf, (hc >> 1) - 1, kSitePfKFree)) break;
               if (hh == 0) {                       // ahead of the half, which carries them to the softmax
                 float* to = scales + (tc % kScaleSlots) * kTileScales + lane;
-                if (lane < 16) to[0] = scale;
-                if (lane >= 8 && lane < 16) to[8] = fmaxf(qstream::lg2(scale), -126.f);
+                if (lane < 16) to[0] = lane < 8 ? scale : qstream::lg2(scale);
                 __syncwarp();
               }
               win.load(base + kOffStaged + buf * kStaged, tm_k, bar(BAR_SF + buf), a, j, hh, lane);
