@@ -312,40 +312,45 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         const bool masked = BN > lim_warp;         // keys behind the last one, or the causal mask
         const uint32_t sc = base + kOffScales + tile * (kTileScales * 4);
         auto factor = [&](int g) { return fmaxf(sl2 * lds4(sc + 4 * g), 1.2e-38f); };   // of 16 keys' scores; not 0: -inf stays
-        // weights times the values' scale, in units of 2^M, in f16: within 2^-11 of each, 2^-25 of 2^M; `sum` is theirs, `add`
-        // that of the weights alone, in units of 2^m.  A scale too small for any of its weights to count is raised to one
-        // whose weights' sum is still in fp32's range.
-        auto weigh = [&](int c, const uint32_t (&sr)[32], uint32_t (&p)[16], float& sum, float& add) {
-          const float d = mw - m;
-          sum = add = 0.f;
+        // Of 16 keys of one block, in units of 2^M and f16: weights times the values' scale, within 2^-11 of each, 2^-25 of 2^M;
+        // `sum` is theirs, `add` that of the weights alone, in units of 2^m.  A scale too small for any of its weights to count is
+        // raised to one whose weights' sum is still in fp32's range.
+        auto weigh = [&](int g, uint32_t (&sr)[16], uint32_t* p, float& sum, float& add) {
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (16 * g + e >= lim) sr[e] = __float_as_uint(-INFINITY);
+          }
+          const float d = mw - m, f = factor(g), lv = fmaxf(lds4(sc + 32 + 4 * g), d - 60.f), z = lv - mw;
+          const uint64_t f2 = f2_pack(f, f), z2 = f2_pack(z, z);
+          uint64_t s2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, z2), x0, x1);
+            x0 = ex2(x0), x1 = ex2(x1);
+            s2[e & 1] = f2_add(s2[e & 1], f2_pack(x0, x1));
+            p[e] = pack_f16x2(x0, x1);
+          }
+          float r0, r1;
+          f2_unpack(f2_add(s2[0], s2[1]), r0, r1);
+          sum += r0 + r1;
+          add = fmaf(r0 + r1, ex2(d - lv), add);
+        };
+        // Raises the maxima to those of keys 32 c .. 32 c + 31, with what they scaled so far.
+        auto raise = [&](int c) {
+          float mt = kNoScore, wt = kNoScore;
+          uint32_t sr[32];
+          tmem_ld32(lane_base + 32 * c, sr);
+          tmem_wait_ld();
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const float f = factor(2 * c + g), lv = fmaxf(lds4(sc + 32 + 4 * (2 * c + g)), d - 60.f), z = lv - mw;
-            const uint64_t f2 = f2_pack(f, f), z2 = f2_pack(z, z);
-            uint64_t s2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+            float top = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int k = 16 * g + 2 * e;
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), f2, z2), x0, x1);
-              x0 = ex2(x0), x1 = ex2(x1);
-              s2[e & 1] = f2_add(s2[e & 1], f2_pack(x0, x1));
-              p[8 * g + e] = pack_f16x2(x0, x1);
-            }
-            float r0, r1;
-            f2_unpack(f2_add(s2[0], s2[1]), r0, r1);
-            sum += r0 + r1;
-            add = fmaf(r0 + r1, ex2(d - lv), add);
-          }
-        };
-        auto raise = [&](int c, const uint32_t (&sr)[32]) {
-          float mt = kNoScore, wt = kNoScore;
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {            // 16 keys of one block
-            auto s = [&](int e) { return __uint_as_float(sr[16 * g + e]); };
-            const float u = max3(max3(s(0), s(1), s(2)), max3(s(3), s(4), s(5)), max3(s(6), s(7), s(8)));
-            const float v = max3(max3(s(9), s(10), s(11)), max3(s(12), s(13), s(14)), s(15));
-            const float top = fmaxf(u, v) * factor(2 * c + g);
+            for (int e = 0; e < 16; ++e)
+              if (!masked || 32 * c + 16 * g + e < lim) top = fmaxf(top, __uint_as_float(sr[16 * g + e]));
+            top *= factor(2 * c + g);
+            top = fmaf(fabsf(top), 0x1p-22f, top); // above what fma makes of the scores
             mt = fmaxf(mt, top);
             wt = fmaxf(wt, top + fmaxf(lds4(sc + 32 + 4 * (2 * c + g)), -126.f));
           }
@@ -379,32 +384,28 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             }
           }
         };
-        auto chunk = [&](int c, uint32_t (&sr)[32]) {
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e >= lim) sr[e] = __float_as_uint(-INFINITY);
-          }
+        uint32_t s0[16], s1[16];
+        tmem_ld16(lane_base, s0);
+        int raised = -1;                           // the last 32 keys that were; once each, whatever the scores
+#pragma unroll 1
+        for (int c = 0; c < 4;) {
           uint32_t p[16];
-          float sum, add;
-          weigh(c, sr, p, sum, add);
-          if (__any_sync(0xffffffffu, sum > 32768.f || add > 1e12f)) {
-            raise(c, sr);
-            weigh(c, sr, p, sum, add);
+          float sum = 0.f, add = 0.f;
+          tmem_wait_ld();
+          tmem_ld16(lane_base + 32 * c + 16, s1);
+          weigh(2 * c, s0, p, sum, add);
+          tmem_wait_ld();
+          if (c < 3) tmem_ld16(lane_base + 32 * c + 32, s0);
+          weigh(2 * c + 1, s1, p + 8, sum, add);
+          if (raised < c && __any_sync(0xffffffffu, sum > 32768.f || add > 1e12f)) {
+            raise(c);
+            raised = c;
+            tmem_ld16(lane_base + 32 * c, s0);     // once more
+            continue;
           }
           l += add;
           tmem_st16(lane_base + 16 * c, p);        // over scores that are in registers
-        };
-        uint32_t buf[2][32];
-        tmem_ld32(lane_base, buf[0]);
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          tmem_wait_ld();
-          tmem_ld32(lane_base + 32 * c + 32, buf[1]);
-          chunk(c, buf[0]);
-          tmem_wait_ld();
-          if (c == 0) tmem_ld32(lane_base + 64, buf[0]);
-          chunk(c + 1, buf[1]);
+          ++c;
         }
         tmem_wait_st();
         tc_fence_before();
@@ -708,6 +709,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         for (int t = 0; t < nq; ++t) {
           const uint32_t at = base + kOffQ + t * kTile + row * 128;
           uint32_t top = 0;                        // bits of the largest magnitude
+          const bool real = row < G * TT;          // the rows behind hold anything: zeros, whose scores raise no maximum
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const uint4 v = lds16(at + (k >> 3) * kHalf + (((k & 7) ^ (row & 7)) << 4));
@@ -715,13 +717,14 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = max(top, max((in[e] << 16) & 0x7fff0000u, in[e] & 0x7fff0000u));
           }
-          const uint32_t ex = min(254u, 267u - (top >> 23));   // 2^13 / largest, as an exponent
+          const uint32_t ex = real ? min(254u, 267u - (top >> 23)) : 127u;   // 2^13 / largest, as an exponent
           const float f = __uint_as_float(ex << 23);
           reinterpret_cast<float*>(gsm + kOffFactors)[t * BM + row] = __uint_as_float((254u - ex) << 23);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const uint32_t p = at + (k >> 3) * kHalf + (((k & 7) ^ (row & 7)) << 4);
-            const uint4 v = lds16(p);
+            uint4 v = lds16(p);
+            if (!real) v = make_uint4(0, 0, 0, 0);
             auto two = [&](uint32_t x) { return pack_f16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f); };
             sts16(p, two(v.x), two(v.y), two(v.z), two(v.w));
           }

@@ -385,6 +385,7 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
             }
+            x = fmaf(fabsf(x), 0x1p-22f, x), y = fmaf(fabsf(y), 0x1p-22f, y);   // above what fma makes of the scores
             const float to = fmaxf(m[n][e], x), tw = fmaxf(mw[n][e], y);
             if (to != -INFINITY) {                       // the row has seen a key
               l[n][e] *= ex2(m[n][e] - to);
