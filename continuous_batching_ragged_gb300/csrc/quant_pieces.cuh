@@ -35,6 +35,7 @@ constexpr int HN = BN / 2;                       // of a staged half
 constexpr int HD = kPrefixDim;
 constexpr int kStages = 2;                       // K tiles, and V tiles
 constexpr int kThreads = 512;
+constexpr int kWidenRows = 2;                    // that a lane widens at once
 constexpr int kWarpK = 8, kWarpMma = 9, kWarpV = 10, kWarpWiden = 12;
 constexpr uint32_t kHalf = BM * 64 * 2;          // one 64-dim swizzled half of a bf16 tile: 16 KB
 constexpr uint32_t kTile = 2 * kHalf;
@@ -145,6 +146,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 __device__ __forceinline__ float lds4(uint32_t addr) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float2 lds8(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -312,31 +318,6 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         const bool masked = BN > lim_warp;         // keys behind the last one, or the causal mask
         const uint32_t sc = base + kOffScales + tile * (kTileScales * 4);
         auto factor = [&](int g) { return fmaxf(sl2 * lds4(sc + 4 * g), 1.2e-38f); };   // of 16 keys' scores; not 0: -inf stays
-        // Of 16 keys of one block, in units of 2^M and f16: weights times the values' scale, within 2^-11 of each, 2^-25 of 2^M;
-        // `sum` is theirs, `add` that of the weights alone, in units of 2^m.  A scale too small for any of its weights to count is
-        // raised to one whose weights' sum is still in fp32's range.
-        auto weigh = [&](int g, uint32_t (&sr)[16], uint32_t* p, float& sum, float& add) {
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (16 * g + e >= lim) sr[e] = __float_as_uint(-INFINITY);
-          }
-          const float d = mw - m, f = factor(g), lv = fmaxf(lds4(sc + 32 + 4 * g), d - 60.f), z = lv - mw;
-          const uint64_t f2 = f2_pack(f, f), z2 = f2_pack(z, z);
-          uint64_t s2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float x0, x1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, z2), x0, x1);
-            x0 = ex2(x0), x1 = ex2(x1);
-            s2[e & 1] = f2_add(s2[e & 1], f2_pack(x0, x1));
-            p[e] = pack_f16x2(x0, x1);
-          }
-          float r0, r1;
-          f2_unpack(f2_add(s2[0], s2[1]), r0, r1);
-          sum += r0 + r1;
-          add = fmaf(r0 + r1, ex2(d - lv), add);
-        };
         // Raises the maxima to those of keys 32 c .. 32 c + 31, with what they scaled so far.
         auto raise = [&](int c) {
           float mt = kNoScore, wt = kNoScore;
@@ -384,23 +365,52 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             }
           }
         };
-        uint32_t s0[16], s1[16];
-        tmem_ld16(lane_base, s0);
+        // Weights times the values' scale, in units of 2^M and f16: within 2^-11 of each, 2^-25 of 2^M; `sum` is theirs, `add` that of
+        // the weights alone, in units of 2^m.  A scale too small for any of its weights to count is raised to one whose weights' sum
+        // is still in fp32's range.
+        uint32_t sr[32];
+        tmem_ld32(lane_base, sr);
         int raised = -1;                           // the last 32 keys that were; once each, whatever the scores
 #pragma unroll 1
         for (int c = 0; c < 4;) {
+          const float2 ks = lds8(sc + 8 * c), lg = lds8(sc + 32 + 8 * c);
+          const float d = mw - m;
+          float lv[2] = {fmaxf(lg.x, d - 60.f), fmaxf(lg.y, d - 60.f)};
+          const float f[2] = {fmaxf(sl2 * ks.x, 1.2e-38f), fmaxf(sl2 * ks.y, 1.2e-38f)};   // not 0: -inf stays
+          tmem_wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * c + e >= lim) sr[e] = __float_as_uint(-INFINITY);
+          }
+          uint64_t x2[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float z = lv[e >> 3] - mw;
+            x2[e] = f2_fma(f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2_pack(f[e >> 3], f[e >> 3]), f2_pack(z, z));
+          }
+          if (c < 3) tmem_ld32(lane_base + 32 * c + 32, sr);
           uint32_t p[16];
-          float sum = 0.f, add = 0.f;
-          tmem_wait_ld();
-          tmem_ld16(lane_base + 32 * c + 16, s1);
-          weigh(2 * c, s0, p, sum, add);
-          tmem_wait_ld();
-          if (c < 3) tmem_ld16(lane_base + 32 * c + 32, s0);
-          weigh(2 * c + 1, s1, p + 8, sum, add);
-          if (raised < c && __any_sync(0xffffffffu, sum > 32768.f || add > 1e12f)) {
+          uint64_t s2[2][2];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float x0, x1;
+            f2_unpack(x2[e], x0, x1);
+            x0 = ex2(x0), x1 = ex2(x1);
+            p[e] = pack_f16x2(x0, x1);
+            const uint64_t y = f2_pack(x0, x1);
+            s2[e >> 3][e & 1] = (e & 7) < 2 ? y : f2_add(s2[e >> 3][e & 1], y);
+          }
+          float a0, a1, b0, b1;
+          f2_unpack(f2_add(s2[0][0], s2[0][1]), a0, a1);
+          f2_unpack(f2_add(s2[1][0], s2[1][1]), b0, b1);
+          a0 += a1, b0 += b1;
+          const float add = fmaf(a0, ex2(d - lv[0]), b0 * ex2(d - lv[1]));
+          if (raised < c && __any_sync(0xffffffffu, a0 + b0 > 32768.f || add > 1e12f)) {
+            tmem_wait_ld();
             raise(c);
             raised = c;
-            tmem_ld16(lane_base + 32 * c, s0);     // once more
+            tmem_ld32(lane_base + 32 * c, sr);     // once more
             continue;
           }
           l += add;
@@ -743,17 +753,21 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         for (int hh = 0; hh < 2; ++hh, ++hc) {
           const int buf = hc & 1;
           if (!warp_wait(BAR_SF + 2 * type + buf, hc >> 1, type ? kSitePfV : kSitePfK)) break;
-          uint4 x[8];
+#pragma unroll 1
+          for (int k0 = 0; k0 < 8; k0 += kWidenRows) {
+          uint4 x[kWidenRows];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = r0 + 4 * k;
+          for (int k = 0; k < kWidenRows; ++k) {
+            const int r = r0 + 4 * (k0 + k);
             x[k] = lds16(staged + buf * kStaged + r * HD + ((c ^ (r & 7)) << 4));
           }
+          if (k0 + kWidenRows == 8) {
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(BAR_SE + 2 * type + buf));
+          }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = hh * HN + r0 + 4 * k;
+          for (int k = 0; k < kWidenRows; ++k) {
+            const int r = hh * HN + r0 + 4 * (k0 + k);
             if (type && r >= left) x[k] = make_uint4(0, 0, 0, 0);
             const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
             uint32_t y[8];
@@ -761,13 +775,10 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             for (int e = 0; e < 4; ++e) y[2 * e] = e4m3x2_to_f16x2(in[e]), y[2 * e + 1] = e4m3x2_hi_to_f16x2(in[e]);
             const uint32_t row = ring + st * kTile + half * kHalf + r * 128, at0 = row + ((lo ^ (r & 7)) << 4),
                            at1 = row + (((lo + 1) ^ (r & 7)) << 4);
-            if (half) {
-              sts16(at1, y[4], y[5], y[6], y[7]);
-              sts16(at0, y[0], y[1], y[2], y[3]);
-            } else {
-              sts16(at0, y[0], y[1], y[2], y[3]);
-              sts16(at1, y[4], y[5], y[6], y[7]);
-            }
+            const bool h = half;
+            sts16(h ? at1 : at0, h ? y[4] : y[0], h ? y[5] : y[1], h ? y[6] : y[2], h ? y[7] : y[3]);
+            sts16(h ? at0 : at1, h ? y[0] : y[4], h ? y[1] : y[5], h ? y[2] : y[6], h ? y[3] : y[7]);
+          }
           }
           fence_proxy_async_smem();                // for the tensor core
           __syncwarp();
