@@ -48,8 +48,11 @@ constexpr int kMinShareTiles = 3;        // shortest share of a warp
 // and 13.5.
 constexpr int kApartTiles = 4;
 constexpr double kSharingBytes = 1.9e8;  // reads that sharing has to be able to save, for the plan to be worth its time
-// What the plan's estimates go by, in microseconds and bytes.
-constexpr float kTileUsTwo = 2.2f, kTileUsOne = 2.2f, kStreamBytesPerUsPerSm = 3.0e4f;
+// What the plan's estimates go by, in microseconds and bytes: a KV tile for two row tiles and for one, which the widening of
+// either bounds alike (measured 2.0), and what an SM's streams read beside pieces.  3 chunks of 662 tokens behind 2048 keys with
+// 64 decode rows, and with 200, 32/8 heads, us: these 146, 236; tiles of 1.7 153, 315; streams of 2.4e4 153, 315; of 4.2e4 146,
+// 239.
+constexpr float kTileUsTwo = 2.0f, kTileUsOne = 2.0f, kStreamBytesPerUsPerSm = 3.6e4f;
 
 // What the CTAs of a step without a plan kernel make of it, for the join.
 struct StepWork {

@@ -34,8 +34,9 @@ constexpr int BN = 128;                          // keys per KV tile
 constexpr int HN = BN / 2;                       // of a staged half
 constexpr int HD = kPrefixDim;
 constexpr int kStages = 2;                       // K tiles, and V tiles
+constexpr uint32_t kBufs = 2;                    // staged halves of K, and of V (with one, 1209 us of 1007)
 constexpr int kThreads = 512;
-constexpr int kWidenRows = 2;                    // that a lane widens at once
+constexpr int kWidenRows = 2;                    // that a lane widens at once (1: 1031 us of 1007, 4: 1021, 8: 1017)
 constexpr int kWarpK = 8, kWarpMma = 9, kWarpV = 10, kWarpWiden = 12;
 constexpr uint32_t kHalf = BM * 64 * 2;          // one 64-dim swizzled half of a bf16 tile: 16 KB
 constexpr uint32_t kTile = 2 * kHalf;
@@ -49,7 +50,7 @@ constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kOffQ + 2 * kTile;
 constexpr uint32_t kOffV = kOffK + kStages * kTile;
 constexpr uint32_t kOffStaged = kOffV + kStages * kTile;   // K's two, V's two
-constexpr uint32_t kOffBar = kOffStaged + 4 * kStaged;
+constexpr uint32_t kOffBar = kOffStaged + 2 * kBufs * kStaged;
 constexpr int kItemSlots = 2;
 constexpr int kItemReaders = 1 + 1 + 8 + 4;      // V loader, MMA, softmax and widening warps
 enum : int {
@@ -61,9 +62,9 @@ enum : int {
   BAR_O = BAR_P + 2,           // + slot: the piece's last P V in the slot done
   BAR_F = BAR_O + 2,           // + 2 * (0: K, 1: V) + stage: widened
   BAR_E = BAR_F + 4,           // + the same: consumed
-  BAR_SF = BAR_E + 4,          // + 2 * (0: K, 1: V) + buffer: a half landed
-  BAR_SE = BAR_SF + 4,         // + the same: read
-  BAR_IF = BAR_SE + 4,         // + slot: piece published
+  BAR_SF = BAR_E + 4,          // + kBufs * (0: K, 1: V) + buffer: a half landed
+  BAR_SE = BAR_SF + 2 * kBufs,   // + the same: read
+  BAR_IF = BAR_SE + 2 * kBufs,   // + slot: piece published
   BAR_IE = BAR_IF + kItemSlots,  // + slot: piece read by every role
   BAR_DONE = BAR_IE + kItemSlots,
   NUM_BARS = BAR_DONE + 1
@@ -218,6 +219,8 @@ __device__ __forceinline__ void init_bars(uint32_t base) {
   for (int i = 0; i < 4; ++i) {
     mbar_init(bar(BAR_F + i), 4);                  // two warps, two halves
     mbar_init(bar(BAR_E + i), 1);
+  }
+  for (int i = 0; i < 2 * kBufs; ++i) {
     mbar_init(bar(BAR_SF + i), 1);
     mbar_init(bar(BAR_SE + i), 2);                 // two warps
   }
@@ -541,8 +544,8 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             if (j == 1 && !q_loaded && !load_q()) break;
             win.advance(a, it.hk, j, lane);
             for (int hh = 0; hh < 2; ++hh) {
-              const int buf = hc & 1;
-              if (hc >= 2 && !warp_wait(BAR_SE + buf, (hc >> 1) - 1, kSitePfKFree)) break;
+              const int buf = hc % kBufs;
+              if (hc >= kBufs && !warp_wait(BAR_SE + buf, hc / kBufs - 1, kSitePfKFree)) break;
               if (hh == 0) {                       // ahead of the half, which carries them to the softmax
                 float* to = scales + (tc % kScaleSlots) * kTileScales + lane;
                 if (lane < 16) to[0] = lane < 8 ? scale : qstream::lg2(scale);
@@ -561,7 +564,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
       if (!ok && lane == 0) raise_error(a.err, kErrTimeout | site);
       if (lane == 0) {
         // (error path) let copies still in flight land before the memory is used again
-        for (uint32_t x = hc > 2u ? hc - 2 : 0; x < hc; ++x) mbar_wait(bar(BAR_SF + (x & 1)), (x >> 1) & 1);
+        for (uint32_t x = hc > kBufs ? hc - kBufs : 0; x < hc; ++x) mbar_wait(bar(BAR_SF + x % kBufs), (x / kBufs) & 1);
         if (qc > 0) mbar_wait(bar(BAR_Q), (qc - 1) & 1);
       }
     } else if (warp == kWarpV) {
@@ -578,16 +581,16 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         for (int j = 0; ok && j < it.nt; ++j) {
           win.advance(a, it.hk, j, lane);
           for (int hh = 0; hh < 2; ++hh) {
-            const int buf = hc & 1;
-            if (hc >= 2 && !warp_wait(BAR_SE + 2 + buf, (hc >> 1) - 1, kSitePfVFree)) break;
-            win.load(base + kOffStaged + (2 + buf) * kStaged, tm_v, bar(BAR_SF + 2 + buf), a, j, hh, lane);
+            const int buf = kBufs + hc % kBufs;
+            if (hc >= kBufs && !warp_wait(BAR_SE + buf, hc / kBufs - 1, kSitePfVFree)) break;
+            win.load(base + kOffStaged + buf * kStaged, tm_v, bar(BAR_SF + buf), a, j, hh, lane);
             ++hc;
           }
         }
       }
       if (!ok && lane == 0) raise_error(a.err, kErrTimeout | site);
       if (lane == 0)                               // (error path) as above
-        for (uint32_t x = hc > 2u ? hc - 2 : 0; x < hc; ++x) mbar_wait(bar(BAR_SF + 2 + (x & 1)), (x >> 1) & 1);
+        for (uint32_t x = hc > kBufs ? hc - kBufs : 0; x < hc; ++x) mbar_wait(bar(BAR_SF + kBufs + x % kBufs), (x / kBufs) & 1);
     } else if (warp == kWarpMma && lane == 0) {
       // ---------------------------------------------------------- MMA
       constexpr uint32_t idS = idesc_f16_f32(BM, BN, false);   // Q (K-major) x K (K-major)
@@ -700,7 +703,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
   } else {
     // ------------------------------------------------------------ widening: two warps K, two V
     const int type = (warp - kWarpWiden) >> 1, sub = warp & 1;
-    const uint32_t ring = base + (type ? kOffV : kOffK), staged = base + kOffStaged + type * 2 * kStaged;
+    const uint32_t ring = base + (type ? kOffV : kOffK), staged = base + kOffStaged + type * kBufs * kStaged;
     // this lane: 16 dims (chunk c) of rows r0, r0 + 4, ... of its warp's 32; 8 lanes read a row's 128 bytes.  The lanes of the
     // upper 64 dims store their second 16 bytes first, so that 8 lanes' stores touch every bank once.
     const int c = lane & 7, r0 = sub * 32 + (lane >> 3), half = c >> 2, lo = 2 * (c & 3);
@@ -751,8 +754,8 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
         const int left = it.keys - (it.j0 + j) * BN;   // rows from there on may hold anything: V's are zeroed, since 0 * NaN is not 0
 #pragma unroll 1
         for (int hh = 0; hh < 2; ++hh, ++hc) {
-          const int buf = hc & 1;
-          if (!warp_wait(BAR_SF + 2 * type + buf, hc >> 1, type ? kSitePfV : kSitePfK)) break;
+          const int buf = hc % kBufs;
+          if (!warp_wait(BAR_SF + kBufs * type + buf, hc / kBufs, type ? kSitePfV : kSitePfK)) break;
 #pragma unroll 1
           for (int k0 = 0; k0 < 8; k0 += kWidenRows) {
           uint4 x[kWidenRows];
@@ -763,7 +766,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
           }
           if (k0 + kWidenRows == 8) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(BAR_SE + 2 * type + buf));
+          if (lane == 0) mbar_arrive(bar(BAR_SE + kBufs * type + buf));
           }
 #pragma unroll
           for (int k = 0; k < kWidenRows; ++k) {
