@@ -39,15 +39,24 @@ using qstream::WideShape;
 
 constexpr int HD = kPrefixDim;
 constexpr int kMaxSms = 160;             // SMs that the records are sized for
-constexpr int kMaxRows = 64;             // query rows per key/value head that are streamed, 8 or 16 at a time
+// Query rows per key/value head that are streamed, 8 or 16 at a time; with more, a step goes to the plan and its chunks to pieces.
+// 4 and 40 sequences of 64 such rows behind 500 and 4000 keys, 32/8 heads, us: streamed 17, 32, 71, 195, as pieces 29, 36, 61,
+// 212; of 128 rows 19, 45, 106, 371 and 29, 36, 66, 132.
+constexpr int kMaxRows = 64;
 constexpr int kStepTokens = 4096;        // of a step without a plan kernel
-constexpr int kMinShareTiles = 3;        // shortest share of a warp
+// Tiles of a warp's shortest share: more warps load sooner, but leave more records.  4 rows of 1300 keys, 20 of 400 and 8 of
+// 2000, 32/8 heads, us: with 1 10.7, 14.5, 14.6; 3 11.7, 14.1, 14.6; 8 14.6, 15.6, 16.2.
+constexpr int kMinShareTiles = 3;
 // Tiles a warp, at most, of a step whose streams are a CTA's each, which needs no join kernel.  Steps of 1 to 4 tokens, us,
 // so and in shares: 32/8 heads, 12 warps, contexts of 64 5.1 .. 5.6 and 10.1 .. 10.9, of 512 7.9 .. 8.5 and 10.7 .. 11.5,
 // of 1024 (16 warps) 10.9 .. 11.4 and 11.1 .. 11.5; one key/value head, 8 warps, contexts of 512 11.4 and 13.2, of 1024 14.8
 // and 13.5.
 constexpr int kApartTiles = 4;
-constexpr double kSharingBytes = 1.9e8;  // reads that sharing has to be able to save, for the plan to be worth its time
+// Bytes that sharing has to be able to save for the plan, the pieces and the larger join to be worth their time, by the host's
+// bound on the contexts.  Chats of 32/8 heads with up to 512 keys of their own, us, with the plan and without: 32 behind 2000
+// shared ones (1.6e8 bytes) 32.6, 29.8; 64 behind 1000 (1.95e8) 35.0, 31.5; 48 behind 2000 (2.4e8) 34.7, 37.7; 64 behind 2000
+// (3.2e8) 37.1, 45.9.
+constexpr double kSharingBytes = 2.3e8;
 // What the plan's estimates go by, in microseconds and bytes: a KV tile for two row tiles and for one, which the widening of
 // either bounds alike (measured 2.0), and what an SM's streams read beside pieces.  3 chunks of 662 tokens behind 2048 keys with
 // 64 decode rows, and with 200, 32/8 heads, us: these 146, 236; tiles of 1.7 153, 315; streams of 2.4e4 153, 315; of 4.2e4 146,
@@ -445,7 +454,7 @@ cb_status encode_pools(const AttnArgs& a, int rows, CUtensorMap* tk, CUtensorMap
 // Sets of 8 query rows of a stream's units.
 int stream_sets(const AttnArgs& a) { return int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) <= 8 ? 1 : 2; }
 // Of a listed step's, whose sequences may have more rows than one unit: small units, of up to 8 rows, where one token's rows
-// fit them.
+// fit them.  600 rows at 2000 keys, 32 heads on 4 and on 2, us: units of 8 rows 152, 131, of 16 179, 116.
 int listed_sets(int group_heads) { return group_heads <= 8 ? 1 : 2; }
 int listed_warps(int sets) { return sets == 1 ? FewShape::kWarps : WideShape::kWarps; }
 

@@ -12,7 +12,12 @@
 //
 // cb_gather_kv_q8 reads tokens back: q * s, in bf16 or fp32.
 //
-// Both are bound by HBM.
+// What bounds them: a large read-back HBM, a third of it reads (24 sequences of 4096
+// keys, 24 heads: 231 us, 0.83 of the copy rate; 32-byte stores, more or fewer warps and
+// loads in flight change nothing).  An append is bound by its dependent steps: slots, page
+// and scale, rows, their maximum, stores.  2048 tokens of 32 heads take 21.9 us of 7.5 at
+// the copy rate, 2.5 of them the scan of the slots; warps wait for loads half of the time and
+// issue a third of it.  64 decode rows: 4.7 us in a graph, a launch.
 #include <algorithm>
 
 #include "device_common.cuh"

@@ -502,7 +502,8 @@ cb_status cb_shared_prefix_attention(const void* q, int32_t num_q_heads, const c
  *
  * Same arguments and result as cb_ragged_attention_gqa, with keys and values
  * number * scale; q and out are bf16.  K and V go to the tensor cores as they are,
- * exact; the scales multiply scores and weights in fp32.
+ * exact in f16; the scales multiply scores and weights in fp32, and the weights are
+ * rounded to f16 (by 2^-11 of each, or 2^-25 of the largest).
  *   cu_groups, prefix_lens, num_groups  as in cb_shared_prefix_attention, or NULL, NULL
  *                 and 0: nothing is shared.  The whole blocks of a prefix have to hold
  *                 the same numbers for every sequence of its group, scales among them;
