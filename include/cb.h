@@ -210,7 +210,8 @@ cb_status cb_compact_blocks(const cb_kv_cache* layers, int32_t num_layers, const
  * k and v are pools as in cb_kv_cache, of e4m3 numbers (1 byte each; four
  * significant bits, 2^-9 to 448).  k_scale and v_scale are device fp32
  * [num_blocks][num_heads]: the numbers of a block and head stand for
- * number * scale.  Caller-owned; pools 16-byte aligned.  Blocks need no
+ * number * scale.  Scales that the caller writes have to be positive and
+ * finite.  Caller-owned; pools 16-byte aligned.  Blocks need no
  * initialisation: a block's scale counts once its first slot has been written.
  * block_size is a power of two up to 1024, head_dim 64, 128 or 256; attention
  * needs block_size 16 to 128 and head_dim 128.
@@ -503,7 +504,9 @@ cb_status cb_shared_prefix_attention(const void* q, int32_t num_q_heads, const c
  * Same arguments and result as cb_ragged_attention_gqa, with keys and values
  * number * scale; q and out are bf16.  K and V go to the tensor cores as they are,
  * exact in f16; the scales multiply scores and weights in fp32, and the weights are
- * rounded to f16 (by 2^-11 of each, or 2^-25 of the largest).
+ * rounded to f16 (by 2^-11 of each, or 2^-25 of the largest).  Scores are fp32's:
+ * beyond 2^24 they are not told apart to whole numbers, and a row with scores beyond
+ * 2^28 may become NaN.
  *   cu_groups, prefix_lens, num_groups  as in cb_shared_prefix_attention, or NULL, NULL
  *                 and 0: nothing is shared.  The whole blocks of a prefix have to hold
  *                 the same numbers for every sequence of its group, scales among them;

@@ -257,6 +257,20 @@ def test_query_magnitudes(native_lib, q):
     st.check()
 
 
+@pytest.mark.parametrize("H,K", [(8, 2), (12, 4)])
+@pytest.mark.parametrize("q", [1, 3, 130])
+@pytest.mark.parametrize("far", [2.0 ** 16, 2.0 ** 40, math.inf])
+def test_enormous_scores(native_lib, H, K, q, far):
+    """Scores up to 2^20 are weighed like others; beyond fp32's reach, or infinite queries, they end, and leave other sequences'
+    rows alone."""
+    from continuous_batching_ragged_gb300 import api
+    st = Step([(q + 300, q), (q + 77, q), (900, 1)], H, K, 16, seed=63)
+    st.q[st.cu_l[1]:st.cu_l[2], ::2] *= far
+    st.run()
+    api.cb_check_device_errors()
+    st.check([0, 1, 2] if far == 2.0 ** 16 else [0, 2])
+
+
 @pytest.mark.parametrize("q", [1, 130])
 def test_not_finite_keys_behind_the_mask(native_lib, q):
     """A NaN among the keys of a chunk's last token leaves the rows before it alone."""
