@@ -57,8 +57,8 @@ constexpr int kApartTiles = 4;
 // shared ones (1.6e8 bytes) 32.6, 29.8; 64 behind 1000 (1.95e8) 35.0, 31.5; 48 behind 2000 (2.4e8) 34.7, 37.7; 64 behind 2000
 // (3.2e8) 37.1, 45.9.
 constexpr double kSharingBytes = 2.3e8;
-// What the plan's estimates go by, in microseconds and bytes: a KV tile for two row tiles and for one, which the widening of
-// either bounds alike (measured 2.0), and what an SM's streams read beside pieces.  3 chunks of 662 tokens behind 2048 keys with
+// What the plan's estimates go by, in microseconds and bytes: a KV tile for two row tiles and for one (2.2, ends
+// included: either is widened alike), and what an SM's streams read beside pieces.  3 chunks of 662 tokens behind 2048 keys with
 // 64 decode rows, and with 200, 32/8 heads, us: these 146, 236; tiles of 1.7 153, 315; streams of 2.4e4 153, 315; of 4.2e4 146,
 // 239.
 constexpr float kTileUsTwo = 2.0f, kTileUsOne = 2.0f, kStreamBytesPerUsPerSm = 3.6e4f;

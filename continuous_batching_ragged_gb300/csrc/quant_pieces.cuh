@@ -16,16 +16,17 @@
 // Warps 0 to 7 are the softmax of row tiles 0 and 1, 8 the K loader, 9 the MMA thread's,
 // 10 the V loader, 12 and 13 widen K, 14 and 15 V; all with 128 registers.
 //
-// What bounds it: a KV tile for two row tiles takes 2.0 us, where its four matrix
-// products of 128^3 would take 1.3 at the measured bf16 rate.  A row tile's softmax
-// (1.3 us, instructions and their latency) stands between its two products, the other
-// tile's fill half of that, and the widening takes issue slots and two 8 KB buffers'
-// latency from both: tensor pipe 46 %, issue 51 %, DRAM 6 %.  2048 tokens of 32 heads
-// behind 30,720 keys: 1005 us, 1060 TFLOP/s.  Measured against this, us: the maxima
+// What bounds it: a KV tile for two row tiles takes 2.4 us, the pieces' ends included,
+// where its four matrix products of 128^3 would take 1.3 at the measured bf16 rate.  A
+// row tile's softmax, instructions that wait for one another, stands between its two
+// products; the other tile's products fill a part of that, and the widening takes issue
+// slots from the softmax.  Tensor pipe 46 %, issue 51 %, DRAM 6 %.  2048 tokens of 32
+// heads behind 30,720 keys: 1005 us, 1060 TFLOP/s.  Measured against this, us: the maxima
 // found first and half of the scores held, 1343; softmax warps with more registers from
 // setmaxnreg, 1579, or 16 of them, 1470; the loop over 32 keys unrolled, 1358, the
 // roles' code being more than the instruction caches hold; P V of the first 64 keys
-// started before the last 64 have weights, 1049.
+// started before the last 64 have weights, 1049; three staging buffers, with V's ring in
+// three halves, 1064.
 #pragma once
 
 #include <cuda.h>
@@ -770,30 +771,29 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
           if (!warp_wait(BAR_SF + kBufs * type + buf, hc / kBufs, type ? kSitePfV : kSitePfK)) break;
 #pragma unroll 1
           for (int k0 = 0; k0 < 8; k0 += kWidenRows) {
-          uint4 x[kWidenRows];
+            uint4 x[kWidenRows];
 #pragma unroll
-          for (int k = 0; k < kWidenRows; ++k) {
-            const int r = r0 + 4 * (k0 + k);
-            x[k] = lds16(staged + buf * kStaged + r * HD + ((c ^ (r & 7)) << 4));
-          }
-          if (k0 + kWidenRows == 8) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(BAR_SE + kBufs * type + buf));
-          }
+            for (int k = 0; k < kWidenRows; ++k) {
+              const int r = r0 + 4 * (k0 + k);
+              x[k] = lds16(staged + buf * kStaged + r * HD + ((c ^ (r & 7)) << 4));
+            }
+            if (k0 + kWidenRows == 8) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(BAR_SE + kBufs * type + buf));
+            }
 #pragma unroll
-          for (int k = 0; k < kWidenRows; ++k) {
-            const int r = hh * HN + r0 + 4 * (k0 + k);
-            if (type && r >= left) x[k] = make_uint4(0, 0, 0, 0);
-            const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            uint32_t y[8];
+            for (int k = 0; k < kWidenRows; ++k) {
+              const int r = hh * HN + r0 + 4 * (k0 + k);
+              if (type && r >= left) x[k] = make_uint4(0, 0, 0, 0);
+              const uint32_t in[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+              uint32_t y[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[2 * e] = e4m3x2_to_f16x2(in[e]), y[2 * e + 1] = e4m3x2_hi_to_f16x2(in[e]);
-            const uint32_t row = ring + st * kTile + half * kHalf + r * 128, at0 = row + ((lo ^ (r & 7)) << 4),
-                           at1 = row + (((lo + 1) ^ (r & 7)) << 4);
-            const bool h = half;
-            sts16(h ? at1 : at0, h ? y[4] : y[0], h ? y[5] : y[1], h ? y[6] : y[2], h ? y[7] : y[3]);
-            sts16(h ? at0 : at1, h ? y[0] : y[4], h ? y[1] : y[5], h ? y[2] : y[6], h ? y[3] : y[7]);
-          }
+              for (int e = 0; e < 4; ++e) y[2 * e] = e4m3x2_to_f16x2(in[e]), y[2 * e + 1] = e4m3x2_hi_to_f16x2(in[e]);
+              const uint32_t row = ring + st * kTile + half * kHalf + r * 128, at0 = row + ((lo ^ (r & 7)) << 4),
+                             at1 = row + (((lo + 1) ^ (r & 7)) << 4);
+              sts16(half ? at1 : at0, half ? y[4] : y[0], half ? y[5] : y[1], half ? y[6] : y[2], half ? y[7] : y[3]);
+              sts16(half ? at0 : at1, half ? y[0] : y[4], half ? y[1] : y[5], half ? y[2] : y[6], half ? y[3] : y[7]);
+            }
           }
           fence_proxy_async_smem();                // for the tensor core
           __syncwarp();
