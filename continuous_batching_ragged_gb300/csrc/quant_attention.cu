@@ -47,11 +47,11 @@ constexpr int kStepTokens = 4096;        // of a step without a plan kernel
 // Tiles of a warp's shortest share: more warps load sooner, but leave more records.  4 rows of 1300 keys, 20 of 400 and 8 of
 // 2000, 32/8 heads, us: with 1 10.7, 14.5, 14.6; 3 11.7, 14.1, 14.6; 8 14.6, 15.6, 16.2.
 constexpr int kMinShareTiles = 3;
-// Tiles a warp, at most, of a step whose streams are a CTA's each, which needs no join kernel.  Steps of 1 to 4 tokens, us,
-// so and in shares: 32/8 heads, 12 warps, contexts of 64 5.1 .. 5.6 and 10.1 .. 10.9, of 512 7.9 .. 8.5 and 10.7 .. 11.5,
-// of 1024 (16 warps) 10.9 .. 11.4 and 11.1 .. 11.5; one key/value head, 8 warps, contexts of 512 11.4 and 13.2, of 1024 14.8
-// and 13.5.
-constexpr int kApartTiles = 4;
+// Tiles a warp, at most, of a step whose streams are a CTA's each, which needs no join kernel.  1, 4 and 16 tokens of 32/8 heads,
+// 12 warps, us, so and in shares: contexts of 512 7.3, 7.8, 8.0 and 10.7, 11.4, 12.4; of 1280 (6.7 tiles) 10.7, 11.1, 12.3 and
+// 11.0, 11.8, 14.7; of 1536 11.6, 12.0, 13.9 and 9.8, 11.9, 16.2; 4 of 32 heads on one, 8 warps: of 768 (6 tiles) 12.1 and 13.7,
+// of 1024 13.6 and 13.8, of 1280 15.3 and 14.1.
+constexpr int kApartTiles = 7;
 // Bytes that sharing has to be able to save for the plan, the pieces and the larger join to be worth their time, by the host's
 // bound on the contexts.  Chats of 32/8 heads with up to 512 keys of their own, us, with the plan and without: 32 behind 2000
 // shared ones (1.6e8 bytes) 32.6, 29.8; 64 behind 1000 (1.95e8) 35.0, 31.5; 48 behind 2000 (2.4e8) 34.7, 37.7; 64 behind 2000
@@ -68,7 +68,6 @@ struct StepWork {
   const int32_t* cu_groups;              // null: none
   const int32_t* prefix_lens;
   int32_t num_groups;
-  int32_t share_tiles;                   // least tiles of a share; 0: a CTA to a stream, which joins its warps' parts itself
   int32_t* header;                       // [0] tiles of a share
   int4* token_info;                      // [num_tokens] (first tile of its sequence's streams, tiles of each, token of the
                                          // sequence, 1: there is something to join)
@@ -130,7 +129,8 @@ __device__ __forceinline__ void init_bars(uint32_t bars) {
   fence_mbar_init();
 }
 
-template <class Sh>
+// APART: a CTA to a stream, whose warps' parts it joins itself; else every warp of the grid takes its share of all tiles.
+template <class Sh, bool APART>
 __global__ void __launch_bounds__(Sh::kThreads, 1)
     q8_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ AttnArgs a, const __grid_constant__ StepWork w) {
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(Sh::kThreads, 1)
   if (writer && ((bad && tid == 0) || (tid < S && !ok))) raise_error(a.err, kErrInvalid);
   int per, begin = 0, limit = all_tiles, k = id;   // tiles of a share; the tiles that are shared; the warp's share of them
   RangeSeq own = {};                               // the sequence of the CTA's one stream
-  if (w.share_tiles > 0) {
-    per = max(w.share_tiles, (all_tiles - 1) / (int(gridDim.x) * kWarps) + 1);
+  if (!APART) {
+    per = max(kMinShareTiles, (all_tiles - 1) / (int(gridDim.x) * kWarps) + 1);
     if (writer) {
       if (tiles > 0)
         for (int t = 0; t < q_len; ++t) w.token_info[c0 + t] = make_int4(off, tiles, t, 1);
@@ -222,14 +222,13 @@ __global__ void __launch_bounds__(Sh::kThreads, 1)
   qstream::run_warp<Sh>(&tm_k, &tm_v, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
                         reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * Sh::kStages),
                         reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
-  if (w.share_tiles > 0 || own.tiles <= 1) return;
+  if (!APART || own.tiles <= 1) return;
   __syncthreads();                                 // the warps' records are written
   const int x = int(blockIdx.x) - own.stream0, hk = x % Hkv, row0 = x / Hkv * Sh::kRows, parts = (own.tiles - 1) / per + 1;
   for (int r = warp; r < min(Sh::kRows, own.q_len * G - row0); r += kWarps) {
     Joined j{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
-    for (int k0 = 0; k0 < parts; k0 += kJoinFlight)
-      join_parts<kJoinFlight>(j, w.recs, w.rec_ml, k0, parts, lane,
-                              [&](int part) { return size_t(2 * (part * int(gridDim.x) + int(blockIdx.x))) * Sh::kRows + r; });
+    join_parts<kWarps>(j, w.recs, w.rec_ml, 0, parts, lane,
+                       [&](int part) { return size_t(2 * (part * int(gridDim.x) + int(blockIdx.x))) * Sh::kRows + r; });
     write_row(a, size_t(own.tok0 + (row0 + r) / G) * H + hk * G + (row0 + r) % G, j, lane);
   }
 }
@@ -424,9 +423,10 @@ cb_status allow_shared_memory() {
   const auto allow = [&e](const void* kernel, uint32_t bytes) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
   };
-  allow(reinterpret_cast<const void*>(q8_step_kernel<SharesShape>), SharesShape::kSmem);
-  allow(reinterpret_cast<const void*>(q8_step_kernel<FewShape>), FewShape::kSmem);
-  allow(reinterpret_cast<const void*>(q8_step_kernel<WideShape>), WideShape::kSmem);
+  allow(reinterpret_cast<const void*>(q8_step_kernel<SharesShape, false>), SharesShape::kSmem);
+  allow(reinterpret_cast<const void*>(q8_step_kernel<FewShape, true>), FewShape::kSmem);
+  allow(reinterpret_cast<const void*>(q8_step_kernel<WideShape, false>), WideShape::kSmem);
+  allow(reinterpret_cast<const void*>(q8_step_kernel<WideShape, true>), WideShape::kSmem);
   allow(reinterpret_cast<const void*>(q8_streams_kernel<FewShape>), FewShape::kSmem);
   allow(reinterpret_cast<const void*>(q8_streams_kernel<WideShape>), WideShape::kSmem);
   allow(reinterpret_cast<const void*>(q8_pieces_kernel), qpieces::kSmemBytes);
@@ -485,7 +485,6 @@ cb_status run_step(const AttnArgs& a, const int32_t* cu_groups, const int32_t* p
                           ((int64_t(a.max_q_len) * (a.num_heads / a.num_kv_heads) + 8 * sets - 1) / (8 * sets));
   const bool apart = streams <= sms && num_groups <= (sets == 1 ? FewShape::kThreads : WideShape::kThreads) &&
                      a.max_context_len <= kApartTiles * qstream::kTileKeys * listed_warps(sets);
-  w.share_tiles = apart ? 0 : kMinShareTiles;
   char* p = static_cast<char*>(workspace);
   w.header = reinterpret_cast<int32_t*>(p);
   w.token_info = reinterpret_cast<int4*>(p + 256);
@@ -497,14 +496,14 @@ cb_status run_step(const AttnArgs& a, const int32_t* cu_groups, const int32_t* p
   if (st != CB_OK) return st;
   cudaError_t e;
   if (sets == 1 && !apart)
-    e = launch_kernel(q8_step_kernel<SharesShape>, dim3(unsigned(sms)), dim3(SharesShape::kThreads), SharesShape::kSmem, stream, true,
-                      tk, tv, a, w);
-  else if (sets == 1)
-    e = launch_kernel(q8_step_kernel<FewShape>, dim3(unsigned(streams)), dim3(FewShape::kThreads), FewShape::kSmem, stream, true, tk,
-                      tv, a, w);
-  else
-    e = launch_kernel(q8_step_kernel<WideShape>, dim3(unsigned(apart ? streams : sms)), dim3(WideShape::kThreads), WideShape::kSmem,
+    e = launch_kernel(q8_step_kernel<SharesShape, false>, dim3(unsigned(sms)), dim3(SharesShape::kThreads), SharesShape::kSmem,
                       stream, true, tk, tv, a, w);
+  else if (sets == 1)
+    e = launch_kernel(q8_step_kernel<FewShape, true>, dim3(unsigned(streams)), dim3(FewShape::kThreads), FewShape::kSmem, stream,
+                      true, tk, tv, a, w);
+  else
+    e = launch_kernel(apart ? q8_step_kernel<WideShape, true> : q8_step_kernel<WideShape, false>,
+                      dim3(unsigned(apart ? streams : sms)), dim3(WideShape::kThreads), WideShape::kSmem, stream, true, tk, tv, a, w);
   if (e != cudaSuccess) return cuda_fail(e, "8-bit attention: launch");
   if (apart) return CB_OK;
   const int64_t rows = int64_t(a.num_tokens) * a.num_heads;

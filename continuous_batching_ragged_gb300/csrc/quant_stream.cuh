@@ -24,8 +24,8 @@
 //     maximum M of score + log2(vs); the output's weights 2^(s - M) vs are at most
 //     2^8 (stale maxima are kept as long as that holds), while the sum, in fp32, stays
 //     that of 2^(s - m).
-// Measured: 256 rows of 32 heads over 4096 keys 727 us, 0.98 of the copy rate; 201 rows,
-// 32/8 heads, 155 us, 0.91; 140 rows of 32 heads on one 45 us, of which 12 are its bytes'
+// Measured: 256 rows of 32 heads over 4096 keys 711 us, the copy rate; 201 rows, 32/8
+// heads, 152 us, 0.93; 140 rows of 32 heads on one 45 us, of which 12 are its bytes'
 // and 17 a step's least time with its join: 8 warps an SM, and of a tile's instructions
 // each waits for the last (issue 38 %, DRAM 26 %).
 #pragma once
@@ -51,7 +51,7 @@ constexpr int kBarArrivals = 3;                        // of a stage: the copies
 // Warps of a CTA, and 192 KB of tiles in flight.  Two tiles an iteration: more independent work between one matrix step and
 // the next, and half the barriers' and maxima's part of it (256 rows of 32 heads at 4096 keys: 777 us one at a time, 727 so).
 // 16 warps take 128 registers each, which hides most latency where streams are long and HBM bounds them (727 us; 12 warps 768);
-// 12 warps start and end sooner (4 rows at 512 keys 8.7 us and 9.5, 64 rows behind a shared prompt 37.3 and 39.3).  With 16 rows
+// 12 warps start and end sooner (4 rows at 512 keys 8.7 us and, with 16, 9.5, 64 rows behind a shared prompt 37.3 and 39.3).  With 16 rows
 // a unit 8 warps of 231 registers (140 rows of 32 heads on one: 44.9 us; 12 warps, which spill: 53.4).
 template <int NT, int WARPS>
 struct Shape {
