@@ -233,22 +233,21 @@ def cb_gather_kv_q8(cache: QuantKVCache, block_tables: torch.Tensor, cu_keys: to
     """cb_gather_kv_q8: sequence s's cached tokens from starts[s] (0 where not given) on
     to rows cu_keys[s] .. cu_keys[s+1]-1 of k_out and v_out, [rows, H, A] bf16 or fp32
     (either may be None)."""
-    for name, t in (("block_tables", block_tables), ("cu_keys", cu_keys), ("starts", starts)):
-        if t is not None and t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
+    if not block_tables.dtype is cu_keys.dtype is torch.int32 or (starts is not None and starts.dtype is not torch.int32):
+        raise ValueError("block_tables, cu_keys and starts must be int32")
     S = cu_keys.numel() - 1
     if block_tables.dim() != 2 or block_tables.shape[0] != S or (starts is not None and starts.numel() != S):
         raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq], cu_keys [num_seqs + 1], starts [num_seqs]")
     c = cache.c_struct()
-    outs = [t for t in (k_out, v_out) if t is not None]
-    if not outs:
+    out = v_out if k_out is None else k_out
+    if out is None:
         return
-    for t in outs:
-        if t.dtype not in _DTYPES or t.dtype != outs[0].dtype or t.shape != (outs[0].shape[0], c.num_heads, c.head_dim):
-            raise ValueError("k_out and v_out must be [rows, H, A] of one dtype, bf16 or fp32")
+    shape, dtype = out.shape, _DTYPES.get(out.dtype)
+    if dtype is None or out.dim() != 3 or shape[1] != c.num_heads or shape[2] != c.head_dim or \
+            (v_out is not None and out is not v_out and (v_out.dtype is not out.dtype or v_out.shape != shape)):
+        raise ValueError("k_out and v_out must be [rows, H, A] of one dtype, bf16 or fp32")
     check(native.lib().cb_gather_kv_q8(c, _ptr(block_tables), _ptr(cu_keys), _ptr(starts), S, block_tables.shape[1],
-                                       outs[0].shape[0], _DTYPES[outs[0].dtype], _ptr(k_out), _ptr(v_out),
-                                       _stream_handle(stream)), "cb_gather_kv_q8")
+                                       shape[0], dtype, _ptr(k_out), _ptr(v_out), _stream_handle(stream)), "cb_gather_kv_q8")
 
 
 def _stack(layers) -> KVCacheStack:
@@ -423,26 +422,30 @@ def cb_ragged_attention_q8(q: torch.Tensor, cache: QuantKVCache, cu_seqlens_q: t
                            stream=None) -> torch.Tensor:
     """cb_ragged_attention_q8: attention over a cache in 8 bits; q, out [T, heads, A]
     bf16.  With cu_groups and prefix_lens, as in cb_shared_prefix_attention."""
-    for name, t in (("cu_seqlens_q", cu_seqlens_q), ("context_lens", context_lens), ("block_tables", block_tables),
-                    ("cu_groups", cu_groups), ("prefix_lens", prefix_lens)):
-        if t is not None and t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
+    if not cu_seqlens_q.dtype is context_lens.dtype is block_tables.dtype is torch.int32:
+        raise ValueError("cu_seqlens_q, context_lens and block_tables must be int32")
     c = cache.c_struct()
-    if q.dim() != 3 or q.shape[2] != c.head_dim:
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != c.head_dim:
         raise ValueError("q must be [num_tokens, heads, head_dim] of the cache's head_dim")
-    (S,), (T, heads, _) = context_lens.shape, q.shape
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or cu_seqlens_q.shape[0] != S + 1:
-        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq] and cu_seqlens_q [num_seqs + 1]")
+    T, heads, _ = shape
+    S = context_lens.numel()
+    if context_lens.dim() != 1 or block_tables.dim() != 2 or block_tables.shape[0] != S or cu_seqlens_q.numel() != S + 1:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq], context_lens [num_seqs] and cu_seqlens_q [num_seqs + 1]")
     num_groups = 0
     if cu_groups is not None or prefix_lens is not None:
         if cu_groups is None or prefix_lens is None or cu_groups.numel() != prefix_lens.numel() + 1:
             raise ValueError("cu_groups must be [num_groups + 1], and prefix_lens [num_groups] given with it")
+        if not cu_groups.dtype is prefix_lens.dtype is torch.int32:
+            raise ValueError("cu_groups and prefix_lens must be int32")
         num_groups = prefix_lens.numel()
-    if out.shape != q.shape or not out.dtype == q.dtype == torch.bfloat16:
+    if out.shape != shape or not out.dtype is q.dtype is torch.bfloat16:
         raise ValueError("q and out must have one shape and be bf16")
     ws_ptr, ws_bytes = None, 0
-    if workspace is not None and workspace.numel():
-        ws_ptr, ws_bytes = _ptr(workspace), workspace.numel() * workspace.element_size()
+    if workspace is not None:
+        ws_bytes = workspace.nbytes
+        if ws_bytes:
+            ws_ptr = _ptr(workspace)
     check(native.lib().cb_ragged_attention_q8(
         _ptr(q), heads, c, _ptr(cu_seqlens_q), _ptr(context_lens), _ptr(block_tables), _ptr(cu_groups), _ptr(prefix_lens),
         num_groups, S, T, block_tables.shape[1], max_q_len, max_context_len, scale, _ptr(out), ws_ptr, ws_bytes,
