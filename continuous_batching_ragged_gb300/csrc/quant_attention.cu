@@ -302,7 +302,8 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
 // Joins the rows that lie in several shares.  WIDE: a CTA to a row, each warp with its part of the records, where rows are
-// few and may have very many; else a warp to a row.
+// few (4 an SM at most) and may have very many; else a warp to a row.  A step with one and the other, 32/8 heads, us: 1 row of
+// 8000 keys 15.6, 34.8; of 60,000 37, 91; 16 of 4000 25.5, 32.6; 19 of 1500 17.3, 21.4.
 template <bool WIDE>
 __global__ void __launch_bounds__(kJoinThreads) q8_join_kernel(const AttnArgs a, const StepWork w, int row_tile) {
   __shared__ float4 part_acc[WIDE ? kJoinWarps : 1][32];
