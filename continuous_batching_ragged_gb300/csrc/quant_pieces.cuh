@@ -68,7 +68,8 @@ constexpr int kItemSlots = 2;
 constexpr int kItemReaders = 1 + 1 + 8 + 4;      // V loader, MMA, softmax and widening warps
 enum : int {
   BAR_Q = 0,                   // Q tiles landed
-  BAR_QE = 1,                  // every S MMA of the piece has read Q, every softmax warp its rows' factors
+  BAR_QE = 1,                  // every S MMA of the piece has read Q, every softmax warp its rows' factors; a warp without rows
+                               // arrives behind the piece's QF, or it could arrive for the next piece before this one's others
   BAR_QF = 2,                  // Q tiles in f16, their rows' factors written
   BAR_S = 3,                   // + slot: S ready
   BAR_P = BAR_S + 2,           // + slot: P written (128 arrivals)
@@ -283,6 +284,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
     const uint32_t lane_base = tmem + (uint32_t(wq * 32) << 16) + 256 * t;
     uint32_t cnt = 0, ocnt = 0;                    // S/P phases and O phases of this slot consumed
     uint32_t tiles = 0;                            // of the pieces before
+    uint32_t qn = 0;                               // pieces before that have tiles, and so Q
     for (int n = 0; ok; ++n) {
       if (!item_landed(n)) break;
       // what the piece's end needs of it is read there: the slot is given back after that
@@ -299,7 +301,11 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
       const int step = alt ? 2 : 1;
       const int steps = alt ? (nt - t + 1) / 2 : nt;
       const bool work = wq * 32 < rows;            // some row of this warp is real
-      if (nt > 0 && (steps == 0 || !work) && lane == 0) mbar_arrive(bar(BAR_QE));   // no factor to read
+      if (nt > 0 && (steps == 0 || !work)) {       // no factor to read
+        if (!warp_wait(BAR_QF, qn, kSitePfQ)) break;
+        if (lane == 0) mbar_arrive(bar(BAR_QE));
+      }
+      qn += nt > 0;
       if (rows <= 0) {                             // no rows in the second tile
         tiles += nt;
         item_read(n);

@@ -476,3 +476,48 @@ def test_serving_steps(native_lib, H, K):
             st.cu_l, st.ctx_l, st.q_l, st.tables_l = cu, ctx_l, new, tables_l
             st.check([s])
         held = ctx_l
+
+
+def run_repeated(*args, sequences=None, **kw):
+    """Checked, and the same bits three times over: what one piece of a CTA leaves in shared memory is not the next one's."""
+    st = run_checked(*args, sequences=sequences, **kw)
+    first = st.out.clone()
+    for _ in range(3):
+        st.out.fill_(float("nan"))
+        st.run()
+        torch.cuda.synchronize()
+        assert torch.equal(first, st.out)
+    return st
+
+
+# One pair of row tiles and one token: of such a chunk's two pieces one has both row tiles, one exactly one; and a prompt of one KV
+# tile whose rows are pieces and fit one row tile (no such prompt with 128 heads on one).
+TILES = [(8, 8, 16), (8, 2, 16), (32, 8, 16), (12, 4, 32), (16, 2, 64), (32, 1, 16), (128, 1, 16)]
+
+
+def tile_sizes(H, K):
+    G = H // K
+    return 2 * (128 // G) + 1, (min(128 // G, 64 // G + 6) if G < 64 else 2)
+
+
+@pytest.mark.parametrize("H,K,B", TILES)
+@pytest.mark.parametrize("before", [0, 40, 600])
+@pytest.mark.parametrize("kind", ["chunks", "prompts", "mixed"])
+def test_pieces_in_turn(native_lib, H, K, B, before, kind):
+    """More pieces than SMs, each CTA with several in turn: pieces whose second row tile is empty, and prompts of one KV tile, whose
+    second slot is; a piece's queries stay until its last scores have read them."""
+    odd, short = tile_sizes(H, K)
+    n = -(-460 // (2 * K))
+    chunk, prompt = (before + odd, odd), (short + min(before, 20), short)
+    seqs = {"chunks": [chunk] * n, "prompts": [prompt] * (2 * n), "mixed": [chunk, prompt, (before + 3 * odd + 1, odd - 1), prompt, prompt] * (n // 2)}[kind]
+    run_repeated(seqs, H, K, B, seed=70 + H + before, sequences=range(0, len(seqs), max(1, len(seqs) // 40)))
+
+
+@pytest.mark.parametrize("H,K,B", TILES)
+def test_group_pieces_in_turn(native_lib, H, K, B):
+    """The same for groups whose members' rows are one pair of row tiles and one token, behind prefixes of several KV tiles."""
+    odd, _ = tile_sizes(H, K)
+    n = -(-320 // (2 * K))
+    groups = [(640, [(1 + (7 * i + g) % 40, 1) for i in range(odd)]) for g in range(n)]
+    S = n * odd
+    run_repeated(groups, H, K, B, groups=True, seed=71 + H, sequences=range(0, S, max(1, S // 60)))
