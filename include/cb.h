@@ -245,9 +245,9 @@ typedef struct {
  *   slot_mapping  device int64 [num_tokens], as in cb_append_kv: a negative slot skips
  *                 the token, one past the pool sets CB_ERR_BOUNDS and skips it.
  *                 The tokens of one block follow one another, at rising slots; skipped
- *                 ones may lie between.  (A block whose slots do not rise is left out
- *                 and sets CB_ERR_INVALID; a block that comes again after tokens of
- *                 another one gets wrong numbers.)
+ *                 ones may lie between.  (A block whose slots do not rise, or that
+ *                 comes again after tokens of another one, is left out and sets
+ *                 CB_ERR_INVALID.)
  *   dims          NULL, or the device sizes of a planned step: the token count is
  *                 dims[1] and num_tokens its capacity, as in cb_append_kv_dims.
  * At most 65,536 tokens a call; head_dim 256 needs bf16 (CB_ERR_UNSUPPORTED otherwise).

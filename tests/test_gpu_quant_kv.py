@@ -428,3 +428,50 @@ def test_captured_append_with_a_count(native_lib):
         api.cb_check_device_errors()
         p.plain(k[:n], v[:n], mine)
         p.check()
+
+
+@pytest.mark.parametrize("blocks,K,B,A", [(12, 2, 16, 128), (12, 1, 64, 64), (70_000, 1, 1, 64), (66_000, 2, 2, 64)])
+def test_pages_that_come_again(native_lib, blocks, K, B, A):
+    """A page whose tokens do not follow one another is left as it was and reported, whether at other slots, at the same one or as
+    decode rows; the pages between are written, and pages of a large pool that only look alike to the check."""
+    from continuous_batching_ragged_gb300 import api, native
+    p = Pool(blocks, K, B, A, seed=30)
+    far = 65_536 if blocks > 65_536 else 0         # pages 3 and 3 + far, and so on
+    run = list(range(min(B, 3)))
+    parts = [(3, run, False), (5, [0], True), (3 + far // 2, [B - 1], True), (3, [B - 1], False), (7, run, True), (4, [0], False),
+             (6, run, True), (4, [0], False), (4, [0], False), (8, [B - 1], True)]
+    if far:
+        parts += [(7 + far, [0], True), (9 + far, [0], True), (9, [B - 1], True), (4 + far, [0], True), (10 + far, [0], False), (10, [0], True),
+                  (10 + far, [B - 1], False)]
+    else:
+        parts[2] = (2, [B - 1], True)
+    slots = [page * B + o for page, offs, _ in parts for o in offs]
+    good = [page * B + o if ok else -1 for page, offs, ok in parts for o in offs]
+    k, v = (rows(len(slots), K, A, "bf16", s) for s in (31, 32))
+    p.append(k, v, slots)
+    with pytest.raises(native.CBError) as e:
+        api.cb_check_device_errors()
+    assert e.value.status == native.CB_ERR_INVALID
+    p.plain(k, v, good)
+    p.check()
+    p.append(k, v, good)
+    api.cb_check_device_errors()
+    p.plain(k, v, good)
+    p.check()
+
+
+def test_many_pages_that_come_again(native_lib):
+    """More runs than a CTA has threads, half of them of pages that another run is of."""
+    from continuous_batching_ragged_gb300 import api, native
+    p = Pool(1500, 1, 16, 64, seed=33)
+    perm = torch.randperm(1500, generator=torch.Generator().manual_seed(34)).tolist()
+    once, twice = perm[:600], perm[600:900]
+    slots = [x * 16 for i in range(600) for x in [once[i]] + [twice[i // 2]] * (i % 2)] + [x * 16 + 1 for x in twice]
+    k, v = (rows(len(slots), 1, 64, "f32", s) for s in (35, 36))
+    p.append(k, v, slots)
+    with pytest.raises(native.CBError) as e:
+        api.cb_check_device_errors()
+    assert e.value.status == native.CB_ERR_INVALID
+    keep = set(once)
+    p.plain(k, v, [s if s // 16 in keep else -1 for s in slots])
+    p.check()
