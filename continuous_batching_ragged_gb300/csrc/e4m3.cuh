@@ -38,4 +38,18 @@ __device__ __forceinline__ uint32_t float_to_e4m3x4(float a, float b, float c, f
   return r;
 }
 
+// y, off from an exact value by `rest` (its sign counts) and by less than one step: the value cut off towards zero, its last bit
+// set where bits were cut off.  Rounded to fewer bits after that, it is rounded once.  NaN stays.
+__device__ __forceinline__ float to_odd(float y, float rest) {
+  uint32_t u = __float_as_uint(y);
+  if (!(rest == 0.f)) u = (u - ((u ^ __float_as_uint(rest)) >> 31)) | 1u;
+  return __uint_as_float(u);
+}
+// Of numbers with up to 4 and 24 bits, so, if the product is 2^-100 or more.
+__device__ __forceinline__ float product_to_odd(float x, float s) {
+  const float y = x * s;
+  return to_odd(y, fmaf(x, s, -y));
+}
+__device__ __forceinline__ bool is_power_of_two(float x) { return (__float_as_uint(x) & 0x7fffffu) == 0; }   // of positive ones that are not denormal
+
 }  // namespace cb

@@ -447,17 +447,29 @@ struct GatherArgs {
   unsigned* err;
 };
 
+// f * s cut off to fp32 as to_odd does, whatever s.
+__device__ __forceinline__ float scaled_to_odd(float f, float s) {
+  if (s >= 0x1p-90f) return cb::product_to_odd(f, s);
+  const double p = double(f) * double(s);          // exact
+  const float y = __double2float_rz(p);
+  return double(y) == p ? y : __uint_as_float(__float_as_uint(y) | 1u);
+}
+// Rounded once: four bits times a power of two are exact in fp32; times another scale they have up to 28 bits.
 __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint4& x, float s) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t r[8];
+  auto row = [&](auto times) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float f[4];
-    cb::e4m3x4_to_float(w[i], f);
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0] * s, f[1] * s), hi = __floats2bfloat162_rn(f[2] * s, f[3] * s);
-    r[2 * i] = *reinterpret_cast<const uint32_t*>(&lo);
-    r[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hi);
-  }
+    for (int i = 0; i < 4; ++i) {
+      float f[4];
+      cb::e4m3x4_to_float(w[i], f);
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(times(f[0]), times(f[1])), hi = __floats2bfloat162_rn(times(f[2]), times(f[3]));
+      r[2 * i] = *reinterpret_cast<const uint32_t*>(&lo);
+      r[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+    }
+  };
+  if (cb::is_power_of_two(s)) row([&](float f) { return f * s; });
+  else row([&](float f) { return scaled_to_odd(f, s); });
   reinterpret_cast<uint4*>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
   reinterpret_cast<uint4*>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }

@@ -475,3 +475,43 @@ def test_many_pages_that_come_again(native_lib):
     keep = set(once)
     p.plain(k, v, [s if s // 16 in keep else -1 for s in slots])
     p.check()
+
+
+def bf16_once(x):
+    """64-bit numbers in bf16's normal range to the nearest bf16 ones, ties to even (a conversion by way of fp32 rounds twice)."""
+    m, e = torch.frexp(x)
+    return torch.ldexp(torch.round(m * 256), e - 8)
+
+
+def tie_scales(f, n, top, seed):
+    """n fp32 scales, 2^top and more, whose product with f rounds in fp32 to a number halfway between two bf16 ones without being it."""
+    g = torch.Generator().manual_seed(seed)
+    tie = torch.randint(128, 256, (40 * n,), generator=g) * 2 + 1
+    s = (tie.double() * 2.0 ** (top - 8) / f).float()
+    p = s.double() * f
+    near = p.float().double()
+    half = torch.frexp(near)[0] * 512
+    s = s[(half == torch.round(half)) & (half % 2 == 1) & (near != p)]
+    assert s.numel() >= n
+    return s[:n]
+
+
+@pytest.mark.parametrize("top", [0, -60, -95, -115, 100])
+def test_gather_rounds_once(native_lib, top):
+    """Products that fp32 would first round to a tie of bf16, and the scales' own neighbours; whatever the scales' size."""
+    from continuous_batching_ragged_gb300 import api
+    K, B, A = 2, 16, 128
+    for f in (1.125, 1.375, 1.625, 1.75, 1.875):
+        s = tie_scales(f, 6, top, 40)
+        s = torch.cat([s, s.nextafter(torch.tensor(0.0)), s.nextafter(torch.tensor(math.inf))])
+        p = Pool(18, K, B, A, seed=41)
+        x = torch.tensor([f, -f, 8 * f, f / 8])[torch.randint(0, 4, (18, K, B, A), generator=torch.Generator().manual_seed(42))]
+        p.k.copy_(x.to(E4M3))
+        p.ks.copy_(s[:, None].expand(18, K))
+        k = torch.empty((18 * B, K, A), dtype=torch.bfloat16, device="cuda")
+        api.cb_gather_kv_q8(p.cache, ints([list(range(18))]), ints([0, 18 * B]), k_out=k, v_out=None)
+        api.cb_check_device_errors()
+        want = gather_plain(p, [list(range(18))], [0, 18 * B], [0], 18 * B)[0]
+        assert same(k, bf16_once(want))
+        twice = want.float().bfloat16().double()
+        assert bool((twice != bf16_once(want)).any())  # the numbers tell the two apart
