@@ -38,8 +38,8 @@ __device__ __forceinline__ uint32_t float_to_e4m3x4(float a, float b, float c, f
   return r;
 }
 
-// y, off from an exact value by `rest` (its sign counts) and by less than one step: the value cut off towards zero, its last bit
-// set where bits were cut off.  Rounded to fewer bits after that, it is rounded once.  NaN stays.
+// y, off from an exact value of its sign by `rest` (whose sign counts) and by less than one step: the value cut off towards zero, its
+// last bit set where bits were cut off.  Rounded to fewer bits after that, it is rounded once.  NaN stays.
 __device__ __forceinline__ float to_odd(float y, float rest) {
   uint32_t u = __float_as_uint(y);
   if (!(rest == 0.f)) u = (u - ((u ^ __float_as_uint(rest)) >> 31)) | 1u;

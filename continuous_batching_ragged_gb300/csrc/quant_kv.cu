@@ -8,7 +8,10 @@
 // Powers of two: dividing by s is exact, so every number is rounded once, by at
 // most half a step (2^-4 of it), and a page that is scaled anew loses nothing but
 // the last bits of its smallest numbers.  e4m3's steps are relative, so a finer
-// scale would gain nothing but the range between 224 and 448 steps.
+// scale would gain nothing but the range between 224 and 448 steps.  A kept scale of
+// the caller's own may be no power of two: then quotients are cut off to fp32 with the
+// last bit set where bits were cut off, and rounded once all the same, apart from the
+// others, a row at a time.
 //
 // cb_gather_kv_q8 reads tokens back: q * s, in bf16 or fp32.
 //
@@ -116,11 +119,37 @@ __device__ __forceinline__ uint32_t to_e4m3(const float (&x)[4], float inv) {
   for (int i = 0; i < 4; ++i) y[i] = scaled<FINITE>(x[i], inv);
   return cb::float_to_e4m3x4(y[0], y[1], y[2], y[3]);
 }
+// A row's lane of numbers, for a scale that is no power of two: x / s to odd, from the remainder of a quotient that is off by less
+// than one step.  Numbers that are not finite become NaN.
+template <int N>
+__device__ __forceinline__ void store_quotients(uint8_t* to, const float (&x)[N], float s) {
+  const float up = s < 0x1p-40f ? 0x1p60f : 1.0f;   // remainders that count are ordinary fp32 numbers, and exact
+  const float su = s * up, inv = 1.0f / su;
+  float y[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float xu = x[i] * up, q = xu * inv, near = fmaf(fmaf(-q, su, xu), inv, q);
+    y[i] = cb::to_odd(near + (near - near), fmaf(-near, su, xu));
+  }
+#pragma unroll
+  for (int i = 0; i < N; i += 4) reinterpret_cast<uint32_t*>(to)[i / 4] = cb::float_to_e4m3x4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+}
 __device__ __forceinline__ void store_lane(uint8_t* row, int c, const uint2& v) { reinterpret_cast<uint2*>(row)[c] = v; }
 __device__ __forceinline__ void store_lane(uint8_t* row, int c, uint32_t v) { reinterpret_cast<uint32_t*>(row)[c] = v; }
 
 // The first n 16-byte chunks of a head's page, times `ratio`: by `lanes` lanes, of which this is `lane`.
 __device__ __forceinline__ void rescale_rows(uint8_t* rows, int n, int lane, int lanes, float ratio) {
+  if (!cb::is_power_of_two(ratio)) {             // from a scale of the caller's own
+#pragma unroll 1
+    for (int i = lane; i < 4 * n; i += lanes) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(rows) + i;
+      float f[4];
+      cb::e4m3x4_to_float(*w, f);
+      *w = cb::float_to_e4m3x4(cb::product_to_odd(f[0], ratio), cb::product_to_odd(f[1], ratio), cb::product_to_odd(f[2], ratio),
+                               cb::product_to_odd(f[3], ratio));
+    }
+    return;
+  }
   for (int i = lane; i < n; i += lanes) {
     uint4 old = reinterpret_cast<uint4*>(rows)[i];
     uint32_t* w = &old.x;
@@ -292,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtasPerSm) append_q8_kernel(c
           raw[i] = mine[i] ? src[int64_t(t0) * (is_v ? a.v_stride : a.k_stride)] : make_uint4(0, 0, 0, 0);
           held[i] = mine[i] && first > 0 ? *scale[i] : 0.f;
         }
+        unsigned odd = 0;                          // heads whose scale is no power of two, and so the one that they had
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float f[EPV];
@@ -303,9 +333,22 @@ __global__ void __launch_bounds__(kThreads, kAppendCtasPerSm) append_q8_kernel(c
           for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
           const float s = fmaxf(scale_for(amax), held[i]), inv = 1.0f / s;
           if (!mine[i]) continue;
+          if (!cb::is_power_of_two(s)) {
+            odd |= 1u << i;
+            continue;
+          }
           if (first > 0 && s > held[i]) rescale_rows(rows[i], first * (A / 16), c, LPR, held[i] * inv);
           if (c == 0) *scale[i] = s;
           store_lane(rows[i] + first * A, c, to_e4m3<false>(f, inv));
+        }
+#pragma unroll 1
+        for (; odd; odd &= odd - 1) {
+          const int part = q + (__ffs(odd) - 1) * RPW + r0, h = part % K;
+          const bool is_v = part >= K;
+          float f[EPV];
+          Vec16<T>::to_float((static_cast<const uint4*>(is_v ? a.v_new : a.k_new) + int64_t(h) * LPR + c)[int64_t(t0) * (is_v ? a.v_stride : a.k_stride)], f);
+          store_quotients(static_cast<uint8_t*>(is_v ? a.v : a.k) + ((page * K + h) * int64_t(B) + first) * A + EPV * c, f,
+                          (is_v ? a.v_scale : a.k_scale)[page * K + h]);
         }
       }
       continue;
@@ -406,15 +449,37 @@ __global__ void __launch_bounds__(kThreads, kAppendCtasPerSm) append_q8_kernel(c
         for (int v = 0; v < kHeads; ++v) amax[v] = top[v].get();
       }
       float inv[kHeads];
+      bool even = finite;                          // and the scales are powers of two
 #pragma unroll
       for (int v = 0; v < kHeads; ++v) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) amax[v] = fmaxf(amax[v], __shfl_xor_sync(0xffffffffu, amax[v], o));
         const float s = fmaxf(scale_for(amax[v]), held[v]);
         inv[v] = 1.0f / s;
+        even = even && cb::is_power_of_two(s);
         if (v >= n) continue;
         if (first > 0 && s > held[v]) rescale_rows(rows[v], first * (A / 16), lane, 32, held[v] * inv[v]);
         if (lane == 0) *scale[v] = s;
+      }
+      if (!even) {                                 // rare: the rows once more, one at a time
+        __syncwarp();                              // the scales are written
+#pragma unroll 1
+        for (int p = 0; t0 + p < t1; p += RPW) {
+          const int t = t0 + p + r0;
+          const int64_t slot = t < t1 ? a.slots[t] : -1;
+          if (slot < 0 || slot >= a.num_slots) continue;
+#pragma unroll 1
+          for (int v = 0; v < n; ++v) {
+            const int part = q + v, h = part % K;
+            const bool is_v = part >= K;
+            float f[EPV];
+            Vec16<T>::to_float((static_cast<const uint4*>(is_v ? a.v_new : a.k_new) + int64_t(h) * LPR + c)[int64_t(t) * (is_v ? a.v_stride : a.k_stride)], f);
+            store_quotients(static_cast<uint8_t*>(is_v ? a.v : a.k) + ((page * K + h) * int64_t(B) + (slot & (B - 1))) * A + EPV * c, f,
+                            static_cast<volatile float*>(is_v ? a.v_scale : a.k_scale)[page * K + h]);
+          }
+        }
+        if (!held_all) offs = offsets(0);
+        continue;
       }
       for (int p = 0; t0 + p < t1; p += kSpan) {
         if (!held_all) {
@@ -429,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtasPerSm) append_q8_kernel(c
           for (int v = 0; v < kHeads; ++v) {
             float f[EPV];
             Vec16<T>::to_float(raw[v][i], f);
-            if (o >= 0 && v < n) store_lane(rows[v] + o * A, c, finite ? to_e4m3<true>(f, inv[v]) : to_e4m3<false>(f, inv[v]));
+            if (o >= 0 && v < n) store_lane(rows[v] + o * A, c, to_e4m3<true>(f, inv[v]));
           }
         }
       }

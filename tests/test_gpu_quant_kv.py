@@ -515,3 +515,77 @@ def test_gather_rounds_once(native_lib, top):
         assert same(k, bf16_once(want))
         twice = want.float().bfloat16().double()
         assert bool((twice != bf16_once(want)).any())  # the numbers tell the two apart
+
+
+def near_ties(K, A, dtype, seed, low):
+    """Scales [K], 2^low and more, and numbers [40, K, A] of `dtype` whose quotients lie on, just above or just below ties of e4m3."""
+    g = torch.Generator().manual_seed(seed)
+    tie = (torch.randint(8, 16, (K,), generator=g) * 2 + 1).double() / 16        # between two numbers of four bits
+    x = 1 + torch.randint(1, 128, (K,), generator=g).double() / 128
+    s = (x / tie).float() * 2.0 ** (low + 1)
+    rows_ = (x * 2.0 ** (low + 1))[None, :, None] * torch.exp2(torch.randint(-5, 8, (40, K, A), generator=g).double())
+    rows_ = rows_ * (2 * torch.randint(0, 2, (40, K, A), generator=g) - 1)
+    if dtype == "f32":
+        rows_ = rows_.float()
+        to = torch.randint(0, 3, rows_.shape, generator=g)
+        rows_ = torch.where(to == 1, rows_.nextafter(torch.tensor(math.inf)), torch.where(to == 2, rows_.nextafter(torch.tensor(-math.inf)), rows_))
+    return s, rows_.to(DT[dtype]).cuda()
+
+
+@pytest.mark.parametrize("K,B,A,dtype", [(8, 16, 128, "bf16"), (3, 64, 128, "bf16"), (5, 8, 256, "bf16"), (4, 64, 64, "f32"), (7, 16, 128, "f32")])
+@pytest.mark.parametrize("low", [0, -7, -60, -99, 90])
+def test_kept_scales_of_any_kind(native_lib, K, B, A, dtype, low):
+    """A page keeps a scale that is no power of two: quotients near ties are rounded once, for single tokens, runs, runs longer than a
+    warp holds and among infinities; the page is scaled anew by one larger number."""
+    from continuous_batching_ragged_gb300 import api
+    p = Pool(12, K, B, A, seed=50)
+    (ks, k), (vs, v) = (near_ties(K, A, dtype, s + 51, low) for s in range(2))
+    for i, (to, s) in enumerate(((p.ks, ks), (p.vs, vs), (p.want[2], ks), (p.want[3], vs))):
+        to.copy_(s.to(to.dtype)[None].expand(12, K))
+    k[4, 0, 3], v[6, K - 1, 5] = math.inf, -math.inf
+    n = min(B - 1, 40)
+    slots = [0 * B + 1, 3 * B + B - 1] + [5 * B + o for o in range(1, 1 + min(n, 4))]
+    slots += [7 * B + o for o in range(B - n, B)][:40 - len(slots)]
+    tie = k[:len(slots)], v[:len(slots)]
+    p.append(*tie, slots)
+    p.plain(*tie, slots)
+    api.cb_check_device_errors()
+    p.check()
+    assert float(p.ks[0, 0]) == float(ks[0])          # kept
+    # old numbers, scaled anew by 2^4 / the kept scale and more
+    big = [x[:2].clone() for x in (k, v)]
+    for x in big:
+        x.fill_(448.0 * 2.0 ** (low + 4) if low < 90 else 2.0 ** 105)
+    at = [7 * B + B - 1, 9 * B + 2 % B]
+    p.append(*big, at)
+    p.plain(*big, at)
+    api.cb_check_device_errors()
+    p.check()
+
+
+@pytest.mark.parametrize("top", [0, -60])
+def test_scaled_anew_rounds_once(native_lib, top):
+    """Old numbers whose product with the ratio of the scales fp32 would round to a tie of e4m3."""
+    from continuous_batching_ragged_gb300 import api
+    K, B, A = 6, 16, 128
+    g = torch.Generator().manual_seed(60)
+    for f in (9.0, 11.0, 13.0, 15.0):
+        tie = (torch.randint(8, 16, (400,), generator=g) * 2 + 1).double()
+        s = (tie / f).float()
+        p_ = s.double() * f
+        s = s[(p_.float().double() == tie) & (p_ != tie)][:12 * K]
+        assert s.numel() == 12 * K
+        p = Pool(12, K, B, A, seed=61)
+        x = torch.tensor([f, -f, 2 * f, f / 8, 16.0, 1.0])[torch.randint(0, 6, (12, K, B, A), generator=g)]
+        s = s.reshape(12, K) * 2.0 ** top
+        for to in (p.k, p.v):
+            to.copy_(x.to(E4M3))
+        for to in (p.ks, p.vs):
+            to.copy_(s)
+        p.want = [t.double().cpu() for t in (p.k, p.v, p.ks, p.vs)]
+        k = torch.full((12, K, A), 448 * 2.0 ** (top + 5), device="cuda").bfloat16()
+        slots = [i * B + B - 1 - i % 3 for i in range(10)] + [10 * B + B - 2, 10 * B + B - 1]   # decode rows, and a run
+        p.append(k, k, slots)
+        p.plain(k, k, slots)
+        api.cb_check_device_errors()
+        p.check()
