@@ -155,9 +155,10 @@ __global__ void __launch_bounds__(Sh::kThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // it may start while the stream's last kernel ends
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int s0 = 0, s1 = 0, p = 0, c0 = 0, q_len = 0, n = 0;
+  int s0 = 0, s1 = 0, p = 0, c0 = 0, c1 = 0, n = 0;
   if (tid < NG) s0 = w.cu_groups[tid], s1 = w.cu_groups[tid + 1], p = w.prefix_lens[tid];
-  if (tid < S) c0 = a.cu_seqlens_q[tid], q_len = a.cu_seqlens_q[tid + 1] - c0, n = a.context_lens[tid];
+  if (tid < S) c0 = a.cu_seqlens_q[tid], c1 = a.cu_seqlens_q[tid + 1], n = a.context_lens[tid];
+  const int q_len = c1 - c0;
   if (writer)
     for (int t = tid; t < T; t += kThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
   bool bad = false;
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(Sh::kThreads, 1)
     }
     p = group_p[g];
   }
-  const bool ok = tid < S && p >= 0 && q_len >= 1 && c0 >= 0 && c0 + q_len <= T && q_len <= a.max_q_len && n >= q_len &&
+  const bool ok = tid < S && p >= 0 && c1 > c0 && c0 >= 0 && c1 <= T && q_len <= a.max_q_len && n >= q_len &&
                   p <= n - q_len && n <= a.max_context_len && int64_t(n) <= int64_t(a.max_blocks_per_seq) * a.block_size;
   const int tiles = ok && !bad ? (n - 1) / qstream::kTileKeys + 1 : 0;
   const int streams = tiles > 0 ? (q_len * G + Sh::kRows - 1) / Sh::kRows * Hkv : 0;

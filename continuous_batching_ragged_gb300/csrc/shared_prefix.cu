@@ -293,8 +293,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
       bad = 1;
     } else if (s1 - s0 >= 2 && p >= a.block_size) {
       t0 = cu[s0];
-      const int t1 = cu[s1], q0 = cu[s0 + 1] - t0, ctx0 = ctx[s0];
-      if (t0 >= 0 && t1 <= T && t1 > t0 && q0 >= 1 && ctx0 <= a.max_context_len && ctx0 - q0 >= p &&
+      const int t1 = cu[s1], t0_end = cu[s0 + 1], q0 = t0_end - t0, ctx0 = ctx[s0];
+      if (t0 >= 0 && t1 <= T && t1 > t0 && t0_end > t0 && ctx0 <= a.max_context_len && ctx0 >= q0 && ctx0 - q0 >= p &&
           int64_t(ctx0) <= int64_t(a.max_blocks_per_seq) * a.block_size) {
         tokens = t1 - t0;
         shared = (p >> block_shift) << block_shift;
@@ -335,8 +335,8 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
   }
   for (int s = tid; s < S && !bad; s += kPlanThreads) {
     const int g = last_at_or_before(&groups[0].x, 4, NG, s);   // empty groups start there too, and come before
-    const int p = w.cu_groups ? w.prefix_lens[g] : 0, n = ctx[s], c0 = cu[s], q_len = cu[s + 1] - c0;
-    const bool ok = p >= 0 && q_len >= 1 && c0 >= 0 && c0 + q_len <= T && q_len <= a.max_q_len && n >= q_len &&
+    const int p = w.cu_groups ? w.prefix_lens[g] : 0, n = ctx[s], c0 = cu[s], c1 = cu[s + 1], q_len = c1 - c0;
+    const bool ok = p >= 0 && c1 > c0 && c0 >= 0 && c1 <= T && q_len <= a.max_q_len && n >= q_len &&
                     p <= n - q_len && n <= a.max_context_len && int64_t(n) <= int64_t(a.max_blocks_per_seq) * a.block_size;
     const int4 q = make_int4(ok ? n - groups[g].w : 0, c0, q_len, g);
     seqs[s] = q;
@@ -1239,9 +1239,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // it may start while the stream's last kernel ends
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int s0 = 0, s1 = 0, p = 0, c0 = 0, q_len = 0, n = 0;
+  int s0 = 0, s1 = 0, p = 0, c0 = 0, c1 = 0, n = 0;
   if (tid < NG) s0 = w.cu_groups[tid], s1 = w.cu_groups[tid + 1], p = w.prefix_lens[tid];
-  if (tid < S) c0 = a.cu_seqlens_q[tid], q_len = a.cu_seqlens_q[tid + 1] - c0, n = w.context_lens[tid];
+  if (tid < S) c0 = a.cu_seqlens_q[tid], c1 = a.cu_seqlens_q[tid + 1], n = w.context_lens[tid];
+  const int q_len = c1 - c0;
   if (writer)
     for (int t = tid; t < T; t += kSmallThreads) w.token_info[t] = make_int4(0, 0, 0, 0);
   group_s0[tid] = s0;
@@ -1259,7 +1260,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     if (group_s0[mid] <= tid) g = mid; else hi = mid - 1;
   }
   p = group_p[g];
-  const bool ok = tid < S && p >= 0 && q_len >= 1 && c0 >= 0 && c0 + q_len <= T && q_len <= a.max_q_len && n >= q_len &&
+  const bool ok = tid < S && p >= 0 && c1 > c0 && c0 >= 0 && c1 <= T && q_len <= a.max_q_len && n >= q_len &&
                   p <= n - q_len && n <= a.max_context_len && int64_t(n) <= int64_t(a.max_blocks_per_seq) * a.block_size;
   const int tiles = ok ? (n - 1) / stream::kTileKeys + 1 : 0, rt = ok ? (q_len * G + kStreamRows - 1) / kStreamRows : 0;
   const int64_t my_tiles = warp_sum(int64_t(tiles) * rt * Hkv), my_rows = warp_sum(int64_t(rt) * Hkv);

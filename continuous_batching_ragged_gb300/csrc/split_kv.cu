@@ -140,7 +140,7 @@ __device__ __forceinline__ bool plan_row(const AttnArgs& a, int split, int h, Ro
     if (q_len > 1) return false;          // prefill chunk: not ours
     t = c0;
   }
-  const bool bad = q_len < 1 || ctx < q_len || ctx > a.max_context_len || q_len > a.max_q_len ||
+  const bool bad = c1 <= c0 || ctx < q_len || ctx > a.max_context_len || q_len > a.max_q_len ||
                    c0 < 0 || c1 > a.num_tokens || (ROW_MODE && (t < c0 || t >= c1)) ||
                    (ctx + a.block_size - 1) / a.block_size > a.max_blocks_per_seq;
   if (bad) {
