@@ -749,7 +749,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = max(top, max((in[e] << 16) & 0x7fff0000u, in[e] & 0x7fff0000u));
           }
-          const uint32_t ex = real ? min(254u, 267u - (top >> 23)) : 127u;   // 2^13 / largest, as an exponent
+          const uint32_t ex = real ? min(253u, 267u - (top >> 23)) : 127u;   // 2^13 / largest, as an exponent; its inverse is an ordinary number
           const float f = __uint_as_float(ex << 23);
           reinterpret_cast<float*>(gsm + kOffFactors)[t * BM + row] = __uint_as_float((254u - ex) << 23);
 #pragma unroll

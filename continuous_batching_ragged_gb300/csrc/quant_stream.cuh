@@ -284,7 +284,7 @@ __device__ __forceinline__ void run_warp(const CUtensorMap* tm_k, const CUtensor
       }
 #pragma unroll
       for (int x = 1; x <= 2; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const uint32_t ex = min(254u, 267u - (top >> 23));     // 2^13 / largest, as an exponent
+      const uint32_t ex = min(253u, 267u - (top >> 23));     // 2^13 / largest, as an exponent; its inverse is an ordinary number
       const float f = __uint_as_float(ex << 23), back = a.scale_log2 * __uint_as_float((254u - ex) << 23);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {

@@ -521,3 +521,16 @@ def test_group_pieces_in_turn(native_lib, H, K, B):
     groups = [(640, [(1 + (7 * i + g) % 40, 1) for i in range(odd)]) for g in range(n)]
     S = n * odd
     run_repeated(groups, H, K, B, groups=True, seed=71 + H, sequences=range(0, S, max(1, S // 60)))
+
+
+@pytest.mark.parametrize("q", [1, 3, 130])
+@pytest.mark.parametrize("down", [100, 113, 114, 120])
+def test_smallest_queries_and_largest_keys(native_lib, q, down):
+    """Query numbers down to 2^-122, and key scales that bring their scores back to ones of about 1."""
+    from continuous_batching_ragged_gb300 import api
+    st = Step([(q + 200, q), (130, 1)], 8, 2, 16, seed=64)
+    st.q *= 2.0 ** -down
+    st.ks *= 2.0 ** (down - 1)
+    st.run()
+    api.cb_check_device_errors()
+    st.check()
