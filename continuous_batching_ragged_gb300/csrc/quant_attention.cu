@@ -473,7 +473,7 @@ size_t step_workspace_bytes(int32_t num_tokens) {
 PrefixSizes listed_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
                          int32_t max_context_len) {
   const int sets = listed_sets(num_q_heads / num_kv_heads);
-  return prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len, listed_warps(sets), 8 * sets, true);
+  return prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len, listed_warps(sets), 8 * sets);
 }
 
 cb_status run_step(const AttnArgs& a, const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups, void* workspace,

@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
     static_assert(kLanes == kWaveSteps, "the thread's n is the one that it scores");
     const float piece_bytes = bytes * key_bytes, own_bytes = float(sum_parts(sums[2])) * key_bytes;
     unsigned long long key = ~0ull;
-    if (pieces > 0 && pieces <= w.piece_cap && recs <= w.prefix_rec_cap && own_recs <= w.piece_rec_cap) {
+    if (pieces > 0 && pieces <= w.piece_cap && (recs <= w.prefix_rec_cap || !w.cu_groups) && own_recs <= w.piece_rec_cap) {
       // as many SMs as the pieces fill in 1 .. 16 waves; those of one size run in whole waves, unequal ones fill the gaps
       const int k = sms_of(int(pieces), tid % kWaveSteps + 1, w.num_sms);
       const float per_sm = __fdividef(1.0f, float(k));
@@ -1496,15 +1496,15 @@ int tile_tokens(int group_heads) { return BM / group_heads; }
 }  // namespace
 
 PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
-                         int32_t max_context_len, int stream_warps, int stream_rows, bool pieces) {
+                         int32_t max_context_len, int stream_warps, int stream_rows) {
   PrefixSizes z;
   z.S = size_t(num_seqs), z.T = size_t(num_tokens), z.NG = size_t(std::max(num_groups, 1));
   const size_t G = size_t(num_q_heads / num_kv_heads), rows = z.T * size_t(num_q_heads);
-  const bool chunks = pieces && z.T > z.S && (z.T - z.S + 1) * G > size_t(kMaxStreamRows);   // where every sequence has a token
+  const bool chunks = z.T > z.S && (z.T - z.S + 1) * G > size_t(kMaxStreamRows);   // where every sequence has a token
   // uncut: groups that share have two sequences or more; chunks are all of their tokens
   const size_t pairs = z.T / (2 * size_t(tile_tokens(int(G))));
   z.pieces = size_t(num_kv_heads) * (pairs + std::min(z.NG, z.S / 2) + 1 + (chunks ? pairs + z.S : 0)) + kExtraPieces;
-  z.prefix_recs = std::min(rows * 2 * kMaxSegs, rows * 2 + size_t(kExtraRecs));
+  z.prefix_recs = num_groups > 0 ? std::min(rows * 2 * kMaxSegs, rows * 2 + size_t(kExtraRecs)) : 0;
   z.piece_recs = chunks ? rows * 2 + size_t(kExtraRecs) : 0;
   // ceil(x / L) <= x / L + 1 for every streamed sequence, and all x / L together are at most the units aimed for,
   // twice that where L is halved
@@ -1525,7 +1525,7 @@ size_t prefix_workspace_bytes(const PrefixSizes& z) {
 size_t shared_prefix_workspace_bytes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens,
                                      int32_t num_groups, int32_t max_context_len) {
   return prefix_workspace_bytes(prefix_sizes(num_q_heads, num_kv_heads, num_seqs, num_tokens, num_groups, max_context_len,
-                                             kStreamWarps, kStreamRows, true));
+                                             kStreamWarps, kStreamRows));
 }
 
 // The tensor maps of the K and V pools, boxes of one block and head.
@@ -1669,7 +1669,7 @@ cb_status run_shared_prefix(const AttnArgs& a, const int32_t* cu_groups, const i
                             void* workspace, cudaStream_t stream) {
   NvtxRange nvtx("cb.shared_prefix");
   const PrefixSizes z = prefix_sizes(a.num_heads, a.num_kv_heads, a.num_seqs, a.num_tokens, num_groups, a.max_context_len,
-                                     kStreamWarps, kStreamRows, true);
+                                     kStreamWarps, kStreamRows);
   PrefixWork w;
   cb_status st = prefix_work(a, cu_groups, prefix_lens, num_groups, z, kStreamWarps, kStreamRows, workspace, &w);
   if (st != CB_OK) return st;

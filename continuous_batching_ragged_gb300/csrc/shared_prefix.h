@@ -90,13 +90,13 @@ struct PrefixWork {
 constexpr int kStreamWarps = 8;          // warps of a CTA that stream own keys, each with units of its own
 constexpr int kUnitsPerWarp = 3;         // streamed units that each warp should get
 
-// Capacities of a step's lists.  stream_warps: warps that stream, per SM; stream_rows: query rows of a unit; pieces: whether the kernels behind the plan take
-// pieces at all.
+// Capacities of a step's lists.  stream_warps: warps that stream, per SM; stream_rows: query rows of a unit; without groups there is
+// no record of a prefix.
 struct PrefixSizes {
   size_t S, T, NG, pieces, items, prefix_recs, piece_recs, own_recs;
 };
 PrefixSizes prefix_sizes(int32_t num_q_heads, int32_t num_kv_heads, int32_t num_seqs, int32_t num_tokens, int32_t num_groups,
-                         int32_t max_context_len, int stream_warps, int stream_rows, bool pieces);
+                         int32_t max_context_len, int stream_warps, int stream_rows);
 size_t prefix_workspace_bytes(const PrefixSizes& z);
 // Fills `w` for a step and carves its workspace, whose lists sizes have to be `z`.  num_groups 0 (cu_groups and prefix_lens
 // null): no sequence shares.  The estimates are left to the caller.

@@ -149,3 +149,16 @@ def test_binding_attention(kw):
     with pytest.raises(ValueError):
         api.cb_ragged_attention_q8(f["q"], q8(4, 8, 16, 128), f["cu"], f["ctx"], f["tables"], max_q_len=1, max_context_len=16, scale=0.1,
                                    out=torch.empty_like(f["q"]), workspace=None, cu_groups=f["cu_groups"], prefix_lens=f["prefix_lens"])
+
+
+def test_workspace_without_groups(native_lib):
+    """A step without groups has no room for shared prefixes' records: two a row and 131,072 more."""
+    c = cache()
+
+    def size(seqs, tokens, groups, ctx):
+        return native_lib.cb_ragged_attention_q8_workspace_size(ctypes.byref(c), 32, seqs, tokens, groups, ctx)
+
+    for seqs, tokens, ctx in ((64, 64, 4096), (67, 2050, 4096), (2000, 2000, 512)):
+        assert size(seqs, tokens, 1, ctx) - size(seqs, tokens, 0, ctx) >= 20 << 20
+    assert 0 < size(64, 64, 0, 4096) <= 60 << 20
+    assert size(1, 1, 0, 64) == size(1, 1, 1, 64)     # the records of the whole grid's shares are more
