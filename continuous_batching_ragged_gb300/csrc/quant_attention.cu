@@ -39,10 +39,6 @@ using qstream::WideShape;
 
 constexpr int HD = kPrefixDim;
 constexpr int kMaxSms = 160;             // SMs that the records are sized for
-// Query rows per key/value head that are streamed, 8 or 16 at a time; with more, a step goes to the plan and its chunks to pieces.
-// 4 and 40 sequences of 64 such rows behind 500 and 4000 keys, 32/8 heads, us: streamed 17, 32, 71, 195, as pieces 29, 36, 61,
-// 212; of 128 rows 19, 45, 106, 371 and 29, 36, 66, 132.
-constexpr int kMaxRows = 64;
 constexpr int kStepTokens = 4096;        // of a step without a plan kernel
 // Tiles of a warp's shortest share: more warps load sooner, but leave more records.  4 rows of 1300 keys, 20 of 400 and 8 of
 // 2000, 32/8 heads, us: with 1 10.7, 14.5, 14.6; 3 11.7, 14.1, 14.6; 8 14.6, 15.6, 16.2.
@@ -293,7 +289,7 @@ __global__ void __launch_bounds__(Sh::kThreads, 1)
     n_items = 0;
   }
   __syncwarp();
-  qstream::ListedUnits units{w, a.num_kv_heads, n_items * a.num_kv_heads, -1, 0, 0};   // all claimed: which CTAs start first is open
+  qstream::ListedUnits units{w, a.num_kv_heads, n_items * a.num_kv_heads};
   qstream::run_warp<Sh>(&tm_k, &tm_v, a, w.recs, w.rec_ml, base + warp * Sh::kStages * qstream::kStageBytes, bars,
                         reinterpret_cast<const float2*>(gsm + (bars - base) + 8 * Sh::kStages),
                         reinterpret_cast<SuffixItem*>(gsm + Sh::kOffSlots) + 2 * warp, units);
@@ -538,7 +534,7 @@ cb_status run_quant_attention(const AttnArgs& a, const int32_t* cu_groups, const
   // sequences that may share (all but one of each group), and what sharing may save
   const double saved = num_groups == 0 ? 0.0 : double(a.num_seqs - num_groups) * double(a.max_context_len) * key_bytes;
   const bool fits = a.num_seqs <= threads && num_groups <= threads && a.num_tokens <= kStepTokens &&
-                    (a.max_q_len == 1 || rows <= kMaxRows) && saved <= kSharingBytes &&
+                    (a.max_q_len == 1 || rows <= kMaxStreamRows) && saved <= kSharingBytes &&
                     double(tiles) * double(row_tiles) * a.num_kv_heads * a.num_seqs < double(1 << 30);
   if (fits) return run_step(a, cu_groups, prefix_lens, num_groups, workspace, stream);
 
@@ -567,7 +563,7 @@ cb_status run_quant_attention(const AttnArgs& a, const int32_t* cu_groups, const
   if (st == CB_OK) st = allow_shared_memory();
   if (st == CB_OK) st = launch_prefix_plan(a, w, stream);
   if (st != CB_OK) return st;
-  const bool pieces = num_groups > 0 || (a.max_q_len > 1 && rows > kMaxRows);
+  const bool pieces = num_groups > 0 || (a.max_q_len > 1 && rows > kMaxStreamRows);
   cudaError_t e = cudaSuccess;
   if (pieces)
     e = launch_kernel(q8_pieces_kernel, dim3(unsigned(w.num_sms)), dim3(qpieces::kThreads), qpieces::kSmemBytes, stream, true, tq, tk64,

@@ -33,6 +33,7 @@
 
 #include "device_common.cuh"
 #include "e4m3.cuh"
+#include "packed.cuh"
 #include "quant_stream.cuh"
 #include "shared_prefix.h"
 #include "sm100_ptx.cuh"
@@ -90,53 +91,9 @@ constexpr uint32_t kOffFactors = kOffScales + kScaleSlots * kTileScales * 4;   /
 constexpr uint32_t kSmemBytes = kOffFactors + 2 * BM * 4 + 1024;   // + slack to align the base
 static_assert(kOffItems % 16 == 0 && kOffScales % 16 == 0 && kSmemBytes <= 232448, "shared memory");
 
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
-  return r;
-}
 // idesc_bf16_f32 with f16 A and B
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
   return idesc_bf16_f32(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
-}
-// Packed fp32 pairs: two lanes of work per instruction.
-__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t x, uint64_t y, uint64_t z) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-  return r;
-}
-// 32 bytes in one store (aligned)
-__device__ __forceinline__ void store32(float* p, const uint32_t* x) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
-               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
 }
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 v;
@@ -369,7 +326,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&p[e]));
-              p[e] = pack_f16x2(v.x * alpha, v.y * alpha);
+              p[e] = qstream::pack_f16(v.x * alpha, v.y * alpha);
             }
             tmem_st16(lane_base + 16 * k, p);
           }
@@ -419,7 +376,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             float x0, x1;
             f2_unpack(x2[e], x0, x1);
             x0 = ex2(x0), x1 = ex2(x1);
-            p[e] = pack_f16x2(x0, x1);
+            p[e] = qstream::pack_f16(x0, x1);
             const uint64_t y = f2_pack(x0, x1);
             s2[e >> 3][e & 1] = (e & 7) < 2 ? y : f2_add(s2[e >> 3][e & 1], y);
           }
@@ -757,7 +714,7 @@ __device__ __forceinline__ bool run_pieces(const CUtensorMap* tm_q, const CUtens
             const uint32_t p = at + (k >> 3) * kHalf + (((k & 7) ^ (row & 7)) << 4);
             uint4 v = lds16(p);
             if (!real) v = make_uint4(0, 0, 0, 0);
-            auto two = [&](uint32_t x) { return pack_f16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f); };
+            auto two = [&](uint32_t x) { return qstream::pack_f16(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f); };
             sts16(p, two(v.x), two(v.y), two(v.z), two(v.w));
           }
         }

@@ -112,25 +112,19 @@ struct Taken {
 };
 __device__ __forceinline__ int tiles_of(const SuffixItem& it) { return (it.k1 - it.k0 + kTileKeys - 1) / kTileKeys; }
 
-// Units (item, key/value head) that a plan kernel listed: the first two are given, the later ones claimed.
+// Units (item, key/value head) that a plan kernel listed, all claimed: which CTAs start first is open.
 struct ListedUnits {
   const PrefixWork& w;
   int kv_heads, n_units;
-  int first, step, claimed_from;        // first < 0: the first two are claimed as well
-  int given = 0, claimed = 0;
+  int first = -1, given = 0, claimed = 0;   // the first two are claimed at once
 
   __device__ __forceinline__ void ahead(int lane, bool more) {
     claimed = n_units;
-    if (more && lane == 0) claimed = claimed_from + atomicAdd(w.header + 5, 1);
+    if (more && lane == 0) claimed = atomicAdd(w.header + 5, 1);
   }
   __device__ __forceinline__ Taken take(SuffixItem& it, int lane) {
-    if (first < 0) {
-      int c = 0;
-      if (lane == 0) c = claimed_from + atomicAdd(w.header + 5, 2);
-      first = __shfl_sync(0xffffffffu, c, 0);
-      step = 1;
-    }
-    const int idx = given < 2 ? first + given++ * step : __shfl_sync(0xffffffffu, claimed, 0);
+    if (first < 0) first = __shfl_sync(0xffffffffu, lane == 0 ? atomicAdd(w.header + 5, 2) : 0, 0);
+    const int idx = given < 2 ? first + given++ : __shfl_sync(0xffffffffu, claimed, 0);
     if (idx >= n_units) return {0, 0};
     if (lane < int(sizeof(SuffixItem) / 16))
       reinterpret_cast<int4*>(&it)[lane] = __ldcg(reinterpret_cast<const int4*>(w.items + idx / kv_heads) + lane);

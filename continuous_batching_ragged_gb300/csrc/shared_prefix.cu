@@ -42,6 +42,7 @@
 
 #include "device_common.cuh"
 #include "kernels.h"
+#include "packed.cuh"
 #include "runtime.h"
 #include "shared_prefix.h"
 #include "sm100_ptx.cuh"
@@ -107,9 +108,6 @@ constexpr int64_t kExtraRecs = 131072;   // records beyond two per row (69 MB)
 constexpr int kMinChunkTiles = 4;        // shortest chunk of streamed keys, in 16-key tiles
 constexpr int kStreamRows = 16;          // query rows per row tile of a stream over a bf16 cache
 constexpr int kMaxSms = 160;             // SMs that the lists are sized for
-// Query rows per key/value head up to which a sequence's own keys are streamed,
-// once per 16 rows; beyond, they are pieces.
-constexpr int kMaxStreamRows = 64;
 // Cost model of the segments and of the SM split, in microseconds and bytes.
 constexpr float kTileUsTwo = 1.8f;       // a KV tile against two row tiles
 constexpr float kTileUsOne = 1.4f;       // a KV tile against one row tile, at an SM's share of HBM (0.85 alone)
@@ -552,41 +550,6 @@ __global__ void __launch_bounds__(kPlanThreads) prefix_plan_kernel(const AttnArg
 }
 
 // ------------------------------------------------------------------ prefix phase
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-// Packed fp32 pairs (Blackwell f32x2 FMA / add): two lanes of work per instruction.
-__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t x, uint64_t y, uint64_t z) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t x, uint64_t y) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
-  return r;
-}
-// 32 bytes in one store (aligned)
-__device__ __forceinline__ void store32(float* p, const uint32_t* x) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
-               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
-}
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-  return r;
-}
 
 // The paged blocks of a piece's KV tiles, for one loader warp.  The block table is
 // read 32 entries at a time, one window ahead of the tiles, so that no load waits

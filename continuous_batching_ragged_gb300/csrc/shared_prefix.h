@@ -89,6 +89,10 @@ struct PrefixWork {
 
 constexpr int kStreamWarps = 8;          // warps of a CTA that stream own keys, each with units of its own
 constexpr int kUnitsPerWarp = 3;         // streamed units that each warp should get
+// Query rows per key/value head up to which a sequence's own keys are streamed, once per row tile; beyond, they are pieces, which
+// the plan lists.  Over a cache in 8 bits, 4 and 40 sequences of 64 such rows behind 500 and 4000 keys, 32/8 heads, us: streamed
+// 17, 32, 71, 195, as pieces 29, 36, 61, 212; of 128 rows 19, 45, 106, 371 and 29, 36, 66, 132.
+constexpr int kMaxStreamRows = 64;
 
 // Capacities of a step's lists.  stream_warps: warps that stream, per SM; stream_rows: query rows of a unit; without groups there is
 // no record of a prefix.
