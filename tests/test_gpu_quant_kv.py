@@ -589,3 +589,29 @@ def test_scaled_anew_rounds_once(native_lib, top):
         p.plain(k, k, slots)
         api.cb_check_device_errors()
         p.check()
+
+
+@pytest.mark.parametrize("again", [False, True])
+def test_the_most_tokens(native_lib, again):
+    """65,536 tokens: chunks over thousands of pages and decode rows among them; with one page that comes again at the very end."""
+    from continuous_batching_ragged_gb300 import api, native
+    B, T, blocks = 16, 65_536, 5700
+    p = Pool(blocks, 1, B, 64, seed=70)
+    perm = torch.randperm(blocks, generator=torch.Generator().manual_seed(71)).tolist()
+    singles = perm[4100:4100 + 1536]
+    slots = chunk_slots(perm, B, 7, 40_000) + [x * B + x % B for x in singles] + chunk_slots(perm[2600:], B, 0, T - 41_536)
+    good = list(slots)
+    if again:
+        slots[-1] = slots[40_000]                  # the first decode row's page, and slot
+        good[-1] = good[40_000] = -1
+    assert len(slots) == T
+    k, v = (rows(T, 1, 64, "bf16", s) for s in (72, 73))
+    p.append(k, v, slots)
+    if again:
+        with pytest.raises(native.CBError) as e:
+            api.cb_check_device_errors()
+        assert e.value.status == native.CB_ERR_INVALID
+    else:
+        api.cb_check_device_errors()
+    p.plain(k, v, good)
+    p.check()
