@@ -534,3 +534,22 @@ def test_smallest_queries_and_largest_keys(native_lib, q, down):
     st.run()
     api.cb_check_device_errors()
     st.check()
+
+
+@pytest.mark.parametrize("more", [1, 70])
+@pytest.mark.parametrize("seqs,groups", [([(40, 1), (700, 1)], False), ([(40, 1), (7, 3)], False), ([(30 + i % 50, 1) for i in range(600)], False),
+                                         ([(300, 140), (50, 1)], False), ([(2000, [(9 + i, 1) for i in range(90)])], True)])
+def test_rows_behind_the_last_sequence(native_lib, seqs, groups, more):
+    """Rows of q and out that no sequence has stay as they were; with many heads on one, where a spare row counts as 128."""
+    from continuous_batching_ragged_gb300 import api
+    for H, K in ((8, 2), (128, 1)):
+        st = Step(seqs, H, K, 16, groups=groups, seed=65)
+        T = st.cu_l[-1]
+        st.q = torch.cat([st.q, torch.randn((more, H, A), device="cuda").bfloat16()])
+        st.out = torch.full_like(st.q, float("nan"))
+        n = api.cb_ragged_attention_q8_workspace_size(st.cache, H, len(st.ctx_l), T + more, st.max_ctx, num_groups=len(seqs) if groups else 0)
+        st.ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        st.run()
+        api.cb_check_device_errors()
+        st.check(range(0, len(st.ctx_l), 1 + len(st.ctx_l) // 20))
+        assert bool(st.out[T:].isnan().all()) and bool(st.out[:T].isfinite().all())
