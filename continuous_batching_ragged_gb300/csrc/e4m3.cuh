@@ -45,10 +45,10 @@ __device__ __forceinline__ float to_odd(float y, float rest) {
   if (!(rest == 0.f)) u = (u - ((u ^ __float_as_uint(rest)) >> 31)) | 1u;
   return __uint_as_float(u);
 }
-// Of numbers with up to 4 and 24 bits, so, if the product is 2^-100 or more.
+// The same of a product of numbers with up to 4 and 24 bits, if it is 2^-100 or more.
 __device__ __forceinline__ float product_to_odd(float x, float s) {
-  const float y = x * s;
-  return to_odd(y, fmaf(x, s, -y));
+  const float y = __fmul_rz(x, s);
+  return fmaf(x, s, -y) == 0.f ? y : __uint_as_float(__float_as_uint(y) | 1u);
 }
 __device__ __forceinline__ bool is_power_of_two(float x) { return (__float_as_uint(x) & 0x7fffffu) == 0; }   // of positive ones that are not denormal
 

@@ -512,9 +512,8 @@ struct GatherArgs {
   unsigned* err;
 };
 
-// f * s cut off to fp32 as to_odd does, whatever s.
-__device__ __forceinline__ float scaled_to_odd(float f, float s) {
-  if (s >= 0x1p-90f) return cb::product_to_odd(f, s);
+// f * s cut off to fp32 as product_to_odd does, however small.
+__device__ __forceinline__ float small_to_odd(float f, float s) {
   const double p = double(f) * double(s);          // exact
   const float y = __double2float_rz(p);
   return double(y) == p ? y : __uint_as_float(__float_as_uint(y) | 1u);
@@ -534,7 +533,8 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint4& x, fl
     }
   };
   if (cb::is_power_of_two(s)) row([&](float f) { return f * s; });
-  else row([&](float f) { return scaled_to_odd(f, s); });
+  else if (s >= 0x1p-90f) row([&](float f) { return cb::product_to_odd(f, s); });
+  else row([&](float f) { return small_to_odd(f, s); });
   reinterpret_cast<uint4*>(dst)[0] = make_uint4(r[0], r[1], r[2], r[3]);
   reinterpret_cast<uint4*>(dst)[1] = make_uint4(r[4], r[5], r[6], r[7]);
 }
