@@ -11,7 +11,7 @@
 // scale would gain nothing but the range between 224 and 448 steps.  A kept scale of
 // the caller's own may be no power of two: then quotients are cut off to fp32 with the
 // last bit set where bits were cut off, and rounded once all the same, apart from the
-// others, a row at a time.
+// others.
 //
 // cb_gather_kv_q8 reads tokens back: q * s, in bf16 or fp32.
 //
@@ -461,21 +461,32 @@ __global__ void __launch_bounds__(kThreads, kAppendCtasPerSm) append_q8_kernel(c
         if (first > 0 && s > held[v]) rescale_rows(rows[v], first * (A / 16), lane, 32, held[v] * inv[v]);
         if (lane == 0) *scale[v] = s;
       }
-      if (!even) {                                 // rare: the rows once more, one at a time
+      if (!even) {                                 // rare: the rows once more, four at a time
         __syncwarp();                              // the scales are written
 #pragma unroll 1
-        for (int p = 0; t0 + p < t1; p += RPW) {
-          const int t = t0 + p + r0;
-          const int64_t slot = t < t1 ? a.slots[t] : -1;
-          if (slot < 0 || slot >= a.num_slots) continue;
+        for (int v = 0; v < n; ++v) {
+          const int part = q + v, h = part % K;
+          const bool is_v = part >= K;
+          const uint4* from = static_cast<const uint4*>(is_v ? a.v_new : a.k_new) + int64_t(h) * LPR + c;
+          uint8_t* to = static_cast<uint8_t*>(is_v ? a.v : a.k) + (page * K + h) * int64_t(B) * A + EPV * c;
+          const int64_t step = is_v ? a.v_stride : a.k_stride;
+          const float s = static_cast<volatile float*>(is_v ? a.v_scale : a.k_scale)[page * K + h];
 #pragma unroll 1
-          for (int v = 0; v < n; ++v) {
-            const int part = q + v, h = part % K;
-            const bool is_v = part >= K;
-            float f[EPV];
-            Vec16<T>::to_float((static_cast<const uint4*>(is_v ? a.v_new : a.k_new) + int64_t(h) * LPR + c)[int64_t(t) * (is_v ? a.v_stride : a.k_stride)], f);
-            store_quotients(static_cast<uint8_t*>(is_v ? a.v : a.k) + ((page * K + h) * int64_t(B) + (slot & (B - 1))) * A + EPV * c, f,
-                            static_cast<volatile float*>(is_v ? a.v_scale : a.k_scale)[page * K + h]);
+          for (int p = r0; t0 + p < t1; p += 4 * RPW) {
+            uint4 x[4];
+            int64_t slot[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int t = t0 + p + i * RPW;
+              slot[i] = t < t1 ? a.slots[t] : -1;
+              x[i] = t < t1 ? from[int64_t(t) * step] : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float f[EPV];
+              Vec16<T>::to_float(x[i], f);
+              if (slot[i] >= 0 && slot[i] < a.num_slots) store_quotients(to + int(slot[i] & (B - 1)) * A, f, s);
+            }
           }
         }
         if (!held_all) offs = offsets(0);
