@@ -16,11 +16,12 @@
 // cb_gather_kv_q8 reads tokens back: q * s, in bf16 or fp32.
 //
 // What bounds them: a large read-back HBM, a third of it reads (24 sequences of 4096
-// keys, 24 heads: 231 us, 0.83 of the copy rate; 32-byte stores, more or fewer warps and
-// loads in flight change nothing).  An append is bound by its dependent steps: slots, page
-// and scale, rows, their maximum, stores.  2048 tokens of 32 heads take 21.9 us of 7.5 at
-// the copy rate, 2.5 of them the scan of the slots; warps wait for loads half of the time and
-// issue a third of it.  64 decode rows: 4.7 us in a graph, a launch.
+// keys, 24 heads: 234 us, 0.82 of the copy rate, with scales that are no powers of two 244;
+// 32-byte stores, more or fewer warps and loads in flight change nothing).  An append is bound
+// by its dependent steps: slots, page and scale, rows, their maximum, stores.  2048 tokens of
+// 32 heads take 22.1 us of 7.5 at the copy rate, 2.5 of them the scan of the slots; warps wait
+// for loads half of the time and issue a third of it.  64 decode rows: 4.8 us in a graph, a
+// launch.
 #include <algorithm>
 
 #include "device_common.cuh"
@@ -174,9 +175,9 @@ __device__ __forceinline__ void rescale_rows(uint8_t* rows, int n, int lane, int
 // whatever mix of decode rows and chunks they come from.  Two runs of one page would
 // scale its rows at the same time: each CTA marks the runs' pages, and those that were
 // marked before, whose runs it leaves out; a pool of more pages than there are marks has
-// several to a mark, whose runs are compared one by one.  (2048 tokens of 32 heads take
-// 22.5 us so and 21.6 without; the marks in a pass of their own 22.6, found with one pass
-// and a second one where marks are fewer than runs 22.7.)
+// several to a mark, whose runs are compared one by one.  (Of 2048 tokens of 32 heads, all
+// else equal, the marks take 0.9 us; in a pass of their own 1.0, in one pass with a second
+// where marks are fewer than runs 1.1.)
 template <typename T, int LPR, bool LONG>
 __global__ void __launch_bounds__(kThreads, kAppendCtasPerSm) append_q8_kernel(const AppendArgs a) {
   constexpr int EPV = Vec16<T>::N;               // elements per lane
@@ -623,7 +624,7 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   const int64_t units = int64_t(a.num_tokens) * 2 * a.num_heads;      // at most: a run for each token
   const int64_t grid = std::min<int64_t>((units + kWarps - 1) / kWarps, int64_t(kAppendCtasPerSm) * cb::sm_count());
   // Pages of more than 16 tokens: 32 positions of one head a warp, else 16 of two.  661 tokens of 8 heads and 2048 of 32, us, so
-  // and the other way: pages of 32 7.7, 24.6 and 10.6, 25.8; of 128 20.3, 61 and 27.1, 64; of 16 7.4, 21.7 and 6.7, 25.0.
+  // and the other way: pages of 32 7.6, 24.0 and 10.3, 25.3; of 128 19.0, 57 and 25.3, 59; of 16 7.3, 22.1 and 6.6, 25.1.
   return cb::launch_kernel(a.block_shift > 4 ? append_q8_kernel<T, LPR, true> : append_q8_kernel<T, LPR, false>, dim3(unsigned(grid)),
                            dim3(kThreads), 0, stream, true, a);
 }

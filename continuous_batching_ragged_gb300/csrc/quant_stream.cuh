@@ -27,7 +27,7 @@
 // Measured: 256 rows of 32 heads over 4096 keys 711 to 727 us, 0.98 to 1.0 of the copy
 // rate; 201 rows, 32/8 heads, 152 to 155 us, 0.92; 140 rows of 32 heads on one 45 us, of
 // which 12 are its bytes' and 17 a step's least time with its join: 8 warps an SM, and of
-// a tile's instructions each waits for the last (issue 38 %, DRAM 26 %).
+// a tile's instructions each waits for the last (issue 37 %, DRAM 26 %).
 #pragma once
 
 #include "e4m3.cuh"

@@ -504,7 +504,8 @@ cb_status cb_shared_prefix_attention(const void* q, int32_t num_q_heads, const c
  * Same arguments and result as cb_ragged_attention_gqa, with keys and values
  * number * scale; q and out are bf16.  K and V go to the tensor cores as they are,
  * exact in f16; the scales multiply scores and weights in fp32, and the weights are
- * rounded to f16 (by 2^-11 of each, or 2^-25 of the largest).  Scores are fp32's:
+ * rounded to f16 (by 2^-11 of each, or 2^-25 of the largest; one below 2^-126 of its
+ * row's largest may count as zero, whatever its value's scale).  Scores are fp32's:
  * beyond 2^24 they are not told apart to whole numbers, and a row with scores beyond
  * 2^28 may become NaN.
  *   cu_groups, prefix_lens, num_groups  as in cb_shared_prefix_attention, or NULL, NULL
